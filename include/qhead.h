@@ -323,6 +323,135 @@ int qhead_fwd_noalloc(const qhead_head* head, const void* h, int64_t M, const in
                       const uint8_t* mask, float* logp, float* lse, int32_t* argmax,
                       void* stream);
 
+/* Element types of the operators below (the values of QHEAD_SB_*). */
+#define QHEAD_F16 0
+#define QHEAD_BF16 1
+#define QHEAD_F32 2
+
+/*
+ * Embedding lookup from the head's table (a tied table; no counterpart on the
+ * pages):
+ *     out[m, :] = scale * (s[t, d / 64] * q[t, d] + b[t, d / 64]),  t = tokens[m]
+ * in fp32 from the scales and biases in their own type, rounded once.
+ *   tokens    device, int32 [M].
+ *   mask      device, uint8 [M], or NULL (all rows on); a row that is off is
+ *             written as zeros, its token is not looked at.
+ *   scale     finite.
+ *   out       device, [M, H] of type out_dtype, 16-byte aligned.  A row whose
+ *             token lies outside [0, V) is written as NaN (no read happens).
+ * M == 0 returns QHEAD_OK and launches nothing.
+ */
+int qhead_embed(const qhead_head* head, const int32_t* tokens, int64_t M, const uint8_t* mask,
+                float scale, void* out, int out_dtype, void* stream);
+
+/*
+ * The gradient of qhead_embed with respect to the dequantized table:
+ *     dw[v, :] = (accumulate ? dw[v, :] : 0) + scale * sum_{m on, tokens[m] == v} dout[m, :]
+ * summed in fp32, rows in ascending order in a fixed grouping (deterministic;
+ * no atomic additions).  Only the head's V and H matter.
+ *   dout      device, [M, H] of type dout_dtype, 16-byte aligned.
+ *   dw        device, float [V, H], 16-byte aligned: the layout of
+ *             qhead_bwd_dw's dw, so that a tied table's two gradients can be
+ *             added into one buffer.  Rows whose token lies outside [0, V)
+ *             contribute nothing.  Without accumulate every element is written.
+ *   workspace device, >= qhead_embed_bwd_workspace(head, M) bytes, 256-byte aligned.
+ */
+size_t qhead_embed_bwd_workspace(const qhead_head* head, int64_t M);
+int qhead_embed_bwd(const qhead_head* head, const int32_t* tokens, int64_t M, const uint8_t* mask,
+                    float scale, const void* dout, int dout_dtype, float* dw, int accumulate,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Layer norm of the rows of x (no counterpart on the pages: the norm whose
+ * output is the head's h), or with center == 0 its root-mean-square form:
+ *     xc = x - mean(x)  (center == 0: x);  rstd = 1 / sqrt(mean(xc^2) + eps)
+ *     y  = xc * rstd * weight + bias
+ *   x         device, [M, H] of type x_dtype, row stride ldx >= H elements.
+ *   H         1 <= H <= 8192 (any).
+ *   weight    device, [H] of type w_dtype.
+ *   bias      device, [H] of type w_dtype, or NULL (none).
+ *   eps       >= 0 and finite.  A constant row with eps == 0 gives NaN.
+ *   y         device, [M, H] contiguous, of type y_dtype.
+ *   mean      device, float [M]; required with center, else must be NULL.
+ *   rstd      device, float [M].
+ * Every pointer is aligned to its element; x, y, weight and bias aligned to 16
+ * bytes with H and ldx multiples of 8 take 16-byte accesses.
+ */
+int qhead_layer_norm(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t H,
+                     const void* weight, const void* bias, int w_dtype, float eps, int center,
+                     void* y, int y_dtype, float* mean, float* rstd, void* stream);
+
+/*
+ * The gradient of qhead_layer_norm: with xh = xc * rstd and g = dy * weight,
+ *     dx = rstd * (g - mean(g) - xh * mean(g * xh))   (mean == NULL: no mean(g) term)
+ *     dweight = sum_m dy * xh;  dbias = sum_m dy
+ *   mean      the forward's, or NULL for the uncentred form.
+ *   dy        device, [M, H] of type dy_dtype, row stride ldy >= H elements
+ *             (qhead_bwd's float dh, for example).
+ *   dx        device, [M, H] contiguous, of type x_dtype.
+ *   dweight   device, float [H].
+ *   dbias     device, float [H], or NULL.
+ *   workspace device, >= qhead_layer_norm_bwd_workspace(M, H) bytes, 256-byte aligned.
+ * M == 0 writes zeros to dweight and dbias.  Deterministic.
+ */
+size_t qhead_layer_norm_bwd_workspace(int64_t M, int64_t H);
+int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t H,
+                         const void* weight, int w_dtype, const float* mean, const float* rstd,
+                         const void* dy, int dy_dtype, int64_t ldy, void* dx, float* dweight,
+                         float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Distillation of the head against a teacher's top logits (no counterpart on
+ * the pages, whose losses take one target per row).  Per active row, over its
+ * valid entries k (ids[m, k] >= 0) and the whole vocabulary v, z as in
+ * qhead_fwd:
+ *     p_k  = softmax_k(tlogits[m, k] / temperature)
+ *     lse  = log sum_v exp(z_v / temperature)
+ *     loss = sum_k p_k * (log p_k - z_{ids[m, k]} / temperature + lse)
+ *   h, M, mask  as for qhead_fwd (including |h| < 65504).
+ *   ids       device, int32 [M, K]; a negative id is padding.  A token listed
+ *             twice counts with the sum of its entries' p.
+ *   tlogits   device, [M, K] of type t_dtype: logits or log-probabilities
+ *             (only differences within a row matter); -inf is no mass.
+ *   K         1 <= K <= 1024.
+ *   temperature  > 0 and finite.
+ *   loss, lse device, float [M]; inactive rows 0.  A row without a valid entry
+ *             of finite logit has loss 0; one with an id >= V or a logit that
+ *             is NaN or +inf has loss NaN.
+ *   kept      device, float [M, K + 4], for the backward: in the first K
+ *             columns the exact fp32 logits z of the valid entries (0
+ *             elsewhere), then the exact logits of the two largest other
+ *             vocab rows and (as int32 bits, -1: none) those rows.
+ *   workspace device, >= qhead_distill_fwd_workspace(head, M, K) bytes,
+ *             256-byte aligned.
+ * Every M takes the tensor-core path.  The listed tokens and the two largest
+ * others enter lse with their exact logits, the rest with the tensor-core
+ * kernel's.
+ */
+size_t qhead_distill_fwd_workspace(const qhead_head* head, int64_t M, int64_t K);
+int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const int32_t* ids,
+                      const void* tlogits, int t_dtype, int64_t K, float temperature,
+                      const uint8_t* mask, float* loss, float* lse, float* kept, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * The gradient of sum_m dloss[m] * loss[m] with respect to h, the head frozen:
+ *     dh[m, :] = (dloss[m] / temperature) * sum_v (q_v - p_v) * sech2[m, v] * w[v, :]
+ * with q_v = exp(z_v / temperature - lse).
+ *   lse, kept the forward's, for the same arguments.
+ *   dloss     device, float [M].
+ *   dh        device, bf16 [M, H] (h's type; the contraction's operands carry
+ *             fp16 precision), 16-byte aligned.  Inactive rows and rows with
+ *             nothing to learn from are 0; rows of NaN loss are NaN.
+ *   workspace device, >= qhead_distill_bwd_workspace(head, M, K) bytes,
+ *             256-byte aligned.
+ */
+size_t qhead_distill_bwd_workspace(const qhead_head* head, int64_t M, int64_t K);
+int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const int32_t* ids,
+                      const void* tlogits, int t_dtype, int64_t K, float temperature,
+                      const uint8_t* mask, const float* kept, const float* lse, const float* dloss,
+                      void* dh, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Message for the last error on the calling thread ("" if none).  The
  * pointer stays valid until the thread's next qhead_* call. */
 const char* qhead_last_error(void);
@@ -330,8 +459,8 @@ const char* qhead_last_error(void);
 /*
  * Instrumentation (no counterpart on the pages): arm a one-shot hook on the
  * calling thread.  The thread's next forward or backward call (qhead_fwd,
- * qhead_verify, qhead_fwd_noalloc, qhead_fwd_blockmax, qhead_bwd and the
- * other backward entry points) records the CUDA event `start` on its stream
+ * qhead_verify, qhead_fwd_noalloc, qhead_fwd_blockmax, qhead_distill_fwd,
+ * qhead_bwd and the other backward entry points of the head) records the CUDA event `start` on its stream
  * immediately before its head kernel (the vocab-streaming contraction that
  * dominates the call; for a backward on the tensor-core path, the chain of
  * its per-chunk kernels) and `stop` immediately after it, then disarms the

@@ -15,9 +15,13 @@
 #include <utility>
 
 #include "../../include/qhead.h"
+#include "qh_distill.cuh"
 #include "qh_internal.cuh"
+#include "qh_ops.cuh"
 #include "qh_tmap.h"
 
+static_assert(QHEAD_F16 == QHEAD_SB_F16 && QHEAD_BF16 == QHEAD_SB_BF16 && QHEAD_F32 == QHEAD_SB_F32,
+              "element type codes");
 static_assert(QHEAD_SB_F16 == qh::kSbF16 && QHEAD_SB_BF16 == qh::kSbBf16 &&
                   QHEAD_SB_F32 == qh::kSbF32,
               "scale/bias element type codes");
@@ -304,6 +308,68 @@ int plan_bwd(const qhead_head* hd, int64_t M, BwdPlan* p, bool with_dw = false,
     return QHEAD_OK;
 }
 
+bool dtype_ok(int d) { return d == QHEAD_F16 || d == QHEAD_BF16 || d == QHEAD_F32; }
+
+bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+    if (!ws) return fail(QHEAD_EINVAL, "workspace is NULL");
+    if (misaligned(ws, 256)) return fail(QHEAD_EINVAL, "workspace must be 256-byte aligned");
+    if (have < need)
+        return fail(QHEAD_EINVAL, "workspace too small: need " + std::to_string(need) + " bytes");
+    return QHEAD_OK;
+}
+
+int check_rows(int64_t M) {
+    if (M < 0) return fail(QHEAD_EINVAL, "M < 0");
+    if (M >= ((int64_t)1 << 31) - qh::kRowPad) return fail(QHEAD_EINVAL, "M too large");
+    return QHEAD_OK;
+}
+
+// The distillation's workspace: the head plan's, then the left-out lists
+// (forward) or the rows' cotangents (backward).
+struct DistillPlan {
+    FwdPlan f;
+    BwdPlan b;
+    size_t off_extra = 0, total = 0;
+};
+
+int plan_distill(const qhead_head* hd, int64_t M, int64_t K, bool bwd, DistillPlan* p) {
+    const int rc = bwd ? plan_bwd(hd, M, &p->b) : plan_fwd(hd, M, &p->f, true);
+    if (rc) return rc;
+    p->off_extra = align_up(bwd ? p->b.total : p->f.total, 256);
+    p->total = p->off_extra + (bwd ? 4 * (size_t)M : 4 * (size_t)p->f.Mpad * (size_t)(K + 1));
+    return QHEAD_OK;
+}
+
+int check_distill(const qhead_head* hd, int64_t M, int64_t K) {
+    int rc = check_head(hd);
+    if (rc || (rc = check_rows(M))) return rc;
+    if (K < 1 || K > qh::kMaxTeacher) return fail(QHEAD_EINVAL, "K must be in [1, 1024]");
+    return QHEAD_OK;
+}
+
+int check_distill_inputs(const void* h, const void* ids, const void* tl, int t_dtype, float temp) {
+    if (!h || !ids || !tl) return fail(QHEAD_EINVAL, "h, ids and tlogits are required");
+    if (misaligned(h, 16)) return fail(QHEAD_EINVAL, "h must be 16-byte aligned");
+    if (!dtype_ok(t_dtype)) return fail(QHEAD_EUNSUPPORTED, "t_dtype must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+    if (!(temp > 0.f) || temp > 3.4e38f) return fail(QHEAD_EINVAL, "temperature must be positive and finite");
+    return QHEAD_OK;
+}
+
+int check_norm(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t H, const void* w,
+               int w_dtype) {
+    const int rc = check_rows(M);
+    if (rc) return rc;
+    if (H < 1 || H > qh::kMaxH) return fail(QHEAD_EUNSUPPORTED, "H must be in [1, 8192]");
+    if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype))
+        return fail(QHEAD_EUNSUPPORTED, "dtypes must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+    if (ldx < H) return fail(QHEAD_EINVAL, "ldx < H");
+    if (M > 0 && (!x || !w)) return fail(QHEAD_EINVAL, "x and weight are required");
+    if (misaligned(x, qh::type_bytes(x_dtype)) || misaligned(w, qh::type_bytes(w_dtype)))
+        return fail(QHEAD_EINVAL, "x and weight must be aligned to their elements");
+    return QHEAD_OK;
+}
 
 int cuda_fail(cudaError_t e, const char* what) {
     return fail(QHEAD_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
@@ -724,6 +790,277 @@ int qhead_verify(const qhead_head* head, const void* h, int64_t B, int64_t W,
                                              static_cast<cudaStream_t>(stream));
     if (e) return cuda_fail(e, "accept_prefix");
     return QHEAD_OK;
+}
+
+int qhead_embed(const qhead_head* head, const int32_t* tokens, int64_t M, const uint8_t* mask,
+                float scale, void* out, int out_dtype, void* stream) {
+    g_err.clear();
+    int rc = check_head(head);
+    if (rc || (rc = check_rows(M))) return rc;
+    if (!dtype_ok(out_dtype))
+        return fail(QHEAD_EUNSUPPORTED, "out_dtype must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+    if (!(scale - scale == 0.f)) return fail(QHEAD_EINVAL, "scale must be finite");
+    if (M == 0) return QHEAD_OK;
+    if (!tokens || !out) return fail(QHEAD_EINVAL, "tokens and out are required");
+    if (misaligned(out, 16)) return fail(QHEAD_EINVAL, "out must be 16-byte aligned");
+    const cudaError_t e =
+        qh::launch_embed(head->wq, sb_view(head), head->V, head->H, head->bits, tokens, mask, M, scale,
+                         out, out_dtype, static_cast<cudaStream_t>(stream));
+    return e ? cuda_fail(e, "embed") : QHEAD_OK;
+}
+
+size_t qhead_embed_bwd_workspace(const qhead_head* head, int64_t M) {
+    g_err.clear();
+    if (check_head(head) || check_rows(M)) return (size_t)-1;
+    if (M == 0) return 0;
+    return qh::plan_embed_bwd(M, head->V, head->H).total;
+}
+
+int qhead_embed_bwd(const qhead_head* head, const int32_t* tokens, int64_t M, const uint8_t* mask,
+                    float scale, const void* dout, int dout_dtype, float* dw, int accumulate,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    int rc = check_head(head);
+    if (rc || (rc = check_rows(M))) return rc;
+    if (!dtype_ok(dout_dtype))
+        return fail(QHEAD_EUNSUPPORTED, "dout_dtype must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+    if (!(scale - scale == 0.f)) return fail(QHEAD_EINVAL, "scale must be finite");
+    if (!dw) return fail(QHEAD_EINVAL, "dw is required");
+    if (misaligned(dw, 16)) return fail(QHEAD_EINVAL, "dw must be 16-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        if (accumulate) return QHEAD_OK;
+        const cudaError_t e = cudaMemsetAsync(dw, 0, sizeof(float) * (size_t)head->V * head->H, st);
+        return e ? cuda_fail(e, "dw zero") : QHEAD_OK;
+    }
+    if (!tokens || !dout) return fail(QHEAD_EINVAL, "tokens and dout are required");
+    if (misaligned(dout, 16)) return fail(QHEAD_EINVAL, "dout must be 16-byte aligned");
+    const qh::EmbedBwdPlan p = qh::plan_embed_bwd(M, head->V, head->H);
+    if ((rc = check_workspace(workspace, workspace_bytes, p.total))) return rc;
+    const cudaError_t e = qh::launch_embed_bwd(p, workspace, head->V, head->H, tokens, mask, M, scale,
+                                               dout, dout_dtype, dw, accumulate != 0, st);
+    return e ? cuda_fail(e, "embed_bwd") : QHEAD_OK;
+}
+
+int qhead_layer_norm(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t H,
+                     const void* weight, const void* bias, int w_dtype, float eps, int center,
+                     void* y, int y_dtype, float* mean, float* rstd, void* stream) {
+    g_err.clear();
+    int rc = check_norm(x, x_dtype, ldx, M, H, weight, w_dtype);
+    if (rc) return rc;
+    if (!dtype_ok(y_dtype))
+        return fail(QHEAD_EUNSUPPORTED, "dtypes must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+    if (!(eps >= 0.f) || eps > 3.4e38f) return fail(QHEAD_EINVAL, "eps must be >= 0 and finite");
+    if (!center && mean) return fail(QHEAD_EINVAL, "mean must be NULL without center");
+    if (M == 0) return QHEAD_OK;
+    if (!y || !rstd || (center && !mean))
+        return fail(QHEAD_EINVAL, "y and rstd (and, with center, mean) are required");
+    if (misaligned(y, qh::type_bytes(y_dtype)) || misaligned(bias, qh::type_bytes(w_dtype)) ||
+        misaligned(mean, 4) || misaligned(rstd, 4))
+        return fail(QHEAD_EINVAL, "y, bias, mean and rstd must be aligned to their elements");
+    qh::NormArgs a{x, x_dtype, ldx, M, (int)H, weight, bias, w_dtype, eps, center != 0, y, y_dtype, mean, rstd};
+    const cudaError_t e = qh::launch_norm_fwd(a, static_cast<cudaStream_t>(stream));
+    return e ? cuda_fail(e, "layer_norm") : QHEAD_OK;
+}
+
+size_t qhead_layer_norm_bwd_workspace(int64_t M, int64_t H) {
+    g_err.clear();
+    if (check_rows(M)) return (size_t)-1;
+    if (H < 1 || H > qh::kMaxH) {
+        fail(QHEAD_EUNSUPPORTED, "H must be in [1, 8192]");
+        return (size_t)-1;
+    }
+    return (size_t)qh::norm_bwd_grid(M, (int)H) * 2 * (size_t)H * sizeof(float);
+}
+
+int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t H,
+                         const void* weight, int w_dtype, const float* mean, const float* rstd,
+                         const void* dy, int dy_dtype, int64_t ldy, void* dx, float* dweight,
+                         float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    int rc = check_norm(x, x_dtype, ldx, M, H, weight, w_dtype);
+    if (rc) return rc;
+    if (!dtype_ok(dy_dtype))
+        return fail(QHEAD_EUNSUPPORTED, "dtypes must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+    if (ldy < H) return fail(QHEAD_EINVAL, "ldy < H");
+    if (!dweight) return fail(QHEAD_EINVAL, "dweight is required");
+    if (M > 0 && (!dy || !dx || !rstd)) return fail(QHEAD_EINVAL, "dy, dx and rstd are required");
+    if (misaligned(dy, qh::type_bytes(dy_dtype)) || misaligned(dx, qh::type_bytes(x_dtype)) ||
+        misaligned(mean, 4) || misaligned(rstd, 4) || misaligned(dweight, 4) || misaligned(dbias, 4))
+        return fail(QHEAD_EINVAL, "every pointer must be aligned to its elements");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        cudaError_t e = cudaMemsetAsync(dweight, 0, sizeof(float) * (size_t)H, st);
+        if (!e && dbias) e = cudaMemsetAsync(dbias, 0, sizeof(float) * (size_t)H, st);
+        return e ? cuda_fail(e, "layer_norm_bwd zero") : QHEAD_OK;
+    }
+    const int grid = qh::norm_bwd_grid(M, (int)H);
+    if ((rc = check_workspace(workspace, workspace_bytes, (size_t)grid * 2 * (size_t)H * sizeof(float))))
+        return rc;
+    qh::NormBwdArgs a{x,  x_dtype, ldx, M,       (int)H, weight, w_dtype, mean, rstd, dy, dy_dtype, ldy,
+                      dx, dweight, dbias, static_cast<float*>(workspace), grid};
+    const cudaError_t e = qh::launch_norm_bwd(a, st);
+    return e ? cuda_fail(e, "layer_norm_bwd") : QHEAD_OK;
+}
+
+size_t qhead_distill_fwd_workspace(const qhead_head* head, int64_t M, int64_t K) {
+    g_err.clear();
+    if (check_distill(head, M, K)) return (size_t)-1;
+    if (M == 0) return 0;
+    DistillPlan p;
+    return plan_distill(head, M, K, false, &p) ? (size_t)-1 : p.total;
+}
+
+size_t qhead_distill_bwd_workspace(const qhead_head* head, int64_t M, int64_t K) {
+    g_err.clear();
+    if (check_distill(head, M, K)) return (size_t)-1;
+    if (M == 0) return 0;
+    DistillPlan p;
+    return plan_distill(head, M, K, true, &p) ? (size_t)-1 : p.total;
+}
+
+// Compacts the active rows and stages them as fp16 operands.
+static int stage_rows(const uint8_t* mask, const __nv_bfloat16* hb, int64_t M, int64_t Mpad,
+                      const qhead_head* head, int* rows, int* pos, int* count, int* err, __half* h16,
+                      cudaStream_t st) {
+    cudaError_t e;
+    if (M <= qh::kFusedPrologueMaxM) {
+        e = qh::launch_prologue_fused(mask, hb, M, Mpad, head->H, head->bits, rows, pos, count, h16, Mpad,
+                                      err, st);
+        return e ? cuda_fail(e, "prologue") : QHEAD_OK;
+    }
+    if ((e = qh::launch_compact(mask, M, Mpad, rows, pos, count, err, st))) return cuda_fail(e, "compact");
+    e = qh::launch_convert_h(hb, Mpad, head->H, head->bits, rows, count, h16, st);
+    return e ? cuda_fail(e, "convert_h") : QHEAD_OK;
+}
+
+int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const int32_t* ids,
+                      const void* tlogits, int t_dtype, int64_t K, float temperature,
+                      const uint8_t* mask, float* loss, float* lse, float* kept, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    HookScope hooks;
+    g_err.clear();
+    const int stall = take_stall();
+    int rc = check_distill(head, M, K);
+    if (rc) return rc;
+    if (M == 0) return QHEAD_OK;
+    if ((rc = check_distill_inputs(h, ids, tlogits, t_dtype, temperature))) return rc;
+    if (!loss || !lse || !kept) return fail(QHEAD_EINVAL, "loss, lse and kept are required");
+    DistillPlan dp;
+    if ((rc = plan_distill(head, M, K, false, &dp))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, dp.total))) return rc;
+    const FwdPlan& p = dp.f;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const __half *sc = nullptr, *bi = nullptr;
+    if ((rc = sb_operands(head, workspace, p.off_sb, st, &sc, &bi))) return rc;
+    const auto* hb = static_cast<const __nv_bfloat16*>(h);
+    int* count = at<int>(workspace, p.off_count);
+    int* err = count + 1;
+    int* S_dev = count + 2;
+    int* rows = at<int>(workspace, p.off_rows);
+    int* pos = at<int>(workspace, p.off_pos);
+    __half* h16 = at<__half>(workspace, p.off_h16);
+    qh::Partial* part = at<qh::Partial>(workspace, p.off_part);
+    int* sid = at<int>(workspace, dp.off_extra);
+    const float inv_t = 1.f / temperature;
+    if ((rc = stage_rows(mask, hb, M, p.Mpad, head, rows, pos, count, err, h16, st))) return rc;
+    cudaError_t e;
+    if ((e = qh::launch_distill_prep(head->wq, sb_view(head), head->V, head->H, head->bits, head->softcap,
+                                     hb, pos, M, ids, (int)K, sid, kept, st)))
+        return cuda_fail(e, "distill_prep");
+    CUtensorMap th, tw;
+    if (!qh::tmap_rows_f16_sw128(&th, h16, head->H, p.Mpad, 128) ||
+        !qh::tmap_packed_rows(&tw, head->wq, head->H * head->bits / 32, head->V, 64 * head->bits / 32,
+                              qh::kTcFwdBoxRows))
+        return fail(QHEAD_ECUDA, "TMA tensor map encoding failed");
+    qh::TcFwdArgs ta{};
+    ta.scales = sc; ta.biases = bi; ta.V = head->V; ta.H = head->H; ta.cap = head->softcap;
+    ta.count = count; ta.err = err; ta.stall = stall;
+    ta.vt_begin = 0; ta.vt_end = (int)((head->V + qh::kTcFwdTileRows - 1) / qh::kTcFwdTileRows);
+    ta.part = part; ta.S_out = S_dev;
+    ta.l2e = 1.4426950408889634f * inv_t;
+    ta.sid = sid; ta.sid_ld = (int)K + 1;
+    hook_before(st);
+    e = qh::launch_tc_fwd(th, tw, ta, head->bits, false, p.grid, st);
+    hook_after(st);
+    if (e) return cuda_fail(e, "tc_fwd");
+    e = qh::launch_distill_finalize(head->wq, sb_view(head), head->V, head->H, head->bits, head->softcap,
+                                    hb, pos, M, ids, tlogits, t_dtype, (int)K, inv_t, kept, part, S_dev, err,
+                                    loss, lse, st);
+    return e ? cuda_fail(e, "distill_finalize") : QHEAD_OK;
+}
+
+int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const int32_t* ids,
+                      const void* tlogits, int t_dtype, int64_t K, float temperature,
+                      const uint8_t* mask, const float* kept, const float* lse, const float* dloss,
+                      void* dh, void* workspace, size_t workspace_bytes, void* stream) {
+    HookScope hooks;
+    g_err.clear();
+    const int stall = take_stall();
+    int rc = check_distill(head, M, K);
+    if (rc) return rc;
+    if (M == 0) return QHEAD_OK;
+    if ((rc = check_distill_inputs(h, ids, tlogits, t_dtype, temperature))) return rc;
+    if (!kept || !lse || !dloss || !dh) return fail(QHEAD_EINVAL, "kept, lse, dloss and dh are required");
+    if (misaligned(dh, 16)) return fail(QHEAD_EINVAL, "dh must be 16-byte aligned");
+    DistillPlan dp;
+    if ((rc = plan_distill(head, M, K, true, &dp))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, dp.total))) return rc;
+    const BwdPlan& p = dp.b;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const __half *sc = nullptr, *bi = nullptr;
+    if ((rc = sb_operands(head, workspace, p.off_sb, st, &sc, &bi))) return rc;
+    const auto* hb = static_cast<const __nv_bfloat16*>(h);
+    int* count = at<int>(workspace, p.off_count);
+    int* err = count + 1;
+    int* rows = at<int>(workspace, p.off_rows);
+    int* pos = at<int>(workspace, p.off_pos);
+    __half* h16 = at<__half>(workspace, p.off_h16);
+    __half* coeff = at<__half>(workspace, p.off_coeff);
+    float* dhp = at<float>(workspace, p.off_dhp);
+    float* geff = at<float>(workspace, dp.off_extra);
+    const float inv_t = 1.f / temperature;
+    if ((rc = stage_rows(mask, hb, M, p.Mpad, head, rows, pos, count, err, h16, st))) return rc;
+    CUtensorMap th, tw_logit, tcoef, tw_dh;
+    const int wpr = head->H * head->bits / 32;
+    if (!qh::tmap_rows_f16_sw128(&th, h16, head->H, p.Mpad, 128) ||
+        !qh::tmap_packed_rows(&tw_logit, head->wq, wpr, head->V, 64 * head->bits / 32, qh::kTcFwdBoxRows) ||
+        !qh::tmap_rows_f16_sw128(&tcoef, coeff, p.chunk, p.Mpad, 128) ||
+        !(qh::tc_dh_swizzled(head->H, head->bits)
+              ? qh::tmap_packed_rows_sw128(&tw_dh, head->wq, wpr, head->V, 64)
+              : qh::tmap_packed_rows(&tw_dh, head->wq, wpr, head->V, qh::tc_dh_words(head->H, head->bits),
+                                     64)))
+        return fail(QHEAD_ECUDA, "TMA tensor map encoding failed");
+    const int tr = qh::kTcFwdTileRows;
+    const int n_vt = (int)((head->V + tr - 1) / tr);
+    const int vt_chunk = (int)(p.chunk / tr);
+    cudaError_t e;
+    hook_before(st);
+    for (int vt0 = 0; vt0 < n_vt; vt0 += vt_chunk) {
+        const int vt1 = vt0 + vt_chunk < n_vt ? vt0 + vt_chunk : n_vt;
+        qh::TcFwdArgs ta{};
+        ta.scales = sc; ta.biases = bi; ta.V = head->V; ta.H = head->H; ta.cap = head->softcap;
+        ta.count = count; ta.err = err; ta.stall = vt0 == 0 ? stall : 0;
+        ta.vt_begin = vt0; ta.vt_end = vt1;
+        ta.lse = lse; ta.rows = rows; ta.coeff = coeff; ta.coeff_ld = p.chunk;
+        ta.coeff_rows = (int)p.Mpad;
+        ta.l2e = 1.4426950408889634f * inv_t;
+        if ((e = qh::launch_tc_fwd(th, tw_logit, ta, head->bits, true, p.grid, st)))
+            return cuda_fail(e, "tc_coeff");
+        if ((e = qh::launch_distill_coeff(head->V, head->softcap, pos, M, ids, tlogits, t_dtype, (int)K,
+                                          inv_t, kept, lse, dloss, geff, coeff, p.chunk, (int64_t)vt0 * tr,
+                                          (int64_t)(vt1 - vt0) * tr, st)))
+            return cuda_fail(e, "distill_coeff");
+        qh::TcDhArgs da{};
+        da.scales = sc; da.biases = bi; da.V = head->V; da.H = head->H; da.count = count; da.err = err;
+        da.rows = rows; da.dlogp = geff; da.dh_acc = dhp; da.slice_stride = p.Mpad * head->H;
+        da.v_begin = (int64_t)vt0 * tr; da.n_k = (vt1 - vt0) * tr / 64; da.ks = p.S;
+        da.accumulate = vt0 > 0;
+        if ((e = qh::launch_tc_dh(tcoef, tw_dh, da, head->bits, p.grid, st))) return cuda_fail(e, "tc_dh");
+    }
+    hook_after(st);
+    e = qh::launch_distill_dh(dhp, p.S, p.Mpad, head->H, pos, M, err, dh, st);
+    return e ? cuda_fail(e, "distill_dh") : QHEAD_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,414 @@
+// qh_distill.cu -- the distillation loss of the quantized head against a
+// teacher's top logits: everything around the two tensor-core kernels.
+//
+// Per active row, over the row's valid entries k (ids[k] in [0, V)) and the
+// whole vocabulary v, at temperature T:
+//     p_k  = softmax_k(t_k / T)          the teacher
+//     z_v  = softcap(h . w_v)            the student
+//     lse  = log sum_v exp(z_v / T),  q_v = exp(z_v / T - lse)
+//     loss = sum_k p_k (log p_k - z_k / T + lse)
+//     dh   = (dloss / T) sum_v (q_v - p_v) sech2_v w_v
+//
+// The [M, V] logits come from the same fp16-operand tensor-core kernels as the
+// target-per-row loss (qh_tc_fwd.cu, qh_tc_dh.cu).  An fp16-rounded operand
+// moves a logit by about 3e-4, which is no matter in the tail of the softmax
+// but shows in a loss of a few tenths where the teacher's tokens hold most of
+// the mass, and cancels badly in q_k - p_k.  So the teacher's K logits are
+// computed exactly (fp32, weights widened) once, in the forward, and kept:
+//   * the softmax epilogue leaves the teacher's columns out of its sum and the
+//     finalize adds their exact terms and replaces those of its two largest
+//     other columns, whose exact logits are kept as well;
+//   * the backward's coefficient block gets (q_k - p_k) sech2_k, formed in
+//     fp32 from the exact logits, written over the K + 2 columns of each row
+//     before the contraction with W, so the one-hot part of the gradient needs
+//     no gather of head rows of its own.  (The two other columns belong to
+//     it: with their exact terms in lse but the tensor-core logits in q, a row
+//     with mass there came out 1e-2 off, 1.7e-3 -- bf16's rounding -- with both.)
+//
+// kept [M, K + 4] holds, per row, the K exact capped logits, the two others'
+// and their vocab rows (as integer bits, -1: none).
+#include "qh_distill.cuh"
+#include "qh_tc.cuh"
+
+namespace qh {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kDotsPerWarp = 2;  // teacher logits per warp of the prep kernel
+
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
+
+__device__ __forceinline__ float block_max(float v, float* red) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) v = fmaxf(v, red[w]);
+    __syncthreads();
+    return v;
+}
+
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) v += red[w];
+    __syncthreads();
+    return v;
+}
+
+// Row r of the compact list of left-out columns and the exact capped logits
+// of the row's teacher tokens.  Grid (M, K split): block (r, y) computes the
+// logits k in [8 y, 8 y + 8); block (r, 0) also writes the list: the distinct
+// valid ids in ascending order (each id's rank by counting: K^2 / 128 steps
+// per thread), INT32_MAX behind them.  Measured at 8192 rows of 1536 columns,
+// K = 32: see the table of the design document.
+__global__ void __launch_bounds__(kThreads) distill_prep_kernel(
+    const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, int bits, float cap,
+    const __nv_bfloat16* __restrict__ h, const int* __restrict__ pos,
+    const int32_t* __restrict__ ids, int K, int* __restrict__ sid, float* __restrict__ zk) {
+    const int64_t r = blockIdx.x;
+    const int i = pos[r];
+    const int32_t* idr = ids + r * K;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int k0 = blockIdx.y * kWarps * kDotsPerWarp;
+    zk += r * (K + kKeptExtra);
+    if (i < 0) {
+        for (int k = k0 + threadIdx.x; k < min(K, k0 + kWarps * kDotsPerWarp); k += kThreads) zk[k] = 0.f;
+        return;
+    }
+    if (blockIdx.y == 0) {
+        __shared__ int id_sh[kMaxTeacher];
+        __shared__ uint8_t first_sh[kMaxTeacher];
+        __shared__ int n_sh;
+        if (threadIdx.x == 0) n_sh = 0;
+        for (int k = threadIdx.x; k < K; k += kThreads) id_sh[k] = idr[k];
+        __syncthreads();
+        for (int k = threadIdx.x; k < K; k += kThreads) {
+            const int id = id_sh[k];
+            bool first = id >= 0 && (int64_t)id < V;
+            for (int j = 0; j < k && first; ++j) first = id_sh[j] != id;
+            first_sh[k] = first;
+            if (first) atomicAdd(&n_sh, 1);
+        }
+        __syncthreads();
+        int* out = sid + (int64_t)i * (K + 1);
+        for (int k = threadIdx.x; k < K; k += kThreads) {
+            if (!first_sh[k]) continue;
+            const int id = id_sh[k];
+            int rank = 0;
+            for (int j = 0; j < K; ++j) rank += first_sh[j] && id_sh[j] < id;
+            out[rank] = id;
+        }
+        for (int k = n_sh + threadIdx.x; k < K + 1; k += kThreads) out[k] = INT32_MAX;
+    }
+#pragma unroll 1
+    for (int d = 0; d < kDotsPerWarp; ++d) {
+        const int k = k0 + d * kWarps + warp;
+        if (k >= K) break;
+        const int id = idr[k];
+        const bool ok = id >= 0 && (int64_t)id < V;
+        float z = 0.f;
+        if (ok) z = softcap_exact(warp_exact_logit<8>(h + r * (int64_t)H, wq, sb, id, H, bits), cap);
+        if (lane == 0) zk[k] = z;
+    }
+}
+
+// The teacher's side of a row, shared by the block: ids and scaled logits in
+// shared memory.  bad: an id past V or a logit that is NaN or +inf.
+struct Teacher {
+    float tmax, tsum;  // largest t / T over the valid entries (-inf: none), sum of exponentials
+    bool bad;
+};
+
+template <typename T>
+__device__ __forceinline__ float load_t(const T* p) { return (float)*p; }
+template <>
+__device__ __forceinline__ float load_t(const __half* p) { return __half2float(*p); }
+template <>
+__device__ __forceinline__ float load_t(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+
+template <typename T>
+__device__ __forceinline__ Teacher load_teacher(const int32_t* idr, const T* tr, int K, int64_t V,
+                                                float inv_t, int* id_sh, float* t_sh, float* red) {
+    Teacher te;
+    float mx = -INFINITY;
+    int bad = 0;
+    for (int k = threadIdx.x; k < K; k += kThreads) {
+        const int id = idr[k];
+        float t = -INFINITY;
+        if (id >= 0) {
+            t = load_t(tr + k) * inv_t;
+            if ((int64_t)id >= V || !(t < INFINITY)) bad = 1;
+        }
+        id_sh[k] = id;
+        t_sh[k] = t;
+        mx = fmaxf(mx, t);
+    }
+    te.bad = __syncthreads_or(bad) != 0;
+    te.tmax = block_max(mx, red);
+    float sum = 0.f;
+    if (te.tmax > -INFINITY)
+        for (int k = threadIdx.x; k < K; k += kThreads) sum += expf(t_sh[k] - te.tmax);
+    te.tsum = block_sum(sum, red);
+    return te;
+}
+
+// One block per row: merges the row's partials at the temperature, adds the
+// exact terms of the teacher's distinct tokens, replaces those of the two
+// largest other logits by exact ones, and forms the loss.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) distill_finalize_kernel(
+    const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, int bits, float cap,
+    const __nv_bfloat16* __restrict__ h, const int* __restrict__ pos,
+    const int32_t* __restrict__ ids, const T* __restrict__ tl, int K, float inv_t,
+    float* kept, const Partial* __restrict__ part, const int* __restrict__ S_dev,
+    const int* __restrict__ err, float* __restrict__ loss, float* __restrict__ lse) {
+    const int64_t r = blockIdx.x;
+    const int i = pos[r];
+    float* zr = kept + r * (K + kKeptExtra);
+    // No other columns known: rows that are off or whose kernel gave up.
+    auto no_others = [&]() {
+        zr[K] = zr[K + 1] = 0.f;
+        zr[K + 2] = zr[K + 3] = __int_as_float(-1);
+    };
+    if (i < 0) {
+        if (threadIdx.x == 0) {
+            loss[r] = lse[r] = 0.f;
+            no_others();
+        }
+        return;
+    }
+    __shared__ Partial red_p[kWarps];
+    __shared__ float red[kWarps], cand_sh[2];
+    __shared__ int id_sh[kMaxTeacher];
+    __shared__ float t_sh[kMaxTeacher];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = *S_dev;
+    // Partials: the candidates by RowState, the sum at the temperature.
+    RowState st;
+    st.init();
+    float m = -INFINITY, s = 0.f;
+    int bad = *err != 0;
+    auto fold = [&](float om, float os) {
+        const float nm = fmaxf(m, om);
+        if (nm > -INFINITY) s = s * expf((m - nm) * inv_t) + os * expf((om - nm) * inv_t);
+        m = nm;
+    };
+    const Partial* prow = part + (int64_t)i * S;
+    for (int k = threadIdx.x; k < S; k += kThreads) {
+        const Partial p = prow[k];
+        bad |= p.status;
+        fold(p.m, p.s);
+        st.merge(-INFINITY, 0.f, p.v1, p.i1, p.v2, p.i2);
+    }
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) {
+            loss[r] = lse[r] = nan_f();
+            no_others();
+        }
+        return;
+    }
+#pragma unroll
+    for (int o = 1; o <= 16; o <<= 1) {
+        st.shfl_merge(o);
+        // (the lower lane's state first, so that both partners end equal)
+        const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
+        const float am = lane & o ? om : m, as = lane & o ? os : s;
+        const float bm = lane & o ? m : om, bs = lane & o ? s : os;
+        m = am;
+        s = as;
+        fold(bm, bs);
+    }
+    if (lane == 0) {
+        red_p[warp] = st.to_partial();
+        red_p[warp].m = m;
+        red_p[warp].s = s;
+    }
+    __syncthreads();
+    RowState fin;
+    fin.init();
+    m = -INFINITY;
+    s = 0.f;
+    for (int w = 0; w < kWarps; ++w) {
+        fold(red_p[w].m, red_p[w].s);
+        fin.merge(-INFINITY, 0.f, red_p[w].v1, red_p[w].i1, red_p[w].v2, red_p[w].i2);
+    }
+    // The two candidates' exact logits, one warp each.
+    if (warp < 2) {
+        const int v = warp == 0 ? fin.i1 : fin.i2;
+        const float z = v < V ? softcap_exact(warp_exact_logit<8>(h + r * (int64_t)H, wq, sb, v, H, bits), cap)
+                              : -INFINITY;
+        if (lane == 0) cand_sh[warp] = z;
+    }
+    const Teacher te = load_teacher(ids + r * K, tl + r * K, K, V, inv_t, id_sh, t_sh, red);
+    // (its barriers also publish cand_sh)
+    // The largest of all terms, then their sum.
+    float top = fmaxf(m, fmaxf(cand_sh[0], cand_sh[1]));
+    for (int k = threadIdx.x; k < K; k += kThreads)
+        if (id_sh[k] >= 0 && (int64_t)id_sh[k] < V) top = fmaxf(top, zr[k]);
+    top = block_max(top, red);
+    float sum = 0.f, cross = 0.f;
+    const float lsum = te.tsum > 0.f ? logf(te.tsum) : 0.f;
+    for (int k = threadIdx.x; k < K; k += kThreads) {
+        const int id = id_sh[k];
+        if (id < 0 || (int64_t)id >= V) continue;
+        bool first = true;  // a token listed twice is one term of the sum
+        for (int j = 0; j < k && first; ++j) first = id_sh[j] != id;
+        const float z = zr[k];
+        if (first) sum += expf((z - top) * inv_t);
+        const float lp = t_sh[k] - te.tmax - lsum;
+        const float p = expf(lp);
+        if (p > 0.f) cross += p * (lp - (z - top) * inv_t);  // (log p - z/T, from the maximum)
+    }
+    sum = block_sum(sum, red);
+    cross = block_sum(cross, red);
+    if (threadIdx.x == 0) {
+        float rest = s * expf((m - top) * inv_t);
+        if (m == -INFINITY) rest = 0.f;
+        for (int c = 0; c < 2; ++c) {
+            const float v = c == 0 ? fin.v1 : fin.v2;
+            const int at = c == 0 ? fin.i1 : fin.i2;
+            zr[K + c] = at < V ? cand_sh[c] : 0.f;
+            zr[K + 2 + c] = __int_as_float(at < V ? at : -1);
+            if (at < V)
+                rest += expf((cand_sh[c] - top) * inv_t) - expf((softcap_exact(v, cap) - top) * inv_t);
+        }
+        const float l = logf(fmaxf(rest, 0.f) + sum);  // lse - top / T
+        lse[r] = fmaf(top, inv_t, l);
+        float out = cross + l;
+        if (te.tmax == -INFINITY) out = 0.f;  // nothing to learn from
+        if (te.bad) out = nan_f();
+        loss[r] = out;
+    }
+}
+
+// One block per row, after the coefficient pass of the vocab chunk
+// [v_begin, v_begin + chunk): writes (q_k - p_k) sech2_k * 2^14 over the
+// teacher's columns and the two kept others (|q - p| <= 1: at most 16384 in
+// fp16, one rounding) and
+// the row's cotangent as the contraction kernel takes it, -dloss / T (0 for a
+// row with nothing to learn from, NaN for a bad one).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) distill_coeff_kernel(
+    int64_t V, float cap, const int* __restrict__ pos, const int32_t* __restrict__ ids,
+    const T* __restrict__ tl, int K, float inv_t, const float* __restrict__ kept,
+    const float* __restrict__ lse, const float* __restrict__ dloss, float* __restrict__ geff,
+    __half* __restrict__ coeff, int64_t ld, int64_t v_begin, int64_t chunk) {
+    const int64_t r = blockIdx.x;
+    const int i = pos[r];
+    if (i < 0) return;
+    __shared__ float red[kWarps];
+    __shared__ int id_sh[kMaxTeacher];
+    __shared__ float t_sh[kMaxTeacher];
+    const Teacher te = load_teacher(ids + r * K, tl + r * K, K, V, inv_t, id_sh, t_sh, red);
+    if (threadIdx.x == 0 && v_begin == 0)
+        geff[r] = te.bad ? nan_f() : te.tmax == -INFINITY ? 0.f : -dloss[r] * inv_t;
+    if (te.bad || te.tmax == -INFINITY) return;
+    const float rsum = 1.f / te.tsum, l = lse[r];
+    const float* zr = kept + r * (K + kKeptExtra);
+    for (int k = threadIdx.x; k < K + 2; k += kThreads) {
+        const int id = k < K ? id_sh[k] : __float_as_int(zr[k + 2]);
+        if (id < v_begin || id >= v_begin + chunk || (int64_t)id >= V) continue;
+        float p = 0.f;  // the token's teacher mass (every entry that lists it)
+        if (k < K)
+            for (int j = 0; j < K; ++j)
+                if (id_sh[j] == id) p += expf(t_sh[j] - te.tmax) * rsum;
+        const float z = zr[k];
+        const float th = cap > 0.f ? z / cap : 0.f;
+        const float c = (expf(fmaf(z, inv_t, -l)) - p) * fmaf(-th, th, 1.f);
+        coeff[(int64_t)i * ld + (id - v_begin)] = __float2half_rn(c * 16384.f);
+    }
+}
+
+// One block per row: the K slices of the contraction in order, rounded once to
+// bf16.  Inactive rows are zeros; if a head kernel gave up, active rows NaN.
+__global__ void __launch_bounds__(256) distill_dh_kernel(const float* __restrict__ dhp, int S,
+                                                         int64_t Mpad, int H,
+                                                         const int* __restrict__ pos,
+                                                         const int* __restrict__ err,
+                                                         __nv_bfloat16* __restrict__ dh) {
+    const int64_t r = blockIdx.x;
+    const int i = pos[r];
+    const bool bad = *err != 0;
+    for (int u = threadIdx.x; u < H / 8; u += blockDim.x) {
+        float acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = i >= 0 && bad ? nan_f() : 0.f;
+        if (i >= 0 && !bad) {
+            for (int sl = 0; sl < S; ++sl) {
+                const float4* src =
+                    reinterpret_cast<const float4*>(dhp + ((int64_t)sl * Mpad + i) * H + 8 * u);
+                const float4 a = src[0], b = src[1];
+                acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
+                acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
+            }
+        }
+        __nv_bfloat162 o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
+        *reinterpret_cast<uint4*>(dh + r * (int64_t)H + 8 * u) = *reinterpret_cast<const uint4*>(o);
+    }
+}
+
+// Calls f with a null pointer of the element type of code `type`.
+template <typename F>
+cudaError_t with_type(int type, F&& f) {
+    if (type == kSbF16) return f(static_cast<const __half*>(nullptr));
+    if (type == kSbBf16) return f(static_cast<const __nv_bfloat16*>(nullptr));
+    return f(static_cast<const float*>(nullptr));
+}
+
+}  // namespace
+
+cudaError_t launch_distill_prep(const uint32_t* wq, SbView sb, int64_t V, int H, int bits, float cap,
+                                const __nv_bfloat16* h, const int* pos, int64_t M,
+                                const int32_t* ids, int K, int* sid, float* kept, cudaStream_t st) {
+    constexpr int per = kWarps * kDotsPerWarp;
+    distill_prep_kernel<<<dim3((unsigned)M, (unsigned)((K + per - 1) / per)), kThreads, 0, st>>>(
+        wq, sb, V, H, bits, cap, h, pos, ids, K, sid, kept);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, int H, int bits,
+                                    float cap, const __nv_bfloat16* h, const int* pos, int64_t M,
+                                    const int32_t* ids, const void* tl, int t_type, int K,
+                                    float inv_t, float* kept, const Partial* part,
+                                    const int* S_dev, const int* err, float* loss, float* lse,
+                                    cudaStream_t st) {
+    return with_type(t_type, [&](auto* tag) {
+        distill_finalize_kernel<<<(unsigned)M, kThreads, 0, st>>>(
+            wq, sb, V, H, bits, cap, h, pos, ids, static_cast<decltype(tag)>(tl), K, inv_t, kept, part,
+            S_dev, err, loss, lse);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_distill_coeff(int64_t V, float cap, const int* pos, int64_t M,
+                                 const int32_t* ids, const void* tl, int t_type, int K, float inv_t,
+                                 const float* kept, const float* lse, const float* dloss, float* geff,
+                                 __half* coeff, int64_t ld, int64_t v_begin, int64_t chunk,
+                                 cudaStream_t st) {
+    return with_type(t_type, [&](auto* tag) {
+        distill_coeff_kernel<<<(unsigned)M, kThreads, 0, st>>>(
+            V, cap, pos, ids, static_cast<decltype(tag)>(tl), K, inv_t, kept, lse, dloss, geff, coeff,
+            ld, v_begin, chunk);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_distill_dh(const float* dhp, int S, int64_t Mpad, int H, const int* pos,
+                              int64_t M, const int* err, void* dh, cudaStream_t st) {
+    distill_dh_kernel<<<(unsigned)M, 256, 0, st>>>(dhp, S, Mpad, H, pos, err,
+                                                   static_cast<__nv_bfloat16*>(dh));
+    return cudaGetLastError();
+}
+
+}  // namespace qh

@@ -1,0 +1,31 @@
+// qh_distill.cuh -- launchers of the distillation loss (qh_distill.cu).
+#pragma once
+
+#include "qh_internal.cuh"
+
+namespace qh {
+
+constexpr int kMaxTeacher = 1024;  // teacher entries per row
+constexpr int kKeptExtra = 4;      // kept values per row beyond the K logits
+
+// sid [Mpad, K + 1]: each compact row's distinct valid ids, ascending, then
+// INT32_MAX; kept [M, K + kKeptExtra]: in the first K the exact capped logits of
+// the valid entries (0 for the others and for inactive rows).
+cudaError_t launch_distill_prep(const uint32_t* wq, SbView sb, int64_t V, int H, int bits, float cap,
+                                const __nv_bfloat16* h, const int* pos, int64_t M,
+                                const int32_t* ids, int K, int* sid, float* kept, cudaStream_t st);
+cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, int H, int bits,
+                                    float cap, const __nv_bfloat16* h, const int* pos, int64_t M,
+                                    const int32_t* ids, const void* tl, int t_type, int K,
+                                    float inv_t, float* kept, const Partial* part,
+                                    const int* S_dev, const int* err, float* loss, float* lse,
+                                    cudaStream_t st);
+cudaError_t launch_distill_coeff(int64_t V, float cap, const int* pos, int64_t M,
+                                 const int32_t* ids, const void* tl, int t_type, int K, float inv_t,
+                                 const float* kept, const float* lse, const float* dloss, float* geff,
+                                 __half* coeff, int64_t ld, int64_t v_begin, int64_t chunk,
+                                 cudaStream_t st);
+cudaError_t launch_distill_dh(const float* dhp, int S, int64_t Mpad, int H, const int* pos,
+                              int64_t M, const int* err, void* dh, cudaStream_t st);
+
+}  // namespace qh

@@ -1,0 +1,418 @@
+// qh_embed.cu -- the other end of a tied quantized table: rows looked up and
+// dequantized with a scale, and the gradient of the table.
+//
+//     y[m, :]   = scale * (s[t, d / 64] * q[t, d] + b[t, d / 64]),  t = tokens[m]
+//     dW[v, :] (+)= scale * sum_{m : t_m = v} dy[m, :]
+//
+// Lookup: one fp32 FMA and one multiplication per element, rounded once to the
+// output's type.  It is bound by bytes (the packed row once, the output once).
+//
+// Gradient: the live rows are sorted by token (stable, so every token's rows
+// come in ascending order), then blocks of consecutive sorted rows sum the
+// runs of equal tokens in registers.  A run inside one block is written to dW
+// by that block; the parts of a run that crosses blocks go to the workspace
+// and a second launch adds them in order.  So dW has no atomics, a frequent
+// token's rows are spread over many blocks, and the result does not depend on
+// the launch.  Bytes: dy once, dW's touched rows once (read too when added to).
+// A fresh dW is written in the same launch: blocks behind the summing ones
+// write zeros to the rows whose bit in the touched map is clear.
+#include "qh_ops.cuh"
+#include "qh_tc.cuh"
+
+namespace qh {
+
+namespace {
+
+// The packed codes of one 8-element unit.
+struct Unit {
+    uint32_t w0, w1;
+    float s, b;
+};
+
+__device__ __forceinline__ Unit load_unit(const uint32_t* __restrict__ wq, const SbView& sb, int64_t t,
+                                          int u, int H, int bits) {
+    Unit x;
+    const uint32_t* row = wq + t * (int64_t)(H * bits / 32);
+    if (bits == 4) {
+        x.w0 = row[u];
+        x.w1 = 0u;
+    } else {
+        const uint2 w = reinterpret_cast<const uint2*>(row)[u];
+        x.w0 = w.x;
+        x.w1 = w.y;
+    }
+    const int64_t g = t * (int64_t)(H / 64) + u / 8;
+    x.s = sb_elem(sb.s, g, sb.type);
+    x.b = sb_elem(sb.b, g, sb.type);
+    return x;
+}
+
+__device__ __forceinline__ void unit_values(const Unit& x, int bits, float scale, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t q = bits == 4 ? (x.w0 >> (4 * e)) & 15u
+                                     : ((e < 4 ? x.w0 : x.w1) >> (8 * (e & 3))) & 255u;
+        v[e] = scale * fmaf(x.s, (float)q, x.b);
+    }
+}
+
+// Thread = one 8-element unit of R consecutive rows; the R rows' loads are
+// issued together (two dependent rounds: tokens, then packed units).
+template <int R>
+__global__ void __launch_bounds__(kMaxH / 8) embed_kernel(const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, int bits,
+                             const int32_t* __restrict__ tokens, const uint8_t* __restrict__ mask,
+                             int64_t M, float scale, void* __restrict__ out, int out_type) {
+    const int u = threadIdx.x;
+    if (u >= H / 8) return;
+    const int64_t m0 = (int64_t)blockIdx.x * R;
+    int t[R];
+    bool on[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        on[i] = m0 + i < M && (mask == nullptr || mask[m0 + i] != 0);
+        t[i] = m0 + i < M ? tokens[m0 + i] : 0;
+    }
+    Unit x[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        if (on[i] && t[i] >= 0 && (int64_t)t[i] < V) x[i] = load_unit(wq, sb, t[i], u, H, bits);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (m0 + i >= M) break;
+        float v[8];
+        if (!on[i]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.f;
+        } else if (t[i] < 0 || (int64_t)t[i] >= V) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __int_as_float(0x7fc00000);
+        } else {
+            unit_values(x[i], bits, scale, v);
+        }
+        store8_as(out, (m0 + i) * H + 8 * u, out_type, v);
+    }
+}
+
+// ------------------------------------------------------------------- sorting
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxDigit = 512;    // 9 bits
+constexpr int kSortCluster = 8;   // CTAs of the sorting cluster from kSortOneCta rows
+constexpr int kSortOneCta = 2048;
+
+struct SortSmem {
+    uint32_t cnt[kSortWarps * kMaxDigit];  // per warp and digit: count, then offset
+    uint32_t tot[kMaxDigit];               // this CTA's rows per digit
+    uint32_t base[kMaxDigit];              // first sorted position of the CTA's rows per digit
+    uint32_t warp_tot[kSortWarps];
+};
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+// Stable counting sort of the live rows by token, least-significant digit
+// first, in one cluster: every warp owns a contiguous slice of the keys, counts
+// its digits, and (after the CTAs have exchanged their totals through
+// distributed shared memory) scatters its slice in order.  Rows that are
+// masked or whose token lies outside [0, V) drop out in the first pass.
+// info[0] = live rows.  One launch, no global atomics but the touched map's.
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(
+    const int32_t* __restrict__ tokens, const uint8_t* __restrict__ mask, int64_t M, int64_t V,
+    int passes, int width, uint2* buf_a, uint2* buf_b, int* info, uint32_t* bits, int64_t n_bits) {
+    extern __shared__ unsigned char smem_raw[];
+    SortSmem& sm = *reinterpret_cast<SortSmem*>(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int C = (int)gridDim.x;  // one cluster
+    const int c = (int)blockIdx.x;
+    const int n_digit = 1 << width;
+    if (bits)
+        for (int64_t i = (int64_t)c * kSortThreads + tid; i < n_bits; i += (int64_t)C * kSortThreads)
+            bits[i] = 0u;
+    int64_t n = M;
+    uint32_t* cnt = sm.cnt + warp * kMaxDigit;
+    for (int p = 0; p < passes; ++p) {
+        const uint2* src = p & 1 ? buf_a : buf_b;  // (pass 0 reads the tokens)
+        uint2* dst = p & 1 ? buf_b : buf_a;
+        const int shift = p * width;
+        // this warp's slice, whole batches of 32 keys
+        int64_t len = (n + (int64_t)C * kSortWarps - 1) / ((int64_t)C * kSortWarps);
+        len = (len + 31) / 32 * 32;
+        const int64_t lo = ((int64_t)c * kSortWarps + warp) * len;
+        const int64_t hi = lo + len < n ? lo + len : n;
+        auto key = [&](int64_t i, uint2& k) {  // false: dropped
+            if (i >= hi) return false;
+            if (p == 0) {
+                const int32_t t = tokens[i];
+                k = make_uint2((uint32_t)t, (uint32_t)i);
+                return t >= 0 && (int64_t)t < V && (mask == nullptr || mask[i] != 0);
+            }
+            k = src[i];
+            return true;
+        };
+        for (int d = tid; d < kSortWarps * kMaxDigit; d += kSortThreads) sm.cnt[d] = 0u;
+        __syncthreads();
+        for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+            uint2 k;
+            const bool ok = key(i0 + lane, k);
+            const uint32_t d = ok ? (k.x >> shift) & (uint32_t)(n_digit - 1) : 0xffffffffu;
+            const uint32_t same = __match_any_sync(0xffffffffu, d);
+            if (ok && lane == __ffs(same) - 1) cnt[d] += __popc(same);
+            __syncwarp();
+        }
+        __syncthreads();
+        if (tid < n_digit) {  // counts -> offsets within the CTA's rows of the digit
+            uint32_t run = 0;
+#pragma unroll 8
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t t = sm.cnt[w * kMaxDigit + tid];
+                sm.cnt[w * kMaxDigit + tid] = run;
+                run += t;
+            }
+            sm.tot[tid] = run;
+        }
+        tc::cluster_sync();
+        uint32_t all = 0, before = 0;
+        if (tid < n_digit)
+            for (int o = 0; o < C; ++o) {
+                const uint32_t t = ld_cluster_u32(tc::mapa_shared(&sm.tot[tid], o));
+                if (o < c) before += t;
+                all += t;
+            }
+        // exclusive prefix over the digits
+        uint32_t incl = all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        if (lane == 31) sm.warp_tot[warp] = incl;
+        __syncthreads();
+        uint32_t add = 0, total = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            if (w < warp) add += sm.warp_tot[w];
+            total += sm.warp_tot[w];
+        }
+        if (tid < n_digit) sm.base[tid] = add + incl - all + before;
+        __syncthreads();
+        for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+            uint2 k;
+            const bool ok = key(i0 + lane, k);
+            const uint32_t d = ok ? (k.x >> shift) & (uint32_t)(n_digit - 1) : 0xffffffffu;
+            const uint32_t same = __match_any_sync(0xffffffffu, d);
+            uint32_t at = 0;
+            if (ok) at = sm.base[d] + cnt[d] + __popc(same & ((1u << lane) - 1u));
+            __syncwarp();
+            if (ok && lane == __ffs(same) - 1) cnt[d] += __popc(same);
+            __syncwarp();
+            if (ok) {
+                dst[at] = k;
+                if (bits && p == passes - 1) atomicOr(bits + (k.x >> 5), 1u << (k.x & 31));
+            }
+        }
+        n = total;
+        // The cluster's writes are visible and its totals read before the next pass.
+        tc::cluster_sync();
+    }
+    if (c == 0 && tid == 0) info[0] = (int)n;
+}
+
+// ------------------------------------------------------------------- summing
+
+constexpr int kMaxChunk = 64;
+constexpr int kFillPerSm = 4;
+
+// Block = kChunk sorted rows x all columns, thread = 8 columns.
+template <typename T>
+__global__ void __launch_bounds__(kMaxH / 8) embed_sum_kernel(const uint2* __restrict__ sorted, const int* __restrict__ info,
+                                 int chunk, int64_t n_chunks, int64_t V, int H, float scale,
+                                 const T* __restrict__ dy, float* __restrict__ dw, int accumulate,
+                                 float* __restrict__ part, const uint32_t* __restrict__ bits) {
+    const int u = threadIdx.x;
+    const int units = H / 8;
+    if ((int64_t)blockIdx.x >= n_chunks) {
+        // zeros to the untouched rows of a fresh dW
+        const int64_t f = (int64_t)blockIdx.x - n_chunks, nf = (int64_t)gridDim.x - n_chunks;
+        if (u >= units) return;
+        const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int64_t v = f; v < V; v += nf)
+            if (!(bits[v >> 5] >> (v & 31) & 1u)) store8(dw + v * H + 8 * u, z);
+        return;
+    }
+    __shared__ uint2 key[kMaxChunk + 2];  // the chunk's pairs, one before and one behind
+    const int n = info[0];
+    const int64_t c = blockIdx.x;
+    const int64_t p0 = c * chunk;
+    if (p0 >= n) return;
+    const int len = (int)min((int64_t)chunk, n - p0);
+    for (int i = threadIdx.x; i < len + 2; i += blockDim.x) {
+        const int64_t p = p0 + i - 1;
+        key[i] = p >= 0 && p < n ? sorted[p] : make_uint2(0xffffffffu, 0u);
+    }
+    __syncthreads();
+    if (u >= units) return;
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    bool inside = key[0].x != key[1].x;  // the current run began in this chunk
+    constexpr int U = 4;                 // rows whose loads are issued together
+    for (int i0 = 0; i0 < len; i0 += U) {
+        float x[U][8];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (i0 + k < len) load8(dy + (int64_t)key[1 + i0 + k].y * H + 8 * u, x[k]);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = i0 + k;
+            if (i >= len) break;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] += x[k][e];
+            const uint32_t t = key[1 + i].x;
+            const bool ends = key[2 + i].x != t;
+            if (ends && inside) {
+                float* dst = dw + (int64_t)t * H + 8 * u;
+                float o[8];
+                if (accumulate) {
+                    load8(dst, o);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = fmaf(scale, acc[e], o[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = scale * acc[e];
+                }
+                store8(dst, o);
+            } else if (ends || i == len - 1) {
+                // slot 0: a run from an earlier chunk; slot 1: one that goes on
+                store8(part + (2 * c + (inside ? 1 : 0)) * H + 8 * u, acc);
+            }
+            if (ends) {
+                inside = true;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+            }
+        }
+    }
+}
+
+// Block c: the run that begins in chunk c and goes on past it, if there is
+// one: its parts in order, then dW.
+__global__ void __launch_bounds__(kMaxH / 8) embed_join_kernel(const uint2* __restrict__ sorted, const int* __restrict__ info,
+                                  int chunk, int H, float scale, const float* __restrict__ part,
+                                  float* __restrict__ dw, int accumulate) {
+    const int n = info[0];
+    const int64_t c = blockIdx.x;
+    const int64_t p0 = c * chunk, p1 = p0 + chunk;  // p1: first row of the next chunk
+    if (p1 >= n) return;
+    const uint32_t t = sorted[p1].x;
+    if (sorted[p1 - 1].x != t) return;
+    if (sorted[p0].x == t && p0 > 0 && sorted[p0 - 1].x == t) return;  // began earlier
+    // chunks behind c whose first row belongs to the run (a prefix of them)
+    int more = 0;
+    for (int64_t q = c + 1;; q += blockDim.x) {
+        const int64_t p = (q + threadIdx.x) * chunk;
+        const int got = __syncthreads_count(p < n && sorted[p].x == t);
+        more += got;
+        if (got < (int)blockDim.x) break;
+    }
+    const int u = threadIdx.x;
+    if (u >= H / 8) return;
+    float acc[8], x[8];
+    load8(part + (2 * c + 1) * H + 8 * u, acc);
+#pragma unroll 4
+    for (int k = 1; k <= more; ++k) {
+        load8(part + 2 * (c + k) * H + 8 * u, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += x[e];
+    }
+    float* dst = dw + (int64_t)t * H + 8 * u;
+    float o[8];
+    if (accumulate) load8(dst, o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = accumulate ? fmaf(scale, acc[e], o[e]) : scale * acc[e];
+    store8(dst, o);
+}
+
+size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+int unit_threads(int H) { return (H / 8 + 31) / 32 * 32; }
+
+}  // namespace
+
+cudaError_t launch_embed(const uint32_t* wq, SbView sb, int64_t V, int H, int bits,
+                         const int32_t* tokens, const uint8_t* mask, int64_t M, float scale,
+                         void* out, int out_type, cudaStream_t st) {
+    embed_kernel<1><<<(unsigned)M, unit_threads(H), 0, st>>>(wq, sb, V, H, bits, tokens, mask, M,
+                                                             scale, out, out_type);
+    return cudaGetLastError();
+}
+
+EmbedBwdPlan plan_embed_bwd(int64_t M, int64_t V, int H) {
+    EmbedBwdPlan p;
+    p.chunk = 32;
+    p.n_chunks = (M + p.chunk - 1) / p.chunk;
+    size_t off = 0;
+    p.off_info = off; off = up(off + 16, 256);
+    p.off_bits = off; off = up(off + 4 * (size_t)((V + 31) / 32), 256);
+    p.off_a = off;    off = up(off + 8 * (size_t)M, 256);
+    p.off_b = off;    off = up(off + 8 * (size_t)M, 256);
+    p.off_part = off; off = up(off + 2 * sizeof(float) * (size_t)p.n_chunks * H, 256);
+    p.total = off;
+    return p;
+}
+
+cudaError_t launch_embed_bwd(const EmbedBwdPlan& p, void* ws, int64_t V, int H,
+                             const int32_t* tokens, const uint8_t* mask, int64_t M, float scale,
+                             const void* dy, int dy_type, float* dw, bool accumulate,
+                             cudaStream_t st) {
+    char* w = static_cast<char*>(ws);
+    int* info = reinterpret_cast<int*>(w + p.off_info);
+    uint32_t* bits = accumulate ? nullptr : reinterpret_cast<uint32_t*>(w + p.off_bits);
+    uint2* a = reinterpret_cast<uint2*>(w + p.off_a);
+    uint2* b = reinterpret_cast<uint2*>(w + p.off_b);
+    float* part = reinterpret_cast<float*>(w + p.off_part);
+    int nbits = 1;
+    while (((int64_t)1 << nbits) < V) ++nbits;
+    const int passes = (nbits + 8) / 9, width = (nbits + passes - 1) / passes;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(embed_sort_kernel), (int)sizeof(SortSmem));
+    if (e) return e;
+    const int C = M > kSortOneCta ? kSortCluster : 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = sizeof(SortSmem);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, embed_sort_kernel, tokens, mask, M, V, passes, width, a, b, info, bits,
+                           (V + 31) / 32);
+    if (e) return e;
+    const uint2* sorted = passes & 1 ? a : b;
+    const int threads = unit_threads(H);
+    const unsigned grid = (unsigned)(p.n_chunks + (accumulate ? 0 : kFillPerSm * (int64_t)device_sms()));
+    if (dy_type == kSbF32)
+        embed_sum_kernel<<<grid, threads, 0, st>>>(sorted, info, p.chunk, p.n_chunks, V, H, scale,
+                                                   static_cast<const float*>(dy), dw, accumulate, part, bits);
+    else if (dy_type == kSbBf16)
+        embed_sum_kernel<<<grid, threads, 0, st>>>(sorted, info, p.chunk, p.n_chunks, V, H, scale,
+                                                   static_cast<const __nv_bfloat16*>(dy), dw, accumulate, part, bits);
+    else
+        embed_sum_kernel<<<grid, threads, 0, st>>>(sorted, info, p.chunk, p.n_chunks, V, H, scale,
+                                                   static_cast<const __half*>(dy), dw, accumulate, part, bits);
+    if ((e = cudaGetLastError())) return e;
+    if (p.n_chunks > 1) {
+        embed_join_kernel<<<(unsigned)(p.n_chunks - 1), threads, 0, st>>>(sorted, info, p.chunk, H, scale,
+                                                                          part, dw, accumulate);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+}  // namespace qh

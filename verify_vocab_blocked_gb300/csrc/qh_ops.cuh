@@ -1,0 +1,131 @@
+// qh_ops.cuh -- launchers of the operators beside the head (qh_embed.cu,
+// qh_norm.cu) and their typed 8-element loads and stores.
+#pragma once
+
+#include "qh_internal.cuh"
+
+namespace qh {
+
+// Eight consecutive elements widened to fp32 (the address 16-byte aligned).
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const __half2* h = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(h[i]);
+        v[2 * i] = f.x; v[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+// One rounding to the element type.
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
+    __half2 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(o);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+    __nv_bfloat162 o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(o);
+}
+// The same on a pointer whose element type (kSb*) is known at run time only.
+__device__ __forceinline__ void load8_as(const void* p, int64_t i, int type, float (&v)[8]) {
+    if (type == kSbF32) load8(static_cast<const float*>(p) + i, v);
+    else if (type == kSbBf16) load8(static_cast<const __nv_bfloat16*>(p) + i, v);
+    else load8(static_cast<const __half*>(p) + i, v);
+}
+__device__ __forceinline__ void store8_as(void* p, int64_t i, int type, const float (&v)[8]) {
+    if (type == kSbF32) store8(static_cast<float*>(p) + i, v);
+    else if (type == kSbBf16) store8(static_cast<__nv_bfloat16*>(p) + i, v);
+    else store8(static_cast<__half*>(p) + i, v);
+}
+__device__ __forceinline__ void store_as(void* p, int64_t i, int type, float v) {
+    if (type == kSbF32) static_cast<float*>(p)[i] = v;
+    else if (type == kSbBf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+inline int type_bytes(int type) { return type == kSbF32 ? 4 : 2; }
+
+// ---------------------------------------------------------------- embedding
+
+cudaError_t launch_embed(const uint32_t* wq, SbView sb, int64_t V, int H, int bits,
+                         const int32_t* tokens, const uint8_t* mask, int64_t M, float scale,
+                         void* out, int out_type, cudaStream_t st);
+
+// Workspace of the gradient: two buffers of sorted (token, row) pairs, the
+// count of live rows, a bit per vocab row (touched) and two partial rows per
+// chunk of sorted rows.
+struct EmbedBwdPlan {
+    int chunk = 0;       // sorted rows per block
+    int64_t n_chunks = 0;
+    size_t off_info = 0, off_bits = 0, off_a = 0, off_b = 0, off_part = 0, total = 0;
+};
+EmbedBwdPlan plan_embed_bwd(int64_t M, int64_t V, int H);
+cudaError_t launch_embed_bwd(const EmbedBwdPlan& p, void* ws, int64_t V, int H,
+                             const int32_t* tokens, const uint8_t* mask, int64_t M, float scale,
+                             const void* dy, int dy_type, float* dw, bool accumulate,
+                             cudaStream_t st);
+
+// --------------------------------------------------------------- layer norm
+
+struct NormArgs {
+    const void* x;
+    int x_type;
+    int64_t ldx;
+    int64_t M;
+    int H;
+    const void* w;
+    const void* b;   // NULL: none
+    int w_type;
+    float eps;
+    bool center;
+    void* y;
+    int y_type;
+    float* mean;     // NULL unless center
+    float* rstd;
+};
+cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st);
+
+struct NormBwdArgs {
+    const void* x;
+    int x_type;
+    int64_t ldx;
+    int64_t M;
+    int H;
+    const void* w;
+    int w_type;
+    const float* mean;  // NULL: uncentred
+    const float* rstd;
+    const void* dy;
+    int dy_type;
+    int64_t ldy;
+    void* dx;           // x's type, contiguous
+    float* dw;
+    float* db;          // NULL: not wanted
+    float* part;        // [grid, 2, H]
+    int grid;
+};
+int norm_bwd_grid(int64_t M, int H);
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t st);
+
+}  // namespace qh

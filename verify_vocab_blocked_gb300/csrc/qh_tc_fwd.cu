@@ -148,7 +148,11 @@ __device__ __forceinline__ void unit_coords(const Work& w, int vt_begin, int u, 
 //            [rows x chunk] block (phase 1 of the backward).
 // EPI_FILTER: EPI_COEFF plus the coefficient filter (blocks of 32 rows x 32
 //             vocab rows below filter_eps are written as zeros; a.kbits).
-constexpr int EPI_SOFTMAX = 0, EPI_COEFF = 1, EPI_FILTER = 2;
+// EPI_DISTILL: EPI_SOFTMAX at a temperature, with each row's listed vocab rows
+//             (a.sid) left out of the sum and of the candidates: the finalize
+//             adds their terms from exact fp32 logits.
+// EPI_DCOEFF: EPI_COEFF at a temperature (lse is of the scaled logits).
+constexpr int EPI_SOFTMAX = 0, EPI_COEFF = 1, EPI_FILTER = 2, EPI_DISTILL = 3, EPI_DCOEFF = 4;
 
 // The pair's sequence of (unit, vocab tile) steps, the tiles every role
 // processes in the same order (skipped tiles left out).
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
     const TcFwdArgs a) {
     using L = Layout<BITS>;
     using WR = Warps<BITS>;
+    constexpr bool kCoeff = EPI == EPI_COEFF || EPI == EPI_FILTER || EPI == EPI_DCOEFF;
     constexpr int NS = L::NS;
     constexpr int NSB = L::NSB;
     const __half* __restrict__ scales = a.scales;
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
     const int cid = (int)tc::cluster_id_x(), n_pairs = (int)tc::nclusters_x();
     const int n_active = *a.count;
     const Work W = plan_work(n_active, a.vt_end - a.vt_begin, n_pairs);
-    if (EPI == EPI_SOFTMAX && blockIdx.x == 0 && threadIdx.x == 0) *a.S_out = W.n_seg;
+    if (!kCoeff && blockIdx.x == 0 && threadIdx.x == 0) *a.S_out = W.n_seg;
     // (the same decision in both CTAs of the pair: nothing below has run yet)
     if (W.units == 0 || cid >= W.units) return;
     const int KSTEPS = H / BK;
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
         return t >= a.skip_rows || a.skip[(int64_t)t * a.skip_ld + vt] != 0;
     };
     auto skipped = [&](int mt, int vt) {
-        return EPI != EPI_SOFTMAX && a.skip != nullptr && skip_half(2 * mt, vt) &&
+        return kCoeff && a.skip != nullptr && skip_half(2 * mt, vt) &&
                skip_half(2 * mt + 1, vt);
     };
     // Tile iteration shared by the roles that look ahead (dequant warps).
@@ -488,6 +493,8 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
         const int row = (int)rank * BM + sub * 32 + lane;  // row of the pair's 256-row unit
         const uint32_t lane_addr = static_cast<uint32_t>(sub * 32) << 16;
         const float k2 = cap > 0.f ? 2.f * kLog2e / cap : 0.f;
+        // log2(e) / temperature (the distillation epilogues)
+        const float l2e = EPI == EPI_DISTILL || EPI == EPI_DCOEFF ? a.l2e : kLog2e;
         int buf = 0;
         uint32_t aphase = 0;
         for (int u = cid; u < W.units; u += n_pairs) {
@@ -496,10 +503,10 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
             const int i = mt * BMU + row;  // compact row of this thread
             float m = -INFINITY, s = 0.f, v1 = -INFINITY, v2 = -INFINITY;
             int i1 = INT32_MAX, i2 = INT32_MAX;
-            // EPI_COEFF: log2(p * 2^14) = z * log2e - (lse * log2e - 14)
+            // EPI_COEFF: log2(p * 2^14) = z * l2e - (lse * log2e - 14)
             float lsb = 0.f;
             bool row_ok = i < n_active;
-            if (EPI != EPI_SOFTMAX && row_ok) lsb = a.lse[a.rows[i]] * kLog2e - 14.f;
+            if (kCoeff && row_ok) lsb = a.lse[a.rows[i]] * kLog2e - 14.f;
             // Coefficient filter: |dlogp| and the valid target of this row.
             float fg = 0.f;
             int64_t ftgt = -1;
@@ -508,6 +515,23 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                 fg = fabsf(a.dlogp[r]);
                 const int32_t tg = a.targets[r];
                 ftgt = tg >= 0 && (int64_t)tg < V ? (int64_t)tg : -1;
+            }
+            // EPI_DISTILL: this row's ascending list of left-out vocab rows; sidx
+            // is its first entry at or past the columns still to come.
+            const int* sl = nullptr;
+            int sidx = INT32_MAX;
+            if constexpr (EPI == EPI_DISTILL) {
+                if (row_ok) {
+                    sl = a.sid + (int64_t)i * a.sid_ld;
+                    const int64_t first = (int64_t)vt0 * BN;
+                    int lo = 0, hi = a.sid_ld - 1;  // (entry sid_ld - 1 is INT32_MAX)
+                    while (lo < hi) {
+                        const int mid = (lo + hi) >> 1;
+                        if (sl[mid] < first) lo = mid + 1; else hi = mid;
+                    }
+                    sl += lo;
+                    sidx = *sl;
+                }
             }
             for (int vt = vt0; vt < vt1; ++vt) {
                 // Both 128-row tiles of the unit skip the vocab tile: so does
@@ -519,13 +543,13 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                 // blockMax exit: this CTA's 128-row tile skips the vocab tile
                 // while the other one keeps it: its coefficients are written as
                 // zeros (the dh contraction reads them).  Warp-uniform.
-                const bool zero_half = EPI != EPI_SOFTMAX && a.skip != nullptr &&
+                const bool zero_half = kCoeff && a.skip != nullptr &&
                                        skip_half(2 * mt + (int)rank, vt);
                 float tz = -INFINITY;  // the tile's maximum of z (blockMax)
 #pragma unroll 1
                 for (int c = 0; c < BN / 32; ++c) {
                     const int64_t col0 = (int64_t)vt * BN + c * 32;
-                    if (EPI != EPI_SOFTMAX && zero_half) {
+                    if (kCoeff && zero_half) {
                         if (i < a.coeff_rows) {
                             __half* dst = a.coeff + (int64_t)i * a.coeff_ld +
                                           (col0 - (int64_t)a.vt_begin * BN);
@@ -536,13 +560,14 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                         continue;
                     }
                     uint32_t rr[32];
+                    if (EPI == EPI_DISTILL) __syncwarp();  // (lanes diverge at left-out columns)
                     tc::tmem_ld32(tmem_base + lane_addr + buf * BN + c * 32, rr);
                     tc::tmem_wait_ld();
                     const int nvalid = (int)min((int64_t)32, V - col0);
                     float x[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(rr[j]);
-                    if constexpr (EPI != EPI_SOFTMAX) {
+                    if constexpr (kCoeff) {
                         // coefficient block column = col0 - first column of the chunk
                         __half* dst = a.coeff + (int64_t)i * a.coeff_ld + (col0 - (int64_t)a.vt_begin * BN);
                         uint32_t out[16];
@@ -556,10 +581,10 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                                 float lg2p, sech2 = 1.f;
                                 if (cap > 0.f) {
                                     const float th = fmaf(-2.f, tc::rcp_approx(tc::ex2_approx(xv * k2) + 1.f), 1.f);
-                                    lg2p = fmaf(cap * th, kLog2e, -lsb);
+                                    lg2p = fmaf(cap * th, l2e, -lsb);
                                     sech2 = fmaf(-th, th, 1.f);
                                 } else {
-                                    lg2p = fmaf(xv, kLog2e, -lsb);
+                                    lg2p = fmaf(xv, l2e, -lsb);
                                 }
                                 const bool ok = row_ok && (j + e) < nvalid;
                                 cj[e] = ok ? tc::ex2_approx(lg2p) * sech2 : 0.f;
@@ -594,6 +619,20 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                         }
                     } else {
                         if (nvalid <= 0) continue;
+                        // The slice's left-out columns: their logits count as
+                        // -inf for the maximum and are skipped in the sum.
+                        uint32_t out_cols = 0u;
+                        if constexpr (EPI == EPI_DISTILL) {
+                            while (sidx != INT32_MAX && (int64_t)sidx < col0 + 32) {
+                                out_cols |= 1u << (sidx - (int)col0);
+                                sidx = *++sl;
+                            }
+                            if (out_cols) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (out_cols >> j & 1u) x[j] = -INFINITY;
+                            }
+                        }
                         float rmax = -INFINITY;
                         if (nvalid == 32) {
 #pragma unroll
@@ -603,6 +642,7 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                             for (int j = 0; j < 32; ++j)
                                 if (j < nvalid) rmax = fmaxf(rmax, x[j]);
                         }
+                        if (EPI == EPI_DISTILL && rmax == -INFINITY) continue;  // nothing left
                         // Lowest column of the slice holding its maximum.  No
                         // guard is needed: the column that set rmax is valid and
                         // lies below every padding column.
@@ -624,29 +664,30 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                             zmax = fmaf(-2.f * cap, tc::rcp_approx(tc::ex2_approx(rmax * k2) + 1.f), cap);
                         }
                         const float mn = fmaxf(m, zmax);
-                        const float mb = mn * kLog2e;
+                        const float mb = mn * l2e;
                         float acc = 0.f;
-                        if (nvalid == 32) {
+                        if (nvalid == 32 && (EPI != EPI_DISTILL || out_cols == 0u)) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) acc += tc::ex2_approx(fmaf(x[j], kLog2e, -mb));
+                            for (int j = 0; j < 32; ++j) acc += tc::ex2_approx(fmaf(x[j], l2e, -mb));
                         } else {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                if (j < nvalid) acc += tc::ex2_approx(fmaf(x[j], kLog2e, -mb));
+                                if (j < nvalid && !(out_cols >> j & 1u))
+                                    acc += tc::ex2_approx(fmaf(x[j], l2e, -mb));
                         }
-                        s = s * tc::ex2_approx((m - mn) * kLog2e) + acc;
+                        s = s * tc::ex2_approx((m - mn) * l2e) + acc;
                         m = mn;
                         tz = fmaxf(tz, zmax);
                     }
                 }
-                if (EPI == EPI_SOFTMAX && a.bmax != nullptr && row_ok)
+                if (!kCoeff && a.bmax != nullptr && row_ok)
                     a.bmax[(int64_t)a.rows[i] * a.bmax_ld + vt] = tz;
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive_cluster(acce_lead + 8u * (uint32_t)buf);
                 if (++buf == 2) { buf = 0; aphase ^= 1; }
             }
-            if (EPI == EPI_SOFTMAX && row_ok) {
+            if (!kCoeff && row_ok) {
                 Partial p;
                 p.m = m; p.s = s; p.v1 = v1; p.v2 = v2; p.i1 = i1; p.i2 = i2; p.status = *abort_flag; p.pad1 = 0;
                 a.part[(int64_t)i * W.n_seg + seg] = p;
@@ -734,6 +775,13 @@ cudaError_t launch_tc_fwd(const CUtensorMap& th, const CUtensorMap& tw, const Tc
     a.sb_tma = G % kSbGroups == 0 &&
                tmap_group_rows(&ts, a.scales, G, (uint64_t)a.V, kSbGroups, BNH) &&
                tmap_group_rows(&tb, a.biases, G, (uint64_t)a.V, kSbGroups, BNH);
+    if (a.l2e > 0.f) {
+        if (bits == 4)
+            return coeff_epilogue ? launch_t<4, EPI_DCOEFF>(th, tw, ts, tb, a, grid, st)
+                                  : launch_t<4, EPI_DISTILL>(th, tw, ts, tb, a, grid, st);
+        return coeff_epilogue ? launch_t<8, EPI_DCOEFF>(th, tw, ts, tb, a, grid, st)
+                              : launch_t<8, EPI_DISTILL>(th, tw, ts, tb, a, grid, st);
+    }
     if (bits == 4)
         return !coeff_epilogue ? launch_t<4, EPI_SOFTMAX>(th, tw, ts, tb, a, grid, st)
                : a.kbits != nullptr ? launch_t<4, EPI_FILTER>(th, tw, ts, tb, a, grid, st)

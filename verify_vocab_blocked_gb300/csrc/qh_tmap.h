@@ -86,6 +86,12 @@ struct TcFwdArgs {
     uint8_t* cold_out;
     int64_t cold_out_ld;
     int64_t cold_out_rows;
+    // Distillation epilogues (l2e > 0 selects them): l2e = log2(e) / temperature;
+    // sid: per compact row, sid_ld ascending vocab rows (the last INT32_MAX)
+    // that the softmax epilogue leaves out.
+    float l2e;
+    const int* sid;
+    int sid_ld;
     // Set by launch_tc_fwd: the scale and bias tables are staged by TMA.
     int sb_tma;
 };

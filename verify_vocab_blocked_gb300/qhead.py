@@ -26,7 +26,11 @@ EXPORTS = ("qhead_fwd_workspace", "qhead_bwd_workspace", "qhead_fwd", "qhead_bwd
            "qhead_fwd_noalloc", "qhead_test_stall_next_call", "qhead_verify",
            "qhead_bwd_dw_workspace", "qhead_bwd_dw", "qhead_fwd_blockmax_workspace",
            "qhead_fwd_blockmax", "qhead_bwd_blockskip_workspace", "qhead_bwd_blockskip",
-           "qhead_bwd_filter_workspace", "qhead_bwd_filter")
+           "qhead_bwd_filter_workspace", "qhead_bwd_filter", "qhead_embed",
+           "qhead_embed_bwd_workspace", "qhead_embed_bwd", "qhead_layer_norm",
+           "qhead_layer_norm_bwd_workspace", "qhead_layer_norm_bwd",
+           "qhead_distill_fwd_workspace", "qhead_distill_fwd", "qhead_distill_bwd_workspace",
+           "qhead_distill_bwd")
 
 
 class CHead(ctypes.Structure):
@@ -82,6 +86,29 @@ def lib() -> ctypes.CDLL:
     L.qhead_bwd_filter.restype = ctypes.c_int
     L.qhead_verify.argtypes = [hp, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.qhead_verify.restype = ctypes.c_int
+    i32, f32 = ctypes.c_int, ctypes.c_float
+    L.qhead_embed.argtypes = [hp, vp, i64, vp, f32, vp, i32, vp]
+    L.qhead_embed.restype = i32
+    L.qhead_embed_bwd_workspace.argtypes = [hp, i64]
+    L.qhead_embed_bwd_workspace.restype = sz
+    L.qhead_embed_bwd.argtypes = [hp, vp, i64, vp, f32, vp, i32, vp, i32, vp, sz, vp]
+    L.qhead_embed_bwd.restype = i32
+    L.qhead_layer_norm.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f32, i32, vp, i32, vp, vp,
+                                   vp]
+    L.qhead_layer_norm.restype = i32
+    L.qhead_layer_norm_bwd_workspace.argtypes = [i64, i64]
+    L.qhead_layer_norm_bwd_workspace.restype = sz
+    L.qhead_layer_norm_bwd.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, i32, i64, vp,
+                                       vp, vp, vp, sz, vp]
+    L.qhead_layer_norm_bwd.restype = i32
+    for name in ("qhead_distill_fwd_workspace", "qhead_distill_bwd_workspace"):
+        getattr(L, name).argtypes = [hp, i64, i64]
+        getattr(L, name).restype = sz
+    L.qhead_distill_fwd.argtypes = [hp, vp, i64, vp, vp, i32, i64, f32, vp, vp, vp, vp, vp, sz, vp]
+    L.qhead_distill_fwd.restype = i32
+    L.qhead_distill_bwd.argtypes = [hp, vp, i64, vp, vp, i32, i64, f32, vp, vp, vp, vp, vp, vp, sz,
+                                    vp]
+    L.qhead_distill_bwd.restype = i32
     L.qhead_last_error.argtypes = []
     L.qhead_last_error.restype = ctypes.c_char_p
     L.qhead_version.argtypes = []
@@ -415,3 +442,220 @@ def verify(head: Head, h: torch.Tensor, W: int, draft: torch.Tensor | None,
                               nxt.data_ptr(), workspace.data_ptr(), workspace.numel(),
                               _stream(stream)))
     return n_acc, nxt, am, lse
+
+
+# ------------------------------------------------- the operators beside the head
+
+def _check_matrix(name: str, t: torch.Tensor, dev, contiguous: bool = True):
+    """A float matrix on `dev` whose rows are contiguous (rows too, unless
+    contiguous is off: then their stride may exceed the width)."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in _SB_CODE or t.dim() != 2:
+        raise ValueError(f"{name} must be a float16, bfloat16 or float32 matrix")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.is_contiguous():
+        return
+    if contiguous:
+        raise ValueError(f"{name} must be contiguous")
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def _tokens(head: Head, t: torch.Tensor) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 \
+            or not t.is_contiguous():
+        raise ValueError("tokens must be a contiguous int32 vector")
+    if t.device != head.wq.device:
+        raise ValueError(f"tokens are on {t.device} but the head is on {head.wq.device}")
+    return int(t.shape[0])
+
+
+def _out_code(dtype) -> int:
+    if dtype not in _SB_CODE:
+        raise ValueError("out_dtype must be float16, bfloat16 or float32")
+    return _SB_CODE[dtype]
+
+
+def _size(n: int) -> int:
+    if n == ctypes.c_size_t(-1).value:
+        raise QheadError(QHEAD_EINVAL, last_error())
+    return int(n)
+
+
+def embed(head: Head, tokens: torch.Tensor, scale: float = 1.0, mask: torch.Tensor | None = None, *,
+          out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """[M, H] rows of the dequantized table, times scale: zeros where the mask
+    is off, NaN where a token lies outside [0, V)."""
+    M = _tokens(head, tokens)
+    dev = tokens.device
+    mask = _mask(mask, M, dev)
+    code = _out_code(out_dtype)
+    out = torch.empty(M, head.H, dtype=out_dtype, device=dev)
+    _check(lib().qhead_embed(ctypes.byref(head.c()), tokens.data_ptr(), M, _ptr(mask), scale,
+                             out.data_ptr(), code, _stream(stream)))
+    return out
+
+
+def embed_bwd(head: Head, tokens: torch.Tensor, dout: torch.Tensor, scale: float = 1.0,
+              mask: torch.Tensor | None = None, *, dw: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of embed() with respect to the dequantized table, float32
+    [V, H]: added into dw (and dw returned) when it is given -- bwd_dw()'s, for
+    a tied table -- else into a new tensor whose other rows are 0."""
+    M = _tokens(head, tokens)
+    dev = tokens.device
+    mask = _mask(mask, M, dev)
+    _check_matrix("dout", dout, dev)
+    if tuple(dout.shape) != (M, head.H):
+        raise ValueError(f"dout must have shape [{M}, {head.H}], got {list(dout.shape)}")
+    add = dw is not None
+    if not add:
+        dw = torch.empty(head.V, head.H, dtype=torch.float32, device=dev)
+    elif (not isinstance(dw, torch.Tensor) or dw.dtype != torch.float32 or dw.device != dev
+          or tuple(dw.shape) != (head.V, head.H) or not dw.is_contiguous()):
+        raise ValueError(f"dw must be a contiguous float32 [{head.V}, {head.H}] tensor on {dev}")
+    c = head.c()
+    if workspace is None:
+        workspace = alloc_workspace(_size(lib().qhead_embed_bwd_workspace(ctypes.byref(c), M)), dev)
+    _check(lib().qhead_embed_bwd(ctypes.byref(c), tokens.data_ptr(), M, _ptr(mask), scale,
+                                 dout.data_ptr(), _SB_CODE[dout.dtype], dw.data_ptr(), int(add),
+                                 workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return dw
+
+
+def _check_param(name: str, t: torch.Tensor | None, H: int, dev, dtype=None):
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor) or t.dtype not in _SB_CODE or t.dim() != 1 \
+            or t.shape[0] != H or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float16, bfloat16 or float32 [{H}] tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must have weight's type")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, x on {dev}")
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+               eps: float = 1e-6, *, center: bool = True, out_dtype: torch.dtype = torch.bfloat16,
+               stream=None):
+    """(y [M, H] of out_dtype, mean [M] or None, rstd [M]): the layer norm of
+    x's rows (any float type; the row stride may exceed H), or with center off
+    its root-mean-square form.  y in bfloat16 is the head's h."""
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x must be a torch tensor")
+    dev = x.device
+    _check_matrix("x", x, dev, contiguous=False)
+    M, H = x.shape
+    if weight is None:
+        raise ValueError("weight is required")
+    _check_param("weight", weight, H, dev)
+    _check_param("bias", bias, H, dev, weight.dtype)
+    code = _out_code(out_dtype)
+    y = torch.empty(M, H, dtype=out_dtype, device=dev)
+    rstd = torch.empty(M, dtype=torch.float32, device=dev)
+    mean = torch.empty(M, dtype=torch.float32, device=dev) if center else None
+    _check(lib().qhead_layer_norm(x.data_ptr(), _SB_CODE[x.dtype], _row_stride(x), M, H,
+                                  weight.data_ptr(), _ptr(bias), _SB_CODE[weight.dtype], eps,
+                                  int(center), y.data_ptr(), code, _ptr(mean), rstd.data_ptr(),
+                                  _stream(stream)))
+    return y, mean, rstd
+
+
+def layer_norm_bwd(x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor | None,
+                   rstd: torch.Tensor, dy: torch.Tensor, *, want_dbias: bool = True,
+                   workspace: torch.Tensor | None = None, stream=None):
+    """(dx [M, H] of x's type, dweight [H] float32, dbias [H] float32 or None)
+    for dy = d/dy (any float type: bwd()'s float32 dh as it is); mean and rstd
+    are layer_norm()'s (mean None: the uncentred form)."""
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x must be a torch tensor")
+    dev = x.device
+    _check_matrix("x", x, dev, contiguous=False)
+    M, H = x.shape
+    _check_matrix("dy", dy, dev, contiguous=False)
+    if dy.shape != x.shape:
+        raise ValueError(f"dy must have shape [{M}, {H}], got {list(dy.shape)}")
+    if weight is None:
+        raise ValueError("weight is required")
+    _check_param("weight", weight, H, dev)
+    mean = _check_vec("mean", mean, M, (torch.float32,), dev, required=False)
+    rstd = _f32("rstd", rstd, M, dev)
+    dx = torch.empty(M, H, dtype=x.dtype, device=dev)
+    dw = torch.empty(H, dtype=torch.float32, device=dev)
+    db = torch.empty(H, dtype=torch.float32, device=dev) if want_dbias else None
+    if workspace is None:
+        workspace = alloc_workspace(_size(lib().qhead_layer_norm_bwd_workspace(M, H)), dev)
+    _check(lib().qhead_layer_norm_bwd(x.data_ptr(), _SB_CODE[x.dtype], _row_stride(x), M, H,
+                                      weight.data_ptr(), _SB_CODE[weight.dtype], _ptr(mean),
+                                      rstd.data_ptr(), dy.data_ptr(), _SB_CODE[dy.dtype],
+                                      _row_stride(dy), dx.data_ptr(), dw.data_ptr(), _ptr(db),
+                                      workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return dx, dw, db
+
+
+def _check_teacher(ids: torch.Tensor, tlogits: torch.Tensor, M: int, dev) -> int:
+    if not isinstance(ids, torch.Tensor) or ids.dtype != torch.int32 or ids.dim() != 2 \
+            or not ids.is_contiguous() or ids.shape[0] != M or ids.device != dev:
+        raise ValueError(f"ids must be a contiguous int32 [{M}, K] tensor on {dev}")
+    _check_matrix("tlogits", tlogits, dev)
+    if tlogits.shape != ids.shape:
+        raise ValueError(f"tlogits must have ids' shape {list(ids.shape)}, got "
+                         f"{list(tlogits.shape)}")
+    return int(ids.shape[1])
+
+
+def distill_fwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.Tensor,
+                temperature: float = 1.0, mask: torch.Tensor | None = None, *,
+                workspace: torch.Tensor | None = None, stream=None):
+    """(loss [M], lse [M], kept [M, K + 4]), float32: each row's cross entropy of
+    the head against a teacher's top logits (ids int32 [M, K], negative =
+    padding; tlogits [M, K]), less the teacher's entropy; see
+    qhead_distill_fwd.  lse is of the logits over the temperature; kept begins
+    with the listed tokens' exact logits; distill_bwd() takes both."""
+    M = _check_h(head, h)
+    dev = h.device
+    K = _check_teacher(ids, tlogits, M, dev)
+    mask = _mask(mask, M, dev)
+    loss = torch.empty(M, dtype=torch.float32, device=dev)
+    lse = torch.empty(M, dtype=torch.float32, device=dev)
+    kept = torch.empty(M, K + 4, dtype=torch.float32, device=dev)
+    c = head.c()
+    if workspace is None:
+        n = _size(lib().qhead_distill_fwd_workspace(ctypes.byref(c), M, K))
+        workspace = alloc_workspace(n, dev)
+    _check(lib().qhead_distill_fwd(ctypes.byref(c), h.data_ptr(), M, ids.data_ptr(),
+                                   tlogits.data_ptr(), _SB_CODE[tlogits.dtype], K, temperature,
+                                   _ptr(mask), loss.data_ptr(), lse.data_ptr(), kept.data_ptr(),
+                                   workspace.data_ptr(), workspace.numel(), _stream(stream)))
+    return loss, lse, kept
+
+
+def distill_bwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.Tensor,
+                kept: torch.Tensor, lse: torch.Tensor, dloss: torch.Tensor, temperature: float = 1.0,
+                mask: torch.Tensor | None = None, *, workspace: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """dh [M, H] bfloat16 of sum_m dloss[m] * loss[m], from distill_fwd()'s kept
+    and lse."""
+    M = _check_h(head, h)
+    dev = h.device
+    K = _check_teacher(ids, tlogits, M, dev)
+    mask = _mask(mask, M, dev)
+    lse, dloss = _f32("lse", lse, M, dev), _f32("dloss", dloss, M, dev)
+    _check_matrix("kept", kept, dev)
+    if kept.dtype != torch.float32 or tuple(kept.shape) != (M, K + 4):
+        raise ValueError(f"kept must be a float32 [{M}, {K + 4}] tensor")
+    dh = torch.empty(M, head.H, dtype=torch.bfloat16, device=dev)
+    c = head.c()
+    if workspace is None:
+        n = _size(lib().qhead_distill_bwd_workspace(ctypes.byref(c), M, K))
+        workspace = alloc_workspace(n, dev)
+    _check(lib().qhead_distill_bwd(ctypes.byref(c), h.data_ptr(), M, ids.data_ptr(),
+                                   tlogits.data_ptr(), _SB_CODE[tlogits.dtype], K, temperature,
+                                   _ptr(mask), kept.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
+                                   dh.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                   _stream(stream)))
+    return dh
