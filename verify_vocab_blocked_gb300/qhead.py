@@ -165,15 +165,16 @@ class Head:
         return int(self.wq.shape[1]) * 32 // self.bits
 
     def c(self) -> CHead:
-        for t in (self.wq, self.scales, self.biases):
-            if not t.is_contiguous():
-                raise ValueError("head tensors must be contiguous")
-        if self.scales.dtype not in _SB_CODE or self.biases.dtype != self.scales.dtype:
+        wq, scales, biases = self.wq, self.scales, self.biases
+        if not (wq.is_contiguous() and scales.is_contiguous() and biases.is_contiguous()):
+            raise ValueError("head tensors must be contiguous")
+        code = _SB_CODE.get(scales.dtype)
+        if code is None or biases.dtype != scales.dtype:
             raise ValueError("scales and biases must share one type: float16, bfloat16 or "
                              "float32")
-        return CHead(self.wq.data_ptr(), self.scales.data_ptr(), self.biases.data_ptr(),
-                     self.V, self.H, self.bits, self.group, _SB_CODE[self.scales.dtype],
-                     float(self.softcap))
+        V, words = wq.shape
+        return CHead(wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), V,
+                     words * 32 // self.bits, self.bits, self.group, code, self.softcap)
 
     @staticmethod
     def from_numpy(wq, scales, biases, bits, group=64, softcap=0.0, device="cuda",
@@ -201,8 +202,11 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 
 def _stream(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    """The handle of the given stream, or of the current device's current one
+    (read without building a Stream object, a fifth of a small call's time)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check_h(head: Head, h: torch.Tensor, what: str = "[M, H]") -> int:
