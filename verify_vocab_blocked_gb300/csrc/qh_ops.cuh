@@ -64,6 +64,28 @@ __device__ __forceinline__ void store_as(void* p, int64_t i, int type, float v) 
     else static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
+// Two fp32 lanes per instruction (one issue slot for two products or sums).
+__device__ __forceinline__ unsigned long long f2_bits(float2 a) {
+    return *reinterpret_cast<unsigned long long*>(&a);
+}
+__device__ __forceinline__ float2 bits_f2(unsigned long long a) { return *reinterpret_cast<float2*>(&a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+    return bits_f2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+    return bits_f2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+    return bits_f2(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 inline int type_bytes(int type) { return type == kSbF32 ? 4 : 2; }
 
 // ---------------------------------------------------------------- embedding
