@@ -350,7 +350,7 @@ int qhead_embed(const qhead_head* head, const int32_t* tokens, int64_t M, const 
  * summed in fp32, rows in ascending order in a fixed grouping (deterministic;
  * no atomic additions).  Only the head's V and H matter.
  *   dout      device, [M, H] of type dout_dtype, 16-byte aligned.
- *   dw        device, float [V, H], 16-byte aligned: the layout of
+ *   dw        device, float [V, H], 32-byte aligned: the layout of
  *             qhead_bwd_dw's dw, so that a tied table's two gradients can be
  *             added into one buffer.  Rows whose token lies outside [0, V)
  *             contribute nothing.  Without accumulate every element is written.

@@ -813,7 +813,7 @@ size_t qhead_embed_bwd_workspace(const qhead_head* head, int64_t M) {
     g_err.clear();
     if (check_head(head) || check_rows(M)) return (size_t)-1;
     if (M == 0) return 0;
-    return qh::plan_embed_bwd(M, head->V, head->H).total;
+    return qh::plan_embed_bwd(M, head->H).total;
 }
 
 int qhead_embed_bwd(const qhead_head* head, const int32_t* tokens, int64_t M, const uint8_t* mask,
@@ -826,7 +826,7 @@ int qhead_embed_bwd(const qhead_head* head, const int32_t* tokens, int64_t M, co
         return fail(QHEAD_EUNSUPPORTED, "dout_dtype must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
     if (!(scale - scale == 0.f)) return fail(QHEAD_EINVAL, "scale must be finite");
     if (!dw) return fail(QHEAD_EINVAL, "dw is required");
-    if (misaligned(dw, 16)) return fail(QHEAD_EINVAL, "dw must be 16-byte aligned");
+    if (misaligned(dw, 32)) return fail(QHEAD_EINVAL, "dw must be 32-byte aligned");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (M == 0) {
         if (accumulate) return QHEAD_OK;
@@ -835,7 +835,7 @@ int qhead_embed_bwd(const qhead_head* head, const int32_t* tokens, int64_t M, co
     }
     if (!tokens || !dout) return fail(QHEAD_EINVAL, "tokens and dout are required");
     if (misaligned(dout, 16)) return fail(QHEAD_EINVAL, "dout must be 16-byte aligned");
-    const qh::EmbedBwdPlan p = qh::plan_embed_bwd(M, head->V, head->H);
+    const qh::EmbedBwdPlan p = qh::plan_embed_bwd(M, head->H);
     if ((rc = check_workspace(workspace, workspace_bytes, p.total))) return rc;
     const cudaError_t e = qh::launch_embed_bwd(p, workspace, head->V, head->H, tokens, mask, M, scale,
                                                dout, dout_dtype, dw, accumulate != 0, st);

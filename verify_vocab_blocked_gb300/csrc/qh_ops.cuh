@@ -47,6 +47,19 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
     for (int i = 0; i < 4; ++i) o[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
     *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(o);
 }
+// Eight fp32 in one 32-byte access (the address 32-byte aligned).
+__device__ __forceinline__ void load8_wide(const float* p, float (&v)[8]) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+                   "=f"(v[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void store8_wide(float* p, const float (&v)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]),
+                 "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
 // The same on a pointer whose element type (kSb*) is known at run time only.
 __device__ __forceinline__ void load8_as(const void* p, int64_t i, int type, float (&v)[8]) {
     if (type == kSbF32) load8(static_cast<const float*>(p) + i, v);
@@ -86,6 +99,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
+// Code e (0 .. 7) of an 8-element unit (4 bits: one word, 8 bits: two) as fp32:
+// placed in the mantissa of 2^23, which is subtracted exactly (a conversion
+// instruction runs at an eighth of this rate).
+template <int BITS>
+__device__ __forceinline__ float code_f32(uint32_t w0, uint32_t w1, int e) {
+    const uint32_t q = BITS == 4 ? (w0 >> (4 * e)) & 15u : ((e < 4 ? w0 : w1) >> (8 * (e & 3))) & 255u;
+    return __uint_as_float(q | 0x4B000000u) - 8388608.f;
+}
+
 inline int type_bytes(int type) { return type == kSbF32 ? 4 : 2; }
 
 // ---------------------------------------------------------------- embedding
@@ -95,14 +117,13 @@ cudaError_t launch_embed(const uint32_t* wq, SbView sb, int64_t V, int H, int bi
                          void* out, int out_type, cudaStream_t st);
 
 // Workspace of the gradient: two buffers of sorted (token, row) pairs, the
-// count of live rows, a bit per vocab row (touched) and two partial rows per
-// chunk of sorted rows.
+// count of live rows and two partial rows per chunk of sorted rows.
 struct EmbedBwdPlan {
     int chunk = 0;       // sorted rows per block
     int64_t n_chunks = 0;
-    size_t off_info = 0, off_bits = 0, off_a = 0, off_b = 0, off_part = 0, total = 0;
+    size_t off_info = 0, off_a = 0, off_b = 0, off_part = 0, total = 0;
 };
-EmbedBwdPlan plan_embed_bwd(int64_t M, int64_t V, int H);
+EmbedBwdPlan plan_embed_bwd(int64_t M, int H);
 cudaError_t launch_embed_bwd(const EmbedBwdPlan& p, void* ws, int64_t V, int H,
                              const int32_t* tokens, const uint8_t* mask, int64_t M, float scale,
                              const void* dy, int dy_type, float* dw, bool accumulate,
