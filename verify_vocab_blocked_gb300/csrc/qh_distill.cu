@@ -28,7 +28,10 @@
 // kept [M, K + 4] holds, per row, the K exact capped logits, the two others'
 // and their vocab rows (as integer bits, -1: none).
 #include "qh_distill.cuh"
+#include "qh_ops.cuh"
 #include "qh_tc.cuh"
+
+#include <type_traits>
 
 namespace qh {
 
@@ -36,7 +39,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kDotsPerWarp = 2;  // teacher logits per warp of the prep kernel
+constexpr int kDotsPerWarp = 4;  // teacher logits of one row that a warp forms together
 
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
 
@@ -64,24 +67,100 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return v;
 }
 
+// This thread's part of the exact fp32 logits of N vocab rows v[] (-1: none)
+// under one row of h: the 8-element units u0, u0 + stride, ..., U of them at a time
+// with all their loads issued together.  w = fma(scale, code, bias) in fp32, two
+// lanes per instruction; a code becomes fp32 as a byte in the mantissa of 2^23.
+template <int BITS, int N, int U>
+__device__ __forceinline__ void exact_parts(const __nv_bfloat16* __restrict__ hrow,
+                                            const uint32_t* __restrict__ wq, const SbView& sb,
+                                            const int (&v)[N], int H, int u0, int stride,
+                                            float (&dot)[N]) {
+    const int units = H / 8;
+    float2 acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = both(0.f);
+    for (int ub = u0; ub < units; ub += U * stride) {
+        uint4 h[U];
+        uint32_t w[U][N][BITS / 4];
+        float s[U][N], b[U][N];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int u = ub + k * stride;
+            if (u >= units) continue;
+            h[k] = *reinterpret_cast<const uint4*>(hrow + 8 * u);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (v[i] < 0) continue;
+                const uint32_t* row = wq + (int64_t)v[i] * (H * BITS / 32);
+                if constexpr (BITS == 4) {
+                    w[k][i][0] = row[u];
+                } else {
+                    const uint2 x = reinterpret_cast<const uint2*>(row)[u];
+                    w[k][i][0] = x.x;
+                    w[k][i][1] = x.y;
+                }
+                const int64_t g = (int64_t)v[i] * (H / 64) + u / 8;
+                s[k][i] = sb_elem(sb.s, g, sb.type);
+                b[k][i] = sb_elem(sb.b, g, sb.type);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (ub + k * stride >= units) continue;
+            const uint32_t hw[4] = {h[k].x, h[k].y, h[k].z, h[k].w};
+            float2 hp[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                hp[e] = make_float2(__uint_as_float(hw[e] << 16), __uint_as_float(hw[e] & 0xffff0000u));
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (v[i] < 0) continue;
+                const float2 s2 = both(s[k][i]), b2 = both(b[k][i]);
+                // 4 bits: elements 2 j in the bytes of lo, 2 j + 1 in those of hi
+                const uint32_t lo = BITS == 4 ? w[k][i][0] & 0x0f0f0f0fu : w[k][i][0];
+                const uint32_t hi = BITS == 4 ? w[k][i][0] >> 4 & 0x0f0f0f0fu : w[k][i][BITS / 4 - 1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 q;
+                    if constexpr (BITS == 4) {
+                        q.x = __uint_as_float(__byte_perm(lo, 0x4B000000u, 0x7650u | e));
+                        q.y = __uint_as_float(__byte_perm(hi, 0x4B000000u, 0x7650u | e));
+                    } else {
+                        const uint32_t x = e < 2 ? lo : hi;
+                        q.x = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7650u | (2 * (e & 1))));
+                        q.y = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7650u | (2 * (e & 1) + 1)));
+                    }
+                    q = add2(q, both(-8388608.f));
+                    acc[i] = fma2(hp[e], fma2(s2, q, b2), acc[i]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) dot[i] = acc[i].x + acc[i].y;
+}
+
 // Row r of the compact list of left-out columns and the exact capped logits
 // of the row's teacher tokens.  Grid (M, K split): block (r, y) computes the
-// logits k in [8 y, 8 y + 8); block (r, 0) also writes the list: the distinct
-// valid ids in ascending order (each id's rank by counting: K^2 / 128 steps
-// per thread), INT32_MAX behind them.  Measured at 8192 rows of 1536 columns,
-// K = 32: see the table of the design document.
+// logits k in [16 y, 16 y + 16), four to a warp; block (r, 0) also writes the
+// list: the distinct valid ids in ascending order (each id's rank by counting:
+// K^2 / 128 steps per thread), INT32_MAX behind them.  The gathered rows' bytes
+// bound it, then the issue rate (one dot at a time and a conversion per code:
+// 234 us at 5744 rows of 1536, K = 32).
+template <int BITS>
 __global__ void __launch_bounds__(kThreads) distill_prep_kernel(
-    const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, int bits, float cap,
+    const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, float cap,
     const __nv_bfloat16* __restrict__ h, const int* __restrict__ pos,
-    const int32_t* __restrict__ ids, int K, int* __restrict__ sid, float* __restrict__ zk) {
+    const int32_t* __restrict__ ids, int K, int* __restrict__ sid, float* __restrict__ kept) {
     const int64_t r = blockIdx.x;
     const int i = pos[r];
     const int32_t* idr = ids + r * K;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int k0 = blockIdx.y * kWarps * kDotsPerWarp;
-    zk += r * (K + kKeptExtra);
+    kept += r * (K + kKeptExtra);
     if (i < 0) {
-        for (int k = k0 + threadIdx.x; k < min(K, k0 + kWarps * kDotsPerWarp); k += kThreads) zk[k] = 0.f;
+        for (int k = k0 + threadIdx.x; k < min(K, k0 + kWarps * kDotsPerWarp); k += kThreads) kept[k] = 0.f;
         return;
     }
     if (blockIdx.y == 0) {
@@ -109,15 +188,21 @@ __global__ void __launch_bounds__(kThreads) distill_prep_kernel(
         }
         for (int k = n_sh + threadIdx.x; k < K + 1; k += kThreads) out[k] = INT32_MAX;
     }
-#pragma unroll 1
+    const int kw = k0 + warp * kDotsPerWarp;
+    if (kw >= K) return;
+    int v[kDotsPerWarp];
+#pragma unroll
     for (int d = 0; d < kDotsPerWarp; ++d) {
-        const int k = k0 + d * kWarps + warp;
-        if (k >= K) break;
-        const int id = idr[k];
-        const bool ok = id >= 0 && (int64_t)id < V;
-        float z = 0.f;
-        if (ok) z = softcap_exact(warp_exact_logit<8>(h + r * (int64_t)H, wq, sb, id, H, bits), cap);
-        if (lane == 0) zk[k] = z;
+        const int id = kw + d < K ? idr[kw + d] : -1;
+        v[d] = id >= 0 && (int64_t)id < V ? id : -1;
+    }
+    float z[kDotsPerWarp];
+    exact_parts<BITS, kDotsPerWarp, 2>(h + r * (int64_t)H, wq, sb, v, H, lane, 32, z);
+#pragma unroll
+    for (int d = 0; d < kDotsPerWarp; ++d) {
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) z[d] += __shfl_xor_sync(0xffffffffu, z[d], o);
+        if (lane == 0 && kw + d < K) kept[kw + d] = v[d] >= 0 ? softcap_exact(z[d], cap) : 0.f;
     }
 }
 
@@ -164,9 +249,9 @@ __device__ __forceinline__ Teacher load_teacher(const int32_t* idr, const T* tr,
 // One block per row: merges the row's partials at the temperature, adds the
 // exact terms of the teacher's distinct tokens, replaces those of the two
 // largest other logits by exact ones, and forms the loss.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) distill_finalize_kernel(
-    const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, int bits, float cap,
+template <int BITS, typename T>
+__global__ void __launch_bounds__(kThreads, 6) distill_finalize_kernel(
+    const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, float cap,
     const __nv_bfloat16* __restrict__ h, const int* __restrict__ pos,
     const int32_t* __restrict__ ids, const T* __restrict__ tl, int K, float inv_t,
     float* kept, const Partial* __restrict__ part, const int* __restrict__ S_dev,
@@ -187,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) distill_finalize_kernel(
         return;
     }
     __shared__ Partial red_p[kWarps];
-    __shared__ float red[kWarps], cand_sh[2];
+    __shared__ float red[kWarps];
     __shared__ int id_sh[kMaxTeacher];
     __shared__ float t_sh[kMaxTeacher];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -241,17 +326,18 @@ __global__ void __launch_bounds__(kThreads) distill_finalize_kernel(
         fold(red_p[w].m, red_p[w].s);
         fin.merge(-INFINITY, 0.f, red_p[w].v1, red_p[w].i1, red_p[w].v2, red_p[w].i2);
     }
-    // The two candidates' exact logits, one warp each.
-    if (warp < 2) {
-        const int v = warp == 0 ? fin.i1 : fin.i2;
-        const float z = v < V ? softcap_exact(warp_exact_logit<8>(h + r * (int64_t)H, wq, sb, v, H, bits), cap)
-                              : -INFINITY;
-        if (lane == 0) cand_sh[warp] = z;
+    // The two candidates' exact logits, by the whole block.
+    const int cv[2] = {(int64_t)fin.i1 < V ? fin.i1 : -1, (int64_t)fin.i2 < V ? fin.i2 : -1};
+    float cand[2];
+    exact_parts<BITS, 2, 2>(h + r * (int64_t)H, wq, sb, cv, H, threadIdx.x, kThreads, cand);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        cand[c] = block_sum(cand[c], red);
+        cand[c] = cv[c] >= 0 ? softcap_exact(cand[c], cap) : -INFINITY;
     }
     const Teacher te = load_teacher(ids + r * K, tl + r * K, K, V, inv_t, id_sh, t_sh, red);
-    // (its barriers also publish cand_sh)
     // The largest of all terms, then their sum.
-    float top = fmaxf(m, fmaxf(cand_sh[0], cand_sh[1]));
+    float top = fmaxf(m, fmaxf(cand[0], cand[1]));
     for (int k = threadIdx.x; k < K; k += kThreads)
         if (id_sh[k] >= 0 && (int64_t)id_sh[k] < V) top = fmaxf(top, zr[k]);
     top = block_max(top, red);
@@ -275,11 +361,10 @@ __global__ void __launch_bounds__(kThreads) distill_finalize_kernel(
         if (m == -INFINITY) rest = 0.f;
         for (int c = 0; c < 2; ++c) {
             const float v = c == 0 ? fin.v1 : fin.v2;
-            const int at = c == 0 ? fin.i1 : fin.i2;
-            zr[K + c] = at < V ? cand_sh[c] : 0.f;
-            zr[K + 2 + c] = __int_as_float(at < V ? at : -1);
-            if (at < V)
-                rest += expf((cand_sh[c] - top) * inv_t) - expf((softcap_exact(v, cap) - top) * inv_t);
+            zr[K + c] = cv[c] >= 0 ? cand[c] : 0.f;
+            zr[K + 2 + c] = __int_as_float(cv[c]);
+            if (cv[c] >= 0)
+                rest += expf((cand[c] - top) * inv_t) - expf((softcap_exact(v, cap) - top) * inv_t);
         }
         const float l = logf(fmaxf(rest, 0.f) + sum);  // lse - top / T
         lse[r] = fmaf(top, inv_t, l);
@@ -372,8 +457,11 @@ cudaError_t launch_distill_prep(const uint32_t* wq, SbView sb, int64_t V, int H,
                                 const __nv_bfloat16* h, const int* pos, int64_t M,
                                 const int32_t* ids, int K, int* sid, float* kept, cudaStream_t st) {
     constexpr int per = kWarps * kDotsPerWarp;
-    distill_prep_kernel<<<dim3((unsigned)M, (unsigned)((K + per - 1) / per)), kThreads, 0, st>>>(
-        wq, sb, V, H, bits, cap, h, pos, ids, K, sid, kept);
+    const dim3 grid((unsigned)M, (unsigned)((K + per - 1) / per));
+    if (bits == 4)
+        distill_prep_kernel<4><<<grid, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, K, sid, kept);
+    else
+        distill_prep_kernel<8><<<grid, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, K, sid, kept);
     return cudaGetLastError();
 }
 
@@ -384,9 +472,10 @@ cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, in
                                     const int* S_dev, const int* err, float* loss, float* lse,
                                     cudaStream_t st) {
     return with_type(t_type, [&](auto* tag) {
-        distill_finalize_kernel<<<(unsigned)M, kThreads, 0, st>>>(
-            wq, sb, V, H, bits, cap, h, pos, ids, static_cast<decltype(tag)>(tl), K, inv_t, kept, part,
-            S_dev, err, loss, lse);
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
+        auto* fn = bits == 4 ? distill_finalize_kernel<4, T> : distill_finalize_kernel<8, T>;
+        fn<<<(unsigned)M, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, static_cast<const T*>(tl), K,
+                                             inv_t, kept, part, S_dev, err, loss, lse);
         return cudaGetLastError();
     });
 }
