@@ -67,23 +67,40 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return v;
 }
 
-// This thread's part of the exact fp32 logits of N vocab rows v[] (-1: none)
-// under one row of h: the 8-element units u0, u0 + stride, ..., U of them at a time
-// with all their loads issued together.  w = fma(scale, code, bias) in fp32, two
-// lanes per instruction; a code becomes fp32 as a byte in the mantissa of 2^23.
-template <int BITS, int N, int U>
-__device__ __forceinline__ void exact_parts(const __nv_bfloat16* __restrict__ hrow,
-                                            const uint32_t* __restrict__ wq, const SbView& sb,
-                                            const int (&v)[N], int H, int u0, int stride,
-                                            float (&dot)[N]) {
+// This thread's part of the exact fp32 logits of N vocab rows v[] (-1: none,
+// its part means nothing) under one row of h: the 8-element units u0, u0 + stride,
+// ..., U of them at a time with all their loads issued together.  w =
+// fma(scale, code, bias) in fp32, two lanes per instruction; a code becomes fp32 as
+// a byte in the mantissa of 2^23.  The issue rate bounds it, so the rows'
+// addresses are formed once and the scales' type is a parameter.
+template <int BITS, int SBT, int N, int U>
+__device__ __forceinline__ void exact_parts_of(const __nv_bfloat16* __restrict__ hrow,
+                                               const uint32_t* __restrict__ wq, const SbView& sb,
+                                               const int (&v)[N], int H, int u0, int stride,
+                                               float (&dot)[N]) {
+    using ST = std::conditional_t<SBT == kSbF32, float, unsigned short>;
+    using WT = std::conditional_t<BITS == 4, uint32_t, uint2>;
     const int units = H / 8;
     float2 acc[N];
+    const WT* wr[N];
+    const ST *sr[N], *br[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = both(0.f);
+    for (int i = 0; i < N; ++i) {
+        const int64_t row = v[i] < 0 ? 0 : v[i];
+        acc[i] = both(0.f);
+        wr[i] = reinterpret_cast<const WT*>(wq + row * (H * BITS / 32));
+        sr[i] = static_cast<const ST*>(sb.s) + row * (H / 64);
+        br[i] = static_cast<const ST*>(sb.b) + row * (H / 64);
+    }
+    auto widen = [](ST x) {
+        if constexpr (SBT == kSbF32) return x;
+        else if constexpr (SBT == kSbBf16) return __uint_as_float((uint32_t)x << 16);
+        else return __half2float(__ushort_as_half(x));
+    };
     for (int ub = u0; ub < units; ub += U * stride) {
         uint4 h[U];
-        uint32_t w[U][N][BITS / 4];
-        float s[U][N], b[U][N];
+        WT w[U][N];
+        ST s[U][N], b[U][N];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             const int u = ub + k * stride;
@@ -91,18 +108,9 @@ __device__ __forceinline__ void exact_parts(const __nv_bfloat16* __restrict__ hr
             h[k] = *reinterpret_cast<const uint4*>(hrow + 8 * u);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                if (v[i] < 0) continue;
-                const uint32_t* row = wq + (int64_t)v[i] * (H * BITS / 32);
-                if constexpr (BITS == 4) {
-                    w[k][i][0] = row[u];
-                } else {
-                    const uint2 x = reinterpret_cast<const uint2*>(row)[u];
-                    w[k][i][0] = x.x;
-                    w[k][i][1] = x.y;
-                }
-                const int64_t g = (int64_t)v[i] * (H / 64) + u / 8;
-                s[k][i] = sb_elem(sb.s, g, sb.type);
-                b[k][i] = sb_elem(sb.b, g, sb.type);
+                w[k][i] = wr[i][u];
+                s[k][i] = sr[i][u / 8];
+                b[k][i] = br[i][u / 8];
             }
         }
 #pragma unroll
@@ -115,11 +123,16 @@ __device__ __forceinline__ void exact_parts(const __nv_bfloat16* __restrict__ hr
                 hp[e] = make_float2(__uint_as_float(hw[e] << 16), __uint_as_float(hw[e] & 0xffff0000u));
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                if (v[i] < 0) continue;
-                const float2 s2 = both(s[k][i]), b2 = both(b[k][i]);
-                // 4 bits: elements 2 j in the bytes of lo, 2 j + 1 in those of hi
-                const uint32_t lo = BITS == 4 ? w[k][i][0] & 0x0f0f0f0fu : w[k][i][0];
-                const uint32_t hi = BITS == 4 ? w[k][i][0] >> 4 & 0x0f0f0f0fu : w[k][i][BITS / 4 - 1];
+                const float2 s2 = both(widen(s[k][i])), b2 = both(widen(b[k][i]));
+                // 4 bits: elements 2 e in the bytes of lo, 2 e + 1 in those of hi
+                uint32_t lo, hi;
+                if constexpr (BITS == 4) {
+                    lo = w[k][i] & 0x0f0f0f0fu;
+                    hi = w[k][i] >> 4 & 0x0f0f0f0fu;
+                } else {
+                    lo = w[k][i].x;
+                    hi = w[k][i].y;
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float2 q;
@@ -139,6 +152,16 @@ __device__ __forceinline__ void exact_parts(const __nv_bfloat16* __restrict__ hr
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) dot[i] = acc[i].x + acc[i].y;
+}
+
+template <int BITS, int N, int U>
+__device__ __forceinline__ void exact_parts(const __nv_bfloat16* __restrict__ hrow,
+                                            const uint32_t* __restrict__ wq, const SbView& sb,
+                                            const int (&v)[N], int H, int u0, int stride,
+                                            float (&dot)[N]) {
+    if (sb.type == kSbF16) exact_parts_of<BITS, kSbF16, N, U>(hrow, wq, sb, v, H, u0, stride, dot);
+    else if (sb.type == kSbBf16) exact_parts_of<BITS, kSbBf16, N, U>(hrow, wq, sb, v, H, u0, stride, dot);
+    else exact_parts_of<BITS, kSbF32, N, U>(hrow, wq, sb, v, H, u0, stride, dot);
 }
 
 // Row r of the compact list of left-out columns and the exact capped logits
