@@ -201,7 +201,7 @@ def test_binding_distill():
               (h[:, :128].contiguous(), ids, t)):
         with pytest.raises(ValueError):
             qhead.distill_fwd(hd, *a)
-    z, v = torch.zeros(3, 9), torch.zeros(3)
+    z, v = torch.zeros(3, 5 + qhead.DISTILL_KEPT), torch.zeros(3)
     for kept, lse, dl in ((z.half(), v, v), (z[:, :5].contiguous(), v, v), (z, v[:2], v), (z, v, v.double())):
         with pytest.raises(ValueError):
             qhead.distill_bwd(hd, h, ids, t, kept, lse, dl)

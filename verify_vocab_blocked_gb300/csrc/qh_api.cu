@@ -22,6 +22,7 @@
 
 static_assert(QHEAD_F16 == QHEAD_SB_F16 && QHEAD_BF16 == QHEAD_SB_BF16 && QHEAD_F32 == QHEAD_SB_F32,
               "element type codes");
+static_assert(QHEAD_DISTILL_KEPT == qh::kKeptExtra, "kept values per row");
 static_assert(QHEAD_SB_F16 == qh::kSbF16 && QHEAD_SB_BF16 == qh::kSbBf16 &&
                   QHEAD_SB_F32 == qh::kSbF32,
               "scale/bias element type codes");
@@ -979,6 +980,7 @@ int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const in
     ta.vt_begin = 0; ta.vt_end = (int)((head->V + qh::kTcFwdTileRows - 1) / qh::kTcFwdTileRows);
     ta.part = part; ta.S_out = S_dev;
     ta.l2e = 1.4426950408889634f * inv_t;
+    ta.unbias = qh::distill_unbias(head->H);
     ta.sid = sid; ta.sid_ld = (int)K + 1;
     hook_before(st);
     e = qh::launch_tc_fwd(th, tw, ta, head->bits, false, p.grid, st);
@@ -1045,6 +1047,7 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
         ta.lse = lse; ta.rows = rows; ta.coeff = coeff; ta.coeff_ld = p.chunk;
         ta.coeff_rows = (int)p.Mpad;
         ta.l2e = 1.4426950408889634f * inv_t;
+        ta.unbias = qh::distill_unbias(head->H);
         if ((e = qh::launch_tc_fwd(th, tw_logit, ta, head->bits, true, p.grid, st)))
             return cuda_fail(e, "tc_coeff");
         if ((e = qh::launch_distill_coeff(head->V, head->softcap, pos, M, ids, tlogits, t_dtype, (int)K,

@@ -16,17 +16,18 @@
 // the mass, and cancels badly in q_k - p_k.  So the teacher's K logits are
 // computed exactly (fp32, weights widened) once, in the forward, and kept:
 //   * the softmax epilogue leaves the teacher's columns out of its sum and the
-//     finalize adds their exact terms and replaces those of its two largest
-//     other columns, whose exact logits are kept as well;
+//     finalize adds their exact terms and replaces those of the largest other
+//     columns (up to kOthers), whose exact logits are kept as well;
 //   * the backward's coefficient block gets (q_k - p_k) sech2_k, formed in
-//     fp32 from the exact logits, written over the K + 2 columns of each row
-//     before the contraction with W, so the one-hot part of the gradient needs
-//     no gather of head rows of its own.  (The two other columns belong to
-//     it: with their exact terms in lse but the tensor-core logits in q, a row
-//     with mass there came out 1e-2 off, 1.7e-3 -- bf16's rounding -- with both.)
+//     fp32 from the exact logits, written over the K teacher's and the kept
+//     other columns of each row before the contraction with W, so the one-hot
+//     part of the gradient needs no gather of head rows of its own.  (The other
+//     columns belong to it: with their exact terms in lse but the tensor-core
+//     logits in q, a row with mass there came out 1e-2 off, 1.7e-3 -- bf16's
+//     rounding -- with both.)
 //
-// kept [M, K + 4] holds, per row, the K exact capped logits, the two others'
-// and their vocab rows (as integer bits, -1: none).
+// kept [M, K + 2 kOthers] holds, per row, the K exact capped logits, the others'
+// and their vocab rows plus one (as integer bits, 0: none).
 #include "qh_distill.cuh"
 #include "qh_ops.cuh"
 #include "qh_tc.cuh"
@@ -270,39 +271,48 @@ __device__ __forceinline__ Teacher load_teacher(const int32_t* idr, const T* tr,
 }
 
 // One block per row: merges the row's partials at the temperature, adds the
-// exact terms of the teacher's distinct tokens, replaces those of the two
-// largest other logits by exact ones, and forms the loss.
+// exact terms of the teacher's distinct tokens, replaces those of the largest
+// other logits by exact ones, and forms the loss.  The others: of the segments'
+// candidates those whose share of the sum is at least kShare (a tensor-core
+// logit is 3e-4 off: below that share it moves lse by less than 3e-7), the
+// kOthers largest if there are more.
+constexpr float kShare = 1e-3f;
+constexpr int kMaxShares = 1024;  // at most 1 / kShare terms have that share
+
 template <int BITS, typename T>
-__global__ void __launch_bounds__(kThreads, 6) distill_finalize_kernel(
+__global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
     const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, float cap,
     const __nv_bfloat16* __restrict__ h, const int* __restrict__ pos,
-    const int32_t* __restrict__ ids, const T* __restrict__ tl, int K, float inv_t,
+    const int32_t* __restrict__ ids, const T* __restrict__ tl, int K, float inv_t, float unbias,
     float* kept, const Partial* __restrict__ part, const int* __restrict__ S_dev,
     const int* __restrict__ err, float* __restrict__ loss, float* __restrict__ lse) {
+    __shared__ float2 cand_sh[kMaxShares];  // candidates (v, i) of enough share
+    __shared__ int n_cand;
+    __shared__ float red[kWarps];
+    __shared__ float2 red2[kWarps];
+    __shared__ int id_sh[kMaxTeacher];
+    __shared__ float t_sh[kMaxTeacher];
+    __shared__ float other_v[kOthers], other_z[kOthers];  // the others' logits: kernel's (raw), exact
+    __shared__ int other_i[kOthers];
     const int64_t r = blockIdx.x;
     const int i = pos[r];
     float* zr = kept + r * (K + kKeptExtra);
     // No other columns known: rows that are off or whose kernel gave up.
     auto no_others = [&]() {
-        zr[K] = zr[K + 1] = 0.f;
-        zr[K + 2] = zr[K + 3] = __int_as_float(-1);
+        for (int c = threadIdx.x; c < kOthers; c += kThreads) {
+            zr[K + c] = 0.f;
+            zr[K + kOthers + c] = 0.f;
+        }
     };
     if (i < 0) {
-        if (threadIdx.x == 0) {
-            loss[r] = lse[r] = 0.f;
-            no_others();
-        }
+        if (threadIdx.x == 0) loss[r] = lse[r] = 0.f;
+        no_others();
         return;
     }
-    __shared__ Partial red_p[kWarps];
-    __shared__ float red[kWarps];
-    __shared__ int id_sh[kMaxTeacher];
-    __shared__ float t_sh[kMaxTeacher];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = *S_dev;
-    // Partials: the candidates by RowState, the sum at the temperature.
-    RowState st;
-    st.init();
+    // Without a cap the kernel's factor `unbias` stands in its exponent: m in its terms.
+    const float mscale = cap > 0.f ? 1.f : unbias;
     float m = -INFINITY, s = 0.f;
     int bad = *err != 0;
     auto fold = [&](float om, float os) {
@@ -314,19 +324,16 @@ __global__ void __launch_bounds__(kThreads, 6) distill_finalize_kernel(
     for (int k = threadIdx.x; k < S; k += kThreads) {
         const Partial p = prow[k];
         bad |= p.status;
-        fold(p.m, p.s);
-        st.merge(-INFINITY, 0.f, p.v1, p.i1, p.v2, p.i2);
+        fold(p.m * mscale, p.s);
     }
+    if (threadIdx.x == 0) n_cand = 0;
     if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) {
-            loss[r] = lse[r] = nan_f();
-            no_others();
-        }
+        if (threadIdx.x == 0) loss[r] = lse[r] = nan_f();
+        no_others();
         return;
     }
 #pragma unroll
     for (int o = 1; o <= 16; o <<= 1) {
-        st.shfl_merge(o);
         // (the lower lane's state first, so that both partners end equal)
         const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
         const float am = lane & o ? om : m, as = lane & o ? os : s;
@@ -335,32 +342,15 @@ __global__ void __launch_bounds__(kThreads, 6) distill_finalize_kernel(
         s = as;
         fold(bm, bs);
     }
-    if (lane == 0) {
-        red_p[warp] = st.to_partial();
-        red_p[warp].m = m;
-        red_p[warp].s = s;
-    }
+    if (lane == 0) red2[warp] = make_float2(m, s);
     __syncthreads();
-    RowState fin;
-    fin.init();
     m = -INFINITY;
     s = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-        fold(red_p[w].m, red_p[w].s);
-        fin.merge(-INFINITY, 0.f, red_p[w].v1, red_p[w].i1, red_p[w].v2, red_p[w].i2);
-    }
-    // The two candidates' exact logits, by the whole block.
-    const int cv[2] = {(int64_t)fin.i1 < V ? fin.i1 : -1, (int64_t)fin.i2 < V ? fin.i2 : -1};
-    float cand[2];
-    exact_parts<BITS, 2, 2>(h + r * (int64_t)H, wq, sb, cv, H, threadIdx.x, kThreads, cand);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        cand[c] = block_sum(cand[c], red);
-        cand[c] = cv[c] >= 0 ? softcap_exact(cand[c], cap) : -INFINITY;
-    }
+    for (int w = 0; w < kWarps; ++w) fold(red2[w].x, red2[w].y);
+
+    // The teacher's side, and its tokens' exact terms.
     const Teacher te = load_teacher(ids + r * K, tl + r * K, K, V, inv_t, id_sh, t_sh, red);
-    // The largest of all terms, then their sum.
-    float top = fmaxf(m, fmaxf(cand[0], cand[1]));
+    float top = m;
     for (int k = threadIdx.x; k < K; k += kThreads)
         if (id_sh[k] >= 0 && (int64_t)id_sh[k] < V) top = fmaxf(top, zr[k]);
     top = block_max(top, red);
@@ -375,21 +365,70 @@ __global__ void __launch_bounds__(kThreads, 6) distill_finalize_kernel(
         if (first) sum += expf((z - top) * inv_t);
         const float lp = t_sh[k] - te.tmax - lsum;
         const float p = expf(lp);
-        if (p > 0.f) cross += p * (lp - (z - top) * inv_t);  // (log p - z/T, from the maximum)
+        if (p > 0.f) cross += p * (lp - (z - top) * inv_t);  // (log p - z/T, from `top`)
     }
     sum = block_sum(sum, red);
     cross = block_sum(cross, red);
-    if (threadIdx.x == 0) {
-        float rest = s * expf((m - top) * inv_t);
-        if (m == -INFINITY) rest = 0.f;
-        for (int c = 0; c < 2; ++c) {
-            const float v = c == 0 ? fin.v1 : fin.v2;
-            zr[K + c] = cv[c] >= 0 ? cand[c] : 0.f;
-            zr[K + 2 + c] = __int_as_float(cv[c]);
-            if (cv[c] >= 0)
-                rest += expf((cand[c] - top) * inv_t) - expf((softcap_exact(v, cap) - top) * inv_t);
+    float rest = m > -INFINITY ? s * expf((m - top) * inv_t) : 0.f;
+
+    // The candidates of enough share (in any order), then the largest of them
+    // by rank.  floor_z: the capped logit of that share; the cap is monotone.
+    const float floor_z = top + logf(kShare * (rest + sum)) / inv_t;
+    for (int k = threadIdx.x; k < S; k += kThreads) {
+        const float qv[2] = {prow[k].v1, prow[k].v2};
+        const int qi[2] = {prow[k].i1, prow[k].i2};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float v = qv[e];
+            const int at = qi[e];
+            // (a cap only shrinks a positive logit)
+            if ((v * unbias >= floor_z || floor_z < 0.f) && (int64_t)at < V &&
+                softcap_exact(v * unbias, cap) >= floor_z) {
+                const int n = atomicAdd(&n_cand, 1);
+                if (n < kMaxShares) cand_sh[n] = make_float2(v, __int_as_float(at));
+            }
         }
-        const float l = logf(fmaxf(rest, 0.f) + sum);  // lse - top / T
+    }
+    __syncthreads();
+    const int n_all = min(n_cand, kMaxShares), n_other = min(n_all, kOthers);
+    for (int k = threadIdx.x; k < n_all; k += kThreads) {
+        const float2 q = cand_sh[k];
+        int rank = 0;
+        for (int j = 0; j < n_all; ++j) {
+            const float2 o = cand_sh[j];
+            rank += better(o.x, __float_as_int(o.y), q.x, __float_as_int(q.y));
+        }
+        if (rank < kOthers) {
+            other_v[rank] = q.x;
+            other_i[rank] = __float_as_int(q.y);
+        }
+    }
+    __syncthreads();
+    // Their exact logits, two to a warp; the kernel's terms out.
+#pragma unroll 1
+    for (int c = 2 * warp; c < n_other; c += 2 * kWarps) {
+        const int cv[2] = {other_i[c], c + 1 < n_other ? other_i[c + 1] : -1};
+        float z[2];
+        exact_parts<BITS, 2, 2>(h + r * (int64_t)H, wq, sb, cv, H, lane, 32, z);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) z[e] += __shfl_xor_sync(0xffffffffu, z[e], o);
+            if (cv[e] >= 0 && lane == 0) other_z[c + e] = softcap_exact(z[e], cap);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        float add = 0.f;
+        for (int c = 0; c < kOthers; ++c) {
+            const bool have = c < n_other;
+            zr[K + c] = have ? other_z[c] : 0.f;
+            zr[K + kOthers + c] = __int_as_float(have ? other_i[c] + 1 : 0);
+            if (!have) continue;
+            rest -= expf((softcap_exact(other_v[c] * unbias, cap) - top) * inv_t);
+            add += expf((other_z[c] - top) * inv_t);
+        }
+        const float l = logf(fmaxf(rest, 0.f) + add + sum);  // lse - top / T
         lse[r] = fmaf(top, inv_t, l);
         float out = cross + l;
         if (te.tmax == -INFINITY) out = 0.f;  // nothing to learn from
@@ -400,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 6) distill_finalize_kernel(
 
 // One block per row, after the coefficient pass of the vocab chunk
 // [v_begin, v_begin + chunk): writes (q_k - p_k) sech2_k * 2^14 over the
-// teacher's columns and the two kept others (|q - p| <= 1: at most 16384 in
+// teacher's columns and the kept others (|q - p| <= 1: at most 16384 in
 // fp16, one rounding) and
 // the row's cotangent as the contraction kernel takes it, -dloss / T (0 for a
 // row with nothing to learn from, NaN for a bad one).
@@ -422,8 +461,8 @@ __global__ void __launch_bounds__(kThreads) distill_coeff_kernel(
     if (te.bad || te.tmax == -INFINITY) return;
     const float rsum = 1.f / te.tsum, l = lse[r];
     const float* zr = kept + r * (K + kKeptExtra);
-    for (int k = threadIdx.x; k < K + 2; k += kThreads) {
-        const int id = k < K ? id_sh[k] : __float_as_int(zr[k + 2]);
+    for (int k = threadIdx.x; k < K + kOthers; k += kThreads) {
+        const int id = k < K ? id_sh[k] : __float_as_int(zr[k + kOthers]) - 1;
         if (id < v_begin || id >= v_begin + chunk || (int64_t)id >= V) continue;
         float p = 0.f;  // the token's teacher mass (every entry that lists it)
         if (k < K)
@@ -498,7 +537,7 @@ cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, in
         using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
         auto* fn = bits == 4 ? distill_finalize_kernel<4, T> : distill_finalize_kernel<8, T>;
         fn<<<(unsigned)M, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, static_cast<const T*>(tl), K,
-                                             inv_t, kept, part, S_dev, err, loss, lse);
+                                             inv_t, distill_unbias(H), kept, part, S_dev, err, loss, lse);
         return cudaGetLastError();
     });
 }

@@ -6,7 +6,17 @@
 namespace qh {
 
 constexpr int kMaxTeacher = 1024;  // teacher entries per row
-constexpr int kKeptExtra = 4;      // kept values per row beyond the K logits
+constexpr int kOthers = 16;        // other vocab rows whose exact logits are kept, at most
+constexpr int kKeptExtra = 2 * kOthers;  // kept values per row beyond the K logits
+
+// What a tensor-core logit is multiplied by to take its mean error out.  Its
+// fp32 accumulation truncates: each of the H / 16 steps loses half an ulp of the
+// partial sum on average.  Over mantissas an ulp is 0.72 * 2^-23 of its value
+// in the mean, and the partial sum grows to the logit z evenly, so z comes out
+// short by about (H / 16) * 0.36 * 2^-23 / 2 = (H / 16) * 2.1e-8 of itself;
+// 1.6 to 1.8e-8 was measured from lse's mean error at H = 2560 (-1.2e-5 of 14 at
+// 512 rows, which shows in the loss; nothing else does).
+inline float distill_unbias(int H) { return 1.f + 1.7e-8f * (float)(H / 16); }
 
 // sid [Mpad, K + 1]: each compact row's distinct valid ids, ascending, then
 // INT32_MAX; kept [M, K + kKeptExtra]: in the first K the exact capped logits of

@@ -492,9 +492,12 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
         const int sub = warp & 3;  // TMEM sub-partition of this warp
         const int row = (int)rank * BM + sub * 32 + lane;  // row of the pair's 256-row unit
         const uint32_t lane_addr = static_cast<uint32_t>(sub * 32) << 16;
-        const float k2 = cap > 0.f ? 2.f * kLog2e / cap : 0.f;
-        // log2(e) / temperature (the distillation epilogues)
-        const float l2e = EPI == EPI_DISTILL || EPI == EPI_DCOEFF ? a.l2e : kLog2e;
+        // The distillation epilogues take the logits times a.unbias (with a cap in
+        // its argument, without one in the exponent's factor) and divide by the
+        // temperature: l2e = log2(e) / temperature.
+        constexpr bool kDistill = EPI == EPI_DISTILL || EPI == EPI_DCOEFF;
+        const float k2 = cap > 0.f ? 2.f * kLog2e / cap * (kDistill ? a.unbias : 1.f) : 0.f;
+        const float l2e = kDistill ? (cap > 0.f ? a.l2e : a.l2e * a.unbias) : kLog2e;
         int buf = 0;
         uint32_t aphase = 0;
         for (int u = cid; u < W.units; u += n_pairs) {

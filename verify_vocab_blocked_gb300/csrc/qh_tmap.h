@@ -88,8 +88,9 @@ struct TcFwdArgs {
     int64_t cold_out_rows;
     // Distillation epilogues (l2e > 0 selects them): l2e = log2(e) / temperature;
     // sid: per compact row, sid_ld ascending vocab rows (the last INT32_MAX)
-    // that the softmax epilogue leaves out.
+    // that the softmax epilogue leaves out; unbias: see distill_unbias.
     float l2e;
+    float unbias;
     const int* sid;
     int sid_ld;
     // Set by launch_tc_fwd: the scale and bias tables are staged by TMA.

@@ -20,6 +20,9 @@ QHEAD_SB_F16, QHEAD_SB_BF16, QHEAD_SB_F32 = 0, 1, 2
 _SB_CODE = {torch.float16: QHEAD_SB_F16, torch.bfloat16: QHEAD_SB_BF16,
             torch.float32: QHEAD_SB_F32}
 
+# Columns of distill_fwd's kept beyond the K logits (QHEAD_DISTILL_KEPT).
+DISTILL_KEPT = 32
+
 # Every symbol include/qhead.h declares.
 EXPORTS = ("qhead_fwd_workspace", "qhead_bwd_workspace", "qhead_fwd", "qhead_bwd",
            "qhead_last_error", "qhead_version", "qhead_time_next_head_kernel",
@@ -615,7 +618,7 @@ def _check_teacher(ids: torch.Tensor, tlogits: torch.Tensor, M: int, dev) -> int
 def distill_fwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.Tensor,
                 temperature: float = 1.0, mask: torch.Tensor | None = None, *,
                 workspace: torch.Tensor | None = None, stream=None):
-    """(loss [M], lse [M], kept [M, K + 4]), float32: each row's cross entropy of
+    """(loss [M], lse [M], kept [M, K + 32]), float32: each row's cross entropy of
     the head against a teacher's top logits (ids int32 [M, K], negative =
     padding; tlogits [M, K]), less the teacher's entropy; see
     qhead_distill_fwd.  lse is of the logits over the temperature; kept begins
@@ -626,7 +629,7 @@ def distill_fwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     mask = _mask(mask, M, dev)
     loss = torch.empty(M, dtype=torch.float32, device=dev)
     lse = torch.empty(M, dtype=torch.float32, device=dev)
-    kept = torch.empty(M, K + 4, dtype=torch.float32, device=dev)
+    kept = torch.empty(M, K + DISTILL_KEPT, dtype=torch.float32, device=dev)
     c = head.c()
     if workspace is None:
         n = _size(lib().qhead_distill_fwd_workspace(ctypes.byref(c), M, K))
@@ -650,8 +653,8 @@ def distill_bwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     mask = _mask(mask, M, dev)
     lse, dloss = _f32("lse", lse, M, dev), _f32("dloss", dloss, M, dev)
     _check_matrix("kept", kept, dev)
-    if kept.dtype != torch.float32 or tuple(kept.shape) != (M, K + 4):
-        raise ValueError(f"kept must be a float32 [{M}, {K + 4}] tensor")
+    if kept.dtype != torch.float32 or tuple(kept.shape) != (M, K + DISTILL_KEPT):
+        raise ValueError(f"kept must be a float32 [{M}, {K + DISTILL_KEPT}] tensor")
     dh = torch.empty(M, head.H, dtype=torch.bfloat16, device=dev)
     c = head.c()
     if workspace is None:
