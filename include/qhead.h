@@ -418,17 +418,20 @@ int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int
  *   loss, lse device, float [M]; inactive rows 0.  A row without a valid entry
  *             of finite logit has loss 0; one with an id >= V or a logit that
  *             is NaN or +inf has loss NaN.
- *   kept      device, float [M, K + QHEAD_DISTILL_KEPT], for the backward: in
- *             the first K columns the exact fp32 logits z of the valid entries
- *             (0 elsewhere), then the exact logits of the largest other vocab
- *             rows, up to 16, and (as int32 bits, 0: none) those rows plus one.
+ *   kept      device, float [M, qhead_distill_kept(head, M, K)], 32-byte
+ *             aligned, for the backward: in the first K columns the exact fp32
+ *             logits z of the valid entries (0 elsewhere), then the exact logits
+ *             of the largest other vocab rows, up to 16, and (as int32 bits, 0:
+ *             none) those rows plus one; at M <= 128 also the row's V logits
+ *             (-inf at the listed tokens), so that the backward need not form
+ *             them again.
  *   workspace device, >= qhead_distill_fwd_workspace(head, M, K) bytes,
  *             256-byte aligned.
- * Every M takes the tensor-core path.  The listed tokens and the largest
- * others enter lse with their exact logits, the rest with the tensor-core
- * kernel's.
+ * Up to 16 rows the weight-streaming kernel forms the logits, above them the
+ * tensor-core kernel.  The listed tokens and the largest others enter lse with
+ * their exact logits, the rest with the kernel's.
  */
-#define QHEAD_DISTILL_KEPT 32
+int64_t qhead_distill_kept(const qhead_head* head, int64_t M, int64_t K); /* columns; -1: invalid */
 size_t qhead_distill_fwd_workspace(const qhead_head* head, int64_t M, int64_t K);
 int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const int32_t* ids,
                       const void* tlogits, int t_dtype, int64_t K, float temperature,

@@ -255,3 +255,43 @@ def test_stalled_kernel_gives_nan():
     dh = qhead.distill_bwd(head, h, ids, t, kept, lse, dl, 1.0, mask)
     assert torch.isnan(dh[mask]).all() and (dh[3] == 0).all()
     assert torch.equal(loss, qhead.distill_fwd(head, h, ids, t)[0])
+
+
+@pytest.mark.parametrize("M", [1, 8, 9, 16, 17, 127, 128, 129])
+@pytest.mark.parametrize("bits,cap,T", [(4, 30.0, 1.0), (8, 0.0, 2.0)])
+def test_row_counts_where_the_kernels_change(M, bits, cap, T):
+    """Up to 16 rows the weight-streaming kernel, up to 128 the kept logits; a
+    vocabulary that is no multiple of their blocks, some rows masked."""
+    head, W, h, ids, t = _case(M, 1237, 384, bits, 11, cap, 60 + M)
+    mask = torch.rand(M, device="cuda", generator=gen(M)) < 0.8
+    _check(head, W, h, ids, t, T, mask)
+
+
+@pytest.mark.parametrize("M", [6, 60, 200])
+def test_student_far_from_its_teacher(M):
+    """The student's mass on tokens that the teacher does not list, a few of
+    them holding most of it: their logits are exact too, so the loss is within
+    1e-5 of its value (the tail's 3e-4 logit errors, averaged)."""
+    head, W, h, ids, t = _case(M, 4000, 256, 4, 8, 0.0, 71, near=False)
+    g = gen(72)
+    far = torch.randint(0, 4000, (M, 5), device="cuda", generator=g)
+    rows = W[far]
+    h = (0.1 * h.double() + torch.einsum("mk,mkh->mh", 14.0 / rows.square().sum(2), rows)).to(torch.bfloat16)
+    loss, _, _, _ = _check(head, W, h, ids, t, 1.0)
+    ref = distill64(W, h.double(), ids, t, 1.0, 0.0)[0]
+    assert ((loss.double() - ref).norm() / ref.norm()).item() <= 1e-5
+
+
+@pytest.mark.parametrize("M", [5, 40, 150])
+def test_nan_rows_stay_alone(M):
+    head, W, h, ids, t = _case(M, 900, 256, 8, 6, 30.0, 80)
+    good, _, _ = qhead.distill_fwd(head, h, ids, t)
+    h2 = h.clone()
+    h2[2, 7] = float("nan")
+    h2[4] = float("inf")
+    loss, lse, kept = qhead.distill_fwd(head, h2, ids, t)
+    dh = qhead.distill_bwd(head, h2, ids, t, kept, lse, torch.ones(M, device="cuda"))
+    bad = torch.zeros(M, dtype=torch.bool, device="cuda")
+    bad[2] = bad[4] = True
+    assert torch.isnan(loss[2]) and not torch.isfinite(loss[4]) and torch.isnan(dh[2]).all()
+    assert torch.equal(loss[~bad], good[~bad]) and torch.isfinite(dh[~bad]).all()

@@ -144,6 +144,9 @@ def test_workspace_queries(L):
     assert L.qhead_distill_fwd_workspace(hd, 5, 0) == BAD_SIZE
     assert L.qhead_distill_bwd_workspace(hd, 5, 1025) == BAD_SIZE
     assert L.qhead_distill_bwd_workspace(hd, -1, 4) == BAD_SIZE
+    assert L.qhead_distill_kept(hd, 129, 4) == 4 + 32
+    assert L.qhead_distill_kept(hd, 128, 4) == 40 + 1024      # V = 1000 in blocks of 32
+    assert L.qhead_distill_kept(hd, 5, 0) == -1
 
 
 # ---- the binding's own checks (CPU tensors: refused before any call)
@@ -193,7 +196,7 @@ def test_binding_layer_norm():
             qhead.layer_norm_bwd(*a)
 
 
-def test_binding_distill():
+def test_binding_distill(L):
     hd, h = _cpu_head(), torch.zeros(3, 256, dtype=torch.bfloat16)
     ids, t = torch.zeros(3, 5, dtype=torch.int32), torch.zeros(3, 5)
     for a in ((h.float(), ids, t), (h, ids.long(), t), (h, ids[:2], t), (h, ids, t[:, :4]),
@@ -201,7 +204,8 @@ def test_binding_distill():
               (h[:, :128].contiguous(), ids, t)):
         with pytest.raises(ValueError):
             qhead.distill_fwd(hd, *a)
-    z, v = torch.zeros(3, 5 + qhead.DISTILL_KEPT), torch.zeros(3)
+    cols = qhead.lib().qhead_distill_kept(ctypes.byref(hd.c()), 3, 5)
+    z, v = torch.zeros(3, cols), torch.zeros(3)
     for kept, lse, dl in ((z.half(), v, v), (z[:, :5].contiguous(), v, v), (z, v[:2], v), (z, v, v.double())):
         with pytest.raises(ValueError):
             qhead.distill_bwd(hd, h, ids, t, kept, lse, dl)

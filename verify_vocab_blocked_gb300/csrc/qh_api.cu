@@ -22,7 +22,6 @@
 
 static_assert(QHEAD_F16 == QHEAD_SB_F16 && QHEAD_BF16 == QHEAD_SB_BF16 && QHEAD_F32 == QHEAD_SB_F32,
               "element type codes");
-static_assert(QHEAD_DISTILL_KEPT == qh::kKeptExtra, "kept values per row");
 static_assert(QHEAD_SB_F16 == qh::kSbF16 && QHEAD_SB_BF16 == qh::kSbBf16 &&
                   QHEAD_SB_F32 == qh::kSbF32,
               "scale/bias element type codes");
@@ -328,7 +327,8 @@ int check_rows(int64_t M) {
 }
 
 // The distillation's workspace: the head plan's, then the left-out lists
-// (forward) or the rows' cotangents (backward).
+// (forward) or the rows' cotangents (backward).  The forward of few rows plans
+// the weight-streaming kernel's region and the softmax pass's partials.
 struct DistillPlan {
     FwdPlan f;
     BwdPlan b;
@@ -336,10 +336,13 @@ struct DistillPlan {
 };
 
 int plan_distill(const qhead_head* hd, int64_t M, int64_t K, bool bwd, DistillPlan* p) {
-    const int rc = bwd ? plan_bwd(hd, M, &p->b) : plan_fwd(hd, M, &p->f, true);
+    const bool few = !bwd && M <= qh::kFewM;
+    const int rc = bwd ? plan_bwd(hd, M, &p->b) : plan_fwd(hd, M, &p->f, !few);
     if (rc) return rc;
     p->off_extra = align_up(bwd ? p->b.total : p->f.total, 256);
-    p->total = p->off_extra + (bwd ? 4 * (size_t)M : 4 * (size_t)p->f.Mpad * (size_t)(K + 1));
+    p->total = p->off_extra + (bwd   ? 4 * (size_t)M
+                               : few ? sizeof(qh::Partial) * (size_t)M * qh::kFewSplits
+                                     : 4 * (size_t)p->f.Mpad * (size_t)(K + 1));
     return QHEAD_OK;
 }
 
@@ -904,6 +907,12 @@ int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int
     return e ? cuda_fail(e, "layer_norm_bwd") : QHEAD_OK;
 }
 
+int64_t qhead_distill_kept(const qhead_head* head, int64_t M, int64_t K) {
+    g_err.clear();
+    if (check_distill(head, M, K)) return -1;
+    return qh::kept_columns(M, K, head->V);
+}
+
 size_t qhead_distill_fwd_workspace(const qhead_head* head, int64_t M, int64_t K) {
     g_err.clear();
     if (check_distill(head, M, K)) return (size_t)-1;
@@ -943,6 +952,7 @@ int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const in
     if (M == 0) return QHEAD_OK;
     if ((rc = check_distill_inputs(h, ids, tlogits, t_dtype, temperature))) return rc;
     if (!loss || !lse || !kept) return fail(QHEAD_EINVAL, "loss, lse and kept are required");
+    if (misaligned(kept, 32)) return fail(QHEAD_EINVAL, "kept must be 32-byte aligned");
     DistillPlan dp;
     if ((rc = plan_distill(head, M, K, false, &dp))) return rc;
     if ((rc = check_workspace(workspace, workspace_bytes, dp.total))) return rc;
@@ -960,10 +970,31 @@ int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const in
     qh::Partial* part = at<qh::Partial>(workspace, p.off_part);
     int* sid = at<int>(workspace, dp.off_extra);
     const float inv_t = 1.f / temperature;
-    if ((rc = stage_rows(mask, hb, M, p.Mpad, head, rows, pos, count, err, h16, st))) return rc;
+    const int64_t ld = qh::kept_columns(M, K, head->V);
+    float* zout = M <= qh::kKeepLogitsM ? kept + qh::kept_logits_at(K) : nullptr;
     cudaError_t e;
+    if (M <= qh::kFewM) {
+        // The weight-streaming kernel compacts and converts the rows itself.
+        qh::Partial* few = at<qh::Partial>(workspace, dp.off_extra);
+        hook_before(st);
+        e = qh::launch_stream_fwd(head->wq, sc, bi, head->V, head->H, head->bits, head->softcap, hb, mask, M,
+                                  rows, pos, count, part, p.S, err, stall, st, zout, ld);
+        hook_after(st);
+        if (e) return cuda_fail(e, "stream_fwd");
+        if ((e = qh::launch_distill_prep(head->wq, sb_view(head), head->V, head->H, head->bits,
+                                         head->softcap, hb, pos, M, ids, (int)K, nullptr, kept, ld, zout,
+                                         st)))
+            return cuda_fail(e, "distill_prep");
+        if ((e = qh::launch_distill_split(zout, ld, head->V, head->softcap, inv_t, pos, M, few, st)))
+            return cuda_fail(e, "distill_split");
+        e = qh::launch_distill_finalize(head->wq, sb_view(head), head->V, head->H, head->bits,
+                                        head->softcap, hb, pos, M, ids, tlogits, t_dtype, (int)K, inv_t, 1.f,
+                                        kept, ld, few, qh::kFewSplits, nullptr, err, loss, lse, st);
+        return e ? cuda_fail(e, "distill_finalize") : QHEAD_OK;
+    }
+    if ((rc = stage_rows(mask, hb, M, p.Mpad, head, rows, pos, count, err, h16, st))) return rc;
     if ((e = qh::launch_distill_prep(head->wq, sb_view(head), head->V, head->H, head->bits, head->softcap,
-                                     hb, pos, M, ids, (int)K, sid, kept, st)))
+                                     hb, pos, M, ids, (int)K, sid, kept, ld, nullptr, st)))
         return cuda_fail(e, "distill_prep");
     CUtensorMap th, tw;
     if (!qh::tmap_rows_f16_sw128(&th, h16, head->H, p.Mpad, 128) ||
@@ -974,17 +1005,18 @@ int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const in
     ta.scales = sc; ta.biases = bi; ta.V = head->V; ta.H = head->H; ta.cap = head->softcap;
     ta.count = count; ta.err = err; ta.stall = stall;
     ta.vt_begin = 0; ta.vt_end = (int)((head->V + qh::kTcFwdTileRows - 1) / qh::kTcFwdTileRows);
-    ta.part = part; ta.S_out = S_dev;
+    ta.part = part; ta.S_out = S_dev; ta.rows = rows;
     ta.l2e = 1.4426950408889634f * inv_t;
     ta.unbias = qh::distill_unbias(head->H);
     ta.sid = sid; ta.sid_ld = (int)K + 1;
+    ta.zout = zout; ta.zout_ld = ld;
     hook_before(st);
     e = qh::launch_tc_fwd(th, tw, ta, head->bits, false, p.grid, st);
     hook_after(st);
     if (e) return cuda_fail(e, "tc_fwd");
     e = qh::launch_distill_finalize(head->wq, sb_view(head), head->V, head->H, head->bits, head->softcap,
-                                    hb, pos, M, ids, tlogits, t_dtype, (int)K, inv_t, kept, part, S_dev, err,
-                                    loss, lse, st);
+                                    hb, pos, M, ids, tlogits, t_dtype, (int)K, inv_t, ta.unbias, kept, ld,
+                                    part, 0, S_dev, err, loss, lse, st);
     return e ? cuda_fail(e, "distill_finalize") : QHEAD_OK;
 }
 
@@ -1001,6 +1033,7 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
     if ((rc = check_distill_inputs(h, ids, tlogits, t_dtype, temperature))) return rc;
     if (!kept || !lse || !dloss || !dh) return fail(QHEAD_EINVAL, "kept, lse, dloss and dh are required");
     if (misaligned(dh, 16)) return fail(QHEAD_EINVAL, "dh must be 16-byte aligned");
+    if (misaligned(kept, 32)) return fail(QHEAD_EINVAL, "kept must be 32-byte aligned");
     DistillPlan dp;
     if ((rc = plan_distill(head, M, K, true, &dp))) return rc;
     if ((rc = check_workspace(workspace, workspace_bytes, dp.total))) return rc;
@@ -1018,7 +1051,17 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
     float* dhp = at<float>(workspace, p.off_dhp);
     float* geff = at<float>(workspace, dp.off_extra);
     const float inv_t = 1.f / temperature;
-    if ((rc = stage_rows(mask, hb, M, p.Mpad, head, rows, pos, count, err, h16, st))) return rc;
+    const int64_t ld = qh::kept_columns(M, K, head->V);
+    // The coefficients from the kept logits, unless the stall switch wants the
+    // logit kernel.
+    const float* z = M <= qh::kKeepLogitsM && !stall ? kept + qh::kept_logits_at(K) : nullptr;
+    cudaError_t e;
+    if (z) {
+        if ((e = qh::launch_compact(mask, M, p.Mpad, rows, pos, count, err, st)))
+            return cuda_fail(e, "compact");
+    } else if ((rc = stage_rows(mask, hb, M, p.Mpad, head, rows, pos, count, err, h16, st))) {
+        return rc;
+    }
     CUtensorMap th, tw_logit, tcoef, tw_dh;
     const int wpr = head->H * head->bits / 32;
     if (!qh::tmap_rows_f16_sw128(&th, h16, head->H, p.Mpad, 128) ||
@@ -1032,7 +1075,6 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
     const int tr = qh::kTcFwdTileRows;
     const int n_vt = (int)((head->V + tr - 1) / tr);
     const int vt_chunk = (int)(p.chunk / tr);
-    cudaError_t e;
     hook_before(st);
     for (int vt0 = 0; vt0 < n_vt; vt0 += vt_chunk) {
         const int vt1 = vt0 + vt_chunk < n_vt ? vt0 + vt_chunk : n_vt;
@@ -1044,10 +1086,16 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
         ta.coeff_rows = (int)p.Mpad;
         ta.l2e = 1.4426950408889634f * inv_t;
         ta.unbias = qh::distill_unbias(head->H);
-        if ((e = qh::launch_tc_fwd(th, tw_logit, ta, head->bits, true, p.grid, st)))
+        if (z) {
+            if ((e = qh::launch_distill_from_logits(z, ld, head->V, head->softcap, inv_t, pos, M, lse, coeff,
+                                                    p.chunk, (int64_t)vt0 * tr, (int64_t)(vt1 - vt0) * tr,
+                                                    st)))
+                return cuda_fail(e, "distill_from_logits");
+        } else if ((e = qh::launch_tc_fwd(th, tw_logit, ta, head->bits, true, p.grid, st))) {
             return cuda_fail(e, "tc_coeff");
+        }
         if ((e = qh::launch_distill_coeff(head->V, head->softcap, pos, M, ids, tlogits, t_dtype, (int)K,
-                                          inv_t, kept, lse, dloss, geff, coeff, p.chunk, (int64_t)vt0 * tr,
+                                          inv_t, kept, ld, lse, dloss, geff, coeff, p.chunk, (int64_t)vt0 * tr,
                                           (int64_t)(vt1 - vt0) * tr, st)))
             return cuda_fail(e, "distill_coeff");
         qh::TcDhArgs da{};

@@ -26,8 +26,14 @@
 //     logits in q, a row with mass there came out 1e-2 off, 1.7e-3 -- bf16's
 //     rounding -- with both.)
 //
-// kept [M, K + 2 kOthers] holds, per row, the K exact capped logits, the others'
-// and their vocab rows plus one (as integer bits, 0: none).
+// kept [M, ld] holds, per row, the K exact capped logits, the others' and their
+// vocab rows plus one (as integer bits, 0: none), and at up to kKeepLogitsM rows
+// the row's V logits, -inf at the teacher's: the backward then forms its
+// coefficients from them instead of running the logit kernel again (232 us of
+// 700 at 13 rows of the 262144 x 2560 head; at 4 V bytes a row they are smaller
+// than the backward's coefficient block).  Up to kFewM rows the weight-streaming
+// kernel writes them, whose cost follows the rows (the tensor-core kernel's does
+// not: 227 us from 1 to 128), and a softmax pass of its own reads them.
 #include "qh_distill.cuh"
 #include "qh_ops.cuh"
 #include "qh_tc.cuh"
@@ -169,25 +175,27 @@ __device__ __forceinline__ void exact_parts(const __nv_bfloat16* __restrict__ hr
 // of the row's teacher tokens.  Grid (M, K split): block (r, y) computes the
 // logits k in [16 y, 16 y + 16), four to a warp; block (r, 0) also writes the
 // list: the distinct valid ids in ascending order (each id's rank by counting:
-// K^2 / 128 steps per thread), INT32_MAX behind them.  The gathered rows' bytes
+// K^2 / 128 steps per thread), INT32_MAX behind them.  With the logits given
+// (zout; no list then) it takes the teacher's out of them itself.  The gathered rows' bytes
 // bound it, then the issue rate (one dot at a time and a conversion per code:
 // 234 us at 5744 rows of 1536, K = 32).
 template <int BITS>
 __global__ void __launch_bounds__(kThreads) distill_prep_kernel(
     const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, float cap,
     const __nv_bfloat16* __restrict__ h, const int* __restrict__ pos,
-    const int32_t* __restrict__ ids, int K, int* __restrict__ sid, float* __restrict__ kept) {
+    const int32_t* __restrict__ ids, int K, int* __restrict__ sid, float* kept, int64_t ld,
+    float* zout) {
     const int64_t r = blockIdx.x;
     const int i = pos[r];
     const int32_t* idr = ids + r * K;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int k0 = blockIdx.y * kWarps * kDotsPerWarp;
-    kept += r * (K + kKeptExtra);
+    kept += r * ld;
     if (i < 0) {
         for (int k = k0 + threadIdx.x; k < min(K, k0 + kWarps * kDotsPerWarp); k += kThreads) kept[k] = 0.f;
         return;
     }
-    if (blockIdx.y == 0) {
+    if (sid != nullptr && blockIdx.y == 0) {
         __shared__ int id_sh[kMaxTeacher];
         __shared__ uint8_t first_sh[kMaxTeacher];
         __shared__ int n_sh;
@@ -226,7 +234,10 @@ __global__ void __launch_bounds__(kThreads) distill_prep_kernel(
     for (int d = 0; d < kDotsPerWarp; ++d) {
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) z[d] += __shfl_xor_sync(0xffffffffu, z[d], o);
-        if (lane == 0 && kw + d < K) kept[kw + d] = v[d] >= 0 ? softcap_exact(z[d], cap) : 0.f;
+        if (lane == 0 && kw + d < K) {
+            kept[kw + d] = v[d] >= 0 ? softcap_exact(z[d], cap) : 0.f;
+            if (zout != nullptr && v[d] >= 0) zout[r * ld + v[d]] = -INFINITY;
+        }
     }
 }
 
@@ -284,8 +295,9 @@ __global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
     const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, float cap,
     const __nv_bfloat16* __restrict__ h, const int* __restrict__ pos,
     const int32_t* __restrict__ ids, const T* __restrict__ tl, int K, float inv_t, float unbias,
-    float* kept, const Partial* __restrict__ part, const int* __restrict__ S_dev,
-    const int* __restrict__ err, float* __restrict__ loss, float* __restrict__ lse) {
+    float* kept, int64_t ld, const Partial* __restrict__ part, int S,
+    const int* __restrict__ S_dev, const int* __restrict__ err, float* __restrict__ loss,
+    float* __restrict__ lse) {
     __shared__ float2 cand_sh[kMaxShares];  // candidates (v, i) of enough share
     __shared__ int n_cand;
     __shared__ float red[kWarps];
@@ -296,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
     __shared__ int other_i[kOthers];
     const int64_t r = blockIdx.x;
     const int i = pos[r];
-    float* zr = kept + r * (K + kKeptExtra);
+    float* zr = kept + r * ld;
     // No other columns known: rows that are off or whose kernel gave up.
     auto no_others = [&]() {
         for (int c = threadIdx.x; c < kOthers; c += kThreads) {
@@ -310,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = *S_dev;
+    if (S_dev) S = *S_dev;
     // Without a cap the kernel's factor `unbias` stands in its exponent: m in its terms.
     const float mscale = cap > 0.f ? 1.f : unbias;
     float m = -INFINITY, s = 0.f;
@@ -428,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
             rest -= expf((softcap_exact(other_v[c] * unbias, cap) - top) * inv_t);
             add += expf((other_z[c] - top) * inv_t);
         }
-        const float l = logf(fmaxf(rest, 0.f) + add + sum);  // lse - top / T
+        const float l = logf((rest < 0.f ? 0.f : rest) + add + sum);  // lse - top / T (NaN stays)
         lse[r] = fmaf(top, inv_t, l);
         float out = cross + l;
         if (te.tmax == -INFINITY) out = 0.f;  // nothing to learn from
@@ -446,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
 template <typename T>
 __global__ void __launch_bounds__(kThreads) distill_coeff_kernel(
     int64_t V, float cap, const int* __restrict__ pos, const int32_t* __restrict__ ids,
-    const T* __restrict__ tl, int K, float inv_t, const float* __restrict__ kept,
+    const T* __restrict__ tl, int K, float inv_t, const float* __restrict__ kept, int64_t ld_kept,
     const float* __restrict__ lse, const float* __restrict__ dloss, float* __restrict__ geff,
     __half* __restrict__ coeff, int64_t ld, int64_t v_begin, int64_t chunk) {
     const int64_t r = blockIdx.x;
@@ -460,7 +472,7 @@ __global__ void __launch_bounds__(kThreads) distill_coeff_kernel(
         geff[r] = te.bad ? nan_f() : te.tmax == -INFINITY ? 0.f : -dloss[r] * inv_t;
     if (te.bad || te.tmax == -INFINITY) return;
     const float rsum = 1.f / te.tsum, l = lse[r];
-    const float* zr = kept + r * (K + kKeptExtra);
+    const float* zr = kept + r * ld_kept;
     for (int k = threadIdx.x; k < K + kOthers; k += kThreads) {
         const int id = k < K ? id_sh[k] : __float_as_int(zr[k + kOthers]) - 1;
         if (id < v_begin || id >= v_begin + chunk || (int64_t)id >= V) continue;
@@ -473,6 +485,131 @@ __global__ void __launch_bounds__(kThreads) distill_coeff_kernel(
         const float c = (expf(fmaf(z, inv_t, -l)) - p) * fmaf(-th, th, 1.f);
         coeff[(int64_t)i * ld + (id - v_begin)] = __float2half_rn(c * 16384.f);
     }
+}
+
+// Softmax partials of the kept logits (few rows): block (s, r) takes split s of
+// row r; the largest capped logit, the sum at the temperature relative to it, and
+// the two largest raw logits of its threads' best.
+constexpr int kSplitThreads = 256;
+__global__ void __launch_bounds__(kSplitThreads) distill_split_kernel(
+    const float* __restrict__ z, int64_t ld, int64_t V, float cap, float inv_t,
+    const int* __restrict__ pos, Partial* __restrict__ part, int S) {
+    const int64_t r = blockIdx.y;
+    const int i = pos[r], sp = blockIdx.x;
+    if (i < 0) return;
+    const int64_t v0 = V * sp / S, v1 = V * (sp + 1) / S;
+    const float* zr = z + r * ld;
+    RowState st;
+    st.init();
+    float m = -INFINITY, s = 0.f;
+    bool bad = false;  // a NaN logit
+    for (int64_t vb = v0 + threadIdx.x; vb < v1; vb += 8 * kSplitThreads) {
+        float x[8], top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = vb + k * kSplitThreads < v1 ? zr[vb + k * kSplitThreads] : -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int at = (int)(vb + k * kSplitThreads);
+            bad |= x[k] != x[k];
+            if (x[k] > -INFINITY) {
+                if (better(x[k], at, st.v1, st.i1)) {
+                    st.v2 = st.v1; st.i2 = st.i1; st.v1 = x[k]; st.i1 = at;
+                } else if (better(x[k], at, st.v2, st.i2)) {
+                    st.v2 = x[k]; st.i2 = at;
+                }
+                x[k] = softcap_exact(x[k], cap);
+                top = fmaxf(top, x[k]);
+            }
+        }
+        if (top == -INFINITY) continue;
+        const float nm = fmaxf(m, top);
+        s *= m > -INFINITY ? expf((m - nm) * inv_t) : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (x[k] > -INFINITY) s += expf((x[k] - nm) * inv_t);
+        m = nm;
+    }
+    if (bad) {
+        m = 0.f;
+        s = nan_f();
+    }
+    __shared__ Partial red[kSplitThreads / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto fold = [&](float om, float os) {
+        const float nm = fmaxf(m, om);
+        if (nm > -INFINITY) s = s * expf((m - nm) * inv_t) + os * expf((om - nm) * inv_t);
+        m = nm;
+    };
+#pragma unroll
+    for (int o = 1; o <= 16; o <<= 1) {
+        st.shfl_merge(o);
+        const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
+        const float am = lane & o ? om : m, as = lane & o ? os : s;
+        const float bm = lane & o ? m : om, bs = lane & o ? s : os;
+        m = am;
+        s = as;
+        fold(bm, bs);
+    }
+    if (lane == 0) {
+        red[warp] = st.to_partial();
+        red[warp].m = m;
+        red[warp].s = s;
+    }
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    RowState all;
+    all.init();
+    m = -INFINITY;
+    s = 0.f;
+    for (int w = 0; w < kSplitThreads / 32; ++w) {
+        fold(red[w].m, red[w].s);
+        all.merge(-INFINITY, 0.f, red[w].v1, red[w].i1, red[w].v2, red[w].i2);
+    }
+    Partial p = all.to_partial();
+    p.m = m;
+    p.s = s;
+    part[(int64_t)i * S + sp] = p;
+}
+
+// The coefficient block of the chunk [v_begin, v_begin + chunk) from the kept
+// logits: q sech2 2^14 in fp16, zeros past V (and at the left-out columns, which
+// distill_coeff_kernel fills).  Thread = 8 columns of one active row; the rows
+// past the active ones are not written (nothing reads what the contraction
+// makes of them).
+__global__ void __launch_bounds__(256) distill_from_logits_kernel(
+    const float* __restrict__ z, int64_t ld, int64_t V, float cap, float inv_t,
+    const int* __restrict__ pos, const float* __restrict__ lse, __half* __restrict__ coeff, int64_t ldc,
+    int64_t v_begin, int64_t chunk) {
+    const int64_t r = blockIdx.y;
+    const int i = pos[r];
+    if (i < 0) return;
+    const int64_t c0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (c0 >= chunk) return;
+    const float l = lse[r];
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = -INFINITY;
+    const int64_t v = v_begin + c0;
+    if (v + 8 <= V) {
+        load8_wide(z + r * ld + v, x);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (v + k < V) x[k] = z[r * ld + v + k];
+    }
+    float o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        o[k] = 0.f;
+        if (x[k] == -INFINITY) continue;
+        float th = 0.f, zc = x[k];
+        if (cap > 0.f) {
+            th = tanhf(x[k] / cap);
+            zc = cap * th;
+        }
+        o[k] = expf(fmaf(zc, inv_t, -l)) * fmaf(-th, th, 1.f) * 16384.f;
+    }
+    store8(coeff + (int64_t)i * ldc + c0, o);
 }
 
 // One block per row: the K slices of the contraction in order, rounded once to
@@ -517,42 +654,60 @@ cudaError_t with_type(int type, F&& f) {
 
 cudaError_t launch_distill_prep(const uint32_t* wq, SbView sb, int64_t V, int H, int bits, float cap,
                                 const __nv_bfloat16* h, const int* pos, int64_t M,
-                                const int32_t* ids, int K, int* sid, float* kept, cudaStream_t st) {
+                                const int32_t* ids, int K, int* sid, float* kept, int64_t ld,
+                                float* zout, cudaStream_t st) {
     constexpr int per = kWarps * kDotsPerWarp;
     const dim3 grid((unsigned)M, (unsigned)((K + per - 1) / per));
     if (bits == 4)
-        distill_prep_kernel<4><<<grid, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, K, sid, kept);
+        distill_prep_kernel<4><<<grid, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, K, sid, kept, ld,
+                                                        zout);
     else
-        distill_prep_kernel<8><<<grid, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, K, sid, kept);
+        distill_prep_kernel<8><<<grid, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, K, sid, kept, ld,
+                                                        zout);
     return cudaGetLastError();
 }
 
 cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, int H, int bits,
                                     float cap, const __nv_bfloat16* h, const int* pos, int64_t M,
                                     const int32_t* ids, const void* tl, int t_type, int K,
-                                    float inv_t, float* kept, const Partial* part,
-                                    const int* S_dev, const int* err, float* loss, float* lse,
-                                    cudaStream_t st) {
+                                    float inv_t, float unbias, float* kept, int64_t ld,
+                                    const Partial* part, int S, const int* S_dev, const int* err,
+                                    float* loss, float* lse, cudaStream_t st) {
     return with_type(t_type, [&](auto* tag) {
         using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
         auto* fn = bits == 4 ? distill_finalize_kernel<4, T> : distill_finalize_kernel<8, T>;
         fn<<<(unsigned)M, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, static_cast<const T*>(tl), K,
-                                             inv_t, distill_unbias(H), kept, part, S_dev, err, loss, lse);
+                                             inv_t, unbias, kept, ld, part, S, S_dev, err, loss, lse);
         return cudaGetLastError();
     });
 }
 
 cudaError_t launch_distill_coeff(int64_t V, float cap, const int* pos, int64_t M,
                                  const int32_t* ids, const void* tl, int t_type, int K, float inv_t,
-                                 const float* kept, const float* lse, const float* dloss, float* geff,
-                                 __half* coeff, int64_t ld, int64_t v_begin, int64_t chunk,
-                                 cudaStream_t st) {
+                                 const float* kept, int64_t ld_kept, const float* lse,
+                                 const float* dloss, float* geff, __half* coeff, int64_t ld,
+                                 int64_t v_begin, int64_t chunk, cudaStream_t st) {
     return with_type(t_type, [&](auto* tag) {
         distill_coeff_kernel<<<(unsigned)M, kThreads, 0, st>>>(
-            V, cap, pos, ids, static_cast<decltype(tag)>(tl), K, inv_t, kept, lse, dloss, geff, coeff,
+            V, cap, pos, ids, static_cast<decltype(tag)>(tl), K, inv_t, kept, ld_kept, lse, dloss, geff, coeff,
             ld, v_begin, chunk);
         return cudaGetLastError();
     });
+}
+
+cudaError_t launch_distill_split(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
+                                 const int* pos, int64_t M, Partial* part, cudaStream_t st) {
+    distill_split_kernel<<<dim3(kFewSplits, (unsigned)M), kSplitThreads, 0, st>>>(z, ld, V, cap, inv_t, pos,
+                                                                                  part, kFewSplits);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_distill_from_logits(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
+                                       const int* pos, int64_t M, const float* lse, __half* coeff,
+                                       int64_t ldc, int64_t v_begin, int64_t chunk, cudaStream_t st) {
+    distill_from_logits_kernel<<<dim3((unsigned)((chunk / 8 + 255) / 256), (unsigned)M), 256, 0, st>>>(
+        z, ld, V, cap, inv_t, pos, lse, coeff, ldc, v_begin, chunk);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_distill_dh(const float* dhp, int S, int64_t Mpad, int H, const int* pos,

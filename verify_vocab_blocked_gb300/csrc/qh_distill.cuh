@@ -8,6 +8,16 @@ namespace qh {
 constexpr int kMaxTeacher = 1024;  // teacher entries per row
 constexpr int kOthers = 16;        // other vocab rows whose exact logits are kept, at most
 constexpr int kKeptExtra = 2 * kOthers;  // kept values per row beyond the K logits
+constexpr int64_t kKeepLogitsM = 128;  // rows up to which the logits are kept for the backward
+constexpr int64_t kFewM = 16;          // rows up to which the weight-streaming kernel forms them
+constexpr int kFewSplits = 64;         // vocab splits of their softmax pass
+
+// Columns of kept, and where a row's logits begin in it (whole 32-byte units;
+// the logits in whole blocks of 32).
+inline int64_t kept_logits_at(int64_t K) { return (K + kKeptExtra + 7) / 8 * 8; }
+inline int64_t kept_columns(int64_t M, int64_t K, int64_t V) {
+    return M <= kKeepLogitsM ? kept_logits_at(K) + (V + 31) / 32 * 32 : K + kKeptExtra;
+}
 
 // What a tensor-core logit is multiplied by to take its mean error out.  Its
 // fp32 accumulation truncates: each of the H / 16 steps loses half an ulp of the
@@ -19,22 +29,28 @@ constexpr int kKeptExtra = 2 * kOthers;  // kept values per row beyond the K log
 inline float distill_unbias(int H) { return 1.f + 1.7e-8f * (float)(H / 16); }
 
 // sid [Mpad, K + 1]: each compact row's distinct valid ids, ascending, then
-// INT32_MAX; kept [M, K + kKeptExtra]: in the first K the exact capped logits of
+// INT32_MAX; kept [M, ld]: in the first K the exact capped logits of
 // the valid entries (0 for the others and for inactive rows).
 cudaError_t launch_distill_prep(const uint32_t* wq, SbView sb, int64_t V, int H, int bits, float cap,
                                 const __nv_bfloat16* h, const int* pos, int64_t M,
-                                const int32_t* ids, int K, int* sid, float* kept, cudaStream_t st);
+                                const int32_t* ids, int K, int* sid, float* kept, int64_t ld,
+                                float* zout, cudaStream_t st);
 cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, int H, int bits,
                                     float cap, const __nv_bfloat16* h, const int* pos, int64_t M,
                                     const int32_t* ids, const void* tl, int t_type, int K,
-                                    float inv_t, float* kept, const Partial* part,
-                                    const int* S_dev, const int* err, float* loss, float* lse,
-                                    cudaStream_t st);
+                                    float inv_t, float unbias, float* kept, int64_t ld,
+                                    const Partial* part, int S, const int* S_dev, const int* err,
+                                    float* loss, float* lse, cudaStream_t st);
 cudaError_t launch_distill_coeff(int64_t V, float cap, const int* pos, int64_t M,
                                  const int32_t* ids, const void* tl, int t_type, int K, float inv_t,
-                                 const float* kept, const float* lse, const float* dloss, float* geff,
-                                 __half* coeff, int64_t ld, int64_t v_begin, int64_t chunk,
-                                 cudaStream_t st);
+                                 const float* kept, int64_t ld_kept, const float* lse,
+                                 const float* dloss, float* geff, __half* coeff, int64_t ld,
+                                 int64_t v_begin, int64_t chunk, cudaStream_t st);
+cudaError_t launch_distill_split(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
+                                 const int* pos, int64_t M, Partial* part, cudaStream_t st);
+cudaError_t launch_distill_from_logits(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
+                                       const int* pos, int64_t M, const float* lse, __half* coeff,
+                                       int64_t ldc, int64_t v_begin, int64_t chunk, cudaStream_t st);
 cudaError_t launch_distill_dh(const float* dhp, int S, int64_t Mpad, int H, const int* pos,
                               int64_t M, const int* err, void* dh, cudaStream_t st);
 

@@ -190,7 +190,8 @@ cudaError_t launch_dependent(const void* fn, dim3 grid, dim3 block, size_t smem,
 cudaError_t launch_stream_fwd(const uint32_t* wq, const __half* scales, const __half* biases,
                               int64_t V, int H, int bits, float cap, const __nv_bfloat16* h,
                               const uint8_t* mask, int64_t M, int* rows, int* pos, int* count,
-                              Partial* part, int S, int* err, int stall, cudaStream_t st);
+                              Partial* part, int S, int* err, int stall, cudaStream_t st,
+                              float* zout = nullptr, int64_t zout_ld = 0);
 // Skip map of the blockMax early exit: skip[mt * n_vt + vt] = 1 when every
 // active row of 128-row tile mt has bmax - lse < ln(eps) on vocab tile vt and
 // none of them targets it.

@@ -94,9 +94,19 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t (&p)[4]) {
     p[3] = lop3_and_or(w8, 0x00F000F0u, 0x54005400u);
 }
 
+// The same pairs without their offsets: exact small integers.
+__device__ __forceinline__ void plain4(uint32_t (&p)[4]) {
+    p[0] = h2_as_u32(__hsub2(u32_as_h2(p[0]), u32_as_h2(0x64006400u)));
+    p[1] = h2_as_u32(__hsub2(u32_as_h2(p[1]), u32_as_h2(0x54005400u)));
+    p[2] = h2_as_u32(__hsub2(u32_as_h2(p[2]), u32_as_h2(0x64006400u)));
+    p[3] = h2_as_u32(__hsub2(u32_as_h2(p[3]), u32_as_h2(0x54005400u)));
+}
+
 // Two 8-bit codes of w with offset 1024: sel 0x5140 -> bytes 0, 1; 0x7362 -> 2, 3.
+template <bool PLAIN>
 __device__ __forceinline__ uint32_t codes8(uint32_t w, uint32_t sel) {
-    return __byte_perm(w, 0x64646464u, sel);
+    const uint32_t p = __byte_perm(w, 0x64646464u, sel);
+    return PLAIN ? h2_as_u32(__hsub2(u32_as_h2(p), u32_as_h2(0x64006400u))) : p;
 }
 
 // Groups per stage, padded hidden size (whole stages; the pad is zero) and
@@ -149,7 +159,11 @@ struct StageOffsets {
 // tot += scale * acc.  P: the stage's packed tile; sa2 / sb2: the stage's
 // fp16 scales of rows ra / rb; ncs: negc of the stage's first group at tokens
 // 2t, 2t+1; hst: this thread's h fragment base for the stage.
-template <int BITS, int UNROLL4>
+// PLAIN: the magic offsets are subtracted from the codes (one HSUB2 per pair)
+// instead of cancelling in the accumulator.  There they stand against
+// 1024 sum h, whose ulp the tensor core truncates by: with sum h = -650 over
+// 2560 columns every logit of a row comes out 6e-5 low (1e-6 without).
+template <int BITS, int UNROLL4, bool PLAIN>
 __device__ __forceinline__ void stage_math(float (&tot)[4], const unsigned char* P,
                                            const StageOffsets<BITS>& off, uint2 sa2, uint2 sb2,
                                            const float* ncs, const __half* hst) {
@@ -163,17 +177,20 @@ __device__ __forceinline__ void stage_math(float (&tot)[4], const unsigned char*
             const int ob = gm == 0 ? off.b[0] : gm == 1 ? off.b[1] : gm == 2 ? off.b[2] : off.b[3];
             const uint2 wa = *reinterpret_cast<const uint2*>(P + oa);
             const uint2 wb = *reinterpret_cast<const uint2*>(P + ob);
-            const float2 nc = *reinterpret_cast<const float2*>(ncs + gm * kTokGroup);
+            float2 nc = make_float2(0.f, 0.f);
+            if constexpr (!PLAIN) nc = *reinterpret_cast<const float2*>(ncs + gm * kTokGroup);
             const uint4 q0 = *reinterpret_cast<const uint4*>(hst + 64 * gm);
             const uint4 q1 = *reinterpret_cast<const uint4*>(hst + 64 * gm + 8);
             uint32_t pa[4], pb[4];
             float acc[4];
             codes4(wa.x, pa);
             codes4(wb.x, pb);
+            if constexpr (PLAIN) { plain4(pa); plain4(pb); }
             mma16816_init(acc, pa[0], pb[0], pa[1], pb[1], q0.x, q0.y, nc.x, nc.y, nc.x, nc.y);
             mma16816(acc, pa[2], pb[2], pa[3], pb[3], q0.z, q0.w);
             codes4(wa.y, pa);
             codes4(wb.y, pb);
+            if constexpr (PLAIN) { plain4(pa); plain4(pb); }
             mma16816(acc, pa[0], pb[0], pa[1], pb[1], q1.x, q1.y);
             mma16816(acc, pa[2], pb[2], pa[3], pb[3], q1.z, q1.w);
             const float s_a = gm == 0 ? sa01.x : gm == 1 ? sa01.y : gm == 2 ? sa23.x : sa23.y;
@@ -190,18 +207,19 @@ __device__ __forceinline__ void stage_math(float (&tot)[4], const unsigned char*
         for (int gm = 0; gm < 2; ++gm) {  // the stage's two groups
             const uint4 wa = *reinterpret_cast<const uint4*>(P + (gm ? off.a[1] : off.a[0]));
             const uint4 wb = *reinterpret_cast<const uint4*>(P + (gm ? off.b[1] : off.b[0]));
-            const float2 nc = *reinterpret_cast<const float2*>(ncs + gm * kTokGroup);
+            float2 nc = make_float2(0.f, 0.f);
+            if constexpr (!PLAIN) nc = *reinterpret_cast<const float2*>(ncs + gm * kTokGroup);
             const uint4 q0 = *reinterpret_cast<const uint4*>(hst + 64 * gm);
             const uint4 q1 = *reinterpret_cast<const uint4*>(hst + 64 * gm + 8);
             float acc[4];
-            mma16816_init(acc, codes8(wa.x, 0x5140u), codes8(wb.x, 0x5140u), codes8(wa.x, 0x7362u),
-                          codes8(wb.x, 0x7362u), q0.x, q0.y, nc.x, nc.y, nc.x, nc.y);
-            mma16816(acc, codes8(wa.y, 0x5140u), codes8(wb.y, 0x5140u), codes8(wa.y, 0x7362u),
-                     codes8(wb.y, 0x7362u), q0.z, q0.w);
-            mma16816(acc, codes8(wa.z, 0x5140u), codes8(wb.z, 0x5140u), codes8(wa.z, 0x7362u),
-                     codes8(wb.z, 0x7362u), q1.x, q1.y);
-            mma16816(acc, codes8(wa.w, 0x5140u), codes8(wb.w, 0x5140u), codes8(wa.w, 0x7362u),
-                     codes8(wb.w, 0x7362u), q1.z, q1.w);
+            mma16816_init(acc, codes8<PLAIN>(wa.x, 0x5140u), codes8<PLAIN>(wb.x, 0x5140u), codes8<PLAIN>(wa.x, 0x7362u),
+                          codes8<PLAIN>(wb.x, 0x7362u), q0.x, q0.y, nc.x, nc.y, nc.x, nc.y);
+            mma16816(acc, codes8<PLAIN>(wa.y, 0x5140u), codes8<PLAIN>(wb.y, 0x5140u), codes8<PLAIN>(wa.y, 0x7362u),
+                     codes8<PLAIN>(wb.y, 0x7362u), q0.z, q0.w);
+            mma16816(acc, codes8<PLAIN>(wa.z, 0x5140u), codes8<PLAIN>(wb.z, 0x5140u), codes8<PLAIN>(wa.z, 0x7362u),
+                     codes8<PLAIN>(wb.z, 0x7362u), q1.x, q1.y);
+            mma16816(acc, codes8<PLAIN>(wa.w, 0x5140u), codes8<PLAIN>(wb.w, 0x5140u), codes8<PLAIN>(wa.w, 0x7362u),
+                     codes8<PLAIN>(wb.w, 0x7362u), q1.z, q1.w);
             const float s_a = gm ? sa01.y : sa01.x, s_b = gm ? sb01.y : sb01.x;
             tot[0] = fmaf(s_a, acc[0], tot[0]);
             tot[1] = fmaf(s_a, acc[1], tot[1]);
@@ -270,14 +288,19 @@ __device__ __forceinline__ void push_fast(RowState& st, float z, float raw, int 
 // offsets), and the scales arrive by TMA (tmap_s; the group count is a
 // multiple of 8); NST == 0: n_stages at run time, any shape, scales copied
 // with cp.async (tmap_s unused).
-template <int BITS, int NST>
+// ZOUT: the raw logits go to zout[original row * zout_ld + vocab row], from
+// plain codes (see stage_math), and no softmax state is kept (the distillation
+// of few rows, whose softmax leaves tokens out and whose backward reads the
+// logits).
+template <int BITS, int NST, bool ZOUT>
 __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
     const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_s,
     const __half* __restrict__ scales,
     const __half* __restrict__ biases, int64_t V, int H, float cap,
     const __nv_bfloat16* __restrict__ h, const uint8_t* __restrict__ mask, int M,
     int* __restrict__ rows, int* __restrict__ pos, int* __restrict__ count,
-    Partial* __restrict__ part, int S, int* __restrict__ err, int stall, int n_stages) {
+    Partial* __restrict__ part, int S, int* __restrict__ err, int stall, int n_stages,
+    float* __restrict__ zout, int64_t zout_ld) {
     using Shape = StreamShape<BITS>;
     // Launched as a programmatic dependent: nothing in global memory is
     // touched before the preceding grid on the stream has completed; the
@@ -575,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
                             sa = make_uint2(*reinterpret_cast<const uint32_t*>(Sb + 16 * ra), 0u);
                             sb = make_uint2(*reinterpret_cast<const uint32_t*>(Sb + 16 * rb), 0u);
                         }
-                        stage_math<BITS, 4>(tot, pring + s * kPBytes, off, sa, sb,
+                        stage_math<BITS, 4, ZOUT>(tot, pring + s * kPBytes, off, sa, sb,
                                          negc_s + kNG * c * kTokGroup + 2 * t,
                                          hbase + kStageWords * c * (32 / BITS));
                         __syncwarp();
@@ -593,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
                     // Result ignored: the warp stays converged (see the abort policy).
                     tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull);
                     const unsigned char* Sst = sring + stage * kSBytes;
-                    stage_math<BITS, 2>(tot, pring + stage * kPBytes, off,
+                    stage_math<BITS, 2, ZOUT>(tot, pring + stage * kPBytes, off,
                                      *reinterpret_cast<const uint2*>(Sst + 8 * ra),
                                      *reinterpret_cast<const uint2*>(Sst + 8 * rb),
                                      negc_s + kNG * c * kTokGroup + 2 * t,
@@ -605,6 +628,17 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
             }
             // The last k-block's bias product, if its slot fell past the stages.
             if (kPer * (nkb - 1) + kPer / 2 >= nst) bias_mma(nkb - 1);
+            if constexpr (ZOUT) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = orig_s[2 * t + e];
+                    if (row < 0) continue;
+                    float* zr = zout + (int64_t)row * zout_ld;
+                    if (va < cta_v1) zr[va] = tot[e];
+                    if (vb < cta_v1) zr[vb] = tot[2 + e];
+                }
+                continue;
+            }
             // (computed here, not held across the tile loop: one register fewer)
             const float cap2l = cap > 0.f ? 2.f * 1.4426950408889634f / cap : 0.f;
             if (va < cta_v1) {
@@ -627,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
             red[cw][2 * t + 1] = st[1].to_partial();
         }
     }
+    if (ZOUT) return;
     __syncthreads();
     if (threadIdx.x < kTokGroup) {
         const int j = threadIdx.x;
@@ -655,7 +690,16 @@ struct StreamVariant {
     int smem;
 };
 
-StreamVariant stream_variant(int bits, int H) {
+template <bool ZOUT>
+const void* stream_fn(int bits, bool fast) {
+    if (fast)
+        return bits == 4 ? reinterpret_cast<const void*>(stream_fwd_kernel<4, kFastStages, ZOUT>)
+                         : reinterpret_cast<const void*>(stream_fwd_kernel<8, kFastStages, ZOUT>);
+    return bits == 4 ? reinterpret_cast<const void*>(stream_fwd_kernel<4, 0, ZOUT>)
+                     : reinterpret_cast<const void*>(stream_fwd_kernel<8, 0, ZOUT>);
+}
+
+StreamVariant stream_variant(int bits, int H, bool zout = false) {
     const int per_stage = kStageWords * 32 / bits;
     const int nst = (H + per_stage - 1) / per_stage;  // stages per tile
     StreamVariant v{};
@@ -663,13 +707,11 @@ StreamVariant stream_variant(int bits, int H) {
     // table (groups a multiple of 8).
     if (nst % kFastStages == 0 && (H / 64) % kSBoxGroups == 0 &&
         StreamSmem(H, bits, kFastStages, true).total <= kSmemLimit) {
-        v.fn = bits == 4 ? reinterpret_cast<const void*>(stream_fwd_kernel<4, kFastStages>)
-                         : reinterpret_cast<const void*>(stream_fwd_kernel<8, kFastStages>);
+        v.fn = zout ? stream_fn<true>(bits, true) : stream_fn<false>(bits, true);
         v.n_stages = kFastStages;
         v.tma_scales = true;
     } else {
-        v.fn = bits == 4 ? reinterpret_cast<const void*>(stream_fwd_kernel<4, 0>)
-                         : reinterpret_cast<const void*>(stream_fwd_kernel<8, 0>);
+        v.fn = zout ? stream_fn<true>(bits, false) : stream_fn<false>(bits, false);
         v.n_stages = stream_stages(H, bits);
     }
     v.smem = v.n_stages >= 2 ? StreamSmem(H, bits, v.n_stages, v.tma_scales).total : 0;
@@ -701,13 +743,14 @@ int stream_fwd_ctas_per_sm(int bits, int H) {
 cudaError_t launch_stream_fwd(const uint32_t* wq, const __half* scales, const __half* biases,
                               int64_t V, int H, int bits, float cap, const __nv_bfloat16* h,
                               const uint8_t* mask, int64_t M, int* rows, int* pos, int* count,
-                              Partial* part, int S, int* err, int stall, cudaStream_t st) {
+                              Partial* part, int S, int* err, int stall, cudaStream_t st,
+                              float* zout, int64_t zout_ld) {
     if (M >= 64) return cudaErrorInvalidValue;  // the in-kernel compaction covers 64 rows
     CUtensorMap tw;
     if (!tmap_packed_rows_sw128(&tw, wq, (uint64_t)H * bits / 32, (uint64_t)V, kTile))
         return cudaErrorInvalidValue;
     const int groups = (int)((M + kTokGroup - 1) / kTokGroup);
-    const StreamVariant v = stream_variant(bits, H);
+    const StreamVariant v = stream_variant(bits, H, zout != nullptr);
     if (v.n_stages < 2) return cudaErrorInvalidValue;
     CUtensorMap ts{};  // unused by the run-time-depth variant
     if (v.tma_scales &&
@@ -718,7 +761,7 @@ cudaError_t launch_stream_fwd(const uint32_t* wq, const __half* scales, const __
     int n_stages = v.n_stages;
     int m32 = (int)M;
     void* args[] = {&tw,  &ts,   &scales, &biases, &V, &H,   &cap,   &h,       &mask,
-                    &m32, &rows, &pos,    &count,  &part, &S, &err, &stall, &n_stages};
+                    &m32, &rows, &pos,    &count,  &part, &S, &err, &stall, &n_stages, &zout, &zout_ld};
     return launch_dependent(v.fn, grid, dim3(kThreads), (size_t)v.smem, st, args);
 }
 

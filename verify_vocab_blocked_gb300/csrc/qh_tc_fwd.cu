@@ -522,9 +522,11 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
             // EPI_DISTILL: this row's ascending list of left-out vocab rows; sidx
             // is its first entry at or past the columns still to come.
             const int* sl = nullptr;
+            float* zrow = nullptr;
             int sidx = INT32_MAX;
             if constexpr (EPI == EPI_DISTILL) {
                 if (row_ok) {
+                    if (a.zout) zrow = a.zout + (int64_t)a.rows[i] * a.zout_ld;
                     sl = a.sid + (int64_t)i * a.sid_ld;
                     const int64_t first = (int64_t)vt0 * BN;
                     int lo = 0, hi = a.sid_ld - 1;  // (entry sid_ld - 1 is INT32_MAX)
@@ -634,6 +636,16 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
 #pragma unroll
                                 for (int j = 0; j < 32; ++j)
                                     if (out_cols >> j & 1u) x[j] = -INFINITY;
+                            }
+                            if (zrow != nullptr) {  // few rows: the logits are kept
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    uint32_t o[8];
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j)
+                                        o[j] = __float_as_uint(x[8 * q + j] * a.unbias);
+                                    tc::st_global_v8(zrow + col0 + 8 * q, o);
+                                }
                             }
                         }
                         float rmax = -INFINITY;

@@ -20,9 +20,6 @@ QHEAD_SB_F16, QHEAD_SB_BF16, QHEAD_SB_F32 = 0, 1, 2
 _SB_CODE = {torch.float16: QHEAD_SB_F16, torch.bfloat16: QHEAD_SB_BF16,
             torch.float32: QHEAD_SB_F32}
 
-# Columns of distill_fwd's kept beyond the K logits (QHEAD_DISTILL_KEPT).
-DISTILL_KEPT = 32
-
 # Every symbol include/qhead.h declares.
 EXPORTS = ("qhead_fwd_workspace", "qhead_bwd_workspace", "qhead_fwd", "qhead_bwd",
            "qhead_last_error", "qhead_version", "qhead_time_next_head_kernel",
@@ -33,7 +30,7 @@ EXPORTS = ("qhead_fwd_workspace", "qhead_bwd_workspace", "qhead_fwd", "qhead_bwd
            "qhead_embed_bwd_workspace", "qhead_embed_bwd", "qhead_layer_norm",
            "qhead_layer_norm_bwd_workspace", "qhead_layer_norm_bwd",
            "qhead_distill_fwd_workspace", "qhead_distill_fwd", "qhead_distill_bwd_workspace",
-           "qhead_distill_bwd")
+           "qhead_distill_bwd", "qhead_distill_kept")
 
 
 class CHead(ctypes.Structure):
@@ -107,6 +104,8 @@ def lib() -> ctypes.CDLL:
     for name in ("qhead_distill_fwd_workspace", "qhead_distill_bwd_workspace"):
         getattr(L, name).argtypes = [hp, i64, i64]
         getattr(L, name).restype = sz
+    L.qhead_distill_kept.argtypes = [hp, i64, i64]
+    L.qhead_distill_kept.restype = i64
     L.qhead_distill_fwd.argtypes = [hp, vp, i64, vp, vp, i32, i64, f32, vp, vp, vp, vp, vp, sz, vp]
     L.qhead_distill_fwd.restype = i32
     L.qhead_distill_bwd.argtypes = [hp, vp, i64, vp, vp, i32, i64, f32, vp, vp, vp, vp, vp, vp, sz,
@@ -615,10 +614,17 @@ def _check_teacher(ids: torch.Tensor, tlogits: torch.Tensor, M: int, dev) -> int
     return int(ids.shape[1])
 
 
+def _kept_columns(c: CHead, M: int, K: int) -> int:
+    n = lib().qhead_distill_kept(ctypes.byref(c), M, K)
+    if n < 0:
+        raise QheadError(QHEAD_EINVAL, last_error())
+    return n
+
+
 def distill_fwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.Tensor,
                 temperature: float = 1.0, mask: torch.Tensor | None = None, *,
                 workspace: torch.Tensor | None = None, stream=None):
-    """(loss [M], lse [M], kept [M, K + 32]), float32: each row's cross entropy of
+    """(loss [M], lse [M], kept [M, ...]), float32: each row's cross entropy of
     the head against a teacher's top logits (ids int32 [M, K], negative =
     padding; tlogits [M, K]), less the teacher's entropy; see
     qhead_distill_fwd.  lse is of the logits over the temperature; kept begins
@@ -629,8 +635,8 @@ def distill_fwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     mask = _mask(mask, M, dev)
     loss = torch.empty(M, dtype=torch.float32, device=dev)
     lse = torch.empty(M, dtype=torch.float32, device=dev)
-    kept = torch.empty(M, K + DISTILL_KEPT, dtype=torch.float32, device=dev)
     c = head.c()
+    kept = torch.empty(M, _kept_columns(c, M, K), dtype=torch.float32, device=dev)
     if workspace is None:
         n = _size(lib().qhead_distill_fwd_workspace(ctypes.byref(c), M, K))
         workspace = alloc_workspace(n, dev)
@@ -653,10 +659,11 @@ def distill_bwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     mask = _mask(mask, M, dev)
     lse, dloss = _f32("lse", lse, M, dev), _f32("dloss", dloss, M, dev)
     _check_matrix("kept", kept, dev)
-    if kept.dtype != torch.float32 or tuple(kept.shape) != (M, K + DISTILL_KEPT):
-        raise ValueError(f"kept must be a float32 [{M}, {K + DISTILL_KEPT}] tensor")
-    dh = torch.empty(M, head.H, dtype=torch.bfloat16, device=dev)
     c = head.c()
+    cols = _kept_columns(c, M, K)
+    if kept.dtype != torch.float32 or tuple(kept.shape) != (M, cols):
+        raise ValueError(f"kept must be a float32 [{M}, {cols}] tensor")
+    dh = torch.empty(M, head.H, dtype=torch.bfloat16, device=dev)
     if workspace is None:
         n = _size(lib().qhead_distill_bwd_workspace(ctypes.byref(c), M, K))
         workspace = alloc_workspace(n, dev)
