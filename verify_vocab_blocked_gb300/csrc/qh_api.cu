@@ -16,6 +16,7 @@
 
 #include "../../include/qhead.h"
 #include "qh_distill.cuh"
+#include "qh_few.cuh"
 #include "qh_internal.cuh"
 #include "qh_ops.cuh"
 #include "qh_tmap.h"
@@ -332,14 +333,25 @@ int check_rows(int64_t M) {
 struct DistillPlan {
     FwdPlan f;
     BwdPlan b;
-    size_t off_extra = 0, total = 0;
+    bool few_dh = false;
+    size_t off_few = 0, off_extra = 0, total = 0;
 };
+
+static_assert(qh::kFewM <= qh::kFewRows && qh::kFewM <= qh::kKeepLogitsM, "few rows");
 
 int plan_distill(const qhead_head* hd, int64_t M, int64_t K, bool bwd, DistillPlan* p) {
     const bool few = !bwd && M <= qh::kFewM;
     const int rc = bwd ? plan_bwd(hd, M, &p->b) : plan_fwd(hd, M, &p->f, !few);
     if (rc) return rc;
     p->off_extra = align_up(bwd ? p->b.total : p->f.total, 256);
+    // the contraction of few rows: its partials, if the vocabulary is one chunk
+    const int64_t tr = qh::kTcFwdTileRows;
+    p->few_dh = bwd && M <= qh::kFewM && p->b.chunk >= (hd->V + tr - 1) / tr * tr;
+    if (p->few_dh) {
+        p->off_few = p->off_extra;
+        p->off_extra = align_up(p->off_few + sizeof(float) * (size_t)qh::few_splits(hd->V, hd->H, hd->bits) *
+                                                 qh::kFewRows * hd->H, 256);
+    }
     p->total = p->off_extra + (bwd   ? 4 * (size_t)M
                                : few ? sizeof(qh::Partial) * (size_t)M * qh::kFewSplits
                                      : 4 * (size_t)p->f.Mpad * (size_t)(K + 1));
@@ -1098,6 +1110,12 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
                                           inv_t, kept, ld, lse, dloss, geff, coeff, p.chunk, (int64_t)vt0 * tr,
                                           (int64_t)(vt1 - vt0) * tr, st)))
             return cuda_fail(e, "distill_coeff");
+        if (z && dp.few_dh) {
+            e = qh::launch_few_dh(head->wq, sc, bi, head->V, head->H, head->bits, coeff, p.chunk, M, pos, geff,
+                                  err, at<float>(workspace, dp.off_few), dh, st);
+            hook_after(st);
+            return e ? cuda_fail(e, "few_dh") : QHEAD_OK;
+        }
         qh::TcDhArgs da{};
         da.scales = sc; da.biases = bi; da.V = head->V; da.H = head->H; da.count = count; da.err = err;
         da.rows = rows; da.dlogp = geff; da.dh_acc = dhp; da.slice_stride = p.Mpad * head->H;

@@ -1,0 +1,271 @@
+// qh_few.cu -- the contraction dh[m, :] = sum_v c[m, v] w[v, :] for up to 16 rows.
+//
+// The tensor-core contraction (qh_tc_dh.cu) takes 128 token rows a tile, so its
+// cost does not fall below theirs (200 us at 262144 x 2560 whatever the rows).
+// For few rows the packed table's bytes are the floor (56 us there), and next to
+// it the issue rate of unpacking: here the weights go from global memory to
+// mma.sync operands in registers, with nothing staged but the scales.
+//
+// mma.m16n8k16: M = tokens, K = vocab rows, N = hidden columns.  A warp owns 128
+// columns; lane (g, t) = (lane / 4, lane % 4).  The vocab rows of a block of 64 are
+// dealt so that lane t holds rows 16 t .. 16 t + 15, four to each of the block's
+// four steps: its coefficients are 32 contiguous bytes per token, and its codes of
+// a row (columns 16 g .. 16 g + 15) one 8-byte (4 bits) or 16-byte (8 bits) load.
+// Column tile i of the warp is code i of each lane g, so two rows' words give the
+// B operand's pairs by byte permutation: (row 0 code i, row 1 code i).  w = fma(q, s,
+// b) in fp16, one rounding, as in the tensor-core kernels.  The products of a
+// block's four steps need no data of another lane.
+//
+// Each warp keeps its 16 x 128 sums in registers over the CTA's vocab range and
+// writes them once; the ranges are added in order by a second launch.
+#include "qh_dequant.cuh"
+#include "qh_few.cuh"
+#include "qh_ops.cuh"
+#include "qh_tc.cuh"
+
+namespace qh {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kColsWarp = 128, kColsCta = kColsWarp * kWarps;
+constexpr int kBlockRows = 64;
+constexpr int kGroups = kColsCta / 64;  // groups of a row in the CTA's columns
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The codes of one row in this lane's 16 columns.
+template <int BITS>
+struct Codes {
+    uint32_t w[BITS / 2];
+    __device__ __forceinline__ void load(const uint32_t* p) {
+        if constexpr (BITS == 4) {
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            w[0] = x.x; w[1] = x.y;
+        } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(p);
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        }
+    }
+};
+
+// Eight consecutive codes (half 0 or 1 of the 16) of rows a and b as fp16 pairs.
+template <int BITS>
+__device__ __forceinline__ void pairs8(const Codes<BITS>& a, const Codes<BITS>& b, int half, uint32_t s2,
+                                       uint32_t b2, uint32_t (&p)[8]) {
+    if constexpr (BITS == 4) {
+        const uint32_t x = a.w[half], y = b.w[half];
+        uint32_t q[4];
+        deq4_word(__byte_perm(x, y, 0x5410), s2, b2, q);  // codes 0 .. 3
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = q[i];
+        deq4_word(__byte_perm(x, y, 0x7632), s2, b2, q);  // codes 4 .. 7
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[4 + i] = q[i];
+    } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t x = a.w[2 * half + k], y = b.w[2 * half + k];
+            const uint32_t lo = __byte_perm(x, y, 0x5140), hi = __byte_perm(x, y, 0x7362);
+            p[4 * k] = deq8(lo, 0x4140u, s2, b2);
+            p[4 * k + 1] = deq8(lo, 0x4342u, s2, b2);
+            p[4 * k + 2] = deq8(hi, 0x4140u, s2, b2);
+            p[4 * k + 3] = deq8(hi, 0x4342u, s2, b2);
+        }
+    }
+}
+
+// CTAs to an SM: what the registers of a block's codes, loaded one block ahead, leave.
+constexpr int ctas_per_sm(int bits) { return bits == 4 ? 3 : 2; }
+
+template <int BITS>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS)) few_dh_kernel(
+    const uint32_t* __restrict__ wq, const __half* __restrict__ scales, const __half* __restrict__ biases,
+    int64_t V, int H, const __half* __restrict__ coeff, int64_t ldc, int n_rows, float* __restrict__ part,
+    int S) {
+    // [scales, biases][group][row]: a lane's four rows of a step are 8 bytes
+    __shared__ __align__(16) __half sb_sh[2][2][kGroups][kBlockRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int col0 = blockIdx.x * kColsCta + warp * kColsWarp;  // of the warp
+    const bool on = col0 < H;                                   // (H: whole warps' columns)
+    const int G = H / 64, g0 = blockIdx.x * kGroups;
+    const int64_t nb = (V + kBlockRows - 1) / kBlockRows;
+    const int sp = blockIdx.y;
+    const int64_t b0 = nb * sp / S, b1 = nb * (sp + 1) / S;
+    const int wpr = H * BITS / 32;
+    const uint32_t* wbase = wq + (on ? col0 : 0) * BITS / 32 + g * (BITS / 2);
+    const int my_group = 2 * warp + (g >> 2);
+
+    float acc[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+
+    // Scales and biases of a block: 64 rows x kGroups, four of each per thread.
+    unsigned short sr[4], br[4];
+    auto sb_fetch = [&](int64_t blk) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int id = threadIdx.x + k * kThreads;  // row id / kGroups, group id % kGroups
+            const int64_t v = blk * kBlockRows + id / kGroups;
+            const int gg = g0 + id % kGroups;
+            sr[k] = br[k] = 0;
+            if (blk < b1 && v < V && gg < G) {
+                sr[k] = reinterpret_cast<const unsigned short*>(scales)[v * G + gg];
+                br[k] = reinterpret_cast<const unsigned short*>(biases)[v * G + gg];
+            }
+        }
+    };
+    auto sb_store = [&](int buf) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int id = threadIdx.x + k * kThreads;
+            sb_sh[buf][0][id % kGroups][id / kGroups] = __ushort_as_half(sr[k]);
+            sb_sh[buf][1][id % kGroups][id / kGroups] = __ushort_as_half(br[k]);
+        }
+    };
+    // Rows past V read row V - 1: their coefficients are zero.
+    auto w_row = [&](int64_t blk, int e) {
+        int64_t v = blk * kBlockRows + 16 * t + e;
+        v = v < V ? v : V - 1;
+        return wbase + v * wpr;
+    };
+    Codes<BITS> w[4][4];
+    auto w_fetch = [&](int64_t blk, int s) {
+        if (!on || blk >= b1) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[s][e].load(w_row(blk, 4 * s + e));
+    };
+    uint4 ca[2], cb[2];  // coefficients of tokens g and g + 8, rows 16 t .. 16 t + 15
+    auto c_fetch = [&](int64_t blk) {
+        const __half* c = coeff + blk * kBlockRows + 16 * t;
+        ca[0] = ca[1] = cb[0] = cb[1] = make_uint4(0u, 0u, 0u, 0u);
+        if (blk >= b1) return;
+        if (g < n_rows) {
+            ca[0] = reinterpret_cast<const uint4*>(c + (int64_t)g * ldc)[0];
+            ca[1] = reinterpret_cast<const uint4*>(c + (int64_t)g * ldc)[1];
+        }
+        if (g + 8 < n_rows) {
+            cb[0] = reinterpret_cast<const uint4*>(c + (int64_t)(g + 8) * ldc)[0];
+            cb[1] = reinterpret_cast<const uint4*>(c + (int64_t)(g + 8) * ldc)[1];
+        }
+    };
+
+    sb_fetch(b0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) w_fetch(b0, s);
+    c_fetch(b0);
+    sb_store(0);
+    int buf = 0;
+    for (int64_t blk = b0; blk < b1; ++blk) {
+        __syncthreads();  // this block's scales are in; the other buffer is free
+        sb_fetch(blk + 1);
+        const uint32_t cav[8] = {ca[0].x, ca[0].y, ca[0].z, ca[0].w, ca[1].x, ca[1].y, ca[1].z, ca[1].w};
+        const uint32_t cbv[8] = {cb[0].x, cb[0].y, cb[0].z, cb[0].w, cb[1].x, cb[1].y, cb[1].z, cb[1].w};
+        c_fetch(blk + 1);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const uint32_t a[4] = {cav[2 * s], cbv[2 * s], cav[2 * s + 1], cbv[2 * s + 1]};
+            const uint2 sc = *reinterpret_cast<const uint2*>(&sb_sh[buf][0][my_group][16 * t + 4 * s]);
+            const uint2 bi = *reinterpret_cast<const uint2*>(&sb_sh[buf][1][my_group][16 * t + 4 * s]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t p[8], q[8];
+                pairs8<BITS>(w[s][0], w[s][1], half, sc.x, bi.x, p);
+                pairs8<BITS>(w[s][2], w[s][3], half, sc.y, bi.y, q);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mma(acc[8 * half + i], a, p[i], q[i]);
+            }
+            w_fetch(blk + 1, s);
+        }
+        sb_store(buf ^ 1);
+        buf ^= 1;
+    }
+    if (!on) return;
+    // Tile i, lane (g, t): tokens g, g + 8; columns 32 t + i and 32 t + 16 + i.
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (g + 8 * e >= n_rows) continue;
+        float* dst = part + ((int64_t)sp * kFewRows + g + 8 * e) * H + col0 + 32 * t;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(dst + 16 * n + i) =
+                    make_float4(acc[i][2 * e + n], acc[i + 1][2 * e + n], acc[i + 2][2 * e + n],
+                                acc[i + 3][2 * e + n]);
+    }
+}
+
+// dh[r, :] = (-geff[r] 2^-14) * sum of the ranges' partials, in order, in bf16:
+// block (column block of 128, row); 16 groups of 16 threads take a contiguous
+// share of the ranges each.
+constexpr int kJoinGroups = 16;
+__global__ void __launch_bounds__(16 * kJoinGroups) few_join_kernel(
+    const float* __restrict__ part, int S, int H, const int* __restrict__ pos,
+    const float* __restrict__ geff, const int* __restrict__ err, __nv_bfloat16* __restrict__ dh) {
+    __shared__ float sh[kJoinGroups][16][8];
+    const int64_t r = blockIdx.y;
+    const int i = pos[r];
+    const int u = threadIdx.x & 15, grp = threadIdx.x >> 4;
+    const int d = blockIdx.x * 128 + 8 * u;
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    if (i >= 0) {
+        const int s0 = S * grp / kJoinGroups, s1 = S * (grp + 1) / kJoinGroups;
+#pragma unroll 4
+        for (int s = s0; s < s1; ++s) {
+            float x[8];
+            load8_wide(part + ((int64_t)s * kFewRows + i) * H + d, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] += x[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sh[grp][u][e] = acc[e];
+    __syncthreads();
+    if (grp != 0) return;
+    for (int k = 1; k < kJoinGroups; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += sh[k][u][e];
+    const float scale = i < 0 ? 0.f : *err != 0 ? __int_as_float(0x7fc00000) : -geff[r] * (1.f / 16384.f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = i < 0 ? 0.f : acc[e] * scale;
+    store8(dh + r * (int64_t)H + d, acc);
+}
+
+}  // namespace
+
+int few_splits(int64_t V, int H, int bits) {
+    const int gx = (H + kColsCta - 1) / kColsCta;
+    const int64_t nb = (V + kBlockRows - 1) / kBlockRows;
+    const int64_t want = ctas_per_sm(bits) * 152 / gx;  // one wave
+    return (int)(nb < want ? nb : want < 1 ? 1 : want);
+}
+
+cudaError_t launch_few_dh(const uint32_t* wq, const __half* scales, const __half* biases, int64_t V, int H,
+                          int bits, const __half* coeff, int64_t ldc, int64_t M, const int* pos,
+                          const float* geff, const int* err, float* part, void* dh, cudaStream_t st) {
+    const int S = few_splits(V, H, bits);
+    const dim3 grid((unsigned)((H + kColsCta - 1) / kColsCta), (unsigned)S);
+    if (bits == 4)
+        few_dh_kernel<4><<<grid, kThreads, 0, st>>>(wq, scales, biases, V, H, coeff, ldc, (int)M, part, S);
+    else
+        few_dh_kernel<8><<<grid, kThreads, 0, st>>>(wq, scales, biases, V, H, coeff, ldc, (int)M, part, S);
+    cudaError_t e = cudaGetLastError();
+    if (e) return e;
+    few_join_kernel<<<dim3((unsigned)(H / 128), (unsigned)M), 16 * kJoinGroups, 0, st>>>(
+        part, S, H, pos, geff, err, static_cast<__nv_bfloat16*>(dh));
+    return cudaGetLastError();
+}
+
+}  // namespace qh
