@@ -349,7 +349,7 @@ int plan_distill(const qhead_head* hd, int64_t M, int64_t K, bool bwd, DistillPl
     p->few_dh = bwd && M <= qh::kFewM && p->b.chunk >= (hd->V + tr - 1) / tr * tr;
     if (p->few_dh) {
         p->off_few = p->off_extra;
-        p->off_extra = align_up(p->off_few + sizeof(float) * (size_t)qh::few_splits(hd->V, hd->H, hd->bits) *
+        p->off_extra = align_up(p->off_few + sizeof(float) * (size_t)qh::few_splits(M, hd->V, hd->H, hd->bits) *
                                                  qh::kFewRows * hd->H, 256);
     }
     p->total = p->off_extra + (bwd   ? 4 * (size_t)M

@@ -6,18 +6,25 @@
 // it the issue rate of unpacking: here the weights go from global memory to
 // mma.sync operands in registers, with nothing staged but the scales.
 //
-// mma.m16n8k16: M = tokens, K = vocab rows, N = hidden columns.  A warp owns 128
-// columns; lane (g, t) = (lane / 4, lane % 4).  The vocab rows of a block of 64 are
-// dealt so that lane t holds rows 16 t .. 16 t + 15, four to each of the block's
-// four steps: its coefficients are 32 contiguous bytes per token, and its codes of
-// a row (columns 16 g .. 16 g + 15) one 8-byte (4 bits) or 16-byte (8 bits) load.
-// Column tile i of the warp is code i of each lane g, so two rows' words give the
-// B operand's pairs by byte permutation: (row 0 code i, row 1 code i).  w = fma(q, s,
-// b) in fp16, one rounding, as in the tensor-core kernels.  The products of a
-// block's four steps need no data of another lane.
+// mma.m16n8k16: M = hidden columns, K = vocab rows, N = tokens (one tile of 8, or
+// two).  A warp owns 128 columns; lane (g, t) = (lane / 4, lane % 4).  The vocab
+// rows of a block of 64 are dealt so that lane t holds rows 16 t .. 16 t + 15, four
+// to each of the block's four steps: its coefficients are 32 contiguous bytes per
+// token, and its codes of a row (columns 16 g .. 16 g + 15) one 8-byte (4 bits) or
+// 16-byte (8 bits) load.  Column tile i of the warp is codes i and i + 8 of each
+// lane g, so two rows' words give the A operand's pairs by byte permutation: (row 0
+// code i, row 1 code i).  w = fma(q, s, b) in fp16, one rounding, as in the
+// tensor-core kernels.  The products of a block's four steps need no data of
+// another lane.
 //
-// Each warp keeps its 16 x 128 sums in registers over the CTA's vocab range and
-// writes them once; the ranges are added in order by a second launch.
+// The issue and latency of the unpacking and of mma.sync bound it, not the bytes:
+// 104 us at up to 8 rows, 135 at up to 16 (262144 x 2560, 4 bits; 80 us at 13 rows
+// of 131072 x 2560, 8 bits).  With the tokens as M, 16 whatever their number, up to
+// 16 rows took 148 us; 64 columns a warp, for more warps, 160 and 197 (loads of 4
+// bytes); two token tiles within three CTAs to an SM spill, 199.
+//
+// Each warp keeps its sums in registers over the CTA's vocab range and writes them
+// once; the ranges are added in order by a second launch.
 #include "qh_dequant.cuh"
 #include "qh_few.cuh"
 #include "qh_ops.cuh"
@@ -56,37 +63,28 @@ struct Codes {
     }
 };
 
-// Eight consecutive codes (half 0 or 1 of the 16) of rows a and b as fp16 pairs.
+// Codes 8 half + 4 quad .. + 3 of rows a and b as fp16 pairs.
 template <int BITS>
-__device__ __forceinline__ void pairs8(const Codes<BITS>& a, const Codes<BITS>& b, int half, uint32_t s2,
-                                       uint32_t b2, uint32_t (&p)[8]) {
+__device__ __forceinline__ void pairs4(const Codes<BITS>& a, const Codes<BITS>& b, int half, int quad,
+                                       uint32_t s2, uint32_t b2, uint32_t (&p)[4]) {
     if constexpr (BITS == 4) {
-        const uint32_t x = a.w[half], y = b.w[half];
-        uint32_t q[4];
-        deq4_word(__byte_perm(x, y, 0x5410), s2, b2, q);  // codes 0 .. 3
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = q[i];
-        deq4_word(__byte_perm(x, y, 0x7632), s2, b2, q);  // codes 4 .. 7
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[4 + i] = q[i];
+        deq4_word(__byte_perm(a.w[half], b.w[half], quad ? 0x7632 : 0x5410), s2, b2, p);
     } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t x = a.w[2 * half + k], y = b.w[2 * half + k];
-            const uint32_t lo = __byte_perm(x, y, 0x5140), hi = __byte_perm(x, y, 0x7362);
-            p[4 * k] = deq8(lo, 0x4140u, s2, b2);
-            p[4 * k + 1] = deq8(lo, 0x4342u, s2, b2);
-            p[4 * k + 2] = deq8(hi, 0x4140u, s2, b2);
-            p[4 * k + 3] = deq8(hi, 0x4342u, s2, b2);
-        }
+        const uint32_t x = a.w[2 * half + quad], y = b.w[2 * half + quad];
+        const uint32_t lo = __byte_perm(x, y, 0x5140), hi = __byte_perm(x, y, 0x7362);
+        p[0] = deq8(lo, 0x4140u, s2, b2);
+        p[1] = deq8(lo, 0x4342u, s2, b2);
+        p[2] = deq8(hi, 0x4140u, s2, b2);
+        p[3] = deq8(hi, 0x4342u, s2, b2);
     }
 }
 
-// CTAs to an SM: what the registers of a block's codes, loaded one block ahead, leave.
-constexpr int ctas_per_sm(int bits) { return bits == 4 ? 3 : 2; }
+// CTAs to an SM: what the registers of the sums and of a block's codes, loaded one
+// block ahead, leave.
+constexpr int ctas_per_sm(int bits, int nt) { return bits == 4 && nt == 1 ? 3 : 2; }
 
-template <int BITS>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS)) few_dh_kernel(
+template <int BITS, int NT>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS, NT)) few_dh_kernel(
     const uint32_t* __restrict__ wq, const __half* __restrict__ scales, const __half* __restrict__ biases,
     int64_t V, int H, const __half* __restrict__ coeff, int64_t ldc, int n_rows, float* __restrict__ part,
     int S) {
@@ -103,11 +101,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS)) few_dh_kernel(
     const uint32_t* wbase = wq + (on ? col0 : 0) * BITS / 32 + g * (BITS / 2);
     const int my_group = 2 * warp + (g >> 2);
 
-    float acc[16][4];
+    float acc[8][NT][4];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.f;
 
     // Scales and biases of a block: 64 rows x kGroups, four of each per thread.
     unsigned short sr[4], br[4];
@@ -133,29 +133,30 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS)) few_dh_kernel(
         }
     };
     // Rows past V read row V - 1: their coefficients are zero.
-    auto w_row = [&](int64_t blk, int e) {
-        int64_t v = blk * kBlockRows + 16 * t + e;
-        v = v < V ? v : V - 1;
-        return wbase + v * wpr;
-    };
     Codes<BITS> w[4][4];
     auto w_fetch = [&](int64_t blk, int s) {
         if (!on || blk >= b1) return;
+        const int64_t v = blk * kBlockRows + 16 * t + 4 * s;
+        if (v + 4 <= V) {
+            const uint32_t* p = wbase + v * wpr;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[s][e].load(w_row(blk, 4 * s + e));
+            for (int e = 0; e < 4; ++e) w[s][e].load(p + e * wpr);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[s][e].load(wbase + (v + e < V ? v + e : V - 1) * wpr);
+        }
     };
-    uint4 ca[2], cb[2];  // coefficients of tokens g and g + 8, rows 16 t .. 16 t + 15
+    uint4 cf[NT][2];  // coefficients of tokens g (and g + 8), rows 16 t .. 16 t + 15
     auto c_fetch = [&](int64_t blk) {
         const __half* c = coeff + blk * kBlockRows + 16 * t;
-        ca[0] = ca[1] = cb[0] = cb[1] = make_uint4(0u, 0u, 0u, 0u);
-        if (blk >= b1) return;
-        if (g < n_rows) {
-            ca[0] = reinterpret_cast<const uint4*>(c + (int64_t)g * ldc)[0];
-            ca[1] = reinterpret_cast<const uint4*>(c + (int64_t)g * ldc)[1];
-        }
-        if (g + 8 < n_rows) {
-            cb[0] = reinterpret_cast<const uint4*>(c + (int64_t)(g + 8) * ldc)[0];
-            cb[1] = reinterpret_cast<const uint4*>(c + (int64_t)(g + 8) * ldc)[1];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            cf[n][0] = cf[n][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (blk < b1 && g + 8 * n < n_rows) {
+                const uint4* p = reinterpret_cast<const uint4*>(c + (int64_t)(g + 8 * n) * ldc);
+                cf[n][0] = p[0];
+                cf[n][1] = p[1];
+            }
         }
     };
 
@@ -168,41 +169,57 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS)) few_dh_kernel(
     for (int64_t blk = b0; blk < b1; ++blk) {
         __syncthreads();  // this block's scales are in; the other buffer is free
         sb_fetch(blk + 1);
-        const uint32_t cav[8] = {ca[0].x, ca[0].y, ca[0].z, ca[0].w, ca[1].x, ca[1].y, ca[1].z, ca[1].w};
-        const uint32_t cbv[8] = {cb[0].x, cb[0].y, cb[0].z, cb[0].w, cb[1].x, cb[1].y, cb[1].z, cb[1].w};
+        uint32_t cv[NT][8];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint32_t x[8] = {cf[n][0].x, cf[n][0].y, cf[n][0].z, cf[n][0].w,
+                                   cf[n][1].x, cf[n][1].y, cf[n][1].z, cf[n][1].w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) cv[n][k] = x[k];
+        }
         c_fetch(blk + 1);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            const uint32_t a[4] = {cav[2 * s], cbv[2 * s], cav[2 * s + 1], cbv[2 * s + 1]};
             const uint2 sc = *reinterpret_cast<const uint2*>(&sb_sh[buf][0][my_group][16 * t + 4 * s]);
             const uint2 bi = *reinterpret_cast<const uint2*>(&sb_sh[buf][1][my_group][16 * t + 4 * s]);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t p[8], q[8];
-                pairs8<BITS>(w[s][0], w[s][1], half, sc.x, bi.x, p);
-                pairs8<BITS>(w[s][2], w[s][3], half, sc.y, bi.y, q);
+            for (int quad = 0; quad < 2; ++quad) {
+                uint32_t p[2][4], q[2][4];  // rows (0, 1) and (2, 3), codes of either half
 #pragma unroll
-                for (int i = 0; i < 8; ++i) mma(acc[8 * half + i], a, p[i], q[i]);
+                for (int half = 0; half < 2; ++half) {
+                    pairs4<BITS>(w[s][0], w[s][1], half, quad, sc.x, bi.x, p[half]);
+                    pairs4<BITS>(w[s][2], w[s][3], half, quad, sc.y, bi.y, q[half]);
+                }
+                if (quad == 1) w_fetch(blk + 1, s);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a[4] = {p[0][i], p[1][i], q[0][i], q[1][i]};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        mma(acc[4 * quad + i][n], a, cv[n][2 * s], cv[n][2 * s + 1]);
+                }
             }
-            w_fetch(blk + 1, s);
         }
         sb_store(buf ^ 1);
         buf ^= 1;
     }
     if (!on) return;
-    // Tile i, lane (g, t): tokens g, g + 8; columns 32 t + i and 32 t + 16 + i.
+    // Tile i, lane (g, t): columns 16 g + i and 16 g + i + 8, tokens 2 t and 2 t + 1.
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (g + 8 * e >= n_rows) continue;
-        float* dst = part + ((int64_t)sp * kFewRows + g + 8 * e) * H + col0 + 32 * t;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int e = 0; e < 2; ++e) {
+            const int tok = 8 * n + 2 * t + e;
+            if (tok >= n_rows) continue;
+            float* dst = part + ((int64_t)sp * kFewRows + tok) * H + col0 + 16 * g;
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(dst + 16 * n + i) =
-                    make_float4(acc[i][2 * e + n], acc[i + 1][2 * e + n], acc[i + 2][2 * e + n],
-                                acc[i + 3][2 * e + n]);
-    }
+            for (int hi = 0; hi < 2; ++hi)
+#pragma unroll
+                for (int i = 0; i < 8; i += 4)
+                    *reinterpret_cast<float4*>(dst + 8 * hi + i) =
+                        make_float4(acc[i][n][2 * hi + e], acc[i + 1][n][2 * hi + e],
+                                    acc[i + 2][n][2 * hi + e], acc[i + 3][n][2 * hi + e]);
+        }
 }
 
 // dh[r, :] = (-geff[r] 2^-14) * sum of the ranges' partials, in order, in bf16:
@@ -245,22 +262,21 @@ __global__ void __launch_bounds__(16 * kJoinGroups) few_join_kernel(
 
 }  // namespace
 
-int few_splits(int64_t V, int H, int bits) {
+int few_splits(int64_t M, int64_t V, int H, int bits) {
     const int gx = (H + kColsCta - 1) / kColsCta;
     const int64_t nb = (V + kBlockRows - 1) / kBlockRows;
-    const int64_t want = ctas_per_sm(bits) * 152 / gx;  // one wave
+    const int64_t want = ctas_per_sm(bits, M <= 8 ? 1 : 2) * 152 / gx;  // one wave
     return (int)(nb < want ? nb : want < 1 ? 1 : want);
 }
 
 cudaError_t launch_few_dh(const uint32_t* wq, const __half* scales, const __half* biases, int64_t V, int H,
                           int bits, const __half* coeff, int64_t ldc, int64_t M, const int* pos,
                           const float* geff, const int* err, float* part, void* dh, cudaStream_t st) {
-    const int S = few_splits(V, H, bits);
+    const int S = few_splits(M, V, H, bits);
     const dim3 grid((unsigned)((H + kColsCta - 1) / kColsCta), (unsigned)S);
-    if (bits == 4)
-        few_dh_kernel<4><<<grid, kThreads, 0, st>>>(wq, scales, biases, V, H, coeff, ldc, (int)M, part, S);
-    else
-        few_dh_kernel<8><<<grid, kThreads, 0, st>>>(wq, scales, biases, V, H, coeff, ldc, (int)M, part, S);
+    auto* fn = bits == 4 ? (M <= 8 ? few_dh_kernel<4, 1> : few_dh_kernel<4, 2>)
+                         : (M <= 8 ? few_dh_kernel<8, 1> : few_dh_kernel<8, 2>);
+    fn<<<grid, kThreads, 0, st>>>(wq, scales, biases, V, H, coeff, ldc, (int)M, part, S);
     cudaError_t e = cudaGetLastError();
     if (e) return e;
     few_join_kernel<<<dim3((unsigned)(H / 128), (unsigned)M), 16 * kJoinGroups, 0, st>>>(

@@ -8,7 +8,7 @@ namespace qh {
 constexpr int kFewRows = 16;
 
 // Vocab ranges of the contraction: its partials are [ranges, kFewRows, H] fp32.
-int few_splits(int64_t V, int H, int bits);
+int few_splits(int64_t M, int64_t V, int H, int bits);
 
 // dh [M, H] bf16 = (-geff[r] 2^-14) * sum_v coeff[pos[r], v] w[v, :], M <= kFewRows;
 // coeff [>= M rows, ldc] fp16, 32-byte aligned rows, zero in the columns from V up
