@@ -422,9 +422,9 @@ int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int
  *             aligned, for the backward: in the first K columns the exact fp32
  *             logits z of the valid entries (0 elsewhere), then the exact logits
  *             of the largest other vocab rows, up to 16, and (as int32 bits, 0:
- *             none) those rows plus one; at M <= 128 also the row's V logits
- *             (-inf at the listed tokens), so that the backward need not form
- *             them again.
+ *             none) those rows plus one; at M <= 16, or while M * V * 4 is at
+ *             most 4 GiB, also the row's V logits (-inf at the listed tokens), so
+ *             that the backward need not form them again.
  *   workspace device, >= qhead_distill_fwd_workspace(head, M, K) bytes,
  *             256-byte aligned.
  * Up to 16 rows the weight-streaming kernel forms the logits, above them the

@@ -144,8 +144,11 @@ def test_workspace_queries(L):
     assert L.qhead_distill_fwd_workspace(hd, 5, 0) == BAD_SIZE
     assert L.qhead_distill_bwd_workspace(hd, 5, 1025) == BAD_SIZE
     assert L.qhead_distill_bwd_workspace(hd, -1, 4) == BAD_SIZE
-    assert L.qhead_distill_kept(hd, 129, 4) == 4 + 32
-    assert L.qhead_distill_kept(hd, 128, 4) == 40 + 1024      # V = 1000 in blocks of 32
+    assert L.qhead_distill_kept(hd, 129, 4) == 40 + 1024      # V = 1000 in blocks of 32
+    big = ctypes.byref(_head(V=1 << 20))
+    assert L.qhead_distill_kept(big, 1024, 4) == 40 + (1 << 20)   # 4 GiB of logits
+    assert L.qhead_distill_kept(big, 1025, 4) == 4 + 32
+    assert L.qhead_distill_kept(ctypes.byref(_head(V=1 << 30)), 16, 4) == 40 + (1 << 30)
     assert L.qhead_distill_kept(hd, 5, 0) == -1
 
 

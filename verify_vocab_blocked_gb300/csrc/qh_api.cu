@@ -337,7 +337,7 @@ struct DistillPlan {
     size_t off_few = 0, off_extra = 0, total = 0;
 };
 
-static_assert(qh::kFewM <= qh::kFewRows && qh::kFewM <= qh::kKeepLogitsM, "few rows");
+static_assert(qh::kFewM <= qh::kFewRows, "few rows");
 
 int plan_distill(const qhead_head* hd, int64_t M, int64_t K, bool bwd, DistillPlan* p) {
     const bool few = !bwd && M <= qh::kFewM;
@@ -983,7 +983,7 @@ int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const in
     int* sid = at<int>(workspace, dp.off_extra);
     const float inv_t = 1.f / temperature;
     const int64_t ld = qh::kept_columns(M, K, head->V);
-    float* zout = M <= qh::kKeepLogitsM ? kept + qh::kept_logits_at(K) : nullptr;
+    float* zout = qh::keeps_logits(M, head->V) ? kept + qh::kept_logits_at(K) : nullptr;
     cudaError_t e;
     if (M <= qh::kFewM) {
         // The weight-streaming kernel compacts and converts the rows itself.
@@ -1066,7 +1066,7 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
     const int64_t ld = qh::kept_columns(M, K, head->V);
     // The coefficients from the kept logits, unless the stall switch wants the
     // logit kernel.
-    const float* z = M <= qh::kKeepLogitsM && !stall ? kept + qh::kept_logits_at(K) : nullptr;
+    const float* z = qh::keeps_logits(M, head->V) && !stall ? kept + qh::kept_logits_at(K) : nullptr;
     cudaError_t e;
     if (z) {
         if ((e = qh::launch_compact(mask, M, p.Mpad, rows, pos, count, err, st)))
@@ -1099,8 +1099,8 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
         ta.l2e = 1.4426950408889634f * inv_t;
         ta.unbias = qh::distill_unbias(head->H);
         if (z) {
-            if ((e = qh::launch_distill_from_logits(z, ld, head->V, head->softcap, inv_t, pos, M, lse, coeff,
-                                                    p.chunk, (int64_t)vt0 * tr, (int64_t)(vt1 - vt0) * tr,
+            if ((e = qh::launch_distill_from_logits(z, ld, head->V, head->softcap, inv_t, rows, count, M, lse,
+                                                    coeff, p.chunk, (int64_t)vt0 * tr, (int64_t)(vt1 - vt0) * tr,
                                                     st)))
                 return cuda_fail(e, "distill_from_logits");
         } else if ((e = qh::launch_tc_fwd(th, tw_logit, ta, head->bits, true, p.grid, st))) {

@@ -27,13 +27,12 @@
 //     rounding -- with both.)
 //
 // kept [M, ld] holds, per row, the K exact capped logits, the others' and their
-// vocab rows plus one (as integer bits, 0: none), and at up to kKeepLogitsM rows
-// the row's V logits, -inf at the teacher's: the backward then forms its
-// coefficients from them instead of running the logit kernel again (232 us of
-// 700 at 13 rows of the 262144 x 2560 head; at 4 V bytes a row they are smaller
-// than the backward's coefficient block).  Up to kFewM rows the weight-streaming
-// kernel writes them, whose cost follows the rows (the tensor-core kernel's does
-// not: 227 us from 1 to 128), and a softmax pass of its own reads them.
+// vocab rows plus one (as integer bits, 0: none), and while they fit 4 GiB the
+// row's V logits, -inf at the teacher's: the backward then forms its coefficients
+// from them in one pass instead of running the logit kernel again.  Up to kFewM
+// rows the weight-streaming kernel writes them, whose cost follows the rows (the
+// tensor-core kernel's does not: 227 us from 1 to 128 rows of the 262144 x 2560
+// head), and a softmax pass of its own reads them.
 #include "qh_distill.cuh"
 #include "qh_ops.cuh"
 #include "qh_tc.cuh"
@@ -573,19 +572,24 @@ __global__ void __launch_bounds__(kSplitThreads) distill_split_kernel(
 
 // The coefficient block of the chunk [v_begin, v_begin + chunk) from the kept
 // logits: q sech2 2^14 in fp16, zeros past V (and at the left-out columns, which
-// distill_coeff_kernel fills).  Thread = 8 columns of one active row; the rows
-// past the active ones are not written (nothing reads what the contraction
-// makes of them).
+// distill_coeff_kernel fills), with the arithmetic of the logit kernel's own
+// coefficient epilogue.  Bound by bytes: 4 read, 2 written per logit.  Thread = 8
+// columns of one active row; the rows past the active ones are not written
+// (nothing reads what the contraction makes of them).
 __global__ void __launch_bounds__(256) distill_from_logits_kernel(
     const float* __restrict__ z, int64_t ld, int64_t V, float cap, float inv_t,
-    const int* __restrict__ pos, const float* __restrict__ lse, __half* __restrict__ coeff, int64_t ldc,
-    int64_t v_begin, int64_t chunk) {
-    const int64_t r = blockIdx.y;
-    const int i = pos[r];
-    if (i < 0) return;
-    const int64_t c0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    const int* __restrict__ rows, const int* __restrict__ count, const float* __restrict__ lse,
+    __half* __restrict__ coeff, int64_t ldc, int64_t v_begin, int64_t chunk) {
+    constexpr float kL2e = 1.4426950408889634f;
+    // blocks run along a row, row after row
+    const int per_row = (int)((chunk / 8 + 255) / 256);
+    const int i = blockIdx.x / per_row;
+    if (i >= *count) return;
+    const int64_t r = rows[i];
+    const int64_t c0 = ((int64_t)(blockIdx.x % per_row) * 256 + threadIdx.x) * 8;
     if (c0 >= chunk) return;
-    const float l = lse[r];
+    const float lsb = lse[r] * kL2e - 14.f, l2e = kL2e * inv_t;
+    const float k2 = cap > 0.f ? 2.f * kL2e / cap : 0.f;
     float x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = -INFINITY;
@@ -600,14 +604,13 @@ __global__ void __launch_bounds__(256) distill_from_logits_kernel(
     float o[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        o[k] = 0.f;
-        if (x[k] == -INFINITY) continue;
-        float th = 0.f, zc = x[k];
+        float zc = x[k], sech2 = 1.f;
         if (cap > 0.f) {
-            th = tanhf(x[k] / cap);
+            const float th = fmaf(-2.f, tc::rcp_approx(tc::ex2_approx(x[k] * k2) + 1.f), 1.f);
             zc = cap * th;
+            sech2 = fmaf(-th, th, 1.f);
         }
-        o[k] = expf(fmaf(zc, inv_t, -l)) * fmaf(-th, th, 1.f) * 16384.f;
+        o[k] = x[k] == -INFINITY ? 0.f : tc::ex2_approx(fmaf(zc, l2e, -lsb)) * sech2;
     }
     store8(coeff + (int64_t)i * ldc + c0, o);
 }
@@ -703,10 +706,12 @@ cudaError_t launch_distill_split(const float* z, int64_t ld, int64_t V, float ca
 }
 
 cudaError_t launch_distill_from_logits(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
-                                       const int* pos, int64_t M, const float* lse, __half* coeff,
-                                       int64_t ldc, int64_t v_begin, int64_t chunk, cudaStream_t st) {
-    distill_from_logits_kernel<<<dim3((unsigned)((chunk / 8 + 255) / 256), (unsigned)M), 256, 0, st>>>(
-        z, ld, V, cap, inv_t, pos, lse, coeff, ldc, v_begin, chunk);
+                                       const int* rows, const int* count, int64_t M, const float* lse,
+                                       __half* coeff, int64_t ldc, int64_t v_begin, int64_t chunk,
+                                       cudaStream_t st) {
+    // (within 2^31 blocks: M V is at most 2^30 here, or M at most kFewM)
+    distill_from_logits_kernel<<<(unsigned)((chunk / 8 + 255) / 256 * M), 256, 0, st>>>(
+        z, ld, V, cap, inv_t, rows, count, lse, coeff, ldc, v_begin, chunk);
     return cudaGetLastError();
 }
 

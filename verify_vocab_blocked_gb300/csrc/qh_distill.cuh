@@ -8,15 +8,22 @@ namespace qh {
 constexpr int kMaxTeacher = 1024;  // teacher entries per row
 constexpr int kOthers = 16;        // other vocab rows whose exact logits are kept, at most
 constexpr int kKeptExtra = 2 * kOthers;  // kept values per row beyond the K logits
-constexpr int64_t kKeepLogitsM = 128;  // rows up to which the logits are kept for the backward
 constexpr int64_t kFewM = 16;          // rows up to which the weight-streaming kernel forms them
 constexpr int kFewSplits = 64;         // vocab splits of their softmax pass
+
+// Whether the forward keeps its logits for the backward: up to 4 GiB, the budget of
+// the backward's coefficient block, and always for few rows, whose softmax pass
+// reads them.  The backward then forms its coefficients by one pass over them
+// instead of running the logit kernel again (512 rows of the 262144 x 2560 head:
+// see distill_from_logits_kernel).
+constexpr int64_t kKeepBytes = (int64_t)4 << 30;
+inline bool keeps_logits(int64_t M, int64_t V) { return M <= kFewM || M * V <= kKeepBytes / 4; }
 
 // Columns of kept, and where a row's logits begin in it (whole 32-byte units;
 // the logits in whole blocks of 32).
 inline int64_t kept_logits_at(int64_t K) { return (K + kKeptExtra + 7) / 8 * 8; }
 inline int64_t kept_columns(int64_t M, int64_t K, int64_t V) {
-    return M <= kKeepLogitsM ? kept_logits_at(K) + (V + 31) / 32 * 32 : K + kKeptExtra;
+    return keeps_logits(M, V) ? kept_logits_at(K) + (V + 31) / 32 * 32 : K + kKeptExtra;
 }
 
 // What a tensor-core logit is multiplied by to take its mean error out.  Its
@@ -49,8 +56,9 @@ cudaError_t launch_distill_coeff(int64_t V, float cap, const int* pos, int64_t M
 cudaError_t launch_distill_split(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
                                  const int* pos, int64_t M, Partial* part, cudaStream_t st);
 cudaError_t launch_distill_from_logits(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
-                                       const int* pos, int64_t M, const float* lse, __half* coeff,
-                                       int64_t ldc, int64_t v_begin, int64_t chunk, cudaStream_t st);
+                                       const int* rows, const int* count, int64_t M, const float* lse,
+                                       __half* coeff, int64_t ldc, int64_t v_begin, int64_t chunk,
+                                       cudaStream_t st);
 cudaError_t launch_distill_dh(const float* dhp, int S, int64_t Mpad, int H, const int* pos,
                               int64_t M, const int* err, void* dh, cudaStream_t st);
 

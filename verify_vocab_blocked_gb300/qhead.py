@@ -486,6 +486,16 @@ def _out_code(dtype) -> int:
     return _SB_CODE[dtype]
 
 
+def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
+    """A workspace of this call's own.  It is allocated on the current stream:
+    with another one given, that one's use of it is recorded, so that it is not
+    handed out again before the call's kernels are done."""
+    w = alloc_workspace(nbytes, dev)
+    if stream is not None:
+        w.record_stream(stream)
+    return w
+
+
 def _size(n: int) -> int:
     if n == ctypes.c_size_t(-1).value:
         raise QheadError(QHEAD_EINVAL, last_error())
@@ -526,7 +536,8 @@ def embed_bwd(head: Head, tokens: torch.Tensor, dout: torch.Tensor, scale: float
         raise ValueError(f"dw must be a contiguous float32 [{head.V}, {head.H}] tensor on {dev}")
     c = head.c()
     if workspace is None:
-        workspace = alloc_workspace(_size(lib().qhead_embed_bwd_workspace(ctypes.byref(c), M)), dev)
+        workspace = _scratch(_size(lib().qhead_embed_bwd_workspace(ctypes.byref(c), M)), dev,
+                             stream)
     _check(lib().qhead_embed_bwd(ctypes.byref(c), tokens.data_ptr(), M, _ptr(mask), scale,
                                  dout.data_ptr(), _SB_CODE[dout.dtype], dw.data_ptr(), int(add),
                                  workspace.data_ptr(), workspace.numel(), _stream(stream)))
@@ -594,7 +605,7 @@ def layer_norm_bwd(x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor | N
     dw = torch.empty(H, dtype=torch.float32, device=dev)
     db = torch.empty(H, dtype=torch.float32, device=dev) if want_dbias else None
     if workspace is None:
-        workspace = alloc_workspace(_size(lib().qhead_layer_norm_bwd_workspace(M, H)), dev)
+        workspace = _scratch(_size(lib().qhead_layer_norm_bwd_workspace(M, H)), dev, stream)
     _check(lib().qhead_layer_norm_bwd(x.data_ptr(), _SB_CODE[x.dtype], _row_stride(x, M, H), M, H,
                                       weight.data_ptr(), _SB_CODE[weight.dtype], _ptr(mean),
                                       rstd.data_ptr(), dy.data_ptr(), _SB_CODE[dy.dtype],
@@ -639,7 +650,7 @@ def distill_fwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     kept = torch.empty(M, _kept_columns(c, M, K), dtype=torch.float32, device=dev)
     if workspace is None:
         n = _size(lib().qhead_distill_fwd_workspace(ctypes.byref(c), M, K))
-        workspace = alloc_workspace(n, dev)
+        workspace = _scratch(n, dev, stream)
     _check(lib().qhead_distill_fwd(ctypes.byref(c), h.data_ptr(), M, ids.data_ptr(),
                                    tlogits.data_ptr(), _SB_CODE[tlogits.dtype], K, temperature,
                                    _ptr(mask), loss.data_ptr(), lse.data_ptr(), kept.data_ptr(),
@@ -666,7 +677,7 @@ def distill_bwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     dh = torch.empty(M, head.H, dtype=torch.bfloat16, device=dev)
     if workspace is None:
         n = _size(lib().qhead_distill_bwd_workspace(ctypes.byref(c), M, K))
-        workspace = alloc_workspace(n, dev)
+        workspace = _scratch(n, dev, stream)
     _check(lib().qhead_distill_bwd(ctypes.byref(c), h.data_ptr(), M, ids.data_ptr(),
                                    tlogits.data_ptr(), _SB_CODE[tlogits.dtype], K, temperature,
                                    _ptr(mask), kept.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
