@@ -1099,8 +1099,9 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
         ta.l2e = 1.4426950408889634f * inv_t;
         ta.unbias = qh::distill_unbias(head->H);
         if (z) {
-            if ((e = qh::launch_distill_from_logits(z, ld, head->V, head->softcap, inv_t, rows, count, M, lse,
-                                                    coeff, p.chunk, (int64_t)vt0 * tr, (int64_t)(vt1 - vt0) * tr,
+            if ((e = qh::launch_distill_from_logits(z, ld, head->V, head->softcap, inv_t,
+                                                    M <= qh::kFewM ? 1.f : qh::distill_unbias(head->H),
+                                                    rows, count, M, lse, coeff, p.chunk, (int64_t)vt0 * tr, (int64_t)(vt1 - vt0) * tr,
                                                     st)))
                 return cuda_fail(e, "distill_from_logits");
         } else if ((e = qh::launch_tc_fwd(th, tw_logit, ta, head->bits, true, p.grid, st))) {

@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kSplitThreads) distill_split_kernel(
 // columns of one active row; the rows past the active ones are not written
 // (nothing reads what the contraction makes of them).
 __global__ void __launch_bounds__(256) distill_from_logits_kernel(
-    const float* __restrict__ z, int64_t ld, int64_t V, float cap, float inv_t,
+    const float* __restrict__ z, int64_t ld, int64_t V, float cap, float inv_t, float unbias,
     const int* __restrict__ rows, const int* __restrict__ count, const float* __restrict__ lse,
     __half* __restrict__ coeff, int64_t ldc, int64_t v_begin, int64_t chunk) {
     constexpr float kL2e = 1.4426950408889634f;
@@ -588,8 +588,9 @@ __global__ void __launch_bounds__(256) distill_from_logits_kernel(
     const int64_t r = rows[i];
     const int64_t c0 = ((int64_t)(blockIdx.x % per_row) * 256 + threadIdx.x) * 8;
     if (c0 >= chunk) return;
-    const float lsb = lse[r] * kL2e - 14.f, l2e = kL2e * inv_t;
-    const float k2 = cap > 0.f ? 2.f * kL2e / cap : 0.f;
+    const float lsb = lse[r] * kL2e - 14.f;
+    const float k2 = cap > 0.f ? 2.f * kL2e / cap * unbias : 0.f;
+    const float l2e = kL2e * inv_t * (cap > 0.f ? 1.f : unbias);
     float x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = -INFINITY;
@@ -706,12 +707,12 @@ cudaError_t launch_distill_split(const float* z, int64_t ld, int64_t V, float ca
 }
 
 cudaError_t launch_distill_from_logits(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
-                                       const int* rows, const int* count, int64_t M, const float* lse,
+                                       float unbias, const int* rows, const int* count, int64_t M, const float* lse,
                                        __half* coeff, int64_t ldc, int64_t v_begin, int64_t chunk,
                                        cudaStream_t st) {
     // (within 2^31 blocks: M V is at most 2^30 here, or M at most kFewM)
     distill_from_logits_kernel<<<(unsigned)((chunk / 8 + 255) / 256 * M), 256, 0, st>>>(
-        z, ld, V, cap, inv_t, rows, count, lse, coeff, ldc, v_begin, chunk);
+        z, ld, V, cap, inv_t, unbias, rows, count, lse, coeff, ldc, v_begin, chunk);
     return cudaGetLastError();
 }
 

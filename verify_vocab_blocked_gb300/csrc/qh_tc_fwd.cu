@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                                     uint32_t o[8];
 #pragma unroll
                                     for (int j = 0; j < 8; ++j)
-                                        o[j] = __float_as_uint(x[8 * q + j] * a.unbias);
+                                        o[j] = __float_as_uint(x[8 * q + j]);
                                     tc::st_global_v8(zrow + col0 + 8 * q, o);
                                 }
                             }

@@ -89,7 +89,7 @@ struct TcFwdArgs {
     // Distillation epilogues (l2e > 0 selects them): l2e = log2(e) / temperature;
     // sid: per compact row, sid_ld ascending vocab rows (the last INT32_MAX)
     // that the softmax epilogue leaves out; unbias: see distill_unbias.
-    // zout (NULL: none): the logits times unbias, -inf at the left-out rows, at
+    // zout (NULL: none): the raw logits, -inf at the left-out rows, at
     // zout[original row * zout_ld + vocab row], written in whole blocks of 32.
     float l2e;
     float unbias;

@@ -481,9 +481,10 @@ def _tokens(head: Head, t: torch.Tensor) -> int:
 
 
 def _out_code(dtype) -> int:
-    if dtype not in _SB_CODE:
+    code = _SB_CODE.get(dtype)
+    if code is None:
         raise ValueError("out_dtype must be float16, bfloat16 or float32")
-    return _SB_CODE[dtype]
+    return code
 
 
 def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
@@ -508,10 +509,12 @@ def embed(head: Head, tokens: torch.Tensor, scale: float = 1.0, mask: torch.Tens
     is off, NaN where a token lies outside [0, V)."""
     M = _tokens(head, tokens)
     dev = tokens.device
-    mask = _mask(mask, M, dev)
+    if mask is not None:
+        mask = _mask(mask, M, dev)
     code = _out_code(out_dtype)
-    out = torch.empty(M, head.H, dtype=out_dtype, device=dev)
-    _check(lib().qhead_embed(ctypes.byref(head.c()), tokens.data_ptr(), M, _ptr(mask), scale,
+    c = head.c()
+    out = torch.empty((M, c.H), dtype=out_dtype, device=dev)
+    _check(lib().qhead_embed(ctypes.byref(c), tokens.data_ptr(), M, _ptr(mask), scale,
                              out.data_ptr(), code, _stream(stream)))
     return out
 
