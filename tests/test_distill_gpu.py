@@ -295,3 +295,45 @@ def test_nan_rows_stay_alone(M):
     bad[2] = bad[4] = True
     assert torch.isnan(loss[2]) and not torch.isfinite(loss[4]) and torch.isnan(dh[2]).all()
     assert torch.equal(loss[~bad], good[~bad]) and torch.isfinite(dh[~bad]).all()
+
+
+def test_many_rows_of_a_small_vocabulary():
+    """More rows than a grid's second axis holds, logits kept."""
+    M, V, H, K = 70001, 300, 128, 3
+    head = qhead.Head(*make_table(V, H, 8, 90), 8, softcap=20.0)
+    g = gen(91)
+    h = torch.randn(M, H, device="cuda", generator=g).to(torch.bfloat16)
+    ids = torch.randint(0, V, (M, K), device="cuda", generator=g).int()
+    t = torch.randn(M, K, device="cuda", generator=g)
+    loss, lse, kept = qhead.distill_fwd(head, h, ids, t)
+    dh = qhead.distill_bwd(head, h, ids, t, kept, lse, torch.ones(M, device="cuda"))
+    W = table64(head.wq, head.scales, head.biases, 8)
+    hd = h.double().requires_grad_(True)
+    L, E, _, _ = distill64(W, hd, ids, t, 1.0, 20.0)
+    ref, = torch.autograd.grad(L.sum(), hd)
+    assert (lse.double() - E).abs().max() <= 2e-3
+    assert (loss.double() - L).abs().max() <= 2e-3
+    assert ((dh.double() - ref).norm(dim=1) <= 4e-3 * ref.norm(dim=1) + 1e-7).all()
+
+
+def test_logits_too_large_to_keep():
+    """Past 4 GiB of logits the backward runs the logit kernel again: the same
+    gradient as with the logits kept, within the coefficients' own rounding."""
+    M, V, H, K = 4500, 262144, 128, 4
+    head = qhead.Head(*make_table(V, H, 4, 92), 4)
+    g = gen(93)
+    h = torch.randn(M, H, device="cuda", generator=g).to(torch.bfloat16)
+    ids = torch.randint(0, V, (M, K), device="cuda", generator=g).int()
+    t = torch.randn(M, K, device="cuda", generator=g)
+    dl = torch.ones(M, device="cuda")
+    loss, lse, kept = qhead.distill_fwd(head, h, ids, t)
+    assert kept.shape[1] < V
+    dh = qhead.distill_bwd(head, h, ids, t, kept, lse, dl)
+    n = 400
+    loss2, lse2, kept2 = qhead.distill_fwd(head, h[:n], ids[:n], t[:n])
+    assert kept2.shape[1] > V
+    dh2 = qhead.distill_bwd(head, h[:n], ids[:n], t[:n], kept2, lse2, dl[:n])
+    # an fp32 sum of V terms in two groupings; a coefficient's half step in fp16 twice,
+    # half a step of bf16 twice
+    assert (lse[:n] - lse2).abs().max() <= 1e-4 and (loss[:n] - loss2).abs().max() <= 1e-4
+    assert ((dh[:n].double() - dh2.double()).norm() / dh2.double().norm()).item() <= 2 ** -7

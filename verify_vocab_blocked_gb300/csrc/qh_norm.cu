@@ -186,8 +186,14 @@ __device__ __forceinline__ float value_of(uint32_t u) {
 constexpr int kElemWarps = 8;  // rows of a block at NT = 32
 constexpr int elem_block(int nt) { return nt == 32 ? 32 * kElemWarps : nt; }
 
+// Blocks to an SM (each within 65536 registers).
+constexpr int elem_fwd_blocks(int nt, int ne) {
+    return nt > 256 ? 1 : ne <= 8 ? 1024 / elem_block(nt) : 48 / ne;
+}
+constexpr int elem_bwd_blocks(int nt) { return nt > 256 ? 1 : 512 / elem_block(nt); }
+
 template <typename T, int NT, int NE>
-__global__ void __launch_bounds__(elem_block(NT), NT > 256 ? 1 : NE <= 8 ? 1024 / elem_block(NT) : 48 / NE)
+__global__ void __launch_bounds__(elem_block(NT), elem_fwd_blocks(NT, NE))
     norm_fwd_elem_kernel(const NormArgs a) {
     __shared__ float red[2][64];
     constexpr int warps = NT / 32, rows = NT == 32 ? kElemWarps : 1;
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(elem_block(NT), NT > 256 ? 1 : NE <= 8 ? 1024 
 }
 
 template <typename T, int NT, int NE>
-__global__ void __launch_bounds__(elem_block(NT), NT <= 256 ? 2 : 1)
+__global__ void __launch_bounds__(elem_block(NT), elem_bwd_blocks(NT))
     norm_bwd_elem_kernel(const NormBwdArgs a) {
     __shared__ float red[2][64];
     extern __shared__ float cols[];  // NT = 32: the warps' columns at the end
@@ -662,16 +668,26 @@ cudaError_t pick_fwd(const NormArgs& a, cudaStream_t st) {
     return elem_shape(H, [&](auto nt, auto ne) {
         constexpr int NT = decltype(nt)::value, NE = decltype(ne)::value, B = elem_block(NT);
         const int64_t blocks = NT == 32 ? (a.M + kElemWarps - 1) / kElemWarps : a.M;
-        const int64_t most = 152 * (int64_t)(1024 / B);
+        const int64_t most = 152 * (int64_t)elem_fwd_blocks(NT, NE);
         norm_fwd_elem_kernel<T, NT, NE><<<(unsigned)(blocks < most ? blocks : most), B, 0, st>>>(a);
         return cudaGetLastError();
     });
 }
 
+// The backward's rows are dealt to the blocks in equal shares, so the blocks are as
+// many as the SMs hold at once (152: GB300's SMs; at most a.grid, which the partial
+// rows are planned for).  `a.grid` becomes that number.
+void fit_grid(NormBwdArgs& a, int per_sm) {
+    const int n = 152 * (per_sm < 1 ? 1 : per_sm);
+    if (a.grid > n) a.grid = n;
+}
+
 template <typename T, typename DT, int R, int REGS>
-cudaError_t go_ring(const NormBwdArgs& a, cudaStream_t st) {
+cudaError_t go_ring(NormBwdArgs& a, cudaStream_t st) {
     const int threads = (a.H / 8 + 31) / 32 * 32;
     const int smem = kStages * R * threads * 8 * (int)(sizeof(T) + sizeof(DT));
+    const int by_regs = 65536 / (REGS * threads), by_smem = 227 * 1024 / (smem + 1024 + 512);
+    fit_grid(a, by_regs < by_smem ? by_regs : by_smem);
     auto go = [&](auto center) {
         auto* fn = norm_bwd_ring_kernel<T, DT, R, decltype(center)::value, REGS>;
         if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), smem)) return e;
@@ -684,12 +700,12 @@ cudaError_t go_ring(const NormBwdArgs& a, cudaStream_t st) {
 // Two rows a step while their threads fit 512 (a step's barrier is shared by
 // both), one above.
 template <typename T, typename DT>
-cudaError_t pick_ring(const NormBwdArgs& a, cudaStream_t st) {
+cudaError_t pick_ring(NormBwdArgs& a, cudaStream_t st) {
     return a.H <= 4096 ? go_ring<T, DT, 2, 80>(a, st) : go_ring<T, DT, 1, 64>(a, st);
 }
 
 template <typename T>
-cudaError_t pick_bwd(const NormBwdArgs& a, cudaStream_t st) {
+cudaError_t pick_bwd(NormBwdArgs& a, cudaStream_t st) {
     const bool vec = a.H % 8 == 0 && a.ldx % 8 == 0 && a.ldy % 8 == 0 && aligned16(a.x) &&
                      aligned16(a.dy) && aligned16(a.dx);
     if (vec)
@@ -699,6 +715,7 @@ cudaError_t pick_bwd(const NormBwdArgs& a, cudaStream_t st) {
     return elem_shape(a.H, [&](auto nt, auto ne) {
         constexpr int NT = decltype(nt)::value, NE = decltype(ne)::value;
         const int smem = NT == 32 ? 2 * kElemWarps * a.H * (int)sizeof(float) : 0;
+        fit_grid(a, elem_bwd_blocks(NT));
         norm_bwd_elem_kernel<T, NT, NE><<<(unsigned)a.grid, elem_block(NT), smem, st>>>(a);
         return cudaGetLastError();
     });
@@ -713,9 +730,9 @@ cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t st) {
 }
 
 int norm_bwd_grid(int64_t M, int H) {
-    // Blocks per SM: as many as 80 registers a thread leave (H / 8 threads), at
-    // most 8 -- 16 for narrow rows -- since each adds a partial row.  152:
-    // GB300's SMs (the workspace query needs no device).
+    // The most blocks the partial rows are planned for: as many as 80 registers a
+    // thread leave (H / 8 threads), at most 8 an SM -- 16 for narrow rows -- since
+    // each adds a partial row.  (The workspace query needs no device.)
     const int threads = H < 256 ? 32 : (H / 8 + 31) / 32 * 32;
     const int most = H <= 512 ? 16 : 8;
     int per_sm = 65536 / (80 * threads);
@@ -724,7 +741,8 @@ int norm_bwd_grid(int64_t M, int H) {
     return (int)(M < want ? (M < 1 ? 1 : M) : want);
 }
 
-cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
+cudaError_t launch_norm_bwd(const NormBwdArgs& args, cudaStream_t st) {
+    NormBwdArgs a = args;
     cudaError_t e = a.x_type == kSbF32    ? pick_bwd<float>(a, st)
                     : a.x_type == kSbBf16 ? pick_bwd<__nv_bfloat16>(a, st)
                                           : pick_bwd<__half>(a, st);
@@ -732,10 +750,10 @@ cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t st) {
     const float* part = a.part;
     int n = a.grid, H = a.H;
     float *dw = a.dw, *db = a.db;
-    void* args[] = {&part, &n, &H, &dw, &db};
+    void* ptrs[] = {&part, &n, &H, &dw, &db};
     return launch_dependent(reinterpret_cast<const void*>(norm_join_kernel),
                             dim3((unsigned)((a.H + 31) / 32), a.db ? 2 : 1), dim3(32, kJoinRows), 0, st,
-                            args);
+                            ptrs);
 }
 
 }  // namespace qh
