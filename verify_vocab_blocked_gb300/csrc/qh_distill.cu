@@ -181,9 +181,11 @@ __device__ __forceinline__ void exact_parts(const __nv_bfloat16* __restrict__ hr
 template <int BITS>
 __global__ void __launch_bounds__(kThreads) distill_prep_kernel(
     const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, float cap,
-    const __nv_bfloat16* __restrict__ h, const int* __restrict__ pos,
+    const __nv_bfloat16* __restrict__ h, const int* pos,
     const int32_t* __restrict__ ids, int K, int* __restrict__ sid, float* kept, int64_t ld,
     float* zout) {
+    tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     const int64_t r = blockIdx.x;
     const int i = pos[r];
     const int32_t* idr = ids + r * K;
@@ -294,9 +296,11 @@ __global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
     const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, float cap,
     const __nv_bfloat16* __restrict__ h, const int* __restrict__ pos,
     const int32_t* __restrict__ ids, const T* __restrict__ tl, int K, float inv_t, float unbias,
-    float* kept, int64_t ld, const Partial* __restrict__ part, int S,
-    const int* __restrict__ S_dev, const int* __restrict__ err, float* __restrict__ loss,
+    float* kept, int64_t ld, const Partial* part, int S,
+    const int* S_dev, const int* err, float* __restrict__ loss,
     float* __restrict__ lse) {
+    tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     __shared__ float2 cand_sh[kMaxShares];  // candidates (v, i) of enough share
     __shared__ int n_cand;
     __shared__ float red[kWarps];
@@ -456,10 +460,12 @@ __global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
 // row with nothing to learn from, NaN for a bad one).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) distill_coeff_kernel(
-    int64_t V, float cap, const int* __restrict__ pos, const int32_t* __restrict__ ids,
+    int64_t V, float cap, const int* pos, const int32_t* __restrict__ ids,
     const T* __restrict__ tl, int K, float inv_t, const float* __restrict__ kept, int64_t ld_kept,
     const float* __restrict__ lse, const float* __restrict__ dloss, float* __restrict__ geff,
-    __half* __restrict__ coeff, int64_t ld, int64_t v_begin, int64_t chunk) {
+    __half* coeff, int64_t ld, int64_t v_begin, int64_t chunk) {
+    tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     const int64_t r = blockIdx.x;
     const int i = pos[r];
     if (i < 0) return;
@@ -491,8 +497,10 @@ __global__ void __launch_bounds__(kThreads) distill_coeff_kernel(
 // the two largest raw logits of its threads' best.
 constexpr int kSplitThreads = 256;
 __global__ void __launch_bounds__(kSplitThreads) distill_split_kernel(
-    const float* __restrict__ z, int64_t ld, int64_t V, float cap, float inv_t,
-    const int* __restrict__ pos, Partial* __restrict__ part, int S) {
+    const float* z, int64_t ld, int64_t V, float cap, float inv_t,
+    const int* pos, Partial* __restrict__ part, int S) {
+    tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     const int64_t r = blockIdx.y;
     const int i = pos[r], sp = blockIdx.x;
     if (i < 0) return;
@@ -578,8 +586,10 @@ __global__ void __launch_bounds__(kSplitThreads) distill_split_kernel(
 // (nothing reads what the contraction makes of them).
 __global__ void __launch_bounds__(256) distill_from_logits_kernel(
     const float* __restrict__ z, int64_t ld, int64_t V, float cap, float inv_t, float unbias,
-    const int* __restrict__ rows, const int* __restrict__ count, const float* __restrict__ lse,
+    const int* rows, const int* count, const float* __restrict__ lse,
     __half* __restrict__ coeff, int64_t ldc, int64_t v_begin, int64_t chunk) {
+    tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     constexpr float kL2e = 1.4426950408889634f;
     // blocks run along a row, row after row
     const int per_row = (int)((chunk / 8 + 255) / 256);
@@ -618,11 +628,13 @@ __global__ void __launch_bounds__(256) distill_from_logits_kernel(
 
 // One block per row: the K slices of the contraction in order, rounded once to
 // bf16.  Inactive rows are zeros; if a head kernel gave up, active rows NaN.
-__global__ void __launch_bounds__(256) distill_dh_kernel(const float* __restrict__ dhp, int S,
+__global__ void __launch_bounds__(256) distill_dh_kernel(const float* dhp, int S,
                                                          int64_t Mpad, int H,
                                                          const int* __restrict__ pos,
-                                                         const int* __restrict__ err,
+                                                         const int* err,
                                                          __nv_bfloat16* __restrict__ dh) {
+    tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     const int64_t r = blockIdx.x;
     const int i = pos[r];
     const bool bad = *err != 0;
@@ -662,13 +674,8 @@ cudaError_t launch_distill_prep(const uint32_t* wq, SbView sb, int64_t V, int H,
                                 float* zout, cudaStream_t st) {
     constexpr int per = kWarps * kDotsPerWarp;
     const dim3 grid((unsigned)M, (unsigned)((K + per - 1) / per));
-    if (bits == 4)
-        distill_prep_kernel<4><<<grid, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, K, sid, kept, ld,
-                                                        zout);
-    else
-        distill_prep_kernel<8><<<grid, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, K, sid, kept, ld,
-                                                        zout);
-    return cudaGetLastError();
+    auto* fn = bits == 4 ? distill_prep_kernel<4> : distill_prep_kernel<8>;
+    return launch_after(fn, grid, dim3(kThreads), st, wq, sb, V, H, cap, h, pos, ids, K, sid, kept, ld, zout);
 }
 
 cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, int H, int bits,
@@ -680,9 +687,9 @@ cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, in
     return with_type(t_type, [&](auto* tag) {
         using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
         auto* fn = bits == 4 ? distill_finalize_kernel<4, T> : distill_finalize_kernel<8, T>;
-        fn<<<(unsigned)M, kThreads, 0, st>>>(wq, sb, V, H, cap, h, pos, ids, static_cast<const T*>(tl), K,
-                                             inv_t, unbias, kept, ld, part, S, S_dev, err, loss, lse);
-        return cudaGetLastError();
+        return launch_after(fn, dim3((unsigned)M), dim3(kThreads), st, wq, sb, V, H, cap, h, pos, ids,
+                            static_cast<const T*>(tl), K, inv_t, unbias, kept, ld, part, S, S_dev, err, loss,
+                            lse);
     });
 }
 
@@ -692,35 +699,33 @@ cudaError_t launch_distill_coeff(int64_t V, float cap, const int* pos, int64_t M
                                  const float* dloss, float* geff, __half* coeff, int64_t ld,
                                  int64_t v_begin, int64_t chunk, cudaStream_t st) {
     return with_type(t_type, [&](auto* tag) {
-        distill_coeff_kernel<<<(unsigned)M, kThreads, 0, st>>>(
-            V, cap, pos, ids, static_cast<decltype(tag)>(tl), K, inv_t, kept, ld_kept, lse, dloss, geff, coeff,
-            ld, v_begin, chunk);
-        return cudaGetLastError();
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
+        return launch_after(distill_coeff_kernel<T>, dim3((unsigned)M), dim3(kThreads), st, V, cap, pos, ids,
+                            static_cast<const T*>(tl), K, inv_t, kept, ld_kept, lse, dloss, geff, coeff, ld,
+                            v_begin, chunk);
     });
 }
 
 cudaError_t launch_distill_split(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
                                  const int* pos, int64_t M, Partial* part, cudaStream_t st) {
-    distill_split_kernel<<<dim3(kFewSplits, (unsigned)M), kSplitThreads, 0, st>>>(z, ld, V, cap, inv_t, pos,
-                                                                                  part, kFewSplits);
-    return cudaGetLastError();
+    return launch_after(distill_split_kernel, dim3(kFewSplits, (unsigned)M), dim3(kSplitThreads), st, z, ld, V,
+                        cap, inv_t, pos, part, kFewSplits);
 }
 
 cudaError_t launch_distill_from_logits(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
-                                       float unbias, const int* rows, const int* count, int64_t M, const float* lse,
-                                       __half* coeff, int64_t ldc, int64_t v_begin, int64_t chunk,
-                                       cudaStream_t st) {
+                                       float unbias, const int* rows, const int* count, int64_t M,
+                                       const float* lse, __half* coeff, int64_t ldc, int64_t v_begin,
+                                       int64_t chunk, cudaStream_t st) {
     // (within 2^31 blocks: M V is at most 2^30 here, or M at most kFewM)
-    distill_from_logits_kernel<<<(unsigned)((chunk / 8 + 255) / 256 * M), 256, 0, st>>>(
-        z, ld, V, cap, inv_t, unbias, rows, count, lse, coeff, ldc, v_begin, chunk);
-    return cudaGetLastError();
+    const dim3 grid((unsigned)((chunk / 8 + 255) / 256 * M));
+    return launch_after(distill_from_logits_kernel, grid, dim3(256), st, z, ld, V, cap, inv_t, unbias, rows,
+                        count, lse, coeff, ldc, v_begin, chunk);
 }
 
 cudaError_t launch_distill_dh(const float* dhp, int S, int64_t Mpad, int H, const int* pos,
                               int64_t M, const int* err, void* dh, cudaStream_t st) {
-    distill_dh_kernel<<<(unsigned)M, 256, 0, st>>>(dhp, S, Mpad, H, pos, err,
-                                                   static_cast<__nv_bfloat16*>(dh));
-    return cudaGetLastError();
+    return launch_after(distill_dh_kernel, dim3((unsigned)M), dim3(256), st, dhp, S, Mpad, H, pos, err,
+                        static_cast<__nv_bfloat16*>(dh));
 }
 
 }  // namespace qh

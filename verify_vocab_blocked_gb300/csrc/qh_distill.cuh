@@ -56,9 +56,9 @@ cudaError_t launch_distill_coeff(int64_t V, float cap, const int* pos, int64_t M
 cudaError_t launch_distill_split(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
                                  const int* pos, int64_t M, Partial* part, cudaStream_t st);
 cudaError_t launch_distill_from_logits(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
-                                       float unbias, const int* rows, const int* count, int64_t M, const float* lse,
-                                       __half* coeff, int64_t ldc, int64_t v_begin, int64_t chunk,
-                                       cudaStream_t st);
+                                       float unbias, const int* rows, const int* count, int64_t M,
+                                       const float* lse, __half* coeff, int64_t ldc, int64_t v_begin,
+                                       int64_t chunk, cudaStream_t st);
 cudaError_t launch_distill_dh(const float* dhp, int S, int64_t Mpad, int H, const int* pos,
                               int64_t M, const int* err, void* dh, cudaStream_t st);
 

@@ -341,7 +341,7 @@ constexpr int kMaxChunk = 64;
 // Block = chunk sorted rows x all columns, thread = 8 columns.
 template <typename T>
 __global__ void __launch_bounds__(kMaxH / 8) embed_sum_kernel(
-    const uint2* __restrict__ sorted, const int* __restrict__ info, int chunk, int H, float scale,
+    const uint2* sorted, const int* info, int chunk, int H, float scale,
     const T* __restrict__ dy, float* dw, int accumulate, float* __restrict__ part) {
     tc::grid_dep_wait();
     tc::grid_dep_trigger();
@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(kMaxH / 8) embed_sum_kernel(
 // every chunk of its run: 28 us at 32768 rows with one group).
 constexpr int kJoinGroups = 4;
 __global__ void __launch_bounds__(1024) embed_join_kernel(
-    const uint2* __restrict__ sorted, const int* __restrict__ info, int chunk, int H, float scale,
-    const float* __restrict__ part, float* dw, int accumulate) {
+    const uint2* sorted, const int* info, int chunk, int H, float scale,
+    const float* part, float* dw, int accumulate) {
     extern __shared__ __align__(16) float sums[];  // [groups - 1][H]
     tc::grid_dep_wait();
     const int n = info[0];

@@ -86,8 +86,10 @@ constexpr int ctas_per_sm(int bits, int nt) { return bits == 4 && nt == 1 ? 3 : 
 template <int BITS, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS, NT)) few_dh_kernel(
     const uint32_t* __restrict__ wq, const __half* __restrict__ scales, const __half* __restrict__ biases,
-    int64_t V, int H, const __half* __restrict__ coeff, int64_t ldc, int n_rows, float* __restrict__ part,
+    int64_t V, int H, const __half* coeff, int64_t ldc, int n_rows, float* __restrict__ part,
     int S) {
+    tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     // [scales, biases][group][row]: a lane's four rows of a step are 8 bytes
     __shared__ __align__(16) __half sb_sh[2][2][kGroups][kBlockRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -227,8 +229,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS, NT)) few_dh_kernel
 // share of the ranges each.
 constexpr int kJoinGroups = 16;
 __global__ void __launch_bounds__(16 * kJoinGroups) few_join_kernel(
-    const float* __restrict__ part, int S, int H, const int* __restrict__ pos,
-    const float* __restrict__ geff, const int* __restrict__ err, __nv_bfloat16* __restrict__ dh) {
+    const float* part, int S, int H, const int* __restrict__ pos,
+    const float* geff, const int* err, __nv_bfloat16* __restrict__ dh) {
+    tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     __shared__ float sh[kJoinGroups][16][8];
     const int64_t r = blockIdx.y;
     const int i = pos[r];
@@ -276,12 +280,11 @@ cudaError_t launch_few_dh(const uint32_t* wq, const __half* scales, const __half
     const dim3 grid((unsigned)((H + kColsCta - 1) / kColsCta), (unsigned)S);
     auto* fn = bits == 4 ? (M <= 8 ? few_dh_kernel<4, 1> : few_dh_kernel<4, 2>)
                          : (M <= 8 ? few_dh_kernel<8, 1> : few_dh_kernel<8, 2>);
-    fn<<<grid, kThreads, 0, st>>>(wq, scales, biases, V, H, coeff, ldc, (int)M, part, S);
-    cudaError_t e = cudaGetLastError();
-    if (e) return e;
-    few_join_kernel<<<dim3((unsigned)(H / 128), (unsigned)M), 16 * kJoinGroups, 0, st>>>(
-        part, S, H, pos, geff, err, static_cast<__nv_bfloat16*>(dh));
-    return cudaGetLastError();
+    if (cudaError_t e = launch_after(fn, grid, dim3(kThreads), st, wq, scales, biases, V, H, coeff, ldc, (int)M,
+                                     part, S))
+        return e;
+    return launch_after(few_join_kernel, dim3((unsigned)(H / 128), (unsigned)M), dim3(16 * kJoinGroups), st,
+                        part, S, H, pos, geff, err, static_cast<__nv_bfloat16*>(dh));
 }
 
 }  // namespace qh

@@ -599,7 +599,7 @@ __global__ void __maxnreg__(REGS) norm_bwd_ring_kernel(const NormBwdArgs a) {
 // 32 columns per block of 32 x 16: partial rows y, y + 16, ... per thread, then
 // the 16 sums in order.  blockIdx.y: dw, db.
 constexpr int kJoinRows = 16;
-__global__ void __launch_bounds__(32 * kJoinRows) norm_join_kernel(const float* __restrict__ part,
+__global__ void __launch_bounds__(32 * kJoinRows) norm_join_kernel(const float* part,
                                                                    int n, int H,
                                                                    float* __restrict__ dw,
                                                                    float* __restrict__ db) {

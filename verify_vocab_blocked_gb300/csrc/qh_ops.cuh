@@ -110,6 +110,25 @@ __device__ __forceinline__ float code_f32(uint32_t w0, uint32_t w1, int e) {
 
 inline int type_bytes(int type) { return type == kSbF32 ? 4 : 2; }
 
+// Launches fn as the programmatic dependent of the kernel before it on `st`: its
+// blocks may start early and wait, with tc::grid_dep_wait() as their first
+// statement (in every block, so that it ends only after that kernel).  What that
+// kernel wrote is not read through const __restrict__ pointers: such loads may be
+// moved above the wait.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*fn)(P...), dim3 grid, dim3 block, cudaStream_t st, A... a) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(a)...);
+}
+
 // ---------------------------------------------------------------- embedding
 
 cudaError_t launch_embed(const uint32_t* wq, SbView sb, int64_t V, int H, int bits,
