@@ -3,25 +3,27 @@
 // The tensor-core contraction (qh_tc_dh.cu) takes 128 token rows a tile, so its
 // cost does not fall below theirs (200 us at 262144 x 2560 whatever the rows).
 // For few rows the packed table's bytes are the floor (56 us there), and next to
-// it the issue rate of unpacking: here the weights go from global memory to
-// mma.sync operands in registers, with nothing staged but the scales.
+// it the issue rate of unpacking: here the weights are unpacked in registers,
+// straight into mma.sync operands.
 //
 // mma.m16n8k16: M = hidden columns, K = vocab rows, N = tokens (one tile of 8, or
 // two).  A warp owns 128 columns; lane (g, t) = (lane / 4, lane % 4).  The vocab
-// rows of a block of 64 are dealt so that lane t holds rows 16 t .. 16 t + 15, four
-// to each of the block's four steps: its coefficients are 32 contiguous bytes per
-// token, and its codes of a row (columns 16 g .. 16 g + 15) one 8-byte (4 bits) or
-// 16-byte (8 bits) load.  Column tile i of the warp is codes i and i + 8 of each
+// rows of a block of 32 are dealt so that lane t holds rows 8 t .. 8 t + 7, four to
+// each of the block's two steps: its coefficients are 16 contiguous bytes per
+// token, and its codes of a row (columns 16 g .. 16 g + 15) one read of 8 (4 bits)
+// or 16 bytes (8 bits).  Column tile i of the warp is codes i and i + 8 of each
 // lane g, so two rows' words give the A operand's pairs by byte permutation: (row 0
 // code i, row 1 code i).  w = fma(q, s, b) in fp16, one rounding, as in the
-// tensor-core kernels.  The products of a block's four steps need no data of
-// another lane.
+// tensor-core kernels.
 //
-// The issue and latency of the unpacking and of mma.sync bound it, not the bytes:
-// 104 us at up to 8 rows, 135 at up to 16 (262144 x 2560, 4 bits; 80 us at 13 rows
-// of 131072 x 2560, 8 bits).  With the tokens as M, 16 whatever their number, up to
-// 16 rows took 148 us; 64 columns a warp, for more warps, 160 and 197 (loads of 4
-// bytes); two token tiles within three CTAs to an SM spill, 199.
+// Each warp copies its codes, scales and coefficients through a ring of its own in
+// shared memory (cp.async): no block barrier, and no registers for loads in flight.
+// With them in registers (a block of 64 rows ahead) two CTAs held an SM where now
+// four do, and the kernel took 104 us at up to 8 rows and 135 at up to 16 (262144 x
+// 2560, 4 bits); it takes 81 and 101 (67 at 13 rows of 131072 x 2560, 8 bits: 80).
+// The issue of the unpacking bounds it, and mma.sync beside it (20 us a token tile).
+// With the tokens as M, 16 whatever their number, up to 16 rows took 148 us; 64
+// columns a warp, for more warps, 160 and 197 (loads of 4 bytes).
 //
 // Each warp keeps its sums in registers over the CTA's vocab range and writes them
 // once; the ranges are added in order by a second launch.
@@ -37,8 +39,20 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kColsWarp = 128, kColsCta = kColsWarp * kWarps;
-constexpr int kBlockRows = 64;
-constexpr int kGroups = kColsCta / 64;  // groups of a row in the CTA's columns
+constexpr int kBlockRows = 32, kLaneRows = kBlockRows / 4;
+
+// One stage of a warp's ring: codes (8 rows and 32 bytes of pad at a time: the
+// lanes' reads, 8 rows apart, fall on distinct banks), coefficients [token][row],
+// scales and biases [row][group of 2].
+template <int BITS, int NT>
+struct Stage {
+    static constexpr int kRowBytes = kColsWarp * BITS / 8;
+    static constexpr int kPitch = kLaneRows * kRowBytes + 32;
+    static constexpr int kCoeff = 4 * kPitch, kScale = kCoeff + 8 * NT * kBlockRows * 2;
+    static constexpr int kBytes = kScale + 2 * 4 * kBlockRows;
+    static constexpr int kStages = BITS == 4 ? 3 : 2;
+    static constexpr int kCta = kWarps * kStages * kBytes;
+};
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -79,9 +93,8 @@ __device__ __forceinline__ void pairs4(const Codes<BITS>& a, const Codes<BITS>& 
     }
 }
 
-// CTAs to an SM: what the registers of the sums and of a block's codes, loaded one
-// block ahead, leave.
-constexpr int ctas_per_sm(int bits, int nt) { return bits == 4 && nt == 1 ? 3 : 2; }
+// CTAs to an SM, by the registers of the sums.
+constexpr int ctas_per_sm(int bits, int nt) { return bits == 4 && nt == 1 ? 5 : 4; }
 
 template <int BITS, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS, NT)) few_dh_kernel(
@@ -90,18 +103,20 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS, NT)) few_dh_kernel
     int S) {
     tc::grid_dep_wait();
     tc::grid_dep_trigger();
-    // [scales, biases][group][row]: a lane's four rows of a step are 8 bytes
-    __shared__ __align__(16) __half sb_sh[2][2][kGroups][kBlockRows];
+    using St = Stage<BITS, NT>;
+    extern __shared__ __align__(16) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int col0 = blockIdx.x * kColsCta + warp * kColsWarp;  // of the warp
-    const bool on = col0 < H;                                   // (H: whole warps' columns)
-    const int G = H / 64, g0 = blockIdx.x * kGroups;
+    if (col0 >= H) return;                                      // (H: whole warps' columns)
+    unsigned char* ring = smem + warp * St::kStages * St::kBytes;
+    const int G = H / 64;
     const int64_t nb = (V + kBlockRows - 1) / kBlockRows;
     const int sp = blockIdx.y;
     const int64_t b0 = nb * sp / S, b1 = nb * (sp + 1) / S;
-    const int wpr = H * BITS / 32;
-    const uint32_t* wbase = wq + (on ? col0 : 0) * BITS / 32 + g * (BITS / 2);
-    const int my_group = 2 * warp + (g >> 2);
+    const int64_t wrow = (int64_t)H * BITS / 8;  // bytes
+    const unsigned char* wbase = reinterpret_cast<const unsigned char*>(wq) + col0 * BITS / 8;
+    // scale of the lane's group in both halves' rows: bytes 0-1 or 2-3 of each word
+    const uint32_t sel = g >> 2 ? 0x7632u : 0x5410u;
 
     float acc[8][NT][4];
 #pragma unroll
@@ -111,88 +126,65 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS, NT)) few_dh_kernel
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.f;
 
-    // Scales and biases of a block: 64 rows x kGroups, four of each per thread.
-    unsigned short sr[4], br[4];
-    auto sb_fetch = [&](int64_t blk) {
+    // Rows past V copy row V - 1: their coefficients are zero.
+    auto issue = [&](int64_t blk, int slot) {
+        if (blk < b1) {
+            unsigned char* dst = ring + slot * St::kBytes;
+            const int64_t v0 = blk * kBlockRows, last = V - 1;
+            constexpr int kChunks = St::kRowBytes / 16;  // of a row
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int id = threadIdx.x + k * kThreads;  // row id / kGroups, group id % kGroups
-            const int64_t v = blk * kBlockRows + id / kGroups;
-            const int gg = g0 + id % kGroups;
-            sr[k] = br[k] = 0;
-            if (blk < b1 && v < V && gg < G) {
-                sr[k] = reinterpret_cast<const unsigned short*>(scales)[v * G + gg];
-                br[k] = reinterpret_cast<const unsigned short*>(biases)[v * G + gg];
+            for (int k = 0; k < kBlockRows * kChunks / 32; ++k) {
+                const int id = lane + 32 * k, r = id / kChunks, c = id % kChunks;
+                const int64_t v = v0 + r < last ? v0 + r : last;
+                tc::cp_async_zfill<16>(dst + r / kLaneRows * St::kPitch + r % kLaneRows * St::kRowBytes + 16 * c,
+                                       wbase + v * wrow + 16 * c, 16);
             }
-        }
-    };
-    auto sb_store = [&](int buf) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int id = threadIdx.x + k * kThreads;
-            sb_sh[buf][0][id % kGroups][id / kGroups] = __ushort_as_half(sr[k]);
-            sb_sh[buf][1][id % kGroups][id / kGroups] = __ushort_as_half(br[k]);
-        }
-    };
-    // Rows past V read row V - 1: their coefficients are zero.
-    Codes<BITS> w[4][4];
-    auto w_fetch = [&](int64_t blk, int s) {
-        if (!on || blk >= b1) return;
-        const int64_t v = blk * kBlockRows + 16 * t + 4 * s;
-        if (v + 4 <= V) {
-            const uint32_t* p = wbase + v * wpr;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[s][e].load(p + e * wpr);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[s][e].load(wbase + (v + e < V ? v + e : V - 1) * wpr);
-        }
-    };
-    uint4 cf[NT][2];  // coefficients of tokens g (and g + 8), rows 16 t .. 16 t + 15
-    auto c_fetch = [&](int64_t blk) {
-        const __half* c = coeff + blk * kBlockRows + 16 * t;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            cf[n][0] = cf[n][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (blk < b1 && g + 8 * n < n_rows) {
-                const uint4* p = reinterpret_cast<const uint4*>(c + (int64_t)(g + 8 * n) * ldc);
-                cf[n][0] = p[0];
-                cf[n][1] = p[1];
+            for (int n = 0; n < NT; ++n) {
+                const int tok = g + 8 * n, r = tok < n_rows ? tok : 0;
+                tc::cp_async_zfill<16>(dst + St::kCoeff + 64 * tok + 16 * t, coeff + r * ldc + v0 + 8 * t,
+                                       tok < n_rows ? 16 : 0);
             }
+            const int64_t v = v0 + lane < last ? v0 + lane : last;
+            tc::cp_async_zfill<4>(dst + St::kScale + 4 * lane, scales + v * G + col0 / 64, 4);
+            tc::cp_async_zfill<4>(dst + St::kScale + 4 * (kBlockRows + lane), biases + v * G + col0 / 64, 4);
         }
+        cp_async_commit();
     };
-
-    sb_fetch(b0);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) w_fetch(b0, s);
-    c_fetch(b0);
-    sb_store(0);
-    int buf = 0;
+    for (int s = 0; s < St::kStages - 1; ++s) issue(b0 + s, s);
+    int slot = 0;
     for (int64_t blk = b0; blk < b1; ++blk) {
-        __syncthreads();  // this block's scales are in; the other buffer is free
-        sb_fetch(blk + 1);
-        uint32_t cv[NT][8];
+        cp_async_wait<St::kStages - 2>();
+        __syncwarp();  // the block is in for every lane; every lane has read the one before
+        issue(blk + St::kStages - 1, slot == 0 ? St::kStages - 1 : slot - 1);
+        const unsigned char* src = ring + slot * St::kBytes;
+        uint32_t cv[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint32_t x[8] = {cf[n][0].x, cf[n][0].y, cf[n][0].z, cf[n][0].w,
-                                   cf[n][1].x, cf[n][1].y, cf[n][1].z, cf[n][1].w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) cv[n][k] = x[k];
+            const uint4 x = *reinterpret_cast<const uint4*>(src + St::kCoeff + 64 * (g + 8 * n) + 16 * t);
+            cv[n][0] = x.x; cv[n][1] = x.y; cv[n][2] = x.z; cv[n][3] = x.w;
         }
-        c_fetch(blk + 1);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const uint2 sc = *reinterpret_cast<const uint2*>(&sb_sh[buf][0][my_group][16 * t + 4 * s]);
-            const uint2 bi = *reinterpret_cast<const uint2*>(&sb_sh[buf][1][my_group][16 * t + 4 * s]);
+        for (int s = 0; s < 2; ++s) {
+            const unsigned char* sp4 = src + St::kScale + 4 * (kLaneRows * t + 4 * s);
+            const uint4 su = *reinterpret_cast<const uint4*>(sp4);
+            const uint4 bu = *reinterpret_cast<const uint4*>(sp4 + 4 * kBlockRows);
+            const uint32_t s01 = __byte_perm(su.x, su.y, sel), s23 = __byte_perm(su.z, su.w, sel);
+            const uint32_t b01 = __byte_perm(bu.x, bu.y, sel), b23 = __byte_perm(bu.z, bu.w, sel);
+            Codes<BITS> w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e].load(reinterpret_cast<const uint32_t*>(src + t * St::kPitch + (4 * s + e) * St::kRowBytes) +
+                          g * (BITS / 2));
 #pragma unroll
             for (int quad = 0; quad < 2; ++quad) {
                 uint32_t p[2][4], q[2][4];  // rows (0, 1) and (2, 3), codes of either half
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    pairs4<BITS>(w[s][0], w[s][1], half, quad, sc.x, bi.x, p[half]);
-                    pairs4<BITS>(w[s][2], w[s][3], half, quad, sc.y, bi.y, q[half]);
+                    pairs4<BITS>(w[0], w[1], half, quad, s01, b01, p[half]);
+                    pairs4<BITS>(w[2], w[3], half, quad, s23, b23, q[half]);
                 }
-                if (quad == 1) w_fetch(blk + 1, s);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t a[4] = {p[0][i], p[1][i], q[0][i], q[1][i]};
@@ -202,10 +194,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS, NT)) few_dh_kernel
                 }
             }
         }
-        sb_store(buf ^ 1);
-        buf ^= 1;
+        if (++slot == St::kStages) slot = 0;
     }
-    if (!on) return;
     // Tile i, lane (g, t): columns 16 g + i and 16 g + i + 8, tokens 2 t and 2 t + 1.
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -280,7 +270,10 @@ cudaError_t launch_few_dh(const uint32_t* wq, const __half* scales, const __half
     const dim3 grid((unsigned)((H + kColsCta - 1) / kColsCta), (unsigned)S);
     auto* fn = bits == 4 ? (M <= 8 ? few_dh_kernel<4, 1> : few_dh_kernel<4, 2>)
                          : (M <= 8 ? few_dh_kernel<8, 1> : few_dh_kernel<8, 2>);
-    if (cudaError_t e = launch_after(fn, grid, dim3(kThreads), st, wq, scales, biases, V, H, coeff, ldc, (int)M,
+    const int smem = bits == 4 ? (M <= 8 ? Stage<4, 1>::kCta : Stage<4, 2>::kCta)
+                               : (M <= 8 ? Stage<8, 1>::kCta : Stage<8, 2>::kCta);
+    if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), smem)) return e;
+    if (cudaError_t e = launch_after_smem(fn, grid, dim3(kThreads), smem, st, wq, scales, biases, V, H, coeff, ldc, (int)M,
                                      part, S))
         return e;
     return launch_after(few_join_kernel, dim3((unsigned)(H / 128), (unsigned)M), dim3(16 * kJoinGroups), st,

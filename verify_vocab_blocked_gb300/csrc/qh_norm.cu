@@ -377,11 +377,6 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // PW consecutive elements as pairs.
 template <typename T, int PW>

@@ -108,6 +108,14 @@ __device__ __forceinline__ float code_f32(uint32_t w0, uint32_t w1, int e) {
     return __uint_as_float(q | 0x4B000000u) - 8388608.f;
 }
 
+// Groups of asynchronous copies (cp.async): the end of one, and the wait that
+// leaves the N youngest in flight.
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 inline int type_bytes(int type) { return type == kSbF32 ? 4 : 2; }
 
 // Launches fn as the programmatic dependent of the kernel before it on `st`: its
@@ -116,10 +124,11 @@ inline int type_bytes(int type) { return type == kSbF32 ? 4 : 2; }
 // kernel wrote is not read through const __restrict__ pointers: such loads may be
 // moved above the wait.
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*fn)(P...), dim3 grid, dim3 block, cudaStream_t st, A... a) {
+cudaError_t launch_after_smem(void (*fn)(P...), dim3 grid, dim3 block, int smem, cudaStream_t st, A... a) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -127,6 +136,10 @@ cudaError_t launch_after(void (*fn)(P...), dim3 grid, dim3 block, cudaStream_t s
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(a)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*fn)(P...), dim3 grid, dim3 block, cudaStream_t st, A... a) {
+    return launch_after_smem(fn, grid, block, 0, st, a...);
 }
 
 // ---------------------------------------------------------------- embedding
