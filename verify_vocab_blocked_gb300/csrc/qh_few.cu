@@ -20,8 +20,10 @@
 // shared memory (cp.async): no block barrier, and no registers for loads in flight.
 // With them in registers (a block of 64 rows ahead) two CTAs held an SM where now
 // four do, and the kernel took 104 us at up to 8 rows and 135 at up to 16 (262144 x
-// 2560, 4 bits); it takes 81 and 101 (67 at 13 rows of 131072 x 2560, 8 bits: 80).
-// The issue of the unpacking bounds it, and mma.sync beside it (20 us a token tile).
+// 2560, 4 bits); it takes 74 and 93 (61 at 13 rows of 131072 x 2560, 8 bits: 80).
+// Pointers that advance by a block, against a product per row, are 8 us of that.
+// The issue of the unpacking (58 % of the slots) and mma.sync (20 us a token tile,
+// the most frequent stall) bound it; DRAM stands at 53 %.
 // With the tokens as M, 16 whatever their number, up to 16 rows took 148 us; 64
 // columns a warp, for more warps, 160 and 197 (loads of 4 bytes).
 //
@@ -113,8 +115,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS, NT)) few_dh_kernel
     const int64_t nb = (V + kBlockRows - 1) / kBlockRows;
     const int sp = blockIdx.y;
     const int64_t b0 = nb * sp / S, b1 = nb * (sp + 1) / S;
+    constexpr int kChunks = St::kRowBytes / 16;                // 16-byte copies of a row,
+    constexpr int kCopies = kBlockRows * kChunks / 32;         // of a lane, of rows kStep apart
+    constexpr int kStep = 32 / kChunks;
+    const int r0 = lane / kChunks, c0 = lane % kChunks;
     const int64_t wrow = (int64_t)H * BITS / 8;  // bytes
-    const unsigned char* wbase = reinterpret_cast<const unsigned char*>(wq) + col0 * BITS / 8;
+    const unsigned char* wbase = reinterpret_cast<const unsigned char*>(wq) + col0 * BITS / 8 + 16 * c0;
+    const uint32_t ring_w = tc::smem_u32(ring) + r0 / kLaneRows * St::kPitch + r0 % kLaneRows * St::kRowBytes + 16 * c0;
+    const uint32_t ring_c = tc::smem_u32(ring) + St::kCoeff + 64 * g + 16 * t;
+    const uint32_t ring_s = tc::smem_u32(ring) + St::kScale + 4 * lane;
+    // sources of the next block
+    const unsigned char* wp = wbase + (b0 * kBlockRows + r0) * wrow;
+    const __half* cp = coeff + (int64_t)(g < n_rows ? g : 0) * ldc + b0 * kBlockRows + 8 * t;
+    const int64_t c8 = g + 8 < n_rows ? 8 * ldc : 0;  // to the second tile's token
+    const int cn[2] = {g < n_rows ? 16 : 0, g + 8 < n_rows ? 16 : 0};
+    int64_t so = (b0 * kBlockRows + lane) * G + col0 / 64;
     // scale of the lane's group in both halves' rows: bytes 0-1 or 2-3 of each word
     const uint32_t sel = g >> 2 ? 0x7632u : 0x5410u;
 
@@ -129,25 +144,35 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(BITS, NT)) few_dh_kernel
     // Rows past V copy row V - 1: their coefficients are zero.
     auto issue = [&](int64_t blk, int slot) {
         if (blk < b1) {
-            unsigned char* dst = ring + slot * St::kBytes;
-            const int64_t v0 = blk * kBlockRows, last = V - 1;
-            constexpr int kChunks = St::kRowBytes / 16;  // of a row
+            const uint32_t at = slot * St::kBytes;
+            const int64_t v0 = blk * kBlockRows;
+            if (v0 + kBlockRows <= V) {
 #pragma unroll
-            for (int k = 0; k < kBlockRows * kChunks / 32; ++k) {
-                const int id = lane + 32 * k, r = id / kChunks, c = id % kChunks;
-                const int64_t v = v0 + r < last ? v0 + r : last;
-                tc::cp_async_zfill<16>(dst + r / kLaneRows * St::kPitch + r % kLaneRows * St::kRowBytes + 16 * c,
-                                       wbase + v * wrow + 16 * c, 16);
+                for (int k = 0; k < kCopies; ++k) {
+                    const int r = k * kStep;
+                    cp_async<16>(ring_w + at + r / kLaneRows * St::kPitch + r % kLaneRows * St::kRowBytes,
+                                 wp + r * wrow);
+                }
+                cp_async<4>(ring_s + at, scales + so);
+                cp_async<4>(ring_s + at + 4 * kBlockRows, biases + so);
+            } else {
+                const int64_t last = V - 1;
+#pragma unroll
+                for (int k = 0; k < kCopies; ++k) {
+                    const int r = k * kStep;
+                    const int64_t v = v0 + r0 + r < last ? v0 + r0 + r : last;
+                    cp_async<16>(ring_w + at + r / kLaneRows * St::kPitch + r % kLaneRows * St::kRowBytes,
+                                 wbase + v * wrow);
+                }
+                const int64_t o = (v0 + lane < last ? v0 + lane : last) * G + col0 / 64;
+                cp_async<4>(ring_s + at, scales + o);
+                cp_async<4>(ring_s + at + 4 * kBlockRows, biases + o);
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int tok = g + 8 * n, r = tok < n_rows ? tok : 0;
-                tc::cp_async_zfill<16>(dst + St::kCoeff + 64 * tok + 16 * t, coeff + r * ldc + v0 + 8 * t,
-                                       tok < n_rows ? 16 : 0);
-            }
-            const int64_t v = v0 + lane < last ? v0 + lane : last;
-            tc::cp_async_zfill<4>(dst + St::kScale + 4 * lane, scales + v * G + col0 / 64, 4);
-            tc::cp_async_zfill<4>(dst + St::kScale + 4 * (kBlockRows + lane), biases + v * G + col0 / 64, 4);
+            for (int n = 0; n < NT; ++n) cp_async<16>(ring_c + at + 512 * n, cp + n * c8, cn[n]);
+            wp += kBlockRows * wrow;
+            cp += kBlockRows;
+            so += kBlockRows * G;
         }
         cp_async_commit();
     };

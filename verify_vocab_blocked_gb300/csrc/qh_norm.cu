@@ -370,14 +370,6 @@ __global__ void __launch_bounds__(elem_block(NT), elem_bwd_blocks(NT))
 // 20000 x 4096 fp32, 149 us, 6.6 TB/s, without).
 constexpr int kStages = 3;
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-
 // PW consecutive elements as pairs.
 template <typename T, int PW>
 __device__ __forceinline__ void get_pairs(const unsigned char* p, float2* v) {

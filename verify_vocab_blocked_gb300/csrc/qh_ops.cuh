@@ -108,8 +108,21 @@ __device__ __forceinline__ float code_f32(uint32_t w0, uint32_t w1, int e) {
     return __uint_as_float(q | 0x4B000000u) - 8388608.f;
 }
 
-// Groups of asynchronous copies (cp.async): the end of one, and the wait that
-// leaves the N youngest in flight.
+// Asynchronous copies global -> shared, of 16 bytes past L1, of fewer through it;
+// of `bytes` < BYTES the rest is zeros.  The end of a group of them, and the wait
+// that leaves the N youngest groups in flight.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes) {
+    static_assert(BYTES == 16, "cp.async size");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {

@@ -178,18 +178,14 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// Asynchronous global -> shared copy of 4, 8 or 16 bytes; src_bytes = 0 writes zeros
+// Asynchronous global -> shared copy of 4 or 8 bytes; src_bytes = 0 writes zeros
 // without reading `src` (which must still be a valid address).
 template <int BYTES>
 __device__ __forceinline__ void cp_async_zfill(void* dst, const void* src, int src_bytes) {
-    static_assert(BYTES == 4 || BYTES == 8 || BYTES == 16, "cp.async size");
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes)
-                     : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src),
-                     "n"(BYTES), "r"(src_bytes)
-                     : "memory");
+    static_assert(BYTES == 4 || BYTES == 8, "cp.async size");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src),
+                 "n"(BYTES), "r"(src_bytes)
+                 : "memory");
 }
 
 // Arrive on `bar` when all of this thread's prior cp.async copies have landed
