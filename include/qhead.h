@@ -423,8 +423,11 @@ int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int
  *             logits z of the valid entries (0 elsewhere), then the exact logits
  *             of the largest other vocab rows, up to 16, and (as int32 bits, 0:
  *             none) those rows plus one; at M <= 16, or while M * V * 4 is at
- *             most 4 GiB, also the row's V logits (-inf at the listed tokens), so
- *             that the backward need not form them again.
+ *             most 4 GiB, also the row's V logits, so that the backward need not
+ *             form them again, with (q_v - p_v) * sech2 * 2^126 (-inf: 0) in
+ *             place of those of the tokens whose exact ones are kept.  In a row
+ *             without such others, +inf or -inf as the first's logit tells that
+ *             its gradient is NaN or 0.
  *   workspace device, >= qhead_distill_fwd_workspace(head, M, K) bytes,
  *             256-byte aligned.
  * Up to 16 rows the weight-streaming kernel forms the logits, above them the

@@ -1001,7 +1001,7 @@ int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const in
             return cuda_fail(e, "distill_split");
         e = qh::launch_distill_finalize(head->wq, sb_view(head), head->V, head->H, head->bits,
                                         head->softcap, hb, pos, M, ids, tlogits, t_dtype, (int)K, inv_t, 1.f,
-                                        kept, ld, few, qh::kFewSplits, nullptr, err, loss, lse, st);
+                                        kept, ld, zout, few, qh::kFewSplits, nullptr, err, loss, lse, st);
         return e ? cuda_fail(e, "distill_finalize") : QHEAD_OK;
     }
     if ((rc = stage_rows(mask, hb, M, p.Mpad, head, rows, pos, count, err, h16, st))) return rc;
@@ -1027,7 +1027,7 @@ int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const in
     hook_after(st);
     if (e) return cuda_fail(e, "tc_fwd");
     e = qh::launch_distill_finalize(head->wq, sb_view(head), head->V, head->H, head->bits, head->softcap,
-                                    hb, pos, M, ids, tlogits, t_dtype, (int)K, inv_t, ta.unbias, kept, ld,
+                                    hb, pos, M, ids, tlogits, t_dtype, (int)K, inv_t, ta.unbias, kept, ld, zout,
                                     part, 0, S_dev, err, loss, lse, st);
     return e ? cuda_fail(e, "distill_finalize") : QHEAD_OK;
 }
@@ -1066,7 +1066,7 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
     const int64_t ld = qh::kept_columns(M, K, head->V);
     // The coefficients from the kept logits, unless the stall switch wants the
     // logit kernel.
-    const float* z = qh::keeps_logits(M, head->V) && !stall ? kept + qh::kept_logits_at(K) : nullptr;
+    const bool z = qh::keeps_logits(M, head->V) && !stall;
     cudaError_t e;
     if (z) {
         if ((e = qh::launch_compact(mask, M, p.Mpad, rows, pos, count, err, st)))
@@ -1098,19 +1098,19 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
         ta.coeff_rows = (int)p.Mpad;
         ta.l2e = 1.4426950408889634f * inv_t;
         ta.unbias = qh::distill_unbias(head->H);
+        const int64_t v0 = (int64_t)vt0 * tr, nv = (int64_t)(vt1 - vt0) * tr;
         if (z) {
-            if ((e = qh::launch_distill_from_logits(z, ld, head->V, head->softcap, inv_t,
-                                                    M <= qh::kFewM ? 1.f : qh::distill_unbias(head->H),
-                                                    rows, count, M, lse, coeff, p.chunk, (int64_t)vt0 * tr, (int64_t)(vt1 - vt0) * tr,
-                                                    st)))
+            if ((e = qh::launch_distill_from_logits(kept, K, ld, head->V, head->softcap, inv_t,
+                                                    M <= qh::kFewM ? 1.f : ta.unbias, rows, count, M, lse, dloss,
+                                                    geff, coeff, p.chunk, v0, nv, st)))
                 return cuda_fail(e, "distill_from_logits");
-        } else if ((e = qh::launch_tc_fwd(th, tw_logit, ta, head->bits, true, p.grid, st))) {
-            return cuda_fail(e, "tc_coeff");
+        } else {
+            if ((e = qh::launch_tc_fwd(th, tw_logit, ta, head->bits, true, p.grid, st)))
+                return cuda_fail(e, "tc_coeff");
+            if ((e = qh::launch_distill_coeff(head->V, head->softcap, pos, M, ids, tlogits, t_dtype, (int)K,
+                                              inv_t, kept, ld, lse, dloss, geff, coeff, p.chunk, v0, nv, st)))
+                return cuda_fail(e, "distill_coeff");
         }
-        if ((e = qh::launch_distill_coeff(head->V, head->softcap, pos, M, ids, tlogits, t_dtype, (int)K,
-                                          inv_t, kept, ld, lse, dloss, geff, coeff, p.chunk, (int64_t)vt0 * tr,
-                                          (int64_t)(vt1 - vt0) * tr, st)))
-            return cuda_fail(e, "distill_coeff");
         if (z && dp.few_dh) {
             e = qh::launch_few_dh(head->wq, sc, bi, head->V, head->H, head->bits, coeff, p.chunk, M, pos, geff,
                                   err, at<float>(workspace, dp.off_few), dh, st);

@@ -19,17 +19,20 @@
 //     finalize adds their exact terms and replaces those of the largest other
 //     columns (up to kOthers), whose exact logits are kept as well;
 //   * the backward's coefficient block gets (q_k - p_k) sech2_k, formed in
-//     fp32 from the exact logits, written over the K teacher's and the kept
-//     other columns of each row before the contraction with W, so the one-hot
-//     part of the gradient needs no gather of head rows of its own.  (The other
+//     fp32 from the exact logits, in the K teacher's and the kept other columns
+//     of each row before the contraction with W, so the one-hot part of the
+//     gradient needs no gather of head rows of its own.  (The other
 //     columns belong to it: with their exact terms in lse but the tensor-core
 //     logits in q, a row with mass there came out 1e-2 off, 1.7e-3 -- bf16's
 //     rounding -- with both.)
 //
 // kept [M, ld] holds, per row, the K exact capped logits, the others' and their
 // vocab rows plus one (as integer bits, 0: none), and while they fit 4 GiB the
-// row's V logits, -inf at the teacher's: the backward then forms its coefficients
-// from them in one pass instead of running the logit kernel again.  Up to kFewM
+// row's V logits, with the coefficients themselves, times kMark, in the teacher's
+// and the others' columns: the backward then forms its coefficients from them in
+// one pass instead of running the logit kernel again and a pass over the tokens.
+// A row without others' columns marks in the first's logit what its gradient is:
+// -inf, zero (nothing to learn from), +inf, NaN (a bad teacher).  Up to kFewM
 // rows the weight-streaming kernel writes them, whose cost follows the rows (the
 // tensor-core kernel's does not: 227 us from 1 to 128 rows of the 262144 x 2560
 // head), and a softmax pass of its own reads them.
@@ -46,6 +49,11 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDotsPerWarp = 4;  // teacher logits of one row that a warp forms together
+
+// A kept coefficient's factor (exact), and the size from which on a kept value is
+// one: coefficients below kMarked / kMark = 2^-41 would be zeros in fp16 and are
+// kept as -inf, and no logit comes near 2^85.
+constexpr float kMark = 0x1p126f, kMarked = 0x1p85f;
 
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
 
@@ -292,11 +300,11 @@ constexpr float kShare = 1e-3f;
 constexpr int kMaxShares = 1024;  // at most 1 / kShare terms have that share
 
 template <int BITS, typename T>
-__global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
+__global__ void __launch_bounds__(kThreads, 4) distill_finalize_kernel(
     const uint32_t* __restrict__ wq, SbView sb, int64_t V, int H, float cap,
     const __nv_bfloat16* __restrict__ h, const int* __restrict__ pos,
     const int32_t* __restrict__ ids, const T* __restrict__ tl, int K, float inv_t, float unbias,
-    float* kept, int64_t ld, const Partial* part, int S,
+    float* kept, int64_t ld, float* zout, const Partial* part, int S,
     const int* S_dev, const int* err, float* __restrict__ loss,
     float* __restrict__ lse) {
     tc::grid_dep_wait();
@@ -312,16 +320,17 @@ __global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
     const int64_t r = blockIdx.x;
     const int i = pos[r];
     float* zr = kept + r * ld;
-    // No other columns known: rows that are off or whose kernel gave up.
-    auto no_others = [&]() {
+    // No other columns: rows that are off, whose kernel gave up, or whose gradient
+    // the mark tells.
+    auto no_others = [&](float mark) {
         for (int c = threadIdx.x; c < kOthers; c += kThreads) {
-            zr[K + c] = 0.f;
+            zr[K + c] = c == 0 ? mark : 0.f;
             zr[K + kOthers + c] = 0.f;
         }
     };
     if (i < 0) {
         if (threadIdx.x == 0) loss[r] = lse[r] = 0.f;
-        no_others();
+        no_others(0.f);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
     if (threadIdx.x == 0) n_cand = 0;
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) loss[r] = lse[r] = nan_f();
-        no_others();
+        no_others(INFINITY);
         return;
     }
 #pragma unroll
@@ -449,11 +458,33 @@ __global__ void __launch_bounds__(kThreads, 5) distill_finalize_kernel(
         if (te.tmax == -INFINITY) out = 0.f;  // nothing to learn from
         if (te.bad) out = nan_f();
         loss[r] = out;
+        red[0] = l;
+    }
+    __syncthreads();
+    if (te.bad || te.tmax == -INFINITY) {
+        no_others(te.bad ? INFINITY : -INFINITY);
+        return;
+    }
+    if (zout == nullptr) return;
+    // The listed columns' coefficients (q - p) sech2 among the logits.
+    zout += r * ld;
+    const float l = red[0], rsum = 1.f / te.tsum;
+    for (int k = threadIdx.x; k < K + n_other; k += kThreads) {
+        const int id = k < K ? id_sh[k] : other_i[k - K];
+        if (id < 0 || (int64_t)id >= V) continue;
+        float p = 0.f;  // the token's teacher mass (every entry that lists it)
+        if (k < K)
+            for (int j = 0; j < K; ++j)
+                if (id_sh[j] == id) p += expf(t_sh[j] - te.tmax) * rsum;
+        const float z = k < K ? zr[k] : other_z[k - K];
+        const float th = cap > 0.f ? z / cap : 0.f;
+        const float c = (expf(fmaf(z - top, inv_t, -l)) - p) * fmaf(-th, th, 1.f) * kMark;
+        zout[id] = fabsf(c) < kMarked ? -INFINITY : c;
     }
 }
 
-// One block per row, after the coefficient pass of the vocab chunk
-// [v_begin, v_begin + chunk): writes (q_k - p_k) sech2_k * 2^14 over the
+// Without kept logits: one block per row, after the coefficient pass of the vocab
+// chunk [v_begin, v_begin + chunk): writes (q_k - p_k) sech2_k * 2^14 over the
 // teacher's columns and the kept others (|q - p| <= 1: at most 16384 in
 // fp16, one rounding) and
 // the row's cotangent as the contraction kernel takes it, -dloss / T (0 for a
@@ -579,15 +610,15 @@ __global__ void __launch_bounds__(kSplitThreads) distill_split_kernel(
 }
 
 // The coefficient block of the chunk [v_begin, v_begin + chunk) from the kept
-// logits: q sech2 2^14 in fp16, zeros past V (and at the left-out columns, which
-// distill_coeff_kernel fills), with the arithmetic of the logit kernel's own
-// coefficient epilogue.  Bound by bytes: 4 read, 2 written per logit.  Thread = 8
+// logits: q sech2 2^14 in fp16 (zeros past V) with the arithmetic of the logit
+// kernel's own coefficient epilogue, or the kept coefficient; and the row's
+// cotangent (see distill_coeff_kernel).  Bound by bytes: 4 read, 2 written per logit.  Thread = 8
 // columns of one active row; the rows past the active ones are not written
 // (nothing reads what the contraction makes of them).
 __global__ void __launch_bounds__(256) distill_from_logits_kernel(
-    const float* __restrict__ z, int64_t ld, int64_t V, float cap, float inv_t, float unbias,
-    const int* rows, const int* count, const float* __restrict__ lse,
-    __half* __restrict__ coeff, int64_t ldc, int64_t v_begin, int64_t chunk) {
+    const float* __restrict__ z, const float* __restrict__ first_other, int64_t ld, int64_t V, float cap,
+    float inv_t, float unbias, const int* rows, const int* count, const float* __restrict__ lse,
+    const float* __restrict__ dloss, float* __restrict__ geff, __half* __restrict__ coeff, int64_t ldc, int64_t v_begin, int64_t chunk) {
     tc::grid_dep_wait();
     tc::grid_dep_trigger();
     constexpr float kL2e = 1.4426950408889634f;
@@ -598,6 +629,10 @@ __global__ void __launch_bounds__(256) distill_from_logits_kernel(
     const int64_t r = rows[i];
     const int64_t c0 = ((int64_t)(blockIdx.x % per_row) * 256 + threadIdx.x) * 8;
     if (c0 >= chunk) return;
+    if (v_begin + c0 == 0) {
+        const float mark = first_other[r * ld];
+        geff[r] = mark == INFINITY ? nan_f() : mark == -INFINITY ? 0.f : -dloss[r] * inv_t;
+    }
     const float lsb = lse[r] * kL2e - 14.f;
     const float k2 = cap > 0.f ? 2.f * kL2e / cap * unbias : 0.f;
     const float l2e = kL2e * inv_t * (cap > 0.f ? 1.f : unbias);
@@ -621,7 +656,8 @@ __global__ void __launch_bounds__(256) distill_from_logits_kernel(
             zc = cap * th;
             sech2 = fmaf(-th, th, 1.f);
         }
-        o[k] = x[k] == -INFINITY ? 0.f : tc::ex2_approx(fmaf(zc, l2e, -lsb)) * sech2;
+        o[k] = tc::ex2_approx(fmaf(zc, l2e, -lsb)) * sech2;
+        if (fabsf(x[k]) >= kMarked) o[k] = x[k] == -INFINITY ? 0.f : x[k] * (16384.f / kMark);
     }
     store8(coeff + (int64_t)i * ldc + c0, o);
 }
@@ -681,14 +717,14 @@ cudaError_t launch_distill_prep(const uint32_t* wq, SbView sb, int64_t V, int H,
 cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, int H, int bits,
                                     float cap, const __nv_bfloat16* h, const int* pos, int64_t M,
                                     const int32_t* ids, const void* tl, int t_type, int K,
-                                    float inv_t, float unbias, float* kept, int64_t ld,
+                                    float inv_t, float unbias, float* kept, int64_t ld, float* zout,
                                     const Partial* part, int S, const int* S_dev, const int* err,
                                     float* loss, float* lse, cudaStream_t st) {
     return with_type(t_type, [&](auto* tag) {
         using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
         auto* fn = bits == 4 ? distill_finalize_kernel<4, T> : distill_finalize_kernel<8, T>;
         return launch_after(fn, dim3((unsigned)M), dim3(kThreads), st, wq, sb, V, H, cap, h, pos, ids,
-                            static_cast<const T*>(tl), K, inv_t, unbias, kept, ld, part, S, S_dev, err, loss,
+                            static_cast<const T*>(tl), K, inv_t, unbias, kept, ld, zout, part, S, S_dev, err, loss,
                             lse);
     });
 }
@@ -712,14 +748,14 @@ cudaError_t launch_distill_split(const float* z, int64_t ld, int64_t V, float ca
                         cap, inv_t, pos, part, kFewSplits);
 }
 
-cudaError_t launch_distill_from_logits(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
-                                       float unbias, const int* rows, const int* count, int64_t M,
-                                       const float* lse, __half* coeff, int64_t ldc, int64_t v_begin,
+cudaError_t launch_distill_from_logits(const float* kept, int64_t K, int64_t ld, int64_t V, float cap,
+                                       float inv_t, float unbias, const int* rows, const int* count, int64_t M,
+                                       const float* lse, const float* dloss, float* geff, __half* coeff, int64_t ldc, int64_t v_begin,
                                        int64_t chunk, cudaStream_t st) {
     // (within 2^31 blocks: M V is at most 2^30 here, or M at most kFewM)
     const dim3 grid((unsigned)((chunk / 8 + 255) / 256 * M));
-    return launch_after(distill_from_logits_kernel, grid, dim3(256), st, z, ld, V, cap, inv_t, unbias, rows,
-                        count, lse, coeff, ldc, v_begin, chunk);
+    return launch_after(distill_from_logits_kernel, grid, dim3(256), st, kept + kept_logits_at(K), kept + K, ld, V,
+                        cap, inv_t, unbias, rows, count, lse, dloss, geff, coeff, ldc, v_begin, chunk);
 }
 
 cudaError_t launch_distill_dh(const float* dhp, int S, int64_t Mpad, int H, const int* pos,

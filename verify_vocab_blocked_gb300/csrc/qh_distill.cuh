@@ -45,7 +45,7 @@ cudaError_t launch_distill_prep(const uint32_t* wq, SbView sb, int64_t V, int H,
 cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, int H, int bits,
                                     float cap, const __nv_bfloat16* h, const int* pos, int64_t M,
                                     const int32_t* ids, const void* tl, int t_type, int K,
-                                    float inv_t, float unbias, float* kept, int64_t ld,
+                                    float inv_t, float unbias, float* kept, int64_t ld, float* zout,
                                     const Partial* part, int S, const int* S_dev, const int* err,
                                     float* loss, float* lse, cudaStream_t st);
 cudaError_t launch_distill_coeff(int64_t V, float cap, const int* pos, int64_t M,
@@ -55,10 +55,10 @@ cudaError_t launch_distill_coeff(int64_t V, float cap, const int* pos, int64_t M
                                  int64_t v_begin, int64_t chunk, cudaStream_t st);
 cudaError_t launch_distill_split(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
                                  const int* pos, int64_t M, Partial* part, cudaStream_t st);
-cudaError_t launch_distill_from_logits(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
-                                       float unbias, const int* rows, const int* count, int64_t M,
-                                       const float* lse, __half* coeff, int64_t ldc, int64_t v_begin,
-                                       int64_t chunk, cudaStream_t st);
+cudaError_t launch_distill_from_logits(const float* kept, int64_t K, int64_t ld, int64_t V, float cap,
+                                       float inv_t, float unbias, const int* rows, const int* count, int64_t M,
+                                       const float* lse, const float* dloss, float* geff, __half* coeff,
+                                       int64_t ldc, int64_t v_begin, int64_t chunk, cudaStream_t st);
 cudaError_t launch_distill_dh(const float* dhp, int S, int64_t Mpad, int H, const int* pos,
                               int64_t M, const int* err, void* dh, cudaStream_t st);
 

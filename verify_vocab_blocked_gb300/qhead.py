@@ -167,16 +167,17 @@ class Head:
         return int(self.wq.shape[1]) * 32 // self.bits
 
     def c(self) -> CHead:
-        wq, scales, biases = self.wq, self.scales, self.biases
+        wq, scales, biases, bits = self.wq, self.scales, self.biases, self.bits
         if not (wq.is_contiguous() and scales.is_contiguous() and biases.is_contiguous()):
             raise ValueError("head tensors must be contiguous")
-        code = _SB_CODE.get(scales.dtype)
-        if code is None or biases.dtype != scales.dtype:
+        dtype = scales.dtype
+        code = _SB_CODE.get(dtype)
+        if code is None or biases.dtype != dtype:
             raise ValueError("scales and biases must share one type: float16, bfloat16 or "
                              "float32")
         V, words = wq.shape
         return CHead(wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), V,
-                     words * 32 // self.bits, self.bits, self.group, code, self.softcap)
+                     words * 32 // bits, bits, self.group, code, self.softcap)
 
     @staticmethod
     def from_numpy(wq, scales, biases, bits, group=64, softcap=0.0, device="cuda",
@@ -217,11 +218,13 @@ def _check_h(head: Head, h: torch.Tensor, what: str = "[M, H]") -> int:
     if not isinstance(h, torch.Tensor) or h.dtype != torch.bfloat16 or h.dim() != 2 \
             or not h.is_contiguous():
         raise ValueError(f"h must be a contiguous bf16 {what} tensor")
-    if h.shape[1] != head.H:
-        raise ValueError(f"h has {h.shape[1]} columns but the head's hidden size H is {head.H}")
-    if head.wq.device != h.device:
-        raise ValueError(f"h is on {h.device} but the head is on {head.wq.device}")
-    return int(h.shape[0])
+    M, H = h.shape
+    wq = head.wq
+    if H != wq.shape[1] * 32 // head.bits:
+        raise ValueError(f"h has {H} columns but the head's hidden size H is {head.H}")
+    if wq.device != h.device:
+        raise ValueError(f"h is on {h.device} but the head is on {wq.device}")
+    return M
 
 
 def _check_vec(name: str, t: torch.Tensor | None, n: int, dtypes, dev, required: bool = True):
@@ -622,16 +625,27 @@ def _check_teacher(ids: torch.Tensor, tlogits: torch.Tensor, M: int, dev) -> int
             or not ids.is_contiguous() or ids.shape[0] != M or ids.device != dev:
         raise ValueError(f"ids must be a contiguous int32 [{M}, K] tensor on {dev}")
     _check_matrix("tlogits", tlogits, dev)
-    if tlogits.shape != ids.shape:
-        raise ValueError(f"tlogits must have ids' shape {list(ids.shape)}, got "
-                         f"{list(tlogits.shape)}")
-    return int(ids.shape[1])
+    shape = ids.shape
+    if tlogits.shape != shape:
+        raise ValueError(f"tlogits must have ids' shape {list(shape)}, got {list(tlogits.shape)}")
+    return shape[1]
 
 
-def _kept_columns(c: CHead, M: int, K: int) -> int:
-    n = lib().qhead_distill_kept(ctypes.byref(c), M, K)
-    if n < 0:
-        raise QheadError(QHEAD_EINVAL, last_error())
+_distill_sizes: dict = {}  # (query, device, head's shape, M, K) -> its answer
+
+
+def _distill_size(query: str, c: CHead, M: int, K: int, dev) -> int:
+    """A size that the library gives for a shape, asked for once (the queries are a
+    tenth of a small step's time)."""
+    key = (query, dev, c.V, c.H, c.bits, c.group, c.sb_dtype, M, K)
+    n = _distill_sizes.get(key)
+    if n is None:
+        n = getattr(lib(), query)(ctypes.byref(c), M, K)
+        if n in (-1, ctypes.c_size_t(-1).value):
+            raise QheadError(QHEAD_EINVAL, last_error())
+        if len(_distill_sizes) >= 1024:
+            _distill_sizes.clear()
+        _distill_sizes[key] = n
     return n
 
 
@@ -650,9 +664,9 @@ def distill_fwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     loss = torch.empty(M, dtype=torch.float32, device=dev)
     lse = torch.empty(M, dtype=torch.float32, device=dev)
     c = head.c()
-    kept = torch.empty(M, _kept_columns(c, M, K), dtype=torch.float32, device=dev)
+    kept = torch.empty(M, _distill_size("qhead_distill_kept", c, M, K, dev), dtype=torch.float32, device=dev)
     if workspace is None:
-        n = _size(lib().qhead_distill_fwd_workspace(ctypes.byref(c), M, K))
+        n = _distill_size("qhead_distill_fwd_workspace", c, M, K, dev)
         workspace = _scratch(n, dev, stream)
     _check(lib().qhead_distill_fwd(ctypes.byref(c), h.data_ptr(), M, ids.data_ptr(),
                                    tlogits.data_ptr(), _SB_CODE[tlogits.dtype], K, temperature,
@@ -674,12 +688,12 @@ def distill_bwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     lse, dloss = _f32("lse", lse, M, dev), _f32("dloss", dloss, M, dev)
     _check_matrix("kept", kept, dev)
     c = head.c()
-    cols = _kept_columns(c, M, K)
-    if kept.dtype != torch.float32 or tuple(kept.shape) != (M, cols):
+    cols = _distill_size("qhead_distill_kept", c, M, K, dev)
+    if kept.dtype != torch.float32 or kept.shape != (M, cols):
         raise ValueError(f"kept must be a float32 [{M}, {cols}] tensor")
-    dh = torch.empty(M, head.H, dtype=torch.bfloat16, device=dev)
+    dh = torch.empty_like(h)
     if workspace is None:
-        n = _size(lib().qhead_distill_bwd_workspace(ctypes.byref(c), M, K))
+        n = _distill_size("qhead_distill_bwd_workspace", c, M, K, dev)
         workspace = _scratch(n, dev, stream)
     _check(lib().qhead_distill_bwd(ctypes.byref(c), h.data_ptr(), M, ids.data_ptr(),
                                    tlogits.data_ptr(), _SB_CODE[tlogits.dtype], K, temperature,
