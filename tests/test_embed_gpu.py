@@ -201,3 +201,19 @@ def test_other_stream_and_graph():
     torch.cuda.synchronize()
     assert torch.equal(y2, y0.flip(0))
     assert torch.equal(g2, qhead.embed_bwd(head, t, dy, 3.0))
+
+
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("M,V,H,kind,dtype,masked", [
+    (2, 7, 128, "same", torch.bfloat16, False),
+    (127, 40, 256, "skewed", torch.float32, True),
+    (96, 100, 2560, "same", torch.bfloat16, False),
+    (97, 100, 2560, "skewed", torch.bfloat16, True),
+    (32, 128, 8192, "same", torch.bfloat16, False),
+    (33, 128, 8192, "skewed", torch.float32, False),
+    (128, 3000, 384, "uniform", torch.float16, True),
+    (129, 128, 640, "same", torch.float32, True),
+])
+def test_gradient_few_rows(M, V, H, kind, dtype, masked, add):
+    """Up to 128 rows (fewer when wide) one launch sums them, above them sorted rows."""
+    _check_grad(M, V, H, kind, dtype, add, masked)
