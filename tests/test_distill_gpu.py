@@ -337,3 +337,27 @@ def test_logits_too_large_to_keep():
     # half a step of bf16 twice
     assert (lse[:n] - lse2).abs().max() <= 1e-4 and (loss[:n] - loss2).abs().max() <= 1e-4
     assert ((dh[:n].double() - dh2.double()).norm() / dh2.double().norm()).item() <= 2 ** -7
+
+
+@pytest.mark.parametrize("M,V,H,bits,on", [
+    (9, 260, 2560, 4, 1.0), (16, 511, 2560, 8, 0.4), (12, 700, 3584, 4, 1.0), (13, 600, 4096, 8, 0.8),
+    (16, 257, 8192, 4, 1.0), (11, 1, 128, 4, 1.0), (10, 100, 8192, 8, 0.5),
+])
+def test_two_groups_of_rows(M, V, H, bits, on):
+    """9 to 16 rows: one pass over the table for both groups of 8 while their h fits
+    shared memory, one for each where it does not."""
+    head, W, h, ids, t = _case(M, V, H, bits, min(V, 9), 30.0, 90 + M)
+    mask = torch.rand(M, device="cuda", generator=gen(91)) < on
+    _check(head, W, h, ids, t, 1.0, mask if on < 1 else None)
+
+
+def test_nan_row_of_the_second_group():
+    head, W, h, ids, t = _case(12, 900, 256, 4, 6, 30.0, 80)
+    good, lse0, _ = qhead.distill_fwd(head, h, ids, t)
+    h[10, 3] = float("nan")
+    loss, lse, kept = qhead.distill_fwd(head, h, ids, t)
+    dh = qhead.distill_bwd(head, h, ids, t, kept, lse, torch.ones(12, device="cuda"))
+    rest = torch.arange(12, device="cuda") != 10
+    assert torch.isnan(loss[10]) and torch.isnan(dh[10]).all()
+    assert torch.equal(loss[rest], good[rest]) and torch.equal(lse[rest], lse0[rest])
+    assert torch.isfinite(dh[rest]).all()

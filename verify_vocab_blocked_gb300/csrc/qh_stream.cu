@@ -159,14 +159,15 @@ struct StageOffsets {
 // tot += scale * acc.  P: the stage's packed tile; sa2 / sb2: the stage's
 // fp16 scales of rows ra / rb; ncs: negc of the stage's first group at tokens
 // 2t, 2t+1; hst: this thread's h fragment base for the stage.
+// NT groups of 8 rows, their h htile halves apart.
 // PLAIN: the magic offsets are subtracted from the codes (one HSUB2 per pair)
 // instead of cancelling in the accumulator.  There they stand against
 // 1024 sum h, whose ulp the tensor core truncates by: with sum h = -650 over
 // 2560 columns every logit of a row comes out 6e-5 low (1e-6 without).
-template <int BITS, int UNROLL4, bool PLAIN>
-__device__ __forceinline__ void stage_math(float (&tot)[4], const unsigned char* P,
+template <int BITS, int UNROLL4, bool PLAIN, int NT>
+__device__ __forceinline__ void stage_math(float (&tot)[NT][4], const unsigned char* P,
                                            const StageOffsets<BITS>& off, uint2 sa2, uint2 sb2,
-                                           const float* ncs, const __half* hst) {
+                                           const float* ncs, const __half* hst, int htile) {
     if constexpr (BITS == 4) {
         const float2 sa01 = __half22float2(u32_as_h2(sa2.x)), sa23 = __half22float2(u32_as_h2(sa2.y));
         const float2 sb01 = __half22float2(u32_as_h2(sb2.x)), sb23 = __half22float2(u32_as_h2(sb2.y));
@@ -179,26 +180,39 @@ __device__ __forceinline__ void stage_math(float (&tot)[4], const unsigned char*
             const uint2 wb = *reinterpret_cast<const uint2*>(P + ob);
             float2 nc = make_float2(0.f, 0.f);
             if constexpr (!PLAIN) nc = *reinterpret_cast<const float2*>(ncs + gm * kTokGroup);
-            const uint4 q0 = *reinterpret_cast<const uint4*>(hst + 64 * gm);
-            const uint4 q1 = *reinterpret_cast<const uint4*>(hst + 64 * gm + 8);
+            uint4 q0[NT], q1[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                q0[n] = *reinterpret_cast<const uint4*>(hst + n * htile + 64 * gm);
+                q1[n] = *reinterpret_cast<const uint4*>(hst + n * htile + 64 * gm + 8);
+            }
             uint32_t pa[4], pb[4];
-            float acc[4];
+            float acc[NT][4];
             codes4(wa.x, pa);
             codes4(wb.x, pb);
             if constexpr (PLAIN) { plain4(pa); plain4(pb); }
-            mma16816_init(acc, pa[0], pb[0], pa[1], pb[1], q0.x, q0.y, nc.x, nc.y, nc.x, nc.y);
-            mma16816(acc, pa[2], pb[2], pa[3], pb[3], q0.z, q0.w);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma16816_init(acc[n], pa[0], pb[0], pa[1], pb[1], q0[n].x, q0[n].y, nc.x, nc.y, nc.x, nc.y);
+                mma16816(acc[n], pa[2], pb[2], pa[3], pb[3], q0[n].z, q0[n].w);
+            }
             codes4(wa.y, pa);
             codes4(wb.y, pb);
             if constexpr (PLAIN) { plain4(pa); plain4(pb); }
-            mma16816(acc, pa[0], pb[0], pa[1], pb[1], q1.x, q1.y);
-            mma16816(acc, pa[2], pb[2], pa[3], pb[3], q1.z, q1.w);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma16816(acc[n], pa[0], pb[0], pa[1], pb[1], q1[n].x, q1[n].y);
+                mma16816(acc[n], pa[2], pb[2], pa[3], pb[3], q1[n].z, q1[n].w);
+            }
             const float s_a = gm == 0 ? sa01.x : gm == 1 ? sa01.y : gm == 2 ? sa23.x : sa23.y;
             const float s_b = gm == 0 ? sb01.x : gm == 1 ? sb01.y : gm == 2 ? sb23.x : sb23.y;
-            tot[0] = fmaf(s_a, acc[0], tot[0]);
-            tot[1] = fmaf(s_a, acc[1], tot[1]);
-            tot[2] = fmaf(s_b, acc[2], tot[2]);
-            tot[3] = fmaf(s_b, acc[3], tot[3]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                tot[n][0] = fmaf(s_a, acc[n][0], tot[n][0]);
+                tot[n][1] = fmaf(s_a, acc[n][1], tot[n][1]);
+                tot[n][2] = fmaf(s_b, acc[n][2], tot[n][2]);
+                tot[n][3] = fmaf(s_b, acc[n][3], tot[n][3]);
+            }
         }
     } else {
         const float2 sa01 = __half22float2(u32_as_h2(sa2.x));
@@ -209,22 +223,43 @@ __device__ __forceinline__ void stage_math(float (&tot)[4], const unsigned char*
             const uint4 wb = *reinterpret_cast<const uint4*>(P + (gm ? off.b[1] : off.b[0]));
             float2 nc = make_float2(0.f, 0.f);
             if constexpr (!PLAIN) nc = *reinterpret_cast<const float2*>(ncs + gm * kTokGroup);
-            const uint4 q0 = *reinterpret_cast<const uint4*>(hst + 64 * gm);
-            const uint4 q1 = *reinterpret_cast<const uint4*>(hst + 64 * gm + 8);
-            float acc[4];
-            mma16816_init(acc, codes8<PLAIN>(wa.x, 0x5140u), codes8<PLAIN>(wb.x, 0x5140u), codes8<PLAIN>(wa.x, 0x7362u),
-                          codes8<PLAIN>(wb.x, 0x7362u), q0.x, q0.y, nc.x, nc.y, nc.x, nc.y);
-            mma16816(acc, codes8<PLAIN>(wa.y, 0x5140u), codes8<PLAIN>(wb.y, 0x5140u), codes8<PLAIN>(wa.y, 0x7362u),
-                     codes8<PLAIN>(wb.y, 0x7362u), q0.z, q0.w);
-            mma16816(acc, codes8<PLAIN>(wa.z, 0x5140u), codes8<PLAIN>(wb.z, 0x5140u), codes8<PLAIN>(wa.z, 0x7362u),
-                     codes8<PLAIN>(wb.z, 0x7362u), q1.x, q1.y);
-            mma16816(acc, codes8<PLAIN>(wa.w, 0x5140u), codes8<PLAIN>(wb.w, 0x5140u), codes8<PLAIN>(wa.w, 0x7362u),
-                     codes8<PLAIN>(wb.w, 0x7362u), q1.z, q1.w);
+            uint4 q0[NT], q1[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                q0[n] = *reinterpret_cast<const uint4*>(hst + n * htile + 64 * gm);
+                q1[n] = *reinterpret_cast<const uint4*>(hst + n * htile + 64 * gm + 8);
+            }
+            float acc[NT][4];
+            // (the A operand of one 32-bit word of each row)
+            auto step = [&](uint32_t xa, uint32_t xb, auto&& mul) {
+                mul(codes8<PLAIN>(xa, 0x5140u), codes8<PLAIN>(xb, 0x5140u), codes8<PLAIN>(xa, 0x7362u),
+                    codes8<PLAIN>(xb, 0x7362u));
+            };
+            step(wa.x, wb.x, [&](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma16816_init(acc[n], a0, a1, a2, a3, q0[n].x, q0[n].y, nc.x, nc.y, nc.x, nc.y);
+            });
+            step(wa.y, wb.y, [&](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(acc[n], a0, a1, a2, a3, q0[n].z, q0[n].w);
+            });
+            step(wa.z, wb.z, [&](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(acc[n], a0, a1, a2, a3, q1[n].x, q1[n].y);
+            });
+            step(wa.w, wb.w, [&](uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(acc[n], a0, a1, a2, a3, q1[n].z, q1[n].w);
+            });
             const float s_a = gm ? sa01.y : sa01.x, s_b = gm ? sb01.y : sb01.x;
-            tot[0] = fmaf(s_a, acc[0], tot[0]);
-            tot[1] = fmaf(s_a, acc[1], tot[1]);
-            tot[2] = fmaf(s_b, acc[2], tot[2]);
-            tot[3] = fmaf(s_b, acc[3], tot[3]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                tot[n][0] = fmaf(s_a, acc[n][0], tot[n][0]);
+                tot[n][1] = fmaf(s_a, acc[n][1], tot[n][1]);
+                tot[n][2] = fmaf(s_b, acc[n][2], tot[n][2]);
+                tot[n][3] = fmaf(s_b, acc[n][3], tot[n][3]);
+            }
         }
     }
 }
@@ -236,7 +271,7 @@ __device__ __forceinline__ void stage_math(float (&tot)[4], const unsigned char*
 // per SM: the stage count is the largest that fits (more bytes in flight).
 struct StreamSmem {
     int stages, sslots, Hp, Gs, gp, off_s, off_h, off_negc, off_hs, off_bar, total;
-    __host__ __device__ StreamSmem(int H, int bits, int n_stages, bool tma_scales) {
+    __host__ __device__ StreamSmem(int H, int bits, int n_stages, bool tma_scales, int tokens = kTokGroup) {
         const int per_stage = kStageWords * 32 / bits;      // hidden elements per stage
         Hp = (H + per_stage - 1) / per_stage * per_stage;
         Gs = Hp / 64;
@@ -245,17 +280,17 @@ struct StreamSmem {
         sslots = tma_scales ? (bits == 4 ? ScaleRing<4>::kSlots : ScaleRing<8>::kSlots) : 0;
         off_s = stages * kPBytes;
         off_h = off_s + (tma_scales ? sslots * kSSlotBytes : stages * kSBytes);
-        off_negc = off_h + (kTokGroup * (Hp + 8) * 2 + 15) / 16 * 16;
-        off_hs = off_negc + Gs * kTokGroup * 4;
-        off_bar = (off_hs + 2 * kTokGroup * gp * 2 + 7) / 8 * 8;
+        off_negc = off_h + (tokens * (Hp + 8) * 2 + 15) / 16 * 16;
+        off_hs = off_negc + Gs * tokens * 4;
+        off_bar = (off_hs + 2 * tokens * gp * 2 + 7) / 8 * 8;
         total = off_bar + 8 * 2 * (stages + sslots) + 16 + 1024;  // + alignment slack of the base
     }
 };
 
 // The deepest ring that fits next to the staged h rows (0 if not even two).
-int stream_stages(int H, int bits) {
+int stream_stages(int H, int bits, int tokens = kTokGroup) {
     for (int s = kMaxStages; s >= 2; --s)
-        if (StreamSmem(H, bits, s, false).total <= kSmemLimit) return s;
+        if (StreamSmem(H, bits, s, false, tokens).total <= kSmemLimit) return s;
     return 0;
 }
 
@@ -292,7 +327,11 @@ __device__ __forceinline__ void push_fast(RowState& st, float z, float raw, int 
 // plain codes (see stage_math), and no softmax state is kept (the distillation
 // of few rows, whose softmax leaves tokens out and whose backward reads the
 // logits).
-template <int BITS, int NST, bool ZOUT>
+// NT = 2 (with ZOUT): a CTA holds two groups of 8 rows and unpacks the codes once
+// for both, 13 rows of 262144 x 2560 at 4 bits in 111 us for 121, at 8 bits 131072 x
+// 1536 with 16 rows 53 for 65.  mma.sync bounds it: it takes both groups' products at
+// 16 to 20 cycles each (73 us there), where one group's hide behind the bytes.
+template <int BITS, int NST, bool ZOUT, int NT>
 __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
     const __grid_constant__ CUtensorMap tmap_w, const __grid_constant__ CUtensorMap tmap_s,
     const __half* __restrict__ scales,
@@ -302,6 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
     Partial* __restrict__ part, int S, int* __restrict__ err, int stall, int n_stages,
     float* __restrict__ zout, int64_t zout_ld) {
     using Shape = StreamShape<BITS>;
+    constexpr int kTok = NT * kTokGroup;  // rows of the CTA
+    static_assert(ZOUT || NT == 1, "the softmax states are of one group");
     // Launched as a programmatic dependent: nothing in global memory is
     // touched before the preceding grid on the stream has completed; the
     // finalize that follows may then start its CTAs (they wait for this grid).
@@ -332,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
             *err = 0;
         }
     }
-    const int tok0 = blockIdx.x * kTokGroup;
+    const int tok0 = blockIdx.x * kTok;
     if (tok0 >= n_active) return;
     const int split = blockIdx.y;
 
@@ -343,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
     constexpr bool kTmaScales = NST > 0;
     constexpr int kSPer = ScaleRing<BITS>::kPer;
     constexpr int kSSlots = kTmaScales ? ScaleRing<BITS>::kSlots : 0;
-    const StreamSmem L(H, BITS, NST > 0 ? NST : n_stages, kTmaScales);
+    const StreamSmem L(H, BITS, NST > 0 ? NST : n_stages, kTmaScales, kTok);
     const int kStages = L.stages;
     unsigned char* pring = smem;
     unsigned char* sring = smem + L.off_s;
@@ -351,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
     const int hstride = L.Hp + 8;  // halves; +16 bytes per row spreads the banks
     float* negc_s = reinterpret_cast<float*>(smem + L.off_negc);
     __half* hs_hi = reinterpret_cast<__half*>(smem + L.off_hs);
-    __half* hs_lo = hs_hi + kTokGroup * L.gp;
+    __half* hs_lo = hs_hi + kTok * L.gp;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.off_bar);
     uint64_t* empty = full + kStages;
     uint64_t* sfull = empty + kStages;  // TMA-staged scales: box landed
@@ -449,8 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
         // Stage the group's 8 rows of h as fp16 (8-element blocks in the order
         // (0,4,1,5,2,6,3,7) for 4-bit heads, matching the pairs codes4 yields;
         // zeros past the active rows and in [H, Hp)), consumers only.
-        __shared__ int orig_s[kTokGroup];
-        if (ct < kTokGroup) {
+        __shared__ int orig_s[kTok];
+        if (ct < kTok) {
             int row = -1, k = tok0 + ct;  // compact index -> original row
             if (k < n_active) {
                 for (int r = 0; r < M; ++r) {
@@ -462,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
         }
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
         const int units = L.Hp / 8;
-        for (int idx = ct; idx < kTokGroup * units; idx += 32 * kConsumers) {
+        for (int idx = ct; idx < kTok * units; idx += 32 * kConsumers) {
             const int r = idx / units, cc = idx - r * units;
             const int row = orig_s[r];
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -484,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
         // lanes per (row, group), one 8-element block each, compensated sums
         // combined exactly across the lanes.
         {
-            const int npair = kTokGroup * L.gp;
+            const int npair = kTok * L.gp;
             const int ntask = npair * 8;
             for (int task0 = 0; task0 < ntask; task0 += 32 * kConsumers) {  // uniform trip count
                 const int task = task0 + ct;
@@ -519,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
                 }
                 if (task < ntask && sub == 0) {
                     const float me = 1024.f, mo = BITS == 4 ? 64.f : 1024.f;
-                    if (gg < L.Gs) negc_s[gg * kTokGroup + r] = -((me * es + mo * os) + (me * ec + mo * oc));
+                    if (gg < L.Gs) negc_s[gg * kTok + r] = -((me * es + mo * os) + (me * ec + mo * oc));
                     const float hsv = gg < G ? (es + os) + (ec + oc) : 0.f;
                     const __half hi = __float2half_rn(hsv);
                     hs_hi[pr] = hi;
@@ -552,7 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
             const int64_t va = cta_v0 + (int64_t)tile * kTile + ra;
             const int64_t vb = cta_v0 + (int64_t)tile * kTile + rb;
             // tot: (row ra, tok 2t), (row ra, tok 2t+1), (row rb, tok 2t), (row rb, tok 2t+1)
-            float tot[4] = {0.f, 0.f, 0.f, 0.f};
+            float tot[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) tot[n][0] = tot[n][1] = tot[n][2] = tot[n][3] = 0.f;
             uint32_t bA[4] = {0u, 0u, 0u, 0u};  // biases of the pending k-block (A fragment)
             // sum_g b[v, g] hsum[tok, g] for k-block kb: fp16 biases x (hi + lo) sums.
             auto load_bias = [&](int kb) {
@@ -564,13 +607,16 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
                 bA[3] = ob && k0 + 8 < G ? *reinterpret_cast<const uint32_t*>(biases + vb * G + k0 + 8) : 0u;
             };
             auto bias_mma = [&](int kb) {
-                const int k0 = g * L.gp + 16 * kb + 2 * t;
-                mma16816(tot, bA[0], bA[1], bA[2], bA[3],
-                         *reinterpret_cast<const uint32_t*>(hs_hi + k0),
-                         *reinterpret_cast<const uint32_t*>(hs_hi + k0 + 8));
-                mma16816(tot, bA[0], bA[1], bA[2], bA[3],
-                         *reinterpret_cast<const uint32_t*>(hs_lo + k0),
-                         *reinterpret_cast<const uint32_t*>(hs_lo + k0 + 8));
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int k0 = (g + n * kTokGroup) * L.gp + 16 * kb + 2 * t;
+                    mma16816(tot[n], bA[0], bA[1], bA[2], bA[3],
+                             *reinterpret_cast<const uint32_t*>(hs_hi + k0),
+                             *reinterpret_cast<const uint32_t*>(hs_hi + k0 + 8));
+                    mma16816(tot[n], bA[0], bA[1], bA[2], bA[3],
+                             *reinterpret_cast<const uint32_t*>(hs_lo + k0),
+                             *reinterpret_cast<const uint32_t*>(hs_lo + k0 + 8));
+                }
             };
             auto bias_step = [&](int c) {
                 if ((c & (kPer - 1)) == 0) load_bias(c / kPer);
@@ -598,9 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
                             sa = make_uint2(*reinterpret_cast<const uint32_t*>(Sb + 16 * ra), 0u);
                             sb = make_uint2(*reinterpret_cast<const uint32_t*>(Sb + 16 * rb), 0u);
                         }
-                        stage_math<BITS, 4, ZOUT>(tot, pring + s * kPBytes, off, sa, sb,
-                                         negc_s + kNG * c * kTokGroup + 2 * t,
-                                         hbase + kStageWords * c * (32 / BITS));
+                        stage_math<BITS, 4, ZOUT, NT>(tot, pring + s * kPBytes, off, sa, sb,
+                                         negc_s + kNG * c * kTok + 2 * t,
+                                         hbase + kStageWords * c * (32 / BITS), kTokGroup * hstride);
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(&empty[s]);
                         if (cq == kSPer - 1 || c == nst - 1) {
@@ -616,11 +662,11 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
                     // Result ignored: the warp stays converged (see the abort policy).
                     tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull);
                     const unsigned char* Sst = sring + stage * kSBytes;
-                    stage_math<BITS, 2, ZOUT>(tot, pring + stage * kPBytes, off,
+                    stage_math<BITS, NT == 2 ? 4 : 2, ZOUT, NT>(tot, pring + stage * kPBytes, off,
                                      *reinterpret_cast<const uint2*>(Sst + 8 * ra),
                                      *reinterpret_cast<const uint2*>(Sst + 8 * rb),
-                                     negc_s + kNG * c * kTokGroup + 2 * t,
-                                     hbase + kStageWords * c * (32 / BITS));
+                                     negc_s + kNG * c * kTok + 2 * t,
+                                     hbase + kStageWords * c * (32 / BITS), kTokGroup * hstride);
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&empty[stage]);
                     if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -630,24 +676,26 @@ __global__ void __launch_bounds__(kThreads, 1) stream_fwd_kernel(
             if (kPer * (nkb - 1) + kPer / 2 >= nst) bias_mma(nkb - 1);
             if constexpr (ZOUT) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = orig_s[2 * t + e];
-                    if (row < 0) continue;
-                    float* zr = zout + (int64_t)row * zout_ld;
-                    if (va < cta_v1) zr[va] = tot[e];
-                    if (vb < cta_v1) zr[vb] = tot[2 + e];
-                }
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = orig_s[n * kTokGroup + 2 * t + e];
+                        if (row < 0) continue;
+                        float* zr = zout + (int64_t)row * zout_ld;
+                        if (va < cta_v1) zr[va] = tot[n][e];
+                        if (vb < cta_v1) zr[vb] = tot[n][2 + e];
+                    }
                 continue;
             }
             // (computed here, not held across the tile loop: one register fewer)
             const float cap2l = cap > 0.f ? 2.f * 1.4426950408889634f / cap : 0.f;
             if (va < cta_v1) {
-                push_fast(st[0], softcap_fast(tot[0], cap2l, cap), tot[0], (int)va);
-                push_fast(st[1], softcap_fast(tot[1], cap2l, cap), tot[1], (int)va);
+                push_fast(st[0], softcap_fast(tot[0][0], cap2l, cap), tot[0][0], (int)va);
+                push_fast(st[1], softcap_fast(tot[0][1], cap2l, cap), tot[0][1], (int)va);
             }
             if (vb < cta_v1) {
-                push_fast(st[0], softcap_fast(tot[2], cap2l, cap), tot[2], (int)vb);
-                push_fast(st[1], softcap_fast(tot[3], cap2l, cap), tot[3], (int)vb);
+                push_fast(st[0], softcap_fast(tot[0][2], cap2l, cap), tot[0][2], (int)vb);
+                push_fast(st[1], softcap_fast(tot[0][3], cap2l, cap), tot[0][3], (int)vb);
             }
         }
         // Merge the 8 lanes that share t (lanes t, t+4, ..., t+28).
@@ -693,10 +741,23 @@ struct StreamVariant {
 template <bool ZOUT>
 const void* stream_fn(int bits, bool fast) {
     if (fast)
-        return bits == 4 ? reinterpret_cast<const void*>(stream_fwd_kernel<4, kFastStages, ZOUT>)
-                         : reinterpret_cast<const void*>(stream_fwd_kernel<8, kFastStages, ZOUT>);
-    return bits == 4 ? reinterpret_cast<const void*>(stream_fwd_kernel<4, 0, ZOUT>)
-                     : reinterpret_cast<const void*>(stream_fwd_kernel<8, 0, ZOUT>);
+        return bits == 4 ? reinterpret_cast<const void*>(stream_fwd_kernel<4, kFastStages, ZOUT, 1>)
+                         : reinterpret_cast<const void*>(stream_fwd_kernel<8, kFastStages, ZOUT, 1>);
+    return bits == 4 ? reinterpret_cast<const void*>(stream_fwd_kernel<4, 0, ZOUT, 1>)
+                     : reinterpret_cast<const void*>(stream_fwd_kernel<8, 0, ZOUT, 1>);
+}
+
+// The logits of two groups of rows from one pass over the packed rows, if a ring of
+// kPairStages fits beside their h (smem 0: it does not).
+constexpr int kPairStages = 3;
+StreamVariant stream_pair_variant(int bits, int H) {
+    StreamVariant v{};
+    v.n_stages = stream_stages(H, bits, 2 * kTokGroup);
+    if (v.n_stages < kPairStages) return v;
+    v.fn = bits == 4 ? reinterpret_cast<const void*>(stream_fwd_kernel<4, 0, true, 2>)
+                     : reinterpret_cast<const void*>(stream_fwd_kernel<8, 0, true, 2>);
+    v.smem = StreamSmem(H, bits, v.n_stages, false, 2 * kTokGroup).total;
+    return v;
 }
 
 StreamVariant stream_variant(int bits, int H, bool zout = false) {
@@ -749,8 +810,16 @@ cudaError_t launch_stream_fwd(const uint32_t* wq, const __half* scales, const __
     CUtensorMap tw;
     if (!tmap_packed_rows_sw128(&tw, wq, (uint64_t)H * bits / 32, (uint64_t)V, kTile))
         return cudaErrorInvalidValue;
-    const int groups = (int)((M + kTokGroup - 1) / kTokGroup);
-    const StreamVariant v = stream_variant(bits, H, zout != nullptr);
+    int groups = (int)((M + kTokGroup - 1) / kTokGroup);
+    StreamVariant v = stream_variant(bits, H, zout != nullptr);
+    if (zout != nullptr && groups == 2) {
+        const StreamVariant pair = stream_pair_variant(bits, H);
+        if (pair.smem > 0) {
+            v = pair;
+            groups = 1;
+            S *= 2;  // (no partials here: S is only the split of the vocab rows)
+        }
+    }
     if (v.n_stages < 2) return cudaErrorInvalidValue;
     CUtensorMap ts{};  // unused by the run-time-depth variant
     if (v.tma_scales &&
