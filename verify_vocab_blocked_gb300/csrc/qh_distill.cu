@@ -57,6 +57,10 @@ constexpr float kMark = 0x1p126f, kMarked = 0x1p85f;
 
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7fc00000); }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p) : "memory");
+}
+
 __device__ __forceinline__ float block_max(float v, float* red) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -334,6 +338,11 @@ __global__ void __launch_bounds__(kThreads, 4) distill_finalize_kernel(
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int k = 8 * threadIdx.x; k < K; k += 8 * kThreads) {  // (read behind the partials)
+        prefetch_l1(ids + r * K + k);
+        prefetch_l1(tl + r * K + k);
+        prefetch_l1(zr + k);
+    }
     if (S_dev) S = *S_dev;
     // Without a cap the kernel's factor `unbias` stands in its exponent: m in its terms.
     const float mscale = cap > 0.f ? 1.f : unbias;
@@ -442,23 +451,32 @@ __global__ void __launch_bounds__(kThreads, 4) distill_finalize_kernel(
         }
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        float add = 0.f;
-        for (int c = 0; c < kOthers; ++c) {
-            const bool have = c < n_other;
-            zr[K + c] = have ? other_z[c] : 0.f;
-            zr[K + kOthers + c] = __int_as_float(have ? other_i[c] + 1 : 0);
-            if (!have) continue;
-            rest -= expf((softcap_exact(other_v[c] * unbias, cap) - top) * inv_t);
-            add += expf((other_z[c] - top) * inv_t);
+    if (warp == 0) {
+        const bool have = lane < n_other;
+        float out_of = 0.f, add = 0.f;  // the kernel's terms, the exact ones
+        if (have) {
+            out_of = expf((softcap_exact(other_v[lane] * unbias, cap) - top) * inv_t);
+            add = expf((other_z[lane] - top) * inv_t);
         }
+        if (lane < kOthers) {
+            zr[K + lane] = have ? other_z[lane] : 0.f;
+            zr[K + kOthers + lane] = __int_as_float(have ? other_i[lane] + 1 : 0);
+        }
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            out_of += __shfl_xor_sync(0xffffffffu, out_of, o);
+            add += __shfl_xor_sync(0xffffffffu, add, o);
+        }
+        rest -= out_of;
         const float l = logf((rest < 0.f ? 0.f : rest) + add + sum);  // lse - top / T (NaN stays)
-        lse[r] = fmaf(top, inv_t, l);
-        float out = cross + l;
-        if (te.tmax == -INFINITY) out = 0.f;  // nothing to learn from
-        if (te.bad) out = nan_f();
-        loss[r] = out;
-        red[0] = l;
+        if (lane == 0) {
+            lse[r] = fmaf(top, inv_t, l);
+            float out = cross + l;
+            if (te.tmax == -INFINITY) out = 0.f;  // nothing to learn from
+            if (te.bad) out = nan_f();
+            loss[r] = out;
+            red[0] = l;
+        }
     }
     __syncthreads();
     if (te.bad || te.tmax == -INFINITY) {
@@ -612,23 +630,43 @@ __global__ void __launch_bounds__(kSplitThreads) distill_split_kernel(
 // The coefficient block of the chunk [v_begin, v_begin + chunk) from the kept
 // logits: q sech2 2^14 in fp16 (zeros past V) with the arithmetic of the logit
 // kernel's own coefficient epilogue, or the kept coefficient; and the row's
-// cotangent (see distill_coeff_kernel).  Bound by bytes: 4 read, 2 written per logit.  Thread = 8
-// columns of one active row; the rows past the active ones are not written
-// (nothing reads what the contraction makes of them).
-__global__ void __launch_bounds__(256) distill_from_logits_kernel(
+// cotangent (see distill_coeff_kernel).  Thread = kPieces times 8 columns of one
+// active row; the rows past the active ones are not written (nothing reads what the
+// contraction makes of them).  Bound by bytes, 4 read and 2 written per logit: 6.8
+// TB/s at 5744 x 131072 (666 us; 726 with 2 pieces, 899 with one: the loads of a
+// block that lives for three dependent rounds are in flight in one of them).
+constexpr int kPieces = 4;
+__global__ void __launch_bounds__(256, 4) distill_from_logits_kernel(
     const float* __restrict__ z, const float* __restrict__ first_other, int64_t ld, int64_t V, float cap,
     float inv_t, float unbias, const int* rows, const int* count, const float* __restrict__ lse,
-    const float* __restrict__ dloss, float* __restrict__ geff, __half* __restrict__ coeff, int64_t ldc, int64_t v_begin, int64_t chunk) {
+    const float* __restrict__ dloss, float* __restrict__ geff, __half* __restrict__ coeff, int64_t ldc,
+    int64_t v_begin, int64_t chunk) {
     tc::grid_dep_wait();
     tc::grid_dep_trigger();
     constexpr float kL2e = 1.4426950408889634f;
+    constexpr int kStep = 256 * 8;
     // blocks run along a row, row after row
-    const int per_row = (int)((chunk / 8 + 255) / 256);
+    const int per_row = (int)((chunk + kPieces * kStep - 1) / (kPieces * kStep));
     const int i = blockIdx.x / per_row;
+    const int64_t r = rows[i];  // (-1 past the active rows)
     if (i >= *count) return;
-    const int64_t r = rows[i];
-    const int64_t c0 = ((int64_t)(blockIdx.x % per_row) * 256 + threadIdx.x) * 8;
-    if (c0 >= chunk) return;
+    const int64_t c0 = (int64_t)(blockIdx.x % per_row) * kPieces * kStep + threadIdx.x * 8;
+    const float* zr = z + r * ld + v_begin;
+    float x[kPieces][8];
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+        const int64_t c = c0 + p * kStep, v = v_begin + c;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[p][k] = -INFINITY;
+        if (c >= chunk) continue;
+        if (v + 8 <= V) {
+            load8_wide(zr + c, x[p]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (v + k < V) x[p][k] = zr[c + k];
+        }
+    }
     if (v_begin + c0 == 0) {
         const float mark = first_other[r * ld];
         geff[r] = mark == INFINITY ? nan_f() : mark == -INFINITY ? 0.f : -dloss[r] * inv_t;
@@ -636,30 +674,24 @@ __global__ void __launch_bounds__(256) distill_from_logits_kernel(
     const float lsb = lse[r] * kL2e - 14.f;
     const float k2 = cap > 0.f ? 2.f * kL2e / cap * unbias : 0.f;
     const float l2e = kL2e * inv_t * (cap > 0.f ? 1.f : unbias);
-    float x[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = -INFINITY;
-    const int64_t v = v_begin + c0;
-    if (v + 8 <= V) {
-        load8_wide(z + r * ld + v, x);
-    } else {
+    for (int p = 0; p < kPieces; ++p) {
+        if (c0 + p * kStep >= chunk) break;
+        float o[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (v + k < V) x[k] = z[r * ld + v + k];
-    }
-    float o[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float zc = x[k], sech2 = 1.f;
-        if (cap > 0.f) {
-            const float th = fmaf(-2.f, tc::rcp_approx(tc::ex2_approx(x[k] * k2) + 1.f), 1.f);
-            zc = cap * th;
-            sech2 = fmaf(-th, th, 1.f);
+        for (int k = 0; k < 8; ++k) {
+            const float xv = x[p][k];
+            float zc = xv, sech2 = 1.f;
+            if (cap > 0.f) {
+                const float th = fmaf(-2.f, tc::rcp_approx(tc::ex2_approx(xv * k2) + 1.f), 1.f);
+                zc = cap * th;
+                sech2 = fmaf(-th, th, 1.f);
+            }
+            o[k] = tc::ex2_approx(fmaf(zc, l2e, -lsb)) * sech2;
+            if (fabsf(xv) >= kMarked) o[k] = xv == -INFINITY ? 0.f : xv * (16384.f / kMark);
         }
-        o[k] = tc::ex2_approx(fmaf(zc, l2e, -lsb)) * sech2;
-        if (fabsf(x[k]) >= kMarked) o[k] = x[k] == -INFINITY ? 0.f : x[k] * (16384.f / kMark);
+        store8(coeff + (int64_t)i * ldc + c0 + p * kStep, o);
     }
-    store8(coeff + (int64_t)i * ldc + c0, o);
 }
 
 // One block per row: the K slices of the contraction in order, rounded once to
@@ -753,7 +785,8 @@ cudaError_t launch_distill_from_logits(const float* kept, int64_t K, int64_t ld,
                                        const float* lse, const float* dloss, float* geff, __half* coeff, int64_t ldc, int64_t v_begin,
                                        int64_t chunk, cudaStream_t st) {
     // (within 2^31 blocks: M V is at most 2^30 here, or M at most kFewM)
-    const dim3 grid((unsigned)((chunk / 8 + 255) / 256 * M));
+    constexpr int64_t per = 256 * 8 * kPieces;
+    const dim3 grid((unsigned)((chunk + per - 1) / per * M));
     return launch_after(distill_from_logits_kernel, grid, dim3(256), st, kept + kept_logits_at(K), kept + K, ld, V,
                         cap, inv_t, unbias, rows, count, lse, dloss, geff, coeff, ldc, v_begin, chunk);
 }
