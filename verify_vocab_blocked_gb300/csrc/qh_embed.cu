@@ -120,7 +120,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 // its digits, and (after the CTAs have exchanged their totals through
 // distributed shared memory) scatters its slice in order.  Rows that are
 // masked or whose token lies outside [0, V) drop out in the first pass.
-// info[0] = live rows.  One launch, no global atomics.  Latency bounds it: a
+// info[0] = live rows, info[1] = 0.  One launch, no global atomics.  Latency bounds it: a
 // slice of up to kHeld batches of 32 keys is loaded once a pass, all batches
 // together, and stays in registers between the counting and the scatter.
 constexpr int kHeld = 8;
@@ -254,7 +254,10 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(
         // The cluster's writes are visible and its totals read before the next pass.
         tc::cluster_sync();
     }
-    if (c == 0 && tid == 0) info[0] = (int)n;
+    if (c == 0 && tid == 0) {
+        info[0] = (int)n;
+        info[1] = 0;
+    }
 }
 
 // The same order for up to kRankM rows by counting: a row's position is the number
@@ -290,7 +293,10 @@ __global__ void __launch_bounds__(kRankThreads) embed_rank_kernel(
         for (int o = 16; o >= 1; o >>= 1) live += __shfl_xor_sync(0xffffffffu, live, o);
         if ((threadIdx.x & 31) == 0) atomicAdd(&total, live);
         __syncthreads();
-        if (threadIdx.x == 0) info[0] = total;
+        if (threadIdx.x == 0) {
+            info[0] = total;
+            info[1] = 0;
+        }
     }
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -341,8 +347,8 @@ constexpr int kMaxChunk = 64;
 // Block = chunk sorted rows x all columns, thread = 8 columns.
 template <typename T>
 __global__ void __launch_bounds__(kMaxH / 8) embed_sum_kernel(
-    const uint2* sorted, const int* info, int chunk, int H, float scale,
-    const T* __restrict__ dy, float* dw, int accumulate, float* __restrict__ part) {
+    const uint2* sorted, int* info, int chunk, int H, float scale,
+    const T* __restrict__ dy, float* dw, int accumulate, float* __restrict__ part, int* __restrict__ joins) {
     tc::grid_dep_wait();
     tc::grid_dep_trigger();
     const int u = threadIdx.x;
@@ -358,6 +364,10 @@ __global__ void __launch_bounds__(kMaxH / 8) embed_sum_kernel(
         key[i] = p >= 0 && p < n ? sorted[p] : make_uint2(0xffffffffu, 0u);
     }
     __syncthreads();
+    // (a run that begins here and goes on: its last key is the next chunk's first,
+    // and it does not fill the chunk from one before)
+    if (u == 0 && key[len].x == key[len + 1].x && (key[1].x != key[len].x || key[0].x != key[1].x))
+        joins[atomicAdd(info + 1, 1)] = (int)c;
     if (u >= units) return;
     float acc[8];
 #pragma unroll
@@ -402,63 +412,64 @@ __global__ void __launch_bounds__(kMaxH / 8) embed_sum_kernel(
     }
 }
 
-// Block c: the run that begins in chunk c and goes on past it, if there is
-// one: its parts, then dW.  Groups of threads take a contiguous share of the
-// parts each and their sums are added in order (a frequent token has a part in
-// every chunk of its run: 28 us at 32768 rows with one group).
+// The listed runs (in any order: each is summed by itself) that begin in a chunk and
+// go on past it: their parts, then dW.  Groups of threads take a contiguous share of
+// the parts each and their sums are added in order (a frequent token has a part in
+// every chunk of its run: 28 us at 32768 rows with one group).  Blocks as many as
+// the SMs hold, not one a chunk, most of which would only look and return (32768
+// rows of 1536, skewed: 101 us the whole, 98 so; of one token: 123, 110).
 constexpr int kJoinGroups = 4;
 __global__ void __launch_bounds__(1024) embed_join_kernel(
     const uint2* sorted, const int* info, int chunk, int H, float scale,
-    const float* part, float* dw, int accumulate) {
+    const float* part, float* dw, int accumulate, const int* joins) {
     extern __shared__ __align__(16) float sums[];  // [groups - 1][H]
     tc::grid_dep_wait();
-    const int n = info[0];
-    const int64_t c = blockIdx.x;
-    const int64_t p0 = c * chunk, p1 = p0 + chunk;  // p1: first row of the next chunk
-    if (p1 >= n) return;
-    const uint32_t t = sorted[p1].x, last = sorted[p1 - 1].x, first = sorted[p0].x;
-    const uint32_t prev = p0 > 0 ? sorted[p0 - 1].x : 0xffffffffu;
-    if (last != t || (first == t && prev == t)) return;  // no run on, or it began earlier
-    // chunks behind c whose first row belongs to the run (a prefix of them)
-    int more = 0;
-    for (int64_t q = c + 1;; q += blockDim.x) {
-        const int64_t p = (q + threadIdx.x) * chunk;
-        const int got = __syncthreads_count(p < n && sorted[p].x == t);
-        more += got;
-        if (got < (int)blockDim.x) break;
-    }
-    const int units = H / 8, groups = blockDim.x / units;
-    const int g = threadIdx.x / units, u = threadIdx.x - g * units;
-    float acc[8];
+    const int n = info[0], n_joins = info[1];
+    for (int at = blockIdx.x; at < n_joins; at += gridDim.x) {
+        if (at != (int)blockIdx.x) __syncthreads();  // (the sums are read)
+        const int64_t c = joins[at];
+        const uint32_t t = sorted[(c + 1) * chunk].x;
+        // chunks behind c whose first row belongs to the run (a prefix of them)
+        int more = 0;
+        for (int64_t q = c + 1;; q += blockDim.x) {
+            const int64_t p = (q + threadIdx.x) * chunk;
+            const int got = __syncthreads_count(p < n && sorted[p].x == t);
+            more += got;
+            if (got < (int)blockDim.x) break;
+        }
+        const int units = H / 8, groups = blockDim.x / units;
+        const int g = threadIdx.x / units, u = threadIdx.x - g * units;
+        float acc[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    if (g < groups) {
-        // parts 0 .. more: part 0 in slot 1 of chunk c, part k in slot 0 of chunk c + k
-        const int k0 = (int)((int64_t)(more + 1) * g / groups);
-        const int k1 = (int)((int64_t)(more + 1) * (g + 1) / groups);
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        if (g < groups) {
+            // parts 0 .. more: part 0 in slot 1 of chunk c, part k in slot 0 of chunk c + k
+            const int k0 = (int)((int64_t)(more + 1) * g / groups);
+            const int k1 = (int)((int64_t)(more + 1) * (g + 1) / groups);
 #pragma unroll 4
-        for (int k = k0; k < k1; ++k) {
+            for (int k = k0; k < k1; ++k) {
+                float x[8];
+                load8_wide(part + (2 * (c + k) + (k == 0 ? 1 : 0)) * H + 8 * u, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] += x[e];
+            }
+            if (g > 0) store8(sums + (g - 1) * H + 8 * u, acc);
+        }
+        __syncthreads();
+        if (g != 0) continue;
+        for (int k = 1; k < groups; ++k) {
             float x[8];
-            load8_wide(part + (2 * (c + k) + (k == 0 ? 1 : 0)) * H + 8 * u, x);
+            load8(sums + (k - 1) * H + 8 * u, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] += x[e];
         }
-        if (g > 0) store8(sums + (g - 1) * H + 8 * u, acc);
-    }
-    __syncthreads();
-    if (g != 0) return;
-    for (int k = 1; k < groups; ++k) {
-        float x[8];
-        load8(sums + (k - 1) * H + 8 * u, x);
+        float* dst = dw + (int64_t)t * H + 8 * u;
+        float o[8];
+        if (accumulate) load8_wide(dst, o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += x[e];
+        for (int e = 0; e < 8; ++e) o[e] = accumulate ? fmaf(scale, acc[e], o[e]) : scale * acc[e];
+        store8_wide(dst, o);
     }
-    float* dst = dw + (int64_t)t * H + 8 * u;
-    float o[8];
-    if (accumulate) load8_wide(dst, o);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = accumulate ? fmaf(scale, acc[e], o[e]) : scale * acc[e];
-    store8_wide(dst, o);
 }
 
 // The gradient of few rows in one launch (behind the zeros of a fresh dW): block m,
@@ -570,17 +581,18 @@ EmbedBwdPlan plan_embed_bwd(int64_t M, int H) {
     p.off_a = off;    off = up(off + 8 * (size_t)M, 256);
     p.off_b = off;    off = up(off + 8 * (size_t)M, 256);
     p.off_part = off; off = up(off + 2 * sizeof(float) * (size_t)p.n_chunks * H, 256);
+    p.off_joins = off; off = up(off + 4 * (size_t)p.n_chunks, 256);
     p.total = off;
     return p;
 }
 
 template <typename T>
-static cudaError_t launch_sum(const EmbedBwdPlan& p, const uint2* sorted, const int* info, int H,
+static cudaError_t launch_sum(const EmbedBwdPlan& p, const uint2* sorted, int* info, int H,
                               float scale, const void* dy, float* dw, int accumulate, float* part,
-                              cudaStream_t st) {
+                              int* joins, cudaStream_t st) {
     int chunk = p.chunk;
     const T* y = static_cast<const T*>(dy);
-    void* args[] = {&sorted, &info, &chunk, &H, &scale, &y, &dw, &accumulate, &part};
+    void* args[] = {&sorted, &info, &chunk, &H, &scale, &y, &dw, &accumulate, &part, &joins};
     return launch_dependent(reinterpret_cast<const void*>(embed_sum_kernel<T>), dim3((unsigned)p.n_chunks),
                             dim3(unit_threads(H)), 0, st, args);
 }
@@ -620,6 +632,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdPlan& p, void* ws, int64_t V, int H,
     uint2* a = reinterpret_cast<uint2*>(w + p.off_a);
     uint2* b = reinterpret_cast<uint2*>(w + p.off_b);
     float* part = reinterpret_cast<float*>(w + p.off_part);
+    int* joins = reinterpret_cast<int*>(w + p.off_joins);
     cudaError_t e;
     if (M <= kFewTokens && M <= kFewPerGroup * few_groups(H)) {
         if (!accumulate && (e = launch_zero(dw, V * H / 8, false, st))) return e;
@@ -661,16 +674,17 @@ cudaError_t launch_embed_bwd(const EmbedBwdPlan& p, void* ws, int64_t V, int H,
     }
     if (!accumulate && (e = launch_zero(dw, V * H / 8, true, st))) return e;
     int acc = accumulate ? 1 : 0;
-    e = dy_type == kSbF32    ? launch_sum<float>(p, sorted, info, H, scale, dy, dw, acc, part, st)
-        : dy_type == kSbBf16 ? launch_sum<__nv_bfloat16>(p, sorted, info, H, scale, dy, dw, acc, part, st)
-                             : launch_sum<__half>(p, sorted, info, H, scale, dy, dw, acc, part, st);
+    e = dy_type == kSbF32    ? launch_sum<float>(p, sorted, info, H, scale, dy, dw, acc, part, joins, st)
+        : dy_type == kSbBf16 ? launch_sum<__nv_bfloat16>(p, sorted, info, H, scale, dy, dw, acc, part, joins, st)
+                             : launch_sum<__half>(p, sorted, info, H, scale, dy, dw, acc, part, joins, st);
     if (e || p.n_chunks < 2) return e;
     int chunk = p.chunk, groups = 1024 / (H / 8);
     groups = groups < 1 ? 1 : groups > kJoinGroups ? kJoinGroups : groups;
     const int threads = (groups * (H / 8) + 31) / 32 * 32;
-    void* args[] = {&sorted, &info, &chunk, &H, &scale, &part, &dw, &acc};
+    void* args[] = {&sorted, &info, &chunk, &H, &scale, &part, &dw, &acc, &joins};
+    const int64_t most = 2048 / threads * (int64_t)device_sms(), runs = p.n_chunks - 1;
     return launch_dependent(reinterpret_cast<const void*>(embed_join_kernel),
-                            dim3((unsigned)(p.n_chunks - 1)), dim3(threads),
+                            dim3((unsigned)(runs < most ? runs : most)), dim3(threads),
                             sizeof(float) * (size_t)(groups - 1) * H, st, args);
 }
 

@@ -162,11 +162,12 @@ cudaError_t launch_embed(const uint32_t* wq, SbView sb, int64_t V, int H, int bi
                          void* out, int out_type, cudaStream_t st);
 
 // Workspace of the gradient: two buffers of sorted (token, row) pairs, the
-// count of live rows and two partial rows per chunk of sorted rows.
+// counts of live rows and of joins, two partial rows per chunk of sorted rows and
+// the list of joins.
 struct EmbedBwdPlan {
     int chunk = 0;       // sorted rows per block
     int64_t n_chunks = 0;
-    size_t off_info = 0, off_a = 0, off_b = 0, off_part = 0, total = 0;
+    size_t off_info = 0, off_a = 0, off_b = 0, off_part = 0, off_joins = 0, total = 0;
 };
 EmbedBwdPlan plan_embed_bwd(int64_t M, int H);
 cudaError_t launch_embed_bwd(const EmbedBwdPlan& p, void* ws, int64_t V, int H,
