@@ -286,6 +286,47 @@ def alloc_workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
 
 
+# Memory of a call on a stream given to it.  The caller has ordered that stream
+# behind whatever makes the inputs (stream.wait_stream(...)) and orders what reads
+# the outputs behind it; whose memory a block is, is settled here, so that any tensor
+# of the call may be dropped as soon as the call has returned:
+#   * a workspace and the outputs come from the given stream's own pool: a block that
+#     the current stream's queued work still uses is not among them;
+#   * the outputs are recorded on the current stream, which goes on to use them;
+#   * the inputs are recorded on the given stream, which reads them after the call.
+
+def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
+    """A workspace of this call's own."""
+    if stream is None:
+        return alloc_workspace(nbytes, dev)
+    with torch.cuda.stream(stream):
+        return alloc_workspace(nbytes, dev)
+
+
+def _out(shape, dtype, dev, stream, fill: float | None = None) -> torch.Tensor:
+    """An output of the call (filled, on the call's stream, if `fill` is given)."""
+    if stream is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t if fill is None else t.fill_(fill)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        if fill is not None:
+            t.fill_(fill)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _reads(stream, head: "Head | None", *tensors) -> None:
+    """Records the call's inputs (and a buffer or workspace given to it) on its stream."""
+    if stream is None:
+        return
+    for t in (head.wq, head.scales, head.biases) if head is not None else ():
+        t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def fwd(head: Head, h: torch.Tensor, targets: torch.Tensor | None = None,
         mask: torch.Tensor | None = None, *, want_logp: bool = True, want_lse: bool = True,
         want_argmax: bool = True, workspace: torch.Tensor | None = None, stream=None):
@@ -295,11 +336,12 @@ def fwd(head: Head, h: torch.Tensor, targets: torch.Tensor | None = None,
     targets = _targets(targets, M, dev, required=False)
     mask = _mask(mask, M, dev)
     want_logp = want_logp and targets is not None
-    logp = torch.empty(M, dtype=torch.float32, device=dev) if want_logp else None
-    lse = torch.empty(M, dtype=torch.float32, device=dev) if want_lse else None
-    am = torch.empty(M, dtype=torch.int32, device=dev) if want_argmax else None
+    logp = _out(M, torch.float32, dev, stream) if want_logp else None
+    lse = _out(M, torch.float32, dev, stream) if want_lse else None
+    am = _out(M, torch.int32, dev, stream) if want_argmax else None
+    _reads(stream, head, h, targets, mask, workspace)
     if workspace is None:
-        workspace = alloc_workspace(fwd_workspace(head, M), dev)
+        workspace = _scratch(fwd_workspace(head, M), dev, stream)
     _check(lib().qhead_fwd(ctypes.byref(head.c()), h.data_ptr(), M, _ptr(targets), _ptr(mask),
                            _ptr(logp), _ptr(lse), _ptr(am), workspace.data_ptr(),
                            workspace.numel(), _stream(stream)))
@@ -315,9 +357,10 @@ def bwd(head: Head, h: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
     targets = _targets(targets, M, dev, required=True)
     mask = _mask(mask, M, dev)
     lse, dlogp = _f32("lse", lse, M, dev), _f32("dlogp", dlogp, M, dev)
-    dh = torch.empty(M, head.H, dtype=torch.float32, device=dev)
+    dh = _out((M, head.H), torch.float32, dev, stream)
+    _reads(stream, head, h, targets, lse, dlogp, mask, workspace)
     if workspace is None:
-        workspace = alloc_workspace(bwd_workspace(head, M), dev)
+        workspace = _scratch(bwd_workspace(head, M), dev, stream)
     _check(lib().qhead_bwd(ctypes.byref(head.c()), h.data_ptr(), M, _ptr(targets), _ptr(mask),
                            lse.data_ptr(), dlogp.data_ptr(), dh.data_ptr(), workspace.data_ptr(),
                            workspace.numel(), _stream(stream)))
@@ -334,10 +377,11 @@ def bwd_dw(head: Head, h: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor
     targets = _targets(targets, M, dev, required=True)
     mask = _mask(mask, M, dev)
     lse, dlogp = _f32("lse", lse, M, dev), _f32("dlogp", dlogp, M, dev)
-    dh = torch.empty(M, head.H, dtype=torch.float32, device=dev) if want_dh else None
-    dw = torch.empty(head.V, head.H, dtype=torch.float32, device=dev)
+    dh = _out((M, head.H), torch.float32, dev, stream) if want_dh else None
+    dw = _out((head.V, head.H), torch.float32, dev, stream)
+    _reads(stream, head, h, targets, lse, dlogp, mask, workspace)
     if workspace is None:
-        workspace = alloc_workspace(bwd_dw_workspace(head, M), dev)
+        workspace = _scratch(bwd_dw_workspace(head, M), dev, stream)
     _check(lib().qhead_bwd_dw(ctypes.byref(head.c()), h.data_ptr(), M, targets.data_ptr(),
                               _ptr(mask), lse.data_ptr(), dlogp.data_ptr(), _ptr(dh),
                               dw.data_ptr(), workspace.data_ptr(), workspace.numel(),
@@ -361,12 +405,13 @@ def fwd_blockmax(head: Head, h: torch.Tensor, targets: torch.Tensor | None = Non
     dev = h.device
     targets = _targets(targets, M, dev, required=False)
     mask = _mask(mask, M, dev)
-    logp = torch.empty(M, dtype=torch.float32, device=dev) if targets is not None else None
-    lse = torch.empty(M, dtype=torch.float32, device=dev)
-    am = torch.empty(M, dtype=torch.int32, device=dev)
-    bm = torch.full((M, (head.V + 255) // 256), float("-inf"), dtype=torch.float32, device=dev)
+    logp = _out(M, torch.float32, dev, stream) if targets is not None else None
+    lse = _out(M, torch.float32, dev, stream)
+    am = _out(M, torch.int32, dev, stream)
+    bm = _out((M, (head.V + 255) // 256), torch.float32, dev, stream, fill=float("-inf"))
+    _reads(stream, head, h, targets, mask, workspace)
     if workspace is None:
-        workspace = alloc_workspace(_ws_size("qhead_fwd_blockmax_workspace", head, M), dev)
+        workspace = _scratch(_ws_size("qhead_fwd_blockmax_workspace", head, M), dev, stream)
     _check(lib().qhead_fwd_blockmax(ctypes.byref(head.c()), h.data_ptr(), M, _ptr(targets),
                                     _ptr(mask), _ptr(logp), lse.data_ptr(), am.data_ptr(),
                                     bm.data_ptr(), workspace.data_ptr(), workspace.numel(),
@@ -390,9 +435,10 @@ def bwd_blockskip(head: Head, h: torch.Tensor, targets: torch.Tensor, lse: torch
             or tuple(block_max.shape) != (M, nvt) or not block_max.is_contiguous()
             or block_max.device != dev):
         raise ValueError(f"block_max must be a contiguous float32 [{M}, {nvt}] tensor on {dev}")
-    dh = torch.empty(M, head.H, dtype=torch.float32, device=dev)
+    dh = _out((M, head.H), torch.float32, dev, stream)
+    _reads(stream, head, h, targets, lse, dlogp, block_max, mask, workspace)
     if workspace is None:
-        workspace = alloc_workspace(_ws_size("qhead_bwd_blockskip_workspace", head, M), dev)
+        workspace = _scratch(_ws_size("qhead_bwd_blockskip_workspace", head, M), dev, stream)
     _check(lib().qhead_bwd_blockskip(ctypes.byref(head.c()), h.data_ptr(), M, targets.data_ptr(),
                                      _ptr(mask), lse.data_ptr(), dlogp.data_ptr(),
                                      block_max.data_ptr(), float(eps), dh.data_ptr(),
@@ -411,11 +457,11 @@ def bwd_filter(head: Head, h: torch.Tensor, targets: torch.Tensor, lse: torch.Te
     targets = _targets(targets, M, dev, required=True)
     mask = _mask(mask, M, dev)
     lse, dlogp = _f32("lse", lse, M, dev), _f32("dlogp", dlogp, M, dev)
-    dh = torch.empty(M, head.H, dtype=torch.float32, device=dev)
-    cold = (torch.empty(((M + 31) // 32, (head.V + 31) // 32), dtype=torch.uint8, device=dev)
-            if want_cold else None)
+    dh = _out((M, head.H), torch.float32, dev, stream)
+    cold = _out(((M + 31) // 32, (head.V + 31) // 32), torch.uint8, dev, stream) if want_cold else None
+    _reads(stream, head, h, targets, lse, dlogp, mask, workspace)
     if workspace is None:
-        workspace = alloc_workspace(_ws_size("qhead_bwd_filter_workspace", head, M), dev)
+        workspace = _scratch(_ws_size("qhead_bwd_filter_workspace", head, M), dev, stream)
     _check(lib().qhead_bwd_filter(ctypes.byref(head.c()), h.data_ptr(), M, targets.data_ptr(),
                                   _ptr(mask), lse.data_ptr(), dlogp.data_ptr(), float(eps),
                                   dh.data_ptr(), _ptr(cold), workspace.data_ptr(),
@@ -440,12 +486,13 @@ def verify(head: Head, h: torch.Tensor, W: int, draft: torch.Tensor | None,
     if draft is not None and draft.device != dev:
         raise ValueError(f"draft is on {draft.device}, h on {dev}")
     mask = _mask(mask, M, dev)
-    am = torch.empty(M, dtype=torch.int32, device=dev)
-    lse = torch.empty(M, dtype=torch.float32, device=dev) if want_lse else None
-    n_acc = torch.empty(B, dtype=torch.int32, device=dev)
-    nxt = torch.empty(B, dtype=torch.int32, device=dev)
+    am = _out(M, torch.int32, dev, stream)
+    lse = _out(M, torch.float32, dev, stream) if want_lse else None
+    n_acc = _out(B, torch.int32, dev, stream)
+    nxt = _out(B, torch.int32, dev, stream)
+    _reads(stream, head, h, draft, mask, workspace)
     if workspace is None:
-        workspace = alloc_workspace(fwd_workspace(head, M), dev)
+        workspace = _scratch(fwd_workspace(head, M), dev, stream)
     _check(lib().qhead_verify(ctypes.byref(head.c()), h.data_ptr(), B, W, _ptr(draft),
                               _ptr(mask), _ptr(lse), am.data_ptr(), n_acc.data_ptr(),
                               nxt.data_ptr(), workspace.data_ptr(), workspace.numel(),
@@ -490,16 +537,6 @@ def _out_code(dtype) -> int:
     return code
 
 
-def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
-    """A workspace of this call's own.  It is allocated on the current stream:
-    with another one given, that one's use of it is recorded, so that it is not
-    handed out again before the call's kernels are done."""
-    w = alloc_workspace(nbytes, dev)
-    if stream is not None:
-        w.record_stream(stream)
-    return w
-
-
 def _size(n: int) -> int:
     if n == ctypes.c_size_t(-1).value:
         raise QheadError(QHEAD_EINVAL, last_error())
@@ -516,7 +553,8 @@ def embed(head: Head, tokens: torch.Tensor, scale: float = 1.0, mask: torch.Tens
         mask = _mask(mask, M, dev)
     code = _out_code(out_dtype)
     c = head.c()
-    out = torch.empty((M, c.H), dtype=out_dtype, device=dev)
+    out = _out((M, c.H), out_dtype, dev, stream)
+    _reads(stream, head, tokens, mask)
     _check(lib().qhead_embed(ctypes.byref(c), tokens.data_ptr(), M, _ptr(mask), scale,
                              out.data_ptr(), code, _stream(stream)))
     return out
@@ -536,11 +574,12 @@ def embed_bwd(head: Head, tokens: torch.Tensor, dout: torch.Tensor, scale: float
         raise ValueError(f"dout must have shape [{M}, {head.H}], got {list(dout.shape)}")
     add = dw is not None
     if not add:
-        dw = torch.empty(head.V, head.H, dtype=torch.float32, device=dev)
+        dw = _out((head.V, head.H), torch.float32, dev, stream)
     elif (not isinstance(dw, torch.Tensor) or dw.dtype != torch.float32 or dw.device != dev
           or tuple(dw.shape) != (head.V, head.H) or not dw.is_contiguous()):
         raise ValueError(f"dw must be a contiguous float32 [{head.V}, {head.H}] tensor on {dev}")
     c = head.c()
+    _reads(stream, None, tokens, dout, mask, dw if add else None, workspace)
     if workspace is None:
         workspace = _scratch(_size(lib().qhead_embed_bwd_workspace(ctypes.byref(c), M)), dev,
                              stream)
@@ -578,9 +617,10 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     _check_param("weight", weight, H, dev)
     _check_param("bias", bias, H, dev, weight.dtype)
     code = _out_code(out_dtype)
-    y = torch.empty(M, H, dtype=out_dtype, device=dev)
-    rstd = torch.empty(M, dtype=torch.float32, device=dev)
-    mean = torch.empty(M, dtype=torch.float32, device=dev) if center else None
+    y = _out((M, H), out_dtype, dev, stream)
+    rstd = _out(M, torch.float32, dev, stream)
+    mean = _out(M, torch.float32, dev, stream) if center else None
+    _reads(stream, None, x, weight, bias)
     _check(lib().qhead_layer_norm(x.data_ptr(), _SB_CODE[x.dtype], _row_stride(x, M, H), M, H,
                                   weight.data_ptr(), _ptr(bias), _SB_CODE[weight.dtype], eps,
                                   int(center), y.data_ptr(), code, _ptr(mean), rstd.data_ptr(),
@@ -607,9 +647,10 @@ def layer_norm_bwd(x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor | N
     _check_param("weight", weight, H, dev)
     mean = _check_vec("mean", mean, M, (torch.float32,), dev, required=False)
     rstd = _f32("rstd", rstd, M, dev)
-    dx = torch.empty(M, H, dtype=x.dtype, device=dev)
-    dw = torch.empty(H, dtype=torch.float32, device=dev)
-    db = torch.empty(H, dtype=torch.float32, device=dev) if want_dbias else None
+    dx = _out((M, H), x.dtype, dev, stream)
+    dw = _out(H, torch.float32, dev, stream)
+    db = _out(H, torch.float32, dev, stream) if want_dbias else None
+    _reads(stream, None, x, weight, mean, rstd, dy, workspace)
     if workspace is None:
         workspace = _scratch(_size(lib().qhead_layer_norm_bwd_workspace(M, H)), dev, stream)
     _check(lib().qhead_layer_norm_bwd(x.data_ptr(), _SB_CODE[x.dtype], _row_stride(x, M, H), M, H,
@@ -661,10 +702,11 @@ def distill_fwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     dev = h.device
     K = _check_teacher(ids, tlogits, M, dev)
     mask = _mask(mask, M, dev)
-    loss = torch.empty(M, dtype=torch.float32, device=dev)
-    lse = torch.empty(M, dtype=torch.float32, device=dev)
+    loss = _out(M, torch.float32, dev, stream)
+    lse = _out(M, torch.float32, dev, stream)
     c = head.c()
-    kept = torch.empty(M, _distill_size("qhead_distill_kept", c, M, K, dev), dtype=torch.float32, device=dev)
+    kept = _out((M, _distill_size("qhead_distill_kept", c, M, K, dev)), torch.float32, dev, stream)
+    _reads(stream, head, h, ids, tlogits, mask, workspace)
     if workspace is None:
         n = _distill_size("qhead_distill_fwd_workspace", c, M, K, dev)
         workspace = _scratch(n, dev, stream)
@@ -691,7 +733,8 @@ def distill_bwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     cols = _distill_size("qhead_distill_kept", c, M, K, dev)
     if kept.dtype != torch.float32 or kept.shape != (M, cols):
         raise ValueError(f"kept must be a float32 [{M}, {cols}] tensor")
-    dh = torch.empty_like(h)
+    dh = _out(h.shape, h.dtype, dev, stream)
+    _reads(stream, head, h, ids, tlogits, kept, lse, dloss, mask, workspace)
     if workspace is None:
         n = _distill_size("qhead_distill_bwd_workspace", c, M, K, dev)
         workspace = _scratch(n, dev, stream)
