@@ -12,10 +12,14 @@ The operators beside the head in the same manner: head_distill (the loss
 against a teacher's top logits, differentiable in h), layer_norm
 (differentiable in x, weight and bias) and embed (whose gradient is the
 dequantized table's: it goes into the tensor given for it).
+
+First derivatives only: a backward's result has no derivative of its own, and
+differentiating it (a gradient penalty under create_graph) raises.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import qhead
 
@@ -34,6 +38,7 @@ class HeadLogp(torch.autograd.Function):
         return logp
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_logp: torch.Tensor):
         h, targets, lse = ctx.saved_tensors
         dlogp = grad_logp.to(torch.float32).contiguous()
@@ -62,6 +67,7 @@ class HeadDistill(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_loss: torch.Tensor):
         h, ids, tlogits, lse, kept = ctx.saved_tensors
         dloss = grad_loss.to(torch.float32).contiguous()
@@ -89,6 +95,7 @@ class LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy: torch.Tensor):
         x, weight, mean, rstd = ctx.saved_tensors
         if dy.shape[1] > 1 and dy.stride(1) != 1 or dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]:
@@ -118,6 +125,7 @@ class Embed(torch.autograd.Function):
         return qhead.embed(head, tokens, scale, mask, out_dtype=out_dtype)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout: torch.Tensor):
         tokens, = ctx.saved_tensors
         qhead.embed_bwd(ctx.head, tokens, dout.contiguous(), ctx.scale, ctx.mask, dw=ctx.dw)
