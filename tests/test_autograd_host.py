@@ -1,5 +1,6 @@
 """The autograd forms' own rules, with the library's calls replaced by constants:
-a backward is not differentiated silently, and nothing reaches a GPU."""
+a backward is not differentiated silently, a mask changed in place between the
+directions is noticed, and nothing reaches a GPU."""
 import pytest
 import torch
 
@@ -64,3 +65,24 @@ def test_embed_gradient_goes_into_dw():
     y = autograd.embed(None, torch.zeros(M, dtype=torch.int32), dw=dw)
     y.sum().backward()
     assert (dw == 1.0).all()
+
+
+def _masked(name, mask):
+    t = torch.zeros(M, dtype=torch.int32)
+    if name == "embed":
+        return autograd.embed(None, t, 1.0, mask, dw=torch.zeros(5, H))
+    if name == "logp":
+        return autograd.head_logp(_bf(M, H), None, t, mask)
+    return autograd.head_distill(_bf(M, H), None, torch.zeros(M, K, dtype=torch.int32), torch.zeros(M, K), 1.0,
+                                 mask)
+
+
+@pytest.mark.parametrize("name", ["logp", "distill", "embed"])
+@pytest.mark.parametrize("dtype", [torch.bool, torch.uint8])
+def test_a_mask_changed_between_the_directions(name, dtype):
+    mask = torch.ones(M, dtype=dtype)
+    _masked(name, mask).sum().backward()
+    out = _masked(name, mask)
+    mask[1] = 0
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()

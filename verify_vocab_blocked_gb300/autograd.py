@@ -14,7 +14,9 @@ against a teacher's top logits, differentiable in h), layer_norm
 dequantized table's: it goes into the tensor given for it).
 
 First derivatives only: a backward's result has no derivative of its own, and
-differentiating it (a gradient penalty under create_graph) raises.
+differentiating it (a gradient penalty under create_graph) raises.  Every tensor
+of the forward that the backward reads again, the mask among them, is saved, so
+that one changed in place in between is noticed.
 """
 from __future__ import annotations
 
@@ -33,16 +35,15 @@ class HeadLogp(torch.autograd.Function):
                 mask: torch.Tensor | None = None):
         logp, lse, _ = qhead.fwd(head, h, targets, mask, want_argmax=False)
         ctx.head = head
-        ctx.mask = mask
-        ctx.save_for_backward(h, targets, lse)
+        ctx.save_for_backward(h, targets, lse, mask)
         return logp
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_logp: torch.Tensor):
-        h, targets, lse = ctx.saved_tensors
+        h, targets, lse, mask = ctx.saved_tensors
         dlogp = grad_logp.to(torch.float32).contiguous()
-        dh = qhead.bwd(ctx.head, h, targets, lse, dlogp, ctx.mask)
+        dh = qhead.bwd(ctx.head, h, targets, lse, dlogp, mask)
         return dh.to(h.dtype), None, None, None
 
 
@@ -62,17 +63,16 @@ class HeadDistill(torch.autograd.Function):
     def forward(ctx, h: torch.Tensor, head: qhead.Head, ids: torch.Tensor, tlogits: torch.Tensor,
                 temperature: float = 1.0, mask: torch.Tensor | None = None):
         loss, lse, kept = qhead.distill_fwd(head, h, ids, tlogits, temperature, mask)
-        ctx.head, ctx.temperature, ctx.mask = head, temperature, mask
-        ctx.save_for_backward(h, ids, tlogits, lse, kept)
+        ctx.head, ctx.temperature = head, temperature
+        ctx.save_for_backward(h, ids, tlogits, lse, kept, mask)
         return loss
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_loss: torch.Tensor):
-        h, ids, tlogits, lse, kept = ctx.saved_tensors
+        h, ids, tlogits, lse, kept, mask = ctx.saved_tensors
         dloss = grad_loss.to(torch.float32).contiguous()
-        dh = qhead.distill_bwd(ctx.head, h, ids, tlogits, kept, lse, dloss, ctx.temperature,
-                               ctx.mask)
+        dh = qhead.distill_bwd(ctx.head, h, ids, tlogits, kept, lse, dloss, ctx.temperature, mask)
         return dh, None, None, None, None, None
 
 
@@ -120,15 +120,15 @@ class Embed(torch.autograd.Function):
     @staticmethod
     def forward(ctx, anchor: torch.Tensor, head: qhead.Head, tokens: torch.Tensor, scale: float,
                 mask: torch.Tensor | None, dw: torch.Tensor, out_dtype: torch.dtype):
-        ctx.head, ctx.scale, ctx.mask, ctx.dw = head, scale, mask, dw
-        ctx.save_for_backward(tokens)
+        ctx.head, ctx.scale, ctx.dw = head, scale, dw
+        ctx.save_for_backward(tokens, mask)
         return qhead.embed(head, tokens, scale, mask, out_dtype=out_dtype)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout: torch.Tensor):
-        tokens, = ctx.saved_tensors
-        qhead.embed_bwd(ctx.head, tokens, dout.contiguous(), ctx.scale, ctx.mask, dw=ctx.dw)
+        tokens, mask = ctx.saved_tensors
+        qhead.embed_bwd(ctx.head, tokens, dout.contiguous(), ctx.scale, mask, dw=ctx.dw)
         return None, None, None, None, None, None, None
 
 
