@@ -170,6 +170,8 @@ class Head:
         wq, scales, biases, bits = self.wq, self.scales, self.biases, self.bits
         if not (wq.is_contiguous() and scales.is_contiguous() and biases.is_contiguous()):
             raise ValueError("head tensors must be contiguous")
+        if scales.device != wq.device or biases.device != wq.device:
+            raise ValueError("head tensors must be on one device")
         dtype = scales.dtype
         code = _SB_CODE.get(dtype)
         if code is None or biases.dtype != dtype:
@@ -204,11 +206,25 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> int:
-    """The handle of the given stream, or of the current device's current one
-    (read without building a Stream object, a fifth of a small call's time)."""
+def _usable(dev: torch.device, stream, workspace: torch.Tensor | None = None) -> None:
+    """The checked tensors' device must be the GPU whose stream the kernels are
+    launched on: an address of another device, or of the host, is not for them."""
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors are on {dev}: they must be on a GPU")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev} but the current device is "
+                         f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the tensors are on {dev} but the stream is of {stream.device}")
+    if workspace is not None and workspace.device != dev:
+        raise ValueError(f"the tensors are on {dev} but the workspace is on {workspace.device}")
+
+
+def _stream(stream, dev: torch.device) -> int:
+    """The handle of the given stream, or of the current one (read without
+    building a Stream object, a fifth of a small call's time)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(dev.index)
     return stream.cuda_stream
 
 
@@ -336,6 +352,7 @@ def fwd(head: Head, h: torch.Tensor, targets: torch.Tensor | None = None,
     targets = _targets(targets, M, dev, required=False)
     mask = _mask(mask, M, dev)
     want_logp = want_logp and targets is not None
+    _usable(dev, stream, workspace)
     logp = _out(M, torch.float32, dev, stream) if want_logp else None
     lse = _out(M, torch.float32, dev, stream) if want_lse else None
     am = _out(M, torch.int32, dev, stream) if want_argmax else None
@@ -344,7 +361,7 @@ def fwd(head: Head, h: torch.Tensor, targets: torch.Tensor | None = None,
         workspace = _scratch(fwd_workspace(head, M), dev, stream)
     _check(lib().qhead_fwd(ctypes.byref(head.c()), h.data_ptr(), M, _ptr(targets), _ptr(mask),
                            _ptr(logp), _ptr(lse), _ptr(am), workspace.data_ptr(),
-                           workspace.numel(), _stream(stream)))
+                           workspace.numel(), _stream(stream, dev)))
     return logp, lse, am
 
 
@@ -357,13 +374,14 @@ def bwd(head: Head, h: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
     targets = _targets(targets, M, dev, required=True)
     mask = _mask(mask, M, dev)
     lse, dlogp = _f32("lse", lse, M, dev), _f32("dlogp", dlogp, M, dev)
+    _usable(dev, stream, workspace)
     dh = _out((M, head.H), torch.float32, dev, stream)
     _reads(stream, head, h, targets, lse, dlogp, mask, workspace)
     if workspace is None:
         workspace = _scratch(bwd_workspace(head, M), dev, stream)
     _check(lib().qhead_bwd(ctypes.byref(head.c()), h.data_ptr(), M, _ptr(targets), _ptr(mask),
                            lse.data_ptr(), dlogp.data_ptr(), dh.data_ptr(), workspace.data_ptr(),
-                           workspace.numel(), _stream(stream)))
+                           workspace.numel(), _stream(stream, dev)))
     return dh
 
 
@@ -377,6 +395,7 @@ def bwd_dw(head: Head, h: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor
     targets = _targets(targets, M, dev, required=True)
     mask = _mask(mask, M, dev)
     lse, dlogp = _f32("lse", lse, M, dev), _f32("dlogp", dlogp, M, dev)
+    _usable(dev, stream, workspace)
     dh = _out((M, head.H), torch.float32, dev, stream) if want_dh else None
     dw = _out((head.V, head.H), torch.float32, dev, stream)
     _reads(stream, head, h, targets, lse, dlogp, mask, workspace)
@@ -385,7 +404,7 @@ def bwd_dw(head: Head, h: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor
     _check(lib().qhead_bwd_dw(ctypes.byref(head.c()), h.data_ptr(), M, targets.data_ptr(),
                               _ptr(mask), lse.data_ptr(), dlogp.data_ptr(), _ptr(dh),
                               dw.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                              _stream(stream)))
+                              _stream(stream, dev)))
     return dh, dw
 
 
@@ -405,6 +424,7 @@ def fwd_blockmax(head: Head, h: torch.Tensor, targets: torch.Tensor | None = Non
     dev = h.device
     targets = _targets(targets, M, dev, required=False)
     mask = _mask(mask, M, dev)
+    _usable(dev, stream, workspace)
     logp = _out(M, torch.float32, dev, stream) if targets is not None else None
     lse = _out(M, torch.float32, dev, stream)
     am = _out(M, torch.int32, dev, stream)
@@ -415,7 +435,7 @@ def fwd_blockmax(head: Head, h: torch.Tensor, targets: torch.Tensor | None = Non
     _check(lib().qhead_fwd_blockmax(ctypes.byref(head.c()), h.data_ptr(), M, _ptr(targets),
                                     _ptr(mask), _ptr(logp), lse.data_ptr(), am.data_ptr(),
                                     bm.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                    _stream(stream)))
+                                    _stream(stream, dev)))
     return logp, lse, am, bm
 
 
@@ -435,6 +455,7 @@ def bwd_blockskip(head: Head, h: torch.Tensor, targets: torch.Tensor, lse: torch
             or tuple(block_max.shape) != (M, nvt) or not block_max.is_contiguous()
             or block_max.device != dev):
         raise ValueError(f"block_max must be a contiguous float32 [{M}, {nvt}] tensor on {dev}")
+    _usable(dev, stream, workspace)
     dh = _out((M, head.H), torch.float32, dev, stream)
     _reads(stream, head, h, targets, lse, dlogp, block_max, mask, workspace)
     if workspace is None:
@@ -442,7 +463,7 @@ def bwd_blockskip(head: Head, h: torch.Tensor, targets: torch.Tensor, lse: torch
     _check(lib().qhead_bwd_blockskip(ctypes.byref(head.c()), h.data_ptr(), M, targets.data_ptr(),
                                      _ptr(mask), lse.data_ptr(), dlogp.data_ptr(),
                                      block_max.data_ptr(), float(eps), dh.data_ptr(),
-                                     workspace.data_ptr(), workspace.numel(), _stream(stream)))
+                                     workspace.data_ptr(), workspace.numel(), _stream(stream, dev)))
     return dh
 
 
@@ -457,6 +478,7 @@ def bwd_filter(head: Head, h: torch.Tensor, targets: torch.Tensor, lse: torch.Te
     targets = _targets(targets, M, dev, required=True)
     mask = _mask(mask, M, dev)
     lse, dlogp = _f32("lse", lse, M, dev), _f32("dlogp", dlogp, M, dev)
+    _usable(dev, stream, workspace)
     dh = _out((M, head.H), torch.float32, dev, stream)
     cold = _out(((M + 31) // 32, (head.V + 31) // 32), torch.uint8, dev, stream) if want_cold else None
     _reads(stream, head, h, targets, lse, dlogp, mask, workspace)
@@ -465,7 +487,7 @@ def bwd_filter(head: Head, h: torch.Tensor, targets: torch.Tensor, lse: torch.Te
     _check(lib().qhead_bwd_filter(ctypes.byref(head.c()), h.data_ptr(), M, targets.data_ptr(),
                                   _ptr(mask), lse.data_ptr(), dlogp.data_ptr(), float(eps),
                                   dh.data_ptr(), _ptr(cold), workspace.data_ptr(),
-                                  workspace.numel(), _stream(stream)))
+                                  workspace.numel(), _stream(stream, dev)))
     return dh, cold
 
 
@@ -486,6 +508,7 @@ def verify(head: Head, h: torch.Tensor, W: int, draft: torch.Tensor | None,
     if draft is not None and draft.device != dev:
         raise ValueError(f"draft is on {draft.device}, h on {dev}")
     mask = _mask(mask, M, dev)
+    _usable(dev, stream, workspace)
     am = _out(M, torch.int32, dev, stream)
     lse = _out(M, torch.float32, dev, stream) if want_lse else None
     n_acc = _out(B, torch.int32, dev, stream)
@@ -496,7 +519,7 @@ def verify(head: Head, h: torch.Tensor, W: int, draft: torch.Tensor | None,
     _check(lib().qhead_verify(ctypes.byref(head.c()), h.data_ptr(), B, W, _ptr(draft),
                               _ptr(mask), _ptr(lse), am.data_ptr(), n_acc.data_ptr(),
                               nxt.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                              _stream(stream)))
+                              _stream(stream, dev)))
     return n_acc, nxt, am, lse
 
 
@@ -553,10 +576,11 @@ def embed(head: Head, tokens: torch.Tensor, scale: float = 1.0, mask: torch.Tens
         mask = _mask(mask, M, dev)
     code = _out_code(out_dtype)
     c = head.c()
+    _usable(dev, stream)
     out = _out((M, c.H), out_dtype, dev, stream)
     _reads(stream, head, tokens, mask)
     _check(lib().qhead_embed(ctypes.byref(c), tokens.data_ptr(), M, _ptr(mask), scale,
-                             out.data_ptr(), code, _stream(stream)))
+                             out.data_ptr(), code, _stream(stream, dev)))
     return out
 
 
@@ -573,11 +597,12 @@ def embed_bwd(head: Head, tokens: torch.Tensor, dout: torch.Tensor, scale: float
     if tuple(dout.shape) != (M, head.H):
         raise ValueError(f"dout must have shape [{M}, {head.H}], got {list(dout.shape)}")
     add = dw is not None
+    if add and (not isinstance(dw, torch.Tensor) or dw.dtype != torch.float32 or dw.device != dev
+                or tuple(dw.shape) != (head.V, head.H) or not dw.is_contiguous()):
+        raise ValueError(f"dw must be a contiguous float32 [{head.V}, {head.H}] tensor on {dev}")
+    _usable(dev, stream, workspace)
     if not add:
         dw = _out((head.V, head.H), torch.float32, dev, stream)
-    elif (not isinstance(dw, torch.Tensor) or dw.dtype != torch.float32 or dw.device != dev
-          or tuple(dw.shape) != (head.V, head.H) or not dw.is_contiguous()):
-        raise ValueError(f"dw must be a contiguous float32 [{head.V}, {head.H}] tensor on {dev}")
     c = head.c()
     _reads(stream, None, tokens, dout, mask, dw if add else None, workspace)
     if workspace is None:
@@ -585,7 +610,7 @@ def embed_bwd(head: Head, tokens: torch.Tensor, dout: torch.Tensor, scale: float
                              stream)
     _check(lib().qhead_embed_bwd(ctypes.byref(c), tokens.data_ptr(), M, _ptr(mask), scale,
                                  dout.data_ptr(), _SB_CODE[dout.dtype], dw.data_ptr(), int(add),
-                                 workspace.data_ptr(), workspace.numel(), _stream(stream)))
+                                 workspace.data_ptr(), workspace.numel(), _stream(stream, dev)))
     return dw
 
 
@@ -617,6 +642,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     _check_param("weight", weight, H, dev)
     _check_param("bias", bias, H, dev, weight.dtype)
     code = _out_code(out_dtype)
+    _usable(dev, stream)
     y = _out((M, H), out_dtype, dev, stream)
     rstd = _out(M, torch.float32, dev, stream)
     mean = _out(M, torch.float32, dev, stream) if center else None
@@ -624,7 +650,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     _check(lib().qhead_layer_norm(x.data_ptr(), _SB_CODE[x.dtype], _row_stride(x, M, H), M, H,
                                   weight.data_ptr(), _ptr(bias), _SB_CODE[weight.dtype], eps,
                                   int(center), y.data_ptr(), code, _ptr(mean), rstd.data_ptr(),
-                                  _stream(stream)))
+                                  _stream(stream, dev)))
     return y, mean, rstd
 
 
@@ -647,6 +673,7 @@ def layer_norm_bwd(x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor | N
     _check_param("weight", weight, H, dev)
     mean = _check_vec("mean", mean, M, (torch.float32,), dev, required=False)
     rstd = _f32("rstd", rstd, M, dev)
+    _usable(dev, stream, workspace)
     dx = _out((M, H), x.dtype, dev, stream)
     dw = _out(H, torch.float32, dev, stream)
     db = _out(H, torch.float32, dev, stream) if want_dbias else None
@@ -657,7 +684,7 @@ def layer_norm_bwd(x: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor | N
                                       weight.data_ptr(), _SB_CODE[weight.dtype], _ptr(mean),
                                       rstd.data_ptr(), dy.data_ptr(), _SB_CODE[dy.dtype],
                                       _row_stride(dy, M, H), dx.data_ptr(), dw.data_ptr(), _ptr(db),
-                                      workspace.data_ptr(), workspace.numel(), _stream(stream)))
+                                      workspace.data_ptr(), workspace.numel(), _stream(stream, dev)))
     return dx, dw, db
 
 
@@ -702,6 +729,7 @@ def distill_fwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     dev = h.device
     K = _check_teacher(ids, tlogits, M, dev)
     mask = _mask(mask, M, dev)
+    _usable(dev, stream, workspace)
     loss = _out(M, torch.float32, dev, stream)
     lse = _out(M, torch.float32, dev, stream)
     c = head.c()
@@ -713,7 +741,7 @@ def distill_fwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     _check(lib().qhead_distill_fwd(ctypes.byref(c), h.data_ptr(), M, ids.data_ptr(),
                                    tlogits.data_ptr(), _SB_CODE[tlogits.dtype], K, temperature,
                                    _ptr(mask), loss.data_ptr(), lse.data_ptr(), kept.data_ptr(),
-                                   workspace.data_ptr(), workspace.numel(), _stream(stream)))
+                                   workspace.data_ptr(), workspace.numel(), _stream(stream, dev)))
     return loss, lse, kept
 
 
@@ -733,6 +761,7 @@ def distill_bwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
     cols = _distill_size("qhead_distill_kept", c, M, K, dev)
     if kept.dtype != torch.float32 or kept.shape != (M, cols):
         raise ValueError(f"kept must be a float32 [{M}, {cols}] tensor")
+    _usable(dev, stream, workspace)
     dh = _out(h.shape, h.dtype, dev, stream)
     _reads(stream, head, h, ids, tlogits, kept, lse, dloss, mask, workspace)
     if workspace is None:
@@ -742,5 +771,5 @@ def distill_bwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
                                    tlogits.data_ptr(), _SB_CODE[tlogits.dtype], K, temperature,
                                    _ptr(mask), kept.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
                                    dh.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                   _stream(stream)))
+                                   _stream(stream, dev)))
     return dh
