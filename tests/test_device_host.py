@@ -58,3 +58,14 @@ def test_a_head_of_two_devices():
         split.c()
     with pytest.raises(ValueError, match="one device"):
         qhead.embed(split, torch.zeros(M, dtype=torch.int32))
+
+
+def test_stream_handles(monkeypatch):
+    """With and without torch's accessor of the bare handle."""
+    dev = torch.device("cuda:0")
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: Stream(d))
+    monkeypatch.setattr(qhead, "_raw_stream", lambda i: 40 + i)
+    assert qhead._stream(None, dev) == 40
+    monkeypatch.setattr(qhead, "_raw_stream", None)
+    assert qhead._stream(None, dev) == 7
+    assert qhead._stream(Stream(dev), dev) == 7

@@ -220,12 +220,18 @@ def _usable(dev: torch.device, stream, workspace: torch.Tensor | None = None) ->
         raise ValueError(f"the tensors are on {dev} but the workspace is on {workspace.device}")
 
 
+# The current stream's handle without a Stream object around it, where torch has it
+# (building one is a fifth of a small call's time).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, dev: torch.device) -> int:
-    """The handle of the given stream, or of the current one (read without
-    building a Stream object, a fifth of a small call's time)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
-    return stream.cuda_stream
+    """The handle of the given stream, or of the current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev.index)
 
 
 def _check_h(head: Head, h: torch.Tensor, what: str = "[M, H]") -> int:
