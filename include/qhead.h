@@ -414,7 +414,7 @@ int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int
  *   tlogits   device, [M, K] of type t_dtype: logits or log-probabilities
  *             (only differences within a row matter); -inf is no mass.
  *   K         1 <= K <= 1024.
- *   temperature  > 0 and finite.
+ *   temperature  > 0 and finite, a normal float (its reciprocal is one, too).
  *   loss, lse device, float [M]; inactive rows 0.  A row without a valid entry
  *             of finite logit has loss 0; one with an id >= V or a logit that
  *             is NaN or +inf has loss NaN.

@@ -7,6 +7,7 @@
 // Backward sequence: compact -> head backward (per-split partial dh) ->
 //                    finalize (fixed-order sum, exact one-hot term, zeros for
 //                    masked rows).
+#include <float.h>
 #include <stdio.h>
 
 #include <map>
@@ -369,7 +370,9 @@ int check_distill_inputs(const void* h, const void* ids, const void* tl, int t_d
     if (!h || !ids || !tl) return fail(QHEAD_EINVAL, "h, ids and tlogits are required");
     if (misaligned(h, 16)) return fail(QHEAD_EINVAL, "h must be 16-byte aligned");
     if (!dtype_ok(t_dtype)) return fail(QHEAD_EUNSUPPORTED, "t_dtype must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
-    if (!(temp > 0.f) || temp > 3.4e38f) return fail(QHEAD_EINVAL, "temperature must be positive and finite");
+    // (below the normal range its reciprocal, which the kernels multiply by, is no fp32)
+    if (!(temp >= FLT_MIN) || temp > 3.4e38f)
+        return fail(QHEAD_EINVAL, "temperature must be positive, normal and finite");
     return QHEAD_OK;
 }
 
