@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(16 * kJoinGroups) few_join_kernel(
 int few_splits(int64_t M, int64_t V, int H, int bits) {
     const int gx = (H + kColsCta - 1) / kColsCta;
     const int64_t nb = (V + kBlockRows - 1) / kBlockRows;
-    const int64_t want = ctas_per_sm(bits, M <= 8 ? 1 : 2) * 152 / gx;  // one wave
+    const int64_t want = ctas_per_sm(bits, M <= 8 ? 1 : 2) * (int64_t)device_sms() / gx;  // one wave
     return (int)(nb < want ? nb : want < 1 ? 1 : want);
 }
 

@@ -655,17 +655,17 @@ cudaError_t pick_fwd(const NormArgs& a, cudaStream_t st) {
     return elem_shape(H, [&](auto nt, auto ne) {
         constexpr int NT = decltype(nt)::value, NE = decltype(ne)::value, B = elem_block(NT);
         const int64_t blocks = NT == 32 ? (a.M + kElemWarps - 1) / kElemWarps : a.M;
-        const int64_t most = 152 * (int64_t)elem_fwd_blocks(NT, NE);
+        const int64_t most = device_sms() * (int64_t)elem_fwd_blocks(NT, NE);
         norm_fwd_elem_kernel<T, NT, NE><<<(unsigned)(blocks < most ? blocks : most), B, 0, st>>>(a);
         return cudaGetLastError();
     });
 }
 
 // The backward's rows are dealt to the blocks in equal shares, so the blocks are as
-// many as the SMs hold at once (152: GB300's SMs; at most a.grid, which the partial
-// rows are planned for).  `a.grid` becomes that number.
+// many as the device's SMs hold at once (at most a.grid, which the partial rows are
+// planned for).  `a.grid` becomes that number.
 void fit_grid(NormBwdArgs& a, int per_sm) {
-    const int n = 152 * (per_sm < 1 ? 1 : per_sm);
+    const int n = device_sms() * (per_sm < 1 ? 1 : per_sm);
     if (a.grid > n) a.grid = n;
 }
 
@@ -724,7 +724,8 @@ int norm_bwd_grid(int64_t M, int H) {
     const int most = H <= 512 ? 16 : 8;
     int per_sm = 65536 / (80 * threads);
     per_sm = per_sm < 1 ? 1 : per_sm > most ? most : per_sm;
-    const int64_t want = 152 * per_sm;
+    constexpr int64_t kPlannedSms = 152;  // (a GB300's; a larger device leaves some idle)
+    const int64_t want = kPlannedSms * per_sm;
     return (int)(M < want ? (M < 1 ? 1 : M) : want);
 }
 
