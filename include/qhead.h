@@ -421,8 +421,9 @@ int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int
  *   kept      device, float [M, qhead_distill_kept(head, M, K)], 32-byte
  *             aligned, for the backward: in the first K columns the exact fp32
  *             logits z of the valid entries (0 elsewhere), then the exact logits
- *             of the largest other vocab rows, up to 16, and (as int32 bits, 0:
- *             none) those rows plus one; at M <= 16, or while M * V * 4 is at
+ *             of the largest other vocab rows (those with a thousandth of the sum
+ *             or more, up to 16, wherever they lie), and (as int32 bits, 0: none)
+ *             those rows plus one; at M <= 16, or while M * V * 4 is at
  *             most 4 GiB, also the row's V logits, so that the backward need not
  *             form them again, with (q_v - p_v) * sech2 * 2^126 (-inf: 0) in
  *             place of those of the tokens whose exact ones are kept.  In a row

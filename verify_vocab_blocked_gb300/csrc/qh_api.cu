@@ -328,14 +328,14 @@ int check_rows(int64_t M) {
     return QHEAD_OK;
 }
 
-// The distillation's workspace: the head plan's, then the left-out lists
-// (forward) or the rows' cotangents (backward).  The forward of few rows plans
-// the weight-streaming kernel's region and the softmax pass's partials.
+// The distillation's workspace: the head plan's, then the left-out lists and the
+// slices' maxima (forward) or the rows' cotangents (backward).  The forward of few
+// rows plans the weight-streaming kernel's region and the softmax pass's partials.
 struct DistillPlan {
     FwdPlan f;
     BwdPlan b;
     bool few_dh = false;
-    size_t off_few = 0, off_extra = 0, total = 0;
+    size_t off_few = 0, off_extra = 0, off_smax = 0, total = 0;
 };
 
 static_assert(qh::kFewM <= qh::kFewRows, "few rows");
@@ -356,6 +356,10 @@ int plan_distill(const qhead_head* hd, int64_t M, int64_t K, bool bwd, DistillPl
     p->total = p->off_extra + (bwd   ? 4 * (size_t)M
                                : few ? sizeof(qh::Partial) * (size_t)M * qh::kFewSplits
                                      : 4 * (size_t)p->f.Mpad * (size_t)(K + 1));
+    if (!bwd) {
+        p->off_smax = align_up(p->total, 256);
+        p->total = p->off_smax + 4 * (size_t)M * (size_t)qh::slice_columns(hd->V);
+    }
     return QHEAD_OK;
 }
 
@@ -984,6 +988,7 @@ int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const in
     __half* h16 = at<__half>(workspace, p.off_h16);
     qh::Partial* part = at<qh::Partial>(workspace, p.off_part);
     int* sid = at<int>(workspace, dp.off_extra);
+    float* smax = at<float>(workspace, dp.off_smax);
     const float inv_t = 1.f / temperature;
     const int64_t ld = qh::kept_columns(M, K, head->V);
     float* zout = qh::keeps_logits(M, head->V) ? kept + qh::kept_logits_at(K) : nullptr;
@@ -1000,11 +1005,11 @@ int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const in
                                          head->softcap, hb, pos, M, ids, (int)K, nullptr, kept, ld, zout,
                                          st)))
             return cuda_fail(e, "distill_prep");
-        if ((e = qh::launch_distill_split(zout, ld, head->V, head->softcap, inv_t, pos, M, few, st)))
+        if ((e = qh::launch_distill_split(zout, ld, head->V, head->softcap, inv_t, pos, M, few, smax, st)))
             return cuda_fail(e, "distill_split");
         e = qh::launch_distill_finalize(head->wq, sb_view(head), head->V, head->H, head->bits,
                                         head->softcap, hb, pos, M, ids, tlogits, t_dtype, (int)K, inv_t, 1.f,
-                                        kept, ld, zout, few, qh::kFewSplits, nullptr, err, loss, lse, st);
+                                        kept, ld, zout, few, qh::kFewSplits, nullptr, smax, err, loss, lse, st);
         return e ? cuda_fail(e, "distill_finalize") : QHEAD_OK;
     }
     if ((rc = stage_rows(mask, hb, M, p.Mpad, head, rows, pos, count, err, h16, st))) return rc;
@@ -1025,13 +1030,14 @@ int qhead_distill_fwd(const qhead_head* head, const void* h, int64_t M, const in
     ta.unbias = qh::distill_unbias(head->H);
     ta.sid = sid; ta.sid_ld = (int)K + 1;
     ta.zout = zout; ta.zout_ld = ld;
+    ta.smax = smax; ta.smax_ld = qh::slice_columns(head->V);
     hook_before(st);
     e = qh::launch_tc_fwd(th, tw, ta, head->bits, false, p.grid, st);
     hook_after(st);
     if (e) return cuda_fail(e, "tc_fwd");
     e = qh::launch_distill_finalize(head->wq, sb_view(head), head->V, head->H, head->bits, head->softcap,
                                     hb, pos, M, ids, tlogits, t_dtype, (int)K, inv_t, ta.unbias, kept, ld, zout,
-                                    part, 0, S_dev, err, loss, lse, st);
+                                    part, 0, S_dev, smax, err, loss, lse, st);
     return e ? cuda_fail(e, "distill_finalize") : QHEAD_OK;
 }
 

@@ -17,7 +17,9 @@
 // computed exactly (fp32, weights widened) once, in the forward, and kept:
 //   * the softmax epilogue leaves the teacher's columns out of its sum and the
 //     finalize adds their exact terms and replaces those of the largest other
-//     columns (up to kOthers), whose exact logits are kept as well;
+//     columns (a thousandth of the sum or more, up to kOthers), whose exact logits
+//     are kept as well; it finds them by the maxima that the epilogue writes for
+//     every 32 columns;
 //   * the backward's coefficient block gets (q_k - p_k) sech2_k, formed in
 //     fp32 from the exact logits, in the K teacher's and the kept other columns
 //     of each row before the contraction with W, so the one-hot part of the
@@ -36,6 +38,7 @@
 // rows the weight-streaming kernel writes them, whose cost follows the rows (the
 // tensor-core kernel's does not: 227 us from 1 to 128 rows of the 262144 x 2560
 // head), and a softmax pass of its own reads them.
+#include "qh_dequant.cuh"
 #include "qh_distill.cuh"
 #include "qh_ops.cuh"
 #include "qh_tc.cuh"
@@ -294,14 +297,70 @@ __device__ __forceinline__ Teacher load_teacher(const int32_t* idr, const T* tr,
     return te;
 }
 
+// A logit as the tensor-core kernels form it but for their accumulation's rounding:
+// fp16 operands, w = fma(code, scale, bias) rounded to fp16, summed here in fp32.  One
+// lane computes one vocab row v.
+template <int BITS>
+__device__ float rounded_logit(const __nv_bfloat16* __restrict__ hrow, const uint32_t* __restrict__ wq,
+                               const SbView& sb, int64_t v, int H) {
+    const uint32_t* wr = wq + v * (int64_t)(H * BITS / 32);
+    float acc[2] = {0.f, 0.f};
+#pragma unroll 2
+    for (int u = 0; u < H / 8; ++u) {
+        const int64_t g = v * (int64_t)(H / 64) + u / 8;
+        const uint32_t s2 = bcast_h(__float2half_rn(sb_elem(sb.s, g, sb.type)));
+        const uint32_t b2 = bcast_h(__float2half_rn(sb_elem(sb.b, g, sb.type)));
+        const uint4 hw = *reinterpret_cast<const uint4*>(hrow + 8 * u);
+        const __nv_bfloat16* hp = reinterpret_cast<const __nv_bfloat16*>(&hw);
+        uint32_t p[4];  // 4 bits: elements (k, k + 4); 8 bits: (2 k, 2 k + 1)
+        if constexpr (BITS == 4) {
+            deq4_word(wr[u], s2, b2, p);
+        } else {
+            const uint2 w = reinterpret_cast<const uint2*>(wr)[u];
+            p[0] = deq8(w.x, 0x4140u, s2, b2);
+            p[1] = deq8(w.x, 0x4342u, s2, b2);
+            p[2] = deq8(w.y, 0x4140u, s2, b2);
+            p[3] = deq8(w.y, 0x4342u, s2, b2);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 w = __half22float2(u32_as_h2(p[k]));
+            const int a = BITS == 4 ? k : 2 * k, b = BITS == 4 ? k + 4 : 2 * k + 1;
+            acc[0] = fmaf(__half2float(__float2half_rn(__bfloat162float(hp[a]))), w.x, acc[0]);
+            acc[1] = fmaf(__half2float(__float2half_rn(__bfloat162float(hp[b]))), w.y, acc[1]);
+        }
+    }
+    return acc[0] + acc[1];
+}
+
 // One block per row: merges the row's partials at the temperature, adds the
 // exact terms of the teacher's distinct tokens, replaces those of the largest
-// other logits by exact ones, and forms the loss.  The others: of the segments'
-// candidates those whose share of the sum is at least kShare (a tensor-core
-// logit is 3e-4 off: below that share it moves lse by less than 3e-7), the
-// kOthers largest if there are more.
+// other logits by exact ones, and forms the loss.  The others: the columns whose
+// share of the sum is at least kShare (a tensor-core logit is 3e-4 off: below
+// that share it moves lse by less than 3e-7), the kOthers largest if there are
+// more.  They lie in the slices of 32 columns whose maxima reach that share, and
+// the kOthers largest in the kOthers slices of the largest maxima; those slices are
+// looked through: the kept logits, or where none are kept the logits formed again
+// (two tokens of adjacent ids with 0.4 of the mass each, and one candidate a slice:
+// the loss came out 1e-4 off).
 constexpr float kShare = 1e-3f;
-constexpr int kMaxShares = 1024;  // at most 1 / kShare terms have that share
+constexpr int kMaxShares = 1024;  // at most 1 / kShare slices or columns have that share
+
+// Of the n candidates (value, index) the kOthers largest, in order, by counting.
+__device__ __forceinline__ void take_largest(const float2* cand, int n, float* v, int* at) {
+    for (int k = threadIdx.x; k < n; k += kThreads) {
+        const float2 q = cand[k];
+        int rank = 0;
+        for (int j = 0; j < n; ++j) {
+            const float2 o = cand[j];
+            rank += better(o.x, __float_as_int(o.y), q.x, __float_as_int(q.y));
+        }
+        if (rank < kOthers) {
+            v[rank] = q.x;
+            at[rank] = __float_as_int(q.y);
+        }
+    }
+}
 
 template <int BITS, typename T>
 __global__ void __launch_bounds__(kThreads, 4) distill_finalize_kernel(
@@ -309,17 +368,19 @@ __global__ void __launch_bounds__(kThreads, 4) distill_finalize_kernel(
     const __nv_bfloat16* __restrict__ h, const int* __restrict__ pos,
     const int32_t* __restrict__ ids, const T* __restrict__ tl, int K, float inv_t, float unbias,
     float* kept, int64_t ld, float* zout, const Partial* part, int S,
-    const int* S_dev, const int* err, float* __restrict__ loss,
+    const int* S_dev, const float* smax, const int* err, float* __restrict__ loss,
     float* __restrict__ lse) {
     tc::grid_dep_wait();
     tc::grid_dep_trigger();
-    __shared__ float2 cand_sh[kMaxShares];  // candidates (v, i) of enough share
-    __shared__ int n_cand;
+    __shared__ float2 cand_sh[kMaxShares];  // slices, then columns (v, i) of enough share
+    __shared__ int n_slices, n_cand;
+    __shared__ float hot_v[kOthers];        // the slices that are looked through
+    __shared__ int hot_i[kOthers];
     __shared__ float red[kWarps];
     __shared__ float2 red2[kWarps];
     __shared__ int id_sh[kMaxTeacher];
     __shared__ float t_sh[kMaxTeacher];
-    __shared__ float other_v[kOthers], other_z[kOthers];  // the others' logits: kernel's (raw), exact
+    __shared__ float other_v[kOthers], other_z[kOthers];  // the others' logits: kernel's (raw, unbiased), exact
     __shared__ int other_i[kOthers];
     const int64_t r = blockIdx.x;
     const int i = pos[r];
@@ -343,6 +404,9 @@ __global__ void __launch_bounds__(kThreads, 4) distill_finalize_kernel(
         prefetch_l1(tl + r * K + k);
         prefetch_l1(zr + k);
     }
+    const int n_sl = (int)((V + 31) / 32);
+    const float* sm = smax + (int64_t)i * slice_columns(V);
+    for (int k = 32 * threadIdx.x; k < n_sl; k += 32 * kThreads) prefetch_l1(sm + k);
     if (S_dev) S = *S_dev;
     // Without a cap the kernel's factor `unbias` stands in its exponent: m in its terms.
     const float mscale = cap > 0.f ? 1.f : unbias;
@@ -359,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_finalize_kernel(
         bad |= p.status;
         fold(p.m * mscale, p.s);
     }
-    if (threadIdx.x == 0) n_cand = 0;
+    if (threadIdx.x == 0) n_slices = n_cand = 0;
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) loss[r] = lse[r] = nan_f();
         no_others(INFINITY);
@@ -404,38 +468,60 @@ __global__ void __launch_bounds__(kThreads, 4) distill_finalize_kernel(
     cross = block_sum(cross, red);
     float rest = m > -INFINITY ? s * expf((m - top) * inv_t) : 0.f;
 
-    // The candidates of enough share (in any order), then the largest of them
-    // by rank.  floor_z: the capped logit of that share; the cap is monotone.
-    const float floor_z = top + logf(kShare * (rest + sum)) / inv_t;
-    for (int k = threadIdx.x; k < S; k += kThreads) {
-        const float qv[2] = {prow[k].v1, prow[k].v2};
-        const int qi[2] = {prow[k].i1, prow[k].i2};
+    // The slices of enough share (in any order), then the largest of them by rank.
+    // floor: the raw logit of that share (the cap is monotone).
+    float floor = top + logf(kShare * (rest + sum)) / inv_t;
+    if (cap > 0.f) {
+        const float f = floor / cap;
+        floor = f >= 1.f ? INFINITY : f <= -1.f ? -INFINITY : cap * atanhf(f);
+    }
+    auto enough = [&](float z) { return z > -INFINITY && z >= floor; };
+    for (int k0 = 4 * threadIdx.x; k0 < n_sl; k0 += 16 * kThreads) {
+        float4 q[4];  // (whole tiles of 8: the rest of a group of four is there)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float v = qv[e];
-            const int at = qi[e];
-            // (a cap only shrinks a positive logit)
-            if ((v * unbias >= floor_z || floor_z < 0.f) && (int64_t)at < V &&
-                softcap_exact(v * unbias, cap) >= floor_z) {
-                const int n = atomicAdd(&n_cand, 1);
-                if (n < kMaxShares) cand_sh[n] = make_float2(v, __int_as_float(at));
+        for (int e = 0; e < 4; ++e) {
+            const int k = k0 + 4 * kThreads * e;
+            q[e] = k < n_sl ? *reinterpret_cast<const float4*>(sm + k) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x[4] = {q[e].x, q[e].y, q[e].z, q[e].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = k0 + 4 * kThreads * e + j;
+                if (k < n_sl && enough(x[j] * unbias)) {
+                    const int n = atomicAdd(&n_slices, 1);
+                    if (n < kMaxShares) cand_sh[n] = make_float2(x[j], __int_as_float(k));
+                }
             }
         }
     }
     __syncthreads();
-    const int n_all = min(n_cand, kMaxShares), n_other = min(n_all, kOthers);
-    for (int k = threadIdx.x; k < n_all; k += kThreads) {
-        const float2 q = cand_sh[k];
-        int rank = 0;
-        for (int j = 0; j < n_all; ++j) {
-            const float2 o = cand_sh[j];
-            rank += better(o.x, __float_as_int(o.y), q.x, __float_as_int(q.y));
+    const int all_hot = min(n_slices, kMaxShares), n_hot = min(all_hot, kOthers);
+    take_largest(cand_sh, all_hot, hot_v, hot_i);
+    __syncthreads();
+    // Their columns, a slice to a warp.
+    for (int c = warp; c < n_hot; c += kWarps) {
+        const int col = 32 * hot_i[c] + lane;
+        float x = -INFINITY;  // the kernel's raw logit, unbiased; -inf: a listed token, or past V
+        if ((int64_t)col < V) {
+            if (zout != nullptr) {
+                x = zout[r * ld + col] * unbias;
+            } else {
+                x = rounded_logit<BITS>(h + r * (int64_t)H, wq, sb, col, H);
+                if (enough(x))
+                    for (int k = 0; k < K; ++k)
+                        if (id_sh[k] == col) x = -INFINITY;
+            }
         }
-        if (rank < kOthers) {
-            other_v[rank] = q.x;
-            other_i[rank] = __float_as_int(q.y);
+        if (enough(x)) {
+            const int n = atomicAdd(&n_cand, 1);  // (at most 32 kOthers)
+            cand_sh[n] = make_float2(x, __int_as_float(col));
         }
     }
+    __syncthreads();
+    const int n_all = n_cand, n_other = min(n_all, kOthers);
+    take_largest(cand_sh, n_all, other_v, other_i);
     __syncthreads();
     // Their exact logits, two to a warp; the kernel's terms out.
 #pragma unroll 1
@@ -455,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_finalize_kernel(
         const bool have = lane < n_other;
         float out_of = 0.f, add = 0.f;  // the kernel's terms, the exact ones
         if (have) {
-            out_of = expf((softcap_exact(other_v[lane] * unbias, cap) - top) * inv_t);
+            out_of = expf((softcap_exact(other_v[lane], cap) - top) * inv_t);
             add = expf((other_z[lane] - top) * inv_t);
         }
         if (lane < kOthers) {
@@ -542,37 +628,49 @@ __global__ void __launch_bounds__(kThreads) distill_coeff_kernel(
 }
 
 // Softmax partials of the kept logits (few rows): block (s, r) takes split s of
-// row r; the largest capped logit, the sum at the temperature relative to it, and
-// the two largest raw logits of its threads' best.
+// row r, whole slices of 32 columns; the largest capped logit, the sum at the
+// temperature relative to it, and every slice's largest raw logit.
 constexpr int kSplitThreads = 256;
 __global__ void __launch_bounds__(kSplitThreads) distill_split_kernel(
     const float* z, int64_t ld, int64_t V, float cap, float inv_t,
-    const int* pos, Partial* __restrict__ part, int S) {
+    const int* pos, Partial* __restrict__ part, float* __restrict__ smax, int S) {
     tc::grid_dep_wait();
     tc::grid_dep_trigger();
     const int64_t r = blockIdx.y;
     const int i = pos[r], sp = blockIdx.x;
     if (i < 0) return;
-    const int64_t v0 = V * sp / S, v1 = V * (sp + 1) / S;
+    const int64_t n_sl = (V + 31) / 32;
+    const int64_t v0 = 32 * (n_sl * sp / S), v1 = min(V, 32 * (n_sl * (sp + 1) / S));
     const float* zr = z + r * ld;
-    RowState st;
-    st.init();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* sm = smax + (int64_t)i * slice_columns(V);
     float m = -INFINITY, s = 0.f;
     bool bad = false;  // a NaN logit
-    for (int64_t vb = v0 + threadIdx.x; vb < v1; vb += 8 * kSplitThreads) {
-        float x[8], top = -INFINITY;
+    for (int64_t base = v0; base < v1; base += 8 * kSplitThreads) {
+        const int64_t vb = base + threadIdx.x;
+        float x[8], y[8], top = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = vb + k * kSplitThreads < v1 ? zr[vb + k * kSplitThreads] : -INFINITY;
+        // The warp's 8 slices' maxima: each level halves the values with the lanes;
+        // lane (a, b, c, ..) ends with slice 4 a + 2 b + c.
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = x[k];
+#pragma unroll
+        for (int n = 4, o = 16; n >= 1; n >>= 1, o >>= 1) {
+#pragma unroll
+            for (int k = 0; k < n; ++k) {
+                const float give = lane & o ? y[k] : y[k + n];
+                y[k] = fmaxf(lane & o ? y[k + n] : y[k], __shfl_xor_sync(0xffffffffu, give, o));
+            }
+        }
+        y[0] = fmaxf(y[0], __shfl_xor_sync(0xffffffffu, y[0], 2));
+        y[0] = fmaxf(y[0], __shfl_xor_sync(0xffffffffu, y[0], 1));
+        const int64_t col = base + 32 * warp + (int64_t)(lane >> 2) * kSplitThreads;
+        if ((lane & 3) == 0 && col < v1) sm[col / 32] = y[0];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int at = (int)(vb + k * kSplitThreads);
             bad |= x[k] != x[k];
             if (x[k] > -INFINITY) {
-                if (better(x[k], at, st.v1, st.i1)) {
-                    st.v2 = st.v1; st.i2 = st.i1; st.v1 = x[k]; st.i1 = at;
-                } else if (better(x[k], at, st.v2, st.i2)) {
-                    st.v2 = x[k]; st.i2 = at;
-                }
                 x[k] = softcap_exact(x[k], cap);
                 top = fmaxf(top, x[k]);
             }
@@ -589,8 +687,7 @@ __global__ void __launch_bounds__(kSplitThreads) distill_split_kernel(
         m = 0.f;
         s = nan_f();
     }
-    __shared__ Partial red[kSplitThreads / 32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ float2 red[kSplitThreads / 32];
     auto fold = [&](float om, float os) {
         const float nm = fmaxf(m, om);
         if (nm > -INFINITY) s = s * expf((m - nm) * inv_t) + os * expf((om - nm) * inv_t);
@@ -598,7 +695,6 @@ __global__ void __launch_bounds__(kSplitThreads) distill_split_kernel(
     };
 #pragma unroll
     for (int o = 1; o <= 16; o <<= 1) {
-        st.shfl_merge(o);
         const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
         const float am = lane & o ? om : m, as = lane & o ? os : s;
         const float bm = lane & o ? m : om, bs = lane & o ? s : os;
@@ -606,22 +702,15 @@ __global__ void __launch_bounds__(kSplitThreads) distill_split_kernel(
         s = as;
         fold(bm, bs);
     }
-    if (lane == 0) {
-        red[warp] = st.to_partial();
-        red[warp].m = m;
-        red[warp].s = s;
-    }
+    if (lane == 0) red[warp] = make_float2(m, s);
     __syncthreads();
     if (threadIdx.x != 0) return;
-    RowState all;
-    all.init();
     m = -INFINITY;
     s = 0.f;
-    for (int w = 0; w < kSplitThreads / 32; ++w) {
-        fold(red[w].m, red[w].s);
-        all.merge(-INFINITY, 0.f, red[w].v1, red[w].i1, red[w].v2, red[w].i2);
-    }
-    Partial p = all.to_partial();
+    for (int w = 0; w < kSplitThreads / 32; ++w) fold(red[w].x, red[w].y);
+    RowState none;
+    none.init();
+    Partial p = none.to_partial();
     p.m = m;
     p.s = s;
     part[(int64_t)i * S + sp] = p;
@@ -750,14 +839,14 @@ cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, in
                                     float cap, const __nv_bfloat16* h, const int* pos, int64_t M,
                                     const int32_t* ids, const void* tl, int t_type, int K,
                                     float inv_t, float unbias, float* kept, int64_t ld, float* zout,
-                                    const Partial* part, int S, const int* S_dev, const int* err,
-                                    float* loss, float* lse, cudaStream_t st) {
+                                    const Partial* part, int S, const int* S_dev, const float* smax,
+                                    const int* err, float* loss, float* lse, cudaStream_t st) {
     return with_type(t_type, [&](auto* tag) {
         using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
         auto* fn = bits == 4 ? distill_finalize_kernel<4, T> : distill_finalize_kernel<8, T>;
         return launch_after(fn, dim3((unsigned)M), dim3(kThreads), st, wq, sb, V, H, cap, h, pos, ids,
-                            static_cast<const T*>(tl), K, inv_t, unbias, kept, ld, zout, part, S, S_dev, err, loss,
-                            lse);
+                            static_cast<const T*>(tl), K, inv_t, unbias, kept, ld, zout, part, S, S_dev, smax,
+                            err, loss, lse);
     });
 }
 
@@ -775,9 +864,10 @@ cudaError_t launch_distill_coeff(int64_t V, float cap, const int* pos, int64_t M
 }
 
 cudaError_t launch_distill_split(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
-                                 const int* pos, int64_t M, Partial* part, cudaStream_t st) {
+                                 const int* pos, int64_t M, Partial* part, float* smax,
+                                 cudaStream_t st) {
     return launch_after(distill_split_kernel, dim3(kFewSplits, (unsigned)M), dim3(kSplitThreads), st, z, ld, V,
-                        cap, inv_t, pos, part, kFewSplits);
+                        cap, inv_t, pos, part, smax, kFewSplits);
 }
 
 cudaError_t launch_distill_from_logits(const float* kept, int64_t K, int64_t ld, int64_t V, float cap,

@@ -26,6 +26,10 @@ inline int64_t kept_columns(int64_t M, int64_t K, int64_t V) {
     return keeps_logits(M, V) ? kept_logits_at(K) + (V + 31) / 32 * 32 : K + kKeptExtra;
 }
 
+// The largest raw logit of every 32 vocab rows without the listed ones, per compact
+// row, in whole tiles of 256 vocab rows.
+__host__ __device__ inline int64_t slice_columns(int64_t V) { return (V + 255) / 256 * 8; }
+
 // What a tensor-core logit is multiplied by to take its mean error out.  Its
 // fp32 accumulation truncates: each of the H / 16 steps loses half an ulp of the
 // partial sum on average.  Over mantissas an ulp is 0.72 * 2^-23 of its value
@@ -46,15 +50,16 @@ cudaError_t launch_distill_finalize(const uint32_t* wq, SbView sb, int64_t V, in
                                     float cap, const __nv_bfloat16* h, const int* pos, int64_t M,
                                     const int32_t* ids, const void* tl, int t_type, int K,
                                     float inv_t, float unbias, float* kept, int64_t ld, float* zout,
-                                    const Partial* part, int S, const int* S_dev, const int* err,
-                                    float* loss, float* lse, cudaStream_t st);
+                                    const Partial* part, int S, const int* S_dev, const float* smax,
+                                    const int* err, float* loss, float* lse, cudaStream_t st);
 cudaError_t launch_distill_coeff(int64_t V, float cap, const int* pos, int64_t M,
                                  const int32_t* ids, const void* tl, int t_type, int K, float inv_t,
                                  const float* kept, int64_t ld_kept, const float* lse,
                                  const float* dloss, float* geff, __half* coeff, int64_t ld,
                                  int64_t v_begin, int64_t chunk, cudaStream_t st);
 cudaError_t launch_distill_split(const float* z, int64_t ld, int64_t V, float cap, float inv_t,
-                                 const int* pos, int64_t M, Partial* part, cudaStream_t st);
+                                 const int* pos, int64_t M, Partial* part, float* smax,
+                                 cudaStream_t st);
 cudaError_t launch_distill_from_logits(const float* kept, int64_t K, int64_t ld, int64_t V, float cap,
                                        float inv_t, float unbias, const int* rows, const int* count, int64_t M,
                                        const float* lse, const float* dloss, float* geff, __half* coeff,

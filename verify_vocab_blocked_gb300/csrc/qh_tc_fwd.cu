@@ -85,6 +85,7 @@ constexpr int B_BYTES = BNH * BK * 2;  // this CTA's half of the dequantized til
 constexpr uint32_t kIdesc = tc::idesc_f16_f32(BMU, BN, false, false);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint16_t kPairMask = 0x3;
+static_assert(BN == 8 * 32, "a tile's slice maxima are one 32-byte store");
 
 // One ring of NS stages, each the TMA inputs (h tile + packed half-tile) and
 // the dequantized half-tile made from them: a stage's B slot is free again
@@ -149,8 +150,10 @@ __device__ __forceinline__ void unit_coords(const Work& w, int vt_begin, int u, 
 // EPI_FILTER: EPI_COEFF plus the coefficient filter (blocks of 32 rows x 32
 //             vocab rows below filter_eps are written as zeros; a.kbits).
 // EPI_DISTILL: EPI_SOFTMAX at a temperature, with each row's listed vocab rows
-//             (a.sid) left out of the sum and of the candidates: the finalize
-//             adds their terms from exact fp32 logits.
+//             (a.sid) left out of the sum: the finalize adds their terms from
+//             exact fp32 logits.  No argmax candidates; every slice's largest
+//             logit is written (a.smax), from which the finalize finds the largest
+//             others wherever they lie.
 // EPI_DCOEFF: EPI_COEFF at a temperature (lse is of the scaled logits).
 constexpr int EPI_SOFTMAX = 0, EPI_COEFF = 1, EPI_FILTER = 2, EPI_DISTILL = 3, EPI_DCOEFF = 4;
 
@@ -551,9 +554,19 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                 const bool zero_half = kCoeff && a.skip != nullptr &&
                                        skip_half(2 * mt + (int)rank, vt);
                 float tz = -INFINITY;  // the tile's maximum of z (blockMax)
+                float sm[BN / 32];     // EPI_DISTILL: the slices' raw maxima, the last at the end
+                if constexpr (EPI == EPI_DISTILL) {
+#pragma unroll
+                    for (int k = 0; k < BN / 32; ++k) sm[k] = -INFINITY;
+                }
 #pragma unroll 1
                 for (int c = 0; c < BN / 32; ++c) {
                     const int64_t col0 = (int64_t)vt * BN + c * 32;
+                    if constexpr (EPI == EPI_DISTILL) {  // (constant indices: registers)
+#pragma unroll
+                        for (int k = 0; k + 1 < BN / 32; ++k) sm[k] = sm[k + 1];
+                        sm[BN / 32 - 1] = -INFINITY;
+                    }
                     if (kCoeff && zero_half) {
                         if (i < a.coeff_rows) {
                             __half* dst = a.coeff + (int64_t)i * a.coeff_ld +
@@ -637,7 +650,7 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                                 for (int j = 0; j < 32; ++j)
                                     if (out_cols >> j & 1u) x[j] = -INFINITY;
                             }
-                            if (zrow != nullptr) {  // few rows: the logits are kept
+                            if (zrow != nullptr) {  // the logits are kept for the backward
 #pragma unroll
                                 for (int q = 0; q < 4; ++q) {
                                     uint32_t o[8];
@@ -657,19 +670,23 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                             for (int j = 0; j < 32; ++j)
                                 if (j < nvalid) rmax = fmaxf(rmax, x[j]);
                         }
-                        if (EPI == EPI_DISTILL && rmax == -INFINITY) continue;  // nothing left
-                        // Lowest column of the slice holding its maximum.  No
-                        // guard is needed: the column that set rmax is valid and
-                        // lies below every padding column.
-                        int jb = 31;
+                        if constexpr (EPI == EPI_DISTILL) {
+                            if (rmax == -INFINITY) continue;  // nothing left
+                            sm[BN / 32 - 1] = rmax;
+                        } else {
+                            // Lowest column of the slice holding its maximum.  No
+                            // guard is needed: the column that set rmax is valid and
+                            // lies below every padding column.
+                            int jb = 31;
 #pragma unroll
-                        for (int j = 30; j >= 0; --j) jb = x[j] == rmax ? j : jb;
-                        jb = min(jb, nvalid - 1);  // (no match at all: NaN logits)
-                        // argmax candidates: the maxima of the two slices with the
-                        // largest raw logit
-                        const int ci = (int)col0 + jb;
-                        if (better(rmax, ci, v1, i1)) { v2 = v1; i2 = i1; v1 = rmax; i1 = ci; }
-                        else if (better(rmax, ci, v2, i2)) { v2 = rmax; i2 = ci; }
+                            for (int j = 30; j >= 0; --j) jb = x[j] == rmax ? j : jb;
+                            jb = min(jb, nvalid - 1);  // (no match at all: NaN logits)
+                            // argmax candidates: the maxima of the two slices with the
+                            // largest raw logit
+                            const int ci = (int)col0 + jb;
+                            if (better(rmax, ci, v1, i1)) { v2 = v1; i2 = i1; v1 = rmax; i1 = ci; }
+                            else if (better(rmax, ci, v2, i2)) { v2 = rmax; i2 = ci; }
+                        }
                         // soft cap z = cap * tanh(x / cap) = cap - 2 cap / (exp(2x/cap) + 1)
                         float zmax = rmax;
                         if (cap > 0.f) {
@@ -693,6 +710,14 @@ __global__ void __launch_bounds__(Warps<BITS>::kThreads, 1) tc_fwd_kernel(
                         s = s * tc::ex2_approx((m - mn) * l2e) + acc;
                         m = mn;
                         tz = fmaxf(tz, zmax);
+                    }
+                }
+                if constexpr (EPI == EPI_DISTILL) {
+                    if (row_ok) {
+                        uint32_t o[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(sm[k]);
+                        tc::st_global_v8(a.smax + (int64_t)i * a.smax_ld + 8 * vt, o);
                     }
                 }
                 if (!kCoeff && a.bmax != nullptr && row_ok)

@@ -91,12 +91,17 @@ struct TcFwdArgs {
     // that the softmax epilogue leaves out; unbias: see distill_unbias.
     // zout (NULL: none): the raw logits, -inf at the left-out rows, at
     // zout[original row * zout_ld + vocab row], written in whole blocks of 32.
+    // smax: the largest raw logit of each 32-column slice without the left-out rows
+    // (-inf: none), at smax[compact row * smax_ld + vocab row / 32], written in whole
+    // tiles of 8.
     float l2e;
     float unbias;
     float* zout;
     int64_t zout_ld;
     const int* sid;
     int sid_ld;
+    float* smax;
+    int64_t smax_ld;
     // Set by launch_tc_fwd: the scale and bias tables are staged by TMA.
     int sb_tma;
 };
