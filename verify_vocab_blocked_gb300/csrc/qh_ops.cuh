@@ -71,11 +71,6 @@ __device__ __forceinline__ void store8_as(void* p, int64_t i, int type, const fl
     else if (type == kSbBf16) store8(static_cast<__nv_bfloat16*>(p) + i, v);
     else store8(static_cast<__half*>(p) + i, v);
 }
-__device__ __forceinline__ void store_as(void* p, int64_t i, int type, float v) {
-    if (type == kSbF32) static_cast<float*>(p)[i] = v;
-    else if (type == kSbBf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
 
 // Two fp32 lanes per instruction (one issue slot for two products or sums).
 __device__ __forceinline__ unsigned long long f2_bits(float2 a) {
