@@ -5,9 +5,9 @@
 Tokens are looked up in the packed 4-bit table, a small trainable block stands
 for the model's body, the final norm makes the head's hidden states, and the
 same table scores them against a teacher's top logits.  The backward runs the
-distillation's gradient, the norm's and the lookup's, whose table gradient is
-added into one float32 [V, H] buffer (where qhead.bwd_dw adds a trainable
-head's own).  Synthetic data; prints the loss as the body learns.
+distillation's gradient into h (the table as a head is frozen: that loss has no
+gradient into it), the norm's and the lookup's, whose table gradient is added
+into a float32 [V, H] buffer.  Synthetic data; prints the loss as the body learns.
 """
 import argparse
 import os

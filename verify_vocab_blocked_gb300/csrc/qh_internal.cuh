@@ -18,7 +18,7 @@ void set_error(const std::string& msg);
 // split's vocab rows (m = max z, s = sum exp(z - m)) and two argmax candidates
 // with their vocab indices (the split's two best raw logits; the tensor-core
 // kernel's are the maxima of its two best 32-column slices; empty entries hold
-// v = -inf, i = INT32_MAX).  status: 0, or the code of a bounded wait that
+// v = -inf, i = INT32_MAX; the distillation's records have none).  status: 0, or the code of a bounded wait that
 // expired in the CTA that wrote the record (the finalize then poisons the row).
 struct __align__(32) Partial {
     float m, s, v1, v2;
