@@ -1,6 +1,7 @@
 """Tensors of another device than the one whose stream the kernels are launched on
 are refused before any allocation or call: host tensors that are otherwise valid,
-and (with the current device a stand-in) a second GPU's."""
+and (with the current device a stand-in) a second GPU's; so is a head whose parts are
+on two devices or do not fit one another."""
 import pytest
 import torch
 
@@ -58,6 +59,16 @@ def test_a_head_of_two_devices():
         split.c()
     with pytest.raises(ValueError, match="one device"):
         qhead.embed(split, torch.zeros(M, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("rows,groups", [(1000, 3), (999, 4), (1000, 8)])
+def test_scales_that_do_not_cover_the_rows(rows, groups):
+    """Too few would be read past their end, another grouping in the wrong places."""
+    hd = _inputs()["head"]
+    part = torch.zeros(rows, groups).half()
+    for head in (qhead.Head(hd.wq, part, hd.biases, 4), qhead.Head(hd.wq, hd.scales, part, 4)):
+        with pytest.raises(ValueError, match=r"shape \[1000, 4\]"):
+            head.c()
 
 
 def test_stream_handles(monkeypatch):

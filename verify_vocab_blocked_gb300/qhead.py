@@ -178,8 +178,12 @@ class Head:
             raise ValueError("scales and biases must share one type: float16, bfloat16 or "
                              "float32")
         V, words = wq.shape
+        H = words * 32 // bits
+        groups = H // self.group if self.group > 0 else 0
+        if scales.numel() != V * groups or biases.numel() != V * groups:
+            raise ValueError(f"scales and biases must have shape [{V}, {groups}]")
         return CHead(wq.data_ptr(), scales.data_ptr(), biases.data_ptr(), V,
-                     words * 32 // bits, bits, self.group, code, self.softcap)
+                     H, bits, self.group, code, self.softcap)
 
     @staticmethod
     def from_numpy(wq, scales, biases, bits, group=64, softcap=0.0, device="cuda",
