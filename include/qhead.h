@@ -460,6 +460,73 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
                       const uint8_t* mask, const float* kept, const float* lse, const float* dloss,
                       void* dh, void* workspace, size_t workspace_bytes, void* stream);
 
+/* 8-bit floats (e4m3: 4 exponent bits, 3 mantissa bits, finite up to 448), where a
+ * call says that it takes them. */
+#define QHEAD_E4M3 3
+
+/* Activations of qhead_linear: z; max(z, 0); z / (1 + exp(-z)); z Phi(z) with the
+ * normal distribution function; and its form with tanh,
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+#define QHEAD_ACT_NONE 0
+#define QHEAD_ACT_RELU 1
+#define QHEAD_ACT_SILU 2
+#define QHEAD_ACT_GELU 3
+#define QHEAD_ACT_GELU_TANH 4
+
+/*
+ * Matrix product with bias, activation and residual in its epilogue (no
+ * counterpart on the pages: the block between the norm and the head, such as a
+ * draft head's h + silu(W h + b)):
+ *     z[m, n] = x_scale[m] * w_scale[n] * sum_k x[m, k] * weight[n, k] + bias[n]
+ *     y[m, n] = act(z[m, n]) + residual[m, n]
+ * accumulated and finished in fp32, rounded once.
+ *   x         device, [M, K] of type dtype, row stride ldx >= K elements.
+ *   weight    device, [N, K] of type dtype, row stride ldw >= K elements.
+ *   dtype     QHEAD_BF16, QHEAD_F16, or QHEAD_E4M3 with x_scale and w_scale.
+ *   K, N      >= 1 and at most 2^24.
+ *   x_scale, w_scale  device, float [M] and [N] for QHEAD_E4M3, else NULL.
+ *   bias      device, [N] of type bias_dtype, or NULL.
+ *   residual  device, [M, N] of type res_dtype, row stride ldr >= N, or NULL.
+ *   y         device, [M, N] contiguous, of type y_dtype (bias, residual and y:
+ *             QHEAD_F16, QHEAD_BF16 or QHEAD_F32 each).
+ *   pre       device, fp16 [M, N] contiguous, or NULL: z, for qhead_linear_bwd,
+ *             saturated to the finite range (there act's derivative is what it
+ *             is at the range's ends).
+ *   workspace device, >= qhead_linear_workspace(...) bytes, 256-byte aligned
+ *             (may be NULL when that is 0).
+ * Every pointer is aligned to its elements.  x and weight with 16-byte aligned
+ * starts and row strides of whole 16 bytes are read where they lie; others are
+ * first copied to the workspace.  M == 0 returns QHEAD_OK.  A kernel wait that
+ * expires (see above) makes the outputs that depend on it NaN.
+ */
+size_t qhead_linear_workspace(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K,
+                              const void* weight, int64_t ldw, int64_t N);
+int qhead_linear(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, const void* weight,
+                 int64_t ldw, int64_t N, const float* x_scale, const float* w_scale,
+                 const void* bias, int bias_dtype, int act, const void* residual, int res_dtype,
+                 int64_t ldr, void* y, int y_dtype, void* pre, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/*
+ * The gradient of qhead_linear (the residual's is dy itself):
+ *     dz = dy * act'(z);  dx = dz * weight;  dweight = dz^T * x;  dbias = sum_m dz
+ *   dtype     QHEAD_BF16 or QHEAD_F16: x, weight and the outputs.  dz is rounded
+ *             to it as an operand of the two products (not for dbias).
+ *   dy        device, [M, N] of type dy_dtype (any of the three), row stride ldy >= N.
+ *   pre       the forward's; may be NULL when act is QHEAD_ACT_NONE.
+ *   dx        device, [M, K] contiguous, or NULL (not wanted).
+ *   dweight   device, [N, K] contiguous, or NULL.
+ *   dbias     device, [N], or NULL.
+ *   workspace device, >= qhead_linear_bwd_workspace(...) bytes, 256-byte aligned.
+ * M == 0 writes zeros to dweight and dbias.  Deterministic.
+ */
+size_t qhead_linear_bwd_workspace(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K,
+                                  const void* weight, int64_t ldw, int64_t N);
+int qhead_linear_bwd(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K,
+                     const void* weight, int64_t ldw, int64_t N, const void* dy, int dy_dtype,
+                     int64_t ldy, const void* pre, int act, void* dx, void* dweight, void* dbias,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* Message for the last error on the calling thread ("" if none).  The
  * pointer stays valid until the thread's next qhead_* call. */
 const char* qhead_last_error(void);
@@ -480,8 +547,8 @@ void qhead_time_next_head_kernel(void* start, void* stop);
 /*
  * Test instrumentation (no counterpart on the pages): arm a one-shot switch
  * on the calling thread.  The thread's next forward or backward call (the
- * entry points listed for qhead_time_next_head_kernel) launches its
- * pipelined head kernel with the TMA producer issuing no loads,
+ * entry points listed for qhead_time_next_head_kernel, qhead_linear and
+ * qhead_linear_bwd) launches its pipelined kernel with the TMA producer issuing no loads,
  * so the consumers' bounded waits expire and the call ends as described under
  * "Kernel time limits" (about 2 s later, without a fault).  armed = 0
  * disarms.  Exists so that the time-limit path can be

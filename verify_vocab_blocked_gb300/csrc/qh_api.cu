@@ -10,6 +10,7 @@
 #include <float.h>
 #include <stdio.h>
 
+#include <algorithm>
 #include <map>
 #include <mutex>
 #include <string>
@@ -19,6 +20,7 @@
 #include "qh_distill.cuh"
 #include "qh_few.cuh"
 #include "qh_internal.cuh"
+#include "qh_linear.cuh"
 #include "qh_ops.cuh"
 #include "qh_tmap.h"
 
@@ -27,6 +29,10 @@ static_assert(QHEAD_F16 == QHEAD_SB_F16 && QHEAD_BF16 == QHEAD_SB_BF16 && QHEAD_
 static_assert(QHEAD_SB_F16 == qh::kSbF16 && QHEAD_SB_BF16 == qh::kSbBf16 &&
                   QHEAD_SB_F32 == qh::kSbF32,
               "scale/bias element type codes");
+static_assert(QHEAD_E4M3 == qh::kE4m3 && QHEAD_ACT_NONE == qh::kActNone && QHEAD_ACT_RELU == qh::kActRelu &&
+                  QHEAD_ACT_SILU == qh::kActSilu && QHEAD_ACT_GELU == qh::kActGelu &&
+                  QHEAD_ACT_GELU_TANH == qh::kActGeluTanh,
+              "activation codes");
 
 namespace {
 
@@ -392,6 +398,68 @@ int check_norm(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t H, co
     if (misaligned(x, qh::type_bytes(x_dtype)) || misaligned(w, qh::type_bytes(w_dtype)))
         return fail(QHEAD_EINVAL, "x and weight must be aligned to their elements");
     return QHEAD_OK;
+}
+
+// Where the product's operands are read: at the caller's, or as padded copies at
+// these offsets of the workspace.
+struct LinearPlan {
+    bool pad_x = false, pad_w = false;
+    int64_t ldx = 0, ldw = 0;          // of what the kernels read
+    size_t off_x = 0, off_w = 0;
+    // backward
+    int64_t ldz = 0;
+    size_t off_dz = 0, off_part = 0, total = 0;
+};
+
+// 16-byte rows (a TMA map's rule).
+bool tma_rows(const void* p, int64_t ld, int bytes) { return !misaligned(p, 16) && ld * bytes % 16 == 0; }
+
+int check_linear(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, const void* w, int64_t ldw, int64_t N,
+                 bool bwd) {
+    const int rc = check_rows(M);
+    if (rc) return rc;
+    if (dtype != QHEAD_F16 && dtype != QHEAD_BF16 && (bwd || dtype != QHEAD_E4M3))
+        return fail(QHEAD_EUNSUPPORTED, bwd ? "dtype must be QHEAD_F16 or QHEAD_BF16"
+                                            : "dtype must be QHEAD_F16, QHEAD_BF16 or QHEAD_E4M3");
+    const int64_t most = (int64_t)1 << 24;
+    if (K < 1 || N < 1 || K > most || N > most) return fail(QHEAD_EINVAL, "K and N must be in [1, 2^24]");
+    if (ldx < K || ldw < K) return fail(QHEAD_EINVAL, "ldx and ldw must be at least K");
+    if (ldx > (int64_t)1 << 36 || ldw > (int64_t)1 << 36) return fail(QHEAD_EINVAL, "row stride too large");
+    // (the tiles of any of the three products are counted in 32 bits)
+    const auto tiles = [](int64_t a, int64_t b) { return (a + 127) / 128 * ((b + 127) / 128); };
+    if (std::max(tiles(M, N), std::max(tiles(M, K), tiles(N, K))) >= (int64_t)1 << 30)
+        return fail(QHEAD_EINVAL, "M, K and N too large together");
+    if (!w || (M > 0 && !x)) return fail(QHEAD_EINVAL, "x and weight are required");
+    const int bytes = dtype == QHEAD_E4M3 ? 1 : 2;
+    if (misaligned(x, bytes) || misaligned(w, bytes))
+        return fail(QHEAD_EINVAL, "x and weight must be aligned to their elements");
+    return QHEAD_OK;
+}
+
+LinearPlan plan_of_linear(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, const void* w, int64_t ldw,
+                          int64_t N, bool bwd) {
+    LinearPlan p;
+    const int bytes = dtype == QHEAD_E4M3 ? 1 : 2;
+    const auto pitch = [&](int64_t n) { return (int64_t)align_up((size_t)n * bytes, 16) / bytes; };
+    p.pad_x = !tma_rows(x, ldx, bytes);
+    p.pad_w = !tma_rows(w, ldw, bytes);
+    p.ldx = p.pad_x ? pitch(K) : ldx;
+    p.ldw = p.pad_w ? pitch(K) : ldw;
+    size_t at = 0;
+    const auto take = [&](size_t n) {
+        const size_t o = at;
+        at = align_up(at + n, 256);
+        return o;
+    };
+    if (p.pad_x) p.off_x = take((size_t)M * p.ldx * bytes);
+    if (p.pad_w) p.off_w = take((size_t)N * p.ldw * bytes);
+    if (bwd) {
+        p.ldz = pitch(N);
+        p.off_dz = take((size_t)M * p.ldz * bytes);
+        p.off_part = take(sizeof(float) * (size_t)qh::dz_chunks(M, N) * N);
+    }
+    p.total = at;
+    return p;
 }
 
 int cuda_fail(cudaError_t e, const char* what) {
@@ -924,6 +992,123 @@ int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int
                       dx, dweight, dbias, static_cast<float*>(workspace), grid};
     const cudaError_t e = qh::launch_norm_bwd(a, st);
     return e ? cuda_fail(e, "layer_norm_bwd") : QHEAD_OK;
+}
+
+size_t qhead_linear_workspace(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, const void* weight,
+                              int64_t ldw, int64_t N) {
+    g_err.clear();
+    if (check_linear(x, dtype, ldx, M, K, weight, ldw, N, false)) return (size_t)-1;
+    return M == 0 ? 0 : plan_of_linear(x, dtype, ldx, M, K, weight, ldw, N, false).total;
+}
+
+size_t qhead_linear_bwd_workspace(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, const void* weight,
+                                  int64_t ldw, int64_t N) {
+    g_err.clear();
+    if (check_linear(x, dtype, ldx, M, K, weight, ldw, N, true)) return (size_t)-1;
+    return M == 0 ? 0 : plan_of_linear(x, dtype, ldx, M, K, weight, ldw, N, true).total;
+}
+
+// The operand that the kernels read: the caller's, or its padded copy, made first.
+static cudaError_t linear_operand(const void* p, int64_t ld, int64_t rows, int64_t cols, int dtype, bool pad,
+                                  void* ws, size_t off, int64_t ldp, bool k_major, cudaStream_t st,
+                                  qh::LinOperand* o) {
+    *o = qh::LinOperand{pad ? at<void>(ws, off) : p, pad ? ldp : ld, k_major};
+    return pad ? qh::launch_pad_rows(p, ld, rows, cols, dtype == QHEAD_E4M3 ? 1 : 2, const_cast<void*>(o->p), ldp, st)
+               : cudaSuccess;
+}
+
+int qhead_linear(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, const void* weight, int64_t ldw,
+                 int64_t N, const float* x_scale, const float* w_scale, const void* bias, int bias_dtype, int act,
+                 const void* residual, int res_dtype, int64_t ldr, void* y, int y_dtype, void* pre, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    HookScope scope;
+    int rc = check_linear(x, dtype, ldx, M, K, weight, ldw, N, false);
+    if (rc) return rc;
+    if ((dtype == QHEAD_E4M3) != (w_scale != nullptr) || (M > 0 && (dtype == QHEAD_E4M3) != (x_scale != nullptr)))
+        return fail(QHEAD_EINVAL, "x_scale and w_scale belong to QHEAD_E4M3, which needs both");
+    if (act < QHEAD_ACT_NONE || act > QHEAD_ACT_GELU_TANH) return fail(QHEAD_EUNSUPPORTED, "unknown activation");
+    if (!dtype_ok(y_dtype) || (bias && !dtype_ok(bias_dtype)) || (residual && !dtype_ok(res_dtype)))
+        return fail(QHEAD_EUNSUPPORTED, "bias, residual and y must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+    if (residual && ldr < N) return fail(QHEAD_EINVAL, "ldr < N");
+    if (M == 0) return QHEAD_OK;
+    if (!y) return fail(QHEAD_EINVAL, "y is required");
+    if (misaligned(y, qh::type_bytes(y_dtype)) || misaligned(pre, 2) || misaligned(x_scale, 4) ||
+        misaligned(w_scale, 4) || (bias && misaligned(bias, qh::type_bytes(bias_dtype))) ||
+        (residual && misaligned(residual, qh::type_bytes(res_dtype))))
+        return fail(QHEAD_EINVAL, "every pointer must be aligned to its elements");
+    const LinearPlan p = plan_of_linear(x, dtype, ldx, M, K, weight, ldw, N, false);
+    if (p.total && (rc = check_workspace(workspace, workspace_bytes, p.total))) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    qh::LinArgs a{};
+    cudaError_t e = linear_operand(x, ldx, M, K, dtype, p.pad_x, workspace, p.off_x, p.ldx, true, st, &a.a);
+    if (!e) e = linear_operand(weight, ldw, N, K, dtype, p.pad_w, workspace, p.off_w, p.ldw, true, st, &a.b);
+    if (e) return cuda_fail(e, "linear operands");
+    a.type = dtype;
+    a.M = M, a.N = N, a.K = K;
+    a.a_scale = x_scale, a.b_scale = w_scale;
+    a.bias = bias, a.bias_type = bias_dtype, a.act = act;
+    a.res = residual, a.res_type = res_dtype, a.ldr = ldr;
+    a.y = y, a.y_type = y_dtype, a.pre = static_cast<__half*>(pre);
+    a.stall = take_stall();
+    e = qh::launch_linear(a, qh::plan_linear(a, qh::device_sms()), st);
+    return e ? cuda_fail(e, "linear") : QHEAD_OK;
+}
+
+int qhead_linear_bwd(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, const void* weight, int64_t ldw,
+                     int64_t N, const void* dy, int dy_dtype, int64_t ldy, const void* pre, int act, void* dx,
+                     void* dweight, void* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    HookScope scope;
+    int rc = check_linear(x, dtype, ldx, M, K, weight, ldw, N, true);
+    if (rc) return rc;
+    if (!dtype_ok(dy_dtype)) return fail(QHEAD_EUNSUPPORTED, "dy_dtype must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+    if (act < QHEAD_ACT_NONE || act > QHEAD_ACT_GELU_TANH) return fail(QHEAD_EUNSUPPORTED, "unknown activation");
+    if (ldy < N) return fail(QHEAD_EINVAL, "ldy < N");
+    if (misaligned(dx, 2) || misaligned(dweight, 2) || misaligned(dbias, 2) || misaligned(pre, 2) ||
+        misaligned(dy, qh::type_bytes(dy_dtype)))
+        return fail(QHEAD_EINVAL, "every pointer must be aligned to its elements");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        cudaError_t e = dweight ? cudaMemsetAsync(dweight, 0, 2 * (size_t)N * (size_t)K, st) : cudaSuccess;
+        if (!e && dbias) e = cudaMemsetAsync(dbias, 0, 2 * (size_t)N, st);
+        return e ? cuda_fail(e, "linear_bwd zero") : QHEAD_OK;
+    }
+    if (!dy || (act != QHEAD_ACT_NONE && !pre)) return fail(QHEAD_EINVAL, "dy (and, with an activation, pre) is required");
+    const LinearPlan p = plan_of_linear(x, dtype, ldx, M, K, weight, ldw, N, true);
+    if ((rc = check_workspace(workspace, workspace_bytes, p.total))) return rc;
+    const int stall = take_stall();
+    // dy itself is the operand where nothing changes it and its rows can be copied by TMA
+    const bool as_is = act == QHEAD_ACT_NONE && dy_dtype == dtype && tma_rows(dy, ldy, 2);
+    const bool products = dx || dweight;
+    const qh::LinOperand dz = as_is ? qh::LinOperand{dy, ldy, true} : qh::LinOperand{at<void>(workspace, p.off_dz), p.ldz, true};
+    cudaError_t e = cudaSuccess;
+    if ((products && !as_is) || dbias) {
+        qh::DzArgs d{dy, dy_dtype, ldy, static_cast<const __half*>(pre), act, M, N,
+                     products && !as_is ? const_cast<void*>(dz.p) : nullptr, p.ldz, dtype, dbias,
+                     at<float>(workspace, p.off_part)};
+        if ((e = qh::launch_dz(d, st))) return cuda_fail(e, "linear_bwd dz");
+    }
+    qh::LinArgs a{};
+    a.type = a.y_type = dtype;
+    a.stall = stall;
+    a.a = dz;
+    if (dx) {
+        if ((e = linear_operand(weight, ldw, N, K, dtype, p.pad_w, workspace, p.off_w, p.ldw, false, st, &a.b)))
+            return cuda_fail(e, "linear_bwd weight");
+        a.M = M, a.N = K, a.K = N, a.y = dx;
+        if ((e = qh::launch_linear(a, qh::plan_linear(a, qh::device_sms()), st))) return cuda_fail(e, "linear_bwd dx");
+    }
+    if (dweight) {
+        if ((e = linear_operand(x, ldx, M, K, dtype, p.pad_x, workspace, p.off_x, p.ldx, false, st, &a.b)))
+            return cuda_fail(e, "linear_bwd x");
+        a.a = dz;
+        a.a.k_major = false;
+        a.M = N, a.N = K, a.K = M, a.y = dweight;
+        if ((e = qh::launch_linear(a, qh::plan_linear(a, qh::device_sms()), st)))
+            return cuda_fail(e, "linear_bwd dweight");
+    }
+    return QHEAD_OK;
 }
 
 int64_t qhead_distill_kept(const qhead_head* head, int64_t M, int64_t K) {

@@ -1,0 +1,640 @@
+// qh_linear.cu -- matrix product with bias, activation and residual in its
+// epilogue, on the fifth-generation tensor cores.
+//
+//     D[m, n] = sum_k A[m, k] B[n, k]
+//     z = D a_scale[m] b_scale[n] + bias[n];   y = act(z) + res[m, n]
+//
+// A and B are bf16, fp16 or (K-major only) e4m3, fp32 accumulate; both may be
+// K-major (the forward) or MN-major (the gradients: dx = dz W takes W down its
+// rows, dW = dz^T x both operands).  Everything after the product is fp32 and
+// rounded once.
+//
+// Two kernels:
+//   * pairs: CTA pairs (cta_group::2), 256 x BN output tiles, persistent; one
+//     thread streams both operands' 128-byte-swizzled tiles by TMA, one issues the
+//     MMAs into two accumulators in turn, eight warps run the epilogue of one
+//     while the other fills;
+//   * few: for few rows of A (the tokens), whose time is reading B (the weights)
+//     once: the weights' rows are the MMA's 128, the tokens its 16 to 128 columns,
+//     and the CTAs of a cluster share a tile's reduction, so that a small weight
+//     matrix is read by all SMs; their partial tiles are summed in rank order
+//     through distributed shared memory (deterministic).
+//
+// A bounded wait that expires makes the tile NaN.
+#include "qh_linear.cuh"
+#include "qh_tc.cuh"
+#include "qh_tmap.h"
+
+#include <algorithm>
+
+namespace qh {
+
+namespace {
+
+constexpr int kRowBytes = 128;   // bytes of a K-major row a stage: 64 or 128 elements
+constexpr uint16_t kPairMask = 0x3;
+
+// ----------------------------------------------------------------- epilogue
+
+__device__ __forceinline__ float activate(float z, int act) {
+    switch (act) {
+        case kActRelu: return z < 0.f ? 0.f : z;  // (keeps NaN)
+        case kActSilu: return __fdividef(z, 1.f + __expf(-z));
+        case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678f));
+        case kActGeluTanh: {  // 0.5 (1 + tanh u) = 1 / (1 + exp(-2u))
+            const float u2 = 1.5957691216f * fmaf(0.044715f * z * z, z, z);
+            return __fdividef(z, 1.f + __expf(-u2));
+        }
+        default: return z;
+    }
+}
+
+// fp16 of the pre-activation, for the gradient: beyond fp16's range every
+// activation's derivative is what it is at the range's end, so that it saturates.
+__device__ __forceinline__ __half pre_of(float z) {
+    return __float2half_rn(z != z ? z : fminf(fmaxf(z, -65504.f), 65504.f));
+}
+
+__device__ __forceinline__ void put(void* p, int64_t i, int type, float v) {
+    if (type == kSbF32) static_cast<float*>(p)[i] = v;
+    else if (type == kSbBf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// What a kernel needs of LinArgs beside its tensor maps.
+struct Epi {
+    int64_t M, N;
+    const float* a_scale;
+    const float* b_scale;
+    const void* bias;
+    const void* res;
+    void* y;
+    __half* pre;
+    int64_t ldr;
+    int bias_type, act, res_type, y_type;
+};
+
+// One output of row m and column n, whose column's scale and bias are at hand.
+__device__ __forceinline__ void finish(const Epi& e, int64_t m, int64_t n, float v, float bs, float bias) {
+    if (e.a_scale) v *= e.a_scale[m];
+    v = fmaf(v, bs, bias);
+    const int64_t at = m * e.N + n;
+    if (e.pre) e.pre[at] = pre_of(v);
+    v = activate(v, e.act);
+    if (e.res) v += sb_elem(e.res, m * e.ldr + n, e.res_type);
+    put(e.y, at, e.y_type, v);
+}
+
+// ------------------------------------------------------------------- pairs
+
+template <int BN, bool AMN, bool BMN>
+struct PairLayout {
+    static constexpr int A_BYTES = 128 * kRowBytes;      // this CTA's 128 rows of A
+    static constexpr int B_BYTES = BN / 2 * kRowBytes;   // and its half of B's columns
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int NS = BN == 256 ? 6 : 8;
+    static constexpr int OFF_BAR = NS * STAGE;
+    static constexpr int BAR_BYTES = 8 * (2 * NS + 5) + 16;
+    static constexpr int OFF_T = (OFF_BAR + BAR_BYTES + 127) / 128 * 128;  // transposes
+    static constexpr int SMEM = OFF_T + 8 * 32 * 33 * 4 + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+constexpr int kPairThreads = 10 * 32;
+
+// The tiles in groups of 8 rows of tiles, columns outer: what the pairs work on at
+// a time is near-square, so that each operand's tiles are shared in L2.
+__device__ __forceinline__ void tile_of(int t, int n_mt, int n_nt, int& mt, int& nt) {
+    constexpr int G = 8;
+    const int per = G * n_nt, g = t / per, in = t - g * per;
+    const int rows = min(G, n_mt - g * G);
+    nt = in / rows;
+    mt = g * G + in - nt * rows;
+}
+
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_f8_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
+        "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
+        "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Descriptor of an operand at `addr`: K-major rows of 128 bytes in 8-row atoms, or
+// MN-major blocks of 64 elements 8 KB apart (64 rows of K each).
+template <bool MN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+    return MN ? tc::sdesc_sw128(addr, 8192, 1024) : tc::sdesc_sw128(addr, 0, 1024);
+}
+// Its advance (in 16 bytes) per MMA: 32 bytes of K, or 16 rows of K.
+template <bool MN>
+constexpr uint32_t kStep = MN ? 128u : 2u;
+
+template <int BN, bool AMN, bool BMN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                       const __grid_constant__ Epi e, int n_k, int step_k, uint32_t idesc, int f8, int stall) {
+    using L = PairLayout<BN, AMN, BMN>;
+    constexpr int NS = L::NS;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+    uint64_t* empty = full + NS;
+    uint64_t* accf = empty + NS;
+    uint64_t* acce = accf + 2;
+    uint64_t* mdrain = acce + 2;
+    uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(mdrain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sh + 1);
+    int* err = reinterpret_cast<int*>(tmem_base_sh + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_ctarank();
+    const int n_mt = (int)((e.M + 255) / 256), n_nt = (int)((e.N + BN - 1) / BN);
+    const int tiles = n_mt * n_nt;
+    const int first = (int)tc::cluster_id_x(), stride = (int)tc::nclusters_x();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&accf[i], 1);
+            tc::mbar_init(&acce[i], 16);
+        }
+        tc::mbar_init(mdrain, 1);
+        *abort_flag = 0;
+        *err = 0;
+        tc::fence_mbar_init();
+        tc::prefetch_tmap(&ta);
+        tc::prefetch_tmap(&tb);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc_pair(tmem_base_sh, 2 * BN);
+        tc::tmem_relinquish_pair();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    tc::tc_fence_after();
+    const uint32_t tmem_base = *tmem_base_sh;
+    tc::grid_dep_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, fills = 0;
+            bool ok = stall == 0;
+            const uint32_t full_lead = tc::mapa_shared(full, 0);
+            for (int t = first; t < tiles && ok; t += stride) {
+                int mt, nt;
+                tile_of(t, n_mt, n_nt, mt, nt);
+                const int m0 = mt * 256 + (int)rank * 128, n0 = nt * BN + (int)rank * (BN / 2);
+                for (int kk = 0; kk < n_k && ok; ++kk) {
+                    ok = tc::mbar_wait_cta(&empty[stage], phase ^ 1, abort_flag, err, tc::kErrTimeoutEmpty);
+                    if (!ok) break;
+                    // both CTAs' copies count on the even CTA's barrier
+                    if (rank == 0) tc::mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE);
+                    unsigned char* A = smem + stage * L::STAGE;
+                    unsigned char* B = A + L::A_BYTES;
+                    const uint32_t bar = full_lead + 8 * stage;
+                    const int k = kk * step_k;
+                    if constexpr (AMN) {
+                        tma_load_pair(A, &ta, bar, m0, k);
+                        tma_load_pair(A + 8192, &ta, bar, m0 + 64, k);
+                    } else {
+                        tma_load_pair(A, &ta, bar, k, m0);
+                    }
+                    if constexpr (BMN) {
+#pragma unroll
+                        for (int q = 0; q < BN / 128; ++q) tma_load_pair(B + q * 8192, &tb, bar, n0 + 64 * q, k);
+                    } else {
+                        tma_load_pair(B, &tb, bar, k, n0);
+                    }
+                    ++fills;
+                    if (++stage == NS) { stage = 0; phase ^= 1; }
+                }
+            }
+            // The last stages are consumed (their commits reach both CTAs) before the CTA exits.
+            for (uint32_t i = fills > NS ? fills - NS : 0; i < fills && ok; ++i)
+                ok = tc::mbar_wait_cta(&empty[i % NS], (i / NS) & 1, abort_flag, err, tc::kErrTimeoutEmpty);
+            // And on any path every copy has landed: the even CTA's barriers count both CTAs'.
+            if (rank == 0) tc::drain_ring(full, NS, fills, err);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, aphase = 0;
+            const uint64_t ad0 = operand_desc<AMN>(tc::smem_u32(smem));
+            const uint64_t bd0 = operand_desc<BMN>(tc::smem_u32(smem + L::A_BYTES));
+            bool ok = true;
+            for (int t = first; t < tiles && ok; t += stride) {
+                ok = tc::mbar_wait_cluster(&acce[buf], aphase ^ 1, abort_flag, err, tc::kErrTimeoutAccEmpty);
+                tc::tc_fence_after();
+                const uint32_t d = tmem_base + buf * BN;
+                for (int kk = 0; kk < n_k && ok; ++kk) {
+                    ok = tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint64_t ad = ad0 + (uint32_t)(stage * (L::STAGE >> 4));
+                    const uint64_t bd = bd0 + (uint32_t)(stage * (L::STAGE >> 4));
+                    if (!AMN && !BMN && f8) {
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            umma_f8_pair(d, ad + 2 * s, bd + 2 * s, idesc, (kk | s) != 0);
+                    } else {
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+                            tc::umma_f16_pair(d, ad + kStep<AMN> * s, bd + kStep<BMN> * s, idesc, (kk | s) != 0);
+                    }
+                    tc::umma_commit_pair(&empty[stage], kPairMask);
+                    if (++stage == NS) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+                tc::umma_commit_pair(&accf[buf], kPairMask);
+                if (++buf == 2) { buf = 0; aphase ^= 1; }
+            }
+            if (!ok) {
+                tc::umma_commit_pair(mdrain, 0x1);
+                tc::mbar_drain(mdrain, 0, err);
+            }
+        }
+    } else {
+        const int sub = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t acce_lead = tc::mapa_shared(acce, 0);
+        float* tr = reinterpret_cast<float*>(smem + L::OFF_T) + (warp - 2) * 32 * 33;
+        const float nan = __int_as_float(0x7fc00000);
+        int buf = 0;
+        uint32_t aphase = 0;
+        for (int t = first; t < tiles; t += stride) {
+            int mt, nt;
+            tile_of(t, n_mt, n_nt, mt, nt);
+            const int64_t m0 = (int64_t)mt * 256 + rank * 128 + sub * 32;
+            const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
+            tc::tc_fence_after();
+            const int rows = (int)min((int64_t)32, e.M - m0);  // (<= 0: none)
+            const uint32_t d = tmem_base + ((uint32_t)(sub * 32) << 16) + buf * BN + half * (BN / 2);
+#pragma unroll 1
+            for (int c = 0; c < BN / 64; ++c) {
+                uint32_t r[32];
+                tc::tmem_ld32(d + 32 * c, r);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) tr[lane * 33 + j] = ok ? __uint_as_float(r[j]) : nan;
+                __syncwarp();
+                const int64_t n = (int64_t)nt * BN + half * (BN / 2) + 32 * c + lane;
+                if (n < e.N) {
+                    const float bs = e.b_scale ? e.b_scale[n] : 1.f;
+                    const float bias = e.bias ? sb_elem(e.bias, n, e.bias_type) : 0.f;
+                    for (int i = 0; i < rows; ++i) finish(e, m0 + i, n, tr[i * 33 + lane], bs, bias);
+                }
+                __syncwarp();
+            }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(acce_lead + 8 * buf);
+            if (++buf == 2) { buf = 0; aphase ^= 1; }
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::cluster_sync();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc_pair(tmem_base, 2 * BN);
+    }
+}
+
+// --------------------------------------------------------------------- few
+
+constexpr int kFewThreads = 6 * 32;
+
+template <int T>
+struct FewLayout {
+    static constexpr int W_BYTES = 128 * kRowBytes;
+    static constexpr int X_BYTES = T * kRowBytes;
+    static constexpr int STAGE = W_BYTES + X_BYTES;
+    static constexpr int NS = T <= 32 ? 5 : T == 64 ? 4 : 3;  // two CTAs to an SM
+    static constexpr int OFF_BAR = NS * STAGE;
+    static constexpr int BAR_BYTES = 8 * (2 * NS + 2) + 16;
+    static constexpr int SMEM = OFF_BAR + BAR_BYTES + 1024;
+    static constexpr int TMEM = T < 32 ? 32 : T;
+    static_assert(T * 128 * 4 <= OFF_BAR, "the partial tile lies in the ring");
+    static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs to an SM");
+};
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// tw: the weights, whose rows (or, WMN, columns) are the tile's 128; tx: the tokens.
+// blockIdx.x: 128-row tile and rank in the cluster; blockIdx.y: token tile.
+template <int T, bool WMN>
+__global__ void __launch_bounds__(kFewThreads)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
+                      const __grid_constant__ Epi e, int n_k, int step_k, int split, uint32_t idesc, int f8,
+                      int stall) {
+    using L = FewLayout<T>;
+    constexpr int NS = L::NS;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+    uint64_t* empty = full + NS;
+    uint64_t* accf = empty + NS;
+    uint64_t* mdrain = accf + 1;
+    uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(mdrain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sh + 1);
+    int* err = reinterpret_cast<int*>(tmem_base_sh + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)blockIdx.x % split;  // (= the rank in the cluster of `split`)
+    const int n0 = (int)blockIdx.x / split * 128, m0 = (int)blockIdx.y * T;
+    const int k0 = (int)((int64_t)n_k * rank / split), k1 = (int)((int64_t)n_k * (rank + 1) / split);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 1);
+        }
+        tc::mbar_init(accf, 1);
+        tc::mbar_init(mdrain, 1);
+        *abort_flag = 0;
+        *err = 0;
+        tc::fence_mbar_init();
+        tc::prefetch_tmap(&tw);
+        tc::prefetch_tmap(&tx);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_base_sh, L::TMEM);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem_base = *tmem_base_sh;
+    tc::grid_dep_wait();
+
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0 && stall == 0) {
+            int stage = 0;
+            uint32_t phase = 0, fills = 0;
+            for (int kk = k0; kk < k1 && ok; ++kk) {
+                ok = tc::mbar_wait_cta(&empty[stage], phase ^ 1, abort_flag, err, tc::kErrTimeoutEmpty);
+                if (!ok) break;
+                tc::mbar_arrive_expect_tx(&full[stage], L::STAGE);
+                unsigned char* W = smem + stage * L::STAGE;
+                if constexpr (WMN) {
+                    tc::tma_load_2d(W, &tw, &full[stage], n0, kk * step_k);
+                    tc::tma_load_2d(W + 8192, &tw, &full[stage], n0 + 64, kk * step_k);
+                } else {
+                    tc::tma_load_2d(W, &tw, &full[stage], kk * step_k, n0);
+                }
+                tc::tma_load_2d(W + L::W_BYTES, &tx, &full[stage], kk * step_k, m0);
+                ++fills;
+                if (++stage == NS) { stage = 0; phase ^= 1; }
+            }
+            tc::drain_ring(full, NS, fills, err);  // (every copy has landed, on any path)
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            const uint64_t wd0 = operand_desc<WMN>(tc::smem_u32(smem));
+            const uint64_t xd0 = operand_desc<false>(tc::smem_u32(smem + L::W_BYTES));
+            for (int kk = k0; kk < k1 && ok; ++kk) {
+                ok = tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull);
+                if (!ok) break;
+                tc::tc_fence_after();
+                const uint64_t wd = wd0 + (uint32_t)(stage * (L::STAGE >> 4));
+                const uint64_t xd = xd0 + (uint32_t)(stage * (L::STAGE >> 4));
+                if (!WMN && f8) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) umma_f8(tmem_base, wd + 2 * s, xd + 2 * s, idesc, (kk - k0) | s);
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        tc::umma_f16(tmem_base, wd + kStep<WMN> * s, xd + 2 * s, idesc, (kk - k0) | s);
+                }
+                tc::umma_commit(&empty[stage]);
+                if (++stage == NS) { stage = 0; phase ^= 1; }
+            }
+            if (ok) {
+                tc::umma_commit(accf);
+            } else {
+                tc::umma_commit(mdrain);
+                tc::mbar_drain(mdrain, 0, err);
+            }
+        }
+    } else {
+        // Lane: a weight row; the accumulator's columns: tokens.  All MMAs, and with
+        // them all copies, are done when the accumulator is: the ring is free.
+        const int sub = warp & 3, row = sub * 32 + lane;
+        ok = tc::mbar_wait_cta(accf, 0, abort_flag, err, tc::kErrTimeoutAccFull);
+        tc::tc_fence_after();
+        float* part = reinterpret_cast<float*>(smem);
+        // (after a failed wait copies may be in flight into the ring: the flag tells the cluster)
+#pragma unroll 1
+        for (int c = 0; c < L::TMEM / 32; ++c) {
+            uint32_t r[32];
+            tc::tmem_ld32(tmem_base + ((uint32_t)(sub * 32) << 16) + 32 * c, r);
+            tc::tmem_wait_ld();
+            if (ok) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (32 * c + j < T) part[(32 * c + j) * 128 + row] = __uint_as_float(r[j]);
+            }
+        }
+        if (!ok && lane == 0) *abort_flag = tc::kErrTimeoutAccFull;
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (split > 1) tc::cluster_sync();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem_base, L::TMEM);
+    }
+    if (warp >= 2) {
+        const int row = (warp & 3) * 32 + lane;
+        const int64_t n = (int64_t)n0 + row;
+        const uint32_t part = tc::smem_u32(smem), flag = tc::smem_u32(const_cast<int*>(abort_flag));
+        uint32_t base[8];
+        bool bad = false;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            if (s < split) {
+                uint32_t f;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base[s]) : "r"(part), "r"(s));
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(f) : "r"(flag), "r"(s));
+                bad |= __float_as_int(ld_cluster(f)) != 0;
+            }
+        }
+        if (n < e.N) {
+            const float bs = e.b_scale ? e.b_scale[n] : 1.f;
+            const float bias = e.bias ? sb_elem(e.bias, n, e.bias_type) : 0.f;
+            const int rows = (int)min((int64_t)T, e.M - m0);
+            for (int t = rank; t < rows; t += split) {
+                float v[8], sum = 0.f;
+#pragma unroll
+                for (int s = 0; s < 8; ++s) v[s] = s < split ? ld_cluster(base[s] + (t * 128 + row) * 4) : 0.f;
+#pragma unroll
+                for (int s = 0; s < 8; ++s) sum += v[s];
+                finish(e, m0 + t, n, bad ? __int_as_float(0x7fc00000) : sum, bs, bias);
+            }
+        }
+    }
+    if (split > 1) tc::cluster_sync();  // no CTA leaves while its partial tile is read
+}
+
+// -------------------------------------------------------------------- host
+
+// Instruction descriptor: fp32 accumulate; operand formats at bits 7 and 10
+// (kind::f16: 0 fp16, 1 bf16; kind::f8f6f4: 0 e4m3).
+uint32_t idesc_of(int type, int M, int N, bool amn, bool bmn) {
+    const uint32_t f = type == kSbBf16 ? 1u : 0u;
+    return tc::idesc_f16_f32(M, N, amn, bmn) | f << 7 | f << 10;
+}
+
+// The tensor map of an operand with `rows` of the output's side and `k` of the reduction.
+bool map_operand(CUtensorMap* map, const LinOperand& o, int type, int64_t rows, int64_t k, int box_rows) {
+    const int bytes = type == kE4m3 ? 1 : 2;
+    return o.k_major ? tmap_rows_sw128(map, o.p, bytes, k, rows, o.ld * bytes, box_rows)
+                     : tmap_rows_sw128(map, o.p, bytes, rows, k, o.ld * bytes, 64);
+}
+
+Epi epi_of(const LinArgs& a) {
+    return Epi{a.M, a.N, a.a_scale, a.b_scale, a.bias, a.res, a.y, a.pre, a.ldr, a.bias_type, a.act, a.res_type, a.y_type};
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*fn)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st, A... a) {
+    if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), smem)) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(a)...);
+}
+
+int steps(const LinArgs& a, int* step) {
+    *step = a.type == kE4m3 ? 128 : 64;
+    return (int)((a.K + *step - 1) / *step);
+}
+
+template <int BN, bool AMN, bool BMN>
+cudaError_t go_pair(const LinArgs& a, cudaStream_t st) {
+    using L = PairLayout<BN, AMN, BMN>;
+    CUtensorMap ta, tb;
+    if (!map_operand(&ta, a.a, a.type, a.M, a.K, 128) || !map_operand(&tb, a.b, a.type, a.N, a.K, BN / 2))
+        return cudaErrorInvalidValue;
+    int step;
+    const int n_k = steps(a, &step);
+    const int64_t tiles = (a.M + 255) / 256 * ((a.N + BN - 1) / BN);
+    const int pairs = (int)std::min<int64_t>(tiles, device_sms() / 2);
+    return launch_cluster(linear_pair_kernel<BN, AMN, BMN>, dim3((unsigned)(2 * pairs)), kPairThreads, L::SMEM, 2, st,
+                          ta, tb, epi_of(a), n_k, step, idesc_of(a.type, 256, BN, AMN, BMN), (int)(a.type == kE4m3),
+                          a.stall);
+}
+
+template <int T, bool WMN>
+cudaError_t go_few(const LinArgs& a, int split, cudaStream_t st) {
+    using L = FewLayout<T>;
+    CUtensorMap tw, tx;
+    if (!map_operand(&tw, a.b, a.type, a.N, a.K, 128) || !map_operand(&tx, a.a, a.type, a.M, a.K, T))
+        return cudaErrorInvalidValue;
+    int step;
+    const int n_k = steps(a, &step);
+    const dim3 grid((unsigned)((a.N + 127) / 128 * split), (unsigned)((a.M + T - 1) / T));
+    return launch_cluster(linear_few_kernel<T, WMN>, grid, kFewThreads, L::SMEM, split, st, tw, tx, epi_of(a), n_k,
+                          step, split, idesc_of(a.type, 128, T, WMN, false), (int)(a.type == kE4m3), a.stall);
+}
+
+template <bool WMN>
+cudaError_t pick_few(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
+    switch (p.tile) {
+        case 16: return go_few<16, WMN>(a, p.split, st);
+        case 32: return go_few<32, WMN>(a, p.split, st);
+        case 64: return go_few<64, WMN>(a, p.split, st);
+        default: return go_few<128, WMN>(a, p.split, st);
+    }
+}
+
+template <bool AMN, bool BMN>
+cudaError_t pick_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
+    if (p.tile == 256) return go_pair<256, AMN, BMN>(a, st);
+    return go_pair<128, AMN, BMN>(a, st);
+}
+
+// --------------------------------------------------------------- pad rows
+
+template <typename E>
+__global__ void __launch_bounds__(256) pad_rows_kernel(const E* src, int64_t ld, int64_t rows, int64_t cols, E* dst,
+                                                       int64_t ldd) {
+    tc::grid_dep_wait();
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= cols) return;
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) dst[r * ldd + c] = src[r * ld + c];
+}
+
+}  // namespace
+
+LinPlan plan_linear(const LinArgs& a, int sms) {
+    const bool few_ok = a.a.k_major;
+    if (few_ok && a.M <= 128) {
+        const int tile = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+        int step;
+        const int n_k = steps(a, &step);
+        const int64_t tiles = (a.N + 127) / 128;
+        int split = 1;
+        while (split < 8 && tiles * split * 2 <= 2 * sms && split * 2 <= n_k) split *= 2;
+        return LinPlan{true, tile, split};
+    }
+    const auto cost = [&](int bn) {
+        const int64_t tiles = (a.M + 255) / 256 * ((a.N + bn - 1) / bn), pairs = sms / 2;
+        return (tiles + pairs - 1) / pairs * bn;
+    };
+    return LinPlan{false, cost(128) < cost(256) ? 128 : 256, 1};
+}
+
+cudaError_t launch_linear(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
+    if (p.few) return a.b.k_major ? pick_few<false>(a, p, st) : pick_few<true>(a, p, st);
+    if (!a.a.k_major) return pick_pair<true, true>(a, p, st);
+    return a.b.k_major ? pick_pair<false, false>(a, p, st) : pick_pair<false, true>(a, p, st);
+}
+
+cudaError_t launch_pad_rows(const void* src, int64_t ld, int64_t rows, int64_t cols, int bytes, void* dst,
+                            int64_t ldd, cudaStream_t st) {
+    const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)std::min<int64_t>(rows, 2048));
+    if (bytes == 1)
+        return launch_after(pad_rows_kernel<uint8_t>, grid, dim3(256), st, static_cast<const uint8_t*>(src), ld, rows,
+                            cols, static_cast<uint8_t*>(dst), ldd);
+    return launch_after(pad_rows_kernel<uint16_t>, grid, dim3(256), st, static_cast<const uint16_t*>(src), ld, rows,
+                        cols, static_cast<uint16_t*>(dst), ldd);
+}
+
+}  // namespace qh

@@ -51,6 +51,12 @@ bool tmap_rows_f16_sw128(CUtensorMap* map, const void* base, uint64_t cols, uint
                      box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool tmap_rows_sw128(CUtensorMap* map, const void* base, int elem_bytes, uint64_t cols, uint64_t rows,
+                     uint64_t row_bytes, uint32_t box_rows) {
+    return encode_2d(map, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, base,
+                     cols, rows, row_bytes, 128 / elem_bytes, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 bool tmap_packed_rows(CUtensorMap* map, const uint32_t* wq, uint64_t words_per_row, uint64_t rows,
                       uint32_t box_words, uint32_t box_rows) {
     return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, words_per_row, rows,

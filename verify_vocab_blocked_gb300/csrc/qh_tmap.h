@@ -12,6 +12,11 @@ namespace qh {
 bool tmap_rows_f16_sw128(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                          uint32_t box_rows);
 
+// Row-major matrix of 1- or 2-byte elements with rows of row_bytes (a multiple of
+// 16), box of 128 bytes x box_rows, 128-byte swizzle.
+bool tmap_rows_sw128(CUtensorMap* map, const void* base, int elem_bytes, uint64_t cols, uint64_t rows,
+                     uint64_t row_bytes, uint32_t box_rows);
+
 // Packed uint32 head [rows, words_per_row], box of box_words x box_rows, no swizzle.
 bool tmap_packed_rows(CUtensorMap* map, const uint32_t* wq, uint64_t words_per_row, uint64_t rows,
                       uint32_t box_words, uint32_t box_rows);

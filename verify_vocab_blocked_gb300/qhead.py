@@ -30,7 +30,8 @@ EXPORTS = ("qhead_fwd_workspace", "qhead_bwd_workspace", "qhead_fwd", "qhead_bwd
            "qhead_embed_bwd_workspace", "qhead_embed_bwd", "qhead_layer_norm",
            "qhead_layer_norm_bwd_workspace", "qhead_layer_norm_bwd",
            "qhead_distill_fwd_workspace", "qhead_distill_fwd", "qhead_distill_bwd_workspace",
-           "qhead_distill_bwd", "qhead_distill_kept")
+           "qhead_distill_bwd", "qhead_distill_kept", "qhead_linear_workspace", "qhead_linear",
+           "qhead_linear_bwd_workspace", "qhead_linear_bwd")
 
 
 class CHead(ctypes.Structure):
@@ -111,6 +112,14 @@ def lib() -> ctypes.CDLL:
     L.qhead_distill_bwd.argtypes = [hp, vp, i64, vp, vp, i32, i64, f32, vp, vp, vp, vp, vp, vp, sz,
                                     vp]
     L.qhead_distill_bwd.restype = i32
+    size = [vp, i32, i64, i64, i64, vp, i64, i64]
+    for name in ("qhead_linear_workspace", "qhead_linear_bwd_workspace"):
+        getattr(L, name).argtypes = size
+        getattr(L, name).restype = sz
+    L.qhead_linear.argtypes = size + [vp, vp, vp, i32, i32, vp, i32, i64, vp, i32, vp, vp, sz, vp]
+    L.qhead_linear.restype = i32
+    L.qhead_linear_bwd.argtypes = size + [vp, i32, i64, vp, i32, vp, vp, vp, vp, sz, vp]
+    L.qhead_linear_bwd.restype = i32
     L.qhead_last_error.argtypes = []
     L.qhead_last_error.restype = ctypes.c_char_p
     L.qhead_version.argtypes = []
@@ -783,3 +792,111 @@ def distill_bwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
                                    dh.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                    _stream(stream, dev)))
     return dh
+
+
+# ------------------------------------------------- the block between norm and head
+
+QHEAD_E4M3 = 3
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+_OPERAND_CODE = {torch.float16: QHEAD_SB_F16, torch.bfloat16: QHEAD_SB_BF16, torch.float8_e4m3fn: QHEAD_E4M3}
+
+
+def _act_code(act: str) -> int:
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    return code
+
+
+def _check_operands(x: torch.Tensor, weight: torch.Tensor, types) -> int:
+    """x [M, K] and weight [N, K], of one of `types`; the type's code."""
+    if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor):
+        raise ValueError("x and weight must be torch tensors")
+    if x.dtype not in types or weight.dtype != x.dtype:
+        names = ", ".join(str(t).replace("torch.", "") for t in types)
+        raise ValueError(f"x and weight must share one type of {names}, got {x.dtype} and {weight.dtype}")
+    if x.dim() != 2 or weight.dim() != 2 or x.shape[1] != weight.shape[1]:
+        raise ValueError(f"x must be [M, K] and weight [N, K], got {list(x.shape)} and {list(weight.shape)}")
+    if weight.device != x.device:
+        raise ValueError(f"weight is on {weight.device}, x on {x.device}")
+    for name, t in (("x", x), ("weight", weight)):
+        if not t.is_contiguous() and (t.shape[1] > 1 and t.stride(1) != 1
+                                      or t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return _OPERAND_CODE[x.dtype]
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+           residual: torch.Tensor | None = None, *, x_scale: torch.Tensor | None = None,
+           w_scale: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, want_pre: bool = False,
+           workspace: torch.Tensor | None = None, stream=None):
+    """y [M, N] = act(x @ weight.T + bias) + residual, of out_dtype (x's, or
+    bfloat16 for 8-bit operands, if not given); see qhead_linear.  x [M, K] and
+    weight [N, K] in bfloat16 or float16, or in float8_e4m3fn with a float32
+    scale for each row of both (norm_8bit()'s codes and scale for x).  With
+    want_pre (y, pre): what linear_bwd() takes."""
+    code = _check_operands(x, weight, tuple(_OPERAND_CODE))
+    dev = x.device
+    (M, K), N = x.shape, weight.shape[0]
+    a = _act_code(act)
+    if (code == QHEAD_E4M3) != (x_scale is not None and w_scale is not None) \
+            or (x_scale is None) != (w_scale is None):
+        raise ValueError("x_scale and w_scale belong to float8_e4m3fn operands, which need both")
+    if x_scale is not None:
+        x_scale, w_scale = _f32("x_scale", x_scale, M, dev), _f32("w_scale", w_scale, N, dev)
+    if bias is not None:
+        _check_param("bias", bias, N, dev)
+    if residual is not None:
+        _check_matrix("residual", residual, dev, contiguous=False)
+        if tuple(residual.shape) != (M, N):
+            raise ValueError(f"residual must have shape [{M}, {N}], got {list(residual.shape)}")
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if code == QHEAD_E4M3 else x.dtype
+    out = _out_code(out_dtype)
+    _usable(dev, stream, workspace)
+    y = _out((M, N), out_dtype, dev, stream)
+    pre = _out((M, N), torch.float16, dev, stream) if want_pre else None
+    _reads(stream, None, x, weight, x_scale, w_scale, bias, residual, workspace)
+    L = lib()
+    place = (x.data_ptr(), code, _row_stride(x, M, K), M, K, weight.data_ptr(), _row_stride(weight, N, K), N)
+    if workspace is None:
+        n = _size(L.qhead_linear_workspace(*place))
+        workspace = _scratch(n, dev, stream) if n else None
+    _check(L.qhead_linear(*place, _ptr(x_scale), _ptr(w_scale), _ptr(bias),
+                          0 if bias is None else _SB_CODE[bias.dtype], a, _ptr(residual),
+                          0 if residual is None else _SB_CODE[residual.dtype],
+                          N if residual is None else _row_stride(residual, M, N), y.data_ptr(), out, _ptr(pre),
+                          _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, dev)))
+    return (y, pre) if want_pre else y
+
+
+def linear_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, pre: torch.Tensor | None = None,
+               act: str = "none", *, want_dx: bool = True, want_dw: bool = True, want_dbias: bool = True,
+               workspace: torch.Tensor | None = None, stream=None):
+    """(dx [M, K], dweight [N, K], dbias [N]), each of x's type or None where not
+    wanted, for dy = d/dy (any float type) and linear()'s pre (act "none" needs
+    none).  The residual's gradient is dy."""
+    code = _check_operands(x, weight, (torch.float16, torch.bfloat16))
+    dev = x.device
+    (M, K), N = x.shape, weight.shape[0]
+    a = _act_code(act)
+    _check_matrix("dy", dy, dev, contiguous=False)
+    if tuple(dy.shape) != (M, N):
+        raise ValueError(f"dy must have shape [{M}, {N}], got {list(dy.shape)}")
+    if a:
+        if not isinstance(pre, torch.Tensor) or pre.dtype != torch.float16 or tuple(pre.shape) != (M, N) \
+                or not pre.is_contiguous() or pre.device != dev:
+            raise ValueError(f"pre must be a contiguous float16 [{M}, {N}] tensor on {dev}")
+    _usable(dev, stream, workspace)
+    dx = _out((M, K), x.dtype, dev, stream) if want_dx else None
+    dw = _out((N, K), x.dtype, dev, stream) if want_dw else None
+    db = _out(N, x.dtype, dev, stream) if want_dbias else None
+    _reads(stream, None, x, weight, dy, pre, workspace)
+    L = lib()
+    place = (x.data_ptr(), code, _row_stride(x, M, K), M, K, weight.data_ptr(), _row_stride(weight, N, K), N)
+    if workspace is None:
+        workspace = _scratch(_size(L.qhead_linear_bwd_workspace(*place)), dev, stream)
+    _check(L.qhead_linear_bwd(*place, dy.data_ptr(), _SB_CODE[dy.dtype], _row_stride(dy, M, N), _ptr(pre) if a else None,
+                              a, _ptr(dx), _ptr(dw), _ptr(db), workspace.data_ptr(), workspace.numel(),
+                              _stream(stream, dev)))
+    return dx, dw, db
