@@ -527,6 +527,77 @@ int qhead_linear_bwd(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K
                      int64_t ldy, const void* pre, int act, void* dx, void* dweight, void* dbias,
                      void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * A residual's addition and the norm behind it (no counterpart on the pages):
+ *     t = x + residual;  total = t, rounded;  y = norm(t)
+ * with qhead_layer_norm's norm, taken of the unrounded fp32 t.
+ *   x         device, [M, H] of type x_dtype, row stride ldx >= H.
+ *   residual  device, [M, H] of type res_dtype, row stride ldr >= H.
+ *   total     device, [M, H] contiguous, of type res_dtype.
+ *   M, H, weight, bias, w_dtype, eps, center, y, y_dtype, mean, rstd  as for
+ *             qhead_layer_norm.
+ */
+int qhead_add_norm(const void* x, int x_dtype, int64_t ldx, const void* residual, int res_dtype,
+                   int64_t ldr, int64_t M, int64_t H, const void* weight, const void* bias,
+                   int w_dtype, float eps, int center, void* total, void* y, int y_dtype,
+                   float* mean, float* rstd, void* stream);
+
+/*
+ * The same with an output in 8 bits, for qhead_linear's 8-bit operands:
+ *     scale[m] = max_d |y[m, d]| / 448;  codes[m, d] = e4m3(y[m, d] / scale[m])
+ * rounded to nearest.  (The maximum counts as 1e-30 at least; where y is NaN, so is
+ * the code.)
+ *   residual  NULL: t = x, and total must be NULL.
+ *   codes     device, e4m3 [M, H] contiguous.
+ *   scale     device, float [M].
+ */
+int qhead_norm_8bit(const void* x, int x_dtype, int64_t ldx, const void* residual, int res_dtype,
+                    int64_t ldr, int64_t M, int64_t H, const void* weight, const void* bias,
+                    int w_dtype, float eps, int center, void* total, void* codes, float* scale,
+                    void* stream);
+
+/*
+ * The gradient of qhead_add_norm: dx (of x and of the residual alike) is
+ * qhead_layer_norm_bwd's at total, plus what arrives at total itself.
+ *   total     the forward's, of type t_dtype (as rounded: the norm's gradient is
+ *             taken there, with the forward's mean and rstd).
+ *   dtotal    device, [M, H] of type t_dtype, row stride ldd >= H, or NULL (none).
+ *   dx        device, [M, H] contiguous, of type t_dtype.
+ *   workspace >= qhead_layer_norm_bwd_workspace(M, H) bytes; the rest as there.
+ */
+int qhead_add_norm_bwd(const void* total, int t_dtype, int64_t ldt, int64_t M, int64_t H,
+                       const void* weight, int w_dtype, const float* mean, const float* rstd,
+                       const void* dy, int dy_dtype, int64_t ldy, const void* dtotal, int64_t ldd,
+                       void* dx, float* dweight, float* dbias, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * The global norm of many gradient tensors, and clipping (no counterpart on the
+ * pages):
+ *     norm = sqrt(sum over tensors and elements of g^2)
+ *     out  = g * min(1, max_norm / (norm + 1e-6))
+ *   tensors, sizes, dtypes  HOST arrays of count entries, read during the call:
+ *             device address, elements (>= 0) and type of each (contiguous) tensor.
+ *   count     >= 0 (0: the norm is 0).
+ *   norm      device, float.
+ *   max_norm  > 0 and finite.
+ *   out, out_dtypes  HOST arrays: where each scaled tensor goes and its type; or
+ *             both NULL: in place (then nothing is written if norm is within
+ *             max_norm).  An entry of out may be its own tensor, with the same
+ *             type; apart from that no output may overlap a tensor or another output.
+ *   workspace device, >= qhead_grad_norm_workspace(count) bytes, 256-byte aligned.
+ * A norm that is inf or NaN scales by 0 or NaN as the formula says: look at norm
+ * before the step is taken.  Squares that fp32 cannot hold are summed in fp64.
+ * Deterministic.
+ */
+size_t qhead_grad_norm_workspace(int64_t count);
+int qhead_grad_norm(const void* const* tensors, const int64_t* sizes, const int* dtypes,
+                    int64_t count, float* norm, void* workspace, size_t workspace_bytes,
+                    void* stream);
+int qhead_clip_grads(void* const* tensors, const int64_t* sizes, const int* dtypes, int64_t count,
+                     float max_norm, void* const* out, const int* out_dtypes, float* norm,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* Message for the last error on the calling thread ("" if none).  The
  * pointer stays valid until the thread's next qhead_* call. */
 const char* qhead_last_error(void);

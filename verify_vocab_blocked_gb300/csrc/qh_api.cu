@@ -13,8 +13,10 @@
 #include <algorithm>
 #include <map>
 #include <mutex>
+#include <new>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include "../../include/qhead.h"
 #include "qh_distill.cuh"
@@ -964,12 +966,10 @@ size_t qhead_layer_norm_bwd_workspace(int64_t M, int64_t H) {
     return (size_t)qh::norm_bwd_grid(M, (int)H) * 2 * (size_t)H * sizeof(float);
 }
 
-int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t H,
-                         const void* weight, int w_dtype, const float* mean, const float* rstd,
-                         const void* dy, int dy_dtype, int64_t ldy, void* dx, float* dweight,
-                         float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
-    g_err.clear();
-    int rc = check_norm(x, x_dtype, ldx, M, H, weight, w_dtype);
+static int norm_bwd_args(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t H, const void* weight,
+                         int w_dtype, const float* mean, const float* rstd, const void* dy, int dy_dtype, int64_t ldy,
+                         void* dx, float* dweight, float* dbias, qh::NormBwdArgs* a) {
+    const int rc = check_norm(x, x_dtype, ldx, M, H, weight, w_dtype);
     if (rc) return rc;
     if (!dtype_ok(dy_dtype))
         return fail(QHEAD_EUNSUPPORTED, "dtypes must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
@@ -979,19 +979,202 @@ int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int
     if (misaligned(dy, qh::type_bytes(dy_dtype)) || misaligned(dx, qh::type_bytes(x_dtype)) ||
         misaligned(mean, 4) || misaligned(rstd, 4) || misaligned(dweight, 4) || misaligned(dbias, 4))
         return fail(QHEAD_EINVAL, "every pointer must be aligned to its elements");
+    *a = qh::NormBwdArgs{x, x_dtype, ldx, M, (int)H, weight, w_dtype, mean, rstd, dy, dy_dtype, ldy,
+                         dx, dweight, dbias, nullptr, 0, nullptr, 0};
+    return QHEAD_OK;
+}
+
+static int run_norm_bwd(qh::NormBwdArgs a, void* workspace, size_t workspace_bytes, void* stream) {
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (M == 0) {
-        cudaError_t e = cudaMemsetAsync(dweight, 0, sizeof(float) * (size_t)H, st);
-        if (!e && dbias) e = cudaMemsetAsync(dbias, 0, sizeof(float) * (size_t)H, st);
+    const size_t H = (size_t)a.H;
+    if (a.M == 0) {
+        cudaError_t e = cudaMemsetAsync(a.dw, 0, sizeof(float) * H, st);
+        if (!e && a.db) e = cudaMemsetAsync(a.db, 0, sizeof(float) * H, st);
         return e ? cuda_fail(e, "layer_norm_bwd zero") : QHEAD_OK;
     }
-    const int grid = qh::norm_bwd_grid(M, (int)H);
-    if ((rc = check_workspace(workspace, workspace_bytes, (size_t)grid * 2 * (size_t)H * sizeof(float))))
-        return rc;
-    qh::NormBwdArgs a{x,  x_dtype, ldx, M,       (int)H, weight, w_dtype, mean, rstd, dy, dy_dtype, ldy,
-                      dx, dweight, dbias, static_cast<float*>(workspace), grid};
-    const cudaError_t e = qh::launch_norm_bwd(a, st);
+    a.grid = qh::norm_bwd_grid(a.M, a.H);
+    if (const int rc = check_workspace(workspace, workspace_bytes, (size_t)a.grid * 2 * H * sizeof(float))) return rc;
+    a.part = static_cast<float*>(workspace);
+    const cudaError_t e = a.add ? qh::launch_add_norm_bwd(a, st) : qh::launch_norm_bwd(a, st);
     return e ? cuda_fail(e, "layer_norm_bwd") : QHEAD_OK;
+}
+
+int qhead_layer_norm_bwd(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t H,
+                         const void* weight, int w_dtype, const float* mean, const float* rstd,
+                         const void* dy, int dy_dtype, int64_t ldy, void* dx, float* dweight,
+                         float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    qh::NormBwdArgs a;
+    const int rc = norm_bwd_args(x, x_dtype, ldx, M, H, weight, w_dtype, mean, rstd, dy, dy_dtype, ldy, dx, dweight,
+                                 dbias, &a);
+    return rc ? rc : run_norm_bwd(a, workspace, workspace_bytes, stream);
+}
+
+// Checks and arguments that the two forms of the norm behind an addition share.
+static int add_norm_args(const void* x, int x_dtype, int64_t ldx, const void* residual, int res_dtype, int64_t ldr,
+                         int64_t M, int64_t H, const void* weight, const void* bias, int w_dtype, float eps,
+                         int center, void* total, qh::AddNormArgs* a) {
+    const int rc = check_norm(x, x_dtype, ldx, M, H, weight, w_dtype);
+    if (rc) return rc;
+    if (residual) {
+        if (!dtype_ok(res_dtype))
+            return fail(QHEAD_EUNSUPPORTED, "dtypes must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+        if (ldr < H) return fail(QHEAD_EINVAL, "ldr < H");
+        const size_t size = qh::type_bytes(res_dtype);
+        if (misaligned(residual, size) || misaligned(total, size))
+            return fail(QHEAD_EINVAL, "residual and total must be aligned to their elements");
+    }
+    if (!(eps >= 0.f) || eps > 3.4e38f) return fail(QHEAD_EINVAL, "eps must be >= 0 and finite");
+    if (misaligned(bias, qh::type_bytes(w_dtype))) return fail(QHEAD_EINVAL, "bias must be aligned to its elements");
+    if (M > 0 && (residual != nullptr) != (total != nullptr))
+        return fail(QHEAD_EINVAL, "total goes with a residual");
+    *a = qh::AddNormArgs{};
+    a->x = x, a->x_type = x_dtype, a->ldx = ldx;
+    a->res = residual, a->r_type = res_dtype, a->ldr = ldr;
+    a->M = M, a->H = (int)H;
+    a->w = weight, a->b = bias, a->w_type = w_dtype;
+    a->eps = eps, a->center = center != 0, a->total = total;
+    return QHEAD_OK;
+}
+
+int qhead_add_norm(const void* x, int x_dtype, int64_t ldx, const void* residual, int res_dtype, int64_t ldr,
+                   int64_t M, int64_t H, const void* weight, const void* bias, int w_dtype, float eps, int center,
+                   void* total, void* y, int y_dtype, float* mean, float* rstd, void* stream) {
+    g_err.clear();
+    qh::AddNormArgs a;
+    const int rc = add_norm_args(x, x_dtype, ldx, residual, res_dtype, ldr, M, H, weight, bias, w_dtype, eps, center,
+                                 total, &a);
+    if (rc) return rc;
+    if (!dtype_ok(y_dtype))
+        return fail(QHEAD_EUNSUPPORTED, "dtypes must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+    if (!center && mean) return fail(QHEAD_EINVAL, "mean must be NULL without center");
+    if (M == 0) return QHEAD_OK;
+    if (!residual || !y || !rstd || (center && !mean))
+        return fail(QHEAD_EINVAL, "residual, total, y and rstd (and, with center, mean) are required");
+    if (misaligned(y, qh::type_bytes(y_dtype)) || misaligned(mean, 4) || misaligned(rstd, 4))
+        return fail(QHEAD_EINVAL, "y, mean and rstd must be aligned to their elements");
+    a.y = y, a.y_type = y_dtype, a.mean = mean, a.rstd = rstd;
+    const cudaError_t e = qh::launch_add_norm(a, static_cast<cudaStream_t>(stream));
+    return e ? cuda_fail(e, "add_norm") : QHEAD_OK;
+}
+
+int qhead_norm_8bit(const void* x, int x_dtype, int64_t ldx, const void* residual, int res_dtype, int64_t ldr,
+                    int64_t M, int64_t H, const void* weight, const void* bias, int w_dtype, float eps, int center,
+                    void* total, void* codes, float* scale, void* stream) {
+    g_err.clear();
+    qh::AddNormArgs a;
+    const int rc = add_norm_args(x, x_dtype, ldx, residual, res_dtype, ldr, M, H, weight, bias, w_dtype, eps, center,
+                                 total, &a);
+    if (rc) return rc;
+    if (M == 0) return QHEAD_OK;
+    if (!codes || !scale) return fail(QHEAD_EINVAL, "codes and scale are required");
+    if (misaligned(scale, 4)) return fail(QHEAD_EINVAL, "scale must be aligned to its elements");
+    a.y = codes, a.scale = scale;
+    const cudaError_t e = qh::launch_add_norm(a, static_cast<cudaStream_t>(stream));
+    return e ? cuda_fail(e, "norm_8bit") : QHEAD_OK;
+}
+
+int qhead_add_norm_bwd(const void* total, int t_dtype, int64_t ldt, int64_t M, int64_t H, const void* weight,
+                       int w_dtype, const float* mean, const float* rstd, const void* dy, int dy_dtype, int64_t ldy,
+                       const void* dtotal, int64_t ldd, void* dx, float* dweight, float* dbias, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    if (!dtotal)
+        return qhead_layer_norm_bwd(total, t_dtype, ldt, M, H, weight, w_dtype, mean, rstd, dy, dy_dtype, ldy, dx,
+                                    dweight, dbias, workspace, workspace_bytes, stream);
+    g_err.clear();
+    qh::NormBwdArgs a;
+    int rc = norm_bwd_args(total, t_dtype, ldt, M, H, weight, w_dtype, mean, rstd, dy, dy_dtype, ldy, dx, dweight,
+                           dbias, &a);
+    if (rc) return rc;
+    if (ldd < H) return fail(QHEAD_EINVAL, "ldd < H");
+    if (misaligned(dtotal, qh::type_bytes(t_dtype))) return fail(QHEAD_EINVAL, "dtotal must be aligned to its elements");
+    a.add = dtotal, a.ldadd = ldd;
+    return run_norm_bwd(a, workspace, workspace_bytes, stream);
+}
+
+size_t qhead_grad_norm_workspace(int64_t count) {
+    g_err.clear();
+    if (count < 0 || count > 1 << 20) {
+        fail(QHEAD_EINVAL, "count must be in [0, 2^20]");
+        return (size_t)-1;
+    }
+    return qh::grad_norm_workspace((int)count);
+}
+
+// Address ranges of the outputs, and of the tensors that are not written in place.
+static bool overlapping(const qh::GradTensors& t) {
+    struct Range {
+        uintptr_t at, end;
+        bool out;
+    };
+    std::vector<Range> r;
+    r.reserve(2 * (size_t)t.count);
+    for (int i = 0; i < t.count; ++i) {
+        if (t.n[i] == 0) continue;
+        const uintptr_t p = reinterpret_cast<uintptr_t>(t.p[i]), o = reinterpret_cast<uintptr_t>(t.out[i]);
+        r.push_back({o, o + (uintptr_t)t.n[i] * qh::type_bytes(t.out_type[i]), true});
+        if (p != o) r.push_back({p, p + (uintptr_t)t.n[i] * qh::type_bytes(t.type[i]), false});
+    }
+    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.at < b.at; });
+    uintptr_t any = 0, out = 0;  // the ends so far: of all ranges, of outputs
+    for (const Range& q : r) {
+        if (q.at < (q.out ? any : out)) return true;
+        any = std::max(any, q.end);
+        if (q.out) out = std::max(out, q.end);
+    }
+    return false;
+}
+
+static int grad_norm_impl(const qh::GradTensors& t, float max_norm, float* norm, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    if (!norm || misaligned(norm, 4)) return fail(QHEAD_EINVAL, "norm is required and 4-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (t.count == 0) {
+        const cudaError_t e = cudaMemsetAsync(norm, 0, sizeof(float), st);
+        return e ? cuda_fail(e, "grad_norm zero") : QHEAD_OK;
+    }
+    if (!t.p || !t.n || !t.type) return fail(QHEAD_EINVAL, "tensors, sizes and dtypes are required");
+    int64_t total = 0;
+    for (int i = 0; i < t.count; ++i) {
+        if (!dtype_ok(t.type[i]) || (t.out && !dtype_ok(t.out_type[i])))
+            return fail(QHEAD_EUNSUPPORTED, "dtypes must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+        if (t.n[i] < 0 || (total += t.n[i]) > (int64_t)1 << 42 || t.n[i] > (int64_t)1 << 42)
+            return fail(QHEAD_EINVAL, "sizes must be >= 0 and their sum at most 2^42");
+        if (t.n[i] == 0) continue;
+        if (!t.p[i] || misaligned(t.p[i], qh::type_bytes(t.type[i])))
+            return fail(QHEAD_EINVAL, "every tensor must be given and aligned to its elements");
+        if (t.out && (!t.out[i] || misaligned(t.out[i], qh::type_bytes(t.out_type[i]))))
+            return fail(QHEAD_EINVAL, "every output must be given and aligned to its elements");
+        if (t.out && t.out[i] == t.p[i] && t.out_type[i] != t.type[i])
+            return fail(QHEAD_EINVAL, "an output in its tensor's place must have its type");
+    }
+    int rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, qh::grad_norm_workspace(t.count)))) return rc;
+    if (t.out && overlapping(t)) return fail(QHEAD_EINVAL, "outputs overlap tensors or each other");
+    const cudaError_t e = qh::launch_grad_norm(t, max_norm, norm, workspace, st);
+    return e ? cuda_fail(e, "grad_norm") : QHEAD_OK;
+}
+
+int qhead_grad_norm(const void* const* tensors, const int64_t* sizes, const int* dtypes, int64_t count, float* norm,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    if (count < 0 || count > 1 << 20) return fail(QHEAD_EINVAL, "count must be in [0, 2^20]");
+    return grad_norm_impl({tensors, nullptr, sizes, dtypes, nullptr, (int)count}, 0.f, norm, workspace,
+                          workspace_bytes, stream);
+}
+
+int qhead_clip_grads(void* const* tensors, const int64_t* sizes, const int* dtypes, int64_t count, float max_norm,
+                     void* const* out, const int* out_dtypes, float* norm, void* workspace, size_t workspace_bytes,
+                     void* stream) try {
+    g_err.clear();
+    if (count < 0 || count > 1 << 20) return fail(QHEAD_EINVAL, "count must be in [0, 2^20]");
+    if (!(max_norm > 0.f) || max_norm > 3.4e38f) return fail(QHEAD_EINVAL, "max_norm must be positive and finite");
+    if ((out == nullptr) != (out_dtypes == nullptr)) return fail(QHEAD_EINVAL, "out and out_dtypes go together");
+    return grad_norm_impl({const_cast<const void* const*>(tensors), out ? out : tensors, sizes, dtypes,
+                           out ? out_dtypes : dtypes, (int)count},
+                          max_norm, norm, workspace, workspace_bytes, stream);
+} catch (const std::bad_alloc&) {  // (the ranges that the overlap check sorts)
+    return fail(QHEAD_EINVAL, "out of host memory");
 }
 
 size_t qhead_linear_workspace(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, const void* weight,

@@ -208,8 +208,49 @@ struct NormBwdArgs {
     float* db;          // NULL: not wanted
     float* part;        // [grid, 2, H]
     int grid;
+    const void* add;    // x's type, rows of ldadd: added to dx (launch_add_norm_bwd)
+    int64_t ldadd;
 };
 int norm_bwd_grid(int64_t M, int H);
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t st);
+cudaError_t launch_add_norm_bwd(const NormBwdArgs& a, cudaStream_t st);  // adds a.add into dx
+
+// The norm of x + res (res NULL: of x), whose sum goes to `total`; scale: y is
+// e4m3 codes, their row scales go there.
+struct AddNormArgs {
+    const void* x;
+    int x_type;
+    int64_t ldx;
+    const void* res;
+    int r_type;         // of res and total
+    int64_t ldr;
+    int64_t M;
+    int H;
+    const void* w;
+    const void* b;      // NULL: none
+    int w_type;
+    float eps;
+    bool center;
+    void* total;        // [M, H] contiguous
+    void* y;            // [M, H] contiguous
+    int y_type;
+    float* scale;       // NULL: y is of y_type
+    float* mean;        // NULL: not wanted
+    float* rstd;        // NULL: not wanted
+};
+cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st);
+
+// ------------------------------------------------------------ gradient norm
+
+struct GradTensors {
+    const void* const* p;   // host arrays
+    void* const* out;       // NULL: none are written; may be p
+    const int64_t* n;
+    const int* type;
+    const int* out_type;
+    int count;
+};
+size_t grad_norm_workspace(int count);
+cudaError_t launch_grad_norm(const GradTensors& t, float max_norm, float* norm, void* ws, cudaStream_t st);
 
 }  // namespace qh

@@ -31,7 +31,8 @@ EXPORTS = ("qhead_fwd_workspace", "qhead_bwd_workspace", "qhead_fwd", "qhead_bwd
            "qhead_layer_norm_bwd_workspace", "qhead_layer_norm_bwd",
            "qhead_distill_fwd_workspace", "qhead_distill_fwd", "qhead_distill_bwd_workspace",
            "qhead_distill_bwd", "qhead_distill_kept", "qhead_linear_workspace", "qhead_linear",
-           "qhead_linear_bwd_workspace", "qhead_linear_bwd")
+           "qhead_linear_bwd_workspace", "qhead_linear_bwd", "qhead_add_norm", "qhead_norm_8bit",
+           "qhead_add_norm_bwd", "qhead_grad_norm_workspace", "qhead_grad_norm", "qhead_clip_grads")
 
 
 class CHead(ctypes.Structure):
@@ -120,6 +121,20 @@ def lib() -> ctypes.CDLL:
     L.qhead_linear.restype = i32
     L.qhead_linear_bwd.argtypes = size + [vp, i32, i64, vp, i32, vp, vp, vp, vp, sz, vp]
     L.qhead_linear_bwd.restype = i32
+    added = [vp, i32, i64, vp, i32, i64, i64, i64, vp, vp, i32, f32, i32, vp]
+    L.qhead_add_norm.argtypes = added + [vp, i32, vp, vp, vp]
+    L.qhead_add_norm.restype = i32
+    L.qhead_norm_8bit.argtypes = added + [vp, vp, vp]
+    L.qhead_norm_8bit.restype = i32
+    L.qhead_add_norm_bwd.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, i32, i64, vp, i64, vp,
+                                     vp, vp, vp, sz, vp]
+    L.qhead_add_norm_bwd.restype = i32
+    L.qhead_grad_norm_workspace.argtypes = [i64]
+    L.qhead_grad_norm_workspace.restype = sz
+    L.qhead_grad_norm.argtypes = [vp, vp, vp, i64, vp, vp, sz, vp]
+    L.qhead_grad_norm.restype = i32
+    L.qhead_clip_grads.argtypes = [vp, vp, vp, i64, f32, vp, vp, vp, vp, sz, vp]
+    L.qhead_clip_grads.restype = i32
     L.qhead_last_error.argtypes = []
     L.qhead_last_error.restype = ctypes.c_char_p
     L.qhead_version.argtypes = []
@@ -900,3 +915,167 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, pre: tor
                               a, _ptr(dx), _ptr(dw), _ptr(db), workspace.data_ptr(), workspace.numel(),
                               _stream(stream, dev)))
     return dx, dw, db
+
+
+def _check_added(x, residual, weight, bias):
+    """The operands of a norm behind an addition (residual None: of the norm alone)."""
+    if not isinstance(x, torch.Tensor):
+        raise ValueError("x must be a torch tensor")
+    dev = x.device
+    _check_matrix("x", x, dev, contiguous=False)
+    M, H = x.shape
+    if residual is not None:
+        _check_matrix("residual", residual, dev, contiguous=False)
+        if residual.shape != x.shape:
+            raise ValueError(f"residual must have x's shape [{M}, {H}], got {list(residual.shape)}")
+    if weight is None:
+        raise ValueError("weight is required")
+    _check_param("weight", weight, H, dev)
+    _check_param("bias", bias, H, dev, weight.dtype)
+    return dev, M, H
+
+
+def _added(x, residual, weight, bias, eps, center, total, M, H):
+    """The arguments that both forms of the norm behind an addition begin with."""
+    return (x.data_ptr(), _SB_CODE[x.dtype], _row_stride(x, M, H), _ptr(residual),
+            0 if residual is None else _SB_CODE[residual.dtype],
+            H if residual is None else _row_stride(residual, M, H), M, H, weight.data_ptr(), _ptr(bias),
+            _SB_CODE[weight.dtype], eps, int(center), _ptr(total))
+
+
+def add_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
+             bias: torch.Tensor | None = None, eps: float = 1e-6, *, center: bool = True,
+             out_dtype: torch.dtype = torch.bfloat16, stream=None):
+    """(y [M, H] of out_dtype, total [M, H] of residual's type, mean [M] or None,
+    rstd [M]): total = x + residual, and layer_norm() of it, taken before it is
+    rounded.  Both may have any float type and a row stride above H."""
+    dev, M, H = _check_added(x, residual, weight, bias)
+    if residual is None:
+        raise ValueError("residual is required")
+    code = _out_code(out_dtype)
+    _usable(dev, stream)
+    y = _out((M, H), out_dtype, dev, stream)
+    total = _out((M, H), residual.dtype, dev, stream)
+    rstd = _out(M, torch.float32, dev, stream)
+    mean = _out(M, torch.float32, dev, stream) if center else None
+    _reads(stream, None, x, residual, weight, bias)
+    _check(lib().qhead_add_norm(*_added(x, residual, weight, bias, eps, center, total, M, H), y.data_ptr(), code,
+                                _ptr(mean), rstd.data_ptr(), _stream(stream, dev)))
+    return y, total, mean, rstd
+
+
+def norm_8bit(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, eps: float = 1e-6, *,
+              residual: torch.Tensor | None = None, center: bool = True, stream=None):
+    """(codes float8_e4m3fn [M, H], scale float32 [M], total or None): the norm of
+    x (of x + residual, which total then holds) as 8-bit codes with a scale for each
+    row, codes * scale = y: linear()'s x and x_scale."""
+    dev, M, H = _check_added(x, residual, weight, bias)
+    _usable(dev, stream)
+    codes = _out((M, H), torch.float8_e4m3fn, dev, stream)
+    scale = _out(M, torch.float32, dev, stream)
+    total = None if residual is None else _out((M, H), residual.dtype, dev, stream)
+    _reads(stream, None, x, residual, weight, bias)
+    _check(lib().qhead_norm_8bit(*_added(x, residual, weight, bias, eps, center, total, M, H), codes.data_ptr(),
+                                 scale.data_ptr(), _stream(stream, dev)))
+    return codes, scale, total
+
+
+def add_norm_bwd(total: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor | None, rstd: torch.Tensor,
+                 dy: torch.Tensor, dtotal: torch.Tensor | None = None, *, want_dbias: bool = True,
+                 workspace: torch.Tensor | None = None, stream=None):
+    """(dx [M, H] of total's type, dweight [H] float32, dbias [H] float32 or None)
+    for dy = d/dy and dtotal = d/dtotal (total's type; None: nothing arrives
+    there).  dx is the gradient of x and of the residual; total, mean and rstd are
+    add_norm()'s."""
+    if dtotal is None:
+        return layer_norm_bwd(total, weight, mean, rstd, dy, want_dbias=want_dbias, workspace=workspace,
+                              stream=stream)
+    if not isinstance(total, torch.Tensor):
+        raise ValueError("total must be a torch tensor")
+    dev = total.device
+    _check_matrix("total", total, dev, contiguous=False)
+    M, H = total.shape
+    for name, t in (("dy", dy), ("dtotal", dtotal)):
+        _check_matrix(name, t, dev, contiguous=False)
+        if t.shape != total.shape:
+            raise ValueError(f"{name} must have shape [{M}, {H}], got {list(t.shape)}")
+    if dtotal.dtype != total.dtype:
+        raise ValueError("dtotal must have total's type")
+    if weight is None:
+        raise ValueError("weight is required")
+    _check_param("weight", weight, H, dev)
+    mean = _check_vec("mean", mean, M, (torch.float32,), dev, required=False)
+    rstd = _f32("rstd", rstd, M, dev)
+    _usable(dev, stream, workspace)
+    dx = _out((M, H), total.dtype, dev, stream)
+    dw = _out(H, torch.float32, dev, stream)
+    db = _out(H, torch.float32, dev, stream) if want_dbias else None
+    _reads(stream, None, total, weight, mean, rstd, dy, dtotal, workspace)
+    if workspace is None:
+        workspace = _scratch(_size(lib().qhead_layer_norm_bwd_workspace(M, H)), dev, stream)
+    _check(lib().qhead_add_norm_bwd(total.data_ptr(), _SB_CODE[total.dtype], _row_stride(total, M, H), M, H,
+                                    weight.data_ptr(), _SB_CODE[weight.dtype], _ptr(mean), rstd.data_ptr(),
+                                    dy.data_ptr(), _SB_CODE[dy.dtype], _row_stride(dy, M, H), dtotal.data_ptr(),
+                                    _row_stride(dtotal, M, H), dx.data_ptr(), dw.data_ptr(), _ptr(db),
+                                    workspace.data_ptr(), workspace.numel(), _stream(stream, dev)))
+    return dx, dw, db
+
+
+# ------------------------------------------------- the gradients of a whole model
+
+def _grad_list(name: str, tensors, dev=None):
+    """(tensors as a list, their device, addresses, sizes and type codes as C arrays)."""
+    ts = list(tensors)
+    n = len(ts)
+    for t in ts:
+        if not isinstance(t, torch.Tensor) or t.dtype not in _SB_CODE or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous float16, bfloat16 or float32 tensors")
+        if dev is None:
+            dev = t.device
+        if t.device != dev:
+            raise ValueError(f"{name} are on {t.device} and {dev}: they must be on one GPU")
+    return (ts, dev, (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]),
+            (ctypes.c_int64 * n)(*[t.numel() for t in ts]), (ctypes.c_int * n)(*[_SB_CODE[t.dtype] for t in ts]))
+
+
+def grad_norm(tensors, *, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The 2-norm over all elements of the tensors (contiguous, any float types, on
+    one GPU), as a float32 scalar on the device."""
+    ts, dev, ptrs, sizes, types = _grad_list("tensors", tensors)
+    if not ts:
+        raise ValueError("tensors is empty")
+    _usable(dev, stream, workspace)
+    norm = _out((), torch.float32, dev, stream)
+    _reads(stream, None, *ts, workspace)
+    if workspace is None:
+        workspace = _scratch(_size(lib().qhead_grad_norm_workspace(len(ts))), dev, stream)
+    _check(lib().qhead_grad_norm(ptrs, sizes, types, len(ts), norm.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel(), _stream(stream, dev)))
+    return norm
+
+
+def clip_grads(tensors, max_norm: float, *, out=None, workspace: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """Scales the tensors by min(1, max_norm / (norm + 1e-6)) and returns
+    grad_norm() of them as they were: in place, or into `out`, as many tensors of
+    the same sizes and any float types (16-bit copies of float32 gradients, for
+    example).  In place nothing is written when the norm is within max_norm."""
+    ts, dev, ptrs, sizes, types = _grad_list("tensors", tensors)
+    if not ts:
+        raise ValueError("tensors is empty")
+    os_, optrs, otypes = [], None, None
+    if out is not None:
+        os_, _, optrs, osizes, otypes = _grad_list("out", out, dev)
+        if list(osizes) != list(sizes):
+            raise ValueError("out must hold as many elements as tensors, tensor by tensor")
+    _usable(dev, stream, workspace)
+    norm = _out((), torch.float32, dev, stream)
+    _reads(stream, None, *ts, *os_, workspace)
+    L = lib()
+    if workspace is None:
+        workspace = _scratch(_size(L.qhead_grad_norm_workspace(len(ts))), dev, stream)
+    _check(L.qhead_clip_grads(ptrs, sizes, types, len(ts), max_norm, optrs, otypes, norm.data_ptr(),
+                              workspace.data_ptr(), workspace.numel(), _stream(stream, dev)))
+    # (written behind autograd's back: what it has saved of them is no longer theirs)
+    torch.autograd.graph.increment_version([t for t in (ts if out is None else os_) if not t.is_inference()])
+    return norm
