@@ -72,9 +72,12 @@ struct Epi {
     __half* pre;
     int64_t ldr;
     int bias_type, act, res_type, y_type;
+    float unbias;      // what every sum is multiplied by (see unbias_of)
+    int vec;           // bytes that the rows of y, pre and res are all aligned to: 32, 16 or 0
 };
 
-// One output of row m and column n, whose column's scale and bias are at hand.
+// One output of row m and column n, whose column's scale (with `unbias`) and bias
+// are at hand.
 __device__ __forceinline__ void finish(const Epi& e, int64_t m, int64_t n, float v, float bs, float bias) {
     if (e.a_scale) v *= e.a_scale[m];
     v = fmaf(v, bs, bias);
@@ -85,6 +88,127 @@ __device__ __forceinline__ void finish(const Epi& e, int64_t m, int64_t n, float
     put(e.y, at, e.y_type, v);
 }
 
+// 32 consecutive bytes (words w[0 .. 8)) to or from rows of that alignment, or of 16.
+__device__ __forceinline__ void st32(void* p, const uint32_t* w, int vec) {
+    if (vec == 32) {
+        tc::st_global_v8(p, w);
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+__device__ __forceinline__ void ld32(const void* p, uint32_t* w, int vec) {
+    if (vec == 32) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                     : "l"(p)
+                     : "memory");
+    } else {
+        const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, int type) {
+    if (type == kSbBf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int ACT>
+__device__ __forceinline__ void activate32(float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = activate(v[j], ACT);
+}
+
+// A thread's 32 consecutive columns of row m, all in range; cs, cb: their scales and
+// biases in shared memory.  The residual's loads go out before the caller's
+// accumulator is waited for (`load`) and are used here.
+struct RowChunk {
+    uint32_t r[32];  // the residual's words (16 of a 2-byte type)
+    __device__ __forceinline__ void load(const Epi& e, int64_t m, int64_t n) {
+        if (!e.res) return;
+        if (e.res_type == kSbF32) {
+            const float* p = static_cast<const float*>(e.res) + m * e.ldr + n;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ld32(p + 8 * q, r + 8 * q, e.vec);
+        } else {
+            const __half* p = static_cast<const __half*>(e.res) + m * e.ldr + n;  // (16 bits)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) ld32(p + 16 * q, r + 8 * q, e.vec);
+        }
+    }
+    __device__ __forceinline__ void finish(const Epi& e, int64_t m, int64_t n, float (&v)[32], const float* cs,
+                                           const float* cb) {
+        const float as = e.a_scale ? e.a_scale[m] : 1.f;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            const float4 s = *reinterpret_cast<const float4*>(cs + j), b = *reinterpret_cast<const float4*>(cb + j);
+            v[j] = fmaf(v[j] * as, s.x, b.x);
+            v[j + 1] = fmaf(v[j + 1] * as, s.y, b.y);
+            v[j + 2] = fmaf(v[j + 2] * as, s.z, b.z);
+            v[j + 3] = fmaf(v[j + 3] * as, s.w, b.w);
+        }
+        const int64_t at = m * e.N + n;
+        uint32_t w[16];
+        if (e.pre) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const __half2 h = __halves2half2(pre_of(v[2 * j]), pre_of(v[2 * j + 1]));
+                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            st32(e.pre + at, w, e.vec);
+            st32(e.pre + at + 16, w + 8, e.vec);
+        }
+        switch (e.act) {
+            case kActRelu: activate32<kActRelu>(v); break;
+            case kActSilu: activate32<kActSilu>(v); break;
+            case kActGelu: activate32<kActGelu>(v); break;
+            case kActGeluTanh: activate32<kActGeluTanh>(v); break;
+            default: break;
+        }
+        if (e.res) {
+            if (e.res_type == kSbF32) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
+            } else if (e.res_type == kSbBf16) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    v[2 * j] += __uint_as_float(r[j] << 16);
+                    v[2 * j + 1] += __uint_as_float(r[j] & 0xffff0000u);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[j]));
+                    v[2 * j] += f.x;
+                    v[2 * j + 1] += f.y;
+                }
+            }
+        }
+        if (e.y_type == kSbF32) {
+            float* p = static_cast<float*>(e.y) + at;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) st32(p + 8 * q, reinterpret_cast<const uint32_t*>(v + 8 * q), e.vec);
+        } else {
+            __half* p = static_cast<__half*>(e.y) + at;  // (16 bits)
+            if (e.y_type == kSbBf16) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], kSbBf16);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], kSbF16);
+            }
+            st32(p, w, e.vec);
+            st32(p + 16, w + 8, e.vec);
+        }
+    }
+};
+
 // ------------------------------------------------------------------- pairs
 
 template <int BN, bool AMN, bool BMN>
@@ -92,14 +216,16 @@ struct PairLayout {
     static constexpr int A_BYTES = 128 * kRowBytes;      // this CTA's 128 rows of A
     static constexpr int B_BYTES = BN / 2 * kRowBytes;   // and its half of B's columns
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int NS = BN == 256 ? 6 : 8;
+    static constexpr int NS = BN == 256 ? 5 : 7;
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int BAR_BYTES = 8 * (2 * NS + 5) + 16;
-    static constexpr int OFF_T = (OFF_BAR + BAR_BYTES + 127) / 128 * 128;  // transposes
-    static constexpr int SMEM = OFF_T + 8 * 32 * 33 * 4 + 1024;
+    static constexpr int OFF_T = (OFF_BAR + BAR_BYTES + 127) / 128 * 128;
+    static constexpr int TR = 32 * 33 + BN;  // floats of a warp: a transpose, its columns' scales and biases
+    static constexpr int SMEM = OFF_T + 8 * TR * 4 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 constexpr int kPairThreads = 10 * 32;
+constexpr int kSumSteps = 4;   // stages of a tensor-core sum of a float32 output
 
 // The tiles in groups of 8 rows of tiles, columns outer: what the pairs work on at
 // a time is near-square, so that each operand's tiles are shared in L2.
@@ -144,7 +270,11 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
 template <bool MN>
 constexpr uint32_t kStep = MN ? 128u : 2u;
 
-template <int BN, bool AMN, bool BMN>
+// SUMS: for float32 outputs.  The tensor cores' accumulation truncates, up to a step
+// of the running sum at each MMA; kSumSteps stages are summed there, and these sums
+// in registers, rounded to nearest (K = 1541: 2.1e-6 of the result's norm without,
+// beside 0.8e-6 of an fp32 product).
+template <int BN, bool AMN, bool BMN, bool SUMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                        const __grid_constant__ Epi e, int n_k, int step_k, uint32_t idesc, int f8, int stall) {
@@ -243,30 +373,35 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint64_t bd0 = operand_desc<BMN>(tc::smem_u32(smem + L::A_BYTES));
             bool ok = true;
             for (int t = first; t < tiles && ok; t += stride) {
-                ok = tc::mbar_wait_cluster(&acce[buf], aphase ^ 1, abort_flag, err, tc::kErrTimeoutAccEmpty);
-                tc::tc_fence_after();
-                const uint32_t d = tmem_base + buf * BN;
                 for (int kk = 0; kk < n_k && ok; ++kk) {
+                    const bool begins = kk == 0 || (SUMS && kk % kSumSteps == 0);
+                    if (begins) {
+                        ok = tc::mbar_wait_cluster(&acce[buf], aphase ^ 1, abort_flag, err, tc::kErrTimeoutAccEmpty);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                    }
                     ok = tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull);
                     if (!ok) break;
                     tc::tc_fence_after();
+                    const uint32_t d = tmem_base + buf * BN;
                     const uint64_t ad = ad0 + (uint32_t)(stage * (L::STAGE >> 4));
                     const uint64_t bd = bd0 + (uint32_t)(stage * (L::STAGE >> 4));
                     if (!AMN && !BMN && f8) {
 #pragma unroll
                         for (int s = 0; s < 4; ++s)
-                            umma_f8_pair(d, ad + 2 * s, bd + 2 * s, idesc, (kk | s) != 0);
+                            umma_f8_pair(d, ad + 2 * s, bd + 2 * s, idesc, !begins || s != 0);
                     } else {
 #pragma unroll
                         for (int s = 0; s < 4; ++s)
-                            tc::umma_f16_pair(d, ad + kStep<AMN> * s, bd + kStep<BMN> * s, idesc, (kk | s) != 0);
+                            tc::umma_f16_pair(d, ad + kStep<AMN> * s, bd + kStep<BMN> * s, idesc, !begins || s != 0);
                     }
                     tc::umma_commit_pair(&empty[stage], kPairMask);
                     if (++stage == NS) { stage = 0; phase ^= 1; }
+                    if (kk + 1 == n_k || (SUMS && (kk + 1) % kSumSteps == 0)) {
+                        tc::umma_commit_pair(&accf[buf], kPairMask);
+                        if (++buf == 2) { buf = 0; aphase ^= 1; }
+                    }
                 }
-                if (!ok) break;
-                tc::umma_commit_pair(&accf[buf], kPairMask);
-                if (++buf == 2) { buf = 0; aphase ^= 1; }
             }
             if (!ok) {
                 tc::umma_commit_pair(mdrain, 0x1);
@@ -274,9 +409,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
         }
     } else {
+        // A warp's 32 accumulator rows (its quadrant of the lanes) and half of the columns.
         const int sub = warp & 3, half = (warp - 2) >> 2;
         const uint32_t acce_lead = tc::mapa_shared(acce, 0);
-        float* tr = reinterpret_cast<float*>(smem + L::OFF_T) + (warp - 2) * 32 * 33;
+        float* tr = reinterpret_cast<float*>(smem + L::OFF_T) + (warp - 2) * L::TR;
+        float *cs = tr + 32 * 33, *cb = cs + BN / 2;  // the columns' scales and biases
         const float nan = __int_as_float(0x7fc00000);
         int buf = 0;
         uint32_t aphase = 0;
@@ -284,30 +421,87 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int mt, nt;
             tile_of(t, n_mt, n_nt, mt, nt);
             const int64_t m0 = (int64_t)mt * 256 + rank * 128 + sub * 32;
-            const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
-            tc::tc_fence_after();
+            const int64_t n0 = (int64_t)nt * BN + half * (BN / 2);
             const int rows = (int)min((int64_t)32, e.M - m0);  // (<= 0: none)
-            const uint32_t d = tmem_base + ((uint32_t)(sub * 32) << 16) + buf * BN + half * (BN / 2);
-#pragma unroll 1
-            for (int c = 0; c < BN / 64; ++c) {
-                uint32_t r[32];
-                tc::tmem_ld32(d + 32 * c, r);
-                tc::tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) tr[lane * 33 + j] = ok ? __uint_as_float(r[j]) : nan;
-                __syncwarp();
-                const int64_t n = (int64_t)nt * BN + half * (BN / 2) + 32 * c + lane;
-                if (n < e.N) {
-                    const float bs = e.b_scale ? e.b_scale[n] : 1.f;
-                    const float bias = e.bias ? sb_elem(e.bias, n, e.bias_type) : 0.f;
-                    for (int i = 0; i < rows; ++i) finish(e, m0 + i, n, tr[i * 33 + lane], bs, bias);
-                }
-                __syncwarp();
+            for (int c = 0; c < BN / 64; ++c) {
+                const int64_t n = n0 + 32 * c + lane;
+                cs[32 * c + lane] = e.unbias * (e.b_scale && n < e.N ? e.b_scale[n] : 1.f);
+                cb[32 * c + lane] = e.bias && n < e.N ? sb_elem(e.bias, n, e.bias_type) : 0.f;
             }
-            tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(acce_lead + 8 * buf);
-            if (++buf == 2) { buf = 0; aphase ^= 1; }
+            const uint32_t d0 = tmem_base + ((uint32_t)(sub * 32) << 16) + half * (BN / 2);
+            // f(c, v): the sums of the columns' c-th 32
+            const auto out = [&](int c, const float (&v)[32], RowChunk& row) {
+                const int64_t n = n0 + 32 * c;
+                if (e.vec && n + 32 <= e.N) {
+                    float u[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) u[j] = v[j];
+                    if (lane < rows) row.finish(e, m0 + lane, n, u, cs + 32 * c, cb + 32 * c);
+                } else {
+                    // any alignment and width: through shared memory, a row at a time
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) tr[lane * 33 + j] = v[j];
+                    __syncwarp();
+                    if (n + lane < e.N)
+                        for (int i = 0; i < rows; ++i)
+                            finish(e, m0 + i, n + lane, tr[i * 33 + lane], cs[32 * c + lane], cb[32 * c + lane]);
+                    __syncwarp();
+                }
+            };
+            const auto ask = [&](int c, RowChunk& row) {
+                if (e.vec && n0 + 32 * c + 32 <= e.N && lane < rows) row.load(e, m0 + lane, n0 + 32 * c);
+            };
+            if constexpr (!SUMS) {
+                RowChunk row;
+                ask(0, row);
+                const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
+                tc::tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < BN / 64; ++c) {
+                    uint32_t r[32];
+                    tc::tmem_ld32(d0 + buf * BN + 32 * c, r);
+                    if (c > 0) ask(c, row);
+                    tc::tmem_wait_ld();
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = ok ? __uint_as_float(r[j]) : nan;
+                    out(c, v, row);
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(acce_lead + 8 * buf);
+                if (++buf == 2) { buf = 0; aphase ^= 1; }
+            } else {
+                float v[BN / 64][32];
+                for (int kk = 0; kk < n_k; kk += kSumSteps) {
+                    const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < BN / 64; ++c) {
+                        uint32_t r[32];
+                        tc::tmem_ld32(d0 + buf * BN + 32 * c, r);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float x = ok ? __uint_as_float(r[j]) : nan;
+                            v[c][j] = kk == 0 ? x : v[c][j] + x;
+                        }
+                    }
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(acce_lead + 8 * buf);
+                    if (++buf == 2) { buf = 0; aphase ^= 1; }
+                }
+#pragma unroll
+                for (int c = 0; c < BN / 64; ++c) {
+                    RowChunk row;
+                    ask(c, row);
+                    out(c, v[c], row);
+                }
+            }
+            __syncwarp();
         }
     }
     tc::tc_fence_before();
@@ -322,6 +516,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // --------------------------------------------------------------------- few
 
 constexpr int kFewThreads = 6 * 32;
+constexpr int kFewTmem = 256;   // columns of a CTA's accumulators, at most (two CTAs to an SM)
 
 template <int T>
 struct FewLayout {
@@ -332,7 +527,6 @@ struct FewLayout {
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int BAR_BYTES = 8 * (2 * NS + 2) + 16;
     static constexpr int SMEM = OFF_BAR + BAR_BYTES + 1024;
-    static constexpr int TMEM = T < 32 ? 32 : T;
     static_assert(T * 128 * 4 <= OFF_BAR, "the partial tile lies in the ring");
     static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs to an SM");
 };
@@ -344,12 +538,14 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 }
 
 // tw: the weights, whose rows (or, WMN, columns) are the tile's 128; tx: the tokens.
-// blockIdx.x: 128-row tile and rank in the cluster; blockIdx.y: token tile.
+// blockIdx.x: 128-row tile and rank in the cluster; blockIdx.y: token tile.  `sums`:
+// the stages of an accumulator (a float32 output's reduction takes several, for the
+// pairs' reason, added in registers at the end); `cols`: their columns.
 template <int T, bool WMN>
 __global__ void __launch_bounds__(kFewThreads)
     linear_few_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
-                      const __grid_constant__ Epi e, int n_k, int step_k, int split, uint32_t idesc, int f8,
-                      int stall) {
+                      const __grid_constant__ Epi e, int n_k, int step_k, int split, int sums, int cols,
+                      uint32_t idesc, int f8, int stall) {
     using L = FewLayout<T>;
     constexpr int NS = L::NS;
     extern __shared__ unsigned char smem_raw[];
@@ -381,7 +577,7 @@ __global__ void __launch_bounds__(kFewThreads)
         tc::prefetch_tmap(&tx);
     }
     if (warp == 1) {
-        tc::tmem_alloc(tmem_base_sh, L::TMEM);
+        tc::tmem_alloc(tmem_base_sh, cols);
         tc::tmem_relinquish();
     }
     tc::tc_fence_before();
@@ -424,13 +620,14 @@ __global__ void __launch_bounds__(kFewThreads)
                 tc::tc_fence_after();
                 const uint64_t wd = wd0 + (uint32_t)(stage * (L::STAGE >> 4));
                 const uint64_t xd = xd0 + (uint32_t)(stage * (L::STAGE >> 4));
+                const int in = (kk - k0) % sums;
+                const uint32_t d = tmem_base + (kk - k0) / sums * T;
                 if (!WMN && f8) {
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) umma_f8(tmem_base, wd + 2 * s, xd + 2 * s, idesc, (kk - k0) | s);
+                    for (int s = 0; s < 4; ++s) umma_f8(d, wd + 2 * s, xd + 2 * s, idesc, in | s);
                 } else {
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        tc::umma_f16(tmem_base, wd + kStep<WMN> * s, xd + 2 * s, idesc, (kk - k0) | s);
+                    for (int s = 0; s < 4; ++s) tc::umma_f16(d, wd + kStep<WMN> * s, xd + 2 * s, idesc, in | s);
                 }
                 tc::umma_commit(&empty[stage]);
                 if (++stage == NS) { stage = 0; phase ^= 1; }
@@ -450,15 +647,27 @@ __global__ void __launch_bounds__(kFewThreads)
         tc::tc_fence_after();
         float* part = reinterpret_cast<float*>(smem);
         // (after a failed wait copies may be in flight into the ring: the flag tells the cluster)
+        const int accs = (k1 - k0 + sums - 1) / sums;
+        const uint32_t d = tmem_base + ((uint32_t)(sub * 32) << 16);
 #pragma unroll 1
-        for (int c = 0; c < L::TMEM / 32; ++c) {
-            uint32_t r[32];
-            tc::tmem_ld32(tmem_base + ((uint32_t)(sub * 32) << 16) + 32 * c, r);
-            tc::tmem_wait_ld();
+        for (int c = 0; c < (T + 31) / 32; ++c) {
+            constexpr int W = T < 32 ? T : 32;  // columns of the chunk; T = 16: two accumulators a load
+            float v[W];
+#pragma unroll 1
+            for (int a = 0; a < accs; a += 32 / W) {
+                uint32_t r[32];
+                tc::tmem_ld32(d + a * T + 32 * c, r);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < W; ++j) v[j] = a == 0 ? __uint_as_float(r[j]) : v[j] + __uint_as_float(r[j]);
+                if (W < 32 && a + 1 < accs) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v[j] += __uint_as_float(r[32 - W + j]);
+                }
+            }
             if (ok) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (32 * c + j < T) part[(32 * c + j) * 128 + row] = __uint_as_float(r[j]);
+                for (int j = 0; j < W; ++j) part[(32 * c + j) * 128 + row] = v[j];
             }
         }
         if (!ok && lane == 0) *abort_flag = tc::kErrTimeoutAccFull;
@@ -468,7 +677,7 @@ __global__ void __launch_bounds__(kFewThreads)
     if (split > 1) tc::cluster_sync();
     if (warp == 1) {
         tc::tc_fence_after();
-        tc::tmem_dealloc(tmem_base, L::TMEM);
+        tc::tmem_dealloc(tmem_base, cols);
     }
     if (warp >= 2) {
         const int row = (warp & 3) * 32 + lane;
@@ -486,7 +695,7 @@ __global__ void __launch_bounds__(kFewThreads)
             }
         }
         if (n < e.N) {
-            const float bs = e.b_scale ? e.b_scale[n] : 1.f;
+            const float bs = e.unbias * (e.b_scale ? e.b_scale[n] : 1.f);
             const float bias = e.bias ? sb_elem(e.bias, n, e.bias_type) : 0.f;
             const int rows = (int)min((int64_t)T, e.M - m0);
             for (int t = rank; t < rows; t += split) {
@@ -518,8 +727,20 @@ bool map_operand(CUtensorMap* map, const LinOperand& o, int type, int64_t rows, 
                      : tmap_rows_sw128(map, o.p, bytes, rows, k, o.ld * bytes, 64);
 }
 
-Epi epi_of(const LinArgs& a) {
-    return Epi{a.M, a.N, a.a_scale, a.b_scale, a.bias, a.res, a.y, a.pre, a.ldr, a.bias_type, a.act, a.res_type, a.y_type};
+// What a sum of `k_steps` MMAs is multiplied by: each truncates half a step of the
+// running sum in the mean, which grows evenly to the result (measured 1.7e-8 of it).
+float unbias_of(int mmas) { return 1.f + 1.7e-8f * (float)mmas; }
+
+// `mmas`: of a tensor-core sum.
+Epi epi_of(const LinArgs& a, int mmas) {
+    const auto rows = [](const void* p, int64_t ld, int type, int by) {
+        return !p || (reinterpret_cast<uintptr_t>(p) % by == 0 && ld * type_bytes(type) % by == 0);
+    };
+    const auto all = [&](int by) {
+        return rows(a.y, a.N, a.y_type, by) && rows(a.pre, a.N, kSbF16, by) && rows(a.res, a.ldr, a.res_type, by);
+    };
+    return Epi{a.M, a.N, a.a_scale, a.b_scale, a.bias, a.res, a.y, a.pre, a.ldr, a.bias_type, a.act, a.res_type, a.y_type,
+               unbias_of(mmas), all(32) ? 32 : all(16) ? 16 : 0};
 }
 
 template <typename... P, typename... A>
@@ -546,7 +767,7 @@ int steps(const LinArgs& a, int* step) {
     return (int)((a.K + *step - 1) / *step);
 }
 
-template <int BN, bool AMN, bool BMN>
+template <int BN, bool AMN, bool BMN, bool SUMS>
 cudaError_t go_pair(const LinArgs& a, cudaStream_t st) {
     using L = PairLayout<BN, AMN, BMN>;
     CUtensorMap ta, tb;
@@ -556,8 +777,8 @@ cudaError_t go_pair(const LinArgs& a, cudaStream_t st) {
     const int n_k = steps(a, &step);
     const int64_t tiles = (a.M + 255) / 256 * ((a.N + BN - 1) / BN);
     const int pairs = (int)std::min<int64_t>(tiles, device_sms() / 2);
-    return launch_cluster(linear_pair_kernel<BN, AMN, BMN>, dim3((unsigned)(2 * pairs)), kPairThreads, L::SMEM, 2, st,
-                          ta, tb, epi_of(a), n_k, step, idesc_of(a.type, 256, BN, AMN, BMN), (int)(a.type == kE4m3),
+    return launch_cluster(linear_pair_kernel<BN, AMN, BMN, SUMS>, dim3((unsigned)(2 * pairs)), kPairThreads, L::SMEM, 2, st,
+                          ta, tb, epi_of(a, 4 * (SUMS ? std::min(n_k, kSumSteps) : n_k)), n_k, step, idesc_of(a.type, 256, BN, AMN, BMN), (int)(a.type == kE4m3),
                           a.stall);
 }
 
@@ -569,9 +790,17 @@ cudaError_t go_few(const LinArgs& a, int split, cudaStream_t st) {
         return cudaErrorInvalidValue;
     int step;
     const int n_k = steps(a, &step);
+    // a CTA's stages in one accumulator, or for float32 kSumSteps in each while they fit
+    const int share = (n_k + split - 1) / split;
+    int accs = 1;
+    if (a.y_type == kSbF32) accs = std::min(kFewTmem / T, (share + kSumSteps - 1) / kSumSteps);
+    const int sums = (share + accs - 1) / accs;
+    int cols = 32;
+    while (cols < accs * T) cols *= 2;
     const dim3 grid((unsigned)((a.N + 127) / 128 * split), (unsigned)((a.M + T - 1) / T));
-    return launch_cluster(linear_few_kernel<T, WMN>, grid, kFewThreads, L::SMEM, split, st, tw, tx, epi_of(a), n_k,
-                          step, split, idesc_of(a.type, 128, T, WMN, false), (int)(a.type == kE4m3), a.stall);
+    return launch_cluster(linear_few_kernel<T, WMN>, grid, kFewThreads, L::SMEM, split, st, tw, tx,
+                          epi_of(a, 4 * sums), n_k, step, split, sums, cols, idesc_of(a.type, 128, T, WMN, false),
+                          (int)(a.type == kE4m3), a.stall);
 }
 
 template <bool WMN>
@@ -586,19 +815,31 @@ cudaError_t pick_few(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
 
 template <bool AMN, bool BMN>
 cudaError_t pick_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
-    if (p.tile == 256) return go_pair<256, AMN, BMN>(a, st);
-    return go_pair<128, AMN, BMN>(a, st);
+    if constexpr (!AMN && !BMN) {
+        if (a.y_type == kSbF32) return go_pair<128, AMN, BMN, true>(a, st);
+    }
+    return p.tile == 256 ? go_pair<256, AMN, BMN, false>(a, st) : go_pair<128, AMN, BMN, false>(a, st);
 }
 
 // --------------------------------------------------------------- pad rows
 
+// Column blockIdx.x * 256 + thread of 8 rows at a time, whose loads are in flight
+// together.
 template <typename E>
 __global__ void __launch_bounds__(256) pad_rows_kernel(const E* src, int64_t ld, int64_t rows, int64_t cols, E* dst,
                                                        int64_t ldd) {
     tc::grid_dep_wait();
     const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (c >= cols) return;
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) dst[r * ldd + c] = src[r * ld + c];
+    for (int64_t r = 8 * (int64_t)blockIdx.y; r < rows; r += 8 * (int64_t)gridDim.y) {
+        E v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (r + i < rows) v[i] = src[(r + i) * ld + c];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (r + i < rows) dst[(r + i) * ldd + c] = v[i];
+    }
 }
 
 }  // namespace
@@ -618,7 +859,8 @@ LinPlan plan_linear(const LinArgs& a, int sms) {
         const int64_t tiles = (a.M + 255) / 256 * ((a.N + bn - 1) / bn), pairs = sms / 2;
         return (tiles + pairs - 1) / pairs * bn;
     };
-    return LinPlan{false, cost(128) < cost(256) ? 128 : 256, 1};
+    // (256 columns of sums in registers would not fit)
+    return LinPlan{false, a.y_type == kSbF32 || cost(128) < cost(256) ? 128 : 256, 1};
 }
 
 cudaError_t launch_linear(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
@@ -629,7 +871,7 @@ cudaError_t launch_linear(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
 
 cudaError_t launch_pad_rows(const void* src, int64_t ld, int64_t rows, int64_t cols, int bytes, void* dst,
                             int64_t ldd, cudaStream_t st) {
-    const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)std::min<int64_t>(rows, 2048));
+    const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)std::min<int64_t>((rows + 7) / 8, 4096));
     if (bytes == 1)
         return launch_after(pad_rows_kernel<uint8_t>, grid, dim3(256), st, static_cast<const uint8_t*>(src), ld, rows,
                             cols, static_cast<uint8_t*>(dst), ldd);
