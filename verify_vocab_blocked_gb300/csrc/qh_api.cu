@@ -407,11 +407,17 @@ int check_norm(const void* x, int x_dtype, int64_t ldx, int64_t M, int64_t H, co
 struct LinearPlan {
     bool pad_x = false, pad_w = false;
     int64_t ldx = 0, ldw = 0;          // of what the kernels read
-    size_t off_x = 0, off_w = 0;
+    size_t off_x = 0, off_w = 0, off_part = 0;
     // backward
     int64_t ldz = 0;
-    size_t off_dz = 0, off_part = 0, total = 0;
+    size_t off_dz = 0, off_db = 0, total = 0;
 };
+
+// The SMs that products are planned for (a machine without a GPU asks for sizes only).
+int linear_sms() {
+    const int n = qh::device_sms();
+    return n > 1 ? n : 152;
+}
 
 // 16-byte rows (a TMA map's rule).
 bool tma_rows(const void* p, int64_t ld, int bytes) { return !misaligned(p, 16) && ld * bytes % 16 == 0; }
@@ -458,8 +464,20 @@ LinearPlan plan_of_linear(const void* x, int dtype, int64_t ldx, int64_t M, int6
     if (bwd) {
         p.ldz = pitch(N);
         p.off_dz = take((size_t)M * p.ldz * bytes);
-        p.off_part = take(sizeof(float) * (size_t)qh::dz_chunks(M, N) * N);
+        p.off_db = take(sizeof(float) * (size_t)qh::dz_chunks(M, N) * N);
     }
+    // the products' shared tiles, one product after the other
+    const int sms = linear_sms();
+    const auto part = [&](int64_t m, int64_t n, int64_t k, bool a_k_major, int y_type) {
+        qh::LinArgs a{};
+        a.a.k_major = a_k_major;
+        a.type = dtype, a.y_type = y_type;
+        a.M = m, a.N = n, a.K = k;
+        return qh::plan_linear(a, sms).part_bytes;
+    };
+    // (a float32 output is planned in other tiles)
+    p.off_part = take(bwd ? std::max(part(M, K, N, true, dtype), part(N, K, M, false, dtype))
+                          : std::max(part(M, N, K, true, QHEAD_BF16), part(M, N, K, true, QHEAD_F32)));
     p.total = at;
     return p;
 }
@@ -1233,8 +1251,9 @@ int qhead_linear(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, co
     a.bias = bias, a.bias_type = bias_dtype, a.act = act;
     a.res = residual, a.res_type = res_dtype, a.ldr = ldr;
     a.y = y, a.y_type = y_dtype, a.pre = static_cast<__half*>(pre);
+    a.part = at<float>(workspace, p.off_part);
     a.stall = take_stall();
-    e = qh::launch_linear(a, qh::plan_linear(a, qh::device_sms()), st);
+    e = qh::launch_linear(a, qh::plan_linear(a, linear_sms()), st);
     return e ? cuda_fail(e, "linear") : QHEAD_OK;
 }
 
@@ -1269,18 +1288,19 @@ int qhead_linear_bwd(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K
     if ((products && !as_is) || dbias) {
         qh::DzArgs d{dy, dy_dtype, ldy, static_cast<const __half*>(pre), act, M, N,
                      products && !as_is ? const_cast<void*>(dz.p) : nullptr, p.ldz, dtype, dbias,
-                     at<float>(workspace, p.off_part)};
+                     at<float>(workspace, p.off_db)};
         if ((e = qh::launch_dz(d, st))) return cuda_fail(e, "linear_bwd dz");
     }
     qh::LinArgs a{};
     a.type = a.y_type = dtype;
     a.stall = stall;
+    a.part = at<float>(workspace, p.off_part);
     a.a = dz;
     if (dx) {
         if ((e = linear_operand(weight, ldw, N, K, dtype, p.pad_w, workspace, p.off_w, p.ldw, false, st, &a.b)))
             return cuda_fail(e, "linear_bwd weight");
         a.M = M, a.N = K, a.K = N, a.y = dx;
-        if ((e = qh::launch_linear(a, qh::plan_linear(a, qh::device_sms()), st))) return cuda_fail(e, "linear_bwd dx");
+        if ((e = qh::launch_linear(a, qh::plan_linear(a, linear_sms()), st))) return cuda_fail(e, "linear_bwd dx");
     }
     if (dweight) {
         if ((e = linear_operand(x, ldx, M, K, dtype, p.pad_x, workspace, p.off_x, p.ldx, false, st, &a.b)))
@@ -1288,7 +1308,7 @@ int qhead_linear_bwd(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K
         a.a = dz;
         a.a.k_major = false;
         a.M = N, a.N = K, a.K = M, a.y = dweight;
-        if ((e = qh::launch_linear(a, qh::plan_linear(a, qh::device_sms()), st)))
+        if ((e = qh::launch_linear(a, qh::plan_linear(a, linear_sms()), st)))
             return cuda_fail(e, "linear_bwd dweight");
     }
     return QHEAD_OK;

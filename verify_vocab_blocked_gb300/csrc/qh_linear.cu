@@ -76,6 +76,21 @@ struct Epi {
     int vec;           // bytes that the rows of y, pre and res are all aligned to: 32, 16 or 0
 };
 
+// What a pair walks: `full` whole tiles, then the others' parts, `split` of the
+// reduction each (one after another), whose sums go to part[item - full].
+struct Walk {
+    int full, items, split;
+    float* part;
+};
+__device__ __forceinline__ void item_of(const Walk& w, int i, int n_k, int& tile, int& k0, int& k1) {
+    tile = i, k0 = 0, k1 = n_k;
+    if (i < w.full) return;
+    const int j = i - w.full, s = j % w.split;
+    tile = w.full + j / w.split;
+    k0 = (int)((int64_t)n_k * s / w.split);
+    k1 = (int)((int64_t)n_k * (s + 1) / w.split);
+}
+
 // One output of row m and column n, whose column's scale (with `unbias`) and bias
 // are at hand.
 __device__ __forceinline__ void finish(const Epi& e, int64_t m, int64_t n, float v, float bs, float bias) {
@@ -211,6 +226,14 @@ struct RowChunk {
 
 // ------------------------------------------------------------------- pairs
 
+// One lane of a converged warp.  (The loops around it are run by the whole warp: the
+// compiler then keeps descriptors and barriers in uniform registers.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 template <int BN, bool AMN, bool BMN>
 struct PairLayout {
     static constexpr int A_BYTES = 128 * kRowBytes;      // this CTA's 128 rows of A
@@ -226,6 +249,7 @@ struct PairLayout {
 };
 constexpr int kPairThreads = 10 * 32;
 constexpr int kSumSteps = 4;   // stages of a tensor-core sum of a float32 output
+constexpr int kJoinStages = 12;  // stages in the time that joining a shared tile takes
 
 // The tiles in groups of 8 rows of tiles, columns outer: what the pairs work on at
 // a time is near-square, so that each operand's tiles are shared in L2.
@@ -277,7 +301,8 @@ constexpr uint32_t kStep = MN ? 128u : 2u;
 template <int BN, bool AMN, bool BMN, bool SUMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                       const __grid_constant__ Epi e, int n_k, int step_k, uint32_t idesc, int f8, int stall) {
+                       const __grid_constant__ Epi e, const Walk walk, int n_k, int step_k, uint32_t idesc, int f8,
+                       int stall) {
     using L = PairLayout<BN, AMN, BMN>;
     constexpr int NS = L::NS;
     extern __shared__ unsigned char smem_raw[];
@@ -294,7 +319,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_ctarank();
     const int n_mt = (int)((e.M + 255) / 256), n_nt = (int)((e.N + BN - 1) / BN);
-    const int tiles = n_mt * n_nt;
     const int first = (int)tc::cluster_id_x(), stride = (int)tc::nclusters_x();
 
     if (threadIdx.x == 0) {
@@ -325,18 +349,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tc::grid_dep_wait();
 
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, fills = 0;
-            bool ok = stall == 0;
-            const uint32_t full_lead = tc::mapa_shared(full, 0);
-            for (int t = first; t < tiles && ok; t += stride) {
-                int mt, nt;
-                tile_of(t, n_mt, n_nt, mt, nt);
-                const int m0 = mt * 256 + (int)rank * 128, n0 = nt * BN + (int)rank * (BN / 2);
-                for (int kk = 0; kk < n_k && ok; ++kk) {
-                    ok = tc::mbar_wait_cta(&empty[stage], phase ^ 1, abort_flag, err, tc::kErrTimeoutEmpty);
-                    if (!ok) break;
+        int stage = 0;
+        uint32_t phase = 0, fills = 0;
+        bool ok = stall == 0;
+        const uint32_t full_lead = tc::mapa_shared(full, 0);
+        for (int i = first; i < walk.items && ok; i += stride) {
+            int t, mt, nt, k0, k1;
+            item_of(walk, i, n_k, t, k0, k1);
+            tile_of(t, n_mt, n_nt, mt, nt);
+            const int m0 = mt * 256 + (int)rank * 128, n0 = nt * BN + (int)rank * (BN / 2);
+            for (int kk = k0; kk < k1; ++kk) {
+                ok = __all_sync(0xffffffffu,
+                                tc::mbar_wait_cta(&empty[stage], phase ^ 1, abort_flag, err, tc::kErrTimeoutEmpty));
+                if (!ok) break;
+                if (elect_one()) {
                     // both CTAs' copies count on the even CTA's barrier
                     if (rank == 0) tc::mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE);
                     unsigned char* A = smem + stage * L::STAGE;
@@ -355,55 +381,63 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     } else {
                         tma_load_pair(B, &tb, bar, k, n0);
                     }
-                    ++fills;
-                    if (++stage == NS) { stage = 0; phase ^= 1; }
                 }
+                __syncwarp();
+                ++fills;
+                if (++stage == NS) { stage = 0; phase ^= 1; }
             }
-            // The last stages are consumed (their commits reach both CTAs) before the CTA exits.
-            for (uint32_t i = fills > NS ? fills - NS : 0; i < fills && ok; ++i)
-                ok = tc::mbar_wait_cta(&empty[i % NS], (i / NS) & 1, abort_flag, err, tc::kErrTimeoutEmpty);
-            // And on any path every copy has landed: the even CTA's barriers count both CTAs'.
-            if (rank == 0) tc::drain_ring(full, NS, fills, err);
         }
+        // The last stages are consumed (their commits reach both CTAs) before the CTA exits.
+        for (uint32_t i = fills > NS ? fills - NS : 0; i < fills && ok; ++i)
+            ok = tc::mbar_wait_cta(&empty[i % NS], (i / NS) & 1, abort_flag, err, tc::kErrTimeoutEmpty);
+        // And on any path every copy has landed: the even CTA's barriers count both CTAs'.
+        if (rank == 0 && lane == 0) tc::drain_ring(full, NS, fills, err);
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             int stage = 0, buf = 0;
             uint32_t phase = 0, aphase = 0;
             const uint64_t ad0 = operand_desc<AMN>(tc::smem_u32(smem));
             const uint64_t bd0 = operand_desc<BMN>(tc::smem_u32(smem + L::A_BYTES));
             bool ok = true;
-            for (int t = first; t < tiles && ok; t += stride) {
-                for (int kk = 0; kk < n_k && ok; ++kk) {
-                    const bool begins = kk == 0 || (SUMS && kk % kSumSteps == 0);
+            for (int i = first; i < walk.items && ok; i += stride) {
+                int t, k0, k1;
+                item_of(walk, i, n_k, t, k0, k1);
+                for (int kk = k0; kk < k1; ++kk) {
+                    const bool begins = kk == k0 || (SUMS && (kk - k0) % kSumSteps == 0);
                     if (begins) {
-                        ok = tc::mbar_wait_cluster(&acce[buf], aphase ^ 1, abort_flag, err, tc::kErrTimeoutAccEmpty);
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&acce[buf], aphase ^ 1, abort_flag, err,
+                                                                           tc::kErrTimeoutAccEmpty));
                         if (!ok) break;
                         tc::tc_fence_after();
                     }
-                    ok = tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull);
+                    ok = __all_sync(0xffffffffu,
+                                    tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull));
                     if (!ok) break;
                     tc::tc_fence_after();
                     const uint32_t d = tmem_base + buf * BN;
                     const uint64_t ad = ad0 + (uint32_t)(stage * (L::STAGE >> 4));
                     const uint64_t bd = bd0 + (uint32_t)(stage * (L::STAGE >> 4));
-                    if (!AMN && !BMN && f8) {
+                    const bool ends = kk + 1 == k1 || (SUMS && (kk + 1 - k0) % kSumSteps == 0);
+                    if (elect_one()) {
+                        if (!AMN && !BMN && f8) {
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            umma_f8_pair(d, ad + 2 * s, bd + 2 * s, idesc, !begins || s != 0);
-                    } else {
+                            for (int s = 0; s < 4; ++s)
+                                umma_f8_pair(d, ad + 2 * s, bd + 2 * s, idesc, !begins || s != 0);
+                        } else {
 #pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            tc::umma_f16_pair(d, ad + kStep<AMN> * s, bd + kStep<BMN> * s, idesc, !begins || s != 0);
+                            for (int s = 0; s < 4; ++s)
+                                tc::umma_f16_pair(d, ad + kStep<AMN> * s, bd + kStep<BMN> * s, idesc,
+                                                  !begins || s != 0);
+                        }
+                        tc::umma_commit_pair(&empty[stage], kPairMask);
+                        if (ends) tc::umma_commit_pair(&accf[buf], kPairMask);
                     }
-                    tc::umma_commit_pair(&empty[stage], kPairMask);
+                    __syncwarp();
                     if (++stage == NS) { stage = 0; phase ^= 1; }
-                    if (kk + 1 == n_k || (SUMS && (kk + 1) % kSumSteps == 0)) {
-                        tc::umma_commit_pair(&accf[buf], kPairMask);
-                        if (++buf == 2) { buf = 0; aphase ^= 1; }
-                    }
+                    if (ends && ++buf == 2) { buf = 0; aphase ^= 1; }
                 }
             }
-            if (!ok) {
+            if (!ok && elect_one()) {
                 tc::umma_commit_pair(mdrain, 0x1);
                 tc::mbar_drain(mdrain, 0, err);
             }
@@ -417,9 +451,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const float nan = __int_as_float(0x7fc00000);
         int buf = 0;
         uint32_t aphase = 0;
-        for (int t = first; t < tiles; t += stride) {
-            int mt, nt;
+        for (int i = first; i < walk.items; i += stride) {
+            int t, mt, nt, k0, k1;
+            item_of(walk, i, n_k, t, k0, k1);
             tile_of(t, n_mt, n_nt, mt, nt);
+            float* part = i < walk.full ? nullptr
+                                        : walk.part + (int64_t)(i - walk.full) * 256 * BN +
+                                              (rank * 128 + sub * 32 + lane) * BN + half * (BN / 2);
             const int64_t m0 = (int64_t)mt * 256 + rank * 128 + sub * 32;
             const int64_t n0 = (int64_t)nt * BN + half * (BN / 2);
             const int rows = (int)min((int64_t)32, e.M - m0);  // (<= 0: none)
@@ -434,7 +472,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // f(c, v): the sums of the columns' c-th 32
             const auto out = [&](int c, const float (&v)[32], RowChunk& row) {
                 const int64_t n = n0 + 32 * c;
-                if (e.vec && n + 32 <= e.N) {
+                if (part) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        tc::st_global_v8(part + 32 * c + 8 * q, reinterpret_cast<const uint32_t*>(v + 8 * q));
+                } else if (e.vec && n + 32 <= e.N) {
                     float u[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) u[j] = v[j];
@@ -445,13 +487,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     for (int j = 0; j < 32; ++j) tr[lane * 33 + j] = v[j];
                     __syncwarp();
                     if (n + lane < e.N)
-                        for (int i = 0; i < rows; ++i)
-                            finish(e, m0 + i, n + lane, tr[i * 33 + lane], cs[32 * c + lane], cb[32 * c + lane]);
+                        for (int k = 0; k < rows; ++k)
+                            finish(e, m0 + k, n + lane, tr[k * 33 + lane], cs[32 * c + lane], cb[32 * c + lane]);
                     __syncwarp();
                 }
             };
             const auto ask = [&](int c, RowChunk& row) {
-                if (e.vec && n0 + 32 * c + 32 <= e.N && lane < rows) row.load(e, m0 + lane, n0 + 32 * c);
+                if (!part && e.vec && n0 + 32 * c + 32 <= e.N && lane < rows) row.load(e, m0 + lane, n0 + 32 * c);
             };
             if constexpr (!SUMS) {
                 RowChunk row;
@@ -475,7 +517,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (++buf == 2) { buf = 0; aphase ^= 1; }
             } else {
                 float v[BN / 64][32];
-                for (int kk = 0; kk < n_k; kk += kSumSteps) {
+                for (int kk = k0; kk < k1; kk += kSumSteps) {
                     const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
                     tc::tc_fence_after();
 #pragma unroll
@@ -486,7 +528,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const float x = ok ? __uint_as_float(r[j]) : nan;
-                            v[c][j] = kk == 0 ? x : v[c][j] + x;
+                            v[c][j] = kk == k0 ? x : v[c][j] + x;
                         }
                     }
                     tc::tc_fence_before();
@@ -510,6 +552,40 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == 1) {
         tc::tc_fence_after();
         tc::tmem_dealloc_pair(tmem_base, 2 * BN);
+    }
+}
+
+// The tiles whose reduction was shared: their parts' sums added in order, and the
+// epilogue.  A warp a row of a tile, 8 columns a lane; blockIdx.y: tile.
+template <int BN>
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ Epi e, const Walk walk) {
+    tc::grid_dep_wait();
+    const int n_mt = (int)((e.M + 255) / 256), n_nt = (int)((e.N + BN - 1) / BN);
+    int mt, nt;
+    tile_of(walk.full + blockIdx.y, n_mt, n_nt, mt, nt);
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int64_t m = (int64_t)mt * 256 + row;
+    if (m >= e.M) return;
+    const float* p = walk.part + (int64_t)blockIdx.y * walk.split * 256 * BN + row * BN;
+#pragma unroll
+    for (int h = 0; h < BN / 128; ++h) {
+        const int c = 128 * h + 4 * (threadIdx.x & 31);
+        const int64_t n = (int64_t)nt * BN + c;
+        if (n >= e.N) continue;
+        float4 v = *reinterpret_cast<const float4*>(p + c);
+#pragma unroll 4
+        for (int s = 1; s < walk.split; ++s) {
+            const float4 u = *reinterpret_cast<const float4*>(p + (int64_t)s * 256 * BN + c);
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
+        const float x[4] = {v.x, v.y, v.z, v.w};
+        const int cols = (int)min((int64_t)4, e.N - n);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j >= cols) break;
+            const float bs = e.unbias * (e.b_scale ? e.b_scale[n + j] : 1.f);
+            finish(e, m, n + j, x[j], bs, e.bias ? sb_elem(e.bias, n + j, e.bias_type) : 0.f);
+        }
     }
 }
 
@@ -588,12 +664,13 @@ __global__ void __launch_bounds__(kFewThreads)
 
     bool ok = true;
     if (warp == 0) {
-        if (lane == 0 && stall == 0) {
-            int stage = 0;
-            uint32_t phase = 0, fills = 0;
-            for (int kk = k0; kk < k1 && ok; ++kk) {
-                ok = tc::mbar_wait_cta(&empty[stage], phase ^ 1, abort_flag, err, tc::kErrTimeoutEmpty);
-                if (!ok) break;
+        int stage = 0;
+        uint32_t phase = 0, fills = 0;
+        for (int kk = k0; kk < k1 && stall == 0; ++kk) {
+            ok = __all_sync(0xffffffffu,
+                            tc::mbar_wait_cta(&empty[stage], phase ^ 1, abort_flag, err, tc::kErrTimeoutEmpty));
+            if (!ok) break;
+            if (elect_one()) {
                 tc::mbar_arrive_expect_tx(&full[stage], L::STAGE);
                 unsigned char* W = smem + stage * L::STAGE;
                 if constexpr (WMN) {
@@ -603,25 +680,27 @@ __global__ void __launch_bounds__(kFewThreads)
                     tc::tma_load_2d(W, &tw, &full[stage], kk * step_k, n0);
                 }
                 tc::tma_load_2d(W + L::W_BYTES, &tx, &full[stage], kk * step_k, m0);
-                ++fills;
-                if (++stage == NS) { stage = 0; phase ^= 1; }
             }
-            tc::drain_ring(full, NS, fills, err);  // (every copy has landed, on any path)
+            __syncwarp();
+            ++fills;
+            if (++stage == NS) { stage = 0; phase ^= 1; }
         }
+        if (lane == 0) tc::drain_ring(full, NS, fills, err);  // (every copy has landed, on any path)
     } else if (warp == 1) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0;
-            const uint64_t wd0 = operand_desc<WMN>(tc::smem_u32(smem));
-            const uint64_t xd0 = operand_desc<false>(tc::smem_u32(smem + L::W_BYTES));
-            for (int kk = k0; kk < k1 && ok; ++kk) {
-                ok = tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull);
-                if (!ok) break;
-                tc::tc_fence_after();
-                const uint64_t wd = wd0 + (uint32_t)(stage * (L::STAGE >> 4));
-                const uint64_t xd = xd0 + (uint32_t)(stage * (L::STAGE >> 4));
-                const int in = (kk - k0) % sums;
-                const uint32_t d = tmem_base + (kk - k0) / sums * T;
+        int stage = 0;
+        uint32_t phase = 0;
+        const uint64_t wd0 = operand_desc<WMN>(tc::smem_u32(smem));
+        const uint64_t xd0 = operand_desc<false>(tc::smem_u32(smem + L::W_BYTES));
+        for (int kk = k0; kk < k1; ++kk) {
+            ok = __all_sync(0xffffffffu,
+                            tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull));
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint64_t wd = wd0 + (uint32_t)(stage * (L::STAGE >> 4));
+            const uint64_t xd = xd0 + (uint32_t)(stage * (L::STAGE >> 4));
+            const int in = (kk - k0) % sums;
+            const uint32_t d = tmem_base + (kk - k0) / sums * T;
+            if (elect_one()) {
                 if (!WMN && f8) {
 #pragma unroll
                     for (int s = 0; s < 4; ++s) umma_f8(d, wd + 2 * s, xd + 2 * s, idesc, in | s);
@@ -630,14 +709,14 @@ __global__ void __launch_bounds__(kFewThreads)
                     for (int s = 0; s < 4; ++s) tc::umma_f16(d, wd + kStep<WMN> * s, xd + 2 * s, idesc, in | s);
                 }
                 tc::umma_commit(&empty[stage]);
-                if (++stage == NS) { stage = 0; phase ^= 1; }
+                if (kk + 1 == k1) tc::umma_commit(accf);
             }
-            if (ok) {
-                tc::umma_commit(accf);
-            } else {
-                tc::umma_commit(mdrain);
-                tc::mbar_drain(mdrain, 0, err);
-            }
+            __syncwarp();
+            if (++stage == NS) { stage = 0; phase ^= 1; }
+        }
+        if (!ok && elect_one()) {
+            tc::umma_commit(mdrain);
+            tc::mbar_drain(mdrain, 0, err);
         }
     } else {
         // Lane: a weight row; the accumulator's columns: tokens.  All MMAs, and with
@@ -729,6 +808,7 @@ bool map_operand(CUtensorMap* map, const LinOperand& o, int type, int64_t rows, 
 
 // What a sum of `k_steps` MMAs is multiplied by: each truncates half a step of the
 // running sum in the mean, which grows evenly to the result (measured 1.7e-8 of it).
+// Only float32 outputs show it.
 float unbias_of(int mmas) { return 1.f + 1.7e-8f * (float)mmas; }
 
 // `mmas`: of a tensor-core sum.
@@ -768,18 +848,24 @@ int steps(const LinArgs& a, int* step) {
 }
 
 template <int BN, bool AMN, bool BMN, bool SUMS>
-cudaError_t go_pair(const LinArgs& a, cudaStream_t st) {
+cudaError_t go_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
     using L = PairLayout<BN, AMN, BMN>;
     CUtensorMap ta, tb;
     if (!map_operand(&ta, a.a, a.type, a.M, a.K, 128) || !map_operand(&tb, a.b, a.type, a.N, a.K, BN / 2))
         return cudaErrorInvalidValue;
     int step;
     const int n_k = steps(a, &step);
-    const int64_t tiles = (a.M + 255) / 256 * ((a.N + BN - 1) / BN);
-    const int pairs = (int)std::min<int64_t>(tiles, device_sms() / 2);
-    return launch_cluster(linear_pair_kernel<BN, AMN, BMN, SUMS>, dim3((unsigned)(2 * pairs)), kPairThreads, L::SMEM, 2, st,
-                          ta, tb, epi_of(a, 4 * (SUMS ? std::min(n_k, kSumSteps) : n_k)), n_k, step, idesc_of(a.type, 256, BN, AMN, BMN), (int)(a.type == kE4m3),
-                          a.stall);
+    const int tiles = (int)((a.M + 255) / 256 * ((a.N + BN - 1) / BN));
+    const int full = p.split > 1 ? tiles / p.pairs * p.pairs : tiles;
+    const Walk walk{full, full + (tiles - full) * p.split, p.split, a.part};
+    const int pairs = std::min(walk.items, p.pairs);
+    const Epi e = epi_of(a, SUMS ? 4 * std::min(n_k, kSumSteps) : 0);
+    if (cudaError_t err = launch_cluster(linear_pair_kernel<BN, AMN, BMN, SUMS>, dim3((unsigned)(2 * pairs)),
+                                         kPairThreads, L::SMEM, 2, st, ta, tb, e, walk, n_k, step,
+                                         idesc_of(a.type, 256, BN, AMN, BMN), (int)(a.type == kE4m3), a.stall))
+        return err;
+    if (full == tiles) return cudaSuccess;
+    return launch_after(linear_join_kernel<BN>, dim3(32, (unsigned)(tiles - full)), dim3(256), st, e, walk);
 }
 
 template <int T, bool WMN>
@@ -799,7 +885,7 @@ cudaError_t go_few(const LinArgs& a, int split, cudaStream_t st) {
     while (cols < accs * T) cols *= 2;
     const dim3 grid((unsigned)((a.N + 127) / 128 * split), (unsigned)((a.M + T - 1) / T));
     return launch_cluster(linear_few_kernel<T, WMN>, grid, kFewThreads, L::SMEM, split, st, tw, tx,
-                          epi_of(a, 4 * sums), n_k, step, split, sums, cols, idesc_of(a.type, 128, T, WMN, false),
+                          epi_of(a, a.y_type == kSbF32 ? 4 * sums : 0), n_k, step, split, sums, cols, idesc_of(a.type, 128, T, WMN, false),
                           (int)(a.type == kE4m3), a.stall);
 }
 
@@ -816,9 +902,9 @@ cudaError_t pick_few(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
 template <bool AMN, bool BMN>
 cudaError_t pick_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
     if constexpr (!AMN && !BMN) {
-        if (a.y_type == kSbF32) return go_pair<128, AMN, BMN, true>(a, st);
+        if (p.tile == 128) return go_pair<128, AMN, BMN, true>(a, p, st);
     }
-    return p.tile == 256 ? go_pair<256, AMN, BMN, false>(a, st) : go_pair<128, AMN, BMN, false>(a, st);
+    return go_pair<256, AMN, BMN, false>(a, p, st);
 }
 
 // --------------------------------------------------------------- pad rows
@@ -845,22 +931,30 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const E* src, int64_t ld,
 }  // namespace
 
 LinPlan plan_linear(const LinArgs& a, int sms) {
-    const bool few_ok = a.a.k_major;
-    if (few_ok && a.M <= 128) {
-        const int tile = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
-        int step;
-        const int n_k = steps(a, &step);
+    LinPlan p{};
+    p.split = 1;
+    int step;
+    const int n_k = steps(a, &step);
+    if (a.a.k_major && a.M <= 128) {
+        p.few = true;
+        p.tile = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
         const int64_t tiles = (a.N + 127) / 128;
-        int split = 1;
-        while (split < 8 && tiles * split * 2 <= 2 * sms && split * 2 <= n_k) split *= 2;
-        return LinPlan{true, tile, split};
+        while (p.split < 8 && tiles * p.split * 2 <= 2 * sms && p.split * 2 <= n_k) p.split *= 2;
+        return p;
     }
-    const auto cost = [&](int bn) {
-        const int64_t tiles = (a.M + 255) / 256 * ((a.N + bn - 1) / bn), pairs = sms / 2;
-        return (tiles + pairs - 1) / pairs * bn;
-    };
     // (256 columns of sums in registers would not fit)
-    return LinPlan{false, a.y_type == kSbF32 || cost(128) < cost(256) ? 128 : 256, 1};
+    p.tile = a.y_type == kSbF32 ? 128 : 256;
+    p.pairs = std::max(1, sms / 2);
+    const int64_t tiles = (a.M + 255) / 256 * ((a.N + p.tile - 1) / p.tile);
+    const int tail = (int)(tiles % p.pairs);
+    // The tiles past the last full round shared by the idle pairs, in parts of 4 stages
+    // at least, where that takes more stages off the round than the join costs.
+    if (tail > 0) {
+        const int split = (int)std::min<int64_t>(p.pairs / tail, n_k / 4);
+        if (split > 1 && n_k - (n_k + split - 1) / split >= kJoinStages) p.split = split;
+    }
+    if (p.split > 1) p.part_bytes = sizeof(float) * (size_t)tail * p.split * 256 * p.tile;
+    return p;
 }
 
 cudaError_t launch_linear(const LinArgs& a, const LinPlan& p, cudaStream_t st) {

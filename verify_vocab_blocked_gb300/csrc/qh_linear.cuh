@@ -38,6 +38,7 @@ struct LinArgs {
     void* y;           // [M, N]
     int y_type;
     __half* pre;       // [M, N]
+    float* part;       // LinPlan::part_bytes
     int stall;         // test switch: no loads are issued, the waits expire
 };
 
@@ -45,7 +46,10 @@ struct LinArgs {
 struct LinPlan {
     bool few;          // tokens on the tile's short side (else CTA pairs)
     int tile;          // few: rows of A a tile (16 .. 128); pairs: columns a tile
-    int split;         // few: CTAs (of a cluster) that share a tile's reduction
+    int split;         // few: CTAs (of a cluster) that share a tile's reduction; pairs:
+                       // parts of the reduction of each tile past the last full round
+    int pairs;         // pairs: CTA pairs a round
+    size_t part_bytes; // pairs: the parts' sums, 32-byte aligned (LinArgs::part)
 };
 LinPlan plan_linear(const LinArgs& a, int sms);
 cudaError_t launch_linear(const LinArgs& a, const LinPlan& p, cudaStream_t st);
