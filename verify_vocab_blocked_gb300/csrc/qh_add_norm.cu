@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(G == 1 ? 128 : 32 * G) add_norm_kernel(const A
     const int t = G == 1 ? threadIdx.x & 31 : threadIdx.x;
     const int64_t r = G == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     if (G == 1 && r >= a.M) return;  // (whole warps)
     float v[NV][8];
     {
@@ -168,6 +169,7 @@ __global__ void __launch_bounds__(elem_block(NT)) add_norm_elem_kernel(const Add
     __shared__ float red[3][64];
     constexpr int warps = NT / 32, rows = NT == 32 ? kElemWarps : 1;
     tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     const int t = threadIdx.x % NT;
     const int64_t r = (int64_t)blockIdx.x * rows + threadIdx.x / NT;
     if (r >= a.M) return;  // (whole rows)

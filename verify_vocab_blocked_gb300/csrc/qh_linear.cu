@@ -248,7 +248,7 @@ struct PairLayout {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 constexpr int kPairThreads = 10 * 32;
-constexpr int kSumSteps = 4;   // stages of a tensor-core sum of a float32 output
+constexpr int kSumSteps = 16; // stages of a tensor-core sum of a float32 output
 constexpr int kJoinStages = 12;  // stages in the time that joining a shared tile takes
 
 // The tiles in groups of 8 rows of tiles, columns outer: what the pairs work on at
@@ -294,10 +294,11 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
 template <bool MN>
 constexpr uint32_t kStep = MN ? 128u : 2u;
 
-// SUMS: for float32 outputs.  The tensor cores' accumulation truncates, up to a step
-// of the running sum at each MMA; kSumSteps stages are summed there, and these sums
-// in registers, rounded to nearest (K = 1541: 2.1e-6 of the result's norm without,
-// beside 0.8e-6 of an fp32 product).
+// SUMS: for float32 outputs of 16-bit operands.  The tensor cores' accumulation
+// truncates, up to a step of the running sum at each MMA; kSumSteps stages are summed
+// there, and these sums in registers, rounded to nearest.  Error over the result's
+// norm at K = 1541: 2.1e-6 in one sum, 4e-7 so (4 stages 1.4e-7, but then the epilogue
+// sets the pace: 2048 x 2560 x 10240 in 196 us, 111 with 16), 3 to 7e-7 an fp32 product.
 template <int BN, bool AMN, bool BMN, bool SUMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -347,6 +348,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tc::tc_fence_after();
     const uint32_t tmem_base = *tmem_base_sh;
     tc::grid_dep_wait();
+    tc::grid_dep_trigger();
 
     if (warp == 0) {
         int stage = 0;
@@ -560,6 +562,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 template <int BN>
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ Epi e, const Walk walk) {
     tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     const int n_mt = (int)((e.M + 255) / 256), n_nt = (int)((e.N + BN - 1) / BN);
     int mt, nt;
     tile_of(walk.full + blockIdx.y, n_mt, n_nt, mt, nt);
@@ -661,6 +664,7 @@ __global__ void __launch_bounds__(kFewThreads)
     tc::tc_fence_after();
     const uint32_t tmem_base = *tmem_base_sh;
     tc::grid_dep_wait();
+    tc::grid_dep_trigger();
 
     bool ok = true;
     if (warp == 0) {
@@ -806,10 +810,11 @@ bool map_operand(CUtensorMap* map, const LinOperand& o, int type, int64_t rows, 
                      : tmap_rows_sw128(map, o.p, bytes, rows, k, o.ld * bytes, 64);
 }
 
-// What a sum of `k_steps` MMAs is multiplied by: each truncates half a step of the
-// running sum in the mean, which grows evenly to the result (measured 1.7e-8 of it).
-// Only float32 outputs show it.
-float unbias_of(int mmas) { return 1.f + 1.7e-8f * (float)mmas; }
+// What a float32 output's sum of `mmas` MMAs is multiplied by: each truncates part of a
+// step of the running sum.  Measured over K = 256 to 10240: 1.1e-8 of the result at each
+// for values of both signs, up to 2.5e-8 for positive ones; none for e4m3, whose
+// products have few bits.
+float unbias_of(int mmas, int type) { return type == kE4m3 ? 1.f : 1.f + 1.4e-8f * (float)mmas; }
 
 // `mmas`: of a tensor-core sum.
 Epi epi_of(const LinArgs& a, int mmas) {
@@ -820,7 +825,7 @@ Epi epi_of(const LinArgs& a, int mmas) {
         return rows(a.y, a.N, a.y_type, by) && rows(a.pre, a.N, kSbF16, by) && rows(a.res, a.ldr, a.res_type, by);
     };
     return Epi{a.M, a.N, a.a_scale, a.b_scale, a.bias, a.res, a.y, a.pre, a.ldr, a.bias_type, a.act, a.res_type, a.y_type,
-               unbias_of(mmas), all(32) ? 32 : all(16) ? 16 : 0};
+               unbias_of(mmas, a.type), all(32) ? 32 : all(16) ? 16 : 0};
 }
 
 template <typename... P, typename... A>
@@ -842,6 +847,9 @@ cudaError_t launch_cluster(void (*fn)(P...), dim3 grid, int threads, int smem, i
     return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(a)...);
 }
 
+// Whether the output asks for the tensor cores' sums to be short: see SUMS.
+bool in_sums(const LinArgs& a) { return a.y_type == kSbF32 && a.type != kE4m3; }
+
 int steps(const LinArgs& a, int* step) {
     *step = a.type == kE4m3 ? 128 : 64;
     return (int)((a.K + *step - 1) / *step);
@@ -859,7 +867,7 @@ cudaError_t go_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
     const int full = p.split > 1 ? tiles / p.pairs * p.pairs : tiles;
     const Walk walk{full, full + (tiles - full) * p.split, p.split, a.part};
     const int pairs = std::min(walk.items, p.pairs);
-    const Epi e = epi_of(a, SUMS ? 4 * std::min(n_k, kSumSteps) : 0);
+    const Epi e = epi_of(a, in_sums(a) ? 4 * std::min(n_k, kSumSteps) : 0);
     if (cudaError_t err = launch_cluster(linear_pair_kernel<BN, AMN, BMN, SUMS>, dim3((unsigned)(2 * pairs)),
                                          kPairThreads, L::SMEM, 2, st, ta, tb, e, walk, n_k, step,
                                          idesc_of(a.type, 256, BN, AMN, BMN), (int)(a.type == kE4m3), a.stall))
@@ -879,13 +887,13 @@ cudaError_t go_few(const LinArgs& a, int split, cudaStream_t st) {
     // a CTA's stages in one accumulator, or for float32 kSumSteps in each while they fit
     const int share = (n_k + split - 1) / split;
     int accs = 1;
-    if (a.y_type == kSbF32) accs = std::min(kFewTmem / T, (share + kSumSteps - 1) / kSumSteps);
+    if (in_sums(a)) accs = std::min(kFewTmem / T, (share + kSumSteps - 1) / kSumSteps);
     const int sums = (share + accs - 1) / accs;
     int cols = 32;
     while (cols < accs * T) cols *= 2;
     const dim3 grid((unsigned)((a.N + 127) / 128 * split), (unsigned)((a.M + T - 1) / T));
     return launch_cluster(linear_few_kernel<T, WMN>, grid, kFewThreads, L::SMEM, split, st, tw, tx,
-                          epi_of(a, a.y_type == kSbF32 ? 4 * sums : 0), n_k, step, split, sums, cols, idesc_of(a.type, 128, T, WMN, false),
+                          epi_of(a, in_sums(a) ? 4 * sums : 0), n_k, step, split, sums, cols, idesc_of(a.type, 128, T, WMN, false),
                           (int)(a.type == kE4m3), a.stall);
 }
 
@@ -915,6 +923,7 @@ template <typename E>
 __global__ void __launch_bounds__(256) pad_rows_kernel(const E* src, int64_t ld, int64_t rows, int64_t cols, E* dst,
                                                        int64_t ldd) {
     tc::grid_dep_wait();
+    tc::grid_dep_trigger();
     const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (c >= cols) return;
     for (int64_t r = 8 * (int64_t)blockIdx.y; r < rows; r += 8 * (int64_t)gridDim.y) {
@@ -943,7 +952,7 @@ LinPlan plan_linear(const LinArgs& a, int sms) {
         return p;
     }
     // (256 columns of sums in registers would not fit)
-    p.tile = a.y_type == kSbF32 ? 128 : 256;
+    p.tile = in_sums(a) && n_k > kSumSteps ? 128 : 256;
     p.pairs = std::max(1, sms / 2);
     const int64_t tiles = (a.M + 255) / 256 * ((a.N + p.tile - 1) / p.tile);
     const int tail = (int)(tiles % p.pairs);

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from dataclasses import dataclass
 
 import torch
@@ -813,7 +814,8 @@ def distill_bwd(head: Head, h: torch.Tensor, ids: torch.Tensor, tlogits: torch.T
 
 QHEAD_E4M3 = 3
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
-_OPERAND_CODE = {torch.float16: QHEAD_SB_F16, torch.bfloat16: QHEAD_SB_BF16, torch.float8_e4m3fn: QHEAD_E4M3}
+_HALF_CODE = {torch.float16: QHEAD_SB_F16, torch.bfloat16: QHEAD_SB_BF16}
+_OPERAND_CODE = {**_HALF_CODE, torch.float8_e4m3fn: QHEAD_E4M3}
 
 
 def _act_code(act: str) -> int:
@@ -823,22 +825,49 @@ def _act_code(act: str) -> int:
     return code
 
 
-def _check_operands(x: torch.Tensor, weight: torch.Tensor, types) -> int:
-    """x [M, K] and weight [N, K], of one of `types`; the type's code."""
+def _rows_of(name: str, t: torch.Tensor, n: int, K: int) -> int:
+    """The row stride of a matrix [n, K] whose rows are contiguous."""
+    if t.is_contiguous():
+        return K
+    if K > 1 and t.stride(1) != 1 or n > 1 and t.stride(0) < K:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return K if n <= 1 else max(t.stride(0), K)
+
+
+def _check_operands(x: torch.Tensor, weight: torch.Tensor, codes) -> tuple:
+    """x [M, K] and weight [N, K], of one of the types of `codes`: what the library's
+    calls and queries take of them (address, type, row stride, M, K, address, row
+    stride, N)."""
     if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor):
         raise ValueError("x and weight must be torch tensors")
-    if x.dtype not in types or weight.dtype != x.dtype:
-        names = ", ".join(str(t).replace("torch.", "") for t in types)
-        raise ValueError(f"x and weight must share one type of {names}, got {x.dtype} and {weight.dtype}")
-    if x.dim() != 2 or weight.dim() != 2 or x.shape[1] != weight.shape[1]:
-        raise ValueError(f"x must be [M, K] and weight [N, K], got {list(x.shape)} and {list(weight.shape)}")
+    dtype = x.dtype
+    code = codes.get(dtype)
+    if code is None or weight.dtype != dtype:
+        names = ", ".join(str(t).replace("torch.", "") for t in codes)
+        raise ValueError(f"x and weight must share one type of {names}, got {dtype} and {weight.dtype}")
+    xs, ws = x.shape, weight.shape
+    if len(xs) != 2 or len(ws) != 2 or xs[1] != ws[1]:
+        raise ValueError(f"x must be [M, K] and weight [N, K], got {list(xs)} and {list(ws)}")
     if weight.device != x.device:
         raise ValueError(f"weight is on {weight.device}, x on {x.device}")
-    for name, t in (("x", x), ("weight", weight)):
-        if not t.is_contiguous() and (t.shape[1] > 1 and t.stride(1) != 1
-                                      or t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-            raise ValueError(f"{name} must have contiguous rows that do not overlap")
-    return _OPERAND_CODE[x.dtype]
+    (M, K), N = xs, ws[0]
+    return x.data_ptr(), code, _rows_of("x", x, M, K), M, K, weight.data_ptr(), _rows_of("weight", weight, N, K), N
+
+
+_linear_sizes: dict = {}  # (query, device, what the operands' place and shape decide) -> its answer
+
+
+def _linear_size(query: str, place: tuple, dev) -> int:
+    """The workspace that the library asks for, asked for once a shape and alignment."""
+    p, code, ldx, M, K, q, ldw, N = place
+    key = (query, dev, p & 15, code, ldx, M, K, q & 15, ldw, N)
+    n = _linear_sizes.get(key)
+    if n is None:
+        n = _size(getattr(lib(), query)(*place))
+        if len(_linear_sizes) >= 1024:
+            _linear_sizes.clear()
+        _linear_sizes[key] = n
+    return n
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
@@ -850,21 +879,24 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     weight [N, K] in bfloat16 or float16, or in float8_e4m3fn with a float32
     scale for each row of both (norm_8bit()'s codes and scale for x).  With
     want_pre (y, pre): what linear_bwd() takes."""
-    code = _check_operands(x, weight, tuple(_OPERAND_CODE))
-    dev = x.device
-    (M, K), N = x.shape, weight.shape[0]
+    place = _check_operands(x, weight, _OPERAND_CODE)
+    code, M, N, dev = place[1], place[3], place[7], x.device
     a = _act_code(act)
     if (code == QHEAD_E4M3) != (x_scale is not None and w_scale is not None) \
             or (x_scale is None) != (w_scale is None):
         raise ValueError("x_scale and w_scale belong to float8_e4m3fn operands, which need both")
     if x_scale is not None:
         x_scale, w_scale = _f32("x_scale", x_scale, M, dev), _f32("w_scale", w_scale, N, dev)
+    b = b_code = r = r_code = None
     if bias is not None:
         _check_param("bias", bias, N, dev)
+        b, b_code = bias.data_ptr(), _SB_CODE[bias.dtype]
+    ldr = N
     if residual is not None:
         _check_matrix("residual", residual, dev, contiguous=False)
-        if tuple(residual.shape) != (M, N):
+        if residual.shape != (M, N):
             raise ValueError(f"residual must have shape [{M}, {N}], got {list(residual.shape)}")
+        r, r_code, ldr = residual.data_ptr(), _SB_CODE[residual.dtype], _row_stride(residual, M, N)
     if out_dtype is None:
         out_dtype = torch.bfloat16 if code == QHEAD_E4M3 else x.dtype
     out = _out_code(out_dtype)
@@ -872,16 +904,12 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     y = _out((M, N), out_dtype, dev, stream)
     pre = _out((M, N), torch.float16, dev, stream) if want_pre else None
     _reads(stream, None, x, weight, x_scale, w_scale, bias, residual, workspace)
-    L = lib()
-    place = (x.data_ptr(), code, _row_stride(x, M, K), M, K, weight.data_ptr(), _row_stride(weight, N, K), N)
     if workspace is None:
-        n = _size(L.qhead_linear_workspace(*place))
+        n = _linear_size("qhead_linear_workspace", place, dev)
         workspace = _scratch(n, dev, stream) if n else None
-    _check(L.qhead_linear(*place, _ptr(x_scale), _ptr(w_scale), _ptr(bias),
-                          0 if bias is None else _SB_CODE[bias.dtype], a, _ptr(residual),
-                          0 if residual is None else _SB_CODE[residual.dtype],
-                          N if residual is None else _row_stride(residual, M, N), y.data_ptr(), out, _ptr(pre),
-                          _ptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream, dev)))
+    _check(lib().qhead_linear(*place, _ptr(x_scale), _ptr(w_scale), b, b_code or 0, a, r, r_code or 0, ldr,
+                              y.data_ptr(), out, _ptr(pre), _ptr(workspace),
+                              0 if workspace is None else workspace.numel(), _stream(stream, dev)))
     return (y, pre) if want_pre else y
 
 
@@ -891,29 +919,25 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, pre: tor
     """(dx [M, K], dweight [N, K], dbias [N]), each of x's type or None where not
     wanted, for dy = d/dy (any float type) and linear()'s pre (act "none" needs
     none).  The residual's gradient is dy."""
-    code = _check_operands(x, weight, (torch.float16, torch.bfloat16))
-    dev = x.device
-    (M, K), N = x.shape, weight.shape[0]
+    place = _check_operands(x, weight, _HALF_CODE)
+    M, K, N, dev = place[3], place[4], place[7], x.device
     a = _act_code(act)
     _check_matrix("dy", dy, dev, contiguous=False)
-    if tuple(dy.shape) != (M, N):
+    if dy.shape != (M, N):
         raise ValueError(f"dy must have shape [{M}, {N}], got {list(dy.shape)}")
-    if a:
-        if not isinstance(pre, torch.Tensor) or pre.dtype != torch.float16 or tuple(pre.shape) != (M, N) \
-                or not pre.is_contiguous() or pre.device != dev:
-            raise ValueError(f"pre must be a contiguous float16 [{M}, {N}] tensor on {dev}")
+    if a and (not isinstance(pre, torch.Tensor) or pre.dtype != torch.float16 or pre.shape != (M, N)
+              or not pre.is_contiguous() or pre.device != dev):
+        raise ValueError(f"pre must be a contiguous float16 [{M}, {N}] tensor on {dev}")
     _usable(dev, stream, workspace)
     dx = _out((M, K), x.dtype, dev, stream) if want_dx else None
     dw = _out((N, K), x.dtype, dev, stream) if want_dw else None
     db = _out(N, x.dtype, dev, stream) if want_dbias else None
     _reads(stream, None, x, weight, dy, pre, workspace)
-    L = lib()
-    place = (x.data_ptr(), code, _row_stride(x, M, K), M, K, weight.data_ptr(), _row_stride(weight, N, K), N)
     if workspace is None:
-        workspace = _scratch(_size(L.qhead_linear_bwd_workspace(*place)), dev, stream)
-    _check(L.qhead_linear_bwd(*place, dy.data_ptr(), _SB_CODE[dy.dtype], _row_stride(dy, M, N), _ptr(pre) if a else None,
-                              a, _ptr(dx), _ptr(dw), _ptr(db), workspace.data_ptr(), workspace.numel(),
-                              _stream(stream, dev)))
+        workspace = _scratch(_linear_size("qhead_linear_bwd_workspace", place, dev), dev, stream)
+    _check(lib().qhead_linear_bwd(*place, dy.data_ptr(), _SB_CODE[dy.dtype], _row_stride(dy, M, N),
+                                  _ptr(pre) if a else None, a, _ptr(dx), _ptr(dw), _ptr(db), workspace.data_ptr(),
+                                  workspace.numel(), _stream(stream, dev)))
     return dx, dw, db
 
 
@@ -1027,15 +1051,23 @@ def _grad_list(name: str, tensors, dev=None):
     """(tensors as a list, their device, addresses, sizes and type codes as C arrays)."""
     ts = list(tensors)
     n = len(ts)
+    codes = []
     for t in ts:
-        if not isinstance(t, torch.Tensor) or t.dtype not in _SB_CODE or not t.is_contiguous():
+        code = _SB_CODE.get(t.dtype) if isinstance(t, torch.Tensor) else None
+        if code is None or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous float16, bfloat16 or float32 tensors")
+        codes.append(code)
+    for d in {t.device for t in ts}:
         if dev is None:
-            dev = t.device
-        if t.device != dev:
-            raise ValueError(f"{name} are on {t.device} and {dev}: they must be on one GPU")
-    return (ts, dev, (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts]),
-            (ctypes.c_int64 * n)(*[t.numel() for t in ts]), (ctypes.c_int * n)(*[_SB_CODE[t.dtype] for t in ts]))
+            dev = d
+        if d != dev:
+            raise ValueError(f"{name} are on {d} and {dev}: they must be on one GPU")
+    return (ts, dev, array("Q", [t.data_ptr() for t in ts]), array("q", [t.numel() for t in ts]),
+            array("i", codes))
+
+
+def _at(a) -> int | None:
+    return None if a is None else a.buffer_info()[0]
 
 
 def grad_norm(tensors, *, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -1049,7 +1081,7 @@ def grad_norm(tensors, *, workspace: torch.Tensor | None = None, stream=None) ->
     _reads(stream, None, *ts, workspace)
     if workspace is None:
         workspace = _scratch(_size(lib().qhead_grad_norm_workspace(len(ts))), dev, stream)
-    _check(lib().qhead_grad_norm(ptrs, sizes, types, len(ts), norm.data_ptr(), workspace.data_ptr(),
+    _check(lib().qhead_grad_norm(_at(ptrs), _at(sizes), _at(types), len(ts), norm.data_ptr(), workspace.data_ptr(),
                                  workspace.numel(), _stream(stream, dev)))
     return norm
 
@@ -1066,16 +1098,15 @@ def clip_grads(tensors, max_norm: float, *, out=None, workspace: torch.Tensor | 
     os_, optrs, otypes = [], None, None
     if out is not None:
         os_, _, optrs, osizes, otypes = _grad_list("out", out, dev)
-        if list(osizes) != list(sizes):
+        if osizes != sizes:
             raise ValueError("out must hold as many elements as tensors, tensor by tensor")
     _usable(dev, stream, workspace)
     norm = _out((), torch.float32, dev, stream)
     _reads(stream, None, *ts, *os_, workspace)
-    L = lib()
     if workspace is None:
-        workspace = _scratch(_size(L.qhead_grad_norm_workspace(len(ts))), dev, stream)
-    _check(L.qhead_clip_grads(ptrs, sizes, types, len(ts), max_norm, optrs, otypes, norm.data_ptr(),
-                              workspace.data_ptr(), workspace.numel(), _stream(stream, dev)))
+        workspace = _scratch(_size(lib().qhead_grad_norm_workspace(len(ts))), dev, stream)
+    _check(lib().qhead_clip_grads(_at(ptrs), _at(sizes), _at(types), len(ts), max_norm, _at(optrs), _at(otypes),
+                              norm.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream(stream, dev)))
     # (written behind autograd's back: what it has saved of them is no longer theirs)
-    torch.autograd.graph.increment_version([t for t in (ts if out is None else os_) if not t.is_inference()])
+    torch.autograd.graph.increment_version([t for t in os_ or ts if not t.is_inference()])
     return norm
