@@ -111,7 +111,6 @@ template <int MOST>
 __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ Table<MOST> t, double* part) {
     __shared__ double red[kThreads / 32];
     tc::grid_dep_wait();
-    tc::grid_dep_trigger();
     const int chunks = t.first[t.count];
     double sum = 0.0;
     for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -123,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
             sum += chunk_squares(static_cast<const T*>(t.p[i]) + at, n);
         });
     }
+    tc::grid_dep_trigger();  // (earlier, the next kernel's blocks would crowd some SMs)
     sum = block_sum(sum, red);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
@@ -136,7 +136,6 @@ __device__ __forceinline__ double norm_of(const double* part, int parts, double*
 __global__ void __launch_bounds__(kThreads) norm_kernel(const double* part, int parts, float* norm) {
     __shared__ double red[kThreads / 32];
     tc::grid_dep_wait();
-    tc::grid_dep_trigger();
     const double v = norm_of(part, parts, red);
     if (threadIdx.x == 0) *norm = (float)v;
 }
@@ -169,7 +168,6 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__
                                                          int parts, float max_norm, float* norm) {
     __shared__ double red[kThreads / 32];
     tc::grid_dep_wait();
-    tc::grid_dep_trigger();
     const double v = norm_of(part, parts, red);
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)v;
     float coef = (float)((double)max_norm / (v + 1e-6));

@@ -284,6 +284,17 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 
+// tc::tmem_wait_ld for a load issued earlier, whose registers nothing may read before.
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
 // Descriptor of an operand at `addr`: K-major rows of 128 bytes in 8-row atoms, or
 // MN-major blocks of 64 elements 8 KB apart (64 rows of K each).
 template <bool MN>
@@ -348,7 +359,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tc::tc_fence_after();
     const uint32_t tmem_base = *tmem_base_sh;
     tc::grid_dep_wait();
-    tc::grid_dep_trigger();
 
     if (warp == 0) {
         int stage = 0;
@@ -389,6 +399,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (++stage == NS) { stage = 0; phase ^= 1; }
             }
         }
+        tc::grid_dep_trigger();  // (earlier, the next kernel's blocks would crowd some SMs)
         // The last stages are consumed (their commits reach both CTAs) before the CTA exits.
         for (uint32_t i = fills > NS ? fills - NS : 0; i < fills && ok; ++i)
             ok = tc::mbar_wait_cta(&empty[i % NS], (i / NS) & 1, abort_flag, err, tc::kErrTimeoutEmpty);
@@ -497,25 +508,42 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const auto ask = [&](int c, RowChunk& row) {
                 if (!part && e.vec && n0 + 32 * c + 32 <= e.N && lane < rows) row.load(e, m0 + lane, n0 + 32 * c);
             };
+            // The accumulator has been read (nothing in memory is handed over: a release would
+            // wait for the warp's stores, 36 us instead of 2x at 256 x 2560 x 10240's dW).
+            const auto release = [&](int k) {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster_relaxed(acce_lead + 8 * k);
+            };
             if constexpr (!SUMS) {
                 RowChunk row;
                 ask(0, row);
                 const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
                 tc::tc_fence_after();
+                const uint32_t d = d0 + buf * BN;
+                uint32_t r[32];
+                tc::tmem_ld32(d, r);
+                tc::tmem_wait_ld();
 #pragma unroll 1
                 for (int c = 0; c < BN / 64; ++c) {
-                    uint32_t r[32];
-                    tc::tmem_ld32(d0 + buf * BN + 32 * c, r);
-                    if (c > 0) ask(c, row);
-                    tc::tmem_wait_ld();
                     float v[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = ok ? __uint_as_float(r[j]) : nan;
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                    if (!ok) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = nan;
+                    }
+                    if (c + 1 < BN / 64) {
+                        tc::tmem_ld32(d + 32 * (c + 1), r);  // (while these are finished)
+                    } else {
+                        release(buf);
+                    }
                     out(c, v, row);
+                    if (c + 1 < BN / 64) {
+                        ask(c + 1, row);
+                        tmem_wait_ld_of(r);
+                    }
                 }
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster(acce_lead + 8 * buf);
                 if (++buf == 2) { buf = 0; aphase ^= 1; }
             } else {
                 float v[BN / 64][32];
@@ -533,9 +561,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             v[c][j] = kk == k0 ? x : v[c][j] + x;
                         }
                     }
-                    tc::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster(acce_lead + 8 * buf);
+                    release(buf);
                     if (++buf == 2) { buf = 0; aphase ^= 1; }
                 }
 #pragma unroll
@@ -558,38 +584,53 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 }
 
 // The tiles whose reduction was shared: their parts' sums added in order, and the
-// epilogue.  A warp a row of a tile, 8 columns a lane; blockIdx.y: tile.
+// epilogue.  BN / 8 lanes a row of a tile, 8 columns each; blockIdx.y: tile.
+constexpr int kJoinThreads = 256;
 template <int BN>
-__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ Epi e, const Walk walk) {
+__global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const __grid_constant__ Epi e, const Walk walk) {
     tc::grid_dep_wait();
     tc::grid_dep_trigger();
+    constexpr int kLanes = BN / 8, kRows = kJoinThreads / kLanes;
     const int n_mt = (int)((e.M + 255) / 256), n_nt = (int)((e.N + BN - 1) / BN);
     int mt, nt;
     tile_of(walk.full + blockIdx.y, n_mt, n_nt, mt, nt);
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int64_t m = (int64_t)mt * 256 + row;
-    if (m >= e.M) return;
-    const float* p = walk.part + (int64_t)blockIdx.y * walk.split * 256 * BN + row * BN;
-#pragma unroll
-    for (int h = 0; h < BN / 128; ++h) {
-        const int c = 128 * h + 4 * (threadIdx.x & 31);
-        const int64_t n = (int64_t)nt * BN + c;
-        if (n >= e.N) continue;
-        float4 v = *reinterpret_cast<const float4*>(p + c);
+    const int row = blockIdx.x * kRows + threadIdx.x / kLanes, c = 8 * (threadIdx.x % kLanes);
+    const int64_t m = (int64_t)mt * 256 + row, n = (int64_t)nt * BN + c;
+    if (m >= e.M || n >= e.N) return;
+    const float* p = walk.part + (int64_t)blockIdx.y * walk.split * 256 * BN + row * BN + c;
+    const bool vec = e.vec && n + 8 <= e.N;
+    float v[8], r[8], u[8];
+    load8_wide(p, v);
+    if (vec && e.res) load8_as(e.res, m * e.ldr + n, e.res_type, r);
 #pragma unroll 4
-        for (int s = 1; s < walk.split; ++s) {
-            const float4 u = *reinterpret_cast<const float4*>(p + (int64_t)s * 256 * BN + c);
-            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
-        }
-        const float x[4] = {v.x, v.y, v.z, v.w};
-        const int cols = (int)min((int64_t)4, e.N - n);
+    for (int s = 1; s < walk.split; ++s) {
+        load8_wide(p + (int64_t)s * 256 * BN, u);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j >= cols) break;
-            const float bs = e.unbias * (e.b_scale ? e.b_scale[n + j] : 1.f);
-            finish(e, m, n + j, x[j], bs, e.bias ? sb_elem(e.bias, n + j, e.bias_type) : 0.f);
-        }
+        for (int j = 0; j < 8; ++j) v[j] += u[j];
     }
+    if (!vec) {
+        for (int j = 0; j < 8 && n + j < e.N; ++j)
+            finish(e, m, n + j, v[j], e.unbias * (e.b_scale ? e.b_scale[n + j] : 1.f),
+                   e.bias ? sb_elem(e.bias, n + j, e.bias_type) : 0.f);
+        return;
+    }
+    const float as = e.unbias * (e.a_scale ? e.a_scale[m] : 1.f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = fmaf(v[j] * as, e.b_scale ? e.b_scale[n + j] : 1.f, e.bias ? sb_elem(e.bias, n + j, e.bias_type) : 0.f);
+    if (e.pre) {
+        __half h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = pre_of(v[j]);
+        *reinterpret_cast<uint4*>(e.pre + m * e.N + n) = *reinterpret_cast<const uint4*>(h);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = activate(v[j], e.act);
+    if (e.res) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += r[j];
+    }
+    store8_as(e.y, m * e.N + n, e.y_type, v);
 }
 
 // --------------------------------------------------------------------- few
@@ -610,14 +651,119 @@ struct FewLayout {
     static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs to an SM");
 };
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+// Four consecutive elements as they lie in memory (16 bits: two words), and widened.
+__device__ __forceinline__ uint4 load4(const void* p, int64_t i, int type) {
+    if (type == kSbF32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __half*>(p) + i);  // (16 bits)
+    return make_uint4(u.x, u.y, 0u, 0u);
+}
+__device__ __forceinline__ void add4(float (&v)[4], uint4 u, int type) {
+    if (type == kSbF32) {
+        v[0] += __uint_as_float(u.x), v[1] += __uint_as_float(u.y);
+        v[2] += __uint_as_float(u.z), v[3] += __uint_as_float(u.w);
+    } else if (type == kSbBf16) {
+        v[0] += __uint_as_float(u.x << 16), v[1] += __uint_as_float(u.x & 0xffff0000u);
+        v[2] += __uint_as_float(u.y << 16), v[3] += __uint_as_float(u.y & 0xffff0000u);
+    } else {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+        v[0] += a.x, v[1] += a.y, v[2] += b.x, v[3] += b.y;
+    }
+}
+
+// The outputs of a CTA's share of the tokens (every S-th, S the CTAs that share the
+// reduction), a warp a token: a lane adds four columns' partial sums of all ranks, in
+// order.  Four tokens a step, whose loads are in flight together.  part: the partial
+// tile, [token][128] in every rank's shared memory.
+template <int S>
+__device__ __forceinline__ void few_outputs(const Epi& e, uint32_t part, int rank, int warp, int64_t m0, int rows,
+                                            int64_t n0, bool bad) {
+    constexpr int U = S > 4 ? 2 : 4;
+    const int lane = threadIdx.x & 31;
+    const int64_t n = n0 + 4 * lane;
+    if (n >= e.N) return;
+    uint32_t base[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) base[s] = at_rank(part + 16 * lane, s);
+    float bs[4], bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const bool in = n + j < e.N;
+        bs[j] = e.unbias * (e.b_scale && in ? e.b_scale[n + j] : 1.f);
+        bias[j] = e.bias && in ? sb_elem(e.bias, n + j, e.bias_type) : 0.f;
+    }
+    const bool vec = e.vec && n + 4 <= e.N;
+    for (int t0 = rank + S * warp; t0 < rows; t0 += 4 * S * U) {
+        float v[U][4];
+        uint4 r[U];
+        float as[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + 4 * S * u;
+            if (t >= rows) continue;
+            if (vec && e.res) r[u] = load4(e.res, (m0 + t) * e.ldr + n, e.res_type);
+            as[u] = e.a_scale ? e.a_scale[m0 + t] : 1.f;
+            float4 x[S];
+#pragma unroll
+            for (int s = 0; s < S; ++s) x[s] = ld_cluster4(base[s] + t * 512);
+            v[u][0] = x[0].x, v[u][1] = x[0].y, v[u][2] = x[0].z, v[u][3] = x[0].w;
+#pragma unroll
+            for (int s = 1; s < S; ++s) v[u][0] += x[s].x, v[u][1] += x[s].y, v[u][2] += x[s].z, v[u][3] += x[s].w;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + 4 * S * u;
+            if (t >= rows) continue;
+            const int64_t m = m0 + t, at = m * e.N + n;
+            if (bad) v[u][0] = v[u][1] = v[u][2] = v[u][3] = __int_as_float(0x7fc00000);
+            if (!vec) {
+                for (int j = 0; j < 4 && n + j < e.N; ++j) finish(e, m, n + j, v[u][j], bs[j], bias[j]);
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[u][j] = fmaf(v[u][j] * as[u], bs[j], bias[j]);
+            if (e.pre) {
+                __half h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = pre_of(v[u][j]);
+                *reinterpret_cast<uint2*>(e.pre + at) = *reinterpret_cast<const uint2*>(h);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[u][j] = activate(v[u][j], e.act);
+            if (e.res) add4(v[u], r[u], e.res_type);
+            if (e.y_type == kSbF32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(e.y) + at) =
+                    make_float4(v[u][0], v[u][1], v[u][2], v[u][3]);
+            } else {
+                *reinterpret_cast<uint2*>(static_cast<__half*>(e.y) + at) =  // (16 bits)
+                    make_uint2(pack2(v[u][0], v[u][1], e.y_type), pack2(v[u][2], v[u][3], e.y_type));
+            }
+        }
+    }
 }
 
 // tw: the weights, whose rows (or, WMN, columns) are the tile's 128; tx: the tokens.
-// blockIdx.x: 128-row tile and rank in the cluster; blockIdx.y: token tile.  `sums`:
+// blockIdx.x: 128-row tile and rank in the cluster of `split` (at most 8);
+// blockIdx.y: token tile.  `sums`:
 // the stages of an accumulator (a float32 output's reduction takes several, for the
 // pairs' reason, added in registers at the end); `cols`: their columns.
 template <int T, bool WMN>
@@ -763,32 +909,21 @@ __global__ void __launch_bounds__(kFewThreads)
         tc::tmem_dealloc(tmem_base, cols);
     }
     if (warp >= 2) {
-        const int row = (warp & 3) * 32 + lane;
-        const int64_t n = (int64_t)n0 + row;
         const uint32_t part = tc::smem_u32(smem), flag = tc::smem_u32(const_cast<int*>(abort_flag));
-        uint32_t base[8];
         bool bad = false;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            if (s < split) {
-                uint32_t f;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(base[s]) : "r"(part), "r"(s));
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(f) : "r"(flag), "r"(s));
-                bad |= __float_as_int(ld_cluster(f)) != 0;
-            }
-        }
-        if (n < e.N) {
-            const float bs = e.unbias * (e.b_scale ? e.b_scale[n] : 1.f);
-            const float bias = e.bias ? sb_elem(e.bias, n, e.bias_type) : 0.f;
-            const int rows = (int)min((int64_t)T, e.M - m0);
-            for (int t = rank; t < rows; t += split) {
-                float v[8], sum = 0.f;
-#pragma unroll
-                for (int s = 0; s < 8; ++s) v[s] = s < split ? ld_cluster(base[s] + (t * 128 + row) * 4) : 0.f;
-#pragma unroll
-                for (int s = 0; s < 8; ++s) sum += v[s];
-                finish(e, m0 + t, n, bad ? __int_as_float(0x7fc00000) : sum, bs, bias);
-            }
+        for (int s = 0; s < split; ++s) bad |= ld_cluster(at_rank(flag, s)) != 0;
+        const int rows = (int)min((int64_t)T, e.M - m0);
+        switch (split) {
+#define QH_SHARE(S) case S: few_outputs<S>(e, part, rank, warp - 2, m0, rows, n0, bad); break
+            QH_SHARE(1);
+            QH_SHARE(2);
+            QH_SHARE(3);
+            QH_SHARE(4);
+            QH_SHARE(5);
+            QH_SHARE(6);
+            QH_SHARE(7);
+            QH_SHARE(8);
+#undef QH_SHARE
         }
     }
     if (split > 1) tc::cluster_sync();  // no CTA leaves while its partial tile is read
@@ -873,7 +1008,8 @@ cudaError_t go_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
                                          idesc_of(a.type, 256, BN, AMN, BMN), (int)(a.type == kE4m3), a.stall))
         return err;
     if (full == tiles) return cudaSuccess;
-    return launch_after(linear_join_kernel<BN>, dim3(32, (unsigned)(tiles - full)), dim3(256), st, e, walk);
+    return launch_after(linear_join_kernel<BN>, dim3(256 * BN / 8 / kJoinThreads, (unsigned)(tiles - full)),
+                        dim3(kJoinThreads), st, e, walk);
 }
 
 template <int T, bool WMN>
@@ -944,11 +1080,19 @@ LinPlan plan_linear(const LinArgs& a, int sms) {
     p.split = 1;
     int step;
     const int n_k = steps(a, &step);
-    if (a.a.k_major && a.M <= 128) {
+    // Few rows: tiles of the rows' own number up to 64.  65 to 256 rows go as several
+    // tiles of 64 while these leave three parts of the reduction each (128 x 2560 x 2560:
+    // 10.2 us, in one tile of 128 12.2, on pairs 13.4; 200 rows: 12.6, 13.7 on pairs),
+    // up to 128 else in one of 128 (128 x 2560 x 10240: 19.2 us, 28 in two, 20.3 on pairs).
+    const int64_t strips = (a.N + 127) / 128, most = sms * 8 / 5;
+    const bool several = strips * ((a.M + 63) / 64) * 3 <= most;
+    if (a.a.k_major && (a.M <= 128 || (a.M <= 256 && several))) {
         p.few = true;
-        p.tile = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
-        const int64_t tiles = (a.N + 127) / 128;
-        while (p.split < 8 && tiles * p.split * 2 <= 2 * sms && p.split * 2 <= n_k) p.split *= 2;
+        p.tile = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 || several ? 64 : 128;
+        // about 1.6 CTAs to an SM (two fit): fewer leave SMs idle, more queue (5 x 2560 x
+        // 10240, 80 strips: 13.5 us in 3 parts, 13.8 in 2, 19.2 in 4)
+        const int64_t tiles = strips * ((a.M + p.tile - 1) / p.tile);
+        p.split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, n_k), most / tiles));
         return p;
     }
     // (256 columns of sums in registers would not fit)

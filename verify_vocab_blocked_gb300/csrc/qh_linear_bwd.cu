@@ -85,7 +85,6 @@ __global__ void __launch_bounds__(32 * kWarps) dz_kernel(const DzArgs a, int64_t
     __shared__ float sums[kWarps][kCols];
     constexpr int kRows = DB == 4 ? 2 : 4;
     tc::grid_dep_wait();
-    tc::grid_dep_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c0 = (int64_t)blockIdx.x * kCols + 8 * lane;
     const int64_t r1 = min(a.M, ((int64_t)blockIdx.y + 1) * run);
@@ -119,6 +118,7 @@ __global__ void __launch_bounds__(32 * kWarps) dz_kernel(const DzArgs a, int64_t
             }
         }
     }
+    tc::grid_dep_trigger();
     if (!a.db) return;
 #pragma unroll
     for (int e = 0; e < 8; e += 4)
@@ -130,7 +130,6 @@ __global__ void __launch_bounds__(32 * kWarps) dz_kernel(const DzArgs a, int64_t
 __global__ void __launch_bounds__(32 * kWarps) dz_elem_kernel(const DzArgs a, int64_t run) {
     __shared__ float sums[kWarps][kCols];
     tc::grid_dep_wait();
-    tc::grid_dep_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c0 = (int64_t)blockIdx.x * kCols + lane;
     const int64_t r1 = min(a.M, ((int64_t)blockIdx.y + 1) * run);
@@ -155,6 +154,7 @@ __global__ void __launch_bounds__(32 * kWarps) dz_elem_kernel(const DzArgs a, in
             else static_cast<__half*>(a.dz)[at] = __float2half_rn(g[e]);
         }
     }
+    tc::grid_dep_trigger();
     if (!a.db) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[warp][lane + 32 * e] = acc[e];
@@ -167,7 +167,6 @@ __global__ void __launch_bounds__(32 * kJoinRows) db_join_kernel(const float* pa
                                                                  int type) {
     __shared__ float sh[kJoinRows][33];
     tc::grid_dep_wait();
-    tc::grid_dep_trigger();
     const int64_t n = (int64_t)blockIdx.x * 32 + threadIdx.x;
     const int y = threadIdx.y;
     float s = 0.f;

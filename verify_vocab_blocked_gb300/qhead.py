@@ -1051,17 +1051,13 @@ def _grad_list(name: str, tensors, dev=None):
     """(tensors as a list, their device, addresses, sizes and type codes as C arrays)."""
     ts = list(tensors)
     n = len(ts)
-    codes = []
-    for t in ts:
-        code = _SB_CODE.get(t.dtype) if isinstance(t, torch.Tensor) else None
-        if code is None or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous float16, bfloat16 or float32 tensors")
-        codes.append(code)
-    for d in {t.device for t in ts}:
-        if dev is None:
-            dev = d
-        if d != dev:
-            raise ValueError(f"{name} are on {d} and {dev}: they must be on one GPU")
+    codes = [_SB_CODE.get(t.dtype, -1) if isinstance(t, torch.Tensor) else -1 for t in ts]
+    if -1 in codes or not all([t.is_contiguous() for t in ts]):
+        raise ValueError(f"{name} must be contiguous float16, bfloat16 or float32 tensors")
+    if ts and dev is None:
+        dev = ts[0].device
+    if len({t.get_device() for t in ts}) > 1 or ts and ts[0].device != dev:
+        raise ValueError(f"{name} must be on one GPU{'' if dev is None else f', {dev}'}")
     return (ts, dev, array("Q", [t.data_ptr() for t in ts]), array("q", [t.numel() for t in ts]),
             array("i", codes))
 
