@@ -40,7 +40,10 @@ __device__ __forceinline__ float activate(float z, int act) {
     switch (act) {
         case kActRelu: return z < 0.f ? 0.f : z;  // (keeps NaN)
         case kActSilu: return __fdividef(z, 1.f + __expf(-z));
-        case kActGelu: return 0.5f * z * (1.f + erff(z * 0.70710678f));
+        case kActGelu: {
+            const float h = normal_tail(z).x;
+            return z * (z < 0.f ? h : 1.f - h);
+        }
         case kActGeluTanh: {  // 0.5 (1 + tanh u) = 1 / (1 + exp(-2u))
             const float u2 = 1.5957691216f * fmaf(0.044715f * z * z, z, z);
             return __fdividef(z, 1.f + __expf(-u2));
@@ -49,11 +52,14 @@ __device__ __forceinline__ float activate(float z, int act) {
     }
 }
 
-// fp16 of the pre-activation, for the gradient: beyond fp16's range every
-// activation's derivative is what it is at the range's end, so that it saturates.
-__device__ __forceinline__ __half pre_of(float z) {
-    return __float2half_rn(z != z ? z : fminf(fmaxf(z, -65504.f), 65504.f));
+// The pre-activation as it is kept for the gradient, in fp16: beyond fp16's range every
+// activation's derivative is what it is at the range's end, so that it saturates (NaN
+// stays).
+__device__ __forceinline__ float in_half(float z) {
+    asm("max.NaN.f32 %0, %0, 0fC77FE000;\n\tmin.NaN.f32 %0, %0, 0f477FE000;" : "+f"(z));  // -+ 65504
+    return z;
 }
+__device__ __forceinline__ __half pre_of(float z) { return __float2half_rn(in_half(z)); }
 
 __device__ __forceinline__ void put(void* p, int64_t i, int type, float v) {
     if (type == kSbF32) static_cast<float*>(p)[i] = v;
@@ -135,94 +141,94 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int type) {
 }
 
 template <int ACT>
-__device__ __forceinline__ void activate32(float (&v)[32]) {
+__device__ __forceinline__ void activate16(float (&v)[16]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = activate(v[j], ACT);
+    for (int j = 0; j < 16; ++j) v[j] = activate(v[j], ACT);
 }
 
-// A thread's 32 consecutive columns of row m, all in range; cs, cb: their scales and
-// biases in shared memory.  The residual's loads go out before the caller's
-// accumulator is waited for (`load`) and are used here.
-struct RowChunk {
-    uint32_t r[32];  // the residual's words (16 of a 2-byte type)
+// A thread's 16 consecutive columns, all in range, of row m: the residual's words
+// (8 of a 2-byte type), asked for ahead.
+struct Residual {
+    uint32_t r[16];
     __device__ __forceinline__ void load(const Epi& e, int64_t m, int64_t n) {
-        if (!e.res) return;
         if (e.res_type == kSbF32) {
             const float* p = static_cast<const float*>(e.res) + m * e.ldr + n;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) ld32(p + 8 * q, r + 8 * q, e.vec);
+            ld32(p, r, e.vec);
+            ld32(p + 8, r + 8, e.vec);
         } else {
-            const __half* p = static_cast<const __half*>(e.res) + m * e.ldr + n;  // (16 bits)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) ld32(p + 16 * q, r + 8 * q, e.vec);
+            ld32(static_cast<const __half*>(e.res) + m * e.ldr + n, r, e.vec);  // (16 bits)
         }
     }
-    __device__ __forceinline__ void finish(const Epi& e, int64_t m, int64_t n, float (&v)[32], const float* cs,
-                                           const float* cb) {
-        const float as = e.a_scale ? e.a_scale[m] : 1.f;
+    __device__ __forceinline__ void add(const Epi& e, float (&v)[16]) const {
+        if (e.res_type == kSbF32) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-            const float4 s = *reinterpret_cast<const float4*>(cs + j), b = *reinterpret_cast<const float4*>(cb + j);
-            v[j] = fmaf(v[j] * as, s.x, b.x);
-            v[j + 1] = fmaf(v[j + 1] * as, s.y, b.y);
-            v[j + 2] = fmaf(v[j + 2] * as, s.z, b.z);
-            v[j + 3] = fmaf(v[j + 3] * as, s.w, b.w);
-        }
-        const int64_t at = m * e.N + n;
-        uint32_t w[16];
-        if (e.pre) {
+            for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
+        } else if (e.res_type == kSbBf16) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const __half2 h = __halves2half2(pre_of(v[2 * j]), pre_of(v[2 * j + 1]));
-                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int j = 0; j < 8; ++j) {
+                v[2 * j] += __uint_as_float(r[j] << 16);
+                v[2 * j + 1] += __uint_as_float(r[j] & 0xffff0000u);
             }
-            st32(e.pre + at, w, e.vec);
-            st32(e.pre + at + 16, w + 8, e.vec);
-        }
-        switch (e.act) {
-            case kActRelu: activate32<kActRelu>(v); break;
-            case kActSilu: activate32<kActSilu>(v); break;
-            case kActGelu: activate32<kActGelu>(v); break;
-            case kActGeluTanh: activate32<kActGeluTanh>(v); break;
-            default: break;
-        }
-        if (e.res) {
-            if (e.res_type == kSbF32) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
-            } else if (e.res_type == kSbBf16) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    v[2 * j] += __uint_as_float(r[j] << 16);
-                    v[2 * j + 1] += __uint_as_float(r[j] & 0xffff0000u);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[j]));
-                    v[2 * j] += f.x;
-                    v[2 * j + 1] += f.y;
-                }
-            }
-        }
-        if (e.y_type == kSbF32) {
-            float* p = static_cast<float*>(e.y) + at;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) st32(p + 8 * q, reinterpret_cast<const uint32_t*>(v + 8 * q), e.vec);
         } else {
-            __half* p = static_cast<__half*>(e.y) + at;  // (16 bits)
-            if (e.y_type == kSbBf16) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], kSbBf16);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], kSbF16);
+            for (int j = 0; j < 8; ++j) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[j]));
+                v[2 * j] += f.x;
+                v[2 * j + 1] += f.y;
             }
-            st32(p, w, e.vec);
-            st32(p + 16, w + 8, e.vec);
         }
     }
 };
+
+// These outputs from their sums v; cs, cb: the columns' scales and biases in shared
+// memory.
+__device__ __forceinline__ void finish16(const Epi& e, int64_t m, int64_t n, float (&v)[16], const float* cs,
+                                         const float* cb, const Residual& res) {
+    if (e.b_scale || e.unbias != 1.f) {
+        const float as = e.a_scale ? e.a_scale[m] : 1.f;
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+            const float4 s = *reinterpret_cast<const float4*>(cs + j);
+            v[j] *= as * s.x, v[j + 1] *= as * s.y, v[j + 2] *= as * s.z, v[j + 3] *= as * s.w;
+        }
+    }
+    if (e.bias) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(cb + j);
+            v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
+        }
+    }
+    const int64_t at = m * e.N + n;
+    uint32_t w[8];
+    if (e.pre) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = pack2(in_half(v[2 * j]), in_half(v[2 * j + 1]), kSbF16);
+        st32(e.pre + at, w, e.vec);
+    }
+    switch (e.act) {
+        case kActRelu: activate16<kActRelu>(v); break;
+        case kActSilu: activate16<kActSilu>(v); break;
+        case kActGelu: activate16<kActGelu>(v); break;
+        case kActGeluTanh: activate16<kActGeluTanh>(v); break;
+        default: break;
+    }
+    if (e.res) res.add(e, v);
+    if (e.y_type == kSbF32) {
+        float* p = static_cast<float*>(e.y) + at;
+        st32(p, reinterpret_cast<const uint32_t*>(v), e.vec);
+        st32(p + 8, reinterpret_cast<const uint32_t*>(v + 8), e.vec);
+    } else {
+        if (e.y_type == kSbBf16) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], kSbBf16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], kSbF16);
+        }
+        st32(static_cast<__half*>(e.y) + at, w, e.vec);  // (16 bits)
+    }
+}
 
 // ------------------------------------------------------------------- pairs
 
@@ -234,6 +240,9 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+constexpr int kEpiWarps = 16;
+constexpr int kPairThreads = 32 * (2 + kEpiWarps);
+
 template <int BN, bool AMN, bool BMN>
 struct PairLayout {
     static constexpr int A_BYTES = 128 * kRowBytes;      // this CTA's 128 rows of A
@@ -243,11 +252,11 @@ struct PairLayout {
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int BAR_BYTES = 8 * (2 * NS + 5) + 16;
     static constexpr int OFF_T = (OFF_BAR + BAR_BYTES + 127) / 128 * 128;
-    static constexpr int TR = 32 * 33 + BN;  // floats of a warp: a transpose, its columns' scales and biases
-    static constexpr int SMEM = OFF_T + 8 * TR * 4 + 1024;
+    static constexpr int COLS = BN * 4 / kEpiWarps;      // columns of an epilogue warp
+    static constexpr int TR = 32 * 17 + 2 * COLS;  // its floats: a transpose, its columns' scales and biases
+    static constexpr int SMEM = OFF_T + kEpiWarps * TR * 4 + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
-constexpr int kPairThreads = 10 * 32;
 constexpr int kSumSteps = 16; // stages of a tensor-core sum of a float32 output
 constexpr int kJoinStages = 12;  // stages in the time that joining a shared tile takes
 
@@ -284,13 +293,19 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 
-// tc::tmem_wait_ld for a load issued earlier, whose registers nothing may read before.
-__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
+// Warp-wide: 32 lanes x 16 columns of tensor memory, and the wait for such a load, which
+// ties its registers: nothing may read them before.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
 }
@@ -340,7 +355,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&accf[i], 1);
-            tc::mbar_init(&acce[i], 16);
+            tc::mbar_init(&acce[i], 2 * kEpiWarps);
         }
         tc::mbar_init(mdrain, 1);
         *abort_flag = 0;
@@ -456,11 +471,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
         }
     } else {
-        // A warp's 32 accumulator rows (its quadrant of the lanes) and half of the columns.
-        const int sub = warp & 3, half = (warp - 2) >> 2;
+        // A warp's 32 accumulator rows (its quadrant of the lanes) and COLS columns, 16 at a
+        // time.
+        constexpr int COLS = L::COLS, NC = COLS / 16;
+        const int sub = warp & 3, group = (warp - 2) >> 2;
         const uint32_t acce_lead = tc::mapa_shared(acce, 0);
         float* tr = reinterpret_cast<float*>(smem + L::OFF_T) + (warp - 2) * L::TR;
-        float *cs = tr + 32 * 33, *cb = cs + BN / 2;  // the columns' scales and biases
+        float *cs = tr + 32 * 17, *cb = cs + COLS;  // the columns' scales and biases
         const float nan = __int_as_float(0x7fc00000);
         int buf = 0;
         uint32_t aphase = 0;
@@ -468,95 +485,94 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int t, mt, nt, k0, k1;
             item_of(walk, i, n_k, t, k0, k1);
             tile_of(t, n_mt, n_nt, mt, nt);
+            const int64_t m0 = (int64_t)mt * 256 + rank * 128 + sub * 32;
+            const int64_t n0 = (int64_t)nt * BN + group * COLS;
             float* part = i < walk.full ? nullptr
                                         : walk.part + (int64_t)(i - walk.full) * 256 * BN +
-                                              (rank * 128 + sub * 32 + lane) * BN + half * (BN / 2);
-            const int64_t m0 = (int64_t)mt * 256 + rank * 128 + sub * 32;
-            const int64_t n0 = (int64_t)nt * BN + half * (BN / 2);
+                                              (rank * 128 + sub * 32 + lane) * BN + group * COLS;
             const int rows = (int)min((int64_t)32, e.M - m0);  // (<= 0: none)
 #pragma unroll
-            for (int c = 0; c < BN / 64; ++c) {
-                const int64_t n = n0 + 32 * c + lane;
-                cs[32 * c + lane] = e.unbias * (e.b_scale && n < e.N ? e.b_scale[n] : 1.f);
-                cb[32 * c + lane] = e.bias && n < e.N ? sb_elem(e.bias, n, e.bias_type) : 0.f;
+            for (int c = lane; c < COLS; c += 32) {
+                const int64_t n = n0 + c;
+                cs[c] = e.unbias * (e.b_scale && n < e.N ? e.b_scale[n] : 1.f);
+                cb[c] = e.bias && n < e.N ? sb_elem(e.bias, n, e.bias_type) : 0.f;
             }
             __syncwarp();
-            const uint32_t d0 = tmem_base + ((uint32_t)(sub * 32) << 16) + half * (BN / 2);
-            // f(c, v): the sums of the columns' c-th 32
-            const auto out = [&](int c, const float (&v)[32], RowChunk& row) {
-                const int64_t n = n0 + 32 * c;
+            const uint32_t d0 = tmem_base + ((uint32_t)(sub * 32) << 16) + group * COLS;
+            // The sums v of the columns' c-th 16.
+            const auto out = [&](int c, float (&v)[16], const Residual& res) {
+                const int64_t n = n0 + 16 * c;
                 if (part) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        tc::st_global_v8(part + 32 * c + 8 * q, reinterpret_cast<const uint32_t*>(v + 8 * q));
-                } else if (e.vec && n + 32 <= e.N) {
-                    float u[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) u[j] = v[j];
-                    if (lane < rows) row.finish(e, m0 + lane, n, u, cs + 32 * c, cb + 32 * c);
+                    tc::st_global_v8(part + 16 * c, reinterpret_cast<const uint32_t*>(v));
+                    tc::st_global_v8(part + 16 * c + 8, reinterpret_cast<const uint32_t*>(v + 8));
+                } else if (e.vec && n + 16 <= e.N) {
+                    if (lane < rows) finish16(e, m0 + lane, n, v, cs + 16 * c, cb + 16 * c, res);
                 } else {
-                    // any alignment and width: through shared memory, a row at a time
+                    // any alignment and width: through shared memory, two rows at a time
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) tr[lane * 33 + j] = v[j];
+                    for (int j = 0; j < 16; ++j) tr[lane * 17 + j] = v[j];
                     __syncwarp();
-                    if (n + lane < e.N)
-                        for (int k = 0; k < rows; ++k)
-                            finish(e, m0 + k, n + lane, tr[k * 33 + lane], cs[32 * c + lane], cb[32 * c + lane]);
+                    const int col = lane & 15;
+                    if (n + col < e.N)
+                        for (int k = lane >> 4; k < rows; k += 2)
+                            finish(e, m0 + k, n + col, tr[k * 17 + col], cs[16 * c + col], cb[16 * c + col]);
                     __syncwarp();
                 }
             };
-            const auto ask = [&](int c, RowChunk& row) {
-                if (!part && e.vec && n0 + 32 * c + 32 <= e.N && lane < rows) row.load(e, m0 + lane, n0 + 32 * c);
+            const auto ask = [&](int c, Residual& res) {
+                if (e.res && !part && e.vec && n0 + 16 * c + 16 <= e.N && lane < rows)
+                    res.load(e, m0 + lane, n0 + 16 * c);
             };
-            // The accumulator has been read (nothing in memory is handed over: a release would
-            // wait for the warp's stores, 36 us instead of 2x at 256 x 2560 x 10240's dW).
+            // The accumulator has been read.  (Nothing in memory is handed over: a release would
+            // wait for the warp's stores; 256 rows' dW of 2560 x 10240 took 36 us, 27 so.)
             const auto release = [&](int k) {
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive_cluster_relaxed(acce_lead + 8 * k);
             };
+            Residual res;
+            ask(0, res);
             if constexpr (!SUMS) {
-                RowChunk row;
-                ask(0, row);
                 const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
                 tc::tc_fence_after();
                 const uint32_t d = d0 + buf * BN;
-                uint32_t r[32];
-                tc::tmem_ld32(d, r);
-                tc::tmem_wait_ld();
+                uint32_t r[16];
+                tmem_ld16(d, r);
+                tmem_wait_ld_of(r);
 #pragma unroll 1
-                for (int c = 0; c < BN / 64; ++c) {
-                    float v[32];
+                for (int c = 0; c < NC; ++c) {
+                    float v[16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
                     if (!ok) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = nan;
+                        for (int j = 0; j < 16; ++j) v[j] = nan;
                     }
-                    if (c + 1 < BN / 64) {
-                        tc::tmem_ld32(d + 32 * (c + 1), r);  // (while these are finished)
+                    // the next columns' sums and residual on their way while these are finished
+                    Residual next;
+                    if (c + 1 < NC) {
+                        tmem_ld16(d + 16 * (c + 1), r);
+                        ask(c + 1, next);
                     } else {
                         release(buf);
                     }
-                    out(c, v, row);
-                    if (c + 1 < BN / 64) {
-                        ask(c + 1, row);
-                        tmem_wait_ld_of(r);
-                    }
+                    out(c, v, res);
+                    res = next;
+                    if (c + 1 < NC) tmem_wait_ld_of(r);
                 }
                 if (++buf == 2) { buf = 0; aphase ^= 1; }
             } else {
-                float v[BN / 64][32];
+                float v[NC][16];
                 for (int kk = k0; kk < k1; kk += kSumSteps) {
                     const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
                     tc::tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < BN / 64; ++c) {
-                        uint32_t r[32];
-                        tc::tmem_ld32(d0 + buf * BN + 32 * c, r);
-                        tc::tmem_wait_ld();
+                    for (int c = 0; c < NC; ++c) {
+                        uint32_t r[16];
+                        tmem_ld16(d0 + buf * BN + 16 * c, r);
+                        tmem_wait_ld_of(r);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
+                        for (int j = 0; j < 16; ++j) {
                             const float x = ok ? __uint_as_float(r[j]) : nan;
                             v[c][j] = kk == k0 ? x : v[c][j] + x;
                         }
@@ -565,10 +581,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (++buf == 2) { buf = 0; aphase ^= 1; }
                 }
 #pragma unroll
-                for (int c = 0; c < BN / 64; ++c) {
-                    RowChunk row;
-                    ask(c, row);
-                    out(c, v[c], row);
+                for (int c = 0; c < NC; ++c) {
+                    if (c > 0) ask(c, res);
+                    out(c, v[c], res);
                 }
             }
             __syncwarp();

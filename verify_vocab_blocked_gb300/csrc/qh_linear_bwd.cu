@@ -26,7 +26,10 @@ __device__ __forceinline__ float act_grad(float z, int act) {
             const float p = __fdividef(1.f, 1.f + __expf(-z));
             return p * fmaf(z, 1.f - p, 1.f);
         }
-        case kActGelu: return fmaf(z * 0.39894228f, __expf(-0.5f * z * z), 0.5f * (1.f + erff(z * 0.70710678f)));
+        case kActGelu: {
+            const float2 n = normal_tail(z);
+            return fmaf(z, n.y, z < 0.f ? n.x : 1.f - n.x);
+        }
         case kActGeluTanh: {  // s = (1 + tanh u) / 2;  s + z u' 2 s (1 - s)
             const float z2 = z * z;
             const float s = __fdividef(1.f, 1.f + __expf(-1.5957691216f * fmaf(0.044715f * z2, z, z)));
