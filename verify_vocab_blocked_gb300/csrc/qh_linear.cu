@@ -79,7 +79,7 @@ struct Epi {
     int64_t ldr;
     int bias_type, act, res_type, y_type;
     float unbias;      // what every sum is multiplied by (see unbias_of)
-    int vec;           // bytes that the rows of y, pre and res are all aligned to: 32, 16 or 0
+    int vec;           // the rows of y, pre and res are all aligned to 16 bytes
 };
 
 // What a pair walks: `full` whole tiles, then the others' parts, `split` of the
@@ -109,28 +109,6 @@ __device__ __forceinline__ void finish(const Epi& e, int64_t m, int64_t n, float
     put(e.y, at, e.y_type, v);
 }
 
-// 32 consecutive bytes (words w[0 .. 8)) to or from rows of that alignment, or of 16.
-__device__ __forceinline__ void st32(void* p, const uint32_t* w, int vec) {
-    if (vec == 32) {
-        tc::st_global_v8(p, w);
-    } else {
-        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
-}
-__device__ __forceinline__ void ld32(const void* p, uint32_t* w, int vec) {
-    if (vec == 32) {
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                     : "l"(p)
-                     : "memory");
-    } else {
-        const uint4 a = reinterpret_cast<const uint4*>(p)[0], b = reinterpret_cast<const uint4*>(p)[1];
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-    }
-}
-
 __device__ __forceinline__ uint32_t pack2(float a, float b, int type) {
     if (type == kSbBf16) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -141,94 +119,140 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int type) {
 }
 
 template <int ACT>
-__device__ __forceinline__ void activate16(float (&v)[16]) {
+__device__ __forceinline__ void activate32(float (&v)[32]) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = activate(v[j], ACT);
+    for (int j = 0; j < 32; ++j) v[j] = activate(v[j], ACT);
 }
 
-// A thread's 16 consecutive columns, all in range, of row m: the residual's words
-// (8 of a 2-byte type), asked for ahead.
-struct Residual {
-    uint32_t r[16];
-    __device__ __forceinline__ void load(const Epi& e, int64_t m, int64_t n) {
-        if (e.res_type == kSbF32) {
-            const float* p = static_cast<const float*>(e.res) + m * e.ldr + n;
-            ld32(p, r, e.vec);
-            ld32(p + 8, r + 8, e.vec);
-        } else {
-            ld32(static_cast<const __half*>(e.res) + m * e.ldr + n, r, e.vec);  // (16 bits)
-        }
+// One column's scale, and its bias as it lies in memory (a conversion at the load would
+// wait for it); 1 and 0 where there is none.
+struct Column {
+    float scale;
+    uint32_t bias;
+    __device__ __forceinline__ void load(const Epi& e, int64_t n) {
+        scale = e.b_scale && n < e.N ? e.b_scale[n] : 1.f;
+        bias = 0u;
+        if (!e.bias || n >= e.N) return;
+        if (e.bias_type == kSbF32) bias = static_cast<const uint32_t*>(e.bias)[n];
+        else bias = static_cast<const unsigned short*>(e.bias)[n];
     }
-    __device__ __forceinline__ void add(const Epi& e, float (&v)[16]) const {
-        if (e.res_type == kSbF32) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
-        } else if (e.res_type == kSbBf16) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[2 * j] += __uint_as_float(r[j] << 16);
-                v[2 * j + 1] += __uint_as_float(r[j] & 0xffff0000u);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[j]));
-                v[2 * j] += f.x;
-                v[2 * j + 1] += f.y;
-            }
-        }
+    __device__ __forceinline__ float bias_of(int type) const {
+        if (type == kSbF32) return __uint_as_float(bias);
+        return type == kSbBf16 ? __uint_as_float(bias << 16) : __half2float(__ushort_as_half((unsigned short)bias));
     }
 };
 
-// These outputs from their sums v; cs, cb: the columns' scales and biases in shared
-// memory.
-__device__ __forceinline__ void finish16(const Epi& e, int64_t m, int64_t n, float (&v)[16], const float* cs,
-                                         const float* cb, const Residual& res) {
-    if (e.b_scale || e.unbias != 1.f) {
-        const float as = e.a_scale ? e.a_scale[m] : 1.f;
+__device__ __forceinline__ void activate32(float (&v)[32], int act) {
+    switch (act) {
+        case kActRelu: activate32<kActRelu>(v); break;
+        case kActSilu: activate32<kActSilu>(v); break;
+        case kActGelu: activate32<kActGelu>(v); break;
+        case kActGeluTanh: activate32<kActGeluTanh>(v); break;
+        default: break;
+    }
+}
+
+// A warp's 32 rows x 32 columns in shared memory as TMA lays them: rows of 64 bytes
+// (16-bit types, 64-byte swizzle) or 128 (float32, 128-byte swizzle).  The address of
+// row r's 16-byte piece q.
+__device__ __forceinline__ uint32_t piece16(uint32_t base, int r, int q) { return base + 64 * r + 16 * (q ^ (r >> 1 & 3)); }
+__device__ __forceinline__ uint32_t piece32(uint32_t base, int r, int q) { return base + 128 * r + 16 * (q ^ (r & 7)); }
+
+__device__ __forceinline__ void sts128(uint32_t p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+    return v;
+}
+
+// v to or from row r of such a tile.
+__device__ __forceinline__ void put32(uint32_t base, int r, const float (&v)[32], int type) {
+    if (type == kSbF32) {
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            const float4 s = *reinterpret_cast<const float4*>(cs + j);
-            v[j] *= as * s.x, v[j + 1] *= as * s.y, v[j + 2] *= as * s.z, v[j + 3] *= as * s.w;
+        for (int q = 0; q < 8; ++q)
+            sts128(piece32(base, r, q), __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                   __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            sts128(piece16(base, r, q), pack2(v[8 * q], v[8 * q + 1], type), pack2(v[8 * q + 2], v[8 * q + 3], type),
+                   pack2(v[8 * q + 4], v[8 * q + 5], type), pack2(v[8 * q + 6], v[8 * q + 7], type));
+    }
+}
+__device__ __forceinline__ void add32(uint32_t base, int r, float (&v)[32], int type) {
+    if (type == kSbF32) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const uint4 u = lds128(piece32(base, r, q));
+            v[4 * q] += __uint_as_float(u.x), v[4 * q + 1] += __uint_as_float(u.y);
+            v[4 * q + 2] += __uint_as_float(u.z), v[4 * q + 3] += __uint_as_float(u.w);
+        }
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint4 u = lds128(piece16(base, r, q));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float2 f;
+            if (type == kSbBf16) f = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+            else f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+            v[8 * q + 2 * j] += f.x;
+            v[8 * q + 2 * j + 1] += f.y;
+        }
+    }
+}
+
+// z of row m and a thread's 32 consecutive columns, whose scales and biases the warp's
+// lanes hold: through 256 bytes of shared memory.
+__device__ __forceinline__ void scale32(const Epi& e, int64_t m, const Column& column, uint32_t sh, float (&v)[32]) {
+    if (e.unbias != 1.f) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= e.unbias;
+    }
+    if (!e.bias && !e.b_scale) return;
+    const int lane = threadIdx.x & 31;
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(sh + 4 * lane), "f"(column.scale) : "memory");
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(sh + 128 + 4 * lane), "f"(column.bias_of(e.bias_type)) : "memory");
+    __syncwarp();
+    if (e.b_scale) {
+        const float as = m < e.M ? e.a_scale[m] : 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const uint4 u = lds128(sh + 16 * q);
+            v[4 * q] *= as * __uint_as_float(u.x), v[4 * q + 1] *= as * __uint_as_float(u.y);
+            v[4 * q + 2] *= as * __uint_as_float(u.z), v[4 * q + 3] *= as * __uint_as_float(u.w);
         }
     }
     if (e.bias) {
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-            const float4 b = *reinterpret_cast<const float4*>(cb + j);
-            v[j] += b.x, v[j + 1] += b.y, v[j + 2] += b.z, v[j + 3] += b.w;
+        for (int q = 0; q < 8; ++q) {
+            const uint4 u = lds128(sh + 128 + 16 * q);
+            v[4 * q] += __uint_as_float(u.x), v[4 * q + 1] += __uint_as_float(u.y);
+            v[4 * q + 2] += __uint_as_float(u.z), v[4 * q + 3] += __uint_as_float(u.w);
         }
     }
-    const int64_t at = m * e.N + n;
-    uint32_t w[8];
-    if (e.pre) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = pack2(in_half(v[2 * j]), in_half(v[2 * j + 1]), kSbF16);
-        st32(e.pre + at, w, e.vec);
-    }
-    switch (e.act) {
-        case kActRelu: activate16<kActRelu>(v); break;
-        case kActSilu: activate16<kActSilu>(v); break;
-        case kActGelu: activate16<kActGelu>(v); break;
-        case kActGeluTanh: activate16<kActGeluTanh>(v); break;
-        default: break;
-    }
-    if (e.res) res.add(e, v);
-    if (e.y_type == kSbF32) {
-        float* p = static_cast<float*>(e.y) + at;
-        st32(p, reinterpret_cast<const uint32_t*>(v), e.vec);
-        st32(p + 8, reinterpret_cast<const uint32_t*>(v + 8), e.vec);
-    } else {
-        if (e.y_type == kSbBf16) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], kSbBf16);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1], kSbF16);
-        }
-        st32(static_cast<__half*>(e.y) + at, w, e.vec);  // (16 bits)
-    }
+    __syncwarp();
 }
+
+// A tile of a warp back to global memory: the warp's writes made visible to the copy,
+// which one thread starts (rows and columns outside the matrix are not written), and
+// the wait until such copies have read their tiles.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void tma_stores_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // ------------------------------------------------------------------- pairs
 
@@ -240,25 +264,25 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-constexpr int kEpiWarps = 16;
+constexpr int kEpiWarps = 8;
 constexpr int kPairThreads = 32 * (2 + kEpiWarps);
+constexpr int kSumSteps = 16;    // stages of a tensor-core sum of a float32 output
+constexpr int kJoinStages = 12;  // stages in the time that joining a shared tile takes
 
 template <int BN, bool AMN, bool BMN>
 struct PairLayout {
     static constexpr int A_BYTES = 128 * kRowBytes;      // this CTA's 128 rows of A
     static constexpr int B_BYTES = BN / 2 * kRowBytes;   // and its half of B's columns
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int NS = BN == 256 ? 5 : 7;
-    static constexpr int OFF_BAR = NS * STAGE;
-    static constexpr int BAR_BYTES = 8 * (2 * NS + 5) + 16;
-    static constexpr int OFF_T = (OFF_BAR + BAR_BYTES + 127) / 128 * 128;
-    static constexpr int COLS = BN * 4 / kEpiWarps;      // columns of an epilogue warp
-    static constexpr int TR = 32 * 17 + 2 * COLS;  // its floats: a transpose, its columns' scales and biases
-    static constexpr int SMEM = OFF_T + kEpiWarps * TR * 4 + 1024;
+    // 5 stages of 256 columns: 66 us at 8192 x 2560 x 2560, 71 with 4, 81 with 3
+    static constexpr int NS = BN == 256 ? 5 : 6;
+    static constexpr int OFF_E = NS * STAGE;             // an epilogue warp's tiles: residual, outputs
+    static constexpr int E_TILE = 32 * 128, E_BYTES = 2 * E_TILE;
+    static constexpr int OFF_BAR = OFF_E + kEpiWarps * E_BYTES;
+    static constexpr int BAR_BYTES = 8 * (2 * NS + 5 + 2 * kEpiWarps) + 16;
+    static constexpr int SMEM = OFF_BAR + BAR_BYTES + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
-constexpr int kSumSteps = 16; // stages of a tensor-core sum of a float32 output
-constexpr int kJoinStages = 12;  // stages in the time that joining a shared tile takes
 
 // The tiles in groups of 8 rows of tiles, columns outer: what the pairs work on at
 // a time is near-square, so that each operand's tiles are shared in L2.
@@ -293,19 +317,13 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 
-// Warp-wide: 32 lanes x 16 columns of tensor memory, and the wait for such a load, which
-// ties its registers: nothing may read them before.
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
-}
-__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[16]) {
+// tc::tmem_wait_ld for a load issued earlier, whose registers nothing may read before.
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                  :
                  : "memory");
 }
@@ -328,6 +346,8 @@ constexpr uint32_t kStep = MN ? 128u : 2u;
 template <int BN, bool AMN, bool BMN, bool SUMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                       const __grid_constant__ CUtensorMap ty, const __grid_constant__ CUtensorMap tp,
+                       const __grid_constant__ CUtensorMap tr,
                        const __grid_constant__ Epi e, const Walk walk, int n_k, int step_k, uint32_t idesc, int f8,
                        int stall) {
     using L = PairLayout<BN, AMN, BMN>;
@@ -339,7 +359,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint64_t* accf = empty + NS;
     uint64_t* acce = accf + 2;
     uint64_t* mdrain = acce + 2;
-    uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(mdrain + 1);
+    uint64_t* resf = mdrain + 1;   // an epilogue warp's residual tiles (two) have landed
+    uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(resf + 2 * kEpiWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sh + 1);
     int* err = reinterpret_cast<int*>(tmem_base_sh + 2);
 
@@ -358,6 +379,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tc::mbar_init(&acce[i], 2 * kEpiWarps);
         }
         tc::mbar_init(mdrain, 1);
+        for (int i = 0; i < 2 * kEpiWarps; ++i) tc::mbar_init(&resf[i], 1);
         *abort_flag = 0;
         *err = 0;
         tc::fence_mbar_init();
@@ -471,16 +493,55 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
         }
     } else {
-        // A warp's 32 accumulator rows (its quadrant of the lanes) and COLS columns, 16 at a
-        // time.
-        constexpr int COLS = L::COLS, NC = COLS / 16;
+        // A warp's 32 accumulator rows (its quadrant of the lanes) and COLS columns, 32 at a
+        // time: a row a lane.
+        constexpr int COLS = BN * 4 / kEpiWarps, NC = COLS / 32;
         const int sub = warp & 3, group = (warp - 2) >> 2;
         const uint32_t acce_lead = tc::mapa_shared(acce, 0);
-        float* tr = reinterpret_cast<float*>(smem + L::OFF_T) + (warp - 2) * L::TR;
-        float *cs = tr + 32 * 17, *cb = cs + COLS;  // the columns' scales and biases
+        unsigned char* tiles = smem + L::OFF_E + (warp - 2) * L::E_BYTES;
+        const uint32_t res_tile = tc::smem_u32(tiles), out_tile = res_tile + L::E_TILE;
+        uint64_t* resb = &resf[2 * (warp - 2)];
         const float nan = __int_as_float(0x7fc00000);
         int buf = 0;
         uint32_t aphase = 0;
+        // The residual's 32 x 32 tiles in the order of their use, asked for by lane 0 as many
+        // ahead as fit (two of a 16-bit type), once the warp has read the slot's last.
+        const bool by_tma = e.vec != 0;
+        const int slots = e.res_type == kSbF32 ? 1 : 2;
+        const uint32_t res_bytes = e.res_type == kSbF32 ? 4096 : 2048;
+        int ask_i = first, ask_c = 0, ask_slot = 0;
+        const auto ask = [&]() {
+            if (!by_tma || !e.res || lane != 0) return;
+            for (; ask_i < walk.full; ask_i += stride, ask_c = 0) {
+                int mt, nt;
+                tile_of(ask_i, n_mt, n_nt, mt, nt);
+                const int m = mt * 256 + (int)rank * 128 + sub * 32, n = nt * BN + group * COLS + 32 * ask_c;
+                if (m < e.M && n < e.N && ask_c < NC) {
+                    tc::mbar_arrive_expect_tx(&resb[ask_slot], res_bytes);
+                    tc::tma_load_2d(tiles + 2048 * ask_slot, &tr, &resb[ask_slot], n, m);
+                    ++ask_c;
+                    if (++ask_slot == slots) ask_slot = 0;
+                    return;
+                }
+            }
+        };
+        // (an item's tiles into L2 while the one before is worked on: from DRAM, two tiles
+        // ahead do not cover the latency)
+        const auto ask_l2 = [&](int i) {
+            if (!by_tma || !e.res || lane >= NC || i >= walk.full) return;
+            int mt, nt;
+            tile_of(i, n_mt, n_nt, mt, nt);
+            const int m = mt * 256 + (int)rank * 128 + sub * 32, n = nt * BN + group * COLS + 32 * lane;
+            if (m < e.M && n < e.N)
+                asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(
+                                 reinterpret_cast<uint64_t>(&tr)),
+                             "r"(n), "r"(m)
+                             : "memory");
+        };
+        ask_l2(first);
+        for (int k = 0; k < slots; ++k) ask();
+        int slot = 0;
+        uint32_t rphase = 0;
         for (int i = first; i < walk.items; i += stride) {
             int t, mt, nt, k0, k1;
             item_of(walk, i, n_k, t, k0, k1);
@@ -491,37 +552,71 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                         : walk.part + (int64_t)(i - walk.full) * 256 * BN +
                                               (rank * 128 + sub * 32 + lane) * BN + group * COLS;
             const int rows = (int)min((int64_t)32, e.M - m0);  // (<= 0: none)
-#pragma unroll
-            for (int c = lane; c < COLS; c += 32) {
-                const int64_t n = n0 + c;
-                cs[c] = e.unbias * (e.b_scale && n < e.N ? e.b_scale[n] : 1.f);
-                cb[c] = e.bias && n < e.N ? sb_elem(e.bias, n, e.bias_type) : 0.f;
-            }
-            __syncwarp();
             const uint32_t d0 = tmem_base + ((uint32_t)(sub * 32) << 16) + group * COLS;
-            // The sums v of the columns' c-th 16.
-            const auto out = [&](int c, float (&v)[16], const Residual& res) {
-                const int64_t n = n0 + 16 * c;
+            ask_l2(i + stride);
+            Column column;  // (of the next 32)
+            column.load(e, n0 + lane);
+            // The sums v of the columns' c-th 32.
+            const auto out = [&](int c, float (&v)[32]) {
+                const int64_t n = n0 + 32 * c;
                 if (part) {
-                    tc::st_global_v8(part + 16 * c, reinterpret_cast<const uint32_t*>(v));
-                    tc::st_global_v8(part + 16 * c + 8, reinterpret_cast<const uint32_t*>(v + 8));
-                } else if (e.vec && n + 16 <= e.N) {
-                    if (lane < rows) finish16(e, m0 + lane, n, v, cs + 16 * c, cb + 16 * c, res);
-                } else {
-                    // any alignment and width: through shared memory, two rows at a time
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) tr[lane * 17 + j] = v[j];
+                    for (int q = 0; q < 4; ++q)
+                        tc::st_global_v8(part + 32 * c + 8 * q, reinterpret_cast<const uint32_t*>(v + 8 * q));
+                    return;
+                }
+                if (rows <= 0 || n >= e.N) return;
+                if (!by_tma) {
+                    // any alignment: through shared memory, a row at a time
+                    float* tr = reinterpret_cast<float*>(tiles);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) tr[lane * 33 + j] = v[j];
                     __syncwarp();
-                    const int col = lane & 15;
-                    if (n + col < e.N)
-                        for (int k = lane >> 4; k < rows; k += 2)
-                            finish(e, m0 + k, n + col, tr[k * 17 + col], cs[16 * c + col], cb[16 * c + col]);
+                    const int64_t col = n + lane;
+                    if (col < e.N) {
+                        const float bs = e.unbias * (e.b_scale ? e.b_scale[col] : 1.f);
+                        const float bias = e.bias ? sb_elem(e.bias, col, e.bias_type) : 0.f;
+#pragma unroll 4
+                        for (int k = 0; k < rows; ++k) finish(e, m0 + k, col, tr[k * 33 + lane], bs, bias);
+                    }
+                    __syncwarp();
+                    return;
+                }
+                const Column col = column;
+                if (c + 1 < NC) column.load(e, n + 32 + lane);
+                if (lane == 0) tma_stores_read<0>();  // the output tile is free
+                __syncwarp();
+                scale32(e, m0 + lane, col, out_tile, v);
+                uint32_t y_tile = out_tile;
+                if (e.pre) {
+                    float z[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) z[j] = in_half(v[j]);
+                    put32(out_tile, lane, z, kSbF16);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tma_store(&tp, out_tile, (int)n, (int)m0);
+                    if (e.y_type != kSbF32) y_tile += 2048;  // (both fit)
+                }
+                activate32(v, e.act);
+                if (e.res) {
+                    // (a failed wait: the copy is waited for all the same, and the outputs say so)
+                    const bool ok = tc::mbar_wait_cta(&resb[slot], rphase, abort_flag, err, tc::kErrTimeoutFull);
+                    if (!ok) tc::mbar_drain(&resb[slot], rphase, err);
+                    add32(res_tile + 2048 * slot, lane, v, e.res_type);
+                    if (!ok) v[0] = nan;
+                    if (++slot == slots) { slot = 0; rphase ^= 1; }
+                    __syncwarp();
+                    ask();
+                }
+                if (e.pre && e.y_type == kSbF32) {
+                    if (lane == 0) tma_stores_read<0>();
                     __syncwarp();
                 }
-            };
-            const auto ask = [&](int c, Residual& res) {
-                if (e.res && !part && e.vec && n0 + 16 * c + 16 <= e.N && lane < rows)
-                    res.load(e, m0 + lane, n0 + 16 * c);
+                put32(y_tile, lane, v, e.y_type);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tma_store(&ty, y_tile, (int)n, (int)m0);
             };
             // The accumulator has been read.  (Nothing in memory is handed over: a release would
             // wait for the warp's stores; 256 rows' dW of 2560 x 10240 took 36 us, 27 so.)
@@ -530,49 +625,41 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive_cluster_relaxed(acce_lead + 8 * k);
             };
-            Residual res;
-            ask(0, res);
             if constexpr (!SUMS) {
                 const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
                 tc::tc_fence_after();
                 const uint32_t d = d0 + buf * BN;
-                uint32_t r[16];
-                tmem_ld16(d, r);
+                uint32_t r[32];
+                tc::tmem_ld32(d, r);
                 tmem_wait_ld_of(r);
 #pragma unroll 1
                 for (int c = 0; c < NC; ++c) {
-                    float v[16];
+                    float v[32];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
                     if (!ok) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = nan;
+                        for (int j = 0; j < 32; ++j) v[j] = nan;
                     }
-                    // the next columns' sums and residual on their way while these are finished
-                    Residual next;
-                    if (c + 1 < NC) {
-                        tmem_ld16(d + 16 * (c + 1), r);
-                        ask(c + 1, next);
-                    } else {
-                        release(buf);
-                    }
-                    out(c, v, res);
-                    res = next;
+                    // the next columns' sums on their way while these are finished
+                    if (c + 1 < NC) tc::tmem_ld32(d + 32 * (c + 1), r);
+                    else release(buf);
+                    out(c, v);
                     if (c + 1 < NC) tmem_wait_ld_of(r);
                 }
                 if (++buf == 2) { buf = 0; aphase ^= 1; }
             } else {
-                float v[NC][16];
+                float v[NC][32];
                 for (int kk = k0; kk < k1; kk += kSumSteps) {
                     const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
                     tc::tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
-                        uint32_t r[16];
-                        tmem_ld16(d0 + buf * BN + 16 * c, r);
+                        uint32_t r[32];
+                        tc::tmem_ld32(d0 + buf * BN + 32 * c, r);
                         tmem_wait_ld_of(r);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
+                        for (int j = 0; j < 32; ++j) {
                             const float x = ok ? __uint_as_float(r[j]) : nan;
                             v[c][j] = kk == k0 ? x : v[c][j] + x;
                         }
@@ -581,13 +668,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (++buf == 2) { buf = 0; aphase ^= 1; }
                 }
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    if (c > 0) ask(c, res);
-                    out(c, v[c], res);
-                }
+                for (int c = 0; c < NC; ++c) out(c, v[c]);
             }
-            __syncwarp();
         }
+        if (lane == 0) tma_stores_done();
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -968,14 +1052,18 @@ float unbias_of(int mmas, int type) { return type == kE4m3 ? 1.f : 1.f + 1.4e-8f
 
 // `mmas`: of a tensor-core sum.
 Epi epi_of(const LinArgs& a, int mmas) {
-    const auto rows = [](const void* p, int64_t ld, int type, int by) {
-        return !p || (reinterpret_cast<uintptr_t>(p) % by == 0 && ld * type_bytes(type) % by == 0);
+    const auto rows = [](const void* p, int64_t ld, int type) {
+        return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * type_bytes(type) % 16 == 0);
     };
-    const auto all = [&](int by) {
-        return rows(a.y, a.N, a.y_type, by) && rows(a.pre, a.N, kSbF16, by) && rows(a.res, a.ldr, a.res_type, by);
-    };
+    const bool vec = rows(a.y, a.N, a.y_type) && rows(a.pre, a.N, kSbF16) && rows(a.res, a.ldr, a.res_type);
     return Epi{a.M, a.N, a.a_scale, a.b_scale, a.bias, a.res, a.y, a.pre, a.ldr, a.bias_type, a.act, a.res_type, a.y_type,
-               unbias_of(mmas, a.type), all(32) ? 32 : all(16) ? 16 : 0};
+               unbias_of(mmas, a.type), vec};
+}
+
+// The map of an output's or the residual's 32 x 32 tiles (not made where there is none).
+bool map_tile(CUtensorMap* map, const void* p, int type, int64_t ld, const LinArgs& a, bool vec) {
+    return !p || !vec ||
+           tmap_tiles(map, p, type_bytes(type), (uint64_t)a.N, (uint64_t)a.M, (uint64_t)ld * type_bytes(type));
 }
 
 template <typename... P, typename... A>
@@ -1018,8 +1106,12 @@ cudaError_t go_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
     const Walk walk{full, full + (tiles - full) * p.split, p.split, a.part};
     const int pairs = std::min(walk.items, p.pairs);
     const Epi e = epi_of(a, in_sums(a) ? 4 * std::min(n_k, kSumSteps) : 0);
+    CUtensorMap ty{}, tp{}, tr{};
+    if (!map_tile(&ty, a.y, a.y_type, a.N, a, e.vec) || !map_tile(&tp, a.pre, kSbF16, a.N, a, e.vec) ||
+        !map_tile(&tr, a.res, a.res_type, a.ldr, a, e.vec))
+        return cudaErrorInvalidValue;
     if (cudaError_t err = launch_cluster(linear_pair_kernel<BN, AMN, BMN, SUMS>, dim3((unsigned)(2 * pairs)),
-                                         kPairThreads, L::SMEM, 2, st, ta, tb, e, walk, n_k, step,
+                                         kPairThreads, L::SMEM, 2, st, ta, tb, ty, tp, tr, e, walk, n_k, step,
                                          idesc_of(a.type, 256, BN, AMN, BMN), (int)(a.type == kE4m3), a.stall))
         return err;
     if (full == tiles) return cudaSuccess;

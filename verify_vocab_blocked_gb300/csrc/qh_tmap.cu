@@ -57,6 +57,13 @@ bool tmap_rows_sw128(CUtensorMap* map, const void* base, int elem_bytes, uint64_
                      cols, rows, row_bytes, 128 / elem_bytes, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool tmap_tiles(CUtensorMap* map, const void* base, int elem_bytes, uint64_t cols, uint64_t rows,
+                uint64_t row_bytes) {
+    return encode_2d(map, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, base,
+                     cols, rows, row_bytes, 32, 32,
+                     elem_bytes == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 bool tmap_packed_rows(CUtensorMap* map, const uint32_t* wq, uint64_t words_per_row, uint64_t rows,
                       uint32_t box_words, uint32_t box_rows) {
     return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, wq, words_per_row, rows,

@@ -17,6 +17,11 @@ bool tmap_rows_f16_sw128(CUtensorMap* map, const void* base, uint64_t cols, uint
 bool tmap_rows_sw128(CUtensorMap* map, const void* base, int elem_bytes, uint64_t cols, uint64_t rows,
                      uint64_t row_bytes, uint32_t box_rows);
 
+// Row-major matrix of 2- or 4-byte elements, box of 32 x 32 whose rows of 64 or 128 bytes
+// have the swizzle of that span.
+bool tmap_tiles(CUtensorMap* map, const void* base, int elem_bytes, uint64_t cols, uint64_t rows,
+                uint64_t row_bytes);
+
 // Packed uint32 head [rows, words_per_row], box of box_words x box_rows, no swizzle.
 bool tmap_packed_rows(CUtensorMap* map, const uint32_t* wq, uint64_t words_per_row, uint64_t rows,
                       uint32_t box_words, uint32_t box_rows);
