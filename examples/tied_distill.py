@@ -3,11 +3,11 @@
     python examples/tied_distill.py [--rows 2048] [--vocab 32768] [--hidden 1024] [--steps 20]
 
 Tokens are looked up in the packed 4-bit table, a small trainable block stands
-for the model's body, the final norm makes the head's hidden states, and the
-same table scores them against a teacher's top logits.  The backward runs the
+for the model's body, its residual's addition with the final norm behind it makes the
+head's hidden states, and the same table scores them against a teacher's top logits.  The backward runs the
 distillation's gradient into h (the table as a head is frozen: that loss has no
 gradient into it), the norm's and the lookup's, whose table gradient is added
-into a float32 [V, H] buffer.  Synthetic data; prints the loss as the body learns.
+into a float32 [V, H] buffer; all gradients are clipped together.  Synthetic data; prints the loss as the body learns.
 """
 import argparse
 import os
@@ -17,7 +17,7 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from verify_vocab_blocked_gb300 import qhead, synth  # noqa: E402
-from verify_vocab_blocked_gb300.autograd import embed, head_distill, layer_norm  # noqa: E402
+from verify_vocab_blocked_gb300.autograd import add_norm, embed, head_distill  # noqa: E402
 
 
 def make_teacher(M, V, K, seed, device):
@@ -53,7 +53,7 @@ class Step:
         """The mean loss; gradients in body, gain, shift (.grad) and dw."""
         self.dw.zero_()
         x = embed(self.head, self.tokens, self.scale, self.mask, dw=self.dw)
-        h = layer_norm(x + x @ self.body, self.gain, self.shift)
+        h, _ = add_norm(x @ self.body, x, self.gain, self.shift)
         loss = head_distill(h, self.head, self.ids, self.teacher, 1.0, self.mask)
         mean = loss.sum() / self.mask.sum()
         mean.backward()
@@ -73,9 +73,10 @@ def main():
     for i in range(a.steps):
         opt.zero_grad(set_to_none=True)
         loss = step()
+        norm = qhead.clip_grads([step.body.grad, step.gain.grad, step.shift.grad, step.dw], 1.0)
         opt.step()
         if i % 5 == 0 or i == a.steps - 1:
-            print(f"step {i:3d}  loss {loss.item():.4f}  |dW| {step.dw.norm().item():.4e}")
+            print(f"step {i:3d}  loss {loss.item():.4f}  gradient norm {norm.item():.4e}")
 
 
 if __name__ == "__main__":

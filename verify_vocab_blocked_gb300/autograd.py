@@ -11,7 +11,9 @@ dtype of h (bf16), as autograd requires.
 The operators beside the head in the same manner: head_distill (the loss
 against a teacher's top logits, differentiable in h), layer_norm
 (differentiable in x, weight and bias) and embed (whose gradient is the
-dequantized table's: it goes into the tensor given for it).
+dequantized table's: it goes into the tensor given for it).  And the block between
+them: linear (differentiable in x, weight, bias and residual) and add_norm (in x,
+residual, weight and bias).
 
 First derivatives only: a backward's result has no derivative of its own, and
 differentiating it (a gradient penalty under create_graph) raises.  Every tensor
@@ -83,6 +85,13 @@ def head_distill(h: torch.Tensor, head: qhead.Head, ids: torch.Tensor, tlogits: 
     return HeadDistill.apply(h, head, ids, tlogits, temperature, mask)
 
 
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """t with contiguous rows that do not overlap (an expanded gradient's are not)."""
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        return t.contiguous()
+    return t
+
+
 class LayerNorm(torch.autograd.Function):
     """y of qhead.layer_norm; differentiable in x, weight and bias."""
 
@@ -98,9 +107,7 @@ class LayerNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy: torch.Tensor):
         x, weight, mean, rstd = ctx.saved_tensors
-        if dy.shape[1] > 1 and dy.stride(1) != 1 or dy.shape[0] > 1 and dy.stride(0) < dy.shape[1]:
-            dy = dy.contiguous()  # (an expanded gradient)
-        dx, dw, db = qhead.layer_norm_bwd(x, weight, mean, rstd, dy,
+        dx, dw, db = qhead.layer_norm_bwd(x, weight, mean, rstd, _rows(dy),
                                           want_dbias=ctx.bias_type is not None)
         return (dx, dw.to(weight.dtype), None if db is None else db.to(ctx.bias_type), None, None,
                 None)
@@ -112,6 +119,76 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None 
     """Differentiable layer norm of x's rows (center off: the root-mean-square
     form); in bfloat16 its result is the head's h."""
     return LayerNorm.apply(x, weight, bias, eps, center, out_dtype)
+
+
+class AddNorm(torch.autograd.Function):
+    """y and total of qhead.add_norm; differentiable in x, residual, weight and bias."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor,
+                bias: torch.Tensor | None, eps: float, center: bool, out_dtype: torch.dtype):
+        y, total, mean, rstd = qhead.add_norm(x, residual, weight, bias, eps, center=center,
+                                              out_dtype=out_dtype)
+        ctx.set_materialize_grads(False)
+        ctx.x_type, ctx.bias_type = x.dtype, None if bias is None else bias.dtype
+        ctx.save_for_backward(total, weight, mean, rstd)
+        return y, total
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy: torch.Tensor | None, dtotal: torch.Tensor | None):
+        total, weight, mean, rstd = ctx.saved_tensors
+        if dy is None:  # only the sum is used: the norm has no part in it
+            return None if dtotal is None else dtotal.to(ctx.x_type), dtotal, None, None, None, None, None
+        if dtotal is not None:
+            dtotal = _rows(dtotal)
+        dx, dw, db = qhead.add_norm_bwd(total, weight, mean, rstd, _rows(dy), dtotal,
+                                        want_dbias=ctx.bias_type is not None)
+        return (dx.to(ctx.x_type), dx, dw.to(weight.dtype), None if db is None else db.to(ctx.bias_type), None, None,
+                None)
+
+
+def add_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+             eps: float = 1e-6, *, center: bool = True,
+             out_dtype: torch.dtype = torch.bfloat16) -> tuple[torch.Tensor, torch.Tensor]:
+    """Differentiable (y, total): total = x + residual and its norm (center off: the
+    root-mean-square form)."""
+    return AddNorm.apply(x, residual, weight, bias, eps, center, out_dtype)
+
+
+class Linear(torch.autograd.Function):
+    """y of qhead.linear; differentiable in x, weight, bias and residual."""
+
+    @staticmethod
+    def forward(ctx, x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, act: str,
+                residual: torch.Tensor | None, out_dtype: torch.dtype | None):
+        keep = act != "none" and any(ctx.needs_input_grad[:3])
+        got = qhead.linear(x, weight, bias, act, residual, out_dtype=out_dtype, want_pre=keep)
+        y, pre = got if keep else (got, None)
+        ctx.act = act
+        ctx.bias_type = None if bias is None else bias.dtype
+        ctx.res_type = None if residual is None else residual.dtype
+        ctx.save_for_backward(x, weight, pre)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy: torch.Tensor):
+        x, weight, pre = ctx.saved_tensors
+        want_dx, want_dw, want_db = ctx.needs_input_grad[:3]
+        dx = dw = db = None
+        if want_dx or want_dw or want_db:
+            dx, dw, db = qhead.linear_bwd(x, weight, _rows(dy), pre, ctx.act, want_dx=want_dx, want_dw=want_dw,
+                                          want_dbias=want_db)
+        return (dx, dw, None if db is None else db.to(ctx.bias_type), None,
+                dy.to(ctx.res_type) if ctx.needs_input_grad[4] else None, None)
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
+           residual: torch.Tensor | None = None, *, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Differentiable act(x @ weight.T + bias) + residual (x and weight in bfloat16 or
+    float16)."""
+    return Linear.apply(x, weight, bias, act, residual, out_dtype)
 
 
 class Embed(torch.autograd.Function):
