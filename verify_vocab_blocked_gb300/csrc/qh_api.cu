@@ -464,7 +464,7 @@ LinearPlan plan_of_linear(const void* x, int dtype, int64_t ldx, int64_t M, int6
     if (bwd) {
         p.ldz = pitch(N);
         p.off_dz = take((size_t)M * p.ldz * bytes);
-        p.off_db = take(sizeof(float) * (size_t)qh::dz_chunks(M, N) * N);
+        p.off_db = take(sizeof(float) * (size_t)qh::dz_chunks(M, N, QHEAD_BF16) * N);  // (float32 dy: fewer)
     }
     // the products' shared tiles, one product after the other
     const int sms = linear_sms();

@@ -566,24 +566,41 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     return;
                 }
                 if (rows <= 0 || n >= e.N) return;
+                const Column col = column;
+                if (c + 1 < NC) column.load(e, n + 32 + lane);
                 if (!by_tma) {
-                    // any alignment: through shared memory, a row at a time
+                    // any alignment: through shared memory to rows of 32 lanes
+                    scale32(e, m0 + lane, col, res_tile + 4608, v);
                     float* tr = reinterpret_cast<float*>(tiles);
+                    const int64_t at = m0 * e.N + n + lane;
+                    const int live = n + lane < e.N ? rows : 0;
+                    if (e.pre) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) tr[lane * 33 + j] = in_half(v[j]);
+                        __syncwarp();
+#pragma unroll 8
+                        for (int k = 0; k < live; ++k) e.pre[at + k * e.N] = __float2half_rn(tr[k * 33 + lane]);
+                        __syncwarp();
+                    }
+                    activate32(v, e.act);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) tr[lane * 33 + j] = v[j];
                     __syncwarp();
-                    const int64_t col = n + lane;
-                    if (col < e.N) {
-                        const float bs = e.unbias * (e.b_scale ? e.b_scale[col] : 1.f);
-                        const float bias = e.bias ? sb_elem(e.bias, col, e.bias_type) : 0.f;
-#pragma unroll 4
-                        for (int k = 0; k < rows; ++k) finish(e, m0 + k, col, tr[k * 33 + lane], bs, bias);
+                    if (e.res) {
+                        const int64_t from = m0 * e.ldr + n + lane;
+#pragma unroll 8
+                        for (int k = 0; k < live; ++k) tr[k * 33 + lane] += sb_elem(e.res, from + k * e.ldr, e.res_type);
+                    }
+                    if (e.y_type == kSbF32) {
+#pragma unroll 8
+                        for (int k = 0; k < live; ++k) static_cast<float*>(e.y)[at + k * e.N] = tr[k * 33 + lane];
+                    } else {
+#pragma unroll 8
+                        for (int k = 0; k < live; ++k) put(e.y, at + k * e.N, e.y_type, tr[k * 33 + lane]);
                     }
                     __syncwarp();
                     return;
                 }
-                const Column col = column;
-                if (c + 1 < NC) column.load(e, n + 32 + lane);
                 if (lane == 0) tma_stores_read<0>();  // the output tile is free
                 __syncwarp();
                 scale32(e, m0 + lane, col, out_tile, v);
@@ -763,6 +780,10 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
                  : "memory");
     return v;
 }
+__device__ __forceinline__ float4 ld_cluster_apart(uint32_t addr) {  // 32 floats apart
+    return make_float4(__int_as_float(ld_cluster(addr)), __int_as_float(ld_cluster(addr + 128)),
+                       __int_as_float(ld_cluster(addr + 256)), __int_as_float(ld_cluster(addr + 384)));
+}
 __device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
@@ -791,26 +812,29 @@ __device__ __forceinline__ void add4(float (&v)[4], uint4 u, int type) {
 
 // The outputs of a CTA's share of the tokens (every S-th, S the CTAs that share the
 // reduction), a warp a token: a lane adds four columns' partial sums of all ranks, in
-// order.  Four tokens a step, whose loads are in flight together.  part: the partial
-// tile, [token][128] in every rank's shared memory.
+// order -- consecutive ones where the outputs' rows are aligned, else 32 apart.  Several
+// tokens a step, whose loads are in flight together.  part: the partial tile,
+// [token][128] in every rank's shared memory.
 template <int S>
 __device__ __forceinline__ void few_outputs(const Epi& e, uint32_t part, int rank, int warp, int64_t m0, int rows,
                                             int64_t n0, bool bad) {
     constexpr int U = S > 4 ? 2 : 4;
     const int lane = threadIdx.x & 31;
-    const int64_t n = n0 + 4 * lane;
+    const bool vec = e.vec && n0 + 128 <= e.N;
+    const int apart = vec ? 1 : 32;
+    const int64_t n = n0 + (vec ? 4 * lane : lane);
     if (n >= e.N) return;
     uint32_t base[S];
 #pragma unroll
-    for (int s = 0; s < S; ++s) base[s] = at_rank(part + 16 * lane, s);
+    for (int s = 0; s < S; ++s) base[s] = at_rank(part + (vec ? 16 : 4) * lane, s);
     float bs[4], bias[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const bool in = n + j < e.N;
-        bs[j] = e.unbias * (e.b_scale && in ? e.b_scale[n + j] : 1.f);
-        bias[j] = e.bias && in ? sb_elem(e.bias, n + j, e.bias_type) : 0.f;
+        const int64_t at = n + j * apart;
+        const bool in = at < e.N;
+        bs[j] = e.unbias * (e.b_scale && in ? e.b_scale[at] : 1.f);
+        bias[j] = e.bias && in ? sb_elem(e.bias, at, e.bias_type) : 0.f;
     }
-    const bool vec = e.vec && n + 4 <= e.N;
     for (int t0 = rank + S * warp; t0 < rows; t0 += 4 * S * U) {
         float v[U][4];
         uint4 r[U];
@@ -823,7 +847,7 @@ __device__ __forceinline__ void few_outputs(const Epi& e, uint32_t part, int ran
             as[u] = e.a_scale ? e.a_scale[m0 + t] : 1.f;
             float4 x[S];
 #pragma unroll
-            for (int s = 0; s < S; ++s) x[s] = ld_cluster4(base[s] + t * 512);
+            for (int s = 0; s < S; ++s) x[s] = vec ? ld_cluster4(base[s] + t * 512) : ld_cluster_apart(base[s] + t * 512);
             v[u][0] = x[0].x, v[u][1] = x[0].y, v[u][2] = x[0].z, v[u][3] = x[0].w;
 #pragma unroll
             for (int s = 1; s < S; ++s) v[u][0] += x[s].x, v[u][1] += x[s].y, v[u][2] += x[s].z, v[u][3] += x[s].w;
@@ -835,7 +859,9 @@ __device__ __forceinline__ void few_outputs(const Epi& e, uint32_t part, int ran
             const int64_t m = m0 + t, at = m * e.N + n;
             if (bad) v[u][0] = v[u][1] = v[u][2] = v[u][3] = __int_as_float(0x7fc00000);
             if (!vec) {
-                for (int j = 0; j < 4 && n + j < e.N; ++j) finish(e, m, n + j, v[u][j], bs[j], bias[j]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n + 32 * j < e.N) finish(e, m, n + 32 * j, v[u][j], bs[j], bias[j]);
                 continue;
             }
 #pragma unroll
@@ -1160,23 +1186,44 @@ cudaError_t pick_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
 
 // --------------------------------------------------------------- pad rows
 
-// Column blockIdx.x * 256 + thread of 8 rows at a time, whose loads are in flight
-// together.
+// A thread's 16 bytes of a destination row, from the two 16-byte pieces that they lie
+// across in the source (whose rows start anywhere); at a row's ends, where a piece
+// reaches past the row, element by element.
 template <typename E>
 __global__ void __launch_bounds__(256) pad_rows_kernel(const E* src, int64_t ld, int64_t rows, int64_t cols, E* dst,
                                                        int64_t ldd) {
+    constexpr int V = 16 / (int)sizeof(E);
     tc::grid_dep_wait();
     tc::grid_dep_trigger();
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
     if (c >= cols) return;
-    for (int64_t r = 8 * (int64_t)blockIdx.y; r < rows; r += 8 * (int64_t)gridDim.y) {
-        E v[8];
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+        const E* row = src + r * ld;
+        const E* s = row + c;
+        const int mis = (int)(reinterpret_cast<uintptr_t>(s) & 15);
+        const E* base = s - mis / (int)sizeof(E);
+        uint4 out;
+        if (base >= row && base + (mis ? 2 * V : V) <= row + cols) {
+            const uint4 a = *reinterpret_cast<const uint4*>(base);
+            out = a;
+            if (mis) {
+                const uint4 b = *reinterpret_cast<const uint4*>(base + V);
+                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                const int k = mis >> 2, bits = 8 * (mis & 3);
+                uint32_t u[5];  // (static indices: selects, not an array in memory)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (r + i < rows) v[i] = src[(r + i) * ld + c];
+                for (int j = 0; j < 5; ++j)
+                    u[j] = k == 0 ? w[j] : k == 1 ? w[j + 1] : k == 2 ? w[j + 2] : j + 3 < 8 ? w[j + 3] : 0u;
+                out = make_uint4(__funnelshift_r(u[0], u[1], bits), __funnelshift_r(u[1], u[2], bits),
+                                 __funnelshift_r(u[2], u[3], bits), __funnelshift_r(u[3], u[4], bits));
+            }
+        } else {
+            E v[V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (r + i < rows) dst[(r + i) * ldd + c] = v[i];
+            for (int j = 0; j < V; ++j) v[j] = c + j < cols ? s[j] : E(0);
+            out = *reinterpret_cast<const uint4*>(v);
+        }
+        *reinterpret_cast<uint4*>(dst + r * ldd + c) = out;  // (ldd is a whole number of pieces)
     }
 }
 
@@ -1225,7 +1272,8 @@ cudaError_t launch_linear(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
 
 cudaError_t launch_pad_rows(const void* src, int64_t ld, int64_t rows, int64_t cols, int bytes, void* dst,
                             int64_t ldd, cudaStream_t st) {
-    const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)std::min<int64_t>((rows + 7) / 8, 4096));
+    const int64_t pieces = (cols * bytes + 15) / 16;
+    const dim3 grid((unsigned)((pieces + 255) / 256), (unsigned)std::min<int64_t>(rows, 16384));
     if (bytes == 1)
         return launch_after(pad_rows_kernel<uint8_t>, grid, dim3(256), st, static_cast<const uint8_t*>(src), ld, rows,
                             cols, static_cast<uint8_t*>(dst), ldd);

@@ -86,9 +86,9 @@ struct DzArgs {
     int64_t ldz;
     int type;
     void* db;            // [N] of `type`
-    float* part;         // [dz_chunks(M, N), N]
+    float* part;         // [dz_chunks(M, N, dy_type), N]
 };
-int dz_chunks(int64_t M, int64_t N);
+int dz_chunks(int64_t M, int64_t N, int dy_type);
 cudaError_t launch_dz(const DzArgs& a, cudaStream_t st);
 
 }  // namespace qh

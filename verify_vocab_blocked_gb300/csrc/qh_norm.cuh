@@ -248,9 +248,9 @@ __global__ void __launch_bounds__(elem_block(NT), elem_bwd_blocks(NT))
 // ------------------------------------------------------ backward, 16-byte path
 //
 // Thread t owns 8 columns of every row of its block, so a row's x and dy go
-// through a ring of kStages x R rows in shared memory of which each thread fills
+// through a ring of STAGES x R rows in shared memory of which each thread fills
 // (cp.async) and reads only its own slots: no barrier guards the ring, and the
-// loads of the next kStages - 1 steps are in flight while a step's sums go
+// loads of the next STAGES - 1 steps are in flight while a step's sums go
 // through the block's one barrier per step.  (With the loads in registers, a
 // step at a time, the kernel ran at 1.6 TB/s: 381 us at 65536 x 1536 bf16, 90 us
 // with the ring, 6.7 TB/s.)  Two fp32 lanes per instruction: what bounds it beside
@@ -260,7 +260,6 @@ __global__ void __launch_bounds__(elem_block(NT), elem_bwd_blocks(NT))
 // 4-byte operand twice 4, blockDim x 4 apart, so that a warp's copies fill whole
 // sectors (16-byte pieces 32 bytes apart fetch every sector twice: 255 us at
 // 20000 x 4096 fp32, 149 us, 6.6 TB/s, without).
-constexpr int kStages = 3;
 
 // PW consecutive elements as pairs.
 template <typename T, int PW>
@@ -340,7 +339,7 @@ __device__ __forceinline__ void block_sums(float (&s)[N], float* red, int warps)
 }
 
 // ADD: dx is added to a.add, whose pieces (of x's type) take a third share of the slots.
-template <typename T, typename DT, int R, bool CENTER, int REGS, bool ADD>
+template <typename T, typename DT, int R, bool CENTER, int REGS, int STAGES, bool ADD>
 __global__ void __maxnreg__(REGS) norm_bwd_ring_kernel(const NormBwdArgs a) {
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ float red[2][64];
@@ -405,13 +404,13 @@ __global__ void __maxnreg__(REGS) norm_bwd_ring_kernel(const NormBwdArgs a) {
         }
     };
     stats(r0);
-    for (int s = 0; s < kStages - 1; ++s) fetch(s);
+    for (int s = 0; s < STAGES - 1; ++s) fetch(s);
     int stage = 0, flip = 0;
     T* dx = static_cast<T*>(a.dx) + r0 * a.H + PW * t;
     for (; r0 < a.M; r0 += step, dx += step * a.H) {
         // into the slots whose values the step before took into registers
-        fetch(stage == 0 ? kStages - 1 : stage - 1);
-        cp_async_wait<kStages - 1>();
+        fetch(stage == 0 ? STAGES - 1 : stage - 1);
+        cp_async_wait<STAGES - 1>();
         float2 x[R][4], g[R][4];
         float s[2 * R], rs[R];
         const unsigned char* src = ring + stage * stage_bytes;
@@ -473,7 +472,7 @@ __global__ void __maxnreg__(REGS) norm_bwd_ring_kernel(const NormBwdArgs a) {
             for (int i = 0; i < NP; ++i)
                 if (on[i]) put_pairs<T, PW>(dx + k * a.H + PW * nt * i, o + i * PW / 2);
         }
-        if (++stage == kStages) stage = 0;
+        if (++stage == STAGES) stage = 0;
     }
     cp_async_wait<0>();
     tc::grid_dep_trigger();
@@ -524,21 +523,21 @@ void fit_grid(NormBwdArgs& a, int per_sm) {
     if (a.grid > n) a.grid = n;
 }
 
-// Bytes of the ring for R rows a step.
+// Bytes of a ring of `rows` rows.
 template <bool ADD, typename T, typename DT>
-int ring_bytes(int H, int R) {
-    return kStages * R * ((H / 8 + 31) / 32 * 32) * 8 * (int)(sizeof(T) * (ADD ? 2 : 1) + sizeof(DT));
+int ring_bytes(int H, int rows) {
+    return rows * ((H / 8 + 31) / 32 * 32) * 8 * (int)(sizeof(T) * (ADD ? 2 : 1) + sizeof(DT));
 }
 constexpr int kRingMost = 226 * 1024;  // with the static shared memory within 227 KB
 
-template <bool ADD, typename T, typename DT, int R, int REGS>
+template <bool ADD, typename T, typename DT, int R, int REGS, int STAGES>
 cudaError_t go_ring(NormBwdArgs& a, cudaStream_t st) {
     const int threads = (a.H / 8 + 31) / 32 * 32;
-    const int smem = ring_bytes<ADD, T, DT>(a.H, R);
+    const int smem = ring_bytes<ADD, T, DT>(a.H, STAGES * R);
     const int by_regs = 65536 / (REGS * threads), by_smem = 227 * 1024 / (smem + 1024 + 512);
     fit_grid(a, by_regs < by_smem ? by_regs : by_smem);
     auto go = [&](auto center) {
-        auto* fn = norm_bwd_ring_kernel<T, DT, R, decltype(center)::value, REGS, ADD>;
+        auto* fn = norm_bwd_ring_kernel<T, DT, R, decltype(center)::value, REGS, STAGES, ADD>;
         if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), smem)) return e;
         fn<<<(unsigned)a.grid, threads, smem, st>>>(a);
         return cudaGetLastError();
@@ -546,11 +545,16 @@ cudaError_t go_ring(NormBwdArgs& a, cudaStream_t st) {
     return a.mean ? go(std::true_type{}) : go(std::false_type{});
 }
 
-// Two rows a step while their threads fit 512 (a step's barrier is shared by
-// both) and their ring the shared memory, one above.
+// Two rows a step while their threads fit 512 (a step's barrier is shared by both),
+// one above; three stages.  With a third stream the ring leaves room for fewer blocks:
+// two stages of 2-byte rows (32768 x 1536 bf16: 70 us, 74 with three; 16384 x 2560: 62,
+// 67), one row a step of 4-byte ones (32768 x 1536 float32: 109 us, 136 with two;
+// 16384 x 2560: 101, 131).
 template <bool ADD, typename T, typename DT>
 cudaError_t pick_ring(NormBwdArgs& a, cudaStream_t st) {
-    return a.H <= 4096 && ring_bytes<ADD, T, DT>(a.H, 2) <= kRingMost ? go_ring<ADD, T, DT, 2, 80>(a, st) : go_ring<ADD, T, DT, 1, 64>(a, st);
+    if constexpr (ADD && sizeof(T) == 4) return go_ring<ADD, T, DT, 1, 64, 3>(a, st);
+    else if constexpr (ADD) return a.H <= 4096 ? go_ring<ADD, T, DT, 2, 80, 2>(a, st) : go_ring<ADD, T, DT, 1, 64, 2>(a, st);
+    else return a.H <= 4096 ? go_ring<ADD, T, DT, 2, 80, 3>(a, st) : go_ring<ADD, T, DT, 1, 64, 3>(a, st);
 }
 
 template <bool ADD, typename T>
@@ -559,7 +563,7 @@ cudaError_t pick_bwd(NormBwdArgs& a, cudaStream_t st) {
                      aligned16(a.dy) && aligned16(a.dx) && (!ADD || (a.ldadd % 8 == 0 && aligned16(a.add)));
     // (three float32 streams of more than 6272 columns do not fit a ring: single elements)
     const auto ring = [&](auto* tag) -> bool {
-        return vec && ring_bytes<ADD, T, std::remove_pointer_t<decltype(tag)>>(a.H, 1) <= kRingMost;
+        return vec && ring_bytes<ADD, T, std::remove_pointer_t<decltype(tag)>>(a.H, 3) <= kRingMost;
     };
     if (a.dy_type == kSbF32 && ring(static_cast<float*>(nullptr))) return pick_ring<ADD, T, float>(a, st);
     if (a.dy_type != kSbF32 && ring(static_cast<__half*>(nullptr)))
