@@ -13,74 +13,18 @@
 //   * pairs: CTA pairs (cta_group::2), 256 x BN output tiles, persistent; one
 //     thread streams both operands' 128-byte-swizzled tiles by TMA, one issues the
 //     MMAs into two accumulators in turn, eight warps run the epilogue of one
-//     while the other fills;
-//   * few: for few rows of A (the tokens), whose time is reading B (the weights)
-//     once: the weights' rows are the MMA's 128, the tokens its 16 to 128 columns,
-//     and the CTAs of a cluster share a tile's reduction, so that a small weight
-//     matrix is read by all SMs; their partial tiles are summed in rank order
-//     through distributed shared memory (deterministic).
+//     while the other fills, the residual and the outputs going through shared
+//     memory by TMA;
+//   * few (qh_linear_few.cu): for few rows of A.
 //
 // A bounded wait that expires makes the tile NaN.
-#include "qh_linear.cuh"
-#include "qh_tc.cuh"
-#include "qh_tmap.h"
-
-#include <algorithm>
+#include "qh_linear_epi.cuh"
 
 namespace qh {
 
 namespace {
 
-constexpr int kRowBytes = 128;   // bytes of a K-major row a stage: 64 or 128 elements
 constexpr uint16_t kPairMask = 0x3;
-
-// ----------------------------------------------------------------- epilogue
-
-__device__ __forceinline__ float activate(float z, int act) {
-    switch (act) {
-        case kActRelu: return z < 0.f ? 0.f : z;  // (keeps NaN)
-        case kActSilu: return __fdividef(z, 1.f + __expf(-z));
-        case kActGelu: {
-            const float h = normal_tail(z).x;
-            return z * (z < 0.f ? h : 1.f - h);
-        }
-        case kActGeluTanh: {  // 0.5 (1 + tanh u) = 1 / (1 + exp(-2u))
-            const float u2 = 1.5957691216f * fmaf(0.044715f * z * z, z, z);
-            return __fdividef(z, 1.f + __expf(-u2));
-        }
-        default: return z;
-    }
-}
-
-// The pre-activation as it is kept for the gradient, in fp16: beyond fp16's range every
-// activation's derivative is what it is at the range's end, so that it saturates (NaN
-// stays).
-__device__ __forceinline__ float in_half(float z) {
-    asm("max.NaN.f32 %0, %0, 0fC77FE000;\n\tmin.NaN.f32 %0, %0, 0f477FE000;" : "+f"(z));  // -+ 65504
-    return z;
-}
-__device__ __forceinline__ __half pre_of(float z) { return __float2half_rn(in_half(z)); }
-
-__device__ __forceinline__ void put(void* p, int64_t i, int type, float v) {
-    if (type == kSbF32) static_cast<float*>(p)[i] = v;
-    else if (type == kSbBf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
-
-// What a kernel needs of LinArgs beside its tensor maps.
-struct Epi {
-    int64_t M, N;
-    const float* a_scale;
-    const float* b_scale;
-    const void* bias;
-    const void* res;
-    void* y;
-    __half* pre;
-    int64_t ldr;
-    int bias_type, act, res_type, y_type;
-    float unbias;      // what every sum is multiplied by (see unbias_of)
-    int vec;           // the rows of y, pre and res are all aligned to 16 bytes
-};
 
 // What a pair walks: `full` whole tiles, then the others' parts, `split` of the
 // reduction each (one after another), whose sums go to part[item - full].
@@ -95,27 +39,6 @@ __device__ __forceinline__ void item_of(const Walk& w, int i, int n_k, int& tile
     tile = w.full + j / w.split;
     k0 = (int)((int64_t)n_k * s / w.split);
     k1 = (int)((int64_t)n_k * (s + 1) / w.split);
-}
-
-// One output of row m and column n, whose column's scale (with `unbias`) and bias
-// are at hand.
-__device__ __forceinline__ void finish(const Epi& e, int64_t m, int64_t n, float v, float bs, float bias) {
-    if (e.a_scale) v *= e.a_scale[m];
-    v = fmaf(v, bs, bias);
-    const int64_t at = m * e.N + n;
-    if (e.pre) e.pre[at] = pre_of(v);
-    v = activate(v, e.act);
-    if (e.res) v += sb_elem(e.res, m * e.ldr + n, e.res_type);
-    put(e.y, at, e.y_type, v);
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b, int type) {
-    if (type == kSbBf16) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 template <int ACT>
@@ -254,19 +177,8 @@ __device__ __forceinline__ void tma_stores_read() {
 }
 __device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// ------------------------------------------------------------------- pairs
-
-// One lane of a converged warp.  (The loops around it are run by the whole warp: the
-// compiler then keeps descriptors and barriers in uniform registers.)
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 constexpr int kEpiWarps = 8;
 constexpr int kPairThreads = 32 * (2 + kEpiWarps);
-constexpr int kSumSteps = 16;    // stages of a tensor-core sum of a float32 output
 constexpr int kJoinStages = 12;  // stages in the time that joining a shared tile takes
 
 template <int BN, bool AMN, bool BMN>
@@ -309,13 +221,6 @@ __device__ __forceinline__ void umma_f8_pair(uint32_t d, uint64_t a, uint64_t b,
         "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
-        "r"(idesc), "r"(acc)
-        : "memory");
-}
 
 // tc::tmem_wait_ld for a load issued earlier, whose registers nothing may read before.
 __device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
@@ -327,16 +232,6 @@ __device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
                  :
                  : "memory");
 }
-
-// Descriptor of an operand at `addr`: K-major rows of 128 bytes in 8-row atoms, or
-// MN-major blocks of 64 elements 8 KB apart (64 rows of K each).
-template <bool MN>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
-    return MN ? tc::sdesc_sw128(addr, 8192, 1024) : tc::sdesc_sw128(addr, 0, 1024);
-}
-// Its advance (in 16 bytes) per MMA: 32 bytes of K, or 16 rows of K.
-template <bool MN>
-constexpr uint32_t kStep = MN ? 128u : 2u;
 
 // SUMS: for float32 outputs of 16-bit operands.  The tensor cores' accumulation
 // truncates, up to a step of the running sum at each MMA; kSumSteps stages are summed
@@ -749,374 +644,12 @@ __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const __grid_
     store8_as(e.y, m * e.N + n, e.y_type, v);
 }
 
-// --------------------------------------------------------------------- few
-
-constexpr int kFewThreads = 6 * 32;
-constexpr int kFewTmem = 256;   // columns of a CTA's accumulators, at most (two CTAs to an SM)
-
-template <int T>
-struct FewLayout {
-    static constexpr int W_BYTES = 128 * kRowBytes;
-    static constexpr int X_BYTES = T * kRowBytes;
-    static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int NS = T <= 32 ? 5 : T == 64 ? 4 : 3;  // two CTAs to an SM
-    static constexpr int OFF_BAR = NS * STAGE;
-    static constexpr int BAR_BYTES = 8 * (2 * NS + 2) + 16;
-    static constexpr int SMEM = OFF_BAR + BAR_BYTES + 1024;
-    static_assert(T * 128 * 4 <= OFF_BAR, "the partial tile lies in the ring");
-    static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs to an SM");
-};
-
-__device__ __forceinline__ int ld_cluster(uint32_t addr) {
-    int v;
-    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_cluster_apart(uint32_t addr) {  // 32 floats apart
-    return make_float4(__int_as_float(ld_cluster(addr)), __int_as_float(ld_cluster(addr + 128)),
-                       __int_as_float(ld_cluster(addr + 256)), __int_as_float(ld_cluster(addr + 384)));
-}
-__device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-
-// Four consecutive elements as they lie in memory (16 bits: two words), and widened.
-__device__ __forceinline__ uint4 load4(const void* p, int64_t i, int type) {
-    if (type == kSbF32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
-    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __half*>(p) + i);  // (16 bits)
-    return make_uint4(u.x, u.y, 0u, 0u);
-}
-__device__ __forceinline__ void add4(float (&v)[4], uint4 u, int type) {
-    if (type == kSbF32) {
-        v[0] += __uint_as_float(u.x), v[1] += __uint_as_float(u.y);
-        v[2] += __uint_as_float(u.z), v[3] += __uint_as_float(u.w);
-    } else if (type == kSbBf16) {
-        v[0] += __uint_as_float(u.x << 16), v[1] += __uint_as_float(u.x & 0xffff0000u);
-        v[2] += __uint_as_float(u.y << 16), v[3] += __uint_as_float(u.y & 0xffff0000u);
-    } else {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-        v[0] += a.x, v[1] += a.y, v[2] += b.x, v[3] += b.y;
-    }
-}
-
-// The outputs of a CTA's share of the tokens (every S-th, S the CTAs that share the
-// reduction), a warp a token: a lane adds four columns' partial sums of all ranks, in
-// order -- consecutive ones where the outputs' rows are aligned, else 32 apart.  Several
-// tokens a step, whose loads are in flight together.  part: the partial tile,
-// [token][128] in every rank's shared memory.
-template <int S>
-__device__ __forceinline__ void few_outputs(const Epi& e, uint32_t part, int rank, int warp, int64_t m0, int rows,
-                                            int64_t n0, bool bad) {
-    constexpr int U = S > 4 ? 2 : 4;
-    const int lane = threadIdx.x & 31;
-    const bool vec = e.vec && n0 + 128 <= e.N;
-    const int apart = vec ? 1 : 32;
-    const int64_t n = n0 + (vec ? 4 * lane : lane);
-    if (n >= e.N) return;
-    uint32_t base[S];
-#pragma unroll
-    for (int s = 0; s < S; ++s) base[s] = at_rank(part + (vec ? 16 : 4) * lane, s);
-    float bs[4], bias[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t at = n + j * apart;
-        const bool in = at < e.N;
-        bs[j] = e.unbias * (e.b_scale && in ? e.b_scale[at] : 1.f);
-        bias[j] = e.bias && in ? sb_elem(e.bias, at, e.bias_type) : 0.f;
-    }
-    for (int t0 = rank + S * warp; t0 < rows; t0 += 4 * S * U) {
-        float v[U][4];
-        uint4 r[U];
-        float as[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = t0 + 4 * S * u;
-            if (t >= rows) continue;
-            if (vec && e.res) r[u] = load4(e.res, (m0 + t) * e.ldr + n, e.res_type);
-            as[u] = e.a_scale ? e.a_scale[m0 + t] : 1.f;
-            float4 x[S];
-#pragma unroll
-            for (int s = 0; s < S; ++s) x[s] = vec ? ld_cluster4(base[s] + t * 512) : ld_cluster_apart(base[s] + t * 512);
-            v[u][0] = x[0].x, v[u][1] = x[0].y, v[u][2] = x[0].z, v[u][3] = x[0].w;
-#pragma unroll
-            for (int s = 1; s < S; ++s) v[u][0] += x[s].x, v[u][1] += x[s].y, v[u][2] += x[s].z, v[u][3] += x[s].w;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = t0 + 4 * S * u;
-            if (t >= rows) continue;
-            const int64_t m = m0 + t, at = m * e.N + n;
-            if (bad) v[u][0] = v[u][1] = v[u][2] = v[u][3] = __int_as_float(0x7fc00000);
-            if (!vec) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (n + 32 * j < e.N) finish(e, m, n + 32 * j, v[u][j], bs[j], bias[j]);
-                continue;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[u][j] = fmaf(v[u][j] * as[u], bs[j], bias[j]);
-            if (e.pre) {
-                __half h[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) h[j] = pre_of(v[u][j]);
-                *reinterpret_cast<uint2*>(e.pre + at) = *reinterpret_cast<const uint2*>(h);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[u][j] = activate(v[u][j], e.act);
-            if (e.res) add4(v[u], r[u], e.res_type);
-            if (e.y_type == kSbF32) {
-                *reinterpret_cast<float4*>(static_cast<float*>(e.y) + at) =
-                    make_float4(v[u][0], v[u][1], v[u][2], v[u][3]);
-            } else {
-                *reinterpret_cast<uint2*>(static_cast<__half*>(e.y) + at) =  // (16 bits)
-                    make_uint2(pack2(v[u][0], v[u][1], e.y_type), pack2(v[u][2], v[u][3], e.y_type));
-            }
-        }
-    }
-}
-
-// tw: the weights, whose rows (or, WMN, columns) are the tile's 128; tx: the tokens.
-// blockIdx.x: 128-row tile and rank in the cluster of `split` (at most 8);
-// blockIdx.y: token tile.  `sums`:
-// the stages of an accumulator (a float32 output's reduction takes several, for the
-// pairs' reason, added in registers at the end); `cols`: their columns.
-template <int T, bool WMN>
-__global__ void __launch_bounds__(kFewThreads)
-    linear_few_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
-                      const __grid_constant__ Epi e, int n_k, int step_k, int split, int sums, int cols,
-                      uint32_t idesc, int f8, int stall) {
-    using L = FewLayout<T>;
-    constexpr int NS = L::NS;
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-    uint64_t* empty = full + NS;
-    uint64_t* accf = empty + NS;
-    uint64_t* mdrain = accf + 1;
-    uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(mdrain + 1);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sh + 1);
-    int* err = reinterpret_cast<int*>(tmem_base_sh + 2);
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)blockIdx.x % split;  // (= the rank in the cluster of `split`)
-    const int n0 = (int)blockIdx.x / split * 128, m0 = (int)blockIdx.y * T;
-    const int k0 = (int)((int64_t)n_k * rank / split), k1 = (int)((int64_t)n_k * (rank + 1) / split);
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) {
-            tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&empty[i], 1);
-        }
-        tc::mbar_init(accf, 1);
-        tc::mbar_init(mdrain, 1);
-        *abort_flag = 0;
-        *err = 0;
-        tc::fence_mbar_init();
-        tc::prefetch_tmap(&tw);
-        tc::prefetch_tmap(&tx);
-    }
-    if (warp == 1) {
-        tc::tmem_alloc(tmem_base_sh, cols);
-        tc::tmem_relinquish();
-    }
-    tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
-    const uint32_t tmem_base = *tmem_base_sh;
-    tc::grid_dep_wait();
-    tc::grid_dep_trigger();
-
-    bool ok = true;
-    if (warp == 0) {
-        int stage = 0;
-        uint32_t phase = 0, fills = 0;
-        for (int kk = k0; kk < k1 && stall == 0; ++kk) {
-            ok = __all_sync(0xffffffffu,
-                            tc::mbar_wait_cta(&empty[stage], phase ^ 1, abort_flag, err, tc::kErrTimeoutEmpty));
-            if (!ok) break;
-            if (elect_one()) {
-                tc::mbar_arrive_expect_tx(&full[stage], L::STAGE);
-                unsigned char* W = smem + stage * L::STAGE;
-                if constexpr (WMN) {
-                    tc::tma_load_2d(W, &tw, &full[stage], n0, kk * step_k);
-                    tc::tma_load_2d(W + 8192, &tw, &full[stage], n0 + 64, kk * step_k);
-                } else {
-                    tc::tma_load_2d(W, &tw, &full[stage], kk * step_k, n0);
-                }
-                tc::tma_load_2d(W + L::W_BYTES, &tx, &full[stage], kk * step_k, m0);
-            }
-            __syncwarp();
-            ++fills;
-            if (++stage == NS) { stage = 0; phase ^= 1; }
-        }
-        if (lane == 0) tc::drain_ring(full, NS, fills, err);  // (every copy has landed, on any path)
-    } else if (warp == 1) {
-        int stage = 0;
-        uint32_t phase = 0;
-        const uint64_t wd0 = operand_desc<WMN>(tc::smem_u32(smem));
-        const uint64_t xd0 = operand_desc<false>(tc::smem_u32(smem + L::W_BYTES));
-        for (int kk = k0; kk < k1; ++kk) {
-            ok = __all_sync(0xffffffffu,
-                            tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull));
-            if (!ok) break;
-            tc::tc_fence_after();
-            const uint64_t wd = wd0 + (uint32_t)(stage * (L::STAGE >> 4));
-            const uint64_t xd = xd0 + (uint32_t)(stage * (L::STAGE >> 4));
-            const int in = (kk - k0) % sums;
-            const uint32_t d = tmem_base + (kk - k0) / sums * T;
-            if (elect_one()) {
-                if (!WMN && f8) {
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) umma_f8(d, wd + 2 * s, xd + 2 * s, idesc, in | s);
-                } else {
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) tc::umma_f16(d, wd + kStep<WMN> * s, xd + 2 * s, idesc, in | s);
-                }
-                tc::umma_commit(&empty[stage]);
-                if (kk + 1 == k1) tc::umma_commit(accf);
-            }
-            __syncwarp();
-            if (++stage == NS) { stage = 0; phase ^= 1; }
-        }
-        if (!ok && elect_one()) {
-            tc::umma_commit(mdrain);
-            tc::mbar_drain(mdrain, 0, err);
-        }
-    } else {
-        // Lane: a weight row; the accumulator's columns: tokens.  All MMAs, and with
-        // them all copies, are done when the accumulator is: the ring is free.
-        const int sub = warp & 3, row = sub * 32 + lane;
-        ok = tc::mbar_wait_cta(accf, 0, abort_flag, err, tc::kErrTimeoutAccFull);
-        tc::tc_fence_after();
-        float* part = reinterpret_cast<float*>(smem);
-        // (after a failed wait copies may be in flight into the ring: the flag tells the cluster)
-        const int accs = (k1 - k0 + sums - 1) / sums;
-        const uint32_t d = tmem_base + ((uint32_t)(sub * 32) << 16);
-#pragma unroll 1
-        for (int c = 0; c < (T + 31) / 32; ++c) {
-            constexpr int W = T < 32 ? T : 32;  // columns of the chunk; T = 16: two accumulators a load
-            float v[W];
-#pragma unroll 1
-            for (int a = 0; a < accs; a += 32 / W) {
-                uint32_t r[32];
-                tc::tmem_ld32(d + a * T + 32 * c, r);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < W; ++j) v[j] = a == 0 ? __uint_as_float(r[j]) : v[j] + __uint_as_float(r[j]);
-                if (W < 32 && a + 1 < accs) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) v[j] += __uint_as_float(r[32 - W + j]);
-                }
-            }
-            if (ok) {
-#pragma unroll
-                for (int j = 0; j < W; ++j) part[(32 * c + j) * 128 + row] = v[j];
-            }
-        }
-        if (!ok && lane == 0) *abort_flag = tc::kErrTimeoutAccFull;
-    }
-    tc::tc_fence_before();
-    __syncthreads();
-    if (split > 1) tc::cluster_sync();
-    if (warp == 1) {
-        tc::tc_fence_after();
-        tc::tmem_dealloc(tmem_base, cols);
-    }
-    if (warp >= 2) {
-        const uint32_t part = tc::smem_u32(smem), flag = tc::smem_u32(const_cast<int*>(abort_flag));
-        bool bad = false;
-        for (int s = 0; s < split; ++s) bad |= ld_cluster(at_rank(flag, s)) != 0;
-        const int rows = (int)min((int64_t)T, e.M - m0);
-        switch (split) {
-#define QH_SHARE(S) case S: few_outputs<S>(e, part, rank, warp - 2, m0, rows, n0, bad); break
-            QH_SHARE(1);
-            QH_SHARE(2);
-            QH_SHARE(3);
-            QH_SHARE(4);
-            QH_SHARE(5);
-            QH_SHARE(6);
-            QH_SHARE(7);
-            QH_SHARE(8);
-#undef QH_SHARE
-        }
-    }
-    if (split > 1) tc::cluster_sync();  // no CTA leaves while its partial tile is read
-}
-
 // -------------------------------------------------------------------- host
-
-// Instruction descriptor: fp32 accumulate; operand formats at bits 7 and 10
-// (kind::f16: 0 fp16, 1 bf16; kind::f8f6f4: 0 e4m3).
-uint32_t idesc_of(int type, int M, int N, bool amn, bool bmn) {
-    const uint32_t f = type == kSbBf16 ? 1u : 0u;
-    return tc::idesc_f16_f32(M, N, amn, bmn) | f << 7 | f << 10;
-}
-
-// The tensor map of an operand with `rows` of the output's side and `k` of the reduction.
-bool map_operand(CUtensorMap* map, const LinOperand& o, int type, int64_t rows, int64_t k, int box_rows) {
-    const int bytes = type == kE4m3 ? 1 : 2;
-    return o.k_major ? tmap_rows_sw128(map, o.p, bytes, k, rows, o.ld * bytes, box_rows)
-                     : tmap_rows_sw128(map, o.p, bytes, rows, k, o.ld * bytes, 64);
-}
-
-// What a float32 output's sum of `mmas` MMAs is multiplied by: each truncates part of a
-// step of the running sum.  Measured over K = 256 to 10240: 1.1e-8 of the result at each
-// for values of both signs, up to 2.5e-8 for positive ones; none for e4m3, whose
-// products have few bits.
-float unbias_of(int mmas, int type) { return type == kE4m3 ? 1.f : 1.f + 1.4e-8f * (float)mmas; }
-
-// `mmas`: of a tensor-core sum.
-Epi epi_of(const LinArgs& a, int mmas) {
-    const auto rows = [](const void* p, int64_t ld, int type) {
-        return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * type_bytes(type) % 16 == 0);
-    };
-    const bool vec = rows(a.y, a.N, a.y_type) && rows(a.pre, a.N, kSbF16) && rows(a.res, a.ldr, a.res_type);
-    return Epi{a.M, a.N, a.a_scale, a.b_scale, a.bias, a.res, a.y, a.pre, a.ldr, a.bias_type, a.act, a.res_type, a.y_type,
-               unbias_of(mmas, a.type), vec};
-}
 
 // The map of an output's or the residual's 32 x 32 tiles (not made where there is none).
 bool map_tile(CUtensorMap* map, const void* p, int type, int64_t ld, const LinArgs& a, bool vec) {
     return !p || !vec ||
            tmap_tiles(map, p, type_bytes(type), (uint64_t)a.N, (uint64_t)a.M, (uint64_t)ld * type_bytes(type));
-}
-
-template <typename... P, typename... A>
-cudaError_t launch_cluster(void (*fn)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st, A... a) {
-    if (cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(fn), smem)) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(a)...);
-}
-
-// Whether the output asks for the tensor cores' sums to be short: see SUMS.
-bool in_sums(const LinArgs& a) { return a.y_type == kSbF32 && a.type != kE4m3; }
-
-int steps(const LinArgs& a, int* step) {
-    *step = a.type == kE4m3 ? 128 : 64;
-    return (int)((a.K + *step - 1) / *step);
 }
 
 template <int BN, bool AMN, bool BMN, bool SUMS>
@@ -1143,37 +676,6 @@ cudaError_t go_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
     if (full == tiles) return cudaSuccess;
     return launch_after(linear_join_kernel<BN>, dim3(256 * BN / 8 / kJoinThreads, (unsigned)(tiles - full)),
                         dim3(kJoinThreads), st, e, walk);
-}
-
-template <int T, bool WMN>
-cudaError_t go_few(const LinArgs& a, int split, cudaStream_t st) {
-    using L = FewLayout<T>;
-    CUtensorMap tw, tx;
-    if (!map_operand(&tw, a.b, a.type, a.N, a.K, 128) || !map_operand(&tx, a.a, a.type, a.M, a.K, T))
-        return cudaErrorInvalidValue;
-    int step;
-    const int n_k = steps(a, &step);
-    // a CTA's stages in one accumulator, or for float32 kSumSteps in each while they fit
-    const int share = (n_k + split - 1) / split;
-    int accs = 1;
-    if (in_sums(a)) accs = std::min(kFewTmem / T, (share + kSumSteps - 1) / kSumSteps);
-    const int sums = (share + accs - 1) / accs;
-    int cols = 32;
-    while (cols < accs * T) cols *= 2;
-    const dim3 grid((unsigned)((a.N + 127) / 128 * split), (unsigned)((a.M + T - 1) / T));
-    return launch_cluster(linear_few_kernel<T, WMN>, grid, kFewThreads, L::SMEM, split, st, tw, tx,
-                          epi_of(a, in_sums(a) ? 4 * sums : 0), n_k, step, split, sums, cols, idesc_of(a.type, 128, T, WMN, false),
-                          (int)(a.type == kE4m3), a.stall);
-}
-
-template <bool WMN>
-cudaError_t pick_few(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
-    switch (p.tile) {
-        case 16: return go_few<16, WMN>(a, p.split, st);
-        case 32: return go_few<32, WMN>(a, p.split, st);
-        case 64: return go_few<64, WMN>(a, p.split, st);
-        default: return go_few<128, WMN>(a, p.split, st);
-    }
 }
 
 template <bool AMN, bool BMN>
@@ -1234,13 +736,15 @@ LinPlan plan_linear(const LinArgs& a, int sms) {
     p.split = 1;
     int step;
     const int n_k = steps(a, &step);
-    // Few rows: tiles of the rows' own number up to 64.  65 to 256 rows go as several
-    // tiles of 64 while these leave three parts of the reduction each (128 x 2560 x 2560:
-    // 10.2 us, in one tile of 128 12.2, on pairs 13.4; 200 rows: 12.6, 13.7 on pairs),
-    // up to 128 else in one of 128 (128 x 2560 x 10240: 19.2 us, 28 in two, 20.3 on pairs).
+    // Few rows: tiles of the rows' own number up to 64.  65 to 128 rows go as two tiles of
+    // 64 while these leave three parts of the reduction each (128 x 2560 x 2560: 10.3 us,
+    // in one tile of 128 11.7, on pairs 13.4), else in one of 128 (128 x 2560 x 10240: 18.7
+    // us, 23.6 in two, 19.6 on pairs); up to 256 rows as tiles of 64 while, too, the
+    // reduction is short (200 x 2560 x 2560: 12.7 us, 13.7 on pairs; 200 x 10240 x 2560: 27
+    // and 22).
     const int64_t strips = (a.N + 127) / 128, most = sms * 8 / 5;
     const bool several = strips * ((a.M + 63) / 64) * 3 <= most;
-    if (a.a.k_major && (a.M <= 128 || (a.M <= 256 && several))) {
+    if (a.a.k_major && (a.M <= 128 || (a.M <= 256 && several && n_k <= 64))) {
         p.few = true;
         p.tile = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 || several ? 64 : 128;
         // about 1.6 CTAs to an SM (two fit): fewer leave SMs idle, more queue (5 x 2560 x
@@ -1265,7 +769,7 @@ LinPlan plan_linear(const LinArgs& a, int sms) {
 }
 
 cudaError_t launch_linear(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
-    if (p.few) return a.b.k_major ? pick_few<false>(a, p, st) : pick_few<true>(a, p, st);
+    if (p.few) return launch_linear_few(a, p, st);
     if (!a.a.k_major) return pick_pair<true, true>(a, p, st);
     return a.b.k_major ? pick_pair<false, false>(a, p, st) : pick_pair<false, true>(a, p, st);
 }
@@ -1282,3 +786,4 @@ cudaError_t launch_pad_rows(const void* src, int64_t ld, int64_t rows, int64_t c
 }
 
 }  // namespace qh
+

@@ -1,5 +1,5 @@
 // qh_linear.cuh -- launchers of the matrix product with its epilogue and of its
-// gradient (qh_linear.cu, qh_linear_bwd.cu).
+// gradient (qh_linear.cu, qh_linear_few.cu, qh_linear_bwd.cu).
 #pragma once
 
 #include <cuda.h>
@@ -68,6 +68,7 @@ struct LinPlan {
 };
 LinPlan plan_linear(const LinArgs& a, int sms);
 cudaError_t launch_linear(const LinArgs& a, const LinPlan& p, cudaStream_t st);
+cudaError_t launch_linear_few(const LinArgs& a, const LinPlan& p, cudaStream_t st);  // p.few
 
 // Rows of 1- or 2-byte elements into rows whose starts are 16-byte aligned.
 cudaError_t launch_pad_rows(const void* src, int64_t ld, int64_t rows, int64_t cols, int bytes,

@@ -1,0 +1,360 @@
+// qh_linear_few.cu -- the matrix product of few rows (tokens).
+//
+// Its time is reading the weights once.  Their rows are the MMA's 128, the tokens its
+// 16 to 128 columns, and the CTAs of a cluster share a tile's reduction, so that a small
+// weight matrix is read by all SMs; their partial tiles are summed in rank order through
+// distributed shared memory (deterministic).  The weights K-major (the forward) or down
+// their rows (dx = dz W).
+//
+// 5 x 2560 x 2560 bf16 from DRAM: 7.4 us a call in a graph, of which 2 are the bytes; the
+// rest is the chain of launch, first loads, cluster barriers and the last stores.
+// 5 x 2560 x 10240: 13.5 us, 3.9 TB/s.
+#include "qh_linear_epi.cuh"
+
+namespace qh {
+
+namespace {
+
+__device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
+        "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+
+constexpr int kFewThreads = 6 * 32;
+constexpr int kFewTmem = 256;   // columns of a CTA's accumulators, at most (two CTAs to an SM)
+
+template <int T>
+struct FewLayout {
+    static constexpr int W_BYTES = 128 * kRowBytes;
+    static constexpr int X_BYTES = T * kRowBytes;
+    static constexpr int STAGE = W_BYTES + X_BYTES;
+    static constexpr int NS = T <= 32 ? 5 : T == 64 ? 4 : 3;  // two CTAs to an SM
+    static constexpr int OFF_BAR = NS * STAGE;
+    static constexpr int BAR_BYTES = 8 * (2 * NS + 2) + 16;
+    static constexpr int SMEM = OFF_BAR + BAR_BYTES + 1024;
+    static_assert(T * 128 * 4 <= OFF_BAR, "the partial tile lies in the ring");
+    static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs to an SM");
+};
+
+__device__ __forceinline__ int ld_cluster(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_apart(uint32_t addr) {  // 32 floats apart
+    return make_float4(__int_as_float(ld_cluster(addr)), __int_as_float(ld_cluster(addr + 128)),
+                       __int_as_float(ld_cluster(addr + 256)), __int_as_float(ld_cluster(addr + 384)));
+}
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+// Four consecutive elements as they lie in memory (16 bits: two words), and widened.
+__device__ __forceinline__ uint4 load4(const void* p, int64_t i, int type) {
+    if (type == kSbF32) return *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __half*>(p) + i);  // (16 bits)
+    return make_uint4(u.x, u.y, 0u, 0u);
+}
+__device__ __forceinline__ void add4(float (&v)[4], uint4 u, int type) {
+    if (type == kSbF32) {
+        v[0] += __uint_as_float(u.x), v[1] += __uint_as_float(u.y);
+        v[2] += __uint_as_float(u.z), v[3] += __uint_as_float(u.w);
+    } else if (type == kSbBf16) {
+        v[0] += __uint_as_float(u.x << 16), v[1] += __uint_as_float(u.x & 0xffff0000u);
+        v[2] += __uint_as_float(u.y << 16), v[3] += __uint_as_float(u.y & 0xffff0000u);
+    } else {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+        v[0] += a.x, v[1] += a.y, v[2] += b.x, v[3] += b.y;
+    }
+}
+
+// The outputs of a CTA's share of the tokens (every split-th; split <= S CTAs share the
+// reduction), a warp a token: a lane adds four columns' partial sums of all ranks, in
+// order -- consecutive ones where the outputs' rows are aligned, else 32 apart.  Several
+// tokens a step, whose loads are in flight together.  part: the partial tile,
+// [token][128] in every rank's shared memory.
+template <int S>
+__device__ __forceinline__ void few_outputs(const Epi& e, uint32_t part, int rank, int split, int warp, int64_t m0, int rows,
+                                            int64_t n0, bool bad) {
+    constexpr int U = S > 4 ? 2 : 4;
+    const int lane = threadIdx.x & 31;
+    const bool vec = e.vec && n0 + 128 <= e.N;
+    const int apart = vec ? 1 : 32;
+    const int64_t n = n0 + (vec ? 4 * lane : lane);
+    if (n >= e.N) return;
+    uint32_t base[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) base[s] = at_rank(part + (vec ? 16 : 4) * lane, s < split ? s : 0);
+    float bs[4], bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int64_t at = n + j * apart;
+        const bool in = at < e.N;
+        bs[j] = e.unbias * (e.b_scale && in ? e.b_scale[at] : 1.f);
+        bias[j] = e.bias && in ? sb_elem(e.bias, at, e.bias_type) : 0.f;
+    }
+    for (int t0 = rank + split * warp; t0 < rows; t0 += 4 * split * U) {
+        float v[U][4];
+        uint4 r[U];
+        float as[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + 4 * split * u;
+            if (t >= rows) continue;
+            if (vec && e.res) r[u] = load4(e.res, (m0 + t) * e.ldr + n, e.res_type);
+            as[u] = e.a_scale ? e.a_scale[m0 + t] : 1.f;
+            float4 x[S];
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+                if (s < split) x[s] = vec ? ld_cluster4(base[s] + t * 512) : ld_cluster_apart(base[s] + t * 512);
+            v[u][0] = x[0].x, v[u][1] = x[0].y, v[u][2] = x[0].z, v[u][3] = x[0].w;
+#pragma unroll
+            for (int s = 1; s < S; ++s)
+                if (s < split) v[u][0] += x[s].x, v[u][1] += x[s].y, v[u][2] += x[s].z, v[u][3] += x[s].w;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + 4 * split * u;
+            if (t >= rows) continue;
+            const int64_t m = m0 + t, at = m * e.N + n;
+            if (bad) v[u][0] = v[u][1] = v[u][2] = v[u][3] = __int_as_float(0x7fc00000);
+            if (!vec) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n + 32 * j < e.N) finish(e, m, n + 32 * j, v[u][j], bs[j], bias[j]);
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[u][j] = fmaf(v[u][j] * as[u], bs[j], bias[j]);
+            if (e.pre) {
+                __half h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = pre_of(v[u][j]);
+                *reinterpret_cast<uint2*>(e.pre + at) = *reinterpret_cast<const uint2*>(h);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[u][j] = activate(v[u][j], e.act);
+            if (e.res) add4(v[u], r[u], e.res_type);
+            if (e.y_type == kSbF32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(e.y) + at) =
+                    make_float4(v[u][0], v[u][1], v[u][2], v[u][3]);
+            } else {
+                *reinterpret_cast<uint2*>(static_cast<__half*>(e.y) + at) =  // (16 bits)
+                    make_uint2(pack2(v[u][0], v[u][1], e.y_type), pack2(v[u][2], v[u][3], e.y_type));
+            }
+        }
+    }
+}
+
+// tw: the weights, whose rows (or, WMN, columns) are the tile's 128; tx: the tokens.
+// blockIdx.x: 128-row tile and rank in the cluster of `split` (at most 8);
+// blockIdx.y: token tile.  `sums`:
+// the stages of an accumulator (a float32 output's reduction takes several, for the
+// pairs' reason, added in registers at the end); `cols`: their columns.
+template <int T, bool WMN>
+__global__ void __launch_bounds__(kFewThreads)
+    linear_few_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
+                      const __grid_constant__ Epi e, int n_k, int step_k, int split, int sums, int cols,
+                      uint32_t idesc, int f8, int stall) {
+    using L = FewLayout<T>;
+    constexpr int NS = L::NS;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+    uint64_t* empty = full + NS;
+    uint64_t* accf = empty + NS;
+    uint64_t* mdrain = accf + 1;
+    uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(mdrain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sh + 1);
+    int* err = reinterpret_cast<int*>(tmem_base_sh + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)blockIdx.x % split;  // (= the rank in the cluster of `split`)
+    const int n0 = (int)blockIdx.x / split * 128, m0 = (int)blockIdx.y * T;
+    const int k0 = (int)((int64_t)n_k * rank / split), k1 = (int)((int64_t)n_k * (rank + 1) / split);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 1);
+        }
+        tc::mbar_init(accf, 1);
+        tc::mbar_init(mdrain, 1);
+        *abort_flag = 0;
+        *err = 0;
+        tc::fence_mbar_init();
+        tc::prefetch_tmap(&tw);
+        tc::prefetch_tmap(&tx);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_base_sh, cols);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem_base = *tmem_base_sh;
+    tc::grid_dep_wait();
+    tc::grid_dep_trigger();
+
+    bool ok = true;
+    if (warp == 0) {
+        int stage = 0;
+        uint32_t phase = 0, fills = 0;
+        for (int kk = k0; kk < k1 && stall == 0; ++kk) {
+            ok = __all_sync(0xffffffffu,
+                            tc::mbar_wait_cta(&empty[stage], phase ^ 1, abort_flag, err, tc::kErrTimeoutEmpty));
+            if (!ok) break;
+            if (elect_one()) {
+                tc::mbar_arrive_expect_tx(&full[stage], L::STAGE);
+                unsigned char* W = smem + stage * L::STAGE;
+                if constexpr (WMN) {
+                    tc::tma_load_2d(W, &tw, &full[stage], n0, kk * step_k);
+                    tc::tma_load_2d(W + 8192, &tw, &full[stage], n0 + 64, kk * step_k);
+                } else {
+                    tc::tma_load_2d(W, &tw, &full[stage], kk * step_k, n0);
+                }
+                tc::tma_load_2d(W + L::W_BYTES, &tx, &full[stage], kk * step_k, m0);
+            }
+            __syncwarp();
+            ++fills;
+            if (++stage == NS) { stage = 0; phase ^= 1; }
+        }
+        if (lane == 0) tc::drain_ring(full, NS, fills, err);  // (every copy has landed, on any path)
+    } else if (warp == 1) {
+        int stage = 0;
+        uint32_t phase = 0;
+        const uint64_t wd0 = operand_desc<WMN>(tc::smem_u32(smem));
+        const uint64_t xd0 = operand_desc<false>(tc::smem_u32(smem + L::W_BYTES));
+        for (int kk = k0; kk < k1; ++kk) {
+            ok = __all_sync(0xffffffffu,
+                            tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull));
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint64_t wd = wd0 + (uint32_t)(stage * (L::STAGE >> 4));
+            const uint64_t xd = xd0 + (uint32_t)(stage * (L::STAGE >> 4));
+            const int in = (kk - k0) % sums;
+            const uint32_t d = tmem_base + (kk - k0) / sums * T;
+            if (elect_one()) {
+                if (!WMN && f8) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) umma_f8(d, wd + 2 * s, xd + 2 * s, idesc, in | s);
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) tc::umma_f16(d, wd + kStep<WMN> * s, xd + 2 * s, idesc, in | s);
+                }
+                tc::umma_commit(&empty[stage]);
+                if (kk + 1 == k1) tc::umma_commit(accf);
+            }
+            __syncwarp();
+            if (++stage == NS) { stage = 0; phase ^= 1; }
+        }
+        if (!ok && elect_one()) {
+            tc::umma_commit(mdrain);
+            tc::mbar_drain(mdrain, 0, err);
+        }
+    } else {
+        // Lane: a weight row; the accumulator's columns: tokens.  All MMAs, and with
+        // them all copies, are done when the accumulator is: the ring is free.
+        const int sub = warp & 3, row = sub * 32 + lane;
+        ok = tc::mbar_wait_cta(accf, 0, abort_flag, err, tc::kErrTimeoutAccFull);
+        tc::tc_fence_after();
+        float* part = reinterpret_cast<float*>(smem);
+        // (after a failed wait copies may be in flight into the ring: the flag tells the cluster)
+        const int accs = (k1 - k0 + sums - 1) / sums;
+        const uint32_t d = tmem_base + ((uint32_t)(sub * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < (T + 31) / 32; ++c) {
+            constexpr int W = T < 32 ? T : 32;  // columns of the chunk; T = 16: two accumulators a load
+            float v[W];
+#pragma unroll 1
+            for (int a = 0; a < accs; a += 32 / W) {
+                uint32_t r[32];
+                tc::tmem_ld32(d + a * T + 32 * c, r);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < W; ++j) v[j] = a == 0 ? __uint_as_float(r[j]) : v[j] + __uint_as_float(r[j]);
+                if (W < 32 && a + 1 < accs) {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v[j] += __uint_as_float(r[32 - W + j]);
+                }
+            }
+            if (ok) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) part[(32 * c + j) * 128 + row] = v[j];
+            }
+        }
+        if (!ok && lane == 0) *abort_flag = tc::kErrTimeoutAccFull;
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (split > 1) tc::cluster_sync();
+    if (warp == 1) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem_base, cols);
+    }
+    if (warp >= 2) {
+        const uint32_t part = tc::smem_u32(smem), flag = tc::smem_u32(const_cast<int*>(abort_flag));
+        bool bad = false;
+        for (int s = 0; s < split; ++s) bad |= ld_cluster(at_rank(flag, s)) != 0;
+        const int rows = (int)min((int64_t)T, e.M - m0);
+        if (split <= 2) few_outputs<2>(e, part, rank, split, warp - 2, m0, rows, n0, bad);
+        else if (split <= 4) few_outputs<4>(e, part, rank, split, warp - 2, m0, rows, n0, bad);
+        else few_outputs<8>(e, part, rank, split, warp - 2, m0, rows, n0, bad);
+    }
+    if (split > 1) tc::cluster_sync();  // no CTA leaves while its partial tile is read
+}
+
+template <int T, bool WMN>
+cudaError_t go_few(const LinArgs& a, int split, cudaStream_t st) {
+    using L = FewLayout<T>;
+    CUtensorMap tw, tx;
+    if (!map_operand(&tw, a.b, a.type, a.N, a.K, 128) || !map_operand(&tx, a.a, a.type, a.M, a.K, T))
+        return cudaErrorInvalidValue;
+    int step;
+    const int n_k = steps(a, &step);
+    // a CTA's stages in one accumulator, or for float32 kSumSteps in each while they fit
+    const int share = (n_k + split - 1) / split;
+    int accs = 1;
+    if (in_sums(a)) accs = std::min(kFewTmem / T, (share + kSumSteps - 1) / kSumSteps);
+    const int sums = (share + accs - 1) / accs;
+    int cols = 32;
+    while (cols < accs * T) cols *= 2;
+    const dim3 grid((unsigned)((a.N + 127) / 128 * split), (unsigned)((a.M + T - 1) / T));
+    return launch_cluster(linear_few_kernel<T, WMN>, grid, kFewThreads, L::SMEM, split, st, tw, tx,
+                          epi_of(a, in_sums(a) ? 4 * sums : 0), n_k, step, split, sums, cols, idesc_of(a.type, 128, T, WMN, false),
+                          (int)(a.type == kE4m3), a.stall);
+}
+
+template <bool WMN>
+cudaError_t pick_few(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
+    switch (p.tile) {
+        case 16: return go_few<16, WMN>(a, p.split, st);
+        case 32: return go_few<32, WMN>(a, p.split, st);
+        case 64: return go_few<64, WMN>(a, p.split, st);
+        default: return go_few<128, WMN>(a, p.split, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_few(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
+    return a.b.k_major ? pick_few<false>(a, p, st) : pick_few<true>(a, p, st);
+}
+
+}  // namespace qh
