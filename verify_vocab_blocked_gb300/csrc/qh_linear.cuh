@@ -5,6 +5,7 @@
 #include <cuda.h>
 
 #include "qh_ops.cuh"
+#include "qh_tc.cuh"
 
 namespace qh {
 
@@ -13,19 +14,27 @@ constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTa
 // 8-bit operands (QHEAD_E4M3); kSb* are the other element types.
 constexpr int kE4m3 = 3;
 
-// The normal distribution beyond |z|: its mass h = Phi(-|z|), and its density at z.
+// 1 / (1 + 2^a): an infinite power gives 0.
+__device__ __forceinline__ float logistic2(float a) { return tc::rcp_approx(1.f + tc::ex2_approx(a)); }
+// silu(z) / z, and (1 + tanh u) / 2 = 1 / (1 + exp(-2u)) of gelu's form with tanh, u =
+// sqrt(2 / pi) (z + 0.044715 z^3); log2(e) in the constants.
+__device__ __forceinline__ float silu_gate(float z) { return logistic2(z * -1.4426950409f); }
+__device__ __forceinline__ float tanh_gate(float z, float z2) {
+    return logistic2(z * fmaf(z2, -0.10294324f, -2.3022082f));
+}
+
+// The normal distribution beyond |z|: its mass h = Phi(-|z|), and exp(-z^2 / 2).
 // From erfc(x) = p(t) exp(-x^2), t = 1 / (1 + 0.3275911 x) with p of degree 5
 // (Abramowitz and Stegun, 7.1.26; off by at most 1.5e-7, so gelu and its derivative by
-// 0.8e-7 |z|), a third of erff's instructions.
-__device__ __forceinline__ float2 normal_tail(float z) {
-    const float x = fabsf(z) * 0.70710678f;
-    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f) * t;
-    const float e = __expf(-x * x);
-    return make_float2(0.5f * p * e, 0.39894228f * e);
+// 0.8e-7 |z|), a third of erff's instructions.  Here x = |z| / sqrt(2) and h = erfc / 2.
+__device__ __forceinline__ float2 normal_tail(float z, float z2) {
+    const float t = tc::rcp_approx(fmaf(0.23164189f, fabsf(z), 1.f));
+    float p = fmaf(0.5307027145f, t, -0.7265760135f);
+    p = fmaf(p, t, 0.7107068705f);
+    p = fmaf(p, t, -0.142248368f);
+    p = fmaf(p, t, 0.127414796f) * t;
+    const float e = tc::ex2_approx(z2 * -0.7213475204f);
+    return make_float2(p * e, e);
 }
 
 // A matrix operand of the product: rows of `ld` elements whose starts are

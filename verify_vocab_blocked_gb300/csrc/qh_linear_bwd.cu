@@ -23,16 +23,15 @@ __device__ __forceinline__ float act_grad(float z, int act) {
     switch (act) {
         case kActRelu: return z > 0.f ? 1.f : z != z ? z : 0.f;
         case kActSilu: {
-            const float p = __fdividef(1.f, 1.f + __expf(-z));
+            const float p = silu_gate(z);
             return p * fmaf(z, 1.f - p, 1.f);
         }
-        case kActGelu: {
-            const float2 n = normal_tail(z);
-            return fmaf(z, n.y, z < 0.f ? n.x : 1.f - n.x);
+        case kActGelu: {  // Phi(z) + z phi(z)
+            const float2 n = normal_tail(z, z * z);
+            return fmaf(z * 0.39894228f, n.y, z < 0.f ? n.x : 1.f - n.x);
         }
         case kActGeluTanh: {  // s = (1 + tanh u) / 2;  s + z u' 2 s (1 - s)
-            const float z2 = z * z;
-            const float s = __fdividef(1.f, 1.f + __expf(-1.5957691216f * fmaf(0.044715f * z2, z, z)));
+            const float z2 = z * z, s = tanh_gate(z, z2);
             return fmaf(z * 1.5957691216f * fmaf(0.134145f, z2, 1.f), s * (1.f - s), s);
         }
         default: return 1.f;

@@ -20,15 +20,12 @@ constexpr int kSumSteps = 16;    // stages of a tensor-core sum of a float32 out
 __device__ __forceinline__ float activate(float z, int act) {
     switch (act) {
         case kActRelu: return z < 0.f ? 0.f : z;  // (keeps NaN)
-        case kActSilu: return __fdividef(z, 1.f + __expf(-z));
+        case kActSilu: return z * silu_gate(z);
         case kActGelu: {
-            const float h = normal_tail(z).x;
+            const float h = normal_tail(z, z * z).x;
             return z * (z < 0.f ? h : 1.f - h);
         }
-        case kActGeluTanh: {  // 0.5 (1 + tanh u) = 1 / (1 + exp(-2u))
-            const float u2 = 1.5957691216f * fmaf(0.044715f * z * z, z, z);
-            return __fdividef(z, 1.f + __expf(-u2));
-        }
+        case kActGeluTanh: return z * tanh_gate(z, z * z);
         default: return z;
     }
 }
