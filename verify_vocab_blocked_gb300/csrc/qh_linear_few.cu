@@ -40,6 +40,11 @@ struct FewLayout {
     static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs to an SM");
 };
 
+__device__ __forceinline__ void prefetch_l2(const CUtensorMap* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
 __device__ __forceinline__ int ld_cluster(uint32_t addr) {
     int v;
     asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -209,6 +214,17 @@ __global__ void __launch_bounds__(kFewThreads)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem_base = *tmem_base_sh;
+    // The ring's first tiles of the weights on their way into L2 while the kernel before ends
+    // (a hint: what it may still write to them is written there, too).
+    if (warp == 0 && stall == 0 && lane < NS && k0 + lane < k1) {
+        const int k = (k0 + lane) * step_k;
+        if constexpr (WMN) {
+            prefetch_l2(&tw, n0, k);
+            prefetch_l2(&tw, n0 + 64, k);
+        } else {
+            prefetch_l2(&tw, k, n0);
+        }
+    }
     tc::grid_dep_wait();
     tc::grid_dep_trigger();
 
