@@ -747,10 +747,11 @@ LinPlan plan_linear(const LinArgs& a, int sms) {
     if (a.a.k_major && (a.M <= 128 || (a.M <= 256 && several && n_k <= 64))) {
         p.few = true;
         p.tile = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 || several ? 64 : 128;
-        // about 1.6 CTAs to an SM (two fit): fewer leave SMs idle, more queue (5 x 2560 x
-        // 10240, 80 strips: 13.5 us in 3 parts, 13.8 in 2, 19.2 in 4)
-        const int64_t tiles = strips * ((a.M + p.tile - 1) / p.tile);
-        p.split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, n_k), most / tiles));
+        // CTAs as many as 0.8 to 0.9 of those that fit, two to an SM or, of 16 rows, three:
+        // fewer leave SMs idle, more queue (5 x 2560 x 10240, 80 strips: 12.4 us in 5 parts,
+        // 13.9 in 3; 64 rows: 15.4 in 3, 17.5 in 2, 22 in 5)
+        const int64_t tiles = strips * ((a.M + p.tile - 1) / p.tile), fit = p.tile <= 16 ? sms * 8 / 3 : most;
+        p.split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, n_k), fit / tiles));
         return p;
     }
     // (256 columns of sums in registers would not fit)

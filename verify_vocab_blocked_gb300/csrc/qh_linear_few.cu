@@ -6,9 +6,9 @@
 // distributed shared memory (deterministic).  The weights K-major (the forward) or down
 // their rows (dx = dz W).
 //
-// 5 x 2560 x 2560 bf16 from DRAM: 7.4 us a call in a graph, of which 2 are the bytes; the
+// 5 x 2560 x 2560 bf16 from DRAM: 6.7 us a call in a graph, of which 2 are the bytes; the
 // rest is the chain of launch, first loads, cluster barriers and the last stores.
-// 5 x 2560 x 10240: 13.5 us, 3.9 TB/s.
+// 5 x 2560 x 10240: 12.4 us, 4.2 TB/s.
 #include "qh_linear_epi.cuh"
 
 namespace qh {
@@ -25,19 +25,24 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint
 
 
 constexpr int kFewThreads = 6 * 32;
-constexpr int kFewTmem = 256;   // columns of a CTA's accumulators, at most (two CTAs to an SM)
+// CTAs to an SM, and the columns of their accumulators at most: the SM's 512 hold them
+// all, so that no CTA of a cluster waits for tensor memory that another cluster holds.
+constexpr int few_per_sm(int tile) { return tile <= 16 ? 3 : 2; }
+constexpr int few_tmem(int tile) { return tile <= 16 ? 128 : 256; }
 
 template <int T>
 struct FewLayout {
     static constexpr int W_BYTES = 128 * kRowBytes;
     static constexpr int X_BYTES = T * kRowBytes;
     static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int NS = T <= 32 ? 5 : T == 64 ? 4 : 3;  // two CTAs to an SM
+    static constexpr int NS = T == 32 ? 5 : T == 128 ? 3 : 4;
     static constexpr int OFF_BAR = NS * STAGE;
     static constexpr int BAR_BYTES = 8 * (2 * NS + 2) + 16;
     static constexpr int SMEM = OFF_BAR + BAR_BYTES + 1024;
     static_assert(T * 128 * 4 <= OFF_BAR, "the partial tile lies in the ring");
-    static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs to an SM");
+    static_assert(few_per_sm(T) * (SMEM + 1024) <= 228 * 1024, "CTAs to an SM");
+    static_assert((few_per_sm(T) + 1) * (SMEM + 1024) > 228 * 1024 && few_per_sm(T) * few_tmem(T) <= 512,
+                  "tensor memory for all that fit");
 };
 
 __device__ __forceinline__ void prefetch_l2(const CUtensorMap* map, int x, int y) {
@@ -347,7 +352,7 @@ cudaError_t go_few(const LinArgs& a, int split, cudaStream_t st) {
     // a CTA's stages in one accumulator, or for float32 kSumSteps in each while they fit
     const int share = (n_k + split - 1) / split;
     int accs = 1;
-    if (in_sums(a)) accs = std::min(kFewTmem / T, (share + kSumSteps - 1) / kSumSteps);
+    if (in_sums(a)) accs = std::min(few_tmem(T) / T, (share + kSumSteps - 1) / kSumSteps);
     const int sums = (share + accs - 1) / accs;
     int cols = 32;
     while (cols < accs * T) cols *= 2;
