@@ -91,6 +91,17 @@ def check(x, w, xs, ws, b, act, r, out, want_pre=False):
     (301, 1541, 2563, HF, 3, 0, "gelu_tanh", F, None, F),
     (1000, 72, 1000, BF, 8, 8, "relu", F, F, F),
     (2049, 1536, 2560, BF, 0, 0, "gelu", BF, BF, BF),
+    # tiles whose reduction is shared, alone and behind full rounds; ragged, unaligned
+    (300, 4096, 600, BF, 0, 0, "silu", BF, BF, BF),
+    (300, 4100, 601, HF, 4, 0, "gelu", F, HF, HF),
+    (257, 3000, 520, BF, 0, 8, "none", None, F, F),
+    (2500, 2560, 2600, BF, 0, 0, "silu", F, F, BF),
+    # every count of parts of few rows, and several tiles of 64
+    (7, 192, 300, BF, 0, 0, "none", BF, None, BF),
+    (12, 1000, 20000, HF, 0, 0, "relu", None, HF, HF),
+    (100, 2560, 700, BF, 0, 0, "gelu_tanh", BF, BF, BF),
+    (190, 2000, 1300, BF, 8, 0, "silu", BF, F, F),
+    (256, 576, 1001, HF, 0, 0, "none", F, None, HF),
 ])
 def test_forward(M, K, N, t, pad, padw, act, bias, res, out):
     x, w, xs, ws = operands(M, K, N, t, M + K + N, pad, padw)
@@ -109,6 +120,8 @@ def test_forward(M, K, N, t, pad, padw, act, bias, res, out):
     (130, 256, 256, 0, "none", None, None, F),
     (515, 1536, 2563, 0, "gelu_tanh", BF, F, F),
     (300, 1001, 520, 7, "relu", None, BF, HF),
+    (300, 4096, 600, 0, "silu", F, BF, BF),
+    (200, 4000, 700, 0, "none", BF, None, F),
 ])
 def test_forward_of_8_bits(M, K, N, pad, act, bias, res, out):
     x, w, xs, ws = operands(M, K, N, E8, M + K + N, pad)
@@ -164,6 +177,9 @@ def check_bwd(M, K, N, t, act, dt, pad=0, padw=0, seed=0):
     (515, 1536, 1030, BF, "silu", BF, 0, 0),
     (2000, 520, 264, BF, "none", F, 0, 0),
     (4100, 128, 2563, HF, "gelu", HF, 0, 0),
+    (5000, 600, 300, BF, "silu", BF, 0, 0),       # shared reductions: over 5000 rows,
+    (300, 264, 4200, HF, "none", HF, 0, 0),       # over 4200 columns
+    (190, 300, 1000, BF, "gelu_tanh", BF, 0, 0),  # few rows, weights down their rows
 ])
 def test_gradient(M, K, N, t, act, dt, pad, padw):
     check_bwd(M, K, N, t, act, dt, pad, padw)

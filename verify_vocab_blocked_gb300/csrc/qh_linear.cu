@@ -236,7 +236,7 @@ __device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
 // SUMS: for float32 outputs of 16-bit operands.  The tensor cores' accumulation
 // truncates, up to a step of the running sum at each MMA; kSumSteps stages are summed
 // there, and these sums in registers, rounded to nearest.  Error over the result's
-// norm at K = 1541: 2.1e-6 in one sum, 4e-7 so (4 stages 1.4e-7, but then the epilogue
+// norm at K = 1541: 2.1e-6 in one sum, 5.4e-7 so (4 stages 1.4e-7, but then the epilogue
 // sets the pace: 2048 x 2560 x 10240 in 196 us, 111 with 16), 3 to 7e-7 an fp32 product.
 template <int BN, bool AMN, bool BMN, bool SUMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -516,7 +516,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const bool ok = tc::mbar_wait_cta(&resb[slot], rphase, abort_flag, err, tc::kErrTimeoutFull);
                     if (!ok) tc::mbar_drain(&resb[slot], rphase, err);
                     add32(res_tile + 2048 * slot, lane, v, e.res_type);
-                    if (!ok) v[0] = nan;
+                    if (!ok) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = nan;
+                    }
                     if (++slot == slots) { slot = 0; rphase ^= 1; }
                     __syncwarp();
                     ask();
