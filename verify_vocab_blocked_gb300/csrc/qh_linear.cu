@@ -75,11 +75,10 @@ __device__ __forceinline__ void activate32(float (&v)[32], int act) {
     }
 }
 
-// A warp's 32 rows x 32 columns in shared memory as TMA lays them: rows of 64 bytes
-// (16-bit types, 64-byte swizzle) or 128 (float32, 128-byte swizzle).  The address of
-// row r's 16-byte piece q.
-__device__ __forceinline__ uint32_t piece16(uint32_t base, int r, int q) { return base + 64 * r + 16 * (q ^ (r >> 1 & 3)); }
-__device__ __forceinline__ uint32_t piece32(uint32_t base, int r, int q) { return base + 128 * r + 16 * (q ^ (r & 7)); }
+// A warp's 32 rows x 64 bytes in shared memory as TMA lays them with the 64-byte
+// swizzle: 32 columns of a 16-bit type or 16 of float32.  The address of row r's
+// 16-byte piece q.
+__device__ __forceinline__ uint32_t piece(uint32_t base, int r, int q) { return base + 64 * r + 16 * (q ^ (r >> 1 & 3)); }
 
 __device__ __forceinline__ void sts128(uint32_t p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -90,33 +89,33 @@ __device__ __forceinline__ uint4 lds128(uint32_t p) {
     return v;
 }
 
-// v to or from row r of such a tile.
-__device__ __forceinline__ void put32(uint32_t base, int r, const float (&v)[32], int type) {
-    if (type == kSbF32) {
+// v, or 16 of its values from `from` on as float32, to or from row r of such a tile.
+__device__ __forceinline__ void put_half(uint32_t base, int r, const float (&v)[32], int type) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-            sts128(piece32(base, r, q), __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                   __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
-    } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            sts128(piece16(base, r, q), pack2(v[8 * q], v[8 * q + 1], type), pack2(v[8 * q + 2], v[8 * q + 3], type),
-                   pack2(v[8 * q + 4], v[8 * q + 5], type), pack2(v[8 * q + 6], v[8 * q + 7], type));
-    }
+    for (int q = 0; q < 4; ++q)
+        sts128(piece(base, r, q), pack2(v[8 * q], v[8 * q + 1], type), pack2(v[8 * q + 2], v[8 * q + 3], type),
+               pack2(v[8 * q + 4], v[8 * q + 5], type), pack2(v[8 * q + 6], v[8 * q + 7], type));
 }
-__device__ __forceinline__ void add32(uint32_t base, int r, float (&v)[32], int type) {
-    if (type == kSbF32) {
+template <int FROM>
+__device__ __forceinline__ void put_float(uint32_t base, int r, const float (&v)[32]) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const uint4 u = lds128(piece32(base, r, q));
-            v[4 * q] += __uint_as_float(u.x), v[4 * q + 1] += __uint_as_float(u.y);
-            v[4 * q + 2] += __uint_as_float(u.z), v[4 * q + 3] += __uint_as_float(u.w);
-        }
-        return;
-    }
+    for (int q = 0; q < 4; ++q)
+        sts128(piece(base, r, q), __float_as_uint(v[FROM + 4 * q]), __float_as_uint(v[FROM + 4 * q + 1]),
+               __float_as_uint(v[FROM + 4 * q + 2]), __float_as_uint(v[FROM + 4 * q + 3]));
+}
+template <int FROM>
+__device__ __forceinline__ void add_float(uint32_t base, int r, float (&v)[32]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        const uint4 u = lds128(piece16(base, r, q));
+        const uint4 u = lds128(piece(base, r, q));
+        v[FROM + 4 * q] += __uint_as_float(u.x), v[FROM + 4 * q + 1] += __uint_as_float(u.y);
+        v[FROM + 4 * q + 2] += __uint_as_float(u.z), v[FROM + 4 * q + 3] += __uint_as_float(u.w);
+    }
+}
+__device__ __forceinline__ void add_half(uint32_t base, int r, float (&v)[32], int type) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint4 u = lds128(piece(base, r, q));
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -177,7 +176,7 @@ __device__ __forceinline__ void tma_stores_read() {
 }
 __device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kPairThreads = 32 * (2 + kEpiWarps);
 constexpr int kJoinStages = 12;  // stages in the time that joining a shared tile takes
 
@@ -188,10 +187,10 @@ struct PairLayout {
     static constexpr int STAGE = A_BYTES + B_BYTES;
     // 5 stages of 256 columns: 66 us at 8192 x 2560 x 2560, 71 with 4, 81 with 3
     static constexpr int NS = BN == 256 ? 5 : 6;
-    static constexpr int OFF_E = NS * STAGE;             // an epilogue warp's tiles: residual, outputs
-    static constexpr int E_TILE = 32 * 128, E_BYTES = 2 * E_TILE;
+    static constexpr int OFF_E = NS * STAGE;             // an epilogue warp's tiles: residual, output
+    static constexpr int E_TILE = 32 * 64, E_BYTES = 2 * E_TILE;
     static constexpr int OFF_BAR = OFF_E + kEpiWarps * E_BYTES;
-    static constexpr int BAR_BYTES = 8 * (2 * NS + 5 + 2 * kEpiWarps) + 16;
+    static constexpr int BAR_BYTES = 8 * (2 * NS + 5 + kEpiWarps) + 16;
     static constexpr int SMEM = OFF_BAR + BAR_BYTES + 1024;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -254,8 +253,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint64_t* accf = empty + NS;
     uint64_t* acce = accf + 2;
     uint64_t* mdrain = acce + 2;
-    uint64_t* resf = mdrain + 1;   // an epilogue warp's residual tiles (two) have landed
-    uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(resf + 2 * kEpiWarps);
+    uint64_t* resf = mdrain + 1;   // an epilogue warp's residual tile has landed
+    uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(resf + kEpiWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sh + 1);
     int* err = reinterpret_cast<int*>(tmem_base_sh + 2);
 
@@ -274,7 +273,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             tc::mbar_init(&acce[i], 2 * kEpiWarps);
         }
         tc::mbar_init(mdrain, 1);
-        for (int i = 0; i < 2 * kEpiWarps; ++i) tc::mbar_init(&resf[i], 1);
+        for (int i = 0; i < kEpiWarps; ++i) tc::mbar_init(&resf[i], 1);
         *abort_flag = 0;
         *err = 0;
         tc::fence_mbar_init();
@@ -395,38 +394,36 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t acce_lead = tc::mapa_shared(acce, 0);
         unsigned char* tiles = smem + L::OFF_E + (warp - 2) * L::E_BYTES;
         const uint32_t res_tile = tc::smem_u32(tiles), out_tile = res_tile + L::E_TILE;
-        uint64_t* resb = &resf[2 * (warp - 2)];
+        uint64_t* resb = &resf[warp - 2];
         const float nan = __int_as_float(0x7fc00000);
         int buf = 0;
         uint32_t aphase = 0;
-        // The residual's 32 x 32 tiles in the order of their use, asked for by lane 0 as many
-        // ahead as fit (two of a 16-bit type), once the warp has read the slot's last.
+        // The residual's tiles in the order of their use, asked for by lane 0 one ahead, once
+        // the warp has read the one before.
         const bool by_tma = e.vec != 0;
-        const int slots = e.res_type == kSbF32 ? 1 : 2;
-        const uint32_t res_bytes = e.res_type == kSbF32 ? 4096 : 2048;
-        int ask_i = first, ask_c = 0, ask_slot = 0;
+        const int res_cols = e.res_type == kSbF32 ? 16 : 32;
+        int ask_i = first, ask_at = 0;
         const auto ask = [&]() {
             if (!by_tma || !e.res || lane != 0) return;
-            for (; ask_i < walk.full; ask_i += stride, ask_c = 0) {
+            for (; ask_i < walk.full; ask_i += stride, ask_at = 0) {
                 int mt, nt;
                 tile_of(ask_i, n_mt, n_nt, mt, nt);
-                const int m = mt * 256 + (int)rank * 128 + sub * 32, n = nt * BN + group * COLS + 32 * ask_c;
-                if (m < e.M && n < e.N && ask_c < NC) {
-                    tc::mbar_arrive_expect_tx(&resb[ask_slot], res_bytes);
-                    tc::tma_load_2d(tiles + 2048 * ask_slot, &tr, &resb[ask_slot], n, m);
-                    ++ask_c;
-                    if (++ask_slot == slots) ask_slot = 0;
+                const int m = mt * 256 + (int)rank * 128 + sub * 32, n = nt * BN + group * COLS + ask_at;
+                if (m < e.M && n < e.N && ask_at < COLS) {
+                    tc::mbar_arrive_expect_tx(resb, L::E_TILE);
+                    tc::tma_load_2d(tiles, &tr, resb, n, m);
+                    ask_at += res_cols;
                     return;
                 }
             }
         };
-        // (an item's tiles into L2 while the one before is worked on: from DRAM, two tiles
-        // ahead do not cover the latency)
+        // (an item's tiles into L2 while the one before is worked on: from DRAM, one tile ahead
+        // does not cover the latency)
         const auto ask_l2 = [&](int i) {
-            if (!by_tma || !e.res || lane >= NC || i >= walk.full) return;
+            if (!by_tma || !e.res || lane * res_cols >= COLS || i >= walk.full) return;
             int mt, nt;
             tile_of(i, n_mt, n_nt, mt, nt);
-            const int m = mt * 256 + (int)rank * 128 + sub * 32, n = nt * BN + group * COLS + 32 * lane;
+            const int m = mt * 256 + (int)rank * 128 + sub * 32, n = nt * BN + group * COLS + res_cols * lane;
             if (m < e.M && n < e.N)
                 asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(
                                  reinterpret_cast<uint64_t>(&tr)),
@@ -434,8 +431,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                              : "memory");
         };
         ask_l2(first);
-        for (int k = 0; k < slots; ++k) ask();
-        int slot = 0;
+        ask();
         uint32_t rphase = 0;
         for (int i = first; i < walk.items; i += stride) {
             int t, mt, nt, k0, k1;
@@ -465,73 +461,102 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (c + 1 < NC) column.load(e, n + 32 + lane);
                 if (!by_tma) {
                     // any alignment: through shared memory to rows of 32 lanes
-                    scale32(e, m0 + lane, col, res_tile + 4608, v);
-                    float* tr = reinterpret_cast<float*>(tiles);
+                    scale32(e, m0 + lane, col, res_tile, v);
+                    float* tr = reinterpret_cast<float*>(tiles);  // [row][column ^ row]
                     const int64_t at = m0 * e.N + n + lane;
                     const int live = n + lane < e.N ? rows : 0;
                     if (e.pre) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) tr[lane * 33 + j] = in_half(v[j]);
+                        for (int j = 0; j < 32; ++j) tr[lane * 32 + (j ^ lane)] = in_half(v[j]);
                         __syncwarp();
 #pragma unroll 8
-                        for (int k = 0; k < live; ++k) e.pre[at + k * e.N] = __float2half_rn(tr[k * 33 + lane]);
+                        for (int k = 0; k < live; ++k) e.pre[at + k * e.N] = __float2half_rn(tr[k * 32 + (lane ^ k)]);
                         __syncwarp();
                     }
                     activate32(v, e.act);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) tr[lane * 33 + j] = v[j];
+                    for (int j = 0; j < 32; ++j) tr[lane * 32 + (j ^ lane)] = v[j];
                     __syncwarp();
                     if (e.res) {
                         const int64_t from = m0 * e.ldr + n + lane;
 #pragma unroll 8
-                        for (int k = 0; k < live; ++k) tr[k * 33 + lane] += sb_elem(e.res, from + k * e.ldr, e.res_type);
+                        for (int k = 0; k < live; ++k)
+                            tr[k * 32 + (lane ^ k)] += sb_elem(e.res, from + k * e.ldr, e.res_type);
                     }
                     if (e.y_type == kSbF32) {
 #pragma unroll 8
-                        for (int k = 0; k < live; ++k) static_cast<float*>(e.y)[at + k * e.N] = tr[k * 33 + lane];
+                        for (int k = 0; k < live; ++k) static_cast<float*>(e.y)[at + k * e.N] = tr[k * 32 + (lane ^ k)];
                     } else {
 #pragma unroll 8
-                        for (int k = 0; k < live; ++k) put(e.y, at + k * e.N, e.y_type, tr[k * 33 + lane]);
+                        for (int k = 0; k < live; ++k) put(e.y, at + k * e.N, e.y_type, tr[k * 32 + (lane ^ k)]);
                     }
                     __syncwarp();
                     return;
                 }
-                if (lane == 0) tma_stores_read<0>();  // the output tile is free
-                __syncwarp();
+                // The warp's tile at `tile`, written before, to columns `at` on; and the wait
+                // until the tiles sent have been read.
+                const auto send = [&](const CUtensorMap* map, uint32_t tile, int64_t at) {
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tma_store(map, tile, (int)at, (int)m0);
+                };
+                const auto sent = [&]() {
+                    if (lane == 0) tma_stores_read<0>();
+                    __syncwarp();
+                };
+                sent();
                 scale32(e, m0 + lane, col, out_tile, v);
-                uint32_t y_tile = out_tile;
                 if (e.pre) {
                     float z[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) z[j] = in_half(v[j]);
-                    put32(out_tile, lane, z, kSbF16);
-                    tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) tma_store(&tp, out_tile, (int)n, (int)m0);
-                    if (e.y_type != kSbF32) y_tile += 2048;  // (both fit)
+                    put_half(out_tile, lane, z, kSbF16);
+                    send(&tp, out_tile, n);
                 }
                 activate32(v, e.act);
                 if (e.res) {
                     // (a failed wait: the copy is waited for all the same, and the outputs say so)
-                    const bool ok = tc::mbar_wait_cta(&resb[slot], rphase, abort_flag, err, tc::kErrTimeoutFull);
-                    if (!ok) tc::mbar_drain(&resb[slot], rphase, err);
-                    add32(res_tile + 2048 * slot, lane, v, e.res_type);
+                    const auto landed = [&]() {
+                        const bool ok = tc::mbar_wait_cta(resb, rphase, abort_flag, err, tc::kErrTimeoutFull);
+                        if (!ok) tc::mbar_drain(resb, rphase, err);
+                        rphase ^= 1;
+                        return ok;
+                    };
+                    bool ok = landed();
+                    if (e.res_type == kSbF32) {
+                        add_float<0>(res_tile, lane, v);
+                        __syncwarp();
+                        ask();
+                        if (n + 16 < e.N) {
+                            ok &= landed();
+                            add_float<16>(res_tile, lane, v);
+                            __syncwarp();
+                            ask();
+                        }
+                    } else {
+                        add_half(res_tile, lane, v, e.res_type);
+                        __syncwarp();
+                        ask();
+                    }
                     if (!ok) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = nan;
                     }
-                    if (++slot == slots) { slot = 0; rphase ^= 1; }
-                    __syncwarp();
-                    ask();
                 }
-                if (e.pre && e.y_type == kSbF32) {
-                    if (lane == 0) tma_stores_read<0>();
-                    __syncwarp();
+                if (e.pre) sent();
+                if (e.y_type == kSbF32) {
+                    put_float<0>(out_tile, lane, v);
+                    send(&ty, out_tile, n);
+                    if (n + 16 < e.N) {
+                        // (without a residual its tile is free)
+                        if (e.res) sent();
+                        put_float<16>(e.res ? out_tile : res_tile, lane, v);
+                        send(&ty, e.res ? out_tile : res_tile, n + 16);
+                    }
+                } else {
+                    put_half(out_tile, lane, v, e.y_type);
+                    send(&ty, out_tile, n);
                 }
-                put32(y_tile, lane, v, e.y_type);
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) tma_store(&ty, y_tile, (int)n, (int)m0);
             };
             // The accumulator has been read.  (Nothing in memory is handed over: a release would
             // wait for the warp's stores; 256 rows' dW of 2560 x 10240 took 36 us, 27 so.)
@@ -544,11 +569,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
                 tc::tc_fence_after();
                 const uint32_t d = d0 + buf * BN;
-                uint32_t r[32];
-                tc::tmem_ld32(d, r);
-                tmem_wait_ld_of(r);
 #pragma unroll 1
                 for (int c = 0; c < NC; ++c) {
+                    uint32_t r[32];
+                    tc::tmem_ld32(d + 32 * c, r);
+                    tmem_wait_ld_of(r);
                     float v[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
@@ -556,11 +581,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = nan;
                     }
-                    // the next columns' sums on their way while these are finished
-                    if (c + 1 < NC) tc::tmem_ld32(d + 32 * (c + 1), r);
-                    else release(buf);
+                    if (c + 1 == NC) release(buf);
                     out(c, v);
-                    if (c + 1 < NC) tmem_wait_ld_of(r);
                 }
                 if (++buf == 2) { buf = 0; aphase ^= 1; }
             } else {

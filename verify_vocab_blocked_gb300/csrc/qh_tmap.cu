@@ -60,8 +60,7 @@ bool tmap_rows_sw128(CUtensorMap* map, const void* base, int elem_bytes, uint64_
 bool tmap_tiles(CUtensorMap* map, const void* base, int elem_bytes, uint64_t cols, uint64_t rows,
                 uint64_t row_bytes) {
     return encode_2d(map, elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32, base,
-                     cols, rows, row_bytes, 32, 32,
-                     elem_bytes == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                     cols, rows, row_bytes, 64 / elem_bytes, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 bool tmap_packed_rows(CUtensorMap* map, const uint32_t* wq, uint64_t words_per_row, uint64_t rows,

@@ -17,8 +17,7 @@ bool tmap_rows_f16_sw128(CUtensorMap* map, const void* base, uint64_t cols, uint
 bool tmap_rows_sw128(CUtensorMap* map, const void* base, int elem_bytes, uint64_t cols, uint64_t rows,
                      uint64_t row_bytes, uint32_t box_rows);
 
-// Row-major matrix of 2- or 4-byte elements, box of 32 x 32 whose rows of 64 or 128 bytes
-// have the swizzle of that span.
+// Row-major matrix of 2- or 4-byte elements, box of 64 bytes x 32 rows, 64-byte swizzle.
 bool tmap_tiles(CUtensorMap* map, const void* base, int elem_bytes, uint64_t cols, uint64_t rows,
                 uint64_t row_bytes);
 
