@@ -178,7 +178,7 @@ __device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.
 
 constexpr int kEpiWarps = 16;
 constexpr int kPairThreads = 32 * (2 + kEpiWarps);
-constexpr int kJoinStages = 12;  // stages in the time that joining a shared tile takes
+constexpr int kJoinStages = 16;  // stages in the time that joining the shared tiles takes
 
 template <int BN, bool AMN, bool BMN>
 struct PairLayout {
@@ -232,11 +232,24 @@ __device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[32]) {
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait_ld_of8(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+
 // SUMS: for float32 outputs of 16-bit operands.  The tensor cores' accumulation
 // truncates, up to a step of the running sum at each MMA; kSumSteps stages are summed
 // there, and these sums in registers, rounded to nearest.  Error over the result's
 // norm at K = 1541: 2.1e-6 in one sum, 5.4e-7 so (4 stages 1.4e-7, but then the epilogue
-// sets the pace: 2048 x 2560 x 10240 in 196 us, 111 with 16), 3 to 7e-7 an fp32 product.
+// sets the pace), 3 to 8e-7 an fp32 product.
 template <int BN, bool AMN, bool BMN, bool SUMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -591,14 +604,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
                     tc::tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        uint32_t r[32];
-                        tc::tmem_ld32(d0 + buf * BN + 32 * c, r);
-                        tmem_wait_ld_of(r);
+                    for (int c = 0; c < 4 * NC; ++c) {
+                        uint32_t r[8];
+                        tmem_ld8(d0 + buf * BN + 8 * c, r);
+                        tmem_wait_ld_of8(r);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
+                        for (int j = 0; j < 8; ++j) {
                             const float x = ok ? __uint_as_float(r[j]) : nan;
-                            v[c][j] = kk == k0 ? x : v[c][j] + x;
+                            float& to = v[c / 4][8 * (c % 4) + j];
+                            to = kk == k0 ? x : to + x;
                         }
                     }
                     release(buf);
@@ -620,7 +634,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 }
 
 // The tiles whose reduction was shared: their parts' sums added in order, and the
-// epilogue.  BN / 8 lanes a row of a tile, 8 columns each; blockIdx.y: tile.
+// epilogue.  BN / 8 lanes a row of a tile, 8 columns each -- consecutive ones where the
+// rows of the outputs are aligned, else BN / 8 apart; blockIdx.y: tile.
 constexpr int kJoinThreads = 256;
 template <int BN>
 __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const __grid_constant__ Epi e, const Walk walk) {
@@ -630,25 +645,37 @@ __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const __grid_
     const int n_mt = (int)((e.M + 255) / 256), n_nt = (int)((e.N + BN - 1) / BN);
     int mt, nt;
     tile_of(walk.full + blockIdx.y, n_mt, n_nt, mt, nt);
-    const int row = blockIdx.x * kRows + threadIdx.x / kLanes, c = 8 * (threadIdx.x % kLanes);
-    const int64_t m = (int64_t)mt * 256 + row, n = (int64_t)nt * BN + c;
-    if (m >= e.M || n >= e.N) return;
-    const float* p = walk.part + (int64_t)blockIdx.y * walk.split * 256 * BN + row * BN + c;
-    const bool vec = e.vec && n + 8 <= e.N;
+    const int row = blockIdx.x * kRows + threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+    const int64_t m = (int64_t)mt * 256 + row, n0 = (int64_t)nt * BN;
+    if (m >= e.M) return;
+    const float* p = walk.part + (int64_t)blockIdx.y * walk.split * 256 * BN + row * BN;
+    if (!e.vec || n0 + BN > e.N) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = p[lane + kLanes * j];
+#pragma unroll 2
+        for (int s = 1; s < walk.split; ++s) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += p[(int64_t)s * 256 * BN + lane + kLanes * j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t n = n0 + lane + kLanes * j;
+            if (n < e.N)
+                finish(e, m, n, v[j], e.unbias * (e.b_scale ? e.b_scale[n] : 1.f),
+                       e.bias ? sb_elem(e.bias, n, e.bias_type) : 0.f);
+        }
+        return;
+    }
+    const int64_t n = n0 + 8 * lane;
     float v[8], r[8], u[8];
-    load8_wide(p, v);
-    if (vec && e.res) load8_as(e.res, m * e.ldr + n, e.res_type, r);
+    load8_wide(p + 8 * lane, v);
+    if (e.res) load8_as(e.res, m * e.ldr + n, e.res_type, r);
 #pragma unroll 4
     for (int s = 1; s < walk.split; ++s) {
-        load8_wide(p + (int64_t)s * 256 * BN, u);
+        load8_wide(p + (int64_t)s * 256 * BN + 8 * lane, u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += u[j];
-    }
-    if (!vec) {
-        for (int j = 0; j < 8 && n + j < e.N; ++j)
-            finish(e, m, n + j, v[j], e.unbias * (e.b_scale ? e.b_scale[n + j] : 1.f),
-                   e.bias ? sb_elem(e.bias, n + j, e.bias_type) : 0.f);
-        return;
     }
     const float as = e.unbias * (e.a_scale ? e.a_scale[m] : 1.f);
 #pragma unroll
@@ -699,16 +726,17 @@ cudaError_t go_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
                                          idesc_of(a.type, 256, BN, AMN, BMN), (int)(a.type == kE4m3), a.stall))
         return err;
     if (full == tiles) return cudaSuccess;
+    const Epi parts = epi_of(a, in_sums(a) ? 4 * std::min((n_k + p.split - 1) / p.split, kSumSteps) : 0);
     return launch_after(linear_join_kernel<BN>, dim3(256 * BN / 8 / kJoinThreads, (unsigned)(tiles - full)),
-                        dim3(kJoinThreads), st, e, walk);
+                        dim3(kJoinThreads), st, parts, walk);
 }
 
 template <bool AMN, bool BMN>
 cudaError_t pick_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
     if constexpr (!AMN && !BMN) {
-        if (p.tile == 128) return go_pair<128, AMN, BMN, true>(a, p, st);
+        if (p.sums) return p.tile == 128 ? go_pair<128, AMN, BMN, true>(a, p, st) : go_pair<256, AMN, BMN, true>(a, p, st);
     }
-    return go_pair<256, AMN, BMN, false>(a, p, st);
+    return p.tile == 128 ? go_pair<128, AMN, BMN, false>(a, p, st) : go_pair<256, AMN, BMN, false>(a, p, st);
 }
 
 // --------------------------------------------------------------- pad rows
@@ -779,18 +807,27 @@ LinPlan plan_linear(const LinArgs& a, int sms) {
         p.split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, n_k), fit / tiles));
         return p;
     }
-    // (256 columns of sums in registers would not fit)
-    p.tile = in_sums(a) && n_k > kSumSteps ? 128 : 256;
+    // Pairs: tiles of 256 or 128 columns, whichever takes fewer stages (a stage of 128 costs
+    // 0.85 of one of 256; sums of 256 columns spill registers once a tile).  The tiles past
+    // the last full round are shared by the idle pairs, in parts of 4 stages at least, where
+    // that takes more stages off the round than the join costs.
     p.pairs = std::max(1, sms / 2);
-    const int64_t tiles = (a.M + 255) / 256 * ((a.N + p.tile - 1) / p.tile);
-    const int tail = (int)(tiles % p.pairs);
-    // The tiles past the last full round shared by the idle pairs, in parts of 4 stages
-    // at least, where that takes more stages off the round than the join costs.
-    if (tail > 0) {
-        const int split = (int)std::min<int64_t>(p.pairs / tail, n_k / 4);
-        if (split > 1 && n_k - (n_k + split - 1) / split >= kJoinStages) p.split = split;
+    p.sums = in_sums(a) && n_k > kSumSteps;
+    float best = 0.f;
+    for (const int tile : {256, 128}) {
+        const int64_t tiles = (a.M + 255) / 256 * ((a.N + tile - 1) / tile);
+        const int tail = (int)(tiles % p.pairs);
+        int split = tail > 0 ? (int)std::min<int64_t>(p.pairs / tail, n_k / 4) : 1;
+        if (split > 1 && n_k - (n_k + split - 1) / split < kJoinStages) split = 1;
+        const int64_t last = tail == 0 ? 0 : split > 1 ? (n_k + split - 1) / split + kJoinStages : n_k;
+        const float cost = (float)(tiles / p.pairs * n_k + last) * (tile == 128 ? 0.85f : p.sums ? 1.2f : 1.f);
+        if (tile == 256 || cost < best) {
+            best = cost;
+            p.tile = tile;
+            p.split = std::max(1, split);
+            p.part_bytes = p.split > 1 ? sizeof(float) * (size_t)tail * p.split * 256 * tile : 0;
+        }
     }
-    if (p.split > 1) p.part_bytes = sizeof(float) * (size_t)tail * p.split * 256 * p.tile;
     return p;
 }
 
