@@ -24,9 +24,11 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint
 }
 
 
-constexpr int kFewThreads = 6 * 32;
-// CTAs to an SM, and the columns of their accumulators at most: the SM's 512 hold them
+// Epilogue warps: four, or two for a quadrant of the tensor memory's lanes where there are
+// columns for both.  CTAs to an SM, and the columns of their accumulators at most: the SM's 512 hold them
 // all, so that no CTA of a cluster waits for tensor memory that another cluster holds.
+constexpr int few_warps(int tile) { return tile <= 32 ? 4 : 8; }
+constexpr int few_threads(int tile) { return 32 * (2 + few_warps(tile)); }
 constexpr int few_per_sm(int tile) { return tile <= 16 ? 3 : 2; }
 constexpr int few_tmem(int tile) { return tile <= 16 ? 128 : 256; }
 
@@ -37,9 +39,12 @@ struct FewLayout {
     static constexpr int STAGE = W_BYTES + X_BYTES;
     static constexpr int NS = T == 32 ? 5 : T == 128 ? 3 : 4;
     static constexpr int OFF_BAR = NS * STAGE;
-    static constexpr int BAR_BYTES = 8 * (2 * NS + 2) + 16;
+    static constexpr int BAR_BYTES = 8 * (2 * NS + 3) + 16;
     static constexpr int SMEM = OFF_BAR + BAR_BYTES + 1024;
-    static_assert(T * 128 * 4 <= OFF_BAR, "the partial tile lies in the ring");
+    // The tokens in groups of G, a group's sums 16 (or 8) bytes a row; the share of a CTA of
+    // `split` is every split-th group: split * ceil(NG / split) <= NG + 7 blocks of them.
+    static constexpr int G = T <= 16 ? 2 : 4, NG = T / G;
+    static_assert((NG + 7) * 128 * G * 4 <= OFF_BAR, "the parts of the share lie in the ring");
     static_assert(few_per_sm(T) * (SMEM + 1024) <= 228 * 1024, "CTAs to an SM");
     static_assert((few_per_sm(T) + 1) * (SMEM + 1024) > 228 * 1024 && few_per_sm(T) * few_tmem(T) <= 512,
                   "tensor memory for all that fit");
@@ -49,23 +54,6 @@ __device__ __forceinline__ void prefetch_l2(const CUtensorMap* map, int x, int y
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
                  "r"(x), "r"(y)
                  : "memory");
-}
-__device__ __forceinline__ int ld_cluster(uint32_t addr) {
-    int v;
-    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ float4 ld_cluster_apart(uint32_t addr) {  // 32 floats apart
-    return make_float4(__int_as_float(ld_cluster(addr)), __int_as_float(ld_cluster(addr + 128)),
-                       __int_as_float(ld_cluster(addr + 256)), __int_as_float(ld_cluster(addr + 384)));
 }
 __device__ __forceinline__ uint32_t at_rank(uint32_t addr, int rank) {
     uint32_t r;
@@ -93,54 +81,71 @@ __device__ __forceinline__ void add4(float (&v)[4], uint4 u, int type) {
     }
 }
 
-// The outputs of a CTA's share of the tokens (every split-th; split <= S CTAs share the
-// reduction), a warp a token: a lane adds four columns' partial sums of all ranks, in
-// order -- consecutive ones where the outputs' rows are aligned, else 32 apart.  Several
-// tokens a step, whose loads are in flight together.  part: the partial tile,
-// [token][128] in every rank's shared memory.
-template <int S>
-__device__ __forceinline__ void few_outputs(const Epi& e, uint32_t part, int rank, int split, int warp, int64_t m0, int rows,
-                                            int64_t n0, bool bad) {
-    constexpr int U = S > 4 ? 2 : 4;
+// Stores into a CTA's shared memory, counted in bytes on its barrier.
+__device__ __forceinline__ void st_async4(uint32_t to, uint32_t bar, const float* v) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+                 "r"(__float_as_uint(v[3])), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void st_async2(uint32_t to, uint32_t bar, const float* v) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(to),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(bar)
+                 : "memory");
+}
+// Where a group's row r lies in its block: so that both 32 consecutive rows and every
+// fourth one are read without bank conflicts.
+__device__ __forceinline__ int slot(int r) { return r ^ (r >> 2 & 3) ^ (r >> 4 & 3) << 2; }
+
+// The outputs of a CTA's share of the tokens (groups rank, rank + split, ...), a warp a
+// group: a lane adds four columns' sums of all ranks, in order -- consecutive ones where
+// the outputs' rows are aligned, else 32 apart.  parts: the share's blocks [rank][group],
+// which `landed` waits for.
+template <int T, typename Landed>
+__device__ __forceinline__ void few_outputs(const Epi& e, uint32_t parts, int rank, int split, int warp, int64_t m0,
+                                            int rows, int64_t n0, const float (&bs)[4], const float (&bias)[4],
+                                            const Landed& landed) {
+    using L = FewLayout<T>;
+    constexpr int G = L::G, EW = few_warps(T);
     const int lane = threadIdx.x & 31;
     const bool vec = e.vec && n0 + 128 <= e.N;
-    const int apart = vec ? 1 : 32;
     const int64_t n = n0 + (vec ? 4 * lane : lane);
-    if (n >= e.N) return;
-    uint32_t base[S];
+    const int share = (L::NG + split - 1) / split;
+    bool bad = false;
+    for (int i = warp; (rank + split * i) * G < rows; i += EW) {
+        const int t0 = (rank + split * i) * G;
+        uint4 r[G];
+        float as[G];
 #pragma unroll
-    for (int s = 0; s < S; ++s) base[s] = at_rank(part + (vec ? 16 : 4) * lane, s < split ? s : 0);
-    float bs[4], bias[4];
+        for (int u = 0; u < G; ++u) {
+            const bool in = t0 + u < rows && n < e.N;
+            as[u] = e.a_scale && in ? e.a_scale[m0 + t0 + u] : 1.f;
+            r[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (vec && e.res && in) r[u] = load4(e.res, (m0 + t0 + u) * e.ldr + n, e.res_type);
+        }
+        if (i == warp) bad = !landed();
+        float v[G][4];
+#pragma unroll 2
+        for (int s = 0; s < split; ++s) {
+            const uint32_t block = parts + (s * share + i) * (128 * G * 4);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t at = n + j * apart;
-        const bool in = at < e.N;
-        bs[j] = e.unbias * (e.b_scale && in ? e.b_scale[at] : 1.f);
-        bias[j] = e.bias && in ? sb_elem(e.bias, at, e.bias_type) : 0.f;
-    }
-    for (int t0 = rank + split * warp; t0 < rows; t0 += 4 * split * U) {
-        float v[U][4];
-        uint4 r[U];
-        float as[U];
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at = block + slot(vec ? 4 * lane + j : lane + 32 * j) * (4 * G);
+                float x[G];
+                if constexpr (G == 4)
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                                 : "r"(at));
+                else
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "r"(at));
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = t0 + 4 * split * u;
-            if (t >= rows) continue;
-            if (vec && e.res) r[u] = load4(e.res, (m0 + t) * e.ldr + n, e.res_type);
-            as[u] = e.a_scale ? e.a_scale[m0 + t] : 1.f;
-            float4 x[S];
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-                if (s < split) x[s] = vec ? ld_cluster4(base[s] + t * 512) : ld_cluster_apart(base[s] + t * 512);
-            v[u][0] = x[0].x, v[u][1] = x[0].y, v[u][2] = x[0].z, v[u][3] = x[0].w;
-#pragma unroll
-            for (int s = 1; s < S; ++s)
-                if (s < split) v[u][0] += x[s].x, v[u][1] += x[s].y, v[u][2] += x[s].z, v[u][3] += x[s].w;
+                for (int u = 0; u < G; ++u) v[u][j] = s == 0 ? x[u] : v[u][j] + x[u];
+            }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = t0 + 4 * split * u;
-            if (t >= rows) continue;
+        for (int u = 0; u < G; ++u) {
+            const int t = t0 + u;
+            if (t >= rows || n >= e.N) continue;
             const int64_t m = m0 + t, at = m * e.N + n;
             if (bad) v[u][0] = v[u][1] = v[u][2] = v[u][3] = __int_as_float(0x7fc00000);
             if (!vec) {
@@ -177,19 +182,20 @@ __device__ __forceinline__ void few_outputs(const Epi& e, uint32_t part, int ran
 // the stages of an accumulator (a float32 output's reduction takes several, for the
 // pairs' reason, added in registers at the end); `cols`: their columns.
 template <int T, bool WMN>
-__global__ void __launch_bounds__(kFewThreads)
+__global__ void __launch_bounds__(few_threads(T), few_per_sm(T))
     linear_few_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx,
                       const __grid_constant__ Epi e, int n_k, int step_k, int split, int sums, int cols,
                       uint32_t idesc, int f8, int stall) {
     using L = FewLayout<T>;
-    constexpr int NS = L::NS;
+    constexpr int NS = L::NS, EW = few_warps(T);
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
     uint64_t* empty = full + NS;
     uint64_t* accf = empty + NS;
     uint64_t* mdrain = accf + 1;
-    uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(mdrain + 1);
+    uint64_t* landed = mdrain + 1;  // the share's parts have
+    uint32_t* tmem_base_sh = reinterpret_cast<uint32_t*>(landed + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base_sh + 1);
     int* err = reinterpret_cast<int*>(tmem_base_sh + 2);
 
@@ -197,6 +203,8 @@ __global__ void __launch_bounds__(kFewThreads)
     const int rank = (int)blockIdx.x % split;  // (= the rank in the cluster of `split`)
     const int n0 = (int)blockIdx.x / split * 128, m0 = (int)blockIdx.y * T;
     const int k0 = (int)((int64_t)n_k * rank / split), k1 = (int)((int64_t)n_k * (rank + 1) / split);
+    const int rows = (int)min((int64_t)T, e.M - m0);
+    const int groups = (rows + L::G - 1) / L::G, share = (L::NG + split - 1) / split;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -205,9 +213,12 @@ __global__ void __launch_bounds__(kFewThreads)
         }
         tc::mbar_init(accf, 1);
         tc::mbar_init(mdrain, 1);
+        tc::mbar_init(landed, 1);
         *abort_flag = 0;
         *err = 0;
         tc::fence_mbar_init();
+        // (groups of this rank x ranks x 128 rows; none: the arrival alone)
+        tc::mbar_arrive_expect_tx(landed, (uint32_t)((groups - rank + split - 1) / split * split * (128 * L::G * 4)));
         tc::prefetch_tmap(&tw);
         tc::prefetch_tmap(&tx);
     }
@@ -234,6 +245,7 @@ __global__ void __launch_bounds__(kFewThreads)
     tc::grid_dep_trigger();
 
     bool ok = true;
+    float bs[4], bias[4];  // the scales and biases of a lane's columns
     if (warp == 0) {
         int stage = 0;
         uint32_t phase = 0, fills = 0;
@@ -290,18 +302,30 @@ __global__ void __launch_bounds__(kFewThreads)
             tc::mbar_drain(mdrain, 0, err);
         }
     } else {
-        // Lane: a weight row; the accumulator's columns: tokens.  All MMAs, and with
-        // them all copies, are done when the accumulator is: the ring is free.
-        const int sub = warp & 3, row = sub * 32 + lane;
+        // (their values are on their way while the accumulator fills)
+        const bool vec = e.vec && n0 + 128 <= e.N;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t at = n0 + (vec ? 4 * lane + j : lane + 32 * j);
+            bs[j] = e.unbias * (e.b_scale && at < e.N ? e.b_scale[at] : 1.f);
+            bias[j] = e.bias && at < e.N ? sb_elem(e.bias, at, e.bias_type) : 0.f;
+        }
         ok = tc::mbar_wait_cta(accf, 0, abort_flag, err, tc::kErrTimeoutAccFull);
         tc::tc_fence_after();
-        float* part = reinterpret_cast<float*>(smem);
-        // (after a failed wait copies may be in flight into the ring: the flag tells the cluster)
+    }
+    // Every CTA's MMAs, and with them its copies, are done: the rings are free.
+    __syncwarp();
+    if (split > 1) tc::cluster_sync();
+    if (warp >= 2) {
+        // Lane: a weight row; the accumulator's columns: tokens, whose sums go to the CTA
+        // that finishes them.
+        const int sub = warp & 3, row = sub * 32 + lane;
         const int accs = (k1 - k0 + sums - 1) / sums;
         const uint32_t d = tmem_base + ((uint32_t)(sub * 32) << 16);
+        const uint32_t parts = tc::smem_u32(smem) + rank * share * (128 * L::G * 4) + slot(row) * (4 * L::G);
+        constexpr int W = T < 32 ? T : 32;  // columns of the chunk; T = 16: two accumulators a load
 #pragma unroll 1
-        for (int c = 0; c < (T + 31) / 32; ++c) {
-            constexpr int W = T < 32 ? T : 32;  // columns of the chunk; T = 16: two accumulators a load
+        for (int c = (warp - 2) / 4; W * c < rows; c += EW / 4) {
             float v[W];
 #pragma unroll 1
             for (int a = 0; a < accs; a += 32 / W) {
@@ -315,30 +339,38 @@ __global__ void __launch_bounds__(kFewThreads)
                     for (int j = 0; j < W; ++j) v[j] += __uint_as_float(r[32 - W + j]);
                 }
             }
-            if (ok) {
+            if (!ok) {
 #pragma unroll
-                for (int j = 0; j < W; ++j) part[(32 * c + j) * 128 + row] = v[j];
+                for (int j = 0; j < W; ++j) v[j] = __int_as_float(0x7fc00000);
+            }
+            int g = c * (W / L::G), owner = g % split, i = g / split;
+#pragma unroll
+            for (int q = 0; q < W / L::G; ++q) {
+                if (g + q < groups) {
+                    const uint32_t to = at_rank(parts + i * (128 * L::G * 4), owner);
+                    const uint32_t bar = at_rank(tc::smem_u32(landed), owner);
+                    if constexpr (L::G == 4) st_async4(to, bar, v + 4 * q);
+                    else st_async2(to, bar, v + 2 * q);
+                }
+                if (++owner == split) owner = 0, ++i;
             }
         }
-        if (!ok && lane == 0) *abort_flag = tc::kErrTimeoutAccFull;
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (split > 1) tc::cluster_sync();
     if (warp == 1) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem_base, cols);
     }
     if (warp >= 2) {
-        const uint32_t part = tc::smem_u32(smem), flag = tc::smem_u32(const_cast<int*>(abort_flag));
-        bool bad = false;
-        for (int s = 0; s < split; ++s) bad |= ld_cluster(at_rank(flag, s)) != 0;
-        const int rows = (int)min((int64_t)T, e.M - m0);
-        if (split <= 2) few_outputs<2>(e, part, rank, split, warp - 2, m0, rows, n0, bad);
-        else if (split <= 4) few_outputs<4>(e, part, rank, split, warp - 2, m0, rows, n0, bad);
-        else few_outputs<8>(e, part, rank, split, warp - 2, m0, rows, n0, bad);
+        // (past the cluster's barrier every CTA sends without a wait: the parts do land, and
+        // none is under way to a CTA that has left)
+        few_outputs<T>(e, tc::smem_u32(smem), rank, split, warp - 2, m0, rows, n0, bs, bias, [&]() {
+            const bool all = tc::mbar_wait_cluster(landed, 0, abort_flag, err, tc::kErrTimeoutFull);
+            if (!all) tc::mbar_drain(landed, 0, err);
+            return all && ok;
+        });
     }
-    if (split > 1) tc::cluster_sync();  // no CTA leaves while its partial tile is read
 }
 
 template <int T, bool WMN>
@@ -357,7 +389,7 @@ cudaError_t go_few(const LinArgs& a, int split, cudaStream_t st) {
     int cols = 32;
     while (cols < accs * T) cols *= 2;
     const dim3 grid((unsigned)((a.N + 127) / 128 * split), (unsigned)((a.M + T - 1) / T));
-    return launch_cluster(linear_few_kernel<T, WMN>, grid, kFewThreads, L::SMEM, split, st, tw, tx,
+    return launch_cluster(linear_few_kernel<T, WMN>, grid, few_threads(T), L::SMEM, split, st, tw, tx,
                           epi_of(a, in_sums(a) ? 4 * sums : 0), n_k, step, split, sums, cols, idesc_of(a.type, 128, T, WMN, false),
                           (int)(a.type == kE4m3), a.stall);
 }
