@@ -93,9 +93,31 @@ __device__ __forceinline__ void st_async2(uint32_t to, uint32_t bar, const float
                  "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(bar)
                  : "memory");
 }
+// (load and wait in one: nothing reads the registers before)
+__device__ __forceinline__ void tmem_ld_group(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld_group(uint32_t addr, uint32_t (&r)[2]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1])
+                 : "r"(addr)
+                 : "memory");
+}
 // Where a group's row r lies in its block: so that both 32 consecutive rows and every
 // fourth one are read without bank conflicts.
 __device__ __forceinline__ int slot(int r) { return r ^ (r >> 2 & 3) ^ (r >> 4 & 3) << 2; }
+
+template <int ACT, int G>
+__device__ __forceinline__ void activate_all(float (&v)[G][4]) {
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[u][j] = activate(v[u][j], ACT);
+    }
+}
 
 // The outputs of a CTA's share of the tokens (groups rank, rank + split, ...), a warp a
 // group: a lane adds four columns' sums of all ranks, in order -- consecutive ones where
@@ -125,7 +147,7 @@ __device__ __forceinline__ void few_outputs(const Epi& e, uint32_t parts, int ra
         }
         if (i == warp) bad = !landed();
         float v[G][4];
-#pragma unroll 2
+#pragma unroll 4
         for (int s = 0; s < split; ++s) {
             const uint32_t block = parts + (s * share + i) * (128 * G * 4);
 #pragma unroll
@@ -142,36 +164,58 @@ __device__ __forceinline__ void few_outputs(const Epi& e, uint32_t parts, int ra
                 for (int u = 0; u < G; ++u) v[u][j] = s == 0 ? x[u] : v[u][j] + x[u];
             }
         }
+        if (bad) {
 #pragma unroll
-        for (int u = 0; u < G; ++u) {
-            const int t = t0 + u;
-            if (t >= rows || n >= e.N) continue;
-            const int64_t m = m0 + t, at = m * e.N + n;
-            if (bad) v[u][0] = v[u][1] = v[u][2] = v[u][3] = __int_as_float(0x7fc00000);
-            if (!vec) {
+            for (int u = 0; u < G; ++u) v[u][0] = v[u][1] = v[u][2] = v[u][3] = __int_as_float(0x7fc00000);
+        }
+        const int live = n < e.N ? min(G, rows - t0) : 0;
+        if (!vec) {
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (n + 32 * j < e.N) finish(e, m, n + 32 * j, v[u][j], bs[j], bias[j]);
-                continue;
+                    if (u < live && n + 32 * j < e.N) finish(e, m0 + t0 + u, n + 32 * j, v[u][j], bs[j], bias[j]);
             }
+            continue;
+        }
+        const int64_t at = (m0 + t0) * e.N + n;
+#pragma unroll
+        for (int u = 0; u < G; ++u) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[u][j] = fmaf(v[u][j] * as[u], bs[j], bias[j]);
-            if (e.pre) {
+        }
+        if (e.pre) {
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
                 __half h[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) h[j] = pre_of(v[u][j]);
-                *reinterpret_cast<uint2*>(e.pre + at) = *reinterpret_cast<const uint2*>(h);
+                if (u < live) *reinterpret_cast<uint2*>(e.pre + at + u * e.N) = *reinterpret_cast<const uint2*>(h);
             }
+        }
+        switch (e.act) {
+            case kActRelu: activate_all<kActRelu>(v); break;
+            case kActSilu: activate_all<kActSilu>(v); break;
+            case kActGelu: activate_all<kActGelu>(v); break;
+            case kActGeluTanh: activate_all<kActGeluTanh>(v); break;
+            default: break;
+        }
+        if (e.res) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[u][j] = activate(v[u][j], e.act);
-            if (e.res) add4(v[u], r[u], e.res_type);
-            if (e.y_type == kSbF32) {
-                *reinterpret_cast<float4*>(static_cast<float*>(e.y) + at) =
-                    make_float4(v[u][0], v[u][1], v[u][2], v[u][3]);
-            } else {
-                *reinterpret_cast<uint2*>(static_cast<__half*>(e.y) + at) =  // (16 bits)
-                    make_uint2(pack2(v[u][0], v[u][1], e.y_type), pack2(v[u][2], v[u][3], e.y_type));
-            }
+            for (int u = 0; u < G; ++u) add4(v[u], r[u], e.res_type);
+        }
+        if (e.y_type == kSbF32) {
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+                if (u < live)
+                    *reinterpret_cast<float4*>(static_cast<float*>(e.y) + at + u * e.N) =
+                        make_float4(v[u][0], v[u][1], v[u][2], v[u][3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < G; ++u)
+                if (u < live)
+                    *reinterpret_cast<uint2*>(static_cast<__half*>(e.y) + at + u * e.N) =  // (16 bits)
+                        make_uint2(pack2(v[u][0], v[u][1], e.y_type), pack2(v[u][2], v[u][3], e.y_type));
         }
     }
 }
@@ -323,36 +367,23 @@ __global__ void __launch_bounds__(few_threads(T), few_per_sm(T))
         const int accs = (k1 - k0 + sums - 1) / sums;
         const uint32_t d = tmem_base + ((uint32_t)(sub * 32) << 16);
         const uint32_t parts = tc::smem_u32(smem) + rank * share * (128 * L::G * 4) + slot(row) * (4 * L::G);
-        constexpr int W = T < 32 ? T : 32;  // columns of the chunk; T = 16: two accumulators a load
-#pragma unroll 1
-        for (int c = (warp - 2) / 4; W * c < rows; c += EW / 4) {
-            float v[W];
-#pragma unroll 1
-            for (int a = 0; a < accs; a += 32 / W) {
-                uint32_t r[32];
-                tc::tmem_ld32(d + a * T + 32 * c, r);
-                tc::tmem_wait_ld();
+        // Each CTA begins with its own share and goes on to the next CTA's: in one order for
+        // all, they would all send to the same one at a time.  (EW / 4 warps a quadrant.)
+        for (int o = 0; o < split; ++o) {
+            const int owner = rank + o < split ? rank + o : rank + o - split;
+            const uint32_t to = at_rank(parts, owner), bar = at_rank(tc::smem_u32(landed), owner);
+#pragma unroll 2
+            for (int i = (warp - 2) / 4; owner + split * i < groups; i += EW / 4) {
+                float v[L::G];
+                for (int a = 0; a < accs; ++a) {
+                    uint32_t r[L::G];
+                    tmem_ld_group(d + a * T + (owner + split * i) * L::G, r);
 #pragma unroll
-                for (int j = 0; j < W; ++j) v[j] = a == 0 ? __uint_as_float(r[j]) : v[j] + __uint_as_float(r[j]);
-                if (W < 32 && a + 1 < accs) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) v[j] += __uint_as_float(r[32 - W + j]);
+                    for (int j = 0; j < L::G; ++j)
+                        v[j] = !ok ? __int_as_float(0x7fc00000) : a == 0 ? __uint_as_float(r[j]) : v[j] + __uint_as_float(r[j]);
                 }
-            }
-            if (!ok) {
-#pragma unroll
-                for (int j = 0; j < W; ++j) v[j] = __int_as_float(0x7fc00000);
-            }
-            int g = c * (W / L::G), owner = g % split, i = g / split;
-#pragma unroll
-            for (int q = 0; q < W / L::G; ++q) {
-                if (g + q < groups) {
-                    const uint32_t to = at_rank(parts + i * (128 * L::G * 4), owner);
-                    const uint32_t bar = at_rank(tc::smem_u32(landed), owner);
-                    if constexpr (L::G == 4) st_async4(to, bar, v + 4 * q);
-                    else st_async2(to, bar, v + 2 * q);
-                }
-                if (++owner == split) owner = 0, ++i;
+                if constexpr (L::G == 4) st_async4(to + i * (128 * L::G * 4), bar, v);
+                else st_async2(to + i * (128 * L::G * 4), bar, v);
             }
         }
     }
