@@ -305,20 +305,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tc::grid_dep_wait();
 
     if (warp == 0) {
-        int stage = 0;
-        uint32_t phase = 0, fills = 0;
+        uint32_t fills = 0;
         bool ok = stall == 0;
         const uint32_t full_lead = tc::mapa_shared(full, 0);
-        for (int i = first; i < walk.items && ok; i += stride) {
-            int t, mt, nt, k0, k1;
-            item_of(walk, i, n_k, t, k0, k1);
-            tile_of(t, n_mt, n_nt, mt, nt);
-            const int m0 = mt * 256 + (int)rank * 128, n0 = nt * BN + (int)rank * (BN / 2);
-            for (int kk = k0; kk < k1; ++kk) {
-                ok = __all_sync(0xffffffffu,
-                                tc::mbar_wait_cta(&empty[stage], phase ^ 1, abort_flag, err, tc::kErrTimeoutEmpty));
-                if (!ok) break;
-                if (elect_one()) {
+        const bool leads = elect_one();
+        if (leads) {
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int i = first; i < walk.items && ok; i += stride) {
+                int t, mt, nt, k0, k1;
+                item_of(walk, i, n_k, t, k0, k1);
+                tile_of(t, n_mt, n_nt, mt, nt);
+                const int m0 = mt * 256 + (int)rank * 128, n0 = nt * BN + (int)rank * (BN / 2);
+                for (int kk = k0; kk < k1; ++kk) {
+                    ok = tc::mbar_wait_cta(&empty[stage], phase ^ 1, abort_flag, err, tc::kErrTimeoutEmpty);
+                    if (!ok) break;
                     // both CTAs' copies count on the even CTA's barrier
                     if (rank == 0) tc::mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE);
                     unsigned char* A = smem + stage * L::STAGE;
@@ -337,20 +338,22 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     } else {
                         tma_load_pair(B, &tb, bar, k, n0);
                     }
+                    ++fills;
+                    if (++stage == NS) { stage = 0; phase ^= 1; }
                 }
-                __syncwarp();
-                ++fills;
-                if (++stage == NS) { stage = 0; phase ^= 1; }
             }
         }
+        __syncwarp();
         tc::grid_dep_trigger();  // (earlier, the next kernel's blocks would crowd some SMs)
-        // The last stages are consumed (their commits reach both CTAs) before the CTA exits.
-        for (uint32_t i = fills > NS ? fills - NS : 0; i < fills && ok; ++i)
-            ok = tc::mbar_wait_cta(&empty[i % NS], (i / NS) & 1, abort_flag, err, tc::kErrTimeoutEmpty);
-        // And on any path every copy has landed: the even CTA's barriers count both CTAs'.
-        if (rank == 0 && lane == 0) tc::drain_ring(full, NS, fills, err);
+        if (leads) {
+            // The last stages are consumed (their commits reach both CTAs) before the CTA exits.
+            for (uint32_t i = fills > NS ? fills - NS : 0; i < fills && ok; ++i)
+                ok = tc::mbar_wait_cta(&empty[i % NS], (i / NS) & 1, abort_flag, err, tc::kErrTimeoutEmpty);
+            // And on any path every copy has landed: the even CTA's barriers count both CTAs'.
+            if (rank == 0) tc::drain_ring(full, NS, fills, err);
+        }
     } else if (warp == 1) {
-        if (rank == 0) {
+        if (rank == 0 && elect_one()) {
             int stage = 0, buf = 0;
             uint32_t phase = 0, aphase = 0;
             const uint64_t ad0 = operand_desc<AMN>(tc::smem_u32(smem));
@@ -362,39 +365,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 for (int kk = k0; kk < k1; ++kk) {
                     const bool begins = kk == k0 || (SUMS && (kk - k0) % kSumSteps == 0);
                     if (begins) {
-                        ok = __all_sync(0xffffffffu, tc::mbar_wait_cluster(&acce[buf], aphase ^ 1, abort_flag, err,
-                                                                           tc::kErrTimeoutAccEmpty));
+                        ok = tc::mbar_wait_cluster(&acce[buf], aphase ^ 1, abort_flag, err, tc::kErrTimeoutAccEmpty);
                         if (!ok) break;
                         tc::tc_fence_after();
                     }
-                    ok = __all_sync(0xffffffffu,
-                                    tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull));
+                    ok = tc::mbar_wait_cta(&full[stage], phase, abort_flag, err, tc::kErrTimeoutFull);
                     if (!ok) break;
                     tc::tc_fence_after();
                     const uint32_t d = tmem_base + buf * BN;
                     const uint64_t ad = ad0 + (uint32_t)(stage * (L::STAGE >> 4));
                     const uint64_t bd = bd0 + (uint32_t)(stage * (L::STAGE >> 4));
                     const bool ends = kk + 1 == k1 || (SUMS && (kk + 1 - k0) % kSumSteps == 0);
-                    if (elect_one()) {
-                        if (!AMN && !BMN && f8) {
+                    if (!AMN && !BMN && f8) {
 #pragma unroll
-                            for (int s = 0; s < 4; ++s)
-                                umma_f8_pair(d, ad + 2 * s, bd + 2 * s, idesc, !begins || s != 0);
-                        } else {
+                        for (int s = 0; s < 4; ++s)
+                            umma_f8_pair(d, ad + 2 * s, bd + 2 * s, idesc, !begins || s != 0);
+                    } else {
 #pragma unroll
-                            for (int s = 0; s < 4; ++s)
-                                tc::umma_f16_pair(d, ad + kStep<AMN> * s, bd + kStep<BMN> * s, idesc,
-                                                  !begins || s != 0);
-                        }
-                        tc::umma_commit_pair(&empty[stage], kPairMask);
-                        if (ends) tc::umma_commit_pair(&accf[buf], kPairMask);
+                        for (int s = 0; s < 4; ++s)
+                            tc::umma_f16_pair(d, ad + kStep<AMN> * s, bd + kStep<BMN> * s, idesc, !begins || s != 0);
                     }
-                    __syncwarp();
+                    tc::umma_commit_pair(&empty[stage], kPairMask);
+                    if (ends) tc::umma_commit_pair(&accf[buf], kPairMask);
                     if (++stage == NS) { stage = 0; phase ^= 1; }
                     if (ends && ++buf == 2) { buf = 0; aphase ^= 1; }
                 }
             }
-            if (!ok && elect_one()) {
+            if (!ok) {
                 tc::umma_commit_pair(mdrain, 0x1);
                 tc::mbar_drain(mdrain, 0, err);
             }
@@ -624,6 +621,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         if (lane == 0) tma_stores_done();
     }
+    __syncwarp();
     tc::tc_fence_before();
     __syncthreads();
     tc::cluster_sync();
