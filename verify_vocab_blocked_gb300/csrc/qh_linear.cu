@@ -178,7 +178,6 @@ __device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.
 
 constexpr int kEpiWarps = 16;
 constexpr int kPairThreads = 32 * (2 + kEpiWarps);
-constexpr int kJoinStages = 16;  // stages in the time that joining the shared tiles takes
 
 template <int BN, bool AMN, bool BMN>
 struct PairLayout {
@@ -782,49 +781,66 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const E* src, int64_t ld,
 
 }  // namespace
 
+// Which kernel, tile and split: the least of their times, in us, by two formulas whose
+// constants were fitted to 2000 measured plans (5 to 4096 rows on nine weights of 512 to
+// 20000 columns and rows, read from DRAM).  The choice is 1.6 % above the best one measured
+// in the mean and 20 % at the worst; a rule by the number of rows alone left 1.7 times
+// (301 x 1536 x 1536: 12.7 us on pairs, 7.4 in tiles of 64 rows; 192 x 6144 x 1536: 17.4
+// and 10.8).
 LinPlan plan_linear(const LinArgs& a, int sms) {
     LinPlan p{};
-    p.split = 1;
     int step;
     const int n_k = steps(a, &step);
-    // Few rows: tiles of the rows' own number up to 64.  65 to 128 rows go as two tiles of
-    // 64 while these leave three parts of the reduction each (128 x 2560 x 2560: 10.3 us,
-    // in one tile of 128 11.7, on pairs 13.4), else in one of 128 (128 x 2560 x 10240: 18.7
-    // us, 23.6 in two, 19.6 on pairs); up to 256 rows as tiles of 64 while, too, the
-    // reduction is short (200 x 2560 x 2560: 12.7 us, 13.7 on pairs; 200 x 10240 x 2560: 27
-    // and 22).
-    const int64_t strips = (a.N + 127) / 128, most = sms * 8 / 5;
-    const bool several = strips * ((a.M + 63) / 64) * 3 <= most;
-    if (a.a.k_major && (a.M <= 128 || (a.M <= 256 && several && n_k <= 64))) {
-        p.few = true;
-        p.tile = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 || several ? 64 : 128;
-        // CTAs as many as 0.8 to 0.9 of those that fit, two to an SM or, of 16 rows, three:
-        // fewer leave SMs idle, more queue (5 x 2560 x 10240, 80 strips: 12.4 us in 5 parts,
-        // 13.9 in 3; 64 rows: 15.4 in 3, 17.5 in 2, 22 in 5)
-        const int64_t tiles = strips * ((a.M + p.tile - 1) / p.tile), fit = p.tile <= 16 ? sms * 8 / 3 : most;
-        p.split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, n_k), fit / tiles));
-        return p;
-    }
-    // Pairs: tiles of 256 or 128 columns, whichever takes fewer stages (a stage of 128 costs
-    // 0.85 of one of 256; sums of 256 columns spill registers once a tile).  The tiles past
-    // the last full round are shared by the idle pairs, in parts of 4 stages at least, where
-    // that takes more stages off the round than the join costs.
     p.pairs = std::max(1, sms / 2);
     p.sums = in_sums(a) && n_k > kSumSteps;
     float best = 0.f;
+    const auto better = [&](float cost) {
+        if (p.tile && cost >= best) return false;
+        best = cost;
+        return true;
+    };
+    // Pairs: the rounds' stages (or their epilogues) and the epilogue of one tile.  The tiles past the last full
+    // round may be shared by the idle pairs, in parts of 4 stages at least, whose sums a
+    // second kernel joins.  Sums of 256 columns spill registers once a tile.
     for (const int tile : {256, 128}) {
         const int64_t tiles = (a.M + 255) / 256 * ((a.N + tile - 1) / tile);
         const int tail = (int)(tiles % p.pairs);
-        int split = tail > 0 ? (int)std::min<int64_t>(p.pairs / tail, n_k / 4) : 1;
-        if (split > 1 && n_k - (n_k + split - 1) / split < kJoinStages) split = 1;
-        const int64_t last = tail == 0 ? 0 : split > 1 ? (n_k + split - 1) / split + kJoinStages : n_k;
-        const float cost = (float)(tiles / p.pairs * n_k + last) * (tile == 128 ? 0.85f : p.sums ? 1.2f : 1.f);
-        if (tile == 256 || cost < best) {
-            best = cost;
+        const float stage = tile == 128 ? 0.21f : p.sums ? 0.36f : 0.30f;
+        const float epilogue = tile == 128 ? 1.9f : 3.1f;
+        const float rounds = 2.8f + epilogue + (float)(tiles / p.pairs) * std::max(epilogue, (float)n_k * stage);
+        const int most = tail > 0 ? std::min(std::min(16, p.pairs / tail), n_k / 4) : 1;
+        for (int split = 1; split <= std::max(1, most); ++split) {
+            const float last = tail == 0    ? 0.f
+                               : split == 1 ? (float)n_k * stage
+                                            : (float)((n_k + split - 1) / split) * stage + 4.1f + 0.41f * (float)split;
+            if (!better(rounds + last)) continue;
             p.tile = tile;
-            p.split = std::max(1, split);
-            p.part_bytes = p.split > 1 ? sizeof(float) * (size_t)tail * p.split * 256 * tile : 0;
+            p.split = split;
+            p.part_bytes = split > 1 ? sizeof(float) * (size_t)tail * split * 256 * tile : 0;
         }
+    }
+    // Few rows: a CTA's stages, all CTAs' reads from L2, the weights from DRAM, and the sums
+    // sent to and finished by the CTAs of a cluster.  The reduction is split for as many CTAs
+    // as 0.8 to 0.9 of those that fit (two to an SM or, of 16 rows, three): fewer leave SMs
+    // idle, more queue.  Up to 128 rows in any number of rounds, up to 512 in one.
+    if (!a.a.k_major || a.M > 512) return p;
+    for (const int tile : {16, 32, 64, 128}) {
+        if (tile > 16 ? tile > 2 * a.M - 1 : a.M > 16) continue;
+        const int64_t strips = (a.N + 127) / 128, tiles = strips * ((a.M + tile - 1) / tile);
+        const int64_t fit = tile == 16 ? sms * 8 / 3 : sms * 8 / 5;
+        if (a.M > 128 && tiles > fit) continue;
+        const int split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(8, n_k / 2), fit / tiles));
+        const float n = (float)(tiles * split), rows = (float)std::min<int64_t>(tile, a.M), s = (float)split;
+        const float k = (float)((n_k + split - 1) / split), per_sm = std::max(1.f, n / (float)sms);
+        const float cost = 2.9f + k * (tile == 128 ? 0.25f : 0.17f) * (float)((tiles * split + fit - 1) / fit) +
+                           3.4e-9f * n * k * (float)(kRowBytes * (128 + tile)) +
+                           1.2e-7f * (float)strips * (float)n_k * (float)(kRowBytes * 128) +
+                           rows * per_sm * (0.024f * (s - 1.f) + 0.04f) / s;
+        if (!better(cost)) continue;
+        p.few = true;
+        p.tile = tile;
+        p.split = split;
+        p.part_bytes = 0;
     }
     return p;
 }

@@ -130,7 +130,7 @@ __device__ __forceinline__ void few_outputs(const Epi& e, uint32_t parts, int ra
     using L = FewLayout<T>;
     constexpr int G = L::G, EW = few_warps(T);
     const int lane = threadIdx.x & 31;
-    const bool vec = e.vec && n0 + 128 <= e.N;
+    const bool vec = e.vec != 0;  // (then N is a multiple of 4)
     const int64_t n = n0 + (vec ? 4 * lane : lane);
     const int share = (L::NG + split - 1) / split;
     bool bad = false;
@@ -143,7 +143,16 @@ __device__ __forceinline__ void few_outputs(const Epi& e, uint32_t parts, int ra
             const bool in = t0 + u < rows && n < e.N;
             as[u] = e.a_scale && in ? e.a_scale[m0 + t0 + u] : 1.f;
             r[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (vec && e.res && in) r[u] = load4(e.res, (m0 + t0 + u) * e.ldr + n, e.res_type);
+            if (!e.res || !in) continue;
+            const int64_t from = (m0 + t0 + u) * e.ldr + n;
+            if (vec) {
+                r[u] = load4(e.res, from, e.res_type);
+            } else {
+                r[u].x = __float_as_uint(sb_elem(e.res, from, e.res_type));
+                if (n + 32 < e.N) r[u].y = __float_as_uint(sb_elem(e.res, from + 32, e.res_type));
+                if (n + 64 < e.N) r[u].z = __float_as_uint(sb_elem(e.res, from + 64, e.res_type));
+                if (n + 96 < e.N) r[u].w = __float_as_uint(sb_elem(e.res, from + 96, e.res_type));
+            }
         }
         if (i == warp) bad = !landed();
         float v[G][4];
@@ -169,15 +178,6 @@ __device__ __forceinline__ void few_outputs(const Epi& e, uint32_t parts, int ra
             for (int u = 0; u < G; ++u) v[u][0] = v[u][1] = v[u][2] = v[u][3] = __int_as_float(0x7fc00000);
         }
         const int live = n < e.N ? min(G, rows - t0) : 0;
-        if (!vec) {
-#pragma unroll
-            for (int u = 0; u < G; ++u) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (u < live && n + 32 * j < e.N) finish(e, m0 + t0 + u, n + 32 * j, v[u][j], bs[j], bias[j]);
-            }
-            continue;
-        }
         const int64_t at = (m0 + t0) * e.N + n;
 #pragma unroll
         for (int u = 0; u < G; ++u) {
@@ -190,7 +190,14 @@ __device__ __forceinline__ void few_outputs(const Epi& e, uint32_t parts, int ra
                 __half h[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) h[j] = pre_of(v[u][j]);
-                if (u < live) *reinterpret_cast<uint2*>(e.pre + at + u * e.N) = *reinterpret_cast<const uint2*>(h);
+                if (u >= live) continue;
+                if (vec) {
+                    *reinterpret_cast<uint2*>(e.pre + at + u * e.N) = *reinterpret_cast<const uint2*>(h);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (n + 32 * j < e.N) e.pre[at + u * e.N + 32 * j] = h[j];
+                }
             }
         }
         switch (e.act) {
@@ -202,9 +209,16 @@ __device__ __forceinline__ void few_outputs(const Epi& e, uint32_t parts, int ra
         }
         if (e.res) {
 #pragma unroll
-            for (int u = 0; u < G; ++u) add4(v[u], r[u], e.res_type);
+            for (int u = 0; u < G; ++u) add4(v[u], r[u], vec ? e.res_type : kSbF32);
         }
-        if (e.y_type == kSbF32) {
+        if (!vec) {
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (u < live && n + 32 * j < e.N) put(e.y, at + u * e.N + 32 * j, e.y_type, v[u][j]);
+            }
+        } else if (e.y_type == kSbF32) {
 #pragma unroll
             for (int u = 0; u < G; ++u)
                 if (u < live)
@@ -343,7 +357,7 @@ __global__ void __launch_bounds__(few_threads(T), few_per_sm(T))
         }
     } else {
         // (their values are on their way while the accumulator fills)
-        const bool vec = e.vec && n0 + 128 <= e.N;
+        const bool vec = e.vec != 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int64_t at = n0 + (vec ? 4 * lane + j : lane + 32 * j);
