@@ -290,3 +290,66 @@ def test_a_wait_that_expires(M):
     assert 1.5 <= time.monotonic() - t0 < 60
     assert torch.isnan(y).all()
     assert torch.equal(qhead.linear(x, w), ref)
+
+
+@pytest.mark.parametrize("M,K,N,t,pad,padw,act,bias,res,out", [
+    # 17 to 512 rows in several tiles of 32, 64 and 128, the reduction in 1 to 8 parts
+    (20, 128, 3000, BF, 0, 0, "none", None, None, BF),
+    (96, 2560, 2560, BF, 0, 0, "gelu", F, BF, BF),
+    (192, 6144, 1536, HF, 0, 0, "silu", HF, F, F),
+    (301, 1536, 1536, BF, 0, 0, "silu", BF, BF, BF),
+    (384, 4096, 520, BF, 0, 0, "none", None, F, F),
+    (400, 640, 1003, HF, 3, 5, "gelu_tanh", F, HF, HF),
+    (512, 1000, 1000, BF, 8, 0, "relu", BF, BF, F),
+    # columns that end inside a strip, 4 and 1 of them; more tiles than fit at once
+    (45, 512, 900, BF, 0, 0, "silu", BF, BF, BF),
+    (6, 512, 129, HF, 0, 0, "gelu", None, HF, HF),
+    (5, 256, 70000, BF, 0, 0, "silu", BF, BF, BF),
+    (40, 64, 50001, BF, 0, 0, "none", None, None, BF),
+    # pairs: short reductions, shared tiles of ragged and unaligned rows
+    (100, 64, 40000, BF, 0, 0, "silu", None, BF, BF),
+    (600, 4096, 600, BF, 0, 0, "silu", BF, BF, BF),
+    (600, 4100, 601, HF, 4, 0, "gelu", F, HF, HF),
+    (700, 3000, 520, BF, 0, 8, "none", None, F, F),
+    (515, 10240, 300, BF, 0, 0, "gelu_tanh", BF, None, F),
+])
+def test_forward_of_middle_sizes(M, K, N, t, pad, padw, act, bias, res, out):
+    test_forward(M, K, N, t, pad, padw, act, bias, res, out)
+
+
+@pytest.mark.parametrize("M,K,N,t,act,dt,pad,padw", [
+    (301, 1536, 1536, BF, "silu", BF, 0, 0),
+    (512, 260, 2100, HF, "none", HF, 4, 0),
+    (700, 600, 4200, BF, "gelu", BF, 0, 0),
+    (640, 1001, 515, BF, "silu", F, 1, 0),
+])
+def test_gradient_of_middle_sizes(M, K, N, t, act, dt, pad, padw):
+    check_bwd(M, K, N, t, act, dt, pad, padw)
+
+
+@pytest.mark.parametrize("M,K,N", [(130, 5120, 256), (600, 4096, 600), (2048, 2560, 2560)])
+def test_a_wait_that_expires_in_shared_sums(M, K, N):
+    """... where several CTAs share a tile's reduction."""
+    x, w, _, _ = operands(M, K, N, BF, 7)
+    ref = qhead.linear(x, w)
+    qhead.test_stall_next_call(True)
+    y = qhead.linear(x, w)
+    torch.cuda.synchronize()
+    assert torch.isnan(y).all()
+    assert torch.equal(qhead.linear(x, w), ref)
+
+
+def test_few_rows_many_times_over():
+    """Sums sent between CTAs: the same bits call after call, with calls in flight on two
+    streams."""
+    x, w, _, _ = operands(64, 2560, 2560, BF, 8)
+    x2, w2, _, _ = operands(16, 2560, 4096, BF, 9)
+    ref, ref2 = qhead.linear(x, w, None, "silu"), qhead.linear(x2, w2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got, got2 = [], []
+    for _ in range(100):
+        got.append(qhead.linear(x, w, None, "silu"))
+        got2.append(qhead.linear(x2, w2, stream=side))
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(ref, y) for y in got) and all(torch.equal(ref2, y) for y in got2)
