@@ -12,10 +12,11 @@
 // Two kernels:
 //   * pairs: CTA pairs (cta_group::2), 256 x BN output tiles, persistent; one
 //     thread streams both operands' 128-byte-swizzled tiles by TMA, one issues the
-//     MMAs into two accumulators in turn, eight warps run the epilogue of one
+//     MMAs into two accumulators in turn, sixteen warps run the epilogue of one
 //     while the other fills, the residual and the outputs going through shared
-//     memory by TMA;
-//   * few (qh_linear_few.cu): for few rows of A.
+//     memory by TMA (8192 x 2560 x 10240 bf16: 226 us, 1 900 TFLOP/s; with K = 512, whose
+//     tiles last as long as their epilogue, 59, with silu, residual and pre 127);
+//   * few (qh_linear_few.cu): for up to 512 rows of A.
 //
 // A bounded wait that expires makes the tile NaN.
 #include "qh_linear_epi.cuh"

@@ -2,13 +2,17 @@
 //
 // Its time is reading the weights once.  Their rows are the MMA's 128, the tokens its
 // 16 to 128 columns, and the CTAs of a cluster share a tile's reduction, so that a small
-// weight matrix is read by all SMs; their partial tiles are summed in rank order through
-// distributed shared memory (deterministic).  The weights K-major (the forward) or down
-// their rows (dx = dz W).
+// weight matrix is read by all SMs.  Each CTA finishes a share of the tokens: the others
+// send it their sums by asynchronous stores into its shared memory, counted on its
+// barrier, and it adds them in rank order (deterministic).  Reading them from there
+// instead took 1 to 3 us more: a remote load waits for its way there and back, and the
+// cluster had to stay until the last one.  What is sent moves at about 16 bytes a clock
+// and SM, which keeps the splits of 64 and more tokens dear (64 x 2560 x 2560: 1.9 of 7.2
+// us).  The weights K-major (the forward) or down their rows (dx = dz W).
 //
-// 5 x 2560 x 2560 bf16 from DRAM: 6.7 us a call in a graph, of which 2 are the bytes; the
-// rest is the chain of launch, first loads, cluster barriers and the last stores.
-// 5 x 2560 x 10240: 12.4 us, 4.2 TB/s.
+// 5 x 2560 x 2560 bf16 from DRAM: 5.5 us a call in a graph, of which 2 are the bytes; the
+// rest is the chain of launch, first loads, cluster barrier and the last stores.
+// 5 x 2560 x 10240: 10.5 us, 5.0 TB/s; 128 x 10240 x 2560: 15.9.
 #include "qh_linear_epi.cuh"
 
 namespace qh {
