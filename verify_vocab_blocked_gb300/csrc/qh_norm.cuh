@@ -124,14 +124,17 @@ inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 1
 template <typename F>
 cudaError_t elem_shape(int H, F&& f) {
 #define QH_SHAPE(nt, ne) f(std::integral_constant<int, nt>{}, std::integral_constant<int, ne>{})
-    if (H <= 256) return QH_SHAPE(32, 8);
-    if (H <= 512) return QH_SHAPE(64, 8);
-    if (H <= 1024) return QH_SHAPE(128, 8);
-    if (H <= 2048) return QH_SHAPE(256, 8);
-    if (H <= 3072) return QH_SHAPE(256, 12);
-    if (H <= 4096) return QH_SHAPE(256, 16);
-    if (H <= 6144) return QH_SHAPE(512, 12);
+#define QH_UP_TO(nt, ne) \
+    if (H <= nt * ne) return QH_SHAPE(nt, ne)
+    QH_UP_TO(32, 8);
+    QH_UP_TO(64, 8);
+    QH_UP_TO(128, 8);
+    QH_UP_TO(256, 8);
+    QH_UP_TO(256, 12);
+    QH_UP_TO(256, 16);
+    QH_UP_TO(512, 12);
     return QH_SHAPE(512, 16);
+#undef QH_UP_TO
 #undef QH_SHAPE
 }
 
