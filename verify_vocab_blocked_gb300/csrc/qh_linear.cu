@@ -132,10 +132,6 @@ __device__ __forceinline__ void add_half(uint32_t base, int r, float (&v)[32], i
 // z of row m and a thread's 32 consecutive columns, whose scales and biases the warp's
 // lanes hold: through 256 bytes of shared memory.
 __device__ __forceinline__ void scale32(const Epi& e, int64_t m, const Column& column, uint32_t sh, float (&v)[32]) {
-    if (e.unbias != 1.f) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= e.unbias;
-    }
     if (!e.bias && !e.b_scale) return;
     const int lane = threadIdx.x & 31;
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(sh + 4 * lane), "f"(column.scale) : "memory");
@@ -247,9 +243,12 @@ __device__ __forceinline__ void tmem_wait_ld_of8(uint32_t (&r)[8]) {
 
 // SUMS: for float32 outputs of 16-bit operands.  The tensor cores' accumulation
 // truncates, up to a step of the running sum at each MMA; kSumSteps stages are summed
-// there, and these sums in registers, rounded to nearest.  Error over the result's
-// norm at K = 1541: 2.1e-6 in one sum, 5.4e-7 so (4 stages 1.4e-7, but then the epilogue
-// sets the pace), 3 to 8e-7 an fp32 product.
+// there, and these sums in registers, rounded to nearest.  (What is lost depends on the
+// operands -- a product whose sums fp32 holds loses nothing -- so that no factor on the
+// result could make up for it.)  Error over the result's norm at K = 2560, operands of
+// both signs and positive ones: 4.7e-7 and 8.5e-7 so, 9.2e-7 and 1.9e-6 with 16 stages,
+// 2.4e-7 and 3.6e-7 with 4, an fp32 product 4.5e-7 and 6.4e-7; 8192 x 2560 x 10240: 278,
+// 266 and 326 us (with 4 the epilogue sets the pace).
 template <int BN, bool AMN, bool BMN, bool SUMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -660,7 +659,7 @@ __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const __grid_
         for (int j = 0; j < 8; ++j) {
             const int64_t n = n0 + lane + kLanes * j;
             if (n < e.N)
-                finish(e, m, n, v[j], e.unbias * (e.b_scale ? e.b_scale[n] : 1.f),
+                finish(e, m, n, v[j], e.b_scale ? e.b_scale[n] : 1.f,
                        e.bias ? sb_elem(e.bias, n, e.bias_type) : 0.f);
         }
         return;
@@ -675,7 +674,7 @@ __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const __grid_
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += u[j];
     }
-    const float as = e.unbias * (e.a_scale ? e.a_scale[m] : 1.f);
+    const float as = e.a_scale ? e.a_scale[m] : 1.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         v[j] = fmaf(v[j] * as, e.b_scale ? e.b_scale[n + j] : 1.f, e.bias ? sb_elem(e.bias, n + j, e.bias_type) : 0.f);
@@ -714,7 +713,7 @@ cudaError_t go_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
     const int full = p.split > 1 ? tiles / p.pairs * p.pairs : tiles;
     const Walk walk{full, full + (tiles - full) * p.split, p.split, a.part};
     const int pairs = std::min(walk.items, p.pairs);
-    const Epi e = epi_of(a, in_sums(a) ? 4 * std::min(n_k, kSumSteps) : 0);
+    const Epi e = epi_of(a);
     CUtensorMap ty{}, tp{}, tr{};
     if (!map_tile(&ty, a.y, a.y_type, a.N, a, e.vec) || !map_tile(&tp, a.pre, kSbF16, a.N, a, e.vec) ||
         !map_tile(&tr, a.res, a.res_type, a.ldr, a, e.vec))
@@ -724,9 +723,8 @@ cudaError_t go_pair(const LinArgs& a, const LinPlan& p, cudaStream_t st) {
                                          idesc_of(a.type, 256, BN, AMN, BMN), (int)(a.type == kE4m3), a.stall))
         return err;
     if (full == tiles) return cudaSuccess;
-    const Epi parts = epi_of(a, in_sums(a) ? 4 * std::min((n_k + p.split - 1) / p.split, kSumSteps) : 0);
     return launch_after(linear_join_kernel<BN>, dim3(256 * BN / 8 / kJoinThreads, (unsigned)(tiles - full)),
-                        dim3(kJoinThreads), st, parts, walk);
+                        dim3(kJoinThreads), st, e, walk);
 }
 
 template <bool AMN, bool BMN>

@@ -13,7 +13,7 @@ namespace qh {
 namespace {
 
 constexpr int kRowBytes = 128;   // bytes of a K-major row a stage: 64 or 128 elements
-constexpr int kSumSteps = 16;    // stages of a tensor-core sum of a float32 output (see SUMS)
+constexpr int kSumSteps = 8;     // stages of a tensor-core sum of a float32 output (see SUMS)
 
 // ----------------------------------------------------------------- epilogue
 
@@ -56,12 +56,10 @@ struct Epi {
     __half* pre;
     int64_t ldr;
     int bias_type, act, res_type, y_type;
-    float unbias;      // what every sum is multiplied by (see unbias_of)
     int vec;           // the rows of y, pre and res are all aligned to 16 bytes
 };
 
-// One output of row m and column n, whose column's scale (with `unbias`) and bias
-// are at hand.
+// One output of row m and column n, whose column's scale and bias are at hand.
 __device__ __forceinline__ void finish(const Epi& e, int64_t m, int64_t n, float v, float bs, float bias) {
     if (e.a_scale) v *= e.a_scale[m];
     v = fmaf(v, bs, bias);
@@ -117,20 +115,13 @@ inline bool map_operand(CUtensorMap* map, const LinOperand& o, int type, int64_t
                      : tmap_rows_sw128(map, o.p, bytes, rows, k, o.ld * bytes, 64);
 }
 
-// What a float32 output's sum of `mmas` MMAs is multiplied by: each truncates part of a
-// step of the running sum.  Measured over K = 256 to 10240: 1.1e-8 of the result at each
-// for values of both signs, up to 2.5e-8 for positive ones; none for e4m3, whose
-// products have few bits.
-inline float unbias_of(int mmas, int type) { return type == kE4m3 ? 1.f : 1.f + 1.4e-8f * (float)mmas; }
-
-// `mmas`: of a tensor-core sum.
-inline Epi epi_of(const LinArgs& a, int mmas) {
+inline Epi epi_of(const LinArgs& a) {
     const auto rows = [](const void* p, int64_t ld, int type) {
         return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * type_bytes(type) % 16 == 0);
     };
     const bool vec = rows(a.y, a.N, a.y_type) && rows(a.pre, a.N, kSbF16) && rows(a.res, a.ldr, a.res_type);
     return Epi{a.M, a.N, a.a_scale, a.b_scale, a.bias, a.res, a.y, a.pre, a.ldr, a.bias_type, a.act, a.res_type, a.y_type,
-               unbias_of(mmas, a.type), vec};
+               vec};
 }
 
 template <typename... P, typename... A>

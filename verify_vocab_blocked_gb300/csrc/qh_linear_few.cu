@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(few_threads(T), few_per_sm(T))
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int64_t at = n0 + (vec ? 4 * lane + j : lane + 32 * j);
-            bs[j] = e.unbias * (e.b_scale && at < e.N ? e.b_scale[at] : 1.f);
+            bs[j] = e.b_scale && at < e.N ? e.b_scale[at] : 1.f;
             bias[j] = e.bias && at < e.N ? sb_elem(e.bias, at, e.bias_type) : 0.f;
         }
         ok = tc::mbar_wait_cta(accf, 0, abort_flag, err, tc::kErrTimeoutAccFull);
@@ -435,7 +435,7 @@ cudaError_t go_few(const LinArgs& a, int split, cudaStream_t st) {
     while (cols < accs * T) cols *= 2;
     const dim3 grid((unsigned)((a.N + 127) / 128 * split), (unsigned)((a.M + T - 1) / T));
     return launch_cluster(linear_few_kernel<T, WMN>, grid, few_threads(T), L::SMEM, split, st, tw, tx,
-                          epi_of(a, in_sums(a) ? 4 * sums : 0), n_k, step, split, sums, cols, idesc_of(a.type, 128, T, WMN, false),
+                          epi_of(a), n_k, step, split, sums, cols, idesc_of(a.type, 128, T, WMN, false),
                           (int)(a.type == kE4m3), a.stall);
 }
 
