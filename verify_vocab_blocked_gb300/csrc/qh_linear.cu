@@ -246,9 +246,10 @@ __device__ __forceinline__ void tmem_wait_ld_of8(uint32_t (&r)[8]) {
 // there, and these sums in registers, rounded to nearest.  (What is lost depends on the
 // operands -- a product whose sums fp32 holds loses nothing -- so that no factor on the
 // result could make up for it.)  Error over the result's norm at K = 2560, operands of
-// both signs and positive ones: 4.7e-7 and 8.5e-7 so, 9.2e-7 and 1.9e-6 with 16 stages,
-// 2.4e-7 and 3.6e-7 with 4, an fp32 product 4.5e-7 and 6.4e-7; 8192 x 2560 x 10240: 278,
-// 266 and 326 us (with 4 the epilogue sets the pace).
+// both signs and positive ones, bf16: 4.7e-7 and 8.5e-7 so, 9.2e-7 and 1.9e-6 with 16
+// stages, 2.4e-7 and 3.6e-7 with 4, an fp32 product 4.5e-7 and 6.4e-7; fp16, whose
+// products have more bits to lose: 6.5e-7 and 2.7e-6.  8192 x 2560 x 10240: 278, 266 and
+// 326 us (with 4 the epilogue sets the pace).
 template <int BN, bool AMN, bool BMN, bool SUMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -821,14 +822,17 @@ LinPlan plan_linear(const LinArgs& a, int sms) {
     // Few rows: a CTA's stages, all CTAs' reads from L2, the weights from DRAM, and the sums
     // sent to and finished by the CTAs of a cluster.  The reduction is split for as many CTAs
     // as 0.8 to 0.9 of those that fit (two to an SM or, of 16 rows, three): fewer leave SMs
-    // idle, more queue.  Up to 128 rows in any number of rounds, up to 512 in one.
+    // idle, more queue; a float32 output's in so many that a CTA's sums fit its accumulators
+    // (else it is for the pairs).  Up to 128 rows in any number of rounds, up to 512 in one.
     if (!a.a.k_major || a.M > 512) return p;
     for (const int tile : {16, 32, 64, 128}) {
         if (tile > 16 ? tile > 2 * a.M - 1 : a.M > 16) continue;
         const int64_t strips = (a.N + 127) / 128, tiles = strips * ((a.M + tile - 1) / tile);
         const int64_t fit = tile == 16 ? sms * 8 / 3 : sms * 8 / 5;
         if (a.M > 128 && tiles > fit) continue;
-        const int split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(8, n_k / 2), fit / tiles));
+        int split = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(8, n_k / 2), fit / tiles));
+        while (split < 8 && !few_fits(a, tile, (n_k + split - 1) / split)) ++split;
+        if (!few_fits(a, tile, (n_k + split - 1) / split)) continue;
         const float n = (float)(tiles * split), rows = (float)std::min<int64_t>(tile, a.M), s = (float)split;
         const float k = (float)((n_k + split - 1) / split), per_sm = std::max(1.f, n / (float)sms);
         const float cost = 2.9f + k * (tile == 128 ? 0.25f : 0.17f) * (float)((tiles * split + fit - 1) / fit) +

@@ -151,6 +151,12 @@ inline int steps(const LinArgs& a, int* step) {
     return (int)((a.K + *step - 1) / *step);
 }
 
+// Few rows: the columns of a CTA's accumulators at most, and the accumulators that `share`
+// stages of the reduction take: one, or for float32 one for each kSumSteps stages.
+constexpr int few_tmem(int tile) { return tile <= 16 ? 128 : 256; }
+inline int few_accs(const LinArgs& a, int share) { return in_sums(a) ? (share + kSumSteps - 1) / kSumSteps : 1; }
+inline bool few_fits(const LinArgs& a, int tile, int share) { return few_accs(a, share) * tile <= few_tmem(tile); }
+
 }  // namespace
 
 }  // namespace qh

@@ -29,12 +29,11 @@ __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint
 
 
 // Epilogue warps: four, or two for a quadrant of the tensor memory's lanes where there are
-// columns for both.  CTAs to an SM, and the columns of their accumulators at most: the SM's 512 hold them
-// all, so that no CTA of a cluster waits for tensor memory that another cluster holds.
+// columns for both.  CTAs to an SM: its 512 columns of tensor memory hold the accumulators
+// of them all (few_tmem), so that no CTA of a cluster waits for what another cluster holds.
 constexpr int few_warps(int tile) { return tile <= 32 ? 4 : 8; }
 constexpr int few_threads(int tile) { return 32 * (2 + few_warps(tile)); }
 constexpr int few_per_sm(int tile) { return tile <= 16 ? 3 : 2; }
-constexpr int few_tmem(int tile) { return tile <= 16 ? 128 : 256; }
 
 template <int T>
 struct FewLayout {
@@ -426,10 +425,8 @@ cudaError_t go_few(const LinArgs& a, int split, cudaStream_t st) {
         return cudaErrorInvalidValue;
     int step;
     const int n_k = steps(a, &step);
-    // a CTA's stages in one accumulator, or for float32 kSumSteps in each while they fit
-    const int share = (n_k + split - 1) / split;
-    int accs = 1;
-    if (in_sums(a)) accs = std::min(few_tmem(T) / T, (share + kSumSteps - 1) / kSumSteps);
+    const int share = (n_k + split - 1) / split, accs = few_accs(a, share);
+    if (accs * T > few_tmem(T)) return cudaErrorInvalidValue;  // (no such plan)
     const int sums = (share + accs - 1) / accs;
     int cols = 32;
     while (cols < accs * T) cols *= 2;
