@@ -52,3 +52,18 @@ def test_float32_output(M, K, N, positive, t):
         x, w = x.abs(), w.abs()
     limit = (16.5 * (1 if t == BF else 5) + (K / 512 + 1) ** 0.5) * U
     assert off(qhead.linear(x, w, out_dtype=F), x.double() @ w.double().t()) <= limit
+
+
+@pytest.mark.parametrize("positive", [False, True])
+@pytest.mark.parametrize("M,K,N", [(2048, 10240, 2560), (600, 8192, 600), (128, 40960, 256), (5, 2560, 10240), (300, 20480, 3000)])
+def test_float32_output_of_8_bits(M, K, N, positive):
+    """Products of 8 bits end above the cut; 128 MMAs a sum; the scales add three roundings."""
+    g = gen(M + K + N)
+    x, w = torch.randn(M, K, device="cuda", generator=g), torch.randn(N, K, device="cuda", generator=g)
+    if positive:
+        x, w = x.abs(), w.abs()
+    xs, ws = x.abs().amax(1) / 448, w.abs().amax(1) / 448
+    x, w = (x / xs[:, None]).to(torch.float8_e4m3fn), (w / ws[:, None]).to(torch.float8_e4m3fn)
+    ref = (x.double() @ w.double().t()) * xs.double()[:, None] * ws.double()
+    limit = (64.5 + (K / 4096 + 1) ** 0.5 + 3) * U
+    assert off(qhead.linear(x, w, x_scale=xs, w_scale=ws, out_dtype=F), ref) <= limit

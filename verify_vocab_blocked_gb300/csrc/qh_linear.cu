@@ -241,15 +241,16 @@ __device__ __forceinline__ void tmem_wait_ld_of8(uint32_t (&r)[8]) {
                  : "memory");
 }
 
-// SUMS: for float32 outputs of 16-bit operands.  The tensor cores' accumulation
-// truncates, up to a step of the running sum at each MMA; kSumSteps stages are summed
+// SUMS: for float32 outputs.  The tensor cores' accumulation
+// truncates, up to a step of the running sum at each MMA; sum_steps stages are summed
 // there, and these sums in registers, rounded to nearest.  (What is lost depends on the
 // operands -- a product whose sums fp32 holds loses nothing -- so that no factor on the
 // result could make up for it.)  Error over the result's norm at K = 2560, operands of
 // both signs and positive ones, bf16: 4.7e-7 and 8.5e-7 so, 9.2e-7 and 1.9e-6 with 16
 // stages, 2.4e-7 and 3.6e-7 with 4, an fp32 product 4.5e-7 and 6.4e-7; fp16, whose
-// products have more bits to lose: 6.5e-7 and 2.7e-6.  8192 x 2560 x 10240: 278, 266 and
-// 326 us (with 4 the epilogue sets the pace).
+// products have more bits to lose: 6.5e-7 and 2.7e-6; e4m3, K = 10240: 2.1e-7 and 1.1e-6, in
+// one sum 6.5e-7 and 5.0e-6.  8192 x 2560 x 10240 bf16: 278, 266 and 326 us (with 4 the
+// epilogue sets the pace).
 template <int BN, bool AMN, bool BMN, bool SUMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t rank = tc::cluster_ctarank();
     const int n_mt = (int)((e.M + 255) / 256), n_nt = (int)((e.N + BN - 1) / BN);
     const int first = (int)tc::cluster_id_x(), stride = (int)tc::nclusters_x();
+    const int sum = sum_steps(f8 != 0);  // (of SUMS)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; ++i) {
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 int t, k0, k1;
                 item_of(walk, i, n_k, t, k0, k1);
                 for (int kk = k0; kk < k1; ++kk) {
-                    const bool begins = kk == k0 || (SUMS && (kk - k0) % kSumSteps == 0);
+                    const bool begins = kk == k0 || (SUMS && ((kk - k0) & (sum - 1)) == 0);
                     if (begins) {
                         ok = tc::mbar_wait_cluster(&acce[buf], aphase ^ 1, abort_flag, err, tc::kErrTimeoutAccEmpty);
                         if (!ok) break;
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const uint32_t d = tmem_base + buf * BN;
                     const uint64_t ad = ad0 + (uint32_t)(stage * (L::STAGE >> 4));
                     const uint64_t bd = bd0 + (uint32_t)(stage * (L::STAGE >> 4));
-                    const bool ends = kk + 1 == k1 || (SUMS && (kk + 1 - k0) % kSumSteps == 0);
+                    const bool ends = kk + 1 == k1 || (SUMS && ((kk + 1 - k0) & (sum - 1)) == 0);
                     if (!AMN && !BMN && f8) {
 #pragma unroll
                         for (int s = 0; s < 4; ++s)
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (++buf == 2) { buf = 0; aphase ^= 1; }
             } else {
                 float v[NC][32];
-                for (int kk = k0; kk < k1; kk += kSumSteps) {
+                for (int kk = k0; kk < k1; kk += sum) {
                     const bool ok = tc::mbar_wait_cta(&accf[buf], aphase, abort_flag, err, tc::kErrTimeoutAccFull);
                     tc::tc_fence_after();
 #pragma unroll
@@ -792,7 +794,7 @@ LinPlan plan_linear(const LinArgs& a, int sms) {
     int step;
     const int n_k = steps(a, &step);
     p.pairs = std::max(1, sms / 2);
-    p.sums = in_sums(a) && n_k > kSumSteps;
+    p.sums = in_sums(a) && n_k > sum_steps(a.type == kE4m3);
     float best = 0.f;
     const auto better = [&](float cost) {
         if (p.tile && cost >= best) return false;

@@ -73,7 +73,7 @@ struct LinPlan {
     int split;         // few: CTAs (of a cluster) that share a tile's reduction; pairs:
                        // parts of the reduction of each tile past the last full round
     int pairs;         // pairs: CTA pairs a round
-    bool sums;         // pairs: the reduction in sums of kSumSteps stages
+    bool sums;         // pairs: the reduction in sums of sum_steps stages
     size_t part_bytes; // pairs: the parts' sums, 32-byte aligned (LinArgs::part)
 };
 LinPlan plan_linear(const LinArgs& a, int sms);

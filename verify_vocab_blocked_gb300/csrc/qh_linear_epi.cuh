@@ -13,7 +13,9 @@ namespace qh {
 namespace {
 
 constexpr int kRowBytes = 128;   // bytes of a K-major row a stage: 64 or 128 elements
-constexpr int kSumSteps = 8;     // stages of a tensor-core sum of a float32 output (see SUMS)
+// Stages of a tensor-core sum of a float32 output (see SUMS), a power of two: 8-bit products
+// have few bits to lose.
+__host__ __device__ constexpr int sum_steps(bool f8) { return f8 ? 32 : 8; }
 
 // ----------------------------------------------------------------- epilogue
 
@@ -144,7 +146,7 @@ cudaError_t launch_cluster(void (*fn)(P...), dim3 grid, int threads, int smem, i
 }
 
 // Whether the output asks for the tensor cores' sums to be short: see SUMS.
-inline bool in_sums(const LinArgs& a) { return a.y_type == kSbF32 && a.type != kE4m3; }
+inline bool in_sums(const LinArgs& a) { return a.y_type == kSbF32; }
 
 inline int steps(const LinArgs& a, int* step) {
     *step = a.type == kE4m3 ? 128 : 64;
@@ -152,9 +154,12 @@ inline int steps(const LinArgs& a, int* step) {
 }
 
 // Few rows: the columns of a CTA's accumulators at most, and the accumulators that `share`
-// stages of the reduction take: one, or for float32 one for each kSumSteps stages.
+// stages of the reduction take: one, or for float32 one for each sum_steps stages.
 constexpr int few_tmem(int tile) { return tile <= 16 ? 128 : 256; }
-inline int few_accs(const LinArgs& a, int share) { return in_sums(a) ? (share + kSumSteps - 1) / kSumSteps : 1; }
+inline int few_accs(const LinArgs& a, int share) {
+    const int most = sum_steps(a.type == kE4m3);
+    return in_sums(a) ? (share + most - 1) / most : 1;
+}
 inline bool few_fits(const LinArgs& a, int tile, int share) { return few_accs(a, share) * tile <= few_tmem(tile); }
 
 }  // namespace
