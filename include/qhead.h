@@ -491,7 +491,8 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
  *             QHEAD_F16, QHEAD_BF16 or QHEAD_F32 each).
  *   pre       device, fp16 [M, N] contiguous, or NULL: z, for qhead_linear_bwd,
  *             saturated to the finite range (there act's derivative is what it
- *             is at the range's ends).
+ *             is at the range's ends); where z is not 0 it keeps its sign, as the
+ *             smallest fp16 at least (relu's derivative is that).
  *   workspace device, >= qhead_linear_workspace(...) bytes, 256-byte aligned
  *             (may be NULL when that is 0).
  * Every pointer is aligned to its elements.  x and weight with 16-byte aligned

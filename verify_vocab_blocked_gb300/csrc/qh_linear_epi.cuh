@@ -34,10 +34,12 @@ __device__ __forceinline__ float activate(float z, int act) {
 
 // The pre-activation as it is kept for the gradient, in fp16: beyond fp16's range every
 // activation's derivative is what it is at the range's end, so that it saturates (NaN
-// stays).
+// stays); below it, a value that is not 0 keeps its sign (relu's derivative is that) as
+// fp16's smallest, 2^-24.
 __device__ __forceinline__ float in_half(float z) {
-    asm("max.NaN.f32 %0, %0, 0fC77FE000;\n\tmin.NaN.f32 %0, %0, 0f477FE000;" : "+f"(z));  // -+ 65504
-    return z;
+    float m = fabsf(z);
+    asm("max.NaN.f32 %0, %0, 0f33800000;\n\tmin.NaN.f32 %0, %0, 0f477FE000;" : "+f"(m));  // 2^-24, 65504
+    return z == 0.f ? z : copysignf(m, z);
 }
 __device__ __forceinline__ __half pre_of(float z) { return __float2half_rn(in_half(z)); }
 
