@@ -520,6 +520,9 @@ int qhead_linear(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, co
  *   dbias     device, [N], or NULL.
  *   workspace device, >= qhead_linear_bwd_workspace(...) bytes, 256-byte aligned.
  * M == 0 writes zeros to dweight and dbias.  Deterministic.
+ * qhead_linear_bwd_dbias: the same with a type of its own for dbias (QHEAD_F16,
+ * QHEAD_BF16 or QHEAD_F32: the bias's, such as float32 beside 16-bit operands), to
+ * which the fp32 sum is rounded.
  */
 size_t qhead_linear_bwd_workspace(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K,
                                   const void* weight, int64_t ldw, int64_t N);
@@ -527,6 +530,11 @@ int qhead_linear_bwd(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K
                      const void* weight, int64_t ldw, int64_t N, const void* dy, int dy_dtype,
                      int64_t ldy, const void* pre, int act, void* dx, void* dweight, void* dbias,
                      void* workspace, size_t workspace_bytes, void* stream);
+int qhead_linear_bwd_dbias(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K,
+                           const void* weight, int64_t ldw, int64_t N, const void* dy, int dy_dtype,
+                           int64_t ldy, const void* pre, int act, void* dx, void* dweight,
+                           void* dbias, int dbias_dtype, void* workspace, size_t workspace_bytes,
+                           void* stream);
 
 /*
  * A residual's addition and the norm behind it (no counterpart on the pages):

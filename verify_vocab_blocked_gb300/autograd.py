@@ -178,8 +178,8 @@ class Linear(torch.autograd.Function):
         want_dx, want_dw, want_db = ctx.needs_input_grad[:3]
         dx = dw = db = None
         if want_dx or want_dw or want_db:
-            dx, dw, db = qhead.linear_bwd(x, weight, _rows(dy), pre, ctx.act, want_dx=want_dx, want_dw=want_dw,
-                                          want_dbias=want_db)
+            dx, dw, db = qhead.linear_bwd(x, weight, _rows(dy), pre, ctx.act, ctx.bias_type, want_dx=want_dx,
+                                          want_dw=want_dw, want_dbias=want_db)
         return (dx, dw, None if db is None else db.to(ctx.bias_type), None,
                 dy.to(ctx.res_type) if ctx.needs_input_grad[4] else None, None)
 

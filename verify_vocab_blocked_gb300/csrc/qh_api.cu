@@ -1260,20 +1260,29 @@ int qhead_linear(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, co
 int qhead_linear_bwd(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, const void* weight, int64_t ldw,
                      int64_t N, const void* dy, int dy_dtype, int64_t ldy, const void* pre, int act, void* dx,
                      void* dweight, void* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    return qhead_linear_bwd_dbias(x, dtype, ldx, M, K, weight, ldw, N, dy, dy_dtype, ldy, pre, act, dx, dweight, dbias,
+                                  dtype, workspace, workspace_bytes, stream);
+}
+
+int qhead_linear_bwd_dbias(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, const void* weight,
+                           int64_t ldw, int64_t N, const void* dy, int dy_dtype, int64_t ldy, const void* pre, int act,
+                           void* dx, void* dweight, void* dbias, int dbias_dtype, void* workspace,
+                           size_t workspace_bytes, void* stream) {
     g_err.clear();
     HookScope scope;
     int rc = check_linear(x, dtype, ldx, M, K, weight, ldw, N, true);
     if (rc) return rc;
-    if (!dtype_ok(dy_dtype)) return fail(QHEAD_EUNSUPPORTED, "dy_dtype must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
+    if (!dtype_ok(dy_dtype) || (dbias && !dtype_ok(dbias_dtype)))
+        return fail(QHEAD_EUNSUPPORTED, "dy and dbias must be QHEAD_F16, QHEAD_BF16 or QHEAD_F32");
     if (act < QHEAD_ACT_NONE || act > QHEAD_ACT_GELU_TANH) return fail(QHEAD_EUNSUPPORTED, "unknown activation");
     if (ldy < N) return fail(QHEAD_EINVAL, "ldy < N");
-    if (misaligned(dx, 2) || misaligned(dweight, 2) || misaligned(dbias, 2) || misaligned(pre, 2) ||
-        misaligned(dy, qh::type_bytes(dy_dtype)))
+    if (misaligned(dx, 2) || misaligned(dweight, 2) || (dbias && misaligned(dbias, qh::type_bytes(dbias_dtype))) ||
+        misaligned(pre, 2) || misaligned(dy, qh::type_bytes(dy_dtype)))
         return fail(QHEAD_EINVAL, "every pointer must be aligned to its elements");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (M == 0) {
         cudaError_t e = dweight ? cudaMemsetAsync(dweight, 0, 2 * (size_t)N * (size_t)K, st) : cudaSuccess;
-        if (!e && dbias) e = cudaMemsetAsync(dbias, 0, 2 * (size_t)N, st);
+        if (!e && dbias) e = cudaMemsetAsync(dbias, 0, qh::type_bytes(dbias_dtype) * (size_t)N, st);
         return e ? cuda_fail(e, "linear_bwd zero") : QHEAD_OK;
     }
     if (!dy || (act != QHEAD_ACT_NONE && !pre)) return fail(QHEAD_EINVAL, "dy (and, with an activation, pre) is required");
@@ -1288,7 +1297,7 @@ int qhead_linear_bwd(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K
     if ((products && !as_is) || dbias) {
         qh::DzArgs d{dy, dy_dtype, ldy, static_cast<const __half*>(pre), act, M, N,
                      products && !as_is ? const_cast<void*>(dz.p) : nullptr, p.ldz, dtype, dbias,
-                     at<float>(workspace, p.off_db)};
+                     dbias_dtype, at<float>(workspace, p.off_db)};
         if ((e = qh::launch_dz(d, st))) return cuda_fail(e, "linear_bwd dz");
     }
     qh::LinArgs a{};

@@ -96,7 +96,8 @@ struct DzArgs {
     void* dz;
     int64_t ldz;
     int type;
-    void* db;            // [N] of `type`
+    void* db;            // [N] of db_type
+    int db_type;
     float* part;         // [dz_chunks(M, N, dy_type), N]
 };
 int dz_chunks(int64_t M, int64_t N, int dy_type);

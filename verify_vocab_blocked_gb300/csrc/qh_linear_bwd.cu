@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(32 * kJoinRows) db_join_kernel(const float* pa
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < kJoinRows; ++i) s += sh[i][threadIdx.x];
-    if (type == kSbBf16) static_cast<__nv_bfloat16*>(db)[n] = __float2bfloat16_rn(s);
+    if (type == kSbF32) static_cast<float*>(db)[n] = s;
+    else if (type == kSbBf16) static_cast<__nv_bfloat16*>(db)[n] = __float2bfloat16_rn(s);
     else static_cast<__half*>(db)[n] = __float2half_rn(s);
 }
 
@@ -211,7 +212,7 @@ cudaError_t launch_dz(const DzArgs& a, cudaStream_t st) {
                                                  : launch_after(dz_kernel<2>, grid, block, st, a, run);
     if (e || !a.db) return e;
     return launch_after(db_join_kernel, dim3((unsigned)((a.N + 31) / 32)), dim3(32, kJoinRows), st, (const float*)a.part,
-                        chunks, a.N, a.db, a.type);
+                        chunks, a.N, a.db, a.db_type);
 }
 
 }  // namespace qh

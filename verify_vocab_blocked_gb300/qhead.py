@@ -32,7 +32,7 @@ EXPORTS = ("qhead_fwd_workspace", "qhead_bwd_workspace", "qhead_fwd", "qhead_bwd
            "qhead_layer_norm_bwd_workspace", "qhead_layer_norm_bwd",
            "qhead_distill_fwd_workspace", "qhead_distill_fwd", "qhead_distill_bwd_workspace",
            "qhead_distill_bwd", "qhead_distill_kept", "qhead_linear_workspace", "qhead_linear",
-           "qhead_linear_bwd_workspace", "qhead_linear_bwd", "qhead_add_norm", "qhead_norm_8bit",
+           "qhead_linear_bwd_workspace", "qhead_linear_bwd", "qhead_linear_bwd_dbias", "qhead_add_norm", "qhead_norm_8bit",
            "qhead_add_norm_bwd", "qhead_grad_norm_workspace", "qhead_grad_norm", "qhead_clip_grads")
 
 
@@ -122,6 +122,8 @@ def lib() -> ctypes.CDLL:
     L.qhead_linear.restype = i32
     L.qhead_linear_bwd.argtypes = size + [vp, i32, i64, vp, i32, vp, vp, vp, vp, sz, vp]
     L.qhead_linear_bwd.restype = i32
+    L.qhead_linear_bwd_dbias.argtypes = size + [vp, i32, i64, vp, i32, vp, vp, vp, i32, vp, sz, vp]
+    L.qhead_linear_bwd_dbias.restype = i32
     added = [vp, i32, i64, vp, i32, i64, i64, i64, vp, vp, i32, f32, i32, vp]
     L.qhead_add_norm.argtypes = added + [vp, i32, vp, vp, vp]
     L.qhead_add_norm.restype = i32
@@ -588,10 +590,10 @@ def _tokens(head: Head, t: torch.Tensor) -> int:
     return int(t.shape[0])
 
 
-def _out_code(dtype) -> int:
+def _out_code(dtype, name: str = "out_dtype") -> int:
     code = _SB_CODE.get(dtype)
     if code is None:
-        raise ValueError("out_dtype must be float16, bfloat16 or float32")
+        raise ValueError(f"{name} must be float16, bfloat16 or float32")
     return code
 
 
@@ -914,11 +916,12 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
 
 
 def linear_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, pre: torch.Tensor | None = None,
-               act: str = "none", *, want_dx: bool = True, want_dw: bool = True, want_dbias: bool = True,
-               workspace: torch.Tensor | None = None, stream=None):
-    """(dx [M, K], dweight [N, K], dbias [N]), each of x's type or None where not
-    wanted, for dy = d/dy (any float type) and linear()'s pre (act "none" needs
-    none).  The residual's gradient is dy."""
+               act: str = "none", dbias_dtype: torch.dtype | None = None, *, want_dx: bool = True,
+               want_dw: bool = True, want_dbias: bool = True, workspace: torch.Tensor | None = None, stream=None):
+    """(dx [M, K], dweight [N, K], dbias [N]), None where not wanted, for dy = d/dy
+    (any float type) and linear()'s pre (act "none" needs none): dx and dweight of
+    x's type, dbias of dbias_dtype (if not given, float32 where dy is and else x's).
+    The residual's gradient is dy."""
     place = _check_operands(x, weight, _HALF_CODE)
     M, K, N, dev = place[3], place[4], place[7], x.device
     a = _act_code(act)
@@ -928,16 +931,19 @@ def linear_bwd(x: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, pre: tor
     if a and (not isinstance(pre, torch.Tensor) or pre.dtype != torch.float16 or pre.shape != (M, N)
               or not pre.is_contiguous() or pre.device != dev):
         raise ValueError(f"pre must be a contiguous float16 [{M}, {N}] tensor on {dev}")
+    if dbias_dtype is None:
+        dbias_dtype = dy.dtype if dy.dtype == torch.float32 else x.dtype
+    db_code = _out_code(dbias_dtype, "dbias_dtype")
     _usable(dev, stream, workspace)
     dx = _out((M, K), x.dtype, dev, stream) if want_dx else None
     dw = _out((N, K), x.dtype, dev, stream) if want_dw else None
-    db = _out(N, x.dtype, dev, stream) if want_dbias else None
+    db = _out(N, dbias_dtype, dev, stream) if want_dbias else None
     _reads(stream, None, x, weight, dy, pre, workspace)
     if workspace is None:
         workspace = _scratch(_linear_size("qhead_linear_bwd_workspace", place, dev), dev, stream)
-    _check(lib().qhead_linear_bwd(*place, dy.data_ptr(), _SB_CODE[dy.dtype], _row_stride(dy, M, N),
-                                  _ptr(pre) if a else None, a, _ptr(dx), _ptr(dw), _ptr(db), workspace.data_ptr(),
-                                  workspace.numel(), _stream(stream, dev)))
+    _check(lib().qhead_linear_bwd_dbias(*place, dy.data_ptr(), _SB_CODE[dy.dtype], _row_stride(dy, M, N),
+                                        _ptr(pre) if a else None, a, _ptr(dx), _ptr(dw), _ptr(db), db_code,
+                                        workspace.data_ptr(), workspace.numel(), _stream(stream, dev)))
     return dx, dw, db
 
 
