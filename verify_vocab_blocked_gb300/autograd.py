@@ -161,8 +161,8 @@ class Linear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, act: str,
-                residual: torch.Tensor | None, out_dtype: torch.dtype | None):
-        keep = act != "none" and any(ctx.needs_input_grad[:3])
+                residual: torch.Tensor | None, out_dtype: torch.dtype | None, graded: bool):
+        keep = graded and act != "none" and any(ctx.needs_input_grad[:3])
         got = qhead.linear(x, weight, bias, act, residual, out_dtype=out_dtype, want_pre=keep)
         y, pre = got if keep else (got, None)
         ctx.act = act
@@ -181,14 +181,15 @@ class Linear(torch.autograd.Function):
             dx, dw, db = qhead.linear_bwd(x, weight, _rows(dy), pre, ctx.act, ctx.bias_type, want_dx=want_dx,
                                           want_dw=want_dw, want_dbias=want_db)
         return (dx, dw, None if db is None else db.to(ctx.bias_type), None,
-                dy.to(ctx.res_type) if ctx.needs_input_grad[4] else None, None)
+                dy.to(ctx.res_type) if ctx.needs_input_grad[4] else None, None, None)
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, act: str = "none",
            residual: torch.Tensor | None = None, *, out_dtype: torch.dtype | None = None) -> torch.Tensor:
     """Differentiable act(x @ weight.T + bias) + residual (x and weight in bfloat16 or
     float16)."""
-    return Linear.apply(x, weight, bias, act, residual, out_dtype)
+    # (parameters want gradients under no_grad too, and within forward no mode is on)
+    return Linear.apply(x, weight, bias, act, residual, out_dtype, torch.is_grad_enabled())
 
 
 class Embed(torch.autograd.Function):
