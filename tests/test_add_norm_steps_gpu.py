@@ -38,3 +38,10 @@ def test_single_elements(center, M, H, xt, rt, pad, padr):
 def test_rows_of_16_byte_accesses(H):
     one.test_forward(True, 5001, H, BF, F, F, True, 8, 0)
     one.test_8_bits(False, 5001, H, BF, BF, BF, False, 0, 8)
+
+
+@pytest.mark.parametrize("M,H,tt,dt", [(61, 6400, F, F), (61, 6408, F, F), (1001, 6408, F, F), (61, 7680, F, BF), (61, 7688, F, HF),
+                                       (61, 7688, BF, F)])
+def test_gradient_where_the_ring_ends(M, H, tt, dt):
+    """The widest rows of three streams that a ring holds, and the next ones."""
+    one.test_gradient(True, M, H, tt, dt, F, 0)

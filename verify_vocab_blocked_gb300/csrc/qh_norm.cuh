@@ -564,7 +564,8 @@ template <bool ADD, typename T>
 cudaError_t pick_bwd(NormBwdArgs& a, cudaStream_t st) {
     const bool vec = a.H % 8 == 0 && a.ldx % 8 == 0 && a.ldy % 8 == 0 && aligned16(a.x) &&
                      aligned16(a.dy) && aligned16(a.dx) && (!ADD || (a.ldadd % 8 == 0 && aligned16(a.add)));
-    // (three float32 streams of more than 6272 columns do not fit a ring: single elements)
+    // (three float32 streams of more than 6400 columns, or two beside a 16-bit dy of more
+    // than 7680, do not fit a ring: single elements)
     const auto ring = [&](auto* tag) -> bool {
         return vec && ring_bytes<ADD, T, std::remove_pointer_t<decltype(tag)>>(a.H, 3) <= kRingMost;
     };
