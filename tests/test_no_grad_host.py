@@ -47,3 +47,10 @@ def test_recomputed_under_a_checkpoint(kept, monkeypatch):
     x, w = torch.ones(M, K, dtype=torch.bfloat16), torch.ones(N, K, dtype=torch.bfloat16, requires_grad=True)
     checkpoint(lambda: autograd.linear(x, w, None, "silu"), use_reentrant=False).float().sum().backward()
     assert kept[-1] and (w.grad == 1).all()
+
+
+def test_applied_without_a_mode(kept, monkeypatch):
+    monkeypatch.setattr(qhead, "linear_bwd", lambda x, w, *a, **k: (None, torch.ones_like(w), None))
+    x, w = torch.ones(M, K, dtype=torch.bfloat16), torch.ones(N, K, dtype=torch.bfloat16, requires_grad=True)
+    autograd.Linear.apply(x, w, None, "silu", None, None).float().sum().backward()
+    assert kept == [True] and (w.grad == 1).all()

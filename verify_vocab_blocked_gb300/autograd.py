@@ -161,7 +161,7 @@ class Linear(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None, act: str,
-                residual: torch.Tensor | None, out_dtype: torch.dtype | None, graded: bool):
+                residual: torch.Tensor | None, out_dtype: torch.dtype | None, graded: bool = True):
         keep = graded and act != "none" and any(ctx.needs_input_grad[:3])
         got = qhead.linear(x, weight, bias, act, residual, out_dtype=out_dtype, want_pre=keep)
         y, pre = got if keep else (got, None)
