@@ -247,8 +247,11 @@ def _usable(dev: torch.device, stream, workspace: torch.Tensor | None = None) ->
                          f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device")
     if stream is not None and stream.device != dev:
         raise ValueError(f"the tensors are on {dev} but the stream is of {stream.device}")
-    if workspace is not None and workspace.device != dev:
-        raise ValueError(f"the tensors are on {dev} but the workspace is on {workspace.device}")
+    if workspace is not None:
+        if workspace.device != dev:
+            raise ValueError(f"the tensors are on {dev} but the workspace is on {workspace.device}")
+        if not workspace.is_contiguous():  # (an expanded one has less memory than elements)
+            raise ValueError("workspace must be contiguous")
 
 
 # The current stream's handle without a Stream object around it, where torch has it
