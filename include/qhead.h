@@ -479,7 +479,10 @@ int qhead_distill_bwd(const qhead_head* head, const void* h, int64_t M, const in
  * draft head's h + silu(W h + b)):
  *     z[m, n] = x_scale[m] * w_scale[n] * sum_k x[m, k] * weight[n, k] + bias[n]
  *     y[m, n] = act(z[m, n]) + residual[m, n]
- * accumulated and finished in fp32, rounded once.
+ * accumulated and finished in fp32, rounded once.  (The tensor cores' fp32 sums
+ * truncate: a float32 y is off by 5e-7 of its norm, 3e-6 for positive fp16 operands; a
+ * 16-bit one is formed in one sum, which stays far below its rounding up to some
+ * 10^5 terms.)
  *   x         device, [M, K] of type dtype, row stride ldx >= K elements.
  *   weight    device, [N, K] of type dtype, row stride ldw >= K elements.
  *   dtype     QHEAD_BF16, QHEAD_F16, or QHEAD_E4M3 with x_scale and w_scale.
@@ -512,7 +515,9 @@ int qhead_linear(const void* x, int dtype, int64_t ldx, int64_t M, int64_t K, co
  * The gradient of qhead_linear (the residual's is dy itself):
  *     dz = dy * act'(z);  dx = dz * weight;  dweight = dz^T * x;  dbias = sum_m dz
  *   dtype     QHEAD_BF16 or QHEAD_F16: x, weight and the outputs.  dz is rounded
- *             to it as an operand of the two products (not for dbias).
+ *             to it as an operand of the two products (not for dbias), whatever dy's
+ *             type: beside fp16 operands what is below 2^-25 is lost and what is
+ *             above 65504 infinite, as in a dy of fp16.
  *   dy        device, [M, N] of type dy_dtype (any of the three), row stride ldy >= N.
  *   pre       the forward's; may be NULL when act is QHEAD_ACT_NONE.
  *   dx        device, [M, K] contiguous, or NULL (not wanted).

@@ -152,7 +152,7 @@ def add_norm(x: torch.Tensor, residual: torch.Tensor, weight: torch.Tensor, bias
              eps: float = 1e-6, *, center: bool = True,
              out_dtype: torch.dtype = torch.bfloat16) -> tuple[torch.Tensor, torch.Tensor]:
     """Differentiable (y, total): total = x + residual and its norm (center off: the
-    root-mean-square form)."""
+    root-mean-square form).  The gradient of x is the residual's, formed in its type."""
     return AddNorm.apply(x, residual, weight, bias, eps, center, out_dtype)
 
 

@@ -241,9 +241,8 @@ __device__ __forceinline__ void tmem_wait_ld_of8(uint32_t (&r)[8]) {
                  : "memory");
 }
 
-// SUMS: for float32 outputs.  The tensor cores' accumulation
-// truncates, up to a step of the running sum at each MMA; sum_steps stages are summed
-// there, and these sums in registers, rounded to nearest.  (What is lost depends on the
+// SUMS: for float32 outputs.  The tensor cores' accumulation truncates, up to a step of
+// the running sum at each MMA; sum_steps stages are summed there, and these sums in registers, rounded to nearest.  (What is lost depends on the
 // operands -- a product whose sums fp32 holds loses nothing -- so that no factor on the
 // result could make up for it.)  Error over the result's norm at K = 2560, operands of
 // both signs and positive ones, bf16: 4.7e-7 and 8.5e-7 so, 9.2e-7 and 1.9e-6 with 16
@@ -786,9 +785,9 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const E* src, int64_t ld,
 // Which kernel, tile and split: the least of their times, in us, by two formulas whose
 // constants were fitted to 2000 measured plans (5 to 4096 rows on nine weights of 512 to
 // 20000 columns and rows, read from DRAM).  The choice is 1.6 % above the best one measured
-// in the mean and 20 % at the worst; a rule by the number of rows alone left 1.7 times
-// (301 x 1536 x 1536: 12.7 us on pairs, 7.4 in tiles of 64 rows; 192 x 6144 x 1536: 17.4
-// and 10.8).
+// in the mean and 20 % at the worst (float32 outputs, 24 shapes: 1 and 7 %); a rule by the
+// number of rows alone left 1.7 times (301 x 1536 x 1536: 12.7 us on pairs, 7.4 in tiles of
+// 64 rows; 192 x 6144 x 1536: 17.4 and 10.8).
 LinPlan plan_linear(const LinArgs& a, int sms) {
     LinPlan p{};
     int step;
