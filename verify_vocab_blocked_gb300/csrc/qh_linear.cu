@@ -242,14 +242,14 @@ __device__ __forceinline__ void tmem_wait_ld_of8(uint32_t (&r)[8]) {
 }
 
 // SUMS: for float32 outputs.  The tensor cores' accumulation truncates, up to a step of
-// the running sum at each MMA; sum_steps stages are summed there, and these sums in registers, rounded to nearest.  (What is lost depends on the
-// operands -- a product whose sums fp32 holds loses nothing -- so that no factor on the
-// result could make up for it.)  Error over the result's norm at K = 2560, operands of
-// both signs and positive ones, bf16: 4.7e-7 and 8.5e-7 so, 9.2e-7 and 1.9e-6 with 16
-// stages, 2.4e-7 and 3.6e-7 with 4, an fp32 product 4.5e-7 and 6.4e-7; fp16, whose
-// products have more bits to lose: 6.5e-7 and 2.7e-6; e4m3, K = 10240: 2.1e-7 and 1.1e-6, in
-// one sum 6.5e-7 and 5.0e-6.  8192 x 2560 x 10240 bf16: 278, 266 and 326 us (with 4 the
-// epilogue sets the pace).
+// the running sum at each MMA; sum_steps stages are summed there, and these sums in
+// registers, rounded to nearest.  (What is lost depends on the operands -- a product whose
+// sums fp32 holds loses nothing -- so that no factor on the result could make up for it.)
+// Error over the result's norm at K = 2560, operands of both signs and positive ones,
+// bf16: 4.7e-7 and 8.5e-7 so, 9.2e-7 and 1.9e-6 with 16 stages, 2.4e-7 and 3.6e-7 with 4,
+// an fp32 product 4.5e-7 and 6.4e-7; fp16, whose products have more bits to lose: 6.5e-7
+// and 2.7e-6; e4m3, K = 10240: 2.1e-7 and 1.1e-6, in one sum 6.5e-7 and 5.0e-6.
+// 8192 x 2560 x 10240 bf16: 278, 266 and 326 us (with 4 the epilogue sets the pace).
 template <int BN, bool AMN, bool BMN, bool SUMS>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
